@@ -35,6 +35,9 @@ SOURCES = [
     ("decode_step_d128.cu", []),
     ("decode_step_d256.cu", []),
     ("dequant.cu", []),
+    ("qk_norm_rope.cu", []),
+    ("pages.cu", []),
+    ("chunk_attention.cu", []),
 ]
 
 

@@ -29,6 +29,13 @@ DEV_RANGE = 4
 DEV_LENGTH = 8
 DEV_STALL = 16
 DEV_BOUNDS = 32
+DEV_SEQ = 64
+
+ROPE_NONE = 0
+ROPE_LINEAR = 1
+ROPE_NTK = 2
+ROPE_YARN = 3
+ROPE_BANDS = 4
 
 
 @dataclass(frozen=True)

@@ -10,19 +10,20 @@
 #include <mutex>
 #include <string>
 
+#include "kvq_host.cuh"
 #include "kvq_internal.cuh"
 #include "split_combine.cuh"
 #include "tbq4_bins.cuh"
 
 using namespace kvq;
 
-namespace {
+namespace kvq {
 
 // Rows taken off every cache segment's limit in the bounds-checked build
 // (kvq_test_shrink_bounds); read by make_layout.
-std::atomic<int> g_bounds_shrink{0};
+static std::atomic<int> g_bounds_shrink{0};
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 kvq_status fail(kvq_status st, const char* fmt, ...) {
   char buf[512];
@@ -398,10 +399,6 @@ kvq_status cache_ptrs(const kvq_config* c, const kvq_cache* cache, CachePtrs* cp
   if (any & 15u) return fail(KVQ_ERR_ARG, "cache buffers must be 16-byte aligned");
   return KVQ_OK;
 }
-
-}  // namespace
-
-namespace kvq {
 
 void tbq4_tables(float* centroids, float* thresholds) {
   static float c32[16], t32[15];

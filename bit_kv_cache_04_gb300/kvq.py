@@ -9,12 +9,11 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import fields
 from typing import Optional, Tuple
 
 from .config import (AXIS_CHANNEL, AXIS_TOKEN, DEV_BOUNDS, DEV_CAPACITY, DEV_LENGTH, DEV_PAGE,  # noqa: F401
-                     DEV_RANGE, DEV_STALL, DT_BF16, DT_F16, K_PRE_ROPE, ROTATE_K, ROTATE_V, TBQ4_K, TBQ4_V, ZP_K, ZP_V,
-                     Config, Fmt)
+                     DEV_RANGE, DEV_SEQ, DEV_STALL, DT_BF16, DT_F16, K_PRE_ROPE, ROPE_BANDS, ROPE_LINEAR, ROPE_NONE,
+                     ROPE_NTK, ROPE_YARN, ROTATE_K, ROTATE_V, TBQ4_K, TBQ4_V, ZP_K, ZP_V, Config, Fmt)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # KVQ_LIBRARY selects another build of the same ABI (the tests use it for the
@@ -51,18 +50,31 @@ class _Cache(ctypes.Structure):
                                                   "block_table")]
 
 
+class _RopeParams(ctypes.Structure):
+    _fields_ = [
+        ("D", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+        ("original_len", ctypes.c_int32), ("reserved", ctypes.c_int32), ("attn_factor", ctypes.c_double),
+    ]
+
+
+class RopePlan(ctypes.Structure):
+    """kvq_rope_plan: a prepared rotary turn (rope_plan), host data."""
+
+    _fields_ = [
+        ("D", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("unused", ctypes.c_float), ("turns", ctypes.c_uint64 * 128),
+    ]
+
+
 def _to_c(cfg: Config) -> _Config:
     """kvq_config of a Config."""
-    c = _Config()
-    for f in fields(cfg):
-        v = getattr(cfg, f.name)
-        if isinstance(v, Fmt) or (v is None and f.name in ("k_cold", "v_cold")):
-            v = v or Fmt(0, 0, 0)
-            setattr(c, f.name, _Fmt(v.bits, v.group, v.axis))
-        else:
-            setattr(c, f.name, v)
-    c.reserved = 0
-    return c
+    def f(x: Optional[Fmt]) -> _Fmt:
+        return _Fmt() if x is None else _Fmt(x.bits, x.group, x.axis)
+
+    return _Config(cfg.L, cfg.H_kv, cfg.H_q, cfg.D, cfg.batch, cfg.max_T, cfg.in_dtype, f(cfg.k_fmt), f(cfg.v_fmt),
+                   f(cfg.k_cold), f(cfg.v_cold), cfg.hot_window, cfg.residual_window, cfg.flags, cfg.rope_theta,
+                   cfg.sign_seed, cfg.page_tokens, cfg.n_pages, cfg.max_pages_per_seq, 0)
 
 
 def _load():
@@ -94,6 +106,18 @@ def _load():
         "kvq_dequantize": ([cfgp, cachep, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp], ctypes.c_int),
         "kvq_test_force_stall": ([i32], ctypes.c_int),
         "kvq_test_shrink_bounds": ([i32], ctypes.c_int),
+        "kvq_rope_plan_init": ([P(_RopeParams), P(RopePlan)], ctypes.c_int),
+        "kvq_qk_norm_rope": ([cfgp, P(RopePlan), vp, i64, i64, vp, i64, i64, vp, vp, ctypes.c_float, vp, i32, vp, vp,
+                              vp], ctypes.c_int),
+        "kvq_pages_workspace_bytes": ([cfgp, P(sz)], ctypes.c_int),
+        "kvq_pages_init": ([cfgp, vp, vp, vp, sz, vp], ctypes.c_int),
+        "kvq_pages_release": ([cfgp, vp, vp, vp, vp, i32, vp, sz, vp], ctypes.c_int),
+        "kvq_pages_fork": ([cfgp, cachep, vp, vp, vp, vp, vp, i32, vp, sz, vp], ctypes.c_int),
+        "kvq_pages_reserve": ([cfgp, cachep, vp, vp, vp, vp, vp, i32, vp, sz, vp], ctypes.c_int),
+        "kvq_pages_compact": ([cfgp, cachep, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+        "kvq_chunk_workspace_bytes": ([cfgp, P(sz)], ctypes.c_int),
+        "kvq_chunk_workspace_init": ([cfgp, vp, sz, vp], ctypes.c_int),
+        "kvq_chunk_attention": ([cfgp, cachep, i32, i32, vp, vp, i32, i32, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
         "kvq_read_device_status": ([vp, P(u32), vp], ctypes.c_int),
         "kvq_clear_device_status": ([vp, vp], ctypes.c_int),
     }
@@ -112,7 +136,9 @@ EXPORTED = ("kvq_version", "kvq_last_error", "kvq_validate_config", "kvq_block_b
             "kvq_commit_lengths", "kvq_decode_attention", "kvq_decode_splits", "kvq_decode_attention_static",
             "kvq_dequantize", "kvq_launch_counts", "kvq_tbq4_codebook", "kvq_decode_step", "kvq_step_launches",
             "kvq_read_device_status", "kvq_clear_device_status", "kvq_test_force_stall",
-            "kvq_test_shrink_bounds")
+            "kvq_test_shrink_bounds", "kvq_rope_plan_init", "kvq_qk_norm_rope", "kvq_pages_workspace_bytes",
+            "kvq_pages_init", "kvq_pages_release", "kvq_pages_fork", "kvq_pages_reserve", "kvq_pages_compact",
+            "kvq_chunk_workspace_bytes", "kvq_chunk_workspace_init", "kvq_chunk_attention")
 
 
 def _check(st: int):
@@ -189,6 +215,18 @@ def kvq_decode_splits(cfg: Config, n_layers: int) -> int:
     return out.value
 
 
+def kvq_pages_workspace_bytes(cfg: Config) -> int:
+    out = ctypes.c_size_t()
+    _check(LIB.kvq_pages_workspace_bytes(ctypes.byref(_to_c(cfg)), ctypes.byref(out)))
+    return out.value
+
+
+def kvq_chunk_workspace_bytes(cfg: Config) -> int:
+    out = ctypes.c_size_t()
+    _check(LIB.kvq_chunk_workspace_bytes(ctypes.byref(_to_c(cfg)), ctypes.byref(out)))
+    return out.value
+
+
 def kvq_test_shrink_bounds(rows: int) -> None:
     """Bounds-checked build: treat the last `rows` rows of every cache segment
     as outside it (0 = off)."""
@@ -218,7 +256,7 @@ BUFFER_NAMES = ("k_main", "v_main", "k_cold", "v_cold", "k_resid", "v_resid")
 class KVCache:
     """Device buffers (torch tensors) of one quantized cache plus its workspace."""
 
-    def __init__(self, cfg: Config, device="cuda", block_table=None):
+    def __init__(self, cfg: Config, device="cuda", block_table=None, buffers=None):
         import torch
 
         self.cfg = cfg
@@ -227,7 +265,17 @@ class KVCache:
         sizes = kvq_buffer_sizes(cfg)
         self.buffers = {}
         for name, n in zip(BUFFER_NAMES, sizes):
-            self.buffers[name] = torch.zeros(n, dtype=torch.uint8, device=self.device) if n else None
+            given = None if buffers is None else buffers.get(name)
+            if given is not None and given.numel() * given.element_size() < n:
+                raise ValueError(f"{name}: {given.numel() * given.element_size()} bytes, {n} needed")
+            if buffers is not None and n and given is None:
+                raise ValueError(f"{name} is needed")
+            if given is not None:
+                if not given.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+                self.buffers[name] = given
+            else:
+                self.buffers[name] = torch.zeros(n, dtype=torch.uint8, device=self.device) if n else None
         self.block_table = None
         if block_table is not None:
             self.block_table = torch.as_tensor(block_table, dtype=torch.int32).to(self.device).contiguous()
@@ -236,6 +284,15 @@ class KVCache:
         self.c_cache = _Cache(*[_ptr(self.buffers[n]) for n in BUFFER_NAMES], _ptr(self.block_table))
         _check(LIB.kvq_workspace_init(ctypes.byref(self.c_cfg), _ptr(self.workspace), self.ws_bytes,
                                       _stream(None)))
+        self.chunk_ws_bytes = kvq_chunk_workspace_bytes(cfg)
+        self.chunk_workspace = None  # made by the first chunk_attention
+
+    @classmethod
+    def from_buffers(cls, cfg: Config, buffers: dict, block_table=None) -> "KVCache":
+        """A cache over the caller's filled buffers (contiguous tensors by
+        BUFFER_NAMES, in the layout of include/kvq.h); they are used as they
+        are, and so is an int32 block table on their device."""
+        return cls(cfg, next(iter(buffers.values())).device, block_table, buffers)
 
     # -- the C calls ----------------------------------------------------------
 
@@ -256,6 +313,38 @@ class KVCache:
         _check(LIB.kvq_decode_step(ctypes.byref(self.c_cfg), ctypes.byref(self.c_cache), layer0, n_layers,
                                    _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(seq_lens), _ptr(out), num_splits,
                                    _ptr(self.workspace), self.ws_bytes, _stream(stream)))
+
+    def make_chunk_workspace(self, stream=None):
+        """A prepared workspace for chunk_attention.  Calls that may run at
+        the same time (other streams, graphs replayed side by side) each need one."""
+        import torch
+
+        ws = torch.empty(self.chunk_ws_bytes, dtype=torch.uint8, device=self.device)
+        _check(LIB.kvq_chunk_workspace_init(ctypes.byref(self.c_cfg), _ptr(ws), self.chunk_ws_bytes, _stream(stream)))
+        return ws
+
+    def chunk_attention(self, layer0, n_layers, q, cu_q, total_q, max_q, seq_lens, out, window=0, sinks=0, stream=None,
+                        workspace=None):
+        """Attention of the last cu_q[b+1] - cu_q[b] cached tokens of every sequence (kvq_chunk_attention)."""
+        import torch
+
+        cfg = self.cfg
+        dt = torch.float16 if cfg.in_dtype == DT_F16 else torch.bfloat16
+        for t in (q, out):
+            if t.dtype != dt or t.shape != (n_layers, total_q, cfg.H_q, cfg.D) or not t.is_contiguous():
+                raise ValueError("q and out are contiguous [n_layers, total_q, H_q, D] tensors of the cache's dtype")
+        for t, n in ((cu_q, cfg.batch + 1), (seq_lens, cfg.batch)):
+            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+                raise ValueError("cu_q [batch + 1] and seq_lens [batch] are contiguous int32 tensors")
+        if workspace is None:
+            if self.chunk_workspace is None:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("the first chunk_attention prepares its workspace: make it before the capture")
+                self.chunk_workspace = self.make_chunk_workspace(stream)
+            workspace = self.chunk_workspace
+        _check(LIB.kvq_chunk_attention(ctypes.byref(self.c_cfg), ctypes.byref(self.c_cache), layer0, n_layers,
+                                       _ptr(q), _ptr(cu_q), total_q, max_q, _ptr(seq_lens), window, sinks, _ptr(out),
+                                       _ptr(workspace), workspace.numel(), _stream(stream)))
 
     def dequantize(self, layer, seq, t0, t1, seq_lens, k_out, v_out, stream=None):
         _check(LIB.kvq_dequantize(ctypes.byref(self.c_cfg), ctypes.byref(self.c_cache), layer, seq, t0, t1,
@@ -281,3 +370,113 @@ class KVCache:
                 a = t.cpu().numpy()
                 out[n] = a.view(np.uint16) if n.endswith("resid") else a
         return out
+
+
+def rope_plan(D, rot_dim=None, interleaved=False, theta=10000.0, scaling=ROPE_NONE, factor=1.0, low=1.0, high=32.0,
+              original_len=0, attn_factor=0.0) -> RopePlan:
+    """A prepared rotary turn for qk_norm_rope (kvq_rope_plan_init)."""
+    p = _RopeParams(D, D if rot_dim is None else rot_dim, int(interleaved), scaling, theta, factor, low, high,
+                    original_len, 0, attn_factor)
+    plan = RopePlan()
+    _check(LIB.kvq_rope_plan_init(ctypes.byref(p), ctypes.byref(plan)))
+    return plan
+
+
+def qk_norm_rope(cfg: Config, q, k, positions, q_out, k_out, plan=None, q_weight=None, k_weight=None, eps=1e-6,
+                 stream=None) -> None:
+    """RMS norm and rotary turn of queries and keys in one pass
+    (kvq_qk_norm_rope).  q, k: [tokens, heads, D], any token and head stride;
+    q_out, k_out contiguous; either pair may be None."""
+    import torch
+
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q and k are both None")
+    dt = torch.float16 if cfg.in_dtype == DT_F16 else torch.bfloat16
+    n = some.shape[0]
+    for t, o, w, h in ((q, q_out, q_weight, cfg.H_q), (k, k_out, k_weight, cfg.H_kv)):
+        if t is not None and (t.shape != (n, h, cfg.D) or t.stride(2) != 1 or t.dtype != dt or o is None or
+                              o.shape != t.shape or o.dtype != dt or not o.is_contiguous()):
+            raise ValueError("tensors are [tokens, heads, D] of the configuration with contiguous channels, outputs "
+                             "contiguous and alike")
+        if w is not None and (w.numel() != cfg.D or w.dtype != dt or not w.is_contiguous()):
+            raise ValueError("a weight is a contiguous [D] tensor of the same dtype")
+    if plan is not None and (positions is None or positions.dtype != torch.int32 or positions.numel() != n or
+                             not positions.is_contiguous()):
+        raise ValueError("positions is a contiguous int32 tensor, one of each token")
+    qs = (0, 0) if q is None else q.stride()
+    ks = (0, 0) if k is None else k.stride()
+    _check(LIB.kvq_qk_norm_rope(ctypes.byref(_to_c(cfg)), None if plan is None else ctypes.byref(plan), _ptr(q), qs[0],
+                                qs[1], _ptr(k), ks[0], ks[1], _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions),
+                                n, _ptr(q_out), _ptr(k_out), _stream(stream)))
+
+
+class PagePool:
+    """The pages of a paged KVCache: reader counts and the calls that share,
+    copy, move and free pages (kvq_pages_*).  Works on the cache's block table."""
+
+    def __init__(self, cache: KVCache, refs=None, stream=None):
+        import torch
+
+        self.cache = cache
+        self.ws_bytes = kvq_pages_workspace_bytes(cache.cfg)
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=cache.device)
+        self.refs = refs if refs is not None else torch.empty(cache.cfg.n_pages, dtype=torch.int32, device=cache.device)
+        if self.refs.dtype != torch.int32 or self.refs.numel() != cache.cfg.n_pages or not self.refs.is_contiguous():
+            raise ValueError("refs is a contiguous int32 tensor of n_pages")
+        _check(LIB.kvq_pages_init(self._cfg(), _ptr(cache.block_table), _ptr(self.refs), *self._ws(stream)))
+
+    def _cfg(self):
+        return ctypes.byref(self.cache.c_cfg)
+
+    def _ws(self, stream):
+        return _ptr(self.workspace), self.ws_bytes, _stream(stream)
+
+    def _lists(self, seq_lens, *lists):
+        import torch
+
+        for t in (seq_lens, *lists):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError("lengths and lists are contiguous int32 tensors")
+        if seq_lens.numel() != self.cache.cfg.batch or len({t.numel() for t in lists}) != 1:
+            raise ValueError("seq_lens is [batch]; lists have one length")
+
+    def release(self, seqs, seq_lens, stream=None):
+        """Frees the listed sequences."""
+        self._lists(seq_lens, seqs)
+        _check(LIB.kvq_pages_release(self._cfg(), _ptr(self.cache.block_table), _ptr(self.refs), _ptr(seq_lens),
+                                     _ptr(seqs), seqs.numel(), *self._ws(stream)))
+
+    def fork(self, src, dst, seq_lens, stream=None):
+        """Sequence dst[i] becomes a copy of src[i] that shares its pages."""
+        self._lists(seq_lens, src, dst)
+        _check(LIB.kvq_pages_fork(self._cfg(), ctypes.byref(self.cache.c_cache), _ptr(self.cache.block_table),
+                                  _ptr(self.refs), _ptr(seq_lens), _ptr(src), _ptr(dst), src.numel(),
+                                  *self._ws(stream)))
+
+    def reserve(self, seqs, n_new, seq_lens, stream=None):
+        """Pages for n_new[i] more tokens of seqs[i], and its own copy of a partly filled shared page."""
+        self._lists(seq_lens, seqs, n_new)
+        _check(LIB.kvq_pages_reserve(self._cfg(), ctypes.byref(self.cache.c_cache), _ptr(self.cache.block_table),
+                                     _ptr(self.refs), _ptr(seq_lens), _ptr(seqs), _ptr(n_new), seqs.numel(),
+                                     *self._ws(stream)))
+
+    def compact(self, refs_out=None, table_out=None, stream=None):
+        """Moves the used pages together.  Without outputs the cache's table and the counts are changed in place."""
+        import torch
+
+        table = self.cache.block_table
+        for t, like in ((refs_out, self.refs), (table_out, table)):
+            if t is not None and (t.dtype != torch.int32 or t.numel() != like.numel() or not t.is_contiguous()):
+                raise ValueError("outputs are contiguous int32 tensors like the inputs")
+        _check(LIB.kvq_pages_compact(self._cfg(), ctypes.byref(self.cache.c_cache), _ptr(table), _ptr(self.refs),
+                                     _ptr(table if table_out is None else table_out),
+                                     _ptr(self.refs if refs_out is None else refs_out), *self._ws(stream)))
+
+    def device_status(self, stream=None) -> int:
+        out = ctypes.c_uint32()
+        _check(LIB.kvq_read_device_status(_ptr(self.workspace), ctypes.byref(out), _stream(stream)))
+        return out.value
+
+    def clear_status(self, stream=None):
+        _check(LIB.kvq_clear_device_status(_ptr(self.workspace), _stream(stream)))

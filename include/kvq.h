@@ -147,8 +147,10 @@ enum {
   KVQ_DEV_LENGTH = 1u << 3,   /* a sequence length < 0 or > max_T, or cu_new not ascending */
   KVQ_DEV_STALL = 1u << 4,    /* a decode kernel's own bulk copy into shared memory did not complete
                                  within its bounded wait; that call's outputs are undefined */
-  KVQ_DEV_BOUNDS = 1u << 5    /* bounds-checked build only (libkvq_checked.so): a computed cache address
+  KVQ_DEV_BOUNDS = 1u << 5,   /* bounds-checked build only (libkvq_checked.so): a computed cache address
                                  fell outside its buffer segment; the access was skipped */
+  KVQ_DEV_SEQ = 1u << 6       /* a sequence index of a page call outside [0, batch), listed twice where that is
+                                 not allowed, or a fork target that is not empty */
 };
 
 typedef struct {
@@ -396,6 +398,184 @@ KVQ_API kvq_status kvq_read_device_status(const void* workspace, uint32_t* bits,
 
 /* Clears the device status word. */
 KVQ_API kvq_status kvq_clear_device_status(void* workspace, void* stream);
+
+/* ==== serving operators around the cache =====================================
+ * Queries and keys made ready (norm + rotary turn), pages of a paged cache
+ * shared, moved and freed, and attention of many new tokens over the packed
+ * cache.  These are additions of this library next to the pages' method; the
+ * formulas are stated with each entry. */
+
+/* ---- norm and rotary turn of queries and keys -------------------------------- */
+
+/* How the turn frequencies f_i = theta^(-2i / rot_dim), i in [0, rot_dim / 2),
+ * are scaled for contexts longer than the original one:
+ *  NONE    f_i
+ *  LINEAR  f_i / factor
+ *  NTK     theta replaced by theta * factor^(rot_dim / (rot_dim - 2)) (theta kept when rot_dim = 2)
+ *  YARN    r_i f_i / factor + (1 - r_i) f_i, r_i = clamp((i - a) / max(z - a, 0.001), 0, 1) with
+ *          a = max(0, floor(p(high))), z = min(rot_dim - 1, ceil(p(low))),
+ *          p(x) = rot_dim ln(original_len / (2 pi x)) / (2 ln theta); cos and sin times
+ *          attn_factor (0 means 0.1 ln(factor) + 1)
+ *  BANDS   b_i f_i + (1 - b_i) f_i / factor, b_i = clamp((n_i - low) / (high - low), 0, 1), n_i =
+ *          original_len f_i / (2 pi), the turns within the original context */
+typedef enum {
+  KVQ_ROPE_NONE = 0,
+  KVQ_ROPE_LINEAR = 1,
+  KVQ_ROPE_NTK = 2,
+  KVQ_ROPE_YARN = 3,
+  KVQ_ROPE_BANDS = 4
+} kvq_rope_scaling;
+
+typedef struct {
+  int32_t D;            /* head dim: 128 or 256 */
+  int32_t rot_dim;      /* channels [0, rot_dim) turn, the others pass: even, 2..D */
+  int32_t interleaved;  /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+  int32_t scaling;      /* kvq_rope_scaling */
+  double theta;         /* base, > 1 */
+  double factor;        /* >= 1 (LINEAR, NTK, YARN, BANDS) */
+  double low, high;     /* YARN, BANDS: turns within original_len, 0 < low < high */
+  int32_t original_len; /* YARN, BANDS: >= 1 */
+  int32_t reserved;     /* must be 0 */
+  double attn_factor;   /* factor on cos and sin; 0: the scaling's own (1, or YARN's) */
+} kvq_rope_params;
+
+/* A prepared turn: plain host data that the caller keeps and passes by
+ * pointer; made by kvq_rope_plan_init and not changed by any call.
+ * turns[i] = frequency i in turns per position, as a 64-bit binary fraction
+ * (f_i / (2 pi) * 2^64): position * turns[i] mod 2^64 is the angle, exact to
+ * the fraction's last bits at any 32-bit position. */
+typedef struct {
+  int32_t D, rot_dim, interleaved, reserved;
+  float scale;  /* factor on cos and sin */
+  float unused;
+  uint64_t turns[128];
+} kvq_rope_plan;
+
+KVQ_API kvq_status kvq_rope_plan_init(const kvq_rope_params* params, kvq_rope_plan* plan);
+
+/* Per-head RMS norm and rotary turn of queries and keys in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * w   (only with a weight; over the D channels of one head)
+ *   (y_a, y_b) -> m (y_a cos - y_b sin, y_b cos + y_a sin)  for every pair (a, b) of the plan,
+ * angle = position * f_i, all in fp32 and rounded once to in_dtype.
+ *  plan:   NULL leaves out the turn (then positions may be NULL).
+ *  q, k:   [n_tokens][H_q or H_kv][D] in_dtype, device; strides in elements
+ *          between tokens and between heads (channels contiguous), so heads
+ *          of a fused projection are read in place.  Either may be NULL with its output.
+ *  q_weight, k_weight: [D] in_dtype, device, or NULL (no norm of that tensor).
+ *  positions: [n_tokens] int32, device (any value; negative ones turn backwards).
+ *  q_out, k_out: [n_tokens][H][D] in_dtype, contiguous: the layout kvq_append
+ *          and the attention entries take.  May be the input itself when that is
+ *          contiguous; any other overlap is not allowed.
+ * cfg gives H_q, H_kv, D and in_dtype. */
+KVQ_API kvq_status kvq_qk_norm_rope(const kvq_config* cfg, const kvq_rope_plan* plan, const void* q,
+                                    int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                                    int64_t k_token_stride, int64_t k_head_stride, const void* q_weight,
+                                    const void* k_weight, float eps, const int32_t* positions, int32_t n_tokens,
+                                    void* q_out, void* k_out, void* stream);
+
+/* ---- pages of a paged cache ------------------------------------------------------
+ * The block table [batch][max_pages_per_seq] holds page ids, -1 where there
+ * is none.  refs [n_pages] counts, per page, the table entries that hold it;
+ * a page with refs 0 is free.  Both belong to the caller, like the lengths;
+ * these calls keep them consistent, all on the device, in stream order:
+ * they read no length on the host and can be captured.
+ *
+ * A sequence's pages hold its quantized tokens [0, q_end); the 16-bit window
+ * (residual_window > 0) is per sequence.  A page that several sequences hold
+ * is read by all of them and written by none: before tokens are appended,
+ * kvq_pages_reserve gives the sequence its own copy of a partly filled page.
+ *
+ * All need a paged config (page_tokens > 0) with batch <= 32768.  The
+ * workspace is of kvq_pages_workspace_bytes, 256-byte aligned, prepared by
+ * kvq_pages_init; its first word is the device status word
+ * (kvq_read_device_status).  Lists (seqs, src, dst, n_new) are int32 on the
+ * device, n of them known to the host. */
+KVQ_API kvq_status kvq_pages_workspace_bytes(const kvq_config* cfg, size_t* bytes);
+
+/* Prepares the workspace and counts refs from the block table (all -1: every
+ * page is free).  An entry outside [-1, n_pages) sets KVQ_DEV_PAGE and is not counted. */
+KVQ_API kvq_status kvq_pages_init(const kvq_config* cfg, const int32_t* block_table, int32_t* refs, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/* Frees sequences: their table rows become -1, each page loses one reader
+ * (free when that was the last), their lengths become 0.  An index outside
+ * [0, batch) sets KVQ_DEV_SEQ and is passed over; one listed twice is freed
+ * once.  An entry outside the pool, or a page with no readers, sets KVQ_DEV_PAGE. */
+KVQ_API kvq_status kvq_pages_release(const kvq_config* cfg, int32_t* block_table, int32_t* refs, int32_t* seq_lens,
+                                     const int32_t* seqs, int32_t n, void* workspace, size_t ws_bytes, void* stream);
+
+/* Sequence dst[i] becomes a copy of src[i]: it shares the pages that hold
+ * quantized tokens (each gets one more reader), gets a copy of the 16-bit
+ * window of every layer, and the length.  Pairs that are passed over, with
+ * KVQ_DEV_SEQ set: an index outside [0, batch); a dst that is not empty
+ * (length 0 and no pages) or that an earlier pair has too; a sequence listed both
+ * as a src and as a dst (every pair that has it).
+ * A page of src outside the pool (KVQ_DEV_PAGE) or a bad length (KVQ_DEV_LENGTH) passes the
+ * pair over too. */
+KVQ_API kvq_status kvq_pages_fork(const kvq_config* cfg, const kvq_cache* cache, int32_t* block_table, int32_t* refs,
+                                  int32_t* seq_lens, const int32_t* src, const int32_t* dst, int32_t n,
+                                  void* workspace, size_t ws_bytes, void* stream);
+
+/* Makes room for n_new[i] more tokens of sequence seqs[i] (lengths as before
+ * the append, and not advanced): its table row gets pages for tokens [0,
+ * length + n_new[i]), and if the page that the next quantized token goes to
+ * is partly filled and has other readers, a copy of it (all layers, K and V).  New pages
+ * are the free pages with the lowest ids, given out in list order and, within a sequence, in
+ * row order.  Where several listed sequences share such a page they are
+ * served in list order: the last reader left keeps the page itself.
+ * All or nothing: with too few free pages or a length beyond max_T
+ * (KVQ_DEV_CAPACITY), a bad or repeated index (KVQ_DEV_SEQ), a bad length or
+ * count (KVQ_DEV_LENGTH), or a table that breaks the rules above
+ * (KVQ_DEV_PAGE), nothing changes. */
+KVQ_API kvq_status kvq_pages_reserve(const kvq_config* cfg, const kvq_cache* cache, int32_t* block_table,
+                                     int32_t* refs, const int32_t* seq_lens, const int32_t* seqs,
+                                     const int32_t* n_new, int32_t n, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/* Moves the used pages together: with U pages in use, those with ids >= U go,
+ * in ascending order, to the free ids below U, in ascending order; the new
+ * table and counts are written to table_out and refs_out (which may be the
+ * inputs).  The bytes of the pages left behind stay as they were.  A
+ * table entry outside the pool or of a free page sets KVQ_DEV_PAGE and becomes -1. */
+KVQ_API kvq_status kvq_pages_compact(const kvq_config* cfg, const kvq_cache* cache, const int32_t* block_table,
+                                     const int32_t* refs, int32_t* table_out, int32_t* refs_out, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+/* ---- attention of a chunk of new tokens over the packed cache ---------------------
+ * The last n_b = cu_q[b+1] - cu_q[b] cached tokens of sequence b attend to
+ * the cache, causally, optionally through a sliding window that always keeps
+ * the first `sinks` tokens visible:
+ *   out_i = sum_j softmax_j(q_i.k_j / sqrt(D)) v_j  over cached tokens j with
+ *   j <= p_i and (window = 0 or j > p_i - window or j < sinks),
+ * p_i = seq_lens[b] - n_b + i.  One call covers a decode step (n_b = 1), the
+ * verification of a draft (a few) and prefill chunks (thousands), over every
+ * format, tier and page layout of the cache as kvq_append left it.
+ *  q, out:   [n_layers][total_q][H_q][D] in_dtype, device, 16-byte aligned; the rows of
+ *            a sequence back to back in batch order; q post-RoPE.
+ *  cu_q:     [batch + 1] int32, device, cu_q[0] = 0.  Rows from cu_q[batch]
+ *            to total_q are left as they are; a sequence may have no rows.
+ *  total_q, max_q: host values: rows of q, and a bound on every n_b.
+ *  seq_lens: [batch] int32, device, cached tokens INCLUDING the chunk (the
+ *            chunk was appended and the lengths advanced before this call).
+ *  window:   0 = every earlier token; else tokens in the sliding window, the
+ *            query's own among them.  sinks: >= 0 (no effect when window = 0).
+ * Products run on the tensor cores in in_dtype with fp32 sums: keys and values are
+ * dequantized to in_dtype, probabilities rounded to it; softmax statistics
+ * and outputs are held in fp32 and rounded once.
+ * A sequence with cu_q not ascending, n_b > max_q, a length outside [0,
+ * max_T] or n_b > length sets KVQ_DEV_LENGTH and its rows are left as they are; a page
+ * id out of range sets KVQ_DEV_PAGE and that page's tokens count as zeros.
+ * A NaN or infinity in a 16-bit window token reaches only the queries that see the token.
+ *  workspace: kvq_chunk_workspace_bytes bytes, 256-byte aligned, prepared once
+ *            by kvq_chunk_workspace_init; calls that may run at the same time
+ *            need workspaces of their own.  Its first word is the device
+ *            status word (kvq_read_device_status). */
+KVQ_API kvq_status kvq_chunk_workspace_bytes(const kvq_config* cfg, size_t* bytes);
+KVQ_API kvq_status kvq_chunk_workspace_init(const kvq_config* cfg, void* workspace, size_t ws_bytes, void* stream);
+KVQ_API kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, int32_t layer0,
+                                       int32_t n_layers, const void* q, const int32_t* cu_q, int32_t total_q,
+                                       int32_t max_q, const int32_t* seq_lens, int32_t window, int32_t sinks,
+                                       void* out, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
