@@ -38,6 +38,8 @@ SOURCES = [
     ("qk_norm_rope.cu", []),
     ("pages.cu", []),
     ("chunk_attention.cu", []),
+    ("chunk_attention_d128.cu", []),
+    ("chunk_attention_d256.cu", []),
 ]
 
 

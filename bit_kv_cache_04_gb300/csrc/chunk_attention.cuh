@@ -1,0 +1,69 @@
+// Attention of many new tokens over the packed cache (kvq_chunk_attention):
+// shared definitions and the kernel.
+//
+// For one (layer, sequence, kv head) the query rows are its new tokens times
+// the g query heads of the kv head, row r = token r / g, head r % g.  With S = Q K^T / sqrt(D),
+//   m = max_j S_j, P_j = 2^(log2e (S_j - m)), l = sum_j P_j, out = P V / l,
+// tile by tile of cached tokens with running m and l.  Both products run on
+// the 5th-generation tensor cores (tcgen05.mma, accumulators in TMEM); keys
+// and values are dequantized on the way from their packed blocks to the swizzled
+// shared-memory tiles that the products read, so packed bytes are all that HBM delivers.
+//
+// One CTA per SM, specialized warps, joined by mbarriers:
+//   softmax warps   one TMEM lane (query row) per thread: row maximum, exponentials, P back to
+//                   TMEM in the input dtype, the accumulator's rescaling, outputs
+//   dequant warps   packed blocks -> K and V tiles in shared memory (2 stages each)
+//   product warp    one thread issues every tcgen05.mma
+// D = 128: tiles of 128 tokens and two streams of softmax warps, each with
+// its own S and output accumulator, so that one stream's exponentials run
+// under the other's products.  PAIRED (more than 128 rows a sequence): both
+// streams take the same tokens and different rows (256 rows a CTA, a tile is
+// dequantized once for both).  Not PAIRED: the streams share the rows and take alternate tiles.
+// D = 256: tiles of 64 tokens, 128 rows, one output accumulator and one group
+// of softmax warps over two S buffers (TMEM holds no more).
+// Few rows: with at most 32 (64) rows the queries are repeated in every
+// quarter (half) of the 128 lanes and each repetition takes its own quarter
+// (half) of a tile's tokens, so that all four warps of a stream share the exponentials.
+//
+// The tiles of all (layer, kv head, sequence, row tile) units form one line
+// that is cut into equal runs, one per CTA, whatever the lengths; a unit cut
+// by run ends leaves partial rows (O, m, l) in the workspace, and the CTA that
+// takes the unit's last ticket joins them.  No CTA waits for another.
+#pragma once
+
+#include "block_codec.cuh"
+
+namespace kvq {
+
+constexpr int kChunkDequantWarps = 8;
+constexpr int kChunkSlots = 3;       // partial slots per CTA: first cut unit, last cut unit, whole units
+constexpr int kChunkTickets = 2;     // per CTA: units whose first run is the CTA's first or last one
+constexpr int kChunkSpin = 1 << 22;  // polls after which a wait gives up (KVQ_DEV_STALL)
+
+KVQ_HD constexpr int chunk_tile(int D) { return D == 128 ? 128 : 64; }
+KVQ_HD constexpr int chunk_streams(int D) { return D == 128 ? 2 : 1; }
+KVQ_HD constexpr int chunk_slot_rows(int D) { return 128 * chunk_streams(D); }
+KVQ_HD constexpr int chunk_part_row(int D) { return D + 4; }  // O, m, l, two pads
+
+struct ChunkArgs {
+  Layout lo;
+  CachePtrs cp;
+  int layer0, n_layers;
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  int total_q, max_q, window, sinks;
+  int rep;      // repetitions of the query rows over the lanes: 1, 2, 4
+  int by_warp;  // row tiles per sequence are many: count them with a warp per sequence
+  uint32_t* status;
+  uint32_t* tickets;    // [grid][kChunkTickets]
+  uint32_t* nonfinite;  // [grid][kChunkTickets]: a 16-bit window value of the unit is not finite
+  float* partials;      // [grid][kChunkSlots][slot rows][part row]
+  uint64_t turns[128];  // pre-RoPE keys: turns per position of every pair, 64-bit fractions
+};
+
+cudaError_t launch_chunk_d128(const ChunkArgs& a, bool paired, int grid, cudaStream_t s);
+cudaError_t launch_chunk_d256(const ChunkArgs& a, int grid, cudaStream_t s);
+
+}  // namespace kvq

@@ -192,6 +192,11 @@ def chunk_attention(cfg: O.Config, bufs: Dict[str, np.ndarray], layer: int, q: n
                     ds = (key_roundings * u + 2.0 ** -24 * D + 2.0 ** -20) * (qa @ ka[see].T) / math.sqrt(D)
                     rel = np.expm1(ds + ds.max(-1, keepdims=True)) + 4 * u
                     e = (p * rel) @ va[see]
+                    if cfg.in_dtype == 0:
+                        # P in fp16 is counted from a reference no larger than the row's
+                        # maximum, so the row's largest P, and with it l, is at least 1; below
+                        # 2^-14 P rounds to multiples of 2^-24: half of one per token
+                        e = e + 2.0 ** -25 * va[see].sum(0)
                     if cfg.flags & O.ROTATE_V:  # errors of the rotated domain spread over the block
                         e = np.repeat(np.sqrt(np.sum(e.reshape(g, -1, 128) ** 2, -1)), 128, -1)
                     bound[cu_q[b] + i, h * g:(h + 1) * g] = e + u * np.abs(o) + 2.0 ** -24
