@@ -104,6 +104,25 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
   const int most = cfg->D == 128 ? 4 : 2;  // a repetition keeps at least 32 tokens of a tile
   a.rep = rows <= 32 ? most : rows <= 64 ? 2 : 1;
   a.by_warp = rows > 4 * (paired ? 256 : 128);
+  // Staging: 32-token subtiles as single bulk copies; pages of fewer tokens
+  // as copies of their own when their bytes are whole 16-byte words and a
+  // tile has at most one page per lane; other pages by plain loads.
+  int sub = 0;
+  for (const FmtInfo* f : {&a.lo.kf, &a.lo.vf, &a.lo.kc, &a.lo.vc})
+    sub = std::max(sub, f->axis == KVQ_AXIS_CHANNEL ? f->row : 32 * f->row);
+  a.sub_bytes = (sub + 15) & ~15;
+  a.slot_bytes = a.sub_bytes * (chunk_tile(cfg->D) / 64);
+  a.copy_shift = 5;
+  if (a.lo.paged && a.lo.pt % 32 != 0) {
+    const bool fits = 32 % a.lo.pt == 0 && chunk_tile(cfg->D) / a.lo.pt <= 32 &&
+                      (a.lo.pt * a.lo.kf.row) % 16 == 0 && (a.lo.pt * a.lo.vf.row) % 16 == 0;
+    if (fits) {
+      a.small_pages = 1;
+      while ((1 << a.copy_shift) > a.lo.pt) --a.copy_shift;
+    } else {
+      a.direct = 1;
+    }
+  }
   cudaError_t e = cfg->D == 128 ? launch_chunk_d128(a, paired, w.grid, (cudaStream_t)stream)
                                 : launch_chunk_d256(a, w.grid, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention kernel");

@@ -12,6 +12,7 @@
 // One CTA per SM, specialized warps, joined by mbarriers:
 //   softmax warps   one TMEM lane (query row) per thread: row maximum, exponentials, P back to
 //                   TMEM in the input dtype, the accumulator's rescaling, outputs
+//   loader warp     packed bytes of half tiles ("pieces") into a ring of slots, bulk copies
 //   dequant warps   packed blocks -> K and V tiles in shared memory (2 stages each)
 //   product warp    one thread issues every tcgen05.mma
 // D = 128: tiles of 128 tokens and two streams of softmax warps, each with
@@ -38,6 +39,7 @@ namespace kvq {
 constexpr int kChunkDequantWarps = 8;
 constexpr int kChunkSlots = 3;       // partial slots per CTA: first cut unit, last cut unit, whole units
 constexpr int kChunkTickets = 2;     // per CTA: units whose first run is the CTA's first or last one
+constexpr int kChunkMaxSlots = 16;   // staging ring
 constexpr int kChunkSpin = 1 << 22;  // polls after which a wait gives up (KVQ_DEV_STALL)
 
 KVQ_HD constexpr int chunk_tile(int D) { return D == 128 ? 128 : 64; }
@@ -56,6 +58,12 @@ struct ChunkArgs {
   int total_q, max_q, window, sinks;
   int rep;      // repetitions of the query rows over the lanes: 1, 2, 4
   int by_warp;  // row tiles per sequence are many: count them with a warp per sequence
+  int direct;       // 1: pages cannot be staged by bulk copies
+  int small_pages;  // 1: pages of fewer than 32 tokens
+  int copy_shift;   // log2 of the tokens of one copy: 5, less for small pages
+  int sub_bytes;    // staged bytes of a 32-token subtile, the largest of the formats
+  int slot_bytes;   // of a staged piece (half a tile of one tensor)
+  int slots;        // pieces in the ring
   uint32_t* status;
   uint32_t* tickets;    // [grid][kChunkTickets]
   uint32_t* nonfinite;  // [grid][kChunkTickets]: a 16-bit window value of the unit is not finite

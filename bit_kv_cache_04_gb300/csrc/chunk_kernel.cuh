@@ -247,28 +247,32 @@ __device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t field_pair(uint32_t x, uint32_t mask, uint32_t bias2) {
   return hsub2u((x & mask) | 0x64006400u, bias2);
 }
-__device__ __forceinline__ void load_words(const uint8_t* p, int n, uint32_t* w) {
-  const uint32_t* a = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
-  if (reinterpret_cast<uintptr_t>(p) & 2) {
-    uint32_t x = a[0];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) {
-        const uint32_t y = a[i + 1];
-        w[i] = __funnelshift_r(x, y, 16);
-        x = y;
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) w[i] = a[i];
-  }
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(at));
+  return v;
 }
-__device__ __forceinline__ void codes32(const uint8_t* p, int bits, bool raw, const uint32_t* pair_table,
+__device__ __forceinline__ float lds_half(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(at));
+  return __half2float(__ushort_as_half(v));
+}
+// n words from a 2-byte aligned shared address (aligned loads, shifted; the staging
+// area has a word to spare behind its last slot)
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
+  const uint32_t a = p & ~3u, sh = (p & 2) * 8;
+  uint32_t x[N + 1];
+#pragma unroll
+  for (int i = 0; i <= N; ++i) x[i] = lds32(a + 4 * i);
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], sh);
+}
+__device__ __forceinline__ void codes32(uint32_t p, int bits, bool raw, const uint32_t* pair_table,
                                         uint32_t (&h)[16]) {
-  uint32_t w[8];
   if (bits == 4) {
-    load_words(p, 4, w);
+    uint32_t w[4];
+    load_words(p, w);
     if (pair_table) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) h[i] = pair_table[(w[i / 4] >> (8 * (i % 4))) & 0xff];
@@ -284,7 +288,8 @@ __device__ __forceinline__ void codes32(const uint8_t* p, int bits, bool raw, co
       h[4 * i + 3] = field_pair(__byte_perm(w[i], v, 0x3733), 0x000f000fu, bias);
     }
   } else if (bits == 8) {
-    load_words(p, 8, w);
+    uint32_t w[8];
+    load_words(p, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t u = w[i] ^ 0x80808080u;
@@ -292,7 +297,8 @@ __device__ __forceinline__ void codes32(const uint8_t* p, int bits, bool raw, co
       h[2 * i + 1] = hsub2u(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
     }
   } else if (bits == 3) {
-    load_words(p, 3, w);
+    uint32_t w[3];
+    load_words(p, w);
     const uint32_t g[4] = {w[0], __funnelshift_r(w[0], w[1], 24), __funnelshift_r(w[1], w[2], 16), w[2] >> 8};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -302,7 +308,8 @@ __device__ __forceinline__ void codes32(const uint8_t* p, int bits, bool raw, co
         h[4 * k + j] = field_pair((t & 7u) | ((t & 0x38u) << 13), 0x00070007u, 0x64046404u);
       }
   } else {
-    load_words(p, 2, w);
+    uint32_t w[2];
+    load_words(p, w);
     const uint32_t bias = raw ? 0x64006400u : 0x64026402u;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -323,10 +330,10 @@ struct BlockScale {
   float s, z;
   bool big;  // a value may leave fp16's range
 };
-__device__ __forceinline__ BlockScale block_scale_of_run(const uint8_t* blk, const FmtInfo& f) {
+__device__ __forceinline__ BlockScale block_scale_of_run(uint32_t blk, const FmtInfo& f) {
   BlockScale r;
-  r.s = block_scale(blk);
-  r.z = f.zp ? block_scale(blk + 2) : 0.f;
+  r.s = lds_half(blk);
+  r.z = f.zp ? lds_half(blk + 2) : 0.f;
   if (!(fabsf(r.s) <= 65504.f)) r.s = 0.f;
   if (!(fabsf(r.z) <= 65504.f)) r.z = 0.f;
   const float top = f.codebook ? 1.f : f.zp ? (float)((1 << f.bits) - 1) : (float)(1 << (f.bits - 1));
@@ -390,12 +397,14 @@ __device__ __forceinline__ TileTokens tile_tokens(const Unit& u, int j) {
   return r;
 }
 
-// Dequantizes one tensor's tile into the swizzled shared-memory tile at dst.  Runs of 32 values along
-// the storage axis; rows of the tile are tokens (per-token blocks, values
-// along channels) or channels (per-channel blocks, values along tokens).
+// Dequantizes half of one tensor's tile (a piece: 256 runs of 32 values, one
+// per dequantizing thread) from its staged packed bytes into the swizzled
+// shared-memory tile at dst.  Rows of the tile are tokens (per-token blocks,
+// runs along channels) or channels (per-channel blocks, runs along tokens).
 template <int D, int DT>
 struct Dequant {
   static constexpr int NT = chunk_tile(D);
+  static constexpr int PIECE = NT / 2;  // tokens of a piece
   static constexpr int THREADS = 32 * kChunkDequantWarps;
 
   const ChunkArgs& a;
@@ -405,37 +414,27 @@ struct Dequant {
   int qe, ce;
   const uint32_t* pair_table;
   volatile uint32_t* nonfinite;
+  int a0;           // the piece's first token
+  uint32_t staged;  // its packed bytes: 32-token subtiles, a.sub_bytes apart
+  uint32_t bad;     // copies (of a.copy_shift tokens each) whose page id is out of range
 
   __device__ __forceinline__ bool turned() const { return which == 0 && (a.lo.flags & KVQ_K_PRE_ROPE); }
-
-  // block of the run (row, run) of a quantized tier: address, codes' address
-  __device__ __forceinline__ const uint8_t* token_block(int t, int run, const FmtInfo** f, const uint8_t** codes) const {
-    const bool cold = t < ce;
-    const FmtInfo& fm = cold ? fmt_cold(a.lo, which) : fmt_main(a.lo, which);
-    bool bad = false;
-    const uint8_t* row = cold ? cold_row(a.lo, a.cp, which, u.layer, u.b, u.h, t)
-                              : main_row(a.lo, a.cp, which, u.layer, u.b, u.h, t, &bad);
-    *f = &fm;
-    if (!row) {
-      atomicOr(a.status, KVQ_DEV_PAGE);
-      return nullptr;
-    }
-    const int per = fm.group / 32;  // runs of a block: 1 or 4
-    const uint8_t* blk = row + (per == 1 ? run : run >> 2) * fm.bb;
-    *codes = blk + (fm.zp ? 4 : 2) + (per == 1 ? 0 : (run & 3) * 4 * fm.bits);
+  __device__ __forceinline__ const FmtInfo& fmt_of(int t) const {
+    return t < ce ? fmt_cold(a.lo, which) : fmt_main(a.lo, which);
+  }
+  // block of the run (token or channel row, run) of a quantized tier and its codes
+  __device__ __forceinline__ uint32_t token_block(int t, int run, const FmtInfo& f, uint32_t* codes) const {
+    const int per = f.group / 32;  // runs of a block: 1 or 4
+    const uint32_t blk = staged + ((t - a0) >> 5) * a.sub_bytes + (t & 31) * f.row + (per == 1 ? run : run >> 2) * f.bb;
+    *codes = blk + (f.zp ? 4 : 2) + (per == 1 ? 0 : (run & 3) * 4 * f.bits);
     return blk;
   }
-  __device__ __forceinline__ const uint8_t* channel_block(int t, int c, const FmtInfo** f, const uint8_t** codes) const {
-    const bool cold = t < ce;
-    const FmtInfo& fm = cold ? fmt_cold(a.lo, which) : fmt_main(a.lo, which);
-    bool bad = false;
-    const uint8_t* row = cold ? cold_row(a.lo, a.cp, which, u.layer, u.b, u.h, t)
-                              : main_row(a.lo, a.cp, which, u.layer, u.b, u.h, t, &bad);
-    *f = &fm;
-    const uint8_t* blk = row + (int64_t)c * fm.bb;
-    *codes = blk + (fm.zp ? 4 : 2);
+  __device__ __forceinline__ uint32_t channel_block(int t, int c, const FmtInfo& f, uint32_t* codes) const {
+    const uint32_t blk = staged + ((t - a0) >> 5) * a.sub_bytes + c * f.bb;
+    *codes = blk + (f.zp ? 4 : 2);
     return blk;
   }
+  __device__ __forceinline__ bool no_page(int t) const { return (bad >> ((t - a0) >> a.copy_shift)) & 1u; }
 
   // 16-bit window values as they are; values that are not finite become 0 in V's tile (see fix_rows)
   __device__ __forceinline__ uint32_t clean(uint32_t w) const {
@@ -465,43 +464,46 @@ struct Dequant {
   }
   // channel c of tokens t .. t + 31, zeros from token T on
   __device__ __forceinline__ void raw_channel_run(int t, int c, uint32_t (&h)[16]) const {
+    const uint16_t* p = resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t) + c;
+    int left = a.lo.ring - t % a.lo.ring;  // slots until the ring wraps
     uint32_t x[32];
 #pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      x[j] = *p;  // slots past the length exist, and count as zeros below
+      --left;
+      p += left == 0 ? (int64_t)a.lo.D - (int64_t)a.lo.ring * a.lo.D : (int64_t)a.lo.D;
+    }
+#pragma unroll
     for (int j = 0; j < 32; ++j)
-      x[j] = t + j < u.T ? resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t + j)[c] : 0u;
+      if (t + j >= u.T) x[j] = 0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) h[j] = clean(x[2 * j] | (x[2 * j + 1] << 16));
   }
 
   // One run, turn aside, in the input dtype.
   __device__ __forceinline__ void token_run(int t, int run, uint32_t (&h)[16]) const {
-    if (t >= u.T) {
+    if (t >= u.T || no_page(t)) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) h[i] = 0;
     } else if (t >= qe) {
       raw_token_run(t, run, h);
     } else {
-      const FmtInfo* f;
-      const uint8_t* codes;
-      const uint8_t* blk = token_block(t, run, &f, &codes);
-      if (!blk) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) h[i] = 0;
-        return;
-      }
-      codes32(codes, f->bits, f->zp, f->codebook ? pair_table : nullptr, h);
-      scale32<DT>(h, block_scale_of_run(blk, *f), f->zp);
+      const FmtInfo& f = fmt_of(t);
+      uint32_t codes;
+      const uint32_t blk = token_block(t, run, f, &codes);
+      codes32(codes, f.bits, f.zp, f.codebook ? pair_table : nullptr, h);
+      scale32<DT>(h, block_scale_of_run(blk, f), f.zp);
     }
   }
   __device__ __forceinline__ void channel_run(int t, int c, uint32_t (&h)[16]) const {
     if (t >= qe) {
       raw_channel_run(t, c, h);
     } else {
-      const FmtInfo* f;
-      const uint8_t* codes;
-      const uint8_t* blk = channel_block(t, c, &f, &codes);
-      codes32(codes, f->bits, f->zp, nullptr, h);
-      scale32<DT>(h, block_scale_of_run(blk, *f), f->zp);
+      const FmtInfo& f = fmt_of(t);
+      uint32_t codes;
+      const uint32_t blk = channel_block(t, c, f, &codes);
+      codes32(codes, f.bits, f.zp, nullptr, h);
+      scale32<DT>(h, block_scale_of_run(blk, f), f.zp);
     }
   }
 
@@ -521,22 +523,17 @@ struct Dequant {
   };
   __device__ __forceinline__ void loose_token(int t, int run, Loose& l) const {
     l.raw = true;
-    if (t >= u.T) {
+    if (t >= u.T || no_page(t)) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) l.h[i] = 0;
     } else if (t >= qe) {
       raw_token_run(t, run, l.h);
     } else {
-      const FmtInfo* f;
-      const uint8_t* codes;
-      const uint8_t* blk = token_block(t, run, &f, &codes);
-      if (!blk) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) l.h[i] = 0;
-        return;
-      }
-      codes32(codes, f->bits, f->zp, nullptr, l.h);
-      const BlockScale b = block_scale_of_run(blk, *f);
+      const FmtInfo& f = fmt_of(t);
+      uint32_t codes;
+      const uint32_t blk = token_block(t, run, f, &codes);
+      codes32(codes, f.bits, f.zp, nullptr, l.h);
+      const BlockScale b = block_scale_of_run(blk, f);
       l.raw = false;
       l.s = b.s;
       l.z = b.z;
@@ -547,11 +544,11 @@ struct Dequant {
     if (l.raw) {
       raw_channel_run(t, c, l.h);
     } else {
-      const FmtInfo* f;
-      const uint8_t* codes;
-      const uint8_t* blk = channel_block(t, c, &f, &codes);
-      codes32(codes, f->bits, f->zp, nullptr, l.h);
-      const BlockScale b = block_scale_of_run(blk, *f);
+      const FmtInfo& f = fmt_of(t);
+      uint32_t codes;
+      const uint32_t blk = channel_block(t, c, f, &codes);
+      codes32(codes, f.bits, f.zp, nullptr, l.h);
+      const BlockScale b = block_scale_of_run(blk, f);
       l.s = b.s;
       l.z = b.z;
     }
@@ -570,10 +567,10 @@ struct Dequant {
   // Keys stored pre-RoPE: the runs of channels i and i + D/2 together.
   __device__ void turned_tile(const TileTokens& tt, bool per_channel) const {
     if (per_channel) {
-      constexpr int G = NT / 32;  // token groups of the tile
+      constexpr int G = PIECE / 32;  // token groups of the piece
       for (int e = warp * 32 + lane; e < (D / 2) * G; e += THREADS) {
-        const int c = (e & 7) | ((e / (8 * G)) << 3), run = (e >> 3) % G;
-        const int t = tt.t0 + 32 * run;
+        const int c = (e & 7) | ((e / (8 * G)) << 3);
+        const int t = a0 + 32 * ((e >> 3) % G), run = (t - tt.t0) >> 5;
         if (t + 32 <= tt.v0 || t >= tt.v1) continue;
         Loose x, y;
         loose_channel(t, c, x);
@@ -598,9 +595,8 @@ struct Dequant {
       }
     } else {
       constexpr int R = D / 64;  // runs of half a row
-      for (int e = warp * 32 + lane; e < NT * R; e += THREADS) {
-        const int row = (e & 7) | ((e / (8 * R)) << 3), run = (e >> 3) % R;
-        const int t = tt.t0 + row;
+      for (int e = warp * 32 + lane; e < PIECE * R; e += THREADS) {
+        const int run = (e >> 3) % R, t = a0 + ((e & 7) | ((e / (8 * R)) << 3)), row = t - tt.t0;
         if (t < (tt.v0 & ~31) || t >= ((tt.v1 + 31) & ~31)) continue;
         Loose x, y;
         loose_token(t, run, x);
@@ -621,8 +617,8 @@ struct Dequant {
 
   // Window tokens of a rotated format, turned into the rotated domain: a warp per token.
   __device__ void rotated_window(const TileTokens& tt) const {
-    const int t1 = min(min(u.T, tt.t0 + NT), (tt.v1 + 31) & ~31);
-    for (int t = max(qe, tt.v0 & ~31) + warp; t < t1; t += kChunkDequantWarps) {
+    const int t1 = min(min(u.T, a0 + PIECE), (tt.v1 + 31) & ~31);
+    for (int t = max(max(qe, a0), tt.v0 & ~31) + warp; t < t1; t += kChunkDequantWarps) {
       const uint2* p = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t));
 #pragma unroll
       for (int c = 0; c < D / 128; ++c) {
@@ -640,36 +636,118 @@ struct Dequant {
     }
   }
 
-  __device__ void tile(const TileTokens& tt) const {
+  __device__ void piece(const TileTokens& tt) const {
     const bool per_channel = fmt_main(a.lo, which).axis == KVQ_AXIS_CHANNEL;
     if (turned()) {
       turned_tile(tt, per_channel);
       return;
     }
+    const int e = warp * 32 + lane;
+    uint32_t h[16];
     if (per_channel) {
-      constexpr int G = NT / 32;
-      for (int e = warp * 32 + lane; e < D * G; e += THREADS) {
-        const int c = (e & 7) | ((e / (8 * G)) << 3), run = (e >> 3) % G;
-        const int t = tt.t0 + 32 * run;
-        if (t + 32 <= tt.v0 || t >= tt.v1) continue;
-        uint32_t h[16];
-        channel_run(t, c, h);
-        store32(dst, c, run, D, h);
-      }
+      constexpr int G = PIECE / 32;
+      const int c = (e & 7) | ((e / (8 * G)) << 3), t = a0 + 32 * ((e >> 3) % G);
+      if (t + 32 <= tt.v0 || t >= tt.v1) return;
+      channel_run(t, c, h);
+      store32(dst, c, (t - tt.t0) >> 5, D, h);
       return;
     }
     constexpr int R = D / 32;
     const bool rotated = (a.lo.flags & (which ? KVQ_ROTATE_V : KVQ_ROTATE_K)) != 0;
-    for (int e = warp * 32 + lane; e < NT * R; e += THREADS) {
-      const int row = (e & 7) | ((e / (8 * R)) << 3), run = (e >> 3) % R;
-      const int t = tt.t0 + row;
-      if (t < (tt.v0 & ~31) || t >= ((tt.v1 + 31) & ~31)) continue;
-      if (rotated && t >= qe && t < u.T) continue;
-      uint32_t h[16];
+    const int run = (e >> 3) % R, t = a0 + ((e & 7) | ((e / (8 * R)) << 3));
+    if (t >= (tt.v0 & ~31) && t < ((tt.v1 + 31) & ~31) && !(rotated && t >= qe && t < u.T)) {
       token_run(t, run, h);
-      store32(dst, row, run, NT, h);
+      store32(dst, t - tt.t0, run, NT, h);
     }
     if (rotated) rotated_window(tt);
+  }
+};
+
+// ---- staging -----------------------------------------------------------------------------
+
+// The loader warp: the packed bytes of every piece into a ring of
+// shared-memory slots, as bulk copies of 32-token subtiles (of pages, when those are smaller).
+template <int D>
+struct Loader {
+  static constexpr int NT = chunk_tile(D), PIECE = NT / 2, SUBS = PIECE / 32;
+
+  const ChunkArgs& a;
+  int lane;
+
+  // page id of the lane-th page of the tile (small pages)
+  __device__ __forceinline__ int page_id(const Unit& u, const TileTokens& tt, int qe) const {
+    const int t = tt.t0 + (lane << a.copy_shift);
+    if (!a.small_pages || lane >= (NT >> a.copy_shift) || t >= qe) return -1;
+    return __ldg(a.cp.block_table + (int64_t)u.b * a.lo.max_pages + t / a.lo.pt);
+  }
+
+  __device__ __forceinline__ static void copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+  }
+
+  // One piece into the slot at `dst`; the slot's barrier completes once the bytes are there.
+  __device__ __forceinline__ void piece(const Unit& u, const TileTokens& tt, int which, int half, int qe, int ce, int pid,
+                                        uint32_t dst, uint32_t bar, uint32_t* bad_at) const {
+    const int a0 = tt.t0 + half * PIECE;
+    if (a.direct) {
+      piece_direct(u, tt, which, a0, qe, dst, bar, bad_at);
+      return;
+    }
+    const int n = PIECE >> a.copy_shift;  // copies of the piece, one per lane
+    const int t = a0 + (lane << a.copy_shift), sub = t & ~31;
+    bool active = lane < n && t < qe && sub + 32 > tt.v0 && sub < tt.v1, bad = false;
+    const bool cold = t < ce;
+    const FmtInfo& f = cold ? fmt_cold(a.lo, which) : fmt_main(a.lo, which);
+    const uint8_t* src = nullptr;
+    int p = 0;
+    if (a.small_pages) p = __shfl_sync(0xffffffffu, pid, (lane + half * n) & 31);
+    if (active) {
+      if (a.small_pages) {
+        bad = p < 0 || p >= a.lo.n_pages;
+        const uint8_t* base = which ? a.cp.v_main : a.cp.k_main;
+        src = base + (((int64_t)u.layer * a.lo.n_pages + p) * a.lo.H + u.h) * a.lo.pt * f.row;
+      } else {
+        src = cold ? cold_row(a.lo, a.cp, which, u.layer, u.b, u.h, t)
+                   : main_row(a.lo, a.cp, which, u.layer, u.b, u.h, t, &bad);
+      }
+    }
+    const uint32_t bytes = f.axis == KVQ_AXIS_CHANNEL ? f.row : f.row << a.copy_shift;
+    active = active && !bad && span_ok(a.lo, a.cp, which + (cold ? 2 : 0), src, bytes);
+    const uint32_t bads = __ballot_sync(0xffffffffu, bad);
+    const uint32_t total = __reduce_add_sync(0xffffffffu, active ? bytes : 0u);
+    if (lane == 0) {
+      *bad_at = bads;
+      if (bads) atomicOr(a.status, KVQ_DEV_PAGE);
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(total) : "memory");
+    }
+    __syncwarp();
+    if (active) copy(dst + ((t - a0) >> 5) * a.sub_bytes + (t & 31) * f.row, src, bytes, bar);
+  }
+
+  // Pages whose rows are no whole 16-byte words, or do not divide a subtile: 2 bytes at a time.
+  __device__ __noinline__ void piece_direct(const Unit& u, const TileTokens& tt, int which, int a0, int qe, uint32_t dst,
+                                            uint32_t bar, uint32_t* bad_at) const {
+    const FmtInfo& f = fmt_main(a.lo, which);
+    for (int i = 0; i < PIECE; ++i) {
+      const int t = a0 + i;
+      if (t >= qe || (t & ~31) + 32 <= tt.v0 || (t & ~31) >= tt.v1) continue;
+      bool bad = false;
+      const uint8_t* src = main_row(a.lo, a.cp, which, u.layer, u.b, u.h, t, &bad);
+      const uint32_t to = dst + (i >> 5) * a.sub_bytes + (t & 31) * f.row;
+      for (int e = 2 * lane; e < f.row; e += 64) {
+        // a page out of range reads as blocks of scale 0 (and zero 0)
+        const uint16_t v = bad ? (uint16_t)0 : *reinterpret_cast<const uint16_t*>(src + e);
+        asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(to + e), "h"(v) : "memory");
+      }
+      if (bad && lane == 0) atomicOr(a.status, KVQ_DEV_PAGE);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      *bad_at = 0;
+      bar_arrive(bar);
+    }
   }
 };
 
@@ -682,15 +760,17 @@ struct ChunkShape {
   static constexpr int QTILES = PAIRED ? 2 : 1;
   static constexpr int RT = 128 * QTILES;  // rows of a row tile
   static constexpr int SOFT_WARPS = 4 * STREAMS;
-  static constexpr int WARPS = SOFT_WARPS + kChunkDequantWarps + 1;
+  static constexpr int WARPS = SOFT_WARPS + kChunkDequantWarps + 2;  // and the loader and product warps
   static constexpr int THREADS = 32 * WARPS;
   static constexpr uint32_t Q_BYTES = 128u * D * 2;
   static constexpr uint32_t TILE_BYTES = (uint32_t)NT * D * 2;  // 32 KiB
-  static constexpr uint32_t SMEM = 1024 + QTILES * Q_BYTES + 4 * TILE_BYTES;
+  static constexpr uint32_t FIXED = 1024 + QTILES * Q_BYTES + 4 * TILE_BYTES;  // the rest of the SM's is staging
   static constexpr uint32_t S_COL = 0, O_COL = D == 128 ? 256 : 256;
 };
 
 struct ChunkShared {
+  uint64_t raw_full[kChunkMaxSlots], raw_empty[kChunkMaxSlots];
+  uint32_t bad_pages[kChunkMaxSlots];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], s_full[2], p_full[2], o_full, pv_done, soft;
   uint32_t tmem;
   uint32_t gave_up;
@@ -938,6 +1018,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_at = smem_addr(smem), k_at = q_at + C::QTILES * C::Q_BYTES, v_at = k_at + 2 * C::TILE_BYTES;
+  const uint32_t raw_at = v_at + 2 * C::TILE_BYTES;
 
   // set-up that needs nothing of the stream's earlier work
   if (tid == 0) {
@@ -949,6 +1030,10 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
       bar_init(smem_addr(&sh.q_full[i]), 4);
       bar_init(smem_addr(&sh.s_full[i]), 1);
       bar_init(smem_addr(&sh.p_full[i]), 4);
+    }
+    for (int i = 0; i < a.slots; ++i) {
+      bar_init(smem_addr(&sh.raw_full[i]), 1);
+      bar_init(smem_addr(&sh.raw_empty[i]), kChunkDequantWarps);
     }
     bar_init(smem_addr(&sh.o_full), 1);
     bar_init(smem_addr(&sh.pv_done), 1);
@@ -1047,10 +1132,10 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= C::SOFT_WARPS) {
+  } else if (warp >= C::SOFT_WARPS && warp < C::WARPS - 2) {
     // ---- dequantization ---------------------------------------------------------------
     const int dw = warp - C::SOFT_WARPS;
-    uint32_t kt = 0;
+    uint32_t kt = 0, slot = 0, lap = 0;
     bool ok = true;
     for (; more && ok; more = next_run<D, RT>(a, line, run)) {
       const Unit& u = run.u;
@@ -1063,14 +1148,60 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
 #pragma unroll 1
         for (int which = 0; which < 2 && ok; ++which) {
           ok = __all_sync(0xffffffffu, bar_wait(smem_addr(which ? &sh.v_empty[st] : &sh.k_empty[st]), par, &sh.gave_up));
-          if (!ok) break;
-          const Dequant<D, DT> dq{a, in_cache, which, dw, lane, (which ? v_at : k_at) + st * C::TILE_BYTES, qe, ce,
-                                  sh.pair_table, &sh.nonfinite};
-          dq.tile(tt);
+#pragma unroll 1
+          for (int half = 0; half < 2 && ok; ++half) {
+            ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.raw_full[slot]), lap & 1, &sh.gave_up));
+            if (!ok) break;
+            const Dequant<D, DT> dq{a, in_cache, which, dw, lane, (which ? v_at : k_at) + st * C::TILE_BYTES, qe, ce,
+                                    sh.pair_table, &sh.nonfinite, tt.t0 + half * (NT / 2),
+                                    raw_at + slot * a.slot_bytes, *(volatile uint32_t*)&sh.bad_pages[slot]};
+            dq.piece(tt);
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&sh.raw_empty[slot]));
+            if (++slot == (uint32_t)a.slots) {
+              slot = 0;
+              ++lap;
+            }
+          }
           proxy_fence();
           __syncwarp();
-          if (lane == 0) bar_arrive(smem_addr(which ? &sh.v_full[st] : &sh.k_full[st]));
+          if (ok && lane == 0) bar_arrive(smem_addr(which ? &sh.v_full[st] : &sh.k_full[st]));
         }
+      }
+    }
+  } else if (warp == C::WARPS - 2) {
+    // ---- staging ------------------------------------------------------------------------
+    const Loader<D> ld{a, lane};
+    uint32_t slot = 0, lap = 0, filled = 0;
+    bool ok = true;
+    for (; more && ok; more = next_run<D, RT>(a, line, run)) {
+      Unit u = run.u;
+      u.layer += a.layer0;
+      const int qe = q_end_of(a.lo, u.T), ce = c_end_of(a.lo, u.T);
+      int pid = ld.page_id(u, tile_tokens<D>(u, run.t0), qe);
+      for (int j = run.t0; j < run.t1 && ok; ++j) {
+        const TileTokens tt = tile_tokens<D>(u, j);
+        // the next tile's page ids load while this one waits for slots
+        const int next_pid = j + 1 < run.t1 ? ld.page_id(u, tile_tokens<D>(u, j + 1), qe) : -1;
+#pragma unroll 1
+        for (int i = 0; i < 4 && ok; ++i) {
+          ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.raw_empty[slot]), (lap & 1) ^ 1, &sh.gave_up));
+          if (!ok) break;
+          ld.piece(u, tt, i >> 1, i & 1, qe, ce, pid, raw_at + slot * a.slot_bytes, smem_addr(&sh.raw_full[slot]),
+                   &sh.bad_pages[slot]);
+          ++filled;
+          if (++slot == (uint32_t)a.slots) {
+            slot = 0;
+            ++lap;
+          }
+        }
+        pid = next_pid;
+      }
+    }
+    // the copies in flight land before the CTA ends, also when another warp has given up
+    for (uint32_t i = 0; i < (uint32_t)a.slots && i < filled; ++i) {
+      const uint32_t back = filled - 1 - i, s = back % a.slots, n = back / a.slots;
+      for (int k = 0; k < kChunkSpin && !bar_test(smem_addr(&sh.raw_full[s]), n & 1); ++k) {
       }
     }
   } else {
@@ -1329,13 +1460,20 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
 }
 
 template <int D, int DT, bool PAIRED>
-cudaError_t launch_chunk(const ChunkArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   using C = ChunkShape<D, PAIRED>;
+  // all of the SM's shared memory that the tiles leave is staging
+  const uint32_t all = 227 * 1024 - (uint32_t)sizeof(ChunkShared);
+  const uint32_t left = all - C::FIXED - 16;
+  a.slots = (int)(left / a.slot_bytes);
+  if (a.slots > kChunkMaxSlots) a.slots = kChunkMaxSlots;
+  if (a.slots < 1) return cudaErrorInvalidConfiguration;
+  const uint32_t smem = C::FIXED + 16 + a.slots * a.slot_bytes;
   // set on every call: the attribute belongs to the current device
   cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, PAIRED>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_attention_kernel<D, DT, PAIRED>, dim3(grid), dim3(C::THREADS), C::SMEM, s, a);
+  return launch_dependent(chunk_attention_kernel<D, DT, PAIRED>, dim3(grid), dim3(C::THREADS), smem, s, a);
 }
 
 }  // namespace
