@@ -36,11 +36,13 @@
 
 namespace kvq {
 
-constexpr int kChunkDequantWarps = 8;
+constexpr int kChunkDequantWarps = 8;  // two for each piece of a tile: K, V, two halves each
 constexpr int kChunkSlots = 3;       // partial slots per CTA: first cut unit, last cut unit, whole units
 constexpr int kChunkTickets = 2;     // per CTA: units whose first run is the CTA's first or last one
-constexpr int kChunkMaxSlots = 16;   // staging ring
-constexpr int kChunkSpin = 1 << 22;  // polls after which a wait gives up (KVQ_DEV_STALL)
+constexpr int kChunkMaxSlots = 16;   // staging ring, in pieces
+constexpr int kChunkBars = 8;        // barriers of one kind of piece: more tiles than the ring can span
+constexpr int kChunkSpin = 1 << 20;  // polls after which a wait gives up (KVQ_DEV_STALL)
+constexpr uint32_t kChunkPollNs = 2000;  // a poll's own wait, at most
 
 KVQ_HD constexpr int chunk_tile(int D) { return D == 128 ? 128 : 64; }
 KVQ_HD constexpr int chunk_streams(int D) { return D == 128 ? 2 : 1; }
@@ -57,6 +59,7 @@ struct ChunkArgs {
   const int32_t* seq_lens;
   int total_q, max_q, window, sinks;
   int rep;      // repetitions of the query rows over the lanes: 1, 2, 4
+  uint32_t g_magic;  // floor(2^32 / g) + 1
   int by_warp;  // row tiles per sequence are many: count them with a warp per sequence
   int direct;       // 1: pages cannot be staged by bulk copies
   int small_pages;  // 1: pages of fewer than 32 tokens

@@ -19,15 +19,16 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kChunkPollNs)
       : "memory");
   return ok != 0;
 }
 // Waits, boundedly, for the phase of that parity.  After too many polls, or
 // once another warp has given up, the answer is false and the caller leaves.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+#pragma unroll 1
   for (int i = 0; i < kChunkSpin; ++i) {
     if (bar_test(bar, parity)) return true;
     if (*gave_up) return false;
@@ -41,6 +42,14 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+// One lane of a converged warp.  The instructions below and the bulk copies take their
+// operands from uniform registers: issued by `lane == 0`, or by several lanes with
+// operands of their own, each becomes a loop over the lanes (270 cycles a product).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 // D[tmem] (+)= A[shared] B[shared]
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -86,6 +95,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
@@ -127,10 +146,29 @@ struct Unit {
   int st, lo_tile, nt;   // sink tiles, first window tile, tiles
 };
 
+// One CTA's run of a unit: tiles [t0, t1) of it.  Each warp keeps its own in shared memory: registers are short.
+struct Run {
+  Unit u;
+  int t0, t1;
+  int pos;               // place of the run's first tile on the line
+  int first;             // the CTA's first run
+};
+
+struct LineStart {  // found once per CTA
+  int lh, b, rt, tile;
+  int begin, end;  // the CTA's stretch of the line
+  int per_cta;
+};
+
+// r / g for query rows (g <= 8, r < 2^28: exact with the rounded-up reciprocal)
+__device__ __forceinline__ int div_g(const ChunkArgs& a, int r) {
+  return a.lo.g == 1 ? r : (int)__umulhi((uint32_t)r, a.g_magic);
+}
+
 __device__ __forceinline__ bool valid_seq(const ChunkArgs& a, int b, int* n, int* T, int* cu) {
   const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), t = __ldg(a.seq_lens + b);
   *cu = c0;
-  *n = c1 - c0;
+  *n = (int)((uint32_t)c1 - (uint32_t)c0);
   *T = t;
   return c0 >= 0 && c1 >= c0 && c1 <= a.total_q && c1 - c0 <= a.max_q && t >= c1 - c0 && t <= a.lo.max_T;
 }
@@ -140,8 +178,8 @@ __device__ __forceinline__ void unit_tiles(const ChunkArgs& a, Unit& u) {
   constexpr int NT = chunk_tile(D);
   u.r0 = u.rt * RT;
   u.rows = min(RT, u.n * a.lo.g - u.r0);
-  u.p_lo = u.T - u.n + u.r0 / a.lo.g;
-  u.p_hi = u.T - u.n + (u.r0 + u.rows - 1) / a.lo.g;
+  u.p_lo = u.T - u.n + div_g(a, u.r0);
+  u.p_hi = u.T - u.n + div_g(a, u.r0 + u.rows - 1);
   u.lo = a.window ? max(0, u.p_lo - a.window + 1) : 0;
   u.sink = min(a.sinks, u.lo);
   u.lo_tile = u.lo / NT;
@@ -156,15 +194,15 @@ __device__ __forceinline__ int seq_row_tiles(const ChunkArgs& a, int n) {
 
 // Tiles of sequence b (one layer and kv head): summed by one thread, or by the 32 lanes of a warp.
 template <int D, int RT>
-__device__ __forceinline__ int64_t seq_tiles(const ChunkArgs& a, int b, int lane, int lanes, bool* bad) {
+__device__ __forceinline__ int seq_tiles(const ChunkArgs& a, int b, int lane, int lanes, bool* bad) {
   Unit u;
-  u.b = b;
   if (!valid_seq(a, b, &u.n, &u.T, &u.cu)) {
     *bad = true;
     return 0;
   }
-  int64_t sum = 0;
+  int sum = 0;
   const int nrt = seq_row_tiles<D, RT>(a, u.n);
+#pragma unroll 1
   for (u.rt = lane; u.rt < nrt; u.rt += lanes) {
     unit_tiles<D, RT>(a, u);
     sum += u.nt;
@@ -172,73 +210,60 @@ __device__ __forceinline__ int64_t seq_tiles(const ChunkArgs& a, int b, int lane
   return sum;
 }
 
-// The unit after u (of the same or the next sequence, kv head, layer); false
-// past the last one (only where lengths changed under the kernel).
+// The CTA's first run (step 0) or the one after r; false past the last.  One lane of a warp.
 template <int D, int RT>
-__device__ __forceinline__ bool next_unit(const ChunkArgs& a, Unit& u) {
-  ++u.rt;
-  if (u.rt >= seq_row_tiles<D, RT>(a, u.n)) {
-    u.rt = 0;
-    bool ok;
-    do {
-      if (++u.b == a.lo.B) {
-        u.b = 0;
-        if (++u.h == a.lo.H) {
-          u.h = 0;
-          if (++u.layer == a.n_layers) return false;
+__device__ __noinline__ bool step_run(const ChunkArgs& a, const LineStart& s, Run& r, int step) {
+  Unit u = r.u;
+  int pos, t0;
+  if (step == 0) {
+    pos = s.begin;
+    if (pos >= s.end) return false;
+    u.layer = s.lh / a.lo.H;
+    u.h = s.lh % a.lo.H;
+    u.b = s.b;
+    u.rt = s.rt;
+    (void)valid_seq(a, s.b, &u.n, &u.T, &u.cu);
+    t0 = s.tile;
+  } else {
+    pos = r.pos + r.t1 - r.t0;
+    if (pos >= s.end) return false;
+    t0 = 0;
+    ++u.rt;
+    if (u.rt >= seq_row_tiles<D, RT>(a, u.n)) {  // the next sequence with rows, of the same or the next kv head, layer
+      u.rt = 0;
+      bool found;
+      do {
+        if (++u.b == a.lo.B) {
+          u.b = 0;
+          if (++u.h == a.lo.H) {
+            u.h = 0;
+            if (++u.layer == a.n_layers) return false;  // only where lengths changed under the kernel
+          }
         }
-      }
-      ok = valid_seq(a, u.b, &u.n, &u.T, &u.cu) && u.n > 0;
-    } while (!ok);
+        found = valid_seq(a, u.b, &u.n, &u.T, &u.cu) && u.n > 0;
+      } while (!found);
+    }
   }
   unit_tiles<D, RT>(a, u);
-  return true;
-}
-
-// One CTA's run of a unit: tiles [t0, t1) of it.
-struct Run {
-  Unit u;
-  int t0, t1;
-  int64_t pos;   // place of the run's first tile on the line
-  bool first;    // the CTA's first run
-};
-
-struct LineStart {  // found once per CTA
-  int lh, b, rt, tile;
-  int64_t begin, end;  // the CTA's stretch of the line
-  int64_t per_cta;
-};
-
-template <int D, int RT>
-__device__ __forceinline__ bool first_run(const ChunkArgs& a, const LineStart& s, Run& r) {
-  if (s.begin >= s.end) return false;
-  r.u.layer = s.lh / a.lo.H;
-  r.u.h = s.lh % a.lo.H;
-  r.u.b = s.b;
-  r.u.rt = s.rt;
-  (void)valid_seq(a, s.b, &r.u.n, &r.u.T, &r.u.cu);
-  unit_tiles<D, RT>(a, r.u);
-  r.t0 = s.tile;
-  r.pos = s.begin;
-  r.t1 = (int)min((int64_t)r.u.nt, r.t0 + (s.end - r.pos));
-  r.first = true;
+  r.u = u;
+  r.t0 = t0;
+  r.t1 = min(u.nt, t0 + s.end - pos);
+  r.pos = pos;
+  r.first = step == 0;
   return true;
 }
 template <int D, int RT>
-__device__ __forceinline__ bool next_run(const ChunkArgs& a, const LineStart& s, Run& r) {
-  r.pos += r.t1 - r.t0;
-  if (r.pos >= s.end) return false;
-  if (!next_unit<D, RT>(a, r.u)) return false;
-  r.t0 = 0;
-  r.t1 = (int)min((int64_t)r.u.nt, s.end - r.pos);
-  r.first = false;
-  return true;
+__device__ __forceinline__ bool warp_run(const ChunkArgs& a, const LineStart& s, Run& r, int step) {
+  bool more = false;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) more = step_run<D, RT>(a, s, r, step);
+  return __shfl_sync(0xffffffffu, (int)more, 0) != 0;
 }
 
 // ---- dequantization --------------------------------------------------------------------
 
-// 32 codes of `bits` bits at p (2-byte aligned) as fp16 pairs, exact: signed
-// codes, or the raw fields when `raw` (asymmetric blocks), or table values (TBQ4).
+// 32 codes of BITS bits at p (2-byte aligned) as fp16 pairs, exact: signed
+// codes, or the raw fields (RAW: asymmetric blocks).
 __device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -252,11 +277,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(at));
   return v;
 }
-__device__ __forceinline__ float lds_half(uint32_t at) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(at));
-  return __half2float(__ushort_as_half(v));
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint32_t v;
+  asm volatile("{\n .reg .u16 t;\n ld.shared.u16 t, [%1];\n cvt.u32.u16 %0, t;\n}\n" : "=r"(v) : "r"(at));
+  return v;
 }
+__device__ __forceinline__ float lds_half(uint32_t at) { return __half2float(__ushort_as_half((uint16_t)lds16(at))); }
 // n words from a 2-byte aligned shared address (aligned loads, shifted; the staging
 // area has a word to spare behind its last slot)
 template <int N>
@@ -268,17 +294,12 @@ __device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], sh);
 }
-__device__ __forceinline__ void codes32(uint32_t p, int bits, bool raw, const uint32_t* pair_table,
-                                        uint32_t (&h)[16]) {
-  if (bits == 4) {
-    uint32_t w[4];
-    load_words(p, w);
-    if (pair_table) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) h[i] = pair_table[(w[i / 4] >> (8 * (i % 4))) & 0xff];
-      return;
-    }
-    const uint32_t bias = raw ? 0x64006400u : 0x64086408u;
+template <int BITS, bool RAW>
+__device__ __forceinline__ void codes32(uint32_t p, uint32_t (&h)[16]) {
+  uint32_t w[BITS];
+  load_words(p, w);
+  if constexpr (BITS == 4) {
+    constexpr uint32_t bias = RAW ? 0x64006400u : 0x64086408u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t v = w[i] >> 4;
@@ -287,18 +308,14 @@ __device__ __forceinline__ void codes32(uint32_t p, int bits, bool raw, const ui
       h[4 * i + 2] = field_pair(__byte_perm(w[i], v, 0x2622), 0x000f000fu, bias);
       h[4 * i + 3] = field_pair(__byte_perm(w[i], v, 0x3733), 0x000f000fu, bias);
     }
-  } else if (bits == 8) {
-    uint32_t w[8];
-    load_words(p, w);
+  } else if constexpr (BITS == 8) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t u = w[i] ^ 0x80808080u;
       h[2 * i] = hsub2u(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
       h[2 * i + 1] = hsub2u(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
     }
-  } else if (bits == 3) {
-    uint32_t w[3];
-    load_words(p, w);
+  } else if constexpr (BITS == 3) {
     const uint32_t g[4] = {w[0], __funnelshift_r(w[0], w[1], 24), __funnelshift_r(w[1], w[2], 16), w[2] >> 8};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -308,15 +325,13 @@ __device__ __forceinline__ void codes32(uint32_t p, int bits, bool raw, const ui
         h[4 * k + j] = field_pair((t & 7u) | ((t & 0x38u) << 13), 0x00070007u, 0x64046404u);
       }
   } else {
-    uint32_t w[2];
-    load_words(p, w);
-    const uint32_t bias = raw ? 0x64006400u : 0x64026402u;
+    constexpr uint32_t bias = RAW ? 0x64006400u : 0x64026402u;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const uint32_t x = (w[i] >> (8 * b)) & 0xffu;
-        const uint32_t y = x | (x << 14);  // fields 0 and 2 low; 1 and 3 at bit 16 and 20
+        const uint32_t y = x | (x << 14);  // fields 0 and 2 low; 1 and 3 at bits 16 and 20
         h[8 * i + 2 * b] = field_pair(y, 0x00030003u, bias);
         h[8 * i + 2 * b + 1] = field_pair(y >> 4, 0x00030003u, bias);
       }
@@ -325,12 +340,30 @@ __device__ __forceinline__ void codes32(uint32_t p, int bits, bool raw, const ui
 
 __device__ __forceinline__ float2 half2_f(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 
+// What a run's decoding needs of its format, in registers: fields of the
+// kernel's parameters picked one by one (a reference picked at run time would be
+// a chain of dependent loads).
+struct RunFmt {
+  int bits, group, bb, row;
+  bool zp, codebook;
+};
+__device__ __forceinline__ RunFmt run_fmt(const Layout& lo, int which, bool cold) {
+  RunFmt r;
+  r.bits = which ? (cold ? lo.vc.bits : lo.vf.bits) : (cold ? lo.kc.bits : lo.kf.bits);
+  r.group = which ? (cold ? lo.vc.group : lo.vf.group) : (cold ? lo.kc.group : lo.kf.group);
+  r.bb = which ? (cold ? lo.vc.bb : lo.vf.bb) : (cold ? lo.kc.bb : lo.kf.bb);
+  r.row = which ? (cold ? lo.vc.row : lo.vf.row) : (cold ? lo.kc.row : lo.kf.row);
+  r.zp = (which ? (cold ? lo.vc.zp : lo.vf.zp) : (cold ? lo.kc.zp : lo.kf.zp)) != 0;
+  r.codebook = !cold && (which ? lo.vf.codebook : lo.kf.codebook) != 0;
+  return r;
+}
+
 // Scale and zero of a block; a scale that is not finite (the block's values are unspecified) counts as 0.
 struct BlockScale {
   float s, z;
   bool big;  // a value may leave fp16's range
 };
-__device__ __forceinline__ BlockScale block_scale_of_run(uint32_t blk, const FmtInfo& f) {
+__device__ __forceinline__ BlockScale block_scale_of_run(uint32_t blk, const RunFmt& f) {
   BlockScale r;
   r.s = lds_half(blk);
   r.z = f.zp ? lds_half(blk + 2) : 0.f;
@@ -342,41 +375,36 @@ __device__ __forceinline__ BlockScale block_scale_of_run(uint32_t blk, const Fmt
 }
 
 // codes (fp16 pairs, exact) -> values in the input dtype.  fp16: one rounding of code * scale (+ zero);
-// bf16: through fp32, where the product is exact.  Values past fp16's range saturate: an
-// infinity would turn a masked token's zero probability into NaN.
-template <int DT>
-__device__ __forceinline__ void scale32(uint32_t (&h)[16], const BlockScale& b, bool zp) {
+// bf16: through fp32, where the product is exact.
+template <int DT, bool ZP>
+__device__ __forceinline__ void scale32(uint32_t (&h)[16], uint32_t s16, uint32_t z16) {
   if constexpr (DT == KVQ_DT_F16) {
-    if (!b.big) {
-      const __half2 s2 = __float2half2_rn(b.s), z2 = __float2half2_rn(b.z);
+    const uint32_t ss = __byte_perm(s16, 0, 0x1010), zz = __byte_perm(z16, 0, 0x1010);
+    const __half2 s2 = *reinterpret_cast<const __half2*>(&ss), z2 = *reinterpret_cast<const __half2*>(&zz);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const __half2 c = *reinterpret_cast<const __half2*>(&h[i]);
-        const __half2 v = zp ? __hfma2(c, s2, z2) : __hmul2(c, s2);
-        h[i] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-      return;
+    for (int i = 0; i < 16; ++i) {
+      const __half2 c = *reinterpret_cast<const __half2*>(&h[i]);
+      const __half2 v = ZP ? __hfma2(c, s2, z2) : __hmul2(c, s2);
+      h[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
-  }
+  } else {
+    const float s = __half2float(__ushort_as_half((uint16_t)s16)), z = __half2float(__ushort_as_half((uint16_t)z16));
+    const uint64_t s2 = pk2(s, s), z2 = pk2(z, z);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 c = half2_f(h[i]);
-    float x = fmaf(c.x, b.s, b.z), y = fmaf(c.y, b.s, b.z);
-    if constexpr (DT == KVQ_DT_F16) {
-      x = fminf(fmaxf(x, -65504.f), 65504.f);
-      y = fminf(fmaxf(y, -65504.f), 65504.f);
+    for (int i = 0; i < 16; ++i) {
+      const float2 c = half2_f(h[i]);
+      const uint64_t c2 = pk2(c.x, c.y), v = ZP ? fma2(c2, s2, z2) : mul2(c2, s2);
+      float x, y;
+      upk2(v, x, y);
+      h[i] = pack16<DT>(x, y);
     }
-    h[i] = pack16<DT>(x, y);
   }
 }
 
-__device__ __forceinline__ void store32(uint32_t dst, int row, int run, int rows, const uint32_t (&h)[16]) {
-  const uint32_t blk = dst + (uint32_t)(run >> 1) * rows * 128;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(blk + swz(row, (run & 1) * 4 + j)),
-                 "r"(h[4 * j]), "r"(h[4 * j + 1]), "r"(h[4 * j + 2]), "r"(h[4 * j + 3])
-                 : "memory");
+template <int DT>
+__device__ __forceinline__ float keep_range(float x) {
+  if constexpr (DT == KVQ_DT_F16) return isinf(x) || isnan(x) ? x : fminf(fmaxf(x, -65504.f), 65504.f);
+  return x;
 }
 
 struct TileTokens {
@@ -397,359 +425,485 @@ __device__ __forceinline__ TileTokens tile_tokens(const Unit& u, int j) {
   return r;
 }
 
-// Dequantizes half of one tensor's tile (a piece: 256 runs of 32 values, one
-// per dequantizing thread) from its staged packed bytes into the swizzled
-// shared-memory tile at dst.  Rows of the tile are tokens (per-token blocks,
-// runs along channels) or channels (per-channel blocks, runs along tokens).
-template <int D, int DT>
-struct Dequant {
-  static constexpr int NT = chunk_tile(D);
-  static constexpr int PIECE = NT / 2;  // tokens of a piece
-  static constexpr int THREADS = 32 * kChunkDequantWarps;
+// The part of a unit that addresses the cache, by value for the calls below.
+struct CachePos {
+  int layer, b, h, T, qe, ce;
+};
 
-  const ChunkArgs& a;
-  const Unit& u;
-  int which, warp, lane;
-  uint32_t dst;
-  int qe, ce;
-  const uint32_t* pair_table;
-  volatile uint32_t* nonfinite;
-  int a0;           // the piece's first token
-  uint32_t staged;  // its packed bytes: 32-token subtiles, a.sub_bytes apart
-  uint32_t bad;     // copies (of a.copy_shift tokens each) whose page id is out of range
-
-  __device__ __forceinline__ bool turned() const { return which == 0 && (a.lo.flags & KVQ_K_PRE_ROPE); }
-  __device__ __forceinline__ const FmtInfo& fmt_of(int t) const {
-    return t < ce ? fmt_cold(a.lo, which) : fmt_main(a.lo, which);
-  }
-  // block of the run (token or channel row, run) of a quantized tier and its codes
-  __device__ __forceinline__ uint32_t token_block(int t, int run, const FmtInfo& f, uint32_t* codes) const {
-    const int per = f.group / 32;  // runs of a block: 1 or 4
-    const uint32_t blk = staged + ((t - a0) >> 5) * a.sub_bytes + (t & 31) * f.row + (per == 1 ? run : run >> 2) * f.bb;
-    *codes = blk + (f.zp ? 4 : 2) + (per == 1 ? 0 : (run & 3) * 4 * f.bits);
-    return blk;
-  }
-  __device__ __forceinline__ uint32_t channel_block(int t, int c, const FmtInfo& f, uint32_t* codes) const {
-    const uint32_t blk = staged + ((t - a0) >> 5) * a.sub_bytes + c * f.bb;
-    *codes = blk + (f.zp ? 4 : 2);
-    return blk;
-  }
-  __device__ __forceinline__ bool no_page(int t) const { return (bad >> ((t - a0) >> a.copy_shift)) & 1u; }
-
-  // 16-bit window values as they are; values that are not finite become 0 in V's tile (see fix_rows)
-  __device__ __forceinline__ uint32_t clean(uint32_t w) const {
-    if (which == 0) return w;
-    constexpr uint32_t E = DT == KVQ_DT_F16 ? 0x7c00u : 0x7f80u;
-    if ((w & E) == E) {
-      *nonfinite = 1;
-      w &= 0xffff0000u;
-    }
-    if (((w >> 16) & E) == E) {
-      *nonfinite = 1;
-      w &= 0x0000ffffu;
-    }
-    return w;
-  }
-
-  __device__ __forceinline__ void raw_token_run(int t, int run, uint32_t (&h)[16]) const {
-    const uint4* p = reinterpret_cast<const uint4*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t)) + run * 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 v = p[j];
-      h[4 * j] = clean(v.x);
-      h[4 * j + 1] = clean(v.y);
-      h[4 * j + 2] = clean(v.z);
-      h[4 * j + 3] = clean(v.w);
-    }
-  }
-  // channel c of tokens t .. t + 31, zeros from token T on
-  __device__ __forceinline__ void raw_channel_run(int t, int c, uint32_t (&h)[16]) const {
-    const uint16_t* p = resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t) + c;
-    int left = a.lo.ring - t % a.lo.ring;  // slots until the ring wraps
-    uint32_t x[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      x[j] = *p;  // slots past the length exist, and count as zeros below
-      --left;
-      p += left == 0 ? (int64_t)a.lo.D - (int64_t)a.lo.ring * a.lo.D : (int64_t)a.lo.D;
-    }
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (t + j >= u.T) x[j] = 0;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] = clean(x[2 * j] | (x[2 * j + 1] << 16));
-  }
-
-  // One run, turn aside, in the input dtype.
-  __device__ __forceinline__ void token_run(int t, int run, uint32_t (&h)[16]) const {
-    if (t >= u.T || no_page(t)) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) h[i] = 0;
-    } else if (t >= qe) {
-      raw_token_run(t, run, h);
-    } else {
-      const FmtInfo& f = fmt_of(t);
-      uint32_t codes;
-      const uint32_t blk = token_block(t, run, f, &codes);
-      codes32(codes, f.bits, f.zp, f.codebook ? pair_table : nullptr, h);
-      scale32<DT>(h, block_scale_of_run(blk, f), f.zp);
-    }
-  }
-  __device__ __forceinline__ void channel_run(int t, int c, uint32_t (&h)[16]) const {
-    if (t >= qe) {
-      raw_channel_run(t, c, h);
-    } else {
-      const FmtInfo& f = fmt_of(t);
-      uint32_t codes;
-      const uint32_t blk = channel_block(t, c, f, &codes);
-      codes32(codes, f.bits, f.zp, nullptr, h);
-      scale32<DT>(h, block_scale_of_run(blk, f), f.zp);
-    }
-  }
-
-  // Values of a run as code pairs and (scale, zero), for the turn in fp32; window values are pairs of the input dtype
-  struct Loose {
-    uint32_t h[16];
-    float s, z;
-    bool raw;
-    __device__ __forceinline__ float2 value(int i) const {
-      if (raw) {
-        if constexpr (DT == KVQ_DT_F16) return half2_f(h[i]);
-        return make_float2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u));
-      }
-      const float2 c = half2_f(h[i]);
-      return make_float2(fmaf(c.x, s, z), fmaf(c.y, s, z));
-    }
-  };
-  __device__ __forceinline__ void loose_token(int t, int run, Loose& l) const {
-    l.raw = true;
-    if (t >= u.T || no_page(t)) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) l.h[i] = 0;
-    } else if (t >= qe) {
-      raw_token_run(t, run, l.h);
-    } else {
-      const FmtInfo& f = fmt_of(t);
-      uint32_t codes;
-      const uint32_t blk = token_block(t, run, f, &codes);
-      codes32(codes, f.bits, f.zp, nullptr, l.h);
-      const BlockScale b = block_scale_of_run(blk, f);
-      l.raw = false;
-      l.s = b.s;
-      l.z = b.z;
-    }
-  }
-  __device__ __forceinline__ void loose_channel(int t, int c, Loose& l) const {
-    l.raw = t >= qe;
-    if (l.raw) {
-      raw_channel_run(t, c, l.h);
-    } else {
-      const FmtInfo& f = fmt_of(t);
-      uint32_t codes;
-      const uint32_t blk = channel_block(t, c, f, &codes);
-      codes32(codes, f.bits, f.zp, nullptr, l.h);
-      const BlockScale b = block_scale_of_run(blk, f);
-      l.s = b.s;
-      l.z = b.z;
-    }
-  }
-  // cos and sin of a 64-bit turn fraction
-  __device__ __forceinline__ static float2 cos_sin(uint64_t turn) {
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-    return make_float2(c, s);
-  }
-  __device__ __forceinline__ static float keep_range(float x) {
-    if constexpr (DT == KVQ_DT_F16) return isinf(x) || isnan(x) ? x : fminf(fmaxf(x, -65504.f), 65504.f);
-    return x;
-  }
-
-  // Keys stored pre-RoPE: the runs of channels i and i + D/2 together.
-  __device__ void turned_tile(const TileTokens& tt, bool per_channel) const {
-    if (per_channel) {
-      constexpr int G = PIECE / 32;  // token groups of the piece
-      for (int e = warp * 32 + lane; e < (D / 2) * G; e += THREADS) {
-        const int c = (e & 7) | ((e / (8 * G)) << 3);
-        const int t = a0 + 32 * ((e >> 3) % G), run = (t - tt.t0) >> 5;
-        if (t + 32 <= tt.v0 || t >= tt.v1) continue;
-        Loose x, y;
-        loose_channel(t, c, x);
-        loose_channel(t, c + D / 2, y);
-        const uint64_t w = a.turns[c];
-        // token after token the angle grows by the same step: a complex
-        // product each, 31 times from an exact start (error below 31 x 2^-22)
-        float2 k = cos_sin((uint64_t)t * w);
-        const float2 step = cos_sin(w);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 xa = x.value(i), ya = y.value(i);
-          const float x0 = xa.x * k.x - ya.x * k.y, y0 = ya.x * k.x + xa.x * k.y;
-          k = make_float2(k.x * step.x - k.y * step.y, k.y * step.x + k.x * step.y);
-          const float x1 = xa.y * k.x - ya.y * k.y, y1 = ya.y * k.x + xa.y * k.y;
-          k = make_float2(k.x * step.x - k.y * step.y, k.y * step.x + k.x * step.y);
-          x.h[i] = pack16<DT>(keep_range(x0), keep_range(x1));
-          y.h[i] = pack16<DT>(keep_range(y0), keep_range(y1));
-        }
-        store32(dst, c, run, D, x.h);
-        store32(dst, c + D / 2, run, D, y.h);
-      }
-    } else {
-      constexpr int R = D / 64;  // runs of half a row
-      for (int e = warp * 32 + lane; e < PIECE * R; e += THREADS) {
-        const int run = (e >> 3) % R, t = a0 + ((e & 7) | ((e / (8 * R)) << 3)), row = t - tt.t0;
-        if (t < (tt.v0 & ~31) || t >= ((tt.v1 + 31) & ~31)) continue;
-        Loose x, y;
-        loose_token(t, run, x);
-        loose_token(t, run + R, y);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 k0 = cos_sin((uint64_t)t * a.turns[32 * run + 2 * i]);
-          const float2 k1 = cos_sin((uint64_t)t * a.turns[32 * run + 2 * i + 1]);
-          const float2 xa = x.value(i), ya = y.value(i);
-          x.h[i] = pack16<DT>(keep_range(xa.x * k0.x - ya.x * k0.y), keep_range(xa.y * k1.x - ya.y * k1.y));
-          y.h[i] = pack16<DT>(keep_range(ya.x * k0.x + xa.x * k0.y), keep_range(ya.y * k1.x + xa.y * k1.y));
-        }
-        store32(dst, row, run, NT, x.h);
-        store32(dst, row, run + R, NT, y.h);
-      }
-    }
-  }
-
-  // Window tokens of a rotated format, turned into the rotated domain: a warp per token.
-  __device__ void rotated_window(const TileTokens& tt) const {
-    const int t1 = min(min(u.T, a0 + PIECE), (tt.v1 + 31) & ~31);
-    for (int t = max(max(qe, a0), tt.v0 & ~31) + warp; t < t1; t += kChunkDequantWarps) {
-      const uint2* p = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t));
-#pragma unroll
-      for (int c = 0; c < D / 128; ++c) {
-        const uint2 w = p[32 * c + lane];
-        const uint32_t w0 = clean(w.x), w1 = clean(w.y);
-        float v[4] = {in_to_f32((uint16_t)w0, DT), in_to_f32((uint16_t)(w0 >> 16), DT), in_to_f32((uint16_t)w1, DT),
-                      in_to_f32((uint16_t)(w1 >> 16), DT)};
-        warp_rotate128(v, a.lo.d1, a.lo.d2);
-        const int ch = 128 * c + 4 * lane;
-        const uint32_t at = dst + (uint32_t)(ch >> 6) * NT * 128 + swz(t - tt.t0, (ch & 63) >> 3) + (ch & 4) * 2;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at),
-                     "r"(pack16<DT>(keep_range(v[0]), keep_range(v[1]))), "r"(pack16<DT>(keep_range(v[2]), keep_range(v[3])))
-                     : "memory");
-      }
-    }
-  }
-
-  __device__ void piece(const TileTokens& tt) const {
-    const bool per_channel = fmt_main(a.lo, which).axis == KVQ_AXIS_CHANNEL;
-    if (turned()) {
-      turned_tile(tt, per_channel);
-      return;
-    }
-    const int e = warp * 32 + lane;
-    uint32_t h[16];
+// Where the runs of 32 values of a tensor's tile sit.  Rows of the tile in
+// shared memory are tokens (per-token blocks, runs along channels) or
+// channels (per-channel blocks, runs along tokens).  A piece is half a tile: 256 runs, four a
+// lane of its two warps.  Consecutive lanes take consecutive rows of one run, so that their
+// 16-byte stores fall into different banks.
+template <int D>
+struct RunPlace {
+  static constexpr int NT = chunk_tile(D), PIECE = NT / 2;
+  // run e (0..255) of a piece: first token from the piece's, row and run in the tile's first half
+  __device__ __forceinline__ static void of(bool per_channel, int e, int* toff, int* row, int* run) {
     if (per_channel) {
       constexpr int G = PIECE / 32;
-      const int c = (e & 7) | ((e / (8 * G)) << 3), t = a0 + 32 * ((e >> 3) % G);
-      if (t + 32 <= tt.v0 || t >= tt.v1) return;
-      channel_run(t, c, h);
-      store32(dst, c, (t - tt.t0) >> 5, D, h);
-      return;
+      *row = (e & 7) | ((e / (8 * G)) << 3);
+      *run = (e >> 3) % G;
+      *toff = 32 * *run;
+    } else {
+      constexpr int R = D / 32;
+      *run = (e >> 3) % R;
+      *row = *toff = (e & 7) | ((e / (8 * R)) << 3);
     }
-    constexpr int R = D / 32;
-    const bool rotated = (a.lo.flags & (which ? KVQ_ROTATE_V : KVQ_ROTATE_K)) != 0;
-    const int run = (e >> 3) % R, t = a0 + ((e & 7) | ((e / (8 * R)) << 3));
-    if (t >= (tt.v0 & ~31) && t < ((tt.v1 + 31) & ~31) && !(rotated && t >= qe && t < u.T)) {
-      token_run(t, run, h);
-      store32(dst, t - tt.t0, run, NT, h);
+  }
+  // number in the piece of run i of lane `lane` of the piece's warp `part`: i steps along rows
+  __device__ __forceinline__ static int number(bool per_channel, int part, int i, int lane) {
+    // per-token rows of 256 channels are eight runs long: a warp takes four of them
+    if (D == 256 && !per_channel) return i * 64 + part * 32 + lane;
+    return part * 128 + i * 32 + lane;
+  }
+  // block and codes of a run (channel `row` of a 32-token group, or run `run` of a token) in the staged piece
+  __device__ __forceinline__ static void at(bool per_channel, const RunFmt& f, int sub_bytes, int t, int row, int run,
+                                            uint32_t* b, uint32_t* c) {
+    const uint32_t sub = (t >> 5) * sub_bytes;
+    if (per_channel) {
+      *b = sub + row * f.bb;
+      *c = *b + (f.zp ? 4 : 2);
+    } else {
+      const bool one = f.group == 32;  // a block is one run, or four
+      *b = sub + (t & 31) * f.row + (one ? run : run >> 2) * f.bb;
+      *c = *b + (f.zp ? 4 : 2) + (one ? 0 : (run & 3) * 4 * f.bits);
     }
-    if (rotated) rotated_window(tt);
+  }
+  // shared-memory row of a run in the tile
+  __device__ __forceinline__ static uint32_t line_at(uint32_t dst, int row, int run, int rows) {
+    return dst + (uint32_t)(run >> 1) * rows * 128 + row * 128;
   }
 };
+
+__device__ __forceinline__ void store_run(uint32_t line, int row, int run, const uint32_t (&h)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(line + ((((run & 1) * 4 + j) ^ (row & 7)) << 4)),
+                 "r"(h[4 * j]), "r"(h[4 * j + 1]), "r"(h[4 * j + 2]), "r"(h[4 * j + 3])
+                 : "memory");
+}
+
+// 16-bit window values as they are; in V's tile values that are not finite become 0 (see add_nonfinite)
+template <int DT>
+__device__ __forceinline__ uint32_t clean(uint32_t w, int which, volatile uint32_t* nonfinite) {
+  if (which == 0) return w;
+  constexpr uint32_t E = DT == KVQ_DT_F16 ? 0x7c00u : 0x7f80u;
+  if ((w & E) == E) {
+    *nonfinite = 1;
+    w &= 0xffff0000u;
+  }
+  if (((w >> 16) & E) == E) {
+    *nonfinite = 1;
+    w &= 0x0000ffffu;
+  }
+  return w;
+}
+
+// 32 channels of window token t (zeros past the length)
+template <int DT>
+__device__ __forceinline__ void raw_token_run(const ChunkArgs& a, const CachePos& u, int which, int t, int run,
+                                              volatile uint32_t* nonfinite, uint32_t (&h)[16]) {
+  const uint4* p = reinterpret_cast<const uint4*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t)) + run * 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = t < u.T ? p[j] : make_uint4(0, 0, 0, 0);
+    h[4 * j] = clean<DT>(v.x, which, nonfinite);
+    h[4 * j + 1] = clean<DT>(v.y, which, nonfinite);
+    h[4 * j + 2] = clean<DT>(v.z, which, nonfinite);
+    h[4 * j + 3] = clean<DT>(v.w, which, nonfinite);
+  }
+}
+// channel c of window tokens t .. t + 31 (zeros past the length)
+template <int DT>
+__device__ __forceinline__ void raw_channel_run(const ChunkArgs& a, const CachePos& u, int which, int t, int c,
+                                                volatile uint32_t* nonfinite, uint32_t (&h)[16]) {
+  const uint16_t* p = resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t) + c;
+  const int D = a.lo.D, ring = a.lo.ring;
+  int left = ring - t % ring;  // slots until the ring wraps
+  uint32_t x[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    x[j] = *p;  // slots past the length exist, and count as zeros below
+    --left;
+    p += left == 0 ? (int64_t)D - (int64_t)ring * D : (int64_t)D;
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (t + j >= u.T) x[j] = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) h[j] = clean<DT>(x[2 * j] | (x[2 * j + 1] << 16), which, nonfinite);
+}
+
+// Window tokens [t0, t1) of a rotated format, turned into the rotated domain by one warp.
+template <int D, int DT>
+__device__ __forceinline__ void rotated_window(const ChunkArgs& a, const CachePos& u, int which, int part, uint32_t dst,
+                                               int tile0, int a0, int t0, int t1, int lane, volatile uint32_t* nonfinite) {
+  constexpr int NT = chunk_tile(D);
+  for (int t = t0; t < t1; ++t) {
+    if (D == 128 && ((t - a0) >> 5) != part) continue;  // D = 128: the warp's 32 tokens
+    const uint2* p = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t));
+#pragma unroll
+    for (int c = 0; c < D / 128; ++c) {
+      if (D == 256 && c != part) continue;  // D = 256: the warp's 128 channels
+      const uint2 w = p[32 * c + lane];
+      const uint32_t w0 = clean<DT>(w.x, which, nonfinite), w1 = clean<DT>(w.y, which, nonfinite);
+      float v[4] = {in_to_f32((uint16_t)w0, DT), in_to_f32((uint16_t)(w0 >> 16), DT), in_to_f32((uint16_t)w1, DT),
+                    in_to_f32((uint16_t)(w1 >> 16), DT)};
+      warp_rotate128(v, a.lo.d1, a.lo.d2);
+      const int ch = 128 * c + 4 * lane;
+      const uint32_t at = dst + (uint32_t)(ch >> 6) * NT * 128 + swz(t - tile0, (ch & 63) >> 3) + (ch & 4) * 2;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(pack16<DT>(keep_range<DT>(v[0]), keep_range<DT>(v[1]))),
+                   "r"(pack16<DT>(keep_range<DT>(v[2]), keep_range<DT>(v[3])))
+                   : "memory");
+    }
+  }
+}
+
+// Window tokens [t0, t1) (whole 32-token groups) of a per-channel tensor: a
+// lane per token reads 8 channels at a time, and a warp's 2-byte stores of one
+// channel are 64 bytes of one row.
+template <int D, int DT>
+__device__ __forceinline__ void window_groups(const ChunkArgs& a, const CachePos& u, int which, int part, uint32_t dst, int tile0,
+                                              int t0, int t1, int lane, volatile uint32_t* nonfinite) {
+  for (int g = t0; g < t1; g += 32) {
+    const int t = g + lane, col = t - tile0;  // column of the channel rows
+    const bool in = t < u.T;
+    const uint4* p = reinterpret_cast<const uint4*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, in ? t : g));
+    const uint32_t blk = dst + (uint32_t)(col >> 6) * D * 128 + (col & 7) * 2;
+    const int c16 = (col & 63) >> 3;
+#pragma unroll 1
+    for (int c0 = part * (D / 16); c0 < (part + 1) * (D / 16); c0 += 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = p[c0 + k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w[4] = {clean<DT>(in ? v[k].x : 0u, which, nonfinite), clean<DT>(in ? v[k].y : 0u, which, nonfinite),
+                               clean<DT>(in ? v[k].z : 0u, which, nonfinite), clean<DT>(in ? v[k].w : 0u, which, nonfinite)};
+        const int row = (c0 + k) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // row + e has low bits e
+          asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(blk + (row + e) * 128 + ((c16 ^ e) << 4)),
+                       "h"((uint16_t)(w[e >> 1] >> (16 * (e & 1))))
+                       : "memory");
+      }
+    }
+  }
+}
+
+// The values of one run in fp32 from its codes, whatever the format; values past fp16's range
+// saturate in fp16 (an infinity would turn a masked token's zero probability into NaN).
+template <int DT>
+__device__ __forceinline__ void general_run(RunFmt f, uint32_t blk, uint32_t codes, const uint32_t* pair_table,
+                                         uint32_t line, int row, int run) {
+  uint32_t h[16];
+  if (f.codebook) {
+    uint32_t w[4];
+    load_words(codes, w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = pair_table[(w[i / 4] >> (8 * (i % 4))) & 0xff];
+  } else if (f.bits == 4) {
+    codes32<4, true>(codes, h);
+  } else if (f.bits == 8) {
+    codes32<8, true>(codes, h);
+  } else if (f.bits == 3) {
+    codes32<3, true>(codes, h);
+  } else {
+    codes32<2, true>(codes, h);
+  }
+  const float bias = f.zp || f.codebook ? 0.f : f.bits == 4 ? 8.f : f.bits == 2 ? 2.f : 0.f;  // 8- and 3-bit codes are signed already
+  const BlockScale b = block_scale_of_run(blk, f);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 c = half2_f(h[i]);
+    float x = fmaf(c.x - bias, b.s, b.z), y = fmaf(c.y - bias, b.s, b.z);
+    if constexpr (DT == KVQ_DT_F16) {
+      x = fminf(fmaxf(x, -65504.f), 65504.f);
+      y = fminf(fmaxf(y, -65504.f), 65504.f);
+    }
+    h[i] = pack16<DT>(x, y);
+  }
+  store_run(line, row, run, h);
+}
+
+// One lane's four runs of a piece that lies in one format, wholly in view:
+// the hot path.  Its loop is kept short, and everything else out of line: the five roles run
+// different code at the same time, and what they run has to fit the instruction cache (with
+// this loop unrolled eight times a batch of 64 sequences took 512 us, with one run a turn 393 us).
+struct PiecePlace {
+  uint32_t blk, codes, step;  // first run's block and codes in the staged piece; to the next run
+  uint32_t line, line_step;   // the same in the tile
+  uint32_t piece16[4];        // swizzled places of the run's four 16-byte parts
+};
+// False when a block's values leave fp16's range, or its scale is not finite (the piece is then done again).
+template <int DT, int BITS, bool ZP>
+__device__ __forceinline__ bool fill_piece(const PiecePlace& q, uint32_t staged, uint32_t tile) {
+  uint32_t most = 0, blk = staged + q.blk, line = tile + q.line;
+  const uint32_t codes = q.codes - q.blk;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t s16 = lds16(blk), z16 = ZP ? lds16(blk + 2) : 0u;
+    uint32_t h[16];
+    codes32<BITS, ZP>(blk + codes, h);
+    most = max(most, s16 & 0x7fffu);
+    // the zero's bound is four times the scale's
+    if (ZP) most = max(most, DT == KVQ_DT_F16 ? max(z16 & 0x7fffu, 0x800u) - 0x800u : z16 & 0x7fffu);
+    scale32<DT, ZP>(h, s16, z16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(line + q.piece16[k]), "r"(h[4 * k]),
+                   "r"(h[4 * k + 1]), "r"(h[4 * k + 2]), "r"(h[4 * k + 3])
+                   : "memory");
+    blk += q.step;
+    line += q.line_step;
+  }
+  // bf16: finite is enough.  fp16: |scale| below 2^15 / the largest code's bound (and a zero below 2^15), so that
+  // every value stays below 2^16 less a rounding
+  constexpr uint32_t LIMIT = DT != KVQ_DT_F16 ? 0x7c00u : (uint32_t)(15 - (ZP ? BITS : BITS - 1) + 15) << 10;
+  return !__any_sync(0xffffffffu, most >= LIMIT);
+}
+
+// Half of a piece whose tokens differ in tier, are partly out of view, include pages out of range or the
+// 16-bit window, or whose blocks are TBQ4 or hold values past the range: run by run.
+template <int D, int DT>
+__device__ __forceinline__ void mixed_piece(const ChunkArgs& a, const CachePos& u, int which, int half, int part, int lane,
+                                         bool per_channel, bool rotated, int a0, int v0, int v1, uint32_t staged,
+                                         uint32_t bad, uint32_t dst, int tile0, bool fresh, const uint32_t* pair_table,
+                                         volatile uint32_t* nonfinite) {
+  constexpr int NT = chunk_tile(D);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    int toff, row, run;
+    RunPlace<D>::of(per_channel, RunPlace<D>::number(per_channel, part, i, lane), &toff, &row, &run);
+    const int t = a0 + toff, row_t = row + (per_channel ? 0 : half * (NT / 2)), run_t = run + (per_channel ? half * (NT / 64) : 0);
+    const uint32_t line = RunPlace<D>::line_at(dst, row_t, run_t, per_channel ? D : NT);
+    const bool in = t >= v0 && t < v1;
+    if (in && t < u.qe && !((bad >> (toff >> a.copy_shift)) & 1u)) {
+      const RunFmt f = run_fmt(a.lo, which, t < u.ce);
+      uint32_t blk, codes;
+      RunPlace<D>::at(per_channel, f, a.sub_bytes, toff, row, run, &blk, &codes);
+      general_run<DT>(f, staged + blk, staged + codes, pair_table, line, row_t, run_t);
+    } else if (in && t >= u.qe && !per_channel && !(rotated && t < u.T)) {
+      uint32_t h[16];
+      raw_token_run<DT>(a, u, which, t, run, nonfinite, h);
+      store_run(line, row_t, run_t, h);
+    } else if ((in && t < u.qe) || fresh) {
+      // a page out of range; or a run out of view in a buffer that V has not filled yet: what shared
+      // memory held before the kernel must not meet a zero probability
+      uint32_t h[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) h[k] = 0;
+      store_run(line, row_t, run_t, h);
+    }
+  }
+  // the window tokens of this warp's own half: the same rows or channels as its runs
+  if (rotated) {
+    __syncwarp();
+    rotated_window<D, DT>(a, u, which, part, dst, tile0, a0, max(max(u.qe, a0), v0), min(min(u.T, a0 + NT / 2), v1), lane,
+                          nonfinite);
+  }
+  if (per_channel && v1 > max(u.qe, a0)) {
+    __syncwarp();
+    window_groups<D, DT>(a, u, which, part, dst, tile0, max(max(u.qe, a0), v0), min(a0 + NT / 2, v1), lane, nonfinite);
+  }
+}
+
+// Values of a run as code pairs with (scale, zero), or as pairs of the input dtype (window tokens), for the turn in fp32
+template <int DT>
+struct Loose {
+  uint32_t h[16];
+  float s, z;
+  bool raw;
+  __device__ __forceinline__ float2 value(int i) const {
+    if (raw) {
+      if constexpr (DT == KVQ_DT_F16) return half2_f(h[i]);
+      return make_float2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u));
+    }
+    const float2 c = half2_f(h[i]);
+    return make_float2(fmaf(c.x, s, z), fmaf(c.y, s, z));
+  }
+};
+
+// cos and sin of a 64-bit turn fraction
+__device__ __forceinline__ float2 cos_sin(uint64_t turn) {
+  float s, c;
+  sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+  return make_float2(c, s);
+}
+
+// Keys stored pre-RoPE: a piece's runs of channels i and i + D/2 together.
+template <int D, int DT>
+__device__ __forceinline__ void turned_piece(const ChunkArgs& a, const CachePos& u, const TileTokens& tt, int a0, uint32_t staged,
+                                          uint32_t bad, uint32_t dst, int e0, volatile uint32_t* nonfinite) {
+  constexpr int NT = chunk_tile(D), PIECE = NT / 2, THREADS = 64;  // the piece's two warps
+  const bool per_channel = a.lo.kf.axis == KVQ_AXIS_CHANNEL;
+  auto loose = [&](int t, int row, int run, Loose<DT>& l) {
+    l.raw = t >= u.qe || ((bad >> ((t - a0) >> a.copy_shift)) & 1u);
+    if (!l.raw) {
+      const RunFmt f = run_fmt(a.lo, 0, t < u.ce);
+      uint32_t blk, codes;
+      RunPlace<D>::at(per_channel, f, a.sub_bytes, t - a0, row, run, &blk, &codes);
+      const BlockScale b = block_scale_of_run(staged + blk, f);
+      l.s = b.s;
+      l.z = b.z;
+      if (f.bits == 4)
+        codes32<4, true>(staged + codes, l.h);
+      else if (f.bits == 8)
+        codes32<8, true>(staged + codes, l.h);
+      else if (f.bits == 3)
+        codes32<3, true>(staged + codes, l.h);
+      else
+        codes32<2, true>(staged + codes, l.h);
+      if (!f.zp) l.z = -b.s * (f.bits == 4 ? 8.f : f.bits == 2 ? 2.f : 0.f);  // the bias of raw fields: exact products
+
+    } else if (t < u.qe) {  // a page out of range
+#pragma unroll
+      for (int i = 0; i < 16; ++i) l.h[i] = 0;
+    } else if (per_channel) {
+      raw_channel_run<DT>(a, u, 0, t, row, nonfinite, l.h);
+    } else {
+      raw_token_run<DT>(a, u, 0, t, run, nonfinite, l.h);
+    }
+  };
+  if (per_channel) {
+    constexpr int G = PIECE / 32;  // token groups of the piece
+    for (int e = e0; e < (D / 2) * G; e += THREADS) {
+      const int c = (e & 7) | ((e / (8 * G)) << 3), t = a0 + 32 * ((e >> 3) % G), run = (t - tt.t0) >> 5;
+      if (t + 32 <= tt.v0 || t >= tt.v1) continue;
+      Loose<DT> x, y;
+      loose(t, c, 0, x);
+      loose(t, c + D / 2, 0, y);
+      const uint64_t f = a.turns[c];
+      // token after token the angle grows by the same step: a complex
+      // product each, 31 times from an exact start (error below 31 x 2^-22)
+      float2 k = cos_sin((uint64_t)t * f);
+      const float2 step = cos_sin(f);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 xa = x.value(i), ya = y.value(i);
+        const float x0 = xa.x * k.x - ya.x * k.y, y0 = ya.x * k.x + xa.x * k.y;
+        k = make_float2(k.x * step.x - k.y * step.y, k.y * step.x + k.x * step.y);
+        const float x1 = xa.y * k.x - ya.y * k.y, y1 = ya.y * k.x + xa.y * k.y;
+        k = make_float2(k.x * step.x - k.y * step.y, k.y * step.x + k.x * step.y);
+        x.h[i] = pack16<DT>(keep_range<DT>(x0), keep_range<DT>(x1));
+        y.h[i] = pack16<DT>(keep_range<DT>(y0), keep_range<DT>(y1));
+      }
+      store_run(RunPlace<D>::line_at(dst, c, run, D), c, run, x.h);
+      store_run(RunPlace<D>::line_at(dst, c + D / 2, run, D), c + D / 2, run, y.h);
+    }
+  } else {
+    constexpr int R = D / 64;  // runs of half a row
+    for (int e = e0; e < PIECE * R; e += THREADS) {
+      const int run = (e >> 3) % R, t = a0 + ((e & 7) | ((e / (8 * R)) << 3)), row = t - tt.t0;
+      if (t < (tt.v0 & ~31) || t >= ((tt.v1 + 31) & ~31)) continue;
+      Loose<DT> x, y;
+      loose(t, row, run, x);
+      loose(t, row, run + R, y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 k0 = cos_sin((uint64_t)t * a.turns[32 * run + 2 * i]);
+        const float2 k1 = cos_sin((uint64_t)t * a.turns[32 * run + 2 * i + 1]);
+        const float2 xa = x.value(i), ya = y.value(i);
+        x.h[i] = pack16<DT>(keep_range<DT>(xa.x * k0.x - ya.x * k0.y), keep_range<DT>(xa.y * k1.x - ya.y * k1.y));
+        y.h[i] = pack16<DT>(keep_range<DT>(ya.x * k0.x + xa.x * k0.y), keep_range<DT>(ya.y * k1.x + xa.y * k1.y));
+      }
+      store_run(RunPlace<D>::line_at(dst, row, run, NT), row, run, x.h);
+      store_run(RunPlace<D>::line_at(dst, row, run + R, NT), row, run + R, y.h);
+    }
+  }
+}
 
 // ---- staging -----------------------------------------------------------------------------
 
-// The loader warp: the packed bytes of every piece into a ring of
-// shared-memory slots, as bulk copies of 32-token subtiles (of pages, when those are smaller).
+// The loader warp brings the packed bytes of every piece into a ring of
+// shared-memory slots: bulk copies of 32-token subtiles (of pages, when those
+// are smaller).  A tile's four pieces (K, V, two halves each) are worked out
+// side by side, eight lanes a piece: one lane's addresses are a long chain of
+// dependent instructions, and four in turn kept the products waiting.
+// Piece i of tile kt is number 4 kt + i and goes to slot number mod slots; its
+// barriers are the piece kind's, kt mod kChunkBars: each warp sees every
+// phase of the barriers that it waits on, and the ring never spans kChunkBars tiles.
 template <int D>
 struct Loader {
-  static constexpr int NT = chunk_tile(D), PIECE = NT / 2, SUBS = PIECE / 32;
+  static constexpr int NT = chunk_tile(D), PIECE = NT / 2;
 
-  const ChunkArgs& a;
-  int lane;
+  int which, half, ln;       // this lane's piece and its place among the piece's lanes
+  const uint8_t *main0, *cold0;  // first row of the unit's (layer, sequence, kv head); of page 0 when paged
+  int64_t page_stride;
+  int row_main, row_cold;    // bytes per token (per-token) or per 32-token group (per-channel)
+  int ring;                  // hot ring in rows (tiers), else 0
+  bool per_channel;
 
-  // page id of the lane-th page of the tile (small pages)
-  __device__ __forceinline__ int page_id(const Unit& u, const TileTokens& tt, int qe) const {
-    const int t = tt.t0 + (lane << a.copy_shift);
-    if (!a.small_pages || lane >= (NT >> a.copy_shift) || t >= qe) return -1;
+  __device__ __forceinline__ void lanes(const ChunkArgs& a, int lane) {
+    which = lane >> 4;
+    half = (lane >> 3) & 1;
+    ln = lane & 7;
+    per_channel = (which ? a.lo.vf.axis : a.lo.kf.axis) == KVQ_AXIS_CHANNEL;
+    row_main = which ? a.lo.vf.row : a.lo.kf.row;
+    row_cold = which ? a.lo.vc.row : a.lo.kc.row;
+    ring = a.lo.tiered ? (which ? a.lo.hot_ring_v : a.lo.hot_ring_k) : 0;
+  }
+  __device__ __forceinline__ void unit(const ChunkArgs& a, const CachePos& u) {
+    const uint8_t* m = which ? a.cp.v_main : a.cp.k_main;
+    if (a.lo.paged) {
+      page_stride = (int64_t)a.lo.H * a.lo.pt * row_main;
+      main0 = m + (int64_t)u.layer * a.lo.n_pages * page_stride + (int64_t)u.h * a.lo.pt * row_main;
+      cold0 = nullptr;
+    } else {
+      const int64_t lbh = ((int64_t)u.layer * a.lo.B + u.b) * a.lo.H + u.h;
+      main0 = m + lbh * (which ? a.lo.rows_v_main : a.lo.rows_k_main) * row_main;
+      cold0 = (which ? a.cp.v_cold : a.cp.k_cold) + lbh * (which ? a.lo.rows_v_cold : a.lo.rows_k_cold) * row_cold;
+    }
+  }
+  // page id of copy c of this lane's piece of a tile (-1 where none is read)
+  __device__ __forceinline__ int page_id(const ChunkArgs& a, const CachePos& u, int tile0, int c) const {
+    const int t = tile0 + half * PIECE + (c << a.copy_shift);
+    if (!a.lo.paged || c >= (PIECE >> a.copy_shift) || t >= u.qe) return -1;
     return __ldg(a.cp.block_table + (int64_t)u.b * a.lo.max_pages + t / a.lo.pt);
   }
-
-  __device__ __forceinline__ static void copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-  }
-
-  // One piece into the slot at `dst`; the slot's barrier completes once the bytes are there.
-  __device__ __forceinline__ void piece(const Unit& u, const TileTokens& tt, int which, int half, int qe, int ce, int pid,
-                                        uint32_t dst, uint32_t bar, uint32_t* bad_at) const {
-    const int a0 = tt.t0 + half * PIECE;
-    if (a.direct) {
-      piece_direct(u, tt, which, a0, qe, dst, bar, bad_at);
-      return;
-    }
-    const int n = PIECE >> a.copy_shift;  // copies of the piece, one per lane
-    const int t = a0 + (lane << a.copy_shift), sub = t & ~31;
-    bool active = lane < n && t < qe && sub + 32 > tt.v0 && sub < tt.v1, bad = false;
-    const bool cold = t < ce;
-    const FmtInfo& f = cold ? fmt_cold(a.lo, which) : fmt_main(a.lo, which);
-    const uint8_t* src = nullptr;
-    int p = 0;
-    if (a.small_pages) p = __shfl_sync(0xffffffffu, pid, (lane + half * n) & 31);
-    if (active) {
-      if (a.small_pages) {
-        bad = p < 0 || p >= a.lo.n_pages;
-        const uint8_t* base = which ? a.cp.v_main : a.cp.k_main;
-        src = base + (((int64_t)u.layer * a.lo.n_pages + p) * a.lo.H + u.h) * a.lo.pt * f.row;
-      } else {
-        src = cold ? cold_row(a.lo, a.cp, which, u.layer, u.b, u.h, t)
-                   : main_row(a.lo, a.cp, which, u.layer, u.b, u.h, t, &bad);
+  // source and bytes of copy c (0 bytes: nothing to copy)
+  __device__ __forceinline__ int source(const ChunkArgs& a, const CachePos& u, const TileTokens& tt, int c, int pid,
+                                        const uint8_t** src, int* at, bool* bad) const {
+    const int t = tt.t0 + half * PIECE + (c << a.copy_shift), sub = t & ~31;
+    if (c >= (PIECE >> a.copy_shift) || t >= u.qe || sub + 32 <= tt.v0 || sub >= tt.v1) return 0;
+    const bool cold = t < u.ce;
+    const int row = cold ? row_cold : row_main;
+    *at = ((t - tt.t0 - half * PIECE) >> 5) * a.sub_bytes + (per_channel ? 0 : (t & 31) * row);
+    if (a.lo.paged) {
+      if (pid < 0 || pid >= a.lo.n_pages) {
+        *bad = true;
+        return 0;
       }
+      *src = main0 + pid * page_stride + (int64_t)(t % a.lo.pt) * row;
+    } else {
+      int r = per_channel ? t >> 5 : t;
+      if (ring && !cold) r %= ring;
+      *src = (cold ? cold0 : main0) + (int64_t)r * row;
     }
-    const uint32_t bytes = f.axis == KVQ_AXIS_CHANNEL ? f.row : f.row << a.copy_shift;
-    active = active && !bad && span_ok(a.lo, a.cp, which + (cold ? 2 : 0), src, bytes);
-    const uint32_t bads = __ballot_sync(0xffffffffu, bad);
-    const uint32_t total = __reduce_add_sync(0xffffffffu, active ? bytes : 0u);
-    if (lane == 0) {
-      *bad_at = bads;
-      if (bads) atomicOr(a.status, KVQ_DEV_PAGE);
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(total) : "memory");
-    }
-    __syncwarp();
-    if (active) copy(dst + ((t - a0) >> 5) * a.sub_bytes + (t & 31) * f.row, src, bytes, bar);
-  }
-
-  // Pages whose rows are no whole 16-byte words, or do not divide a subtile: 2 bytes at a time.
-  __device__ __noinline__ void piece_direct(const Unit& u, const TileTokens& tt, int which, int a0, int qe, uint32_t dst,
-                                            uint32_t bar, uint32_t* bad_at) const {
-    const FmtInfo& f = fmt_main(a.lo, which);
-    for (int i = 0; i < PIECE; ++i) {
-      const int t = a0 + i;
-      if (t >= qe || (t & ~31) + 32 <= tt.v0 || (t & ~31) >= tt.v1) continue;
-      bool bad = false;
-      const uint8_t* src = main_row(a.lo, a.cp, which, u.layer, u.b, u.h, t, &bad);
-      const uint32_t to = dst + (i >> 5) * a.sub_bytes + (t & 31) * f.row;
-      for (int e = 2 * lane; e < f.row; e += 64) {
-        // a page out of range reads as blocks of scale 0 (and zero 0)
-        const uint16_t v = bad ? (uint16_t)0 : *reinterpret_cast<const uint16_t*>(src + e);
-        asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(to + e), "h"(v) : "memory");
-      }
-      if (bad && lane == 0) atomicOr(a.status, KVQ_DEV_PAGE);
-    }
-    __syncwarp();
-    if (lane == 0) {
-      *bad_at = 0;
-      bar_arrive(bar);
-    }
+    const int bytes = per_channel ? row : row << a.copy_shift;
+    return span_ok(a.lo, a.cp, which + (cold ? 2 : 0), *src, bytes) ? bytes : 0;
   }
 };
+
+// The lanes' bulk copies, one after the other with uniform operands (see elect_one).
+__device__ __forceinline__ void copy_each(bool mine, uint32_t dst, const uint8_t* src, int bytes, uint32_t bar) {
+  const uint64_t from = reinterpret_cast<uint64_t>(src);
+  uint32_t todo = __ballot_sync(0xffffffffu, mine);
+#pragma unroll 1
+  while (todo) {
+    const int c = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const uint32_t d = __shfl_sync(0xffffffffu, dst, c), n = __shfl_sync(0xffffffffu, (uint32_t)bytes, c),
+                   b = __shfl_sync(0xffffffffu, bar, c);
+    const uint64_t f = __shfl_sync(0xffffffffu, from, c);
+    if (elect_one())
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(d),
+                   "l"(f), "r"(n), "r"(b)
+                   : "memory");
+    __syncwarp();
+  }
+}
 
 // ---- the kernel ----------------------------------------------------------------------
 
@@ -760,7 +914,8 @@ struct ChunkShape {
   static constexpr int QTILES = PAIRED ? 2 : 1;
   static constexpr int RT = 128 * QTILES;  // rows of a row tile
   static constexpr int SOFT_WARPS = 4 * STREAMS;
-  static constexpr int WARPS = SOFT_WARPS + kChunkDequantWarps + 2;  // and the loader and product warps
+  static constexpr int LOAD_WARP = SOFT_WARPS + kChunkDequantWarps, MMA_WARP = LOAD_WARP + 1;
+  static constexpr int WARPS = MMA_WARP + 1;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr uint32_t Q_BYTES = 128u * D * 2;
   static constexpr uint32_t TILE_BYTES = (uint32_t)NT * D * 2;  // 32 KiB
@@ -769,114 +924,173 @@ struct ChunkShape {
 };
 
 struct ChunkShared {
-  uint64_t raw_full[kChunkMaxSlots], raw_empty[kChunkMaxSlots];
-  uint32_t bad_pages[kChunkMaxSlots];
+  uint64_t raw_full[4 * kChunkBars], raw_empty[4 * kChunkBars];  // [piece kind][tile mod kChunkBars]
+  uint32_t bad_pages[4 * kChunkBars];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], s_full[2], p_full[2], o_full, pv_done, soft;
   uint32_t tmem;
   uint32_t gave_up;
   uint32_t nonfinite;
   uint32_t last;  // this CTA joins the unit's partials
   LineStart start;
-  int64_t scan[32];
+  Run runs[18];   // one per warp
+  int scan[32];
   uint32_t pair_table[256];  // TBQ4: centroids of a byte's two indices
 };
 
+// The loader's work for pages whose rows are no whole 16-byte words, or do not divide a subtile: piece
+// by piece, 2 bytes at a time.  A page out of range reads as blocks of scale 0 (and zero 0).
+template <int D, int RT>
+__device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Run& run, bool more, uint32_t raw_at, int lane) {
+  uint32_t kt = 0, slot = 0, n = 0;
+  for (; more; more = warp_run<D, RT>(a, sh.start, run, 1)) {
+    const CachePos u{run.u.layer + a.layer0, run.u.b, run.u.h, run.u.T, q_end_of(a.lo, run.u.T), c_end_of(a.lo, run.u.T)};
+    for (int j = run.t0; j < run.t1; ++j, ++kt) {
+      const TileTokens tt = tile_tokens<D>(run.u, j);
+      for (int piece = 0; piece < 4; ++piece, ++n) {
+        const int which = piece >> 1, a0 = tt.t0 + (piece & 1) * (chunk_tile(D) / 2), row = which ? a.lo.vf.row : a.lo.kf.row;
+        if (n >= (uint32_t)a.slots) {  // the slot's last piece must have been read
+          const uint32_t last = n - a.slots, bar = (last & 3) * kChunkBars + ((last >> 2) & (kChunkBars - 1));
+          if (!__all_sync(0xffffffffu, bar_wait(smem_addr(&sh.raw_empty[bar]), (last >> 2) / kChunkBars & 1, &sh.gave_up))) return;
+        }
+        for (int i = 0; i < chunk_tile(D) / 2; ++i) {
+          const int t = a0 + i;
+          if (t >= u.qe || (t & ~31) + 32 <= tt.v0 || (t & ~31) >= tt.v1) continue;
+          bool bad = false;
+          const uint8_t* src = main_row(a.lo, a.cp, which, u.layer, u.b, u.h, t, &bad);
+          const uint32_t to = raw_at + slot * a.slot_bytes + (i >> 5) * a.sub_bytes + (t & 31) * row;
+          for (int e = 2 * lane; e < row; e += 64) {
+            const uint16_t v = bad ? (uint16_t)0 : *reinterpret_cast<const uint16_t*>(src + e);
+            asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(to + e), "h"(v) : "memory");
+          }
+          if (bad && lane == 0) atomicOr(a.status, KVQ_DEV_PAGE);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          const int bar = piece * kChunkBars + (kt & (kChunkBars - 1));
+          sh.bad_pages[bar] = 0;
+          bar_arrive(smem_addr(&sh.raw_full[bar]));
+        }
+        if (++slot == (uint32_t)a.slots) slot = 0;
+      }
+    }
+  }
+}
+
+// A dequantizing warp's half of a piece that the hot path does not cover: one
+// call with few arguments (the caller's registers are short), everything else worked out again.
+template <int D, int DT>
+__device__ __noinline__ void cold_piece(const ChunkArgs& a, ChunkShared& sh, const Run& run, uint32_t tiles_at,
+                                        uint32_t raw_at, int dw, uint32_t kt, uint32_t slot, int j) {
+  constexpr int NT = chunk_tile(D);
+  const int piece = dw >> 1, which = dw >> 2, half = piece & 1, part = dw & 1, lane = threadIdx.x & 31;
+  const bool per_channel = (which ? a.lo.vf.axis : a.lo.kf.axis) == KVQ_AXIS_CHANNEL;
+  const CachePos u{run.u.layer + a.layer0, run.u.b, run.u.h, run.u.T, q_end_of(a.lo, run.u.T), c_end_of(a.lo, run.u.T)};
+  const TileTokens tt = tile_tokens<D>(run.u, j);
+  const int a0 = tt.t0 + half * (NT / 2);
+  const uint32_t staged = raw_at + slot * a.slot_bytes, bad = sh.bad_pages[piece * kChunkBars + (kt & (kChunkBars - 1))];
+  const uint32_t dst = tiles_at + (kt & 1) * (uint32_t)NT * D * 2;
+  if (which == 0 && (a.lo.flags & KVQ_K_PRE_ROPE))
+    turned_piece<D, DT>(a, u, tt, a0, staged, bad, dst, part * 32 + lane, &sh.nonfinite);
+  else
+    mixed_piece<D, DT>(a, u, which, half, part, lane, per_channel, (a.lo.flags & (which ? KVQ_ROTATE_V : KVQ_ROTATE_K)) != 0, a0,
+                       tt.v0 & ~31, (tt.v1 + 31) & ~31, staged, bad, dst, tt.t0, which == 1 && kt < 2, sh.pair_table,
+                       &sh.nonfinite);
+}
+
 // Sum over the block's threads of x, and the exclusive prefix.
 template <int THREADS>
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* scan, int64_t* total) {
+__device__ __forceinline__ int block_sum(int x, int* scan, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t y = x;
+  int y = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
     if (lane >= o) y += z;
   }
   __syncthreads();
   if (lane == 31) scan[warp] = y;
   __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const int64_t s = scan[w];
-    if (w < warp) before += s;
-    all += s;
-  }
-  *total = all;
-  return before + y - x;
+  // every warp sums the warps' totals by itself
+  const int s = lane < THREADS / 32 ? scan[lane] : 0;
+  *total = __reduce_add_sync(0xffffffffu, s);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? s : 0) + y - x;
 }
 
 // Finds this CTA's stretch of the line of tiles and the unit it starts in.
 template <int D, int RT, int THREADS>
 __device__ __forceinline__ void find_start(const ChunkArgs& a, ChunkShared& sh) {
   const int lane = a.by_warp ? threadIdx.x & 31 : 0, lanes = a.by_warp ? 32 : 1;
-  const int group = threadIdx.x / lanes, groups = THREADS / lanes;
-  const int64_t lh = (int64_t)a.n_layers * a.lo.H;
+  const int group = a.by_warp ? threadIdx.x >> 5 : threadIdx.x, groups = a.by_warp ? THREADS / 32 : THREADS;
   bool bad = false;
-  int64_t line = 0;
+  int line = 0, mine = 0, at = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.lo.B; b0 += groups) {
     const int b = b0 + group;
-    const int64_t mine = b < a.lo.B ? seq_tiles<D, RT>(a, b, lane, lanes, &bad) : 0;
-    int64_t sum;
-    (void)block_sum<THREADS>(mine, sh.scan, &sum);
+    mine = b < a.lo.B ? seq_tiles<D, RT>(a, b, lane, lanes, &bad) : 0;
+    int sum;
+    at = line + block_sum<THREADS>(mine, sh.scan, &sum);
     line += sum;
   }
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0 && __ldg(a.cu_q) != 0) bad = true;
     if (bad) atomicOr(a.status, KVQ_DEV_LENGTH);
   }
-  const int64_t all = line * lh;
+  const int all = line * a.n_layers * a.lo.H;
   // at least two tiles a run: joining costs about as much
-  const int64_t per = max((all + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)2);
-  const int64_t begin = min(all, per * blockIdx.x), end = min(all, begin + per);
+  const int per = max((all + (int)gridDim.x - 1) / (int)gridDim.x, 2);
+  const int begin = (int)min((int64_t)all, (int64_t)per * blockIdx.x), end = min(all - begin, per) + begin;
   if (threadIdx.x == 0) {
     sh.start.begin = begin;
     sh.start.end = end;
     sh.start.per_cta = per;
   }
   if (begin >= end) return;
-  const int64_t x = begin % line;  // place within one (layer, kv head)
-  int64_t base = 0;
+  const int lh = begin / line, x = begin - lh * line;  // place within one (layer, kv head)
+  int base = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.lo.B && base <= x; b0 += groups) {
     const int b = b0 + group;
-    bool ignore = false;
-    int64_t mine = b < a.lo.B ? seq_tiles<D, RT>(a, b, lane, lanes, &ignore) : 0;
-    int64_t sum, at = block_sum<THREADS>(mine, sh.scan, &sum);
-    if (a.by_warp) {  // the sequence's tiles, seen from lane 0
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (a.lo.B > groups) {  // else the sums of the pass above are still there
+      bool ignore = false;
+      mine = b < a.lo.B ? seq_tiles<D, RT>(a, b, lane, lanes, &ignore) : 0;
+      int sum;
+      at = base + block_sum<THREADS>(mine, sh.scan, &sum);
+      base += sum;
+    } else {
+      base = line;
     }
-    at += base;
-    if (lane == 0 && b < a.lo.B && x >= at && x < at + mine) {
+    const int tiles = a.by_warp ? __reduce_add_sync(0xffffffffu, mine) : mine;  // the sequence's, seen from lane 0
+    if (lane == 0 && b < a.lo.B && x >= at && x < at + tiles) {
       Unit u;
       (void)valid_seq(a, b, &u.n, &u.T, &u.cu);
-      int64_t left = x - at;
-      u.rt = 0;
-      for (;;) {
+      int left = x - at;
+#pragma unroll 1
+      for (u.rt = 0;; ++u.rt) {
         unit_tiles<D, RT>(a, u);
         if (left < u.nt) break;
         left -= u.nt;
-        ++u.rt;
       }
-      sh.start.lh = (int)(begin / line);
+      sh.start.lh = lh;
       sh.start.b = b;
       sh.start.rt = u.rt;
-      sh.start.tile = (int)left;
+      sh.start.tile = left;
     }
-    base += sum;
   }
 }
 
 // V's values that are not finite were left out of the products: every row
 // that sees such a window token gets the value itself (an infinity stays one
-// under any positive weight, a NaN stays NaN).  Row of query position p, 4 channels of a lane.
+// under any positive weight, a NaN stays NaN).  Channels [ch, ch + n) of the written output row of
+// query position p.
 template <int DT>
-__device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Unit& u, int p, int ch, float (&o)[4]) {
-  const int qe = q_end_of(a.lo, u.T);
+__device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Run& run, int p, int ch, int n, uint16_t* out) {
+  const int qe = q_end_of(a.lo, run.u.T);
   for (int t = qe; t <= p; ++t) {
     if (a.window && t <= p - a.window && t >= a.sinks) continue;
-    const uint16_t* v = resid_row(a.lo, a.cp, 1, u.layer, u.b, u.h, t) + ch;
-    for (int e = 0; e < 4; ++e) {
-      const float x = in_to_f32(v[e], DT);
-      if (!(fabsf(x) <= 3.402823466e38f)) o[e] += x;
+    const uint16_t* v = resid_row(a.lo, a.cp, 1, run.u.layer + a.layer0, run.u.b, run.u.h, t);
+    for (int c = ch; c < ch + n; ++c) {
+      const float x = in_to_f32(v[c], DT);
+      if (!(fabsf(x) <= 3.402823466e38f)) out[c] = (uint16_t)pack16<DT>(in_to_f32(out[c], DT) + x, 0.f);
     }
   }
 }
@@ -890,25 +1104,33 @@ __device__ __forceinline__ bool soft_sync(uint32_t bar, uint32_t& phase, volatil
   return ok;
 }
 
+// Row r of a row tile: where its query (or output) starts.
+__device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, int r) {
+  const int row = u.r0 + r, tok = div_g(a, row);
+  return (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + u.h * a.lo.g + (row - tok * a.lo.g)) * a.lo.D;
+}
+
 // Joins the partial rows of one unit and writes its output rows; all softmax threads.
 template <int D, int DT, bool PAIRED>
-__device__ void join_unit(const ChunkArgs& a, const Unit& u, const LineStart& line, int64_t unit_pos, bool cut,
-                          bool fix, int tid) {
+__device__ __noinline__ void join_unit(const ChunkArgs& a, const Run& run, const LineStart& line, bool cut, bool fix) {
   using C = ChunkShape<D, PAIRED>;
   constexpr int N = D / 128;
-  constexpr int64_t PR = chunk_part_row(D), SLOT = (int64_t)chunk_slot_rows(D) * PR;
-  const int lane = tid & 31, warp = tid >> 5;
-  const int c0 = cut ? (int)(unit_pos / line.per_cta) : blockIdx.x;
-  const int c1 = cut ? (int)((unit_pos + u.nt - 1) / line.per_cta) : blockIdx.x;
+  constexpr int PR = chunk_part_row(D), SLOT = chunk_slot_rows(D) * PR;
+  const Unit& u = run.u;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int unit_pos = run.pos - run.t0;
+  const int c0 = cut ? unit_pos / line.per_cta : blockIdx.x;
+  const int c1 = cut ? (unit_pos + u.nt - 1) / line.per_cta : blockIdx.x;
+  const int slot0 = !cut ? 2 : unit_pos == c0 * line.per_cta ? 0 : 1;  // of the first CTA; the others' is 0
   const int copies = PAIRED ? 1 : C::STREAMS * a.rep;  // partial rows of one query row in one slot
   const int lanes_per = 128 / a.rep;
   const int parts = (c1 - c0 + 1) * copies;
   auto part = [&](int i, int r) {
-    const int c = c0 + i / copies, k = i % copies;
-    const int slot = !cut ? 2 : c > c0 || unit_pos == (int64_t)c * line.per_cta ? 0 : 1;
-    const int row = PAIRED ? r : (k / a.rep) * 128 + (k % a.rep) * lanes_per + r;
-    return a.partials + ((int64_t)c * kChunkSlots + slot) * SLOT + row * PR;
+    const int c = PAIRED ? i : i / copies, k = PAIRED ? 0 : i - c * copies;  // k: stream k / rep, repetition k % rep
+    const int s = k / a.rep, row = PAIRED ? r : s * 128 + (k - s * a.rep) * lanes_per + r;
+    return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
+#pragma unroll 1
   for (int r = warp; r < u.rows; r += C::SOFT_WARPS) {
     float M = -INFINITY;
     for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(part(i, r) + D));
@@ -917,21 +1139,23 @@ __device__ void join_unit(const ChunkArgs& a, const Unit& u, const LineStart& li
     float L = 0.f, acc[N][4];
 #pragma unroll
     for (int c = 0; c < N; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+#pragma unroll 1
     for (int i0 = 0; i0 < parts; i0 += 32) {
       float w = 0.f;
+      const float* p = part(min(i0 + lane, parts - 1), r);
       if (i0 + lane < parts) {
-        const float* p = part(i0 + lane, r) + D;
-        const float m = __ldcg(p), l = __ldcg(p + 1);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
         // a part that saw none of the row's tokens has m = -inf and l = 0
-        w = m == -INFINITY && l == 0.f ? 0.f : ex2(m - M);
-        L += w == 0.f && l == 0.f ? 0.f : w * l;
+        w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2(ml.x - M);
+        L += w == 0.f && ml.y == 0.f ? 0.f : w * ml.y;
       }
+      const uint32_t off = (uint32_t)((p - a.partials) >> 2);  // in 16-byte words
       const int k1 = min(32, parts - i0);
 #pragma unroll 4
       for (int k = 0; k < k1; ++k) {
         const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float4* o4 = reinterpret_cast<const float4*>(a.partials) + __shfl_sync(0xffffffffu, off, k);
         if (wk == 0.f) continue;
-        const float4* o4 = reinterpret_cast<const float4*>(part(i0 + k, r));
 #pragma unroll
         for (int c = 0; c < N; ++c) {
           const float4 v = __ldcg(o4 + 32 * c + lane);
@@ -944,68 +1168,141 @@ __device__ void join_unit(const ChunkArgs& a, const Unit& u, const LineStart& li
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const int row = u.r0 + r, tok = row / a.lo.g, head = u.h * a.lo.g + row % a.lo.g;
-    uint16_t* dst = a.out + (((int64_t)(u.layer - a.layer0) * a.total_q + u.cu + tok) * a.lo.Hq + head) * D;
+    uint16_t* dst = a.out + query_row(a, u, r);
     const float inv = 1.f / L;
 #pragma unroll
     for (int c = 0; c < N; ++c) {
       float v[4] = {acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv};
       if (a.lo.flags & KVQ_ROTATE_V) warp_unrotate128(v, a.lo.d1, a.lo.d2);
-      if (fix) add_nonfinite<DT>(a, u, u.T - u.n + tok, 128 * c + 4 * lane, v);
       *reinterpret_cast<uint2*>(dst + 128 * c + 4 * lane) = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+      if (fix) add_nonfinite<DT>(a, run, u.T - u.n + div_g(a, u.r0 + r), 128 * c + 4 * lane, 4, dst);
     }
   }
 }
 
 // In-thread inverse of the 128-point transform on TMEM columns [col, col +
-// 128) of this lane, in place: two 64-point halves, then the last stage.
-__device__ void unrotate_columns(uint32_t col, const uint32_t* d1, const uint32_t* d2, float factor) {
-  uint32_t r0[32], r1[32];
+// 128) of this lane, in place and times `factor`: four 32-point transforms,
+// then the two stages between them, eight columns of each at a time.
+__device__ __noinline__ void unrotate_columns(const ChunkArgs& a, uint32_t col, float factor) {
+  uint32_t r[32];
   const float f = factor * hadamard_scale();
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    tmem_ld32(col + 64 * half, r0);
-    tmem_ld32(col + 64 * half + 32, r1);
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld32(col + 32 * c, r);
     tmem_wait_ld();
-    float x[64];
+    const uint32_t signs = a.lo.d2[c];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      x[i] = __uint_as_float(r0[i] ^ (((d2[2 * half] >> i) & 1u) << 31)) * f;
-      x[32 + i] = __uint_as_float(r1[i] ^ (((d2[2 * half + 1] >> i) & 1u) << 31)) * f;
-    }
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i] ^ (((signs >> i) & 1u) << 31)) * f);
 #pragma unroll
-    for (int h = 1; h < 64; h <<= 1)
+    for (int h = 1; h < 32; h <<= 1)
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
+      for (int i = 0; i < 32; ++i)
         if (!(i & h)) {
-          const float u = x[i], v = x[i + h];
-          x[i] = u + v;
-          x[i + h] = u - v;
+          const float u = __uint_as_float(r[i]), v = __uint_as_float(r[i + h]);
+          r[i] = __float_as_uint(u + v);
+          r[i + h] = __float_as_uint(u - v);
         }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      r0[i] = __float_as_uint(x[i]);
-      r1[i] = __float_as_uint(x[32 + i]);
-    }
-    tmem_st32(col + 64 * half, r0);
-    tmem_st32(col + 64 * half + 32, r1);
-    tmem_wait_st();
+    tmem_st32(col + 32 * c, r);
   }
+  tmem_wait_st();
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    tmem_ld32(col + 32 * c, r0);
-    tmem_ld32(col + 64 + 32 * c, r1);
+  for (int k = 0; k < 32; k += 8) {
+    uint32_t q[4][8];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld8(col + 32 * c + k, q[c]);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float u = __uint_as_float(r0[i]), v = __uint_as_float(r1[i]);
-      r0[i] = __float_as_uint(u + v) ^ (((d1[c] >> i) & 1u) << 31);
-      r1[i] = __float_as_uint(u - v) ^ (((d1[2 + c] >> i) & 1u) << 31);
+    for (int i = 0; i < 8; ++i) {
+      const float x0 = __uint_as_float(q[0][i]), x1 = __uint_as_float(q[1][i]), x2 = __uint_as_float(q[2][i]),
+                  x3 = __uint_as_float(q[3][i]);
+      const float s0 = x0 + x1, d0 = x0 - x1, s1 = x2 + x3, d1 = x2 - x3;
+      q[0][i] = __float_as_uint(s0 + s1) ^ (((a.lo.d1[0] >> (k + i)) & 1u) << 31);
+      q[1][i] = __float_as_uint(d0 + d1) ^ (((a.lo.d1[1] >> (k + i)) & 1u) << 31);
+      q[2][i] = __float_as_uint(s0 - s1) ^ (((a.lo.d1[2] >> (k + i)) & 1u) << 31);
+      q[3][i] = __float_as_uint(d0 - d1) ^ (((a.lo.d1[3] >> (k + i)) & 1u) << 31);
     }
-    tmem_st32(col + 32 * c, r0);
-    tmem_st32(col + 64 + 32 * c, r1);
-    tmem_wait_st();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_st8(col + 32 * c + k, q[c]);
   }
+  tmem_wait_st();
+}
+
+// ---- softmax of one tile, one row per thread ----------------------------------------
+
+struct RowSeen {
+  int pos, win_lo, sinks;  // visible tokens: [win_lo, pos] and [0, sinks)
+};
+template <bool MASKED>
+__device__ __forceinline__ void hide(uint32_t (&x)[32], int t, const RowSeen& see) {
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (t + i > see.pos || (t + i < see.win_lo && t + i >= see.sinks)) x[i] = 0xff800000u;
+  }
+}
+// largest score of the row's columns [c0, c1) of S at s_col (tile's first token t0)
+template <bool MASKED>
+__device__ __forceinline__ float tile_max(uint32_t s_col, int c0, int c1, int t0, const RowSeen& see, uint32_t (&x)[32]) {
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    tmem_ld32(s_col + c, x);
+    tmem_wait_ld();
+    hide<MASKED>(x, t0 + c, see);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      m0 = fmaxf(m0, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+      m1 = fmaxf(m1, fmaxf(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])));
+    }
+  }
+  return fmaxf(m0, m1);
+}
+// P = 2^(S sc + mneg) over S, in the input dtype; the sum of P.  x holds the
+// columns already when there are only 32.
+template <int DT, bool MASKED>
+__device__ __forceinline__ float tile_exp(uint32_t s_col, int c0, int c1, int t0, const RowSeen& see, float sc, float mneg,
+                                          uint32_t (&x)[32]) {
+  const uint64_t sc2 = pk2(sc, sc), mneg2 = pk2(mneg, mneg);  // packed pairs: half the instructions
+  uint64_t la = 0, lb = 0;
+  const bool have = c1 - c0 == 32;
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    if (!have) {
+      tmem_ld32(s_col + c, x);
+      tmem_wait_ld();
+      hide<MASKED>(x, t0 + c, see);
+    }
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float e0, e1;
+      upk2(fma2(pk2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, mneg2), e0, e1);
+      e0 = ex2(e0);
+      e1 = ex2(e1);
+      if (i & 1)
+        la = add2(la, pk2(e0, e1));
+      else
+        lb = add2(lb, pk2(e0, e1));
+      p[i] = pack16<DT>(e0, e1);
+    }
+    tmem_st16(s_col + c / 2, p);
+  }
+  float l0, l1;
+  upk2(add2(la, lb), l0, l1);
+  return l0 + l1;
+}
+template <int D>
+__device__ __forceinline__ void rescale_columns(uint32_t o_col, float f) {
+  uint32_t x[32];
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    tmem_ld32(o_col + c, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+    tmem_st32(o_col + c, x);
+  }
+  tmem_wait_st();
 }
 
 template <int D, int DT, bool PAIRED>
@@ -1021,19 +1318,22 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   const uint32_t raw_at = v_at + 2 * C::TILE_BYTES;
 
   // set-up that needs nothing of the stream's earlier work
+  if (warp == 1) {
+    bar_init(smem_addr(&sh.raw_full[lane]), 1);
+    bar_init(smem_addr(&sh.raw_empty[lane]), 2);  // a piece's two warps
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  static_assert(4 * kChunkBars == 32, "one barrier a lane");
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      bar_init(smem_addr(&sh.k_full[i]), kChunkDequantWarps);
-      bar_init(smem_addr(&sh.v_full[i]), kChunkDequantWarps);
+      bar_init(smem_addr(&sh.k_full[i]), kChunkDequantWarps / 2);
+      bar_init(smem_addr(&sh.v_full[i]), kChunkDequantWarps / 2);
       bar_init(smem_addr(&sh.k_empty[i]), 1);
       bar_init(smem_addr(&sh.v_empty[i]), 1);
       bar_init(smem_addr(&sh.q_full[i]), 4);
       bar_init(smem_addr(&sh.s_full[i]), 1);
       bar_init(smem_addr(&sh.p_full[i]), 4);
-    }
-    for (int i = 0; i < a.slots; ++i) {
-      bar_init(smem_addr(&sh.raw_full[i]), 1);
-      bar_init(smem_addr(&sh.raw_empty[i]), kChunkDequantWarps);
     }
     bar_init(smem_addr(&sh.o_full), 1);
     bar_init(smem_addr(&sh.pv_done), 1);
@@ -1042,17 +1342,15 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
     sh.gave_up = 0;
     sh.nonfinite = 0;
   }
-  if (warp == C::WARPS - 1) {
+  if (warp == C::MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_addr(&sh.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
-  // V tiles and queries start as zeros: rows that are never written must not
-  // hold infinities or NaN (a zero probability times one is NaN)
+  // query rows that no unit writes are zeros
+#pragma unroll 1
   for (uint32_t e = tid * 16; e < C::QTILES * C::Q_BYTES; e += C::THREADS * 16)
     *reinterpret_cast<uint4*>(smem + e) = make_uint4(0, 0, 0, 0);
-  for (uint32_t e = tid * 16; e < 2 * C::TILE_BYTES; e += C::THREADS * 16)
-    *reinterpret_cast<uint4*>(smem + C::QTILES * C::Q_BYTES + 2 * C::TILE_BYTES + e) = make_uint4(0, 0, 0, 0);
   if (a.lo.flags & (KVQ_TBQ4_K | KVQ_TBQ4_V))
     for (int i = tid; i < 256; i += C::THREADS) {
       const __half2 p = __floats2half2_rn(a.lo.cb[i & 15], a.lo.cb[i >> 4]);
@@ -1066,165 +1364,287 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const LineStart line = sh.start;
+  Run& run = sh.runs[warp];
+  uint32_t* const gave_up = &sh.gave_up;
   const bool k_chan = a.lo.kf.axis == KVQ_AXIS_CHANNEL, v_chan = a.lo.vf.axis == KVQ_AXIS_CHANNEL;
-  Run run;
-  bool more = first_run<D, RT>(a, line, run);
+  bool more = warp_run<D, RT>(a, sh.start, run, 0);
 
-  if (warp == C::WARPS - 1) {
+  if (warp == C::MMA_WARP) {
     // ---- products: one thread ----------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t F = DT == KVQ_DT_F16 ? 0 : 1;
-      constexpr uint32_t base = (1u << 4) | (F << 7) | (F << 10) | ((128u >> 4) << 24);
-      const uint32_t qk_desc = base | ((uint32_t)k_chan << 16) | ((uint32_t)(NT >> 3) << 17);
-      const uint32_t pv_desc = base | ((uint32_t)!v_chan << 16) | ((uint32_t)(D >> 3) << 17);
-      uint32_t kt = 0;             // tiles of this CTA so far
-      uint32_t np[2] = {0, 0};     // steps of each S buffer so far
-      uint32_t runs = 0;
-      bool ok = true;
-      for (; more && ok; more = next_run<D, RT>(a, line, run), ++runs) {
-        const int tiles = run.t1 - run.t0, steps = PAIRED ? 2 * tiles : tiles;
-        auto tile_of = [&](int s) { return kt + (PAIRED ? s >> 1 : s); };
-        auto qk = [&](int s) {
-          const uint32_t t = tile_of(s), st = t & 1;
-          if (s < C::QTILES) ok = ok && bar_wait(smem_addr(&sh.q_full[s]), runs & 1, &sh.gave_up);
-          ok = ok && bar_wait(smem_addr(&sh.k_full[st]), (t >> 1) & 1, &sh.gave_up);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t q0 = q_at + (PAIRED ? (s & 1) * C::Q_BYTES : 0), k0 = k_at + st * C::TILE_BYTES;
+    constexpr uint32_t F = DT == KVQ_DT_F16 ? 0 : 1;
+    constexpr uint32_t base = (1u << 4) | (F << 7) | (F << 10) | ((128u >> 4) << 24);
+    const uint32_t qk_desc = base | ((uint32_t)k_chan << 16) | ((uint32_t)(NT >> 3) << 17);
+    const uint32_t pv_desc = base | ((uint32_t)!v_chan << 16) | ((uint32_t)(D >> 3) << 17);
+    const uint64_t q_desc = operand_desc(q_at, 0, 1024), k_desc = operand_desc(k_at, k_chan ? D * 128 : 0, 1024),
+                   v_desc = operand_desc(v_at, v_chan ? 0 : NT * 128, 1024);
+    uint32_t kt = 0;             // tiles of this CTA so far
+    uint32_t np0 = 0, np1 = 0;   // steps of each S buffer so far
+    uint32_t runs = 0;
+    bool ok = true;
+    for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1), ++runs) {
+      const int tiles = run.t1 - run.t0, steps = PAIRED ? 2 * tiles : tiles;
+      {
+#pragma unroll 1
+        for (int i = 0; i < 2 * steps + 2 && ok; ++i) {
+          // order: scores of steps 0 and 1, then outputs of step s and scores of s + 2 in turn
+          const int s = i < 2 ? i : (i & 1) ? (i - 3) / 2 + 2 : (i - 2) / 2;
+          const bool scores = i < 2 || (i & 1);
+          if (s >= steps) continue;
+          const uint32_t t = kt + (PAIRED ? s >> 1 : s), st = t & 1, b = s & 1;
+          const uint32_t s_col = tmem + C::S_COL + b * NT;
+          if (scores) {
+            if (s < C::QTILES) ok = bar_wait(smem_addr(&sh.q_full[s]), runs & 1, gave_up);
+            ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&sh.k_full[st]), (t >> 1) & 1, gave_up));
+            if (!ok) break;
+            tc_fence_after();
+            // descriptors differ in their address alone: steps of 16 summed values
+            const uint64_t da = q_desc + (PAIRED ? b * (C::Q_BYTES >> 4) : 0), db = k_desc + st * (C::TILE_BYTES >> 4);
+            if (elect_one()) {
+              if (k_chan) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t da = operand_desc(q0 + (k >> 2) * 16384 + (k & 3) * 32, 0, 1024);
-            const uint64_t db = k_chan ? operand_desc(k0 + k * 2048, D * 128, 1024)
-                                       : operand_desc(k0 + (k >> 2) * (NT * 128) + (k & 3) * 32, 0, 1024);
-            mma_ss(tmem + C::S_COL + (s & 1) * NT, da, db, qk_desc, k > 0);
-          }
-          tc_commit(smem_addr(&sh.s_full[s & 1]));
-          if (!PAIRED || (s & 1)) tc_commit(smem_addr(&sh.k_empty[st]));
-        };
-        auto pv = [&](int s) {
-          const uint32_t t = tile_of(s), st = t & 1;
-          ok = ok && bar_wait(smem_addr(&sh.p_full[s & 1]), np[s & 1] & 1, &sh.gave_up);
-          ++np[s & 1];
-          ok = ok && bar_wait(smem_addr(&sh.v_full[st]), (t >> 1) & 1, &sh.gave_up);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t v0 = v_at + st * C::TILE_BYTES;
-          const uint32_t o = tmem + C::O_COL + (C::STREAMS == 2 ? (s & 1) * D : 0);
-          const bool fresh = C::STREAMS == 2 ? s < 2 : s == 0;
+                for (int k = 0; k < D / 16; ++k)
+                  mma_ss(s_col, da + (k >> 2) * 1024 + (k & 3) * 2, db + k * 128, qk_desc, k > 0);
+              } else {
 #pragma unroll
-          for (int k = 0; k < NT / 16; ++k) {
-            const uint64_t db = v_chan ? operand_desc(v0 + (k >> 2) * (D * 128) + (k & 3) * 32, 0, 1024)
-                                       : operand_desc(v0 + k * 2048, NT * 128, 1024);
-            mma_ts(o, tmem + C::S_COL + (s & 1) * NT + k * 8, db, pv_desc, !fresh || k > 0);
+                for (int k = 0; k < D / 16; ++k)
+                  mma_ss(s_col, da + (k >> 2) * 1024 + (k & 3) * 2, db + (k >> 2) * (NT * 8) + (k & 3) * 2, qk_desc, k > 0);
+              }
+              tc_commit(smem_addr(&sh.s_full[b]));
+              if (!PAIRED || b) tc_commit(smem_addr(&sh.k_empty[st]));
+            }
+            __syncwarp();
+          } else {
+            const uint32_t done = b ? np1 : np0;
+            ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.v_full[st]), (t >> 1) & 1, gave_up) &&
+                                             bar_wait(smem_addr(&sh.p_full[b]), done & 1, gave_up));
+            if (!ok) break;
+            np0 += b ^ 1;
+            np1 += b;
+            tc_fence_after();
+            const uint64_t db = v_desc + st * (C::TILE_BYTES >> 4);
+            const uint32_t o = tmem + C::O_COL + (C::STREAMS == 2 ? b * D : 0);
+            const bool add = C::STREAMS == 2 ? s >= 2 : s > 0;
+            if (elect_one()) {
+              if (v_chan) {
+#pragma unroll
+                for (int k = 0; k < NT / 16; ++k)
+                  mma_ts(o, s_col + k * 8, db + (k >> 2) * (D * 8) + (k & 3) * 2, pv_desc, add || k > 0);
+              } else {
+#pragma unroll
+                for (int k = 0; k < NT / 16; ++k) mma_ts(o, s_col + k * 8, db + k * 128, pv_desc, add || k > 0);
+              }
+              if (C::STREAMS == 1) tc_commit(smem_addr(&sh.pv_done));
+              if (!PAIRED || b) tc_commit(smem_addr(&sh.v_empty[st]));
+            }
+            __syncwarp();
           }
-          if (C::STREAMS == 1) tc_commit(smem_addr(&sh.pv_done));
-          if (!PAIRED || (s & 1)) tc_commit(smem_addr(&sh.v_empty[st]));
-        };
-        qk(0);
-        if (steps > 1) qk(1);
-        for (int s = 0; s < steps && ok; ++s) {
-          pv(s);
-          if (s + 2 < steps && ok) qk(s + 2);
         }
-        if (ok) tc_commit(smem_addr(&sh.o_full));
-        kt += tiles;
+        if (ok && elect_one()) tc_commit(smem_addr(&sh.o_full));
+        __syncwarp();
+      }
+      kt += tiles;
+    }
+  } else if (warp == C::LOAD_WARP && a.direct) {
+    load_direct<D, RT>(a, sh, run, more, raw_at, lane);
+  } else if (warp == C::LOAD_WARP) {
+    // ---- staging ------------------------------------------------------------------------
+    Loader<D> ld;
+    ld.lanes(a, lane);
+    const int piece = lane >> 3;
+    const bool two = (NT / 2) >> a.copy_shift > 8;
+    const uint32_t slots = a.slots;
+    uint32_t kt = 0, slot0 = 0, todo = 0xf;  // tiles so far; slot of the tile's first piece; pieces to ask for
+    bool ok = true;
+    for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1)) {
+      const CachePos u{run.u.layer + a.layer0, run.u.b, run.u.h, run.u.T, q_end_of(a.lo, run.u.T), c_end_of(a.lo, run.u.T)};
+      ld.unit(a, u);
+      const int t1 = run.t1;
+      TileTokens tt = tile_tokens<D>(run.u, run.t0);
+      int pid = ld.page_id(a, u, tt.t0, ld.ln);
+#pragma unroll 1
+      for (int j = run.t0; j < t1; ++j, ++kt) {
+        // the next tile's page ids load while this one waits for slots
+        const TileTokens next = tile_tokens<D>(run.u, min(j + 1, t1 - 1));
+        const int next_pid = ld.page_id(a, u, next.t0, ld.ln);
+        const uint8_t *src0 = nullptr, *src1 = nullptr;
+        int at0 = 0, at1 = 0, bytes0 = 0, bytes1 = 0;
+        uint32_t bads = 0;
+        {
+          bool bad = false;
+          bytes0 = ld.source(a, u, tt, ld.ln, pid, &src0, &at0, &bad);
+          bads = __ballot_sync(0xffffffffu, bad) >> (8 * piece) & 0xffu;
+          if (two) {  // pages of 4 tokens: two copies a lane
+            bad = false;
+            bytes1 = ld.source(a, u, tt, ld.ln + 8, ld.page_id(a, u, tt.t0, ld.ln + 8), &src1, &at1, &bad);
+            bads |= (__ballot_sync(0xffffffffu, bad) >> (8 * piece) & 0xffu) << 8;
+          }
+        }
+        int total = bytes0 + bytes1;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const uint32_t number = 4 * kt + piece, bar = piece * kChunkBars + (kt & (kChunkBars - 1));
+        const uint32_t full = smem_addr(&sh.raw_full[bar]);
+        uint32_t slot = slot0 + piece;
+        while (slot >= slots) slot -= slots;
+        const uint32_t dst = raw_at + slot * a.slot_bytes;
+        // the slot's last piece must have been read
+        const uint32_t last = number - slots, last_bar = (last & 3) * kChunkBars + ((last >> 2) & (kChunkBars - 1));
+        todo = 0xf;
+#pragma unroll 1
+        for (int spin = 0; todo && ok; ++spin) {
+          bool ready = false;
+          if (ld.ln == 0 && (todo >> piece & 1))
+            ready = number < slots || bar_test(smem_addr(&sh.raw_empty[last_bar]), (last >> 2) / kChunkBars & 1);
+          const uint32_t b = __ballot_sync(0xffffffffu, ready);
+          const uint32_t now = (b & 1) | (b >> 7 & 2) | (b >> 14 & 4) | (b >> 21 & 8);
+          const bool go = now >> piece & 1;
+          if (go && ld.ln == 0) {
+            sh.bad_pages[bar] = bads;
+            if (bads) atomicOr(a.status, KVQ_DEV_PAGE);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full), "r"(total) : "memory");
+          }
+          __syncwarp();
+          copy_each(go && bytes0, dst + at0, src0, bytes0, full);
+          if (two) copy_each(go && bytes1, dst + at1, src1, bytes1, full);
+          todo &= ~now;
+          if (!now && (spin > kChunkSpin || *(volatile uint32_t*)gave_up)) {
+            if (lane == 0) *(volatile uint32_t*)gave_up = 1;
+            ok = false;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!ok) break;
+        pid = next_pid;
+        tt = next;
+        slot0 += 4;
+        while (slot0 >= slots) slot0 -= slots;
+      }
+    }
+    // the copies in flight land before the CTA ends, also when a warp has
+    // given up (then `todo` are the last tile's pieces that were not asked for)
+    if (lane < 4) {
+#pragma unroll 1
+      for (uint32_t back = ok || (todo >> lane & 1) ? 1 : 0; back <= 4 && back <= kt; ++back) {
+        const uint32_t t = kt - back, bar = smem_addr(&sh.raw_full[lane * kChunkBars + (t & (kChunkBars - 1))]);
+        for (int k = 0; k < kChunkSpin && !bar_test(bar, t / kChunkBars & 1); ++k) {
+        }
       }
     }
     __syncwarp();
-  } else if (warp >= C::SOFT_WARPS && warp < C::WARPS - 2) {
+  } else if (warp >= C::SOFT_WARPS) {
     // ---- dequantization ---------------------------------------------------------------
-    const int dw = warp - C::SOFT_WARPS;
-    uint32_t kt = 0, slot = 0, lap = 0;
+    // Two warps for each piece (half tile of K or V).
+    uint32_t kt = 0, slot = (warp - C::SOFT_WARPS) >> 1, slots = a.slots;
+    while (slot >= slots) slot -= slots;
     bool ok = true;
-    for (; more && ok; more = next_run<D, RT>(a, line, run)) {
-      const Unit& u = run.u;
-      const int qe = q_end_of(a.lo, u.T), ce = c_end_of(a.lo, u.T);
-      Unit in_cache = u;
-      in_cache.layer += a.layer0;
-      for (int j = run.t0; j < run.t1 && ok; ++j, ++kt) {
-        const uint32_t st = kt & 1, par = ((kt >> 1) & 1) ^ 1;
-        const TileTokens tt = tile_tokens<D>(u, j);
+    for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1)) {
+      int j = run.t0;
 #pragma unroll 1
-        for (int which = 0; which < 2 && ok; ++which) {
-          ok = __all_sync(0xffffffffu, bar_wait(smem_addr(which ? &sh.v_empty[st] : &sh.k_empty[st]), par, &sh.gave_up));
+      while (ok) {
+        // What the hot loop keeps in registers is worked out here, after the
+        // call below, and hidden from hoisting: kept across the call it would live in local memory.
+        int dw = warp - C::SOFT_WARPS;
+        asm volatile("" : "+r"(dw));
+        const int piece = dw >> 1, which = dw >> 2, half = piece & 1, part = dw & 1, j1 = run.t1;
+        const bool per_channel = which ? v_chan : k_chan;
+        const uint32_t empty_at = smem_addr(which ? &sh.v_empty[0] : &sh.k_empty[0]),
+                       filled_at = smem_addr(which ? &sh.v_full[0] : &sh.k_full[0]);
+        const uint32_t full_at = smem_addr(&sh.raw_full[piece * kChunkBars]), read_at = smem_addr(&sh.raw_empty[piece * kChunkBars]);
+        const int qe = q_end_of(a.lo, run.u.T), ce = c_end_of(a.lo, run.u.T);
+        const bool cold = j < j1 && tile_tokens<D>(run.u, j).t0 + half * (NT / 2) < ce;
+        const RunFmt f = run_fmt(a.lo, which, cold);
+        // the hot path's format: bits, 16 for asymmetric blocks; 0: none
+        const int kind = (which == 0 && (a.lo.flags & KVQ_K_PRE_ROPE)) || f.codebook ? 0 : f.bits + (f.zp ? 16 : 0);
+        PiecePlace q;
+        {
+          int toff, row, run32;
+          RunPlace<D>::of(per_channel, RunPlace<D>::number(per_channel, part, 0, lane), &toff, &row, &run32);
+          RunPlace<D>::at(per_channel, f, a.sub_bytes, toff, row, run32, &q.blk, &q.codes);
+          q.step = per_channel ? (D == 128 ? 16 : 32) * f.bb : 8 * f.row;
+          q.line_step = (per_channel ? (D == 128 ? 16 : 32) : 8) * 128;
+          const int tile_row = row + (per_channel ? 0 : half * (NT / 2)), tile_run = run32 + (per_channel ? half * (NT / 64) : 0);
+          q.line = RunPlace<D>::line_at(which ? v_at : k_at, tile_row, tile_run, per_channel ? D : NT);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q.piece16[k] = (((tile_run & 1) * 4 + k) ^ (row & 7)) << 4;
+        }
+        bool landed = false;
 #pragma unroll 1
-          for (int half = 0; half < 2 && ok; ++half) {
-            ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.raw_full[slot]), lap & 1, &sh.gave_up));
-            if (!ok) break;
-            const Dequant<D, DT> dq{a, in_cache, which, dw, lane, (which ? v_at : k_at) + st * C::TILE_BYTES, qe, ce,
-                                    sh.pair_table, &sh.nonfinite, tt.t0 + half * (NT / 2),
-                                    raw_at + slot * a.slot_bytes, *(volatile uint32_t*)&sh.bad_pages[slot]};
-            dq.piece(tt);
-            __syncwarp();
-            if (lane == 0) bar_arrive(smem_addr(&sh.raw_empty[slot]));
-            if (++slot == (uint32_t)a.slots) {
-              slot = 0;
-              ++lap;
-            }
-          }
+        for (; j < j1; ++j, ++kt) {
+          const uint32_t st = kt & 1, bar = kt & (kChunkBars - 1);
+          const TileTokens tt = tile_tokens<D>(run.u, j);
+          const int a0 = tt.t0 + half * (NT / 2), a1 = a0 + NT / 2;
+          if ((a0 < ce) != cold) break;  // the other tier's format
+          ok = __all_sync(0xffffffffu, bar_wait(empty_at + 8 * st, ((kt >> 1) & 1) ^ 1, gave_up) &&
+                                           bar_wait(full_at + 8 * bar, kt / kChunkBars & 1, gave_up));
+          if (!ok) break;
+          landed = true;
+          // a piece of one format, wholly in view (to whole 32-token subtiles) and in range: the common case
+          const uint32_t bad = *(volatile uint32_t*)&sh.bad_pages[piece * kChunkBars + bar];
+          if (!(a0 + 31 >= tt.v0 && a1 - 31 <= tt.v1 && a1 <= qe && (!cold || a1 <= ce) && !bad)) break;
+          const uint32_t staged = raw_at + slot * a.slot_bytes, dst = st * C::TILE_BYTES;
+          bool done = false;
+          if (kind == 4)
+            done = fill_piece<DT, 4, false>(q, staged, dst);
+          else if (kind == 8)
+            done = fill_piece<DT, 8, false>(q, staged, dst);
+          else if (kind == 2)
+            done = fill_piece<DT, 2, false>(q, staged, dst);
+          else if (kind == 3)
+            done = fill_piece<DT, 3, false>(q, staged, dst);
+          else if (kind == 20)
+            done = fill_piece<DT, 4, true>(q, staged, dst);
+          else if (kind == 18)
+            done = fill_piece<DT, 2, true>(q, staged, dst);
+          if (!done) break;
           proxy_fence();
           __syncwarp();
-          if (ok && lane == 0) bar_arrive(smem_addr(which ? &sh.v_full[st] : &sh.k_full[st]));
-        }
-      }
-    }
-  } else if (warp == C::WARPS - 2) {
-    // ---- staging ------------------------------------------------------------------------
-    const Loader<D> ld{a, lane};
-    uint32_t slot = 0, lap = 0, filled = 0;
-    bool ok = true;
-    for (; more && ok; more = next_run<D, RT>(a, line, run)) {
-      Unit u = run.u;
-      u.layer += a.layer0;
-      const int qe = q_end_of(a.lo, u.T), ce = c_end_of(a.lo, u.T);
-      int pid = ld.page_id(u, tile_tokens<D>(u, run.t0), qe);
-      for (int j = run.t0; j < run.t1 && ok; ++j) {
-        const TileTokens tt = tile_tokens<D>(u, j);
-        // the next tile's page ids load while this one waits for slots
-        const int next_pid = j + 1 < run.t1 ? ld.page_id(u, tile_tokens<D>(u, j + 1), qe) : -1;
-#pragma unroll 1
-        for (int i = 0; i < 4 && ok; ++i) {
-          ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.raw_empty[slot]), (lap & 1) ^ 1, &sh.gave_up));
-          if (!ok) break;
-          ld.piece(u, tt, i >> 1, i & 1, qe, ce, pid, raw_at + slot * a.slot_bytes, smem_addr(&sh.raw_full[slot]),
-                   &sh.bad_pages[slot]);
-          ++filled;
-          if (++slot == (uint32_t)a.slots) {
-            slot = 0;
-            ++lap;
+          if (lane == 0) {
+            bar_arrive(read_at + 8 * bar);
+            bar_arrive(filled_at + 8 * st);
           }
+          slot += 4;
+          while (slot >= slots) slot -= slots;
+          landed = false;
         }
-        pid = next_pid;
-      }
-    }
-    // the copies in flight land before the CTA ends, also when another warp has given up
-    for (uint32_t i = 0; i < (uint32_t)a.slots && i < filled; ++i) {
-      const uint32_t back = filled - 1 - i, s = back % a.slots, n = back / a.slots;
-      for (int k = 0; k < kChunkSpin && !bar_test(smem_addr(&sh.raw_full[s]), n & 1); ++k) {
+        if (!ok || j >= j1) break;
+        if (landed) {
+          cold_piece<D, DT>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j);
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(smem_addr(&sh.raw_empty[piece * kChunkBars + (kt & (kChunkBars - 1))]));
+            bar_arrive(smem_addr(which ? &sh.v_full[kt & 1] : &sh.k_full[kt & 1]));
+          }
+          slot += 4;
+          while (slot >= slots) slot -= slots;
+          ++j;
+          ++kt;
+        }
       }
     }
   } else {
     // ---- softmax and outputs -----------------------------------------------------------
-    const int stream = warp >> 2, quad = warp & 3;
-    const int my_lane = quad * 32 + lane;  // TMEM lane: row of the 128-row tile
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const int lanes_per = 128 / a.rep;
-    const int cols = NT / a.rep, col0 = (my_lane / lanes_per) * cols;  // this row's tokens of a tile
-    const float sc = 1.4426950408889634f * rsqrtf((float)D);
-    uint32_t ns[2] = {0, 0}, runs = 0, steps_done = 0, syncs = 0;
+    uint32_t ns0 = 0, ns1 = 0, runs = 0, steps_done = 0, syncs = 0;
     bool ok = true;
-    for (; more && ok; more = next_run<D, RT>(a, line, run), ++runs) {
-      const Unit& u = run.u;
-      const int tiles = run.t1 - run.t0, steps = PAIRED ? 2 * tiles : tiles;
+    for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1), ++runs) {
+      int w = warp;  // worked out anew for every run: see the dequantizing warps
+      asm volatile("" : "+r"(w));
+      const int stream = w >> 2, quad = w & 3;
+      const int my_lane = quad * 32 + lane;  // TMEM lane: row of the 128-row tile
+      const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+      const uint32_t o_col = lane_base + C::O_COL + (C::STREAMS == 2 ? stream * D : 0);
+      const int lanes_per = 128 / a.rep;
+      const int cols = NT / a.rep, col0 = (my_lane / lanes_per) * cols;  // this row's tokens of a tile
+      const int my_row = (PAIRED ? stream * 128 : 0) + (my_lane & (lanes_per - 1));  // query row of the row tile
+      const float sc = 1.4426950408889634f * rsqrtf((float)D);
       // queries: row r of this stream's tile (each repetition a copy)
       if (PAIRED || stream == 0) {
         const int first = PAIRED ? stream * 128 : 0;
-        const int n = min(a.rep > 1 ? lanes_per : 128, u.rows - first);
+        const int n = min(lanes_per, run.u.rows - first);
         const uint32_t q0 = q_at + (PAIRED ? stream * C::Q_BYTES : 0);
+#pragma unroll 2
         for (int r = quad; r < n; r += 4) {
-          const int row = u.r0 + first + r, tok = row / a.lo.g, head = u.h * a.lo.g + row % a.lo.g;
-          const uint16_t* src = a.q + (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + head) * D;
+          const uint16_t* src = a.q + query_row(a, run.u, first + r);
 #pragma unroll
           for (int c = 0; c < D / 128; ++c) {
             uint2 w = __ldg(reinterpret_cast<const uint2*>(src) + 32 * c + lane);
@@ -1235,6 +1655,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
               w = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
             }
             const int ch = 128 * c + 4 * lane;
+#pragma unroll 1
             for (int k = 0; k < a.rep; ++k) {
               const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r + k * lanes_per, (ch & 63) >> 3) + (ch & 4) * 2;
               asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
@@ -1245,44 +1666,28 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(smem_addr(&sh.q_full[PAIRED ? stream : 0]));
       }
-      const int my_row = (PAIRED ? stream * 128 : 0) + my_lane % lanes_per;  // query row of the row tile
-      const int pos = u.T - u.n + (u.r0 + my_row) / a.lo.g;
-      const int win_lo = a.window ? max(0, pos - a.window + 1) : 0;  // visible: [win_lo, pos] and [0, sinks)
+      RowSeen see;
+      see.pos = run.u.T - run.u.n + div_g(a, run.u.r0 + my_row);
+      see.win_lo = a.window ? max(0, see.pos - a.window + 1) : 0;
+      see.sinks = a.sinks;
+      const int steps = (PAIRED ? 2 : 1) * (run.t1 - run.t0);
       float m = -INFINITY, l = 0.f;
-      int first_step = 1;
-      for (int s = C::STREAMS == 2 ? stream : 0; s < steps && ok; s += C::STREAMS) {
+      bool first_step = true;
+#pragma unroll 1
+      for (int s = C::STREAMS == 2 ? stream : 0; s < steps; s += C::STREAMS) {
         const int b = s & 1;
-        ok = bar_wait(smem_addr(&sh.s_full[b]), ns[b] & 1, &sh.gave_up);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ++ns[b];
-        tc_fence_after();
         const int j = run.t0 + (PAIRED ? s >> 1 : s);
-        const int t0 = (j < u.st ? j : u.lo_tile + (j - u.st)) * NT;
-        const bool masked = t0 + NT - 1 > u.p_lo || (a.window && t0 <= u.p_hi - a.window && t0 + NT > a.sinks);
+        const int t0 = (j < run.u.st ? j : run.u.lo_tile + (j - run.u.st)) * NT;
+        const bool masked = t0 + NT - 1 > run.u.p_lo || (a.window && t0 <= run.u.p_hi - a.window && t0 + NT > a.sinks);
         const uint32_t s_col = lane_base + C::S_COL + b * NT;
+        ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
+        if (!ok) break;
+        ns0 += b ^ 1;
+        ns1 += b;
+        tc_fence_after();
         uint32_t x[32];
-        auto mask32 = [&](int c) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int t = t0 + c + i;
-            if (t > pos || (t < win_lo && t >= a.sinks)) x[i] = 0xff800000u;
-          }
-        };
-        float mt = -INFINITY;
-        for (int c = col0; c < col0 + cols; c += 32) {
-          tmem_ld32(s_col + c, x);
-          tmem_wait_ld();
-          if (masked) mask32(c);
-          float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            m0 = fmaxf(m0, __uint_as_float(x[i]));
-            m1 = fmaxf(m1, __uint_as_float(x[i + 1]));
-          }
-          mt = fmaxf(mt, fmaxf(m0, m1));
-        }
-        mt *= sc;
+        const float mt = sc * (masked ? tile_max<true>(s_col, col0, col0 + cols, t0, see, x)
+                                      : tile_max<false>(s_col, col0, col0 + cols, t0, see, x));
         // the reference maximum follows only when it falls behind by 2^8: P
         // stays below 2^8 and the accumulator is rescaled rarely
         const bool grow = mt > m + 8.f;
@@ -1290,50 +1695,26 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
           const float nm = grow ? mt : m;
           const float f = m == -INFINITY ? 0.f : ex2(m - nm);
           l = l == 0.f ? 0.f : l * f;
+          m = nm;
           if (!first_step) {
             if (C::STREAMS == 1) {
               // the products of the step before must have left the accumulator
-              ok = bar_wait(smem_addr(&sh.pv_done), (steps_done - 1) & 1, &sh.gave_up);
-              ok = __all_sync(0xffffffffu, ok);
+              ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.pv_done), (steps_done - 1) & 1, gave_up));
               if (!ok) break;
               tc_fence_after();
             }
-            const uint32_t o_col = lane_base + C::O_COL + (C::STREAMS == 2 ? stream * D : 0);
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              tmem_ld32(o_col + c, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-              tmem_st32(o_col + c, x);
-            }
-            tmem_wait_st();
+            rescale_columns<D>(o_col, f);
           }
-          m = nm;
         }
-        first_step = 0;
+        first_step = false;
         const float mneg = m == -INFINITY ? 0.f : -m;
-        float l0 = 0.f, l1 = 0.f;
-        for (int c = col0; c < col0 + cols; c += 32) {
-          tmem_ld32(s_col + c, x);
-          tmem_wait_ld();
-          if (masked) mask32(c);
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float e0 = ex2(fmaf(__uint_as_float(x[2 * i]), sc, mneg));
-            const float e1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), sc, mneg));
-            l0 += e0;
-            l1 += e1;
-            p[i] = pack16<DT>(e0, e1);
-          }
-          tmem_st16(s_col + c / 2, p);
-        }
-        l += l0 + l1;
+        l += masked ? tile_exp<DT, true>(s_col, col0, col0 + cols, t0, see, sc, mneg, x)
+                    : tile_exp<DT, false>(s_col, col0, col0 + cols, t0, see, sc, mneg, x);
         if (a.rep > 1) {  // the other repetitions' tokens count nothing in this row
           uint32_t z[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = 0;
+#pragma unroll 1
           for (int c = 0; c < NT; c += 32)
             if (c < col0 || c >= col0 + cols) tmem_st16(s_col + c / 2, z);
         }
@@ -1345,68 +1726,45 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
       }
       // ---- the run's outputs -----------------------------------------------------------
       if (!ok) break;
-      ok = bar_wait(smem_addr(&sh.o_full), runs & 1, &sh.gave_up);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.o_full), runs & 1, gave_up));
       if (!ok) break;
       tc_fence_after();
-      const bool cut = run.t0 > 0 || run.t1 < u.nt;
-      const uint32_t o_col = lane_base + C::O_COL + (C::STREAMS == 2 ? stream * D : 0);
-      Unit in_cache = u;
-      in_cache.layer += a.layer0;
+      const bool cut = run.t0 > 0 || run.t1 < run.u.nt, mine = my_row < run.u.rows;
       const bool direct = !cut && (PAIRED || (C::STREAMS == 1 && a.rep == 1));
+      uint32_t x[32];
       if (direct) {
-        const bool mine = my_row < u.rows;
-        const float inv = 1.f / l;
-        if (a.lo.flags & KVQ_ROTATE_V) {
+        const bool rotated = (a.lo.flags & KVQ_ROTATE_V) != 0, fix = *(volatile uint32_t*)&sh.nonfinite != 0;
+        const float inv = 1.f / l, f = rotated ? 1.f : inv;
+        if (rotated) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 128) unrotate_columns(o_col + c, a.lo.d1, a.lo.d2, inv);
+          for (int c = 0; c < D; c += 128) unrotate_columns(a, o_col + c, inv);
         }
-        const int row = u.r0 + my_row, tok = row / a.lo.g, head = u.h * a.lo.g + row % a.lo.g;
-        uint16_t* dst = a.out + (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + head) * D;
-        const float f = a.lo.flags & KVQ_ROTATE_V ? 1.f : inv;
-        const bool fix = *(volatile uint32_t*)&sh.nonfinite != 0;
+        uint16_t* dst = a.out + query_row(a, run.u, mine ? my_row : 0);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-          uint32_t x[32];
           tmem_ld32(o_col + c, x);
           tmem_wait_ld();
           if (mine) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[i + e]) * f;
-            if (fix) {
-              float v0[4] = {v[0], v[1], v[2], v[3]}, v1[4] = {v[4], v[5], v[6], v[7]};
-              add_nonfinite<DT>(a, in_cache, pos, c + i, v0);
-              add_nonfinite<DT>(a, in_cache, pos, c + i + 4, v1);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                v[e] = v0[e];
-                v[4 + e] = v1[e];
-              }
+            for (int i = 0; i < 32; i += 4) {
+              *reinterpret_cast<uint2*>(dst + c + i) =
+                  make_uint2(pack16<DT>(__uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f),
+                             pack16<DT>(__uint_as_float(x[i + 2]) * f, __uint_as_float(x[i + 3]) * f));
             }
-            *reinterpret_cast<uint4*>(dst + c + i) =
-                make_uint4(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]), pack16<DT>(v[4], v[5]), pack16<DT>(v[6], v[7]));
-          }
           }
           __syncwarp();
         }
+        if (fix && mine) add_nonfinite<DT>(a, run, see.pos, 0, D, dst);
+        __syncwarp();
         tc_fence_before();
       } else {
-        const int64_t unit_pos = run.pos - run.t0;
-        // a unit's ticket belongs to its first CTA: entry 0 when the unit
-        // starts with that CTA's stretch, else 1
-        const int c0 = (int)(unit_pos / line.per_cta);
         const int slot = !cut ? 2 : run.first ? 0 : 1;
         float* part = a.partials + (((int64_t)blockIdx.x * kChunkSlots + slot) * chunk_slot_rows(D) + stream * 128 + my_lane) *
                                        chunk_part_row(D);
-        const bool mine = my_row < u.rows;
         // a stream without a step of this run has no accumulator
         const bool none = C::STREAMS == 2 && stream >= steps;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-          uint32_t x[32];
           tmem_ld32(o_col + c, x);
           tmem_wait_ld();
           if (mine) {
@@ -1419,33 +1777,36 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         }
         if (mine) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
         tc_fence_before();
-        const int64_t tick = (int64_t)c0 * kChunkTickets + (unit_pos == (int64_t)c0 * line.per_cta ? 0 : 1);
         const uint32_t soft = smem_addr(&sh.soft);
+        bool join = !cut, fix = false;
+        // a unit's ticket belongs to its first CTA: entry 0 when the unit
+        // starts with that CTA's stretch, else 1
+        const int unit_pos = run.pos - run.t0, c0 = unit_pos / sh.start.per_cta;
+        const int tick = c0 * kChunkTickets + (unit_pos == c0 * sh.start.per_cta ? 0 : 1);
+        if (cut) __threadfence();
+        if (!(ok = soft_sync(soft, syncs, gave_up))) break;
         if (cut) {
-          __threadfence();
-          if (!(ok = soft_sync(soft, syncs, &sh.gave_up))) break;
           if (tid == 0) {
             if (*(volatile uint32_t*)&sh.nonfinite) atomicOr(a.nonfinite + tick, 1u);
             __threadfence();
-            const int c1 = (int)((unit_pos + u.nt - 1) / line.per_cta);
+            const int c1 = (unit_pos + run.u.nt - 1) / sh.start.per_cta;
             sh.last = atomicAdd(a.tickets + tick, 1u) == (uint32_t)(c1 - c0);
           }
-          if (!(ok = soft_sync(soft, syncs, &sh.gave_up))) break;
-          if (*(volatile uint32_t*)&sh.last) {
+          if (!(ok = soft_sync(soft, syncs, gave_up))) break;
+          join = *(volatile uint32_t*)&sh.last != 0;
+          if (join) {
             __threadfence();
-            const bool fix = __ldcg(a.nonfinite + tick) != 0;
-            join_unit<D, DT, PAIRED>(a, in_cache, line, unit_pos, true, fix, tid);
-            if (!(ok = soft_sync(soft, syncs, &sh.gave_up))) break;
-            if (tid == 0) {
-              a.tickets[tick] = 0;
-              a.nonfinite[tick] = 0;
-            }
+            fix = __ldcg(a.nonfinite + tick) != 0;
           }
         } else {
-          if (!(ok = soft_sync(soft, syncs, &sh.gave_up))) break;
-          join_unit<D, DT, PAIRED>(a, in_cache, line, unit_pos, false, *(volatile uint32_t*)&sh.nonfinite != 0, tid);
+          fix = *(volatile uint32_t*)&sh.nonfinite != 0;
         }
-        if (!(ok = soft_sync(soft, syncs, &sh.gave_up))) break;
+        if (join) join_unit<D, DT, PAIRED>(a, run, sh.start, cut, fix);
+        if (!(ok = soft_sync(soft, syncs, gave_up))) break;
+        if (join && cut && tid == 0) {
+          a.tickets[tick] = 0;
+          a.nonfinite[tick] = 0;
+        }
       }
     }
   }
@@ -1453,7 +1814,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && sh.gave_up) atomicOr(a.status, KVQ_DEV_STALL);
-  if (warp == C::WARPS - 1) {
+  if (warp == C::MMA_WARP) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
   }
