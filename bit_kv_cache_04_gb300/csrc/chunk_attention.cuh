@@ -12,7 +12,7 @@
 // One CTA per SM, specialized warps, joined by mbarriers:
 //   softmax warps   one TMEM lane (query row) per thread: row maximum, exponentials, P back to
 //                   TMEM in the input dtype, the accumulator's rescaling, outputs
-//   loader warp     packed bytes of half tiles ("pieces") into a ring of slots, bulk copies
+//   loader warps    packed bytes of half tiles ("pieces") into a ring of slots, bulk copies
 //   dequant warps   packed blocks -> K and V tiles in shared memory (2 stages each)
 //   product warp    one thread issues every tcgen05.mma
 // D = 128: tiles of 128 tokens and two streams of softmax warps, each with

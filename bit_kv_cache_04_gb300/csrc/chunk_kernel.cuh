@@ -43,6 +43,12 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
+// x of lane 0: equal in all lanes by construction, so that what follows from
+// it stays in uniform registers (operands of products and copies, loop counters, addresses).
+template <class T>
+__device__ __forceinline__ T uniform(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
 // One lane of a converged warp.  The instructions below and the bulk copies take their
 // operands from uniform registers: issued by `lane == 0`, or by several lanes with
 // operands of their own, each becomes a loop over the lanes (270 cycles a product).
@@ -95,15 +101,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(addr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -133,6 +137,23 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, u
 
 // Byte offset of 16-byte piece c (of 8) of row r in a swizzled tile of 128-byte rows.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// Sign bits of a lane's four channels (4 lane ..) of a 128-chunk: fetched once per loop, since a
+// lane's own word of the parameters is a serialized load.
+__device__ __forceinline__ uint32_t lane_signs(const uint32_t* d, int lane) {
+  const uint32_t lo = lane & 16 ? d[2] : d[0], hi = lane & 16 ? d[3] : d[1];
+  return (lane & 8 ? hi : lo) >> (4 * (lane & 7));
+}
+// The transform of a 128-chunk held four channels a lane, between the signs s1 and s2 of lane_signs: forward with
+// (d1, d2), inverse with (d2, d1).
+__device__ __forceinline__ void rotate_lanes(float (&v)[4], uint32_t s1, uint32_t s2) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(__float_as_uint(v[e]) ^ ((s1 << (31 - e)) & 0x80000000u));
+  warp_fwht128(v);
+  const float c = hadamard_scale();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(__float_as_uint(v[e] * c) ^ ((s2 << (31 - e)) & 0x80000000u));
+}
 
 // ---- the units' line ---------------------------------------------------------------
 
@@ -212,7 +233,7 @@ __device__ __forceinline__ int seq_tiles(const ChunkArgs& a, int b, int lane, in
 
 // The CTA's first run (step 0) or the one after r; false past the last.  One lane of a warp.
 template <int D, int RT>
-__device__ __noinline__ bool step_run(const ChunkArgs& a, const LineStart& s, Run& r, int step) {
+__device__ __forceinline__ bool step_run(const ChunkArgs& a, const LineStart& s, Run& r, int step) {
   Unit u = r.u;
   int pos, t0;
   if (step == 0) {
@@ -257,6 +278,7 @@ __device__ __forceinline__ bool warp_run(const ChunkArgs& a, const LineStart& s,
   bool more = false;
   __syncwarp();
   if ((threadIdx.x & 31) == 0) more = step_run<D, RT>(a, s, r, step);
+  __syncwarp();  // the run is read by every lane
   return __shfl_sync(0xffffffffu, (int)more, 0) != 0;
 }
 
@@ -550,7 +572,7 @@ __device__ __forceinline__ void rotated_window(const ChunkArgs& a, const CachePo
       const uint32_t w0 = clean<DT>(w.x, which, nonfinite), w1 = clean<DT>(w.y, which, nonfinite);
       float v[4] = {in_to_f32((uint16_t)w0, DT), in_to_f32((uint16_t)(w0 >> 16), DT), in_to_f32((uint16_t)w1, DT),
                     in_to_f32((uint16_t)(w1 >> 16), DT)};
-      warp_rotate128(v, a.lo.d1, a.lo.d2);
+      rotate_lanes(v, lane_signs(a.lo.d1, lane), lane_signs(a.lo.d2, lane));
       const int ch = 128 * c + 4 * lane;
       const uint32_t at = dst + (uint32_t)(ch >> 6) * NT * 128 + swz(t - tile0, (ch & 63) >> 3) + (ch & 4) * 2;
       asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(pack16<DT>(keep_range<DT>(v[0]), keep_range<DT>(v[1]))),
@@ -816,12 +838,11 @@ __device__ __forceinline__ void turned_piece(const ChunkArgs& a, const CachePos&
 
 // ---- staging -----------------------------------------------------------------------------
 
-// The loader warp brings the packed bytes of every piece into a ring of
-// shared-memory slots: bulk copies of 32-token subtiles (of pages, when those
-// are smaller).  A tile's four pieces (K, V, two halves each) are worked out
-// side by side, eight lanes a piece: one lane's addresses are a long chain of
-// dependent instructions, and four in turn kept the products waiting.
-// Piece i of tile kt is number 4 kt + i and goes to slot number mod slots; its
+// Two loader warps, one for K and one for V, bring the packed bytes of their
+// pieces into a common ring of shared-memory slots: bulk copies of 32-token subtiles (of pages,
+// when those are smaller).  A tile's two pieces are worked out side by side, 16 lanes
+// a piece: one lane's addresses are a long chain of dependent instructions.
+// Piece i (K, K, V, V) of tile kt is number 4 kt + i and goes to slot number mod slots; its
 // barriers are the piece kind's, kt mod kChunkBars: each warp sees every
 // phase of the barriers that it waits on, and the ring never spans kChunkBars tiles.
 template <int D>
@@ -835,10 +856,10 @@ struct Loader {
   int ring;                  // hot ring in rows (tiers), else 0
   bool per_channel;
 
-  __device__ __forceinline__ void lanes(const ChunkArgs& a, int lane) {
-    which = lane >> 4;
-    half = (lane >> 3) & 1;
-    ln = lane & 7;
+  __device__ __forceinline__ void lanes(const ChunkArgs& a, int tensor, int lane) {
+    which = tensor;
+    half = lane >> 4;
+    ln = lane & 15;
     per_channel = (which ? a.lo.vf.axis : a.lo.kf.axis) == KVQ_AXIS_CHANNEL;
     row_main = which ? a.lo.vf.row : a.lo.kf.row;
     row_cold = which ? a.lo.vc.row : a.lo.kc.row;
@@ -914,7 +935,7 @@ struct ChunkShape {
   static constexpr int QTILES = PAIRED ? 2 : 1;
   static constexpr int RT = 128 * QTILES;  // rows of a row tile
   static constexpr int SOFT_WARPS = 4 * STREAMS;
-  static constexpr int LOAD_WARP = SOFT_WARPS + kChunkDequantWarps, MMA_WARP = LOAD_WARP + 1;
+  static constexpr int LOAD_WARP = SOFT_WARPS + kChunkDequantWarps, MMA_WARP = LOAD_WARP + 2;  // two loaders: K, V
   static constexpr int WARPS = MMA_WARP + 1;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr uint32_t Q_BYTES = 128u * D * 2;
@@ -932,7 +953,7 @@ struct ChunkShared {
   uint32_t nonfinite;
   uint32_t last;  // this CTA joins the unit's partials
   LineStart start;
-  Run runs[18];   // one per warp
+  Run runs[19];   // one per warp
   int scan[32];
   uint32_t pair_table[256];  // TBQ4: centroids of a byte's two indices
 };
@@ -1130,99 +1151,126 @@ __device__ __noinline__ void join_unit(const ChunkArgs& a, const Run& run, const
     const int s = k / a.rep, row = PAIRED ? r : s * 128 + (k - s * a.rep) * lanes_per + r;
     return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
+  const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
+  // many rows: four of a warp at a time, for one by itself is a chain of loads from L2
+  constexpr int RW = PAIRED ? 4 : 1;
 #pragma unroll 1
-  for (int r = warp; r < u.rows; r += C::SOFT_WARPS) {
-    float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(part(i, r) + D));
+  for (int r0 = warp * RW; r0 < u.rows; r0 += RW * C::SOFT_WARPS) {
+    float M[RW], L[RW], acc[RW][N][4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, acc[N][4];
+    for (int q = 0; q < RW; ++q) {
+      M[q] = -INFINITY;
+      L[q] = 0.f;
 #pragma unroll
-    for (int c = 0; c < N; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+      for (int c = 0; c < N; ++c) acc[q][c][0] = acc[q][c][1] = acc[q][c][2] = acc[q][c][3] = 0.f;
+    }
+#pragma unroll 1
+    for (int i = lane; i < parts; i += 32) {
+      const float* p = part(i, r0) + D;
+#pragma unroll
+      for (int q = 0; q < RW; ++q) M[q] = fmaxf(M[q], __ldcg(p + q * PR));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int q = 0; q < RW; ++q) M[q] = fmaxf(M[q], __shfl_xor_sync(0xffffffffu, M[q], o));
 #pragma unroll 1
     for (int i0 = 0; i0 < parts; i0 += 32) {
-      float w = 0.f;
-      const float* p = part(min(i0 + lane, parts - 1), r);
-      if (i0 + lane < parts) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
+      const float* p = part(min(i0 + lane, parts - 1), r0);
+      float w[RW];
+#pragma unroll
+      for (int q = 0; q < RW; ++q) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + q * PR + D));
         // a part that saw none of the row's tokens has m = -inf and l = 0
-        w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2(ml.x - M);
-        L += w == 0.f && ml.y == 0.f ? 0.f : w * ml.y;
+        const bool none = i0 + lane >= parts || (ml.x == -INFINITY && ml.y == 0.f);
+        w[q] = none ? 0.f : ex2(ml.x - M[q]);
+        L[q] += none ? 0.f : w[q] * ml.y;
       }
       const uint32_t off = (uint32_t)((p - a.partials) >> 2);  // in 16-byte words
       const int k1 = min(32, parts - i0);
-#pragma unroll 4
+#pragma unroll 2
       for (int k = 0; k < k1; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float4* o4 = reinterpret_cast<const float4*>(a.partials) + __shfl_sync(0xffffffffu, off, k);
-        if (wk == 0.f) continue;
+        const float4* o4 = reinterpret_cast<const float4*>(a.partials) + __shfl_sync(0xffffffffu, off, k) + lane;
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-          const float4 v = __ldcg(o4 + 32 * c + lane);
-          acc[c][0] = fmaf(wk, v.x, acc[c][0]);
-          acc[c][1] = fmaf(wk, v.y, acc[c][1]);
-          acc[c][2] = fmaf(wk, v.z, acc[c][2]);
-          acc[c][3] = fmaf(wk, v.w, acc[c][3]);
+        for (int q = 0; q < RW; ++q) {
+          const float wk = __shfl_sync(0xffffffffu, w[q], k);
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            const float4 v = __ldcg(o4 + q * (PR / 4) + 32 * c);
+            if (wk != 0.f) {  // rows that the part has not are not written either
+              acc[q][c][0] = fmaf(wk, v.x, acc[q][c][0]);
+              acc[q][c][1] = fmaf(wk, v.y, acc[q][c][1]);
+              acc[q][c][2] = fmaf(wk, v.z, acc[q][c][2]);
+              acc[q][c][3] = fmaf(wk, v.w, acc[q][c][3]);
+            }
+          }
         }
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    uint16_t* dst = a.out + query_row(a, u, r);
-    const float inv = 1.f / L;
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      float v[4] = {acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv};
-      if (a.lo.flags & KVQ_ROTATE_V) warp_unrotate128(v, a.lo.d1, a.lo.d2);
-      *reinterpret_cast<uint2*>(dst + 128 * c + 4 * lane) = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
-      if (fix) add_nonfinite<DT>(a, run, u.T - u.n + div_g(a, u.r0 + r), 128 * c + 4 * lane, 4, dst);
+      for (int q = 0; q < RW; ++q) L[q] += __shfl_xor_sync(0xffffffffu, L[q], o);
+#pragma unroll
+    for (int q = 0; q < RW; ++q) {
+      if (r0 + q >= u.rows) break;
+      uint16_t* dst = a.out + query_row(a, u, r0 + q);
+      const float inv = 1.f / L[q];
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        float v[4] = {acc[q][c][0] * inv, acc[q][c][1] * inv, acc[q][c][2] * inv, acc[q][c][3] * inv};
+        if (a.lo.flags & KVQ_ROTATE_V) rotate_lanes(v, s2, s1);
+        *reinterpret_cast<uint2*>(dst + 128 * c + 4 * lane) = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+        if (fix) add_nonfinite<DT>(a, run, u.T - u.n + div_g(a, u.r0 + r0 + q), 128 * c + 4 * lane, 4, dst);
+      }
     }
   }
 }
 
-// In-thread inverse of the 128-point transform on TMEM columns [col, col +
-// 128) of this lane, in place and times `factor`: four 32-point transforms,
-// then the two stages between them, eight columns of each at a time.
-__device__ __noinline__ void unrotate_columns(const ChunkArgs& a, uint32_t col, float factor) {
-  uint32_t r[32];
+// The butterflies of the 128-point transform on TMEM columns [col, col + 128)
+// of this lane, in place, after the signs of d2 and `factor`: strides below 16 within 16
+// columns, the others between two sets of 16.  Short loops: this runs once per row tile, and code
+// that runs once costs its fetch.
+__device__ __forceinline__ void unrotate_columns(const ChunkArgs& a, uint32_t col, float factor) {
   const float f = factor * hadamard_scale();
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    tmem_ld32(col + 32 * c, r);
+  for (int c = 0; c < 128; c += 16) {
+    uint32_t r[16];
+    tmem_ld16(col + c, r);
+    const uint32_t signs = a.lo.d2[c >> 5] >> (c & 16);
     tmem_wait_ld();
-    const uint32_t signs = a.lo.d2[c];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i] ^ (((signs >> i) & 1u) << 31)) * f);
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f) ^ ((signs << (31 - i)) & 0x80000000u);
 #pragma unroll
-    for (int h = 1; h < 32; h <<= 1)
+    for (int h = 1; h < 16; h <<= 1)
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < 16; ++i)
         if (!(i & h)) {
           const float u = __uint_as_float(r[i]), v = __uint_as_float(r[i + h]);
           r[i] = __float_as_uint(u + v);
           r[i + h] = __float_as_uint(u - v);
         }
-    tmem_st32(col + 32 * c, r);
+    tmem_st16(col + c, r);
   }
-  tmem_wait_st();
 #pragma unroll 1
-  for (int k = 0; k < 32; k += 8) {
-    uint32_t q[4][8];
+  for (int h = 16; h < 128; h <<= 1) {
+    tmem_wait_st();
+#pragma unroll 1
+    for (int k = 0; k < 64; k += 16) {
+      const int c = (k & ~(h - 1)) * 2 + (k & (h - 1));  // the k-th column set whose bit h is clear
+      uint32_t p[16], q[16];
+      tmem_ld16(col + c, p);
+      tmem_ld16(col + c + h, q);
+      tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld8(col + 32 * c + k, q[c]);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x0 = __uint_as_float(q[0][i]), x1 = __uint_as_float(q[1][i]), x2 = __uint_as_float(q[2][i]),
-                  x3 = __uint_as_float(q[3][i]);
-      const float s0 = x0 + x1, d0 = x0 - x1, s1 = x2 + x3, d1 = x2 - x3;
-      q[0][i] = __float_as_uint(s0 + s1) ^ (((a.lo.d1[0] >> (k + i)) & 1u) << 31);
-      q[1][i] = __float_as_uint(d0 + d1) ^ (((a.lo.d1[1] >> (k + i)) & 1u) << 31);
-      q[2][i] = __float_as_uint(s0 - s1) ^ (((a.lo.d1[2] >> (k + i)) & 1u) << 31);
-      q[3][i] = __float_as_uint(d0 - d1) ^ (((a.lo.d1[3] >> (k + i)) & 1u) << 31);
+      for (int i = 0; i < 16; ++i) {
+        const float u = __uint_as_float(p[i]), v = __uint_as_float(q[i]);
+        p[i] = __float_as_uint(u + v);
+        q[i] = __float_as_uint(u - v);
+      }
+      tmem_st16(col + c, p);
+      tmem_st16(col + c + h, q);
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_st8(col + 32 * c + k, q[c]);
   }
   tmem_wait_st();
 }
@@ -1312,7 +1360,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   constexpr int NT = C::NT, RT = C::RT;
   extern __shared__ uint8_t raw_smem[];
   __shared__ ChunkShared sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_at = smem_addr(smem), k_at = q_at + C::QTILES * C::Q_BYTES, v_at = k_at + 2 * C::TILE_BYTES;
   const uint32_t raw_at = v_at + 2 * C::TILE_BYTES;
@@ -1363,7 +1411,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = uniform(sh.tmem);
   Run& run = sh.runs[warp];
   uint32_t* const gave_up = &sh.gave_up;
   const bool k_chan = a.lo.kf.axis == KVQ_AXIS_CHANNEL, v_chan = a.lo.vf.axis == KVQ_AXIS_CHANNEL;
@@ -1382,7 +1430,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
     uint32_t runs = 0;
     bool ok = true;
     for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1), ++runs) {
-      const int tiles = run.t1 - run.t0, steps = PAIRED ? 2 * tiles : tiles;
+      const int tiles = uniform(run.t1 - run.t0), steps = PAIRED ? 2 * tiles : tiles;
       {
 #pragma unroll 1
         for (int i = 0; i < 2 * steps + 2 && ok; ++i) {
@@ -1444,16 +1492,18 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
       }
       kt += tiles;
     }
-  } else if (warp == C::LOAD_WARP && a.direct) {
-    load_direct<D, RT>(a, sh, run, more, raw_at, lane);
-  } else if (warp == C::LOAD_WARP) {
+  } else if (warp >= C::LOAD_WARP && a.direct) {
+    if (warp == C::LOAD_WARP) load_direct<D, RT>(a, sh, run, more, raw_at, lane);
+  } else if (warp >= C::LOAD_WARP) {
     // ---- staging ------------------------------------------------------------------------
+    int w = warp;
+    asm volatile("" : "+r"(w));
     Loader<D> ld;
-    ld.lanes(a, lane);
-    const int piece = lane >> 3;
-    const bool two = (NT / 2) >> a.copy_shift > 8;
+    ld.lanes(a, w - C::LOAD_WARP, lane);
+    const int piece = 2 * ld.which + ld.half;
     const uint32_t slots = a.slots;
-    uint32_t kt = 0, slot0 = 0, todo = 0xf;  // tiles so far; slot of the tile's first piece; pieces to ask for
+    uint32_t kt = 0, slot = piece, todo = 3;  // tiles so far; this lane's piece's slot; pieces to ask for
+    while (slot >= slots) slot -= slots;
     bool ok = true;
     for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1)) {
       const CachePos u{run.u.layer + a.layer0, run.u.b, run.u.h, run.u.T, q_end_of(a.lo, run.u.T), c_end_of(a.lo, run.u.T)};
@@ -1466,66 +1516,52 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         // the next tile's page ids load while this one waits for slots
         const TileTokens next = tile_tokens<D>(run.u, min(j + 1, t1 - 1));
         const int next_pid = ld.page_id(a, u, next.t0, ld.ln);
-        const uint8_t *src0 = nullptr, *src1 = nullptr;
-        int at0 = 0, at1 = 0, bytes0 = 0, bytes1 = 0;
-        uint32_t bads = 0;
-        {
-          bool bad = false;
-          bytes0 = ld.source(a, u, tt, ld.ln, pid, &src0, &at0, &bad);
-          bads = __ballot_sync(0xffffffffu, bad) >> (8 * piece) & 0xffu;
-          if (two) {  // pages of 4 tokens: two copies a lane
-            bad = false;
-            bytes1 = ld.source(a, u, tt, ld.ln + 8, ld.page_id(a, u, tt.t0, ld.ln + 8), &src1, &at1, &bad);
-            bads |= (__ballot_sync(0xffffffffu, bad) >> (8 * piece) & 0xffu) << 8;
-          }
-        }
-        int total = bytes0 + bytes1;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const uint8_t* src = nullptr;
+        int at = 0;
+        bool bad = false;
+        const int bytes = ld.source(a, u, tt, ld.ln, pid, &src, &at, &bad);
+        const uint32_t bads = __ballot_sync(0xffffffffu, bad) >> (16 * ld.half) & 0xffffu;
+        const uint32_t total0 = __reduce_add_sync(0xffffffffu, ld.half ? 0u : (uint32_t)bytes),
+                       total1 = __reduce_add_sync(0xffffffffu, ld.half ? (uint32_t)bytes : 0u);
         const uint32_t number = 4 * kt + piece, bar = piece * kChunkBars + (kt & (kChunkBars - 1));
-        const uint32_t full = smem_addr(&sh.raw_full[bar]);
-        uint32_t slot = slot0 + piece;
-        while (slot >= slots) slot -= slots;
-        const uint32_t dst = raw_at + slot * a.slot_bytes;
+        const uint32_t full = smem_addr(&sh.raw_full[bar]), dst = raw_at + slot * a.slot_bytes + at;
         // the slot's last piece must have been read
-        const uint32_t last = number - slots, last_bar = (last & 3) * kChunkBars + ((last >> 2) & (kChunkBars - 1));
-        todo = 0xf;
+        const uint32_t last = number - slots;
+        const uint32_t empty = smem_addr(&sh.raw_empty[(last & 3) * kChunkBars + ((last >> 2) & (kChunkBars - 1))]);
+        todo = 3;
 #pragma unroll 1
-        for (int spin = 0; todo && ok; ++spin) {
-          bool ready = false;
-          if (ld.ln == 0 && (todo >> piece & 1))
-            ready = number < slots || bar_test(smem_addr(&sh.raw_empty[last_bar]), (last >> 2) / kChunkBars & 1);
-          const uint32_t b = __ballot_sync(0xffffffffu, ready);
-          const uint32_t now = (b & 1) | (b >> 7 & 2) | (b >> 14 & 4) | (b >> 21 & 8);
-          const bool go = now >> piece & 1;
-          if (go && ld.ln == 0) {
+        for (int spin = 0; todo; ++spin) {
+          const bool ready = ld.ln == 0 && (todo >> ld.half & 1) &&
+                             (number < slots || bar_test(empty, (last >> 2) / kChunkBars & 1));
+          const uint32_t b = __ballot_sync(0xffffffffu, ready), now = (b & 1) | (b >> 15 & 2);
+          if (ready) {
             sh.bad_pages[bar] = bads;
             if (bads) atomicOr(a.status, KVQ_DEV_PAGE);
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full), "r"(total) : "memory");
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full), "r"(ld.half ? total1 : total0)
+                         : "memory");
           }
           __syncwarp();
-          copy_each(go && bytes0, dst + at0, src0, bytes0, full);
-          if (two) copy_each(go && bytes1, dst + at1, src1, bytes1, full);
+          copy_each((now >> ld.half & 1) && bytes, dst, src, bytes, full);
           todo &= ~now;
-          if (!now && (spin > kChunkSpin || *(volatile uint32_t*)gave_up)) {
+          if (!now && (spin > kChunkSpin || __any_sync(0xffffffffu, *(volatile uint32_t*)gave_up != 0))) {
             if (lane == 0) *(volatile uint32_t*)gave_up = 1;
             ok = false;
+            break;
           }
-          ok = __all_sync(0xffffffffu, ok);
         }
         if (!ok) break;
         pid = next_pid;
         tt = next;
-        slot0 += 4;
-        while (slot0 >= slots) slot0 -= slots;
+        slot += 4;
+        while (slot >= slots) slot -= slots;
       }
     }
     // the copies in flight land before the CTA ends, also when a warp has
     // given up (then `todo` are the last tile's pieces that were not asked for)
-    if (lane < 4) {
+    if (ld.ln == 0) {
 #pragma unroll 1
-      for (uint32_t back = ok || (todo >> lane & 1) ? 1 : 0; back <= 4 && back <= kt; ++back) {
-        const uint32_t t = kt - back, bar = smem_addr(&sh.raw_full[lane * kChunkBars + (t & (kChunkBars - 1))]);
+      for (uint32_t back = ok || (todo >> ld.half & 1) ? 1 : 0; back <= 4 && back <= kt; ++back) {
+        const uint32_t t = kt - back, bar = smem_addr(&sh.raw_full[piece * kChunkBars + (t & (kChunkBars - 1))]);
         for (int k = 0; k < kChunkSpin && !bar_test(bar, t / kChunkBars & 1); ++k) {
         }
       }
@@ -1535,6 +1571,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
     // ---- dequantization ---------------------------------------------------------------
     // Two warps for each piece (half tile of K or V).
     uint32_t kt = 0, slot = (warp - C::SOFT_WARPS) >> 1, slots = a.slots;
+    asm volatile("" : "+r"(kt), "+r"(slot));  // not uniform registers: they live across a call
     while (slot >= slots) slot -= slots;
     bool ok = true;
     for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1)) {
@@ -1550,7 +1587,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         const uint32_t empty_at = smem_addr(which ? &sh.v_empty[0] : &sh.k_empty[0]),
                        filled_at = smem_addr(which ? &sh.v_full[0] : &sh.k_full[0]);
         const uint32_t full_at = smem_addr(&sh.raw_full[piece * kChunkBars]), read_at = smem_addr(&sh.raw_empty[piece * kChunkBars]);
-        const int qe = q_end_of(a.lo, run.u.T), ce = c_end_of(a.lo, run.u.T);
+        const int T = run.u.T, qe = q_end_of(a.lo, T), ce = c_end_of(a.lo, T);
         const bool cold = j < j1 && tile_tokens<D>(run.u, j).t0 + half * (NT / 2) < ce;
         const RunFmt f = run_fmt(a.lo, which, cold);
         // the hot path's format: bits, 16 for asymmetric blocks; 0: none
@@ -1625,6 +1662,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   } else {
     // ---- softmax and outputs -----------------------------------------------------------
     uint32_t ns0 = 0, ns1 = 0, runs = 0, steps_done = 0, syncs = 0;
+    asm volatile("" : "+r"(ns0), "+r"(ns1), "+r"(runs), "+r"(steps_done), "+r"(syncs));  // as above
     bool ok = true;
     for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1), ++runs) {
       int w = warp;  // worked out anew for every run: see the dequantizing warps
@@ -1637,29 +1675,40 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
       const int cols = NT / a.rep, col0 = (my_lane / lanes_per) * cols;  // this row's tokens of a tile
       const int my_row = (PAIRED ? stream * 128 : 0) + (my_lane & (lanes_per - 1));  // query row of the row tile
       const float sc = 1.4426950408889634f * rsqrtf((float)D);
-      // queries: row r of this stream's tile (each repetition a copy)
+      // queries: rows quad, quad + 4, ... of this stream's tile (each repetition a copy), 128 channels a
+      // turn, the next turns' loads in flight
       if (PAIRED || stream == 0) {
+        constexpr int NC = D / 128, AHEAD = 6;
         const int first = PAIRED ? stream * 128 : 0;
-        const int n = min(lanes_per, run.u.rows - first);
+        const int n = (max(0, min(lanes_per, run.u.rows - first) - quad + 3) >> 2) * NC;  // turns
         const uint32_t q0 = q_at + (PAIRED ? stream * C::Q_BYTES : 0);
-#pragma unroll 2
-        for (int r = quad; r < n; r += 4) {
-          const uint16_t* src = a.q + query_row(a, run.u, first + r);
+        auto load = [&](int i) {
+          if (i >= n) return make_uint2(0, 0);
+          const uint16_t* src = a.q + query_row(a, run.u, first + quad + 4 * (i / NC)) + 128 * (i % NC);
+          return __ldg(reinterpret_cast<const uint2*>(src) + lane);
+        };
+        uint2 ahead[AHEAD];
 #pragma unroll
-          for (int c = 0; c < D / 128; ++c) {
-            uint2 w = __ldg(reinterpret_cast<const uint2*>(src) + 32 * c + lane);
-            if (a.lo.flags & KVQ_ROTATE_K) {
-              float v[4] = {in_to_f32((uint16_t)w.x, DT), in_to_f32((uint16_t)(w.x >> 16), DT),
-                            in_to_f32((uint16_t)w.y, DT), in_to_f32((uint16_t)(w.y >> 16), DT)};
-              warp_rotate128(v, a.lo.d1, a.lo.d2);
-              w = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
-            }
-            const int ch = 128 * c + 4 * lane;
+        for (int i = 0; i < AHEAD; ++i) ahead[i] = load(i);
+        const bool turn = (a.lo.flags & KVQ_ROTATE_K) != 0;
+        const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
 #pragma unroll 1
-            for (int k = 0; k < a.rep; ++k) {
-              const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r + k * lanes_per, (ch & 63) >> 3) + (ch & 4) * 2;
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
-            }
+        for (int i = 0; i < n; ++i) {
+          uint2 w = ahead[0];
+#pragma unroll
+          for (int k = 0; k + 1 < AHEAD; ++k) ahead[k] = ahead[k + 1];
+          ahead[AHEAD - 1] = load(i + AHEAD);
+          if (turn) {
+            float v[4] = {in_to_f32((uint16_t)w.x, DT), in_to_f32((uint16_t)(w.x >> 16), DT),
+                          in_to_f32((uint16_t)w.y, DT), in_to_f32((uint16_t)(w.y >> 16), DT)};
+            rotate_lanes(v, s1, s2);
+            w = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+          }
+          const int ch = 128 * (i % NC) + 4 * lane, r = quad + 4 * (i / NC);
+#pragma unroll 1
+          for (int k = 0; k < a.rep; ++k) {
+            const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r + k * lanes_per, (ch & 63) >> 3) + (ch & 4) * 2;
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
           }
         }
         proxy_fence();
@@ -1670,15 +1719,16 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
       see.pos = run.u.T - run.u.n + div_g(a, run.u.r0 + my_row);
       see.win_lo = a.window ? max(0, see.pos - a.window + 1) : 0;
       see.sinks = a.sinks;
-      const int steps = (PAIRED ? 2 : 1) * (run.t1 - run.t0);
+      const int steps = (PAIRED ? 2 : 1) * (run.t1 - run.t0), first_tile = run.t0;
+      const int st = run.u.st, skip = run.u.lo_tile - st, p_lo = run.u.p_lo, p_hi = run.u.p_hi;
       float m = -INFINITY, l = 0.f;
       bool first_step = true;
 #pragma unroll 1
       for (int s = C::STREAMS == 2 ? stream : 0; s < steps; s += C::STREAMS) {
         const int b = s & 1;
-        const int j = run.t0 + (PAIRED ? s >> 1 : s);
-        const int t0 = (j < run.u.st ? j : run.u.lo_tile + (j - run.u.st)) * NT;
-        const bool masked = t0 + NT - 1 > run.u.p_lo || (a.window && t0 <= run.u.p_hi - a.window && t0 + NT > a.sinks);
+        const int j = first_tile + (PAIRED ? s >> 1 : s);
+        const int t0 = (j < st ? j : j + skip) * NT;
+        const bool masked = t0 + NT - 1 > p_lo || (a.window && t0 <= p_hi - a.window && t0 + NT > a.sinks);
         const uint32_t s_col = lane_base + C::S_COL + b * NT;
         ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
         if (!ok) break;
@@ -1731,7 +1781,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
       tc_fence_after();
       const bool cut = run.t0 > 0 || run.t1 < run.u.nt, mine = my_row < run.u.rows;
       const bool direct = !cut && (PAIRED || (C::STREAMS == 1 && a.rep == 1));
-      uint32_t x[32];
+      uint32_t x[16];
       if (direct) {
         const bool rotated = (a.lo.flags & KVQ_ROTATE_V) != 0, fix = *(volatile uint32_t*)&sh.nonfinite != 0;
         const float inv = 1.f / l, f = rotated ? 1.f : inv;
@@ -1741,16 +1791,18 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         }
         uint16_t* dst = a.out + query_row(a, run.u, mine ? my_row : 0);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          tmem_ld32(o_col + c, x);
+        for (int c = 0; c < D; c += 16) {
+          tmem_ld16(o_col + c, x);
+          const uint32_t signs = rotated ? a.lo.d1[c >> 5 & 3] >> (c & 16) : 0u;
           tmem_wait_ld();
           if (mine) {
+            uint32_t p[8];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              *reinterpret_cast<uint2*>(dst + c + i) =
-                  make_uint2(pack16<DT>(__uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f),
-                             pack16<DT>(__uint_as_float(x[i + 2]) * f, __uint_as_float(x[i + 3]) * f));
-            }
+            for (int i = 0; i < 8; ++i)
+              p[i] = pack16<DT>(__uint_as_float(x[2 * i] ^ ((signs << (31 - 2 * i)) & 0x80000000u)) * f,
+                                __uint_as_float(x[2 * i + 1] ^ ((signs << (30 - 2 * i)) & 0x80000000u)) * f);
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(p[0], p[1], p[2], p[3]);
+            *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(p[4], p[5], p[6], p[7]);
           }
           __syncwarp();
         }
@@ -1764,12 +1816,12 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         // a stream without a step of this run has no accumulator
         const bool none = C::STREAMS == 2 && stream >= steps;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          tmem_ld32(o_col + c, x);
+        for (int c = 0; c < D; c += 16) {
+          tmem_ld16(o_col + c, x);
           tmem_wait_ld();
           if (mine) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
+            for (int i = 0; i < 16; i += 4)
               *reinterpret_cast<uint4*>(part + c + i) =
                   none ? make_uint4(0, 0, 0, 0) : make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
           }
