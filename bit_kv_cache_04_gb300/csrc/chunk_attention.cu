@@ -73,6 +73,10 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
   if (window < 0 || sinks < 0) return fail(KVQ_ERR_ARG, "window=%d, sinks=%d", window, sinks);
   if (!cu_q || !seq_lens || (total_q > 0 && (!q || !out))) return fail(KVQ_ERR_ARG, "q / cu_q / seq_lens / out is NULL");
   if (((uintptr_t)q | (uintptr_t)out) & 15u) return fail(KVQ_ERR_ARG, "q / out must be 16-byte aligned");
+  {
+    const uintptr_t bytes = (uintptr_t)2 * n_layers * total_q * cfg->H_q * cfg->D, x = (uintptr_t)q, y = (uintptr_t)out;
+    if (total_q > 0 && x < y + bytes && y < x + bytes) return fail(KVQ_ERR_ARG, "q and out overlap");
+  }
   if (((uintptr_t)cu_q | (uintptr_t)seq_lens) & 3u) return fail(KVQ_ERR_ARG, "cu_q / seq_lens must be 4-byte aligned");
   ChunkArgs a{};
   if ((st = cache_ptrs(cfg, cache, &a.cp)) != KVQ_OK) return st;
@@ -108,6 +112,7 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
     return fail(KVQ_ERR_UNSUPPORTED, "too many tiles for one call: pass fewer layers or rows");
   a.g_magic = (uint32_t)((1ull << 32) / a.lo.g + 1);
   const int most = cfg->D == 128 ? 4 : 2;  // a repetition keeps at least 32 tokens of a tile
+  a.turn_here = (cfg->flags & KVQ_ROTATE_K) && rows <= 64 ? 1 : 0;
   a.rep = rows <= 32 ? most : rows <= 64 ? 2 : 1;
   a.by_warp = rows > 4 * row_tile;
   // Staging: 32-token subtiles as single bulk copies; pages of fewer tokens

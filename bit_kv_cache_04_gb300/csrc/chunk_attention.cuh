@@ -58,6 +58,7 @@ struct ChunkArgs {
   const int32_t* cu_q;
   const int32_t* seq_lens;
   int total_q, max_q, window, sinks;
+  int turn_here;  // rotated formats: the kernel turns the (few) queries itself; else a pass before it does
   int rep;      // repetitions of the query rows over the lanes: 1, 2, 4
   uint32_t g_magic;  // floor(2^32 / g) + 1
   int by_warp;  // row tiles per sequence are many: count them with a warp per sequence

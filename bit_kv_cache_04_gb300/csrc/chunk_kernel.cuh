@@ -1000,7 +1000,7 @@ __device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Ru
 // A dequantizing warp's half of a piece that the hot path does not cover: one
 // call with few arguments (the caller's registers are short), everything else worked out again.
 template <int D, int DT>
-__device__ __noinline__ void cold_piece(const ChunkArgs& a, ChunkShared& sh, const Run& run, uint32_t tiles_at,
+__device__ __forceinline__ void cold_piece(const ChunkArgs& a, ChunkShared& sh, const Run& run, uint32_t tiles_at,
                                         uint32_t raw_at, int dw, uint32_t kt, uint32_t slot, int j) {
   constexpr int NT = chunk_tile(D);
   const int piece = dw >> 1, which = dw >> 2, half = piece & 1, part = dw & 1, lane = threadIdx.x & 31;
@@ -1133,7 +1133,7 @@ __device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, 
 
 // Joins the partial rows of one unit and writes its output rows; all softmax threads.
 template <int D, int DT, bool PAIRED>
-__device__ __noinline__ void join_unit(const ChunkArgs& a, const Run& run, const LineStart& line, bool cut, bool fix) {
+__device__ __forceinline__ void join_unit(const ChunkArgs& a, const Run& run, const LineStart& line, bool cut, bool fix) {
   using C = ChunkShape<D, PAIRED>;
   constexpr int N = D / 128;
   constexpr int PR = chunk_part_row(D), SLOT = chunk_slot_rows(D) * PR;
@@ -1152,78 +1152,106 @@ __device__ __noinline__ void join_unit(const ChunkArgs& a, const Run& run, const
     return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
   const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
-  // many rows: four of a warp at a time, for one by itself is a chain of loads from L2
-  constexpr int RW = PAIRED ? 4 : 1;
-#pragma unroll 1
-  for (int r0 = warp * RW; r0 < u.rows; r0 += RW * C::SOFT_WARPS) {
-    float M[RW], L[RW], acc[RW][N][4];
+  auto write = [&](int r, float (&acc)[N][4], float L) {
+    uint16_t* dst = a.out + query_row(a, u, r);
+    const float inv = 1.f / L;
 #pragma unroll
-    for (int q = 0; q < RW; ++q) {
-      M[q] = -INFINITY;
-      L[q] = 0.f;
-#pragma unroll
-      for (int c = 0; c < N; ++c) acc[q][c][0] = acc[q][c][1] = acc[q][c][2] = acc[q][c][3] = 0.f;
+    for (int c = 0; c < N; ++c) {
+      float v[4] = {acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv};
+      if (a.lo.flags & KVQ_ROTATE_V) rotate_lanes(v, s2, s1);
+      *reinterpret_cast<uint2*>(dst + 128 * c + 4 * lane) = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+      if (fix) add_nonfinite<DT>(a, run, u.T - u.n + div_g(a, u.r0 + r), 128 * c + 4 * lane, 4, dst);
     }
-#pragma unroll 1
-    for (int i = lane; i < parts; i += 32) {
-      const float* p = part(i, r0) + D;
+  };
+  if (PAIRED && parts <= 4) {
+    // Many rows of few parts: a lane works out the weights of one row of the
+    // warp's 32; then row by row, the next row's loads in flight.
+    const int r0 = 32 * warp, mine = min(r0 + lane, u.rows - 1);
+    float w[4], M = -INFINITY, L = 0.f;
+    float2 ml[4];
 #pragma unroll
-      for (int q = 0; q < RW; ++q) M[q] = fmaxf(M[q], __ldcg(p + q * PR));
+    for (int i = 0; i < 4; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i < parts) ml[i] = __ldcg(reinterpret_cast<const float2*>(part(i, mine) + D));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int i = 0; i < 4; ++i) M = fmaxf(M, ml[i].x);
 #pragma unroll
-      for (int q = 0; q < RW; ++q) M[q] = fmaxf(M[q], __shfl_xor_sync(0xffffffffu, M[q], o));
+    for (int i = 0; i < 4; ++i) {
+      // a part that saw none of the row's tokens has m = -inf and l = 0
+      const bool none = ml[i].x == -INFINITY && ml[i].y == 0.f;
+      w[i] = none ? 0.f : ex2(ml[i].x - M);
+      L += none ? 0.f : w[i] * ml[i].y;
+    }
+    float4 next[4][N];
+    auto load = [&](int r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+          if (i < parts) next[i][c] = __ldcg(reinterpret_cast<const float4*>(part(i, min(r, u.rows - 1))) + 32 * c + lane);
+    };
+    load(r0);
 #pragma unroll 1
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      const float* p = part(min(i0 + lane, parts - 1), r0);
-      float w[RW];
+    for (int r = r0; r < min(r0 + 32, u.rows); ++r) {
+      float acc[N][4];
 #pragma unroll
-      for (int q = 0; q < RW; ++q) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + q * PR + D));
-        // a part that saw none of the row's tokens has m = -inf and l = 0
-        const bool none = i0 + lane >= parts || (ml.x == -INFINITY && ml.y == 0.f);
-        w[q] = none ? 0.f : ex2(ml.x - M[q]);
-        L[q] += none ? 0.f : w[q] * ml.y;
-      }
-      const uint32_t off = (uint32_t)((p - a.partials) >> 2);  // in 16-byte words
-      const int k1 = min(32, parts - i0);
-#pragma unroll 2
-      for (int k = 0; k < k1; ++k) {
-        const float4* o4 = reinterpret_cast<const float4*>(a.partials) + __shfl_sync(0xffffffffu, off, k) + lane;
+      for (int c = 0; c < N; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
 #pragma unroll
-        for (int q = 0; q < RW; ++q) {
-          const float wk = __shfl_sync(0xffffffffu, w[q], k);
+      for (int i = 0; i < 4; ++i) {
+        const float wk = __shfl_sync(0xffffffffu, w[i], r - r0);
+        if (i < parts && wk != 0.f) {
 #pragma unroll
           for (int c = 0; c < N; ++c) {
-            const float4 v = __ldcg(o4 + q * (PR / 4) + 32 * c);
-            if (wk != 0.f) {  // rows that the part has not are not written either
-              acc[q][c][0] = fmaf(wk, v.x, acc[q][c][0]);
-              acc[q][c][1] = fmaf(wk, v.y, acc[q][c][1]);
-              acc[q][c][2] = fmaf(wk, v.z, acc[q][c][2]);
-              acc[q][c][3] = fmaf(wk, v.w, acc[q][c][3]);
-            }
+            acc[c][0] = fmaf(wk, next[i][c].x, acc[c][0]);
+            acc[c][1] = fmaf(wk, next[i][c].y, acc[c][1]);
+            acc[c][2] = fmaf(wk, next[i][c].z, acc[c][2]);
+            acc[c][3] = fmaf(wk, next[i][c].w, acc[c][3]);
+          }
+        }
+      }
+      load(r + 1);
+      write(r, acc, __shfl_sync(0xffffffffu, L, r - r0));
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int r = warp; r < u.rows; r += C::SOFT_WARPS) {
+    float M = -INFINITY, L = 0.f, acc[N][4];
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+#pragma unroll 1
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(part(i, r) + D));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const float* p = part(min(i0 + lane, parts - 1), r);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
+      const bool none = i0 + lane >= parts || (ml.x == -INFINITY && ml.y == 0.f);
+      const float w = none ? 0.f : ex2(ml.x - M);
+      L += none ? 0.f : w * ml.y;
+      const uint32_t off = (uint32_t)((p - a.partials) >> 2);  // in 16-byte words
+      const int k1 = min(32, parts - i0);
+#pragma unroll 4
+      for (int k = 0; k < k1; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float4* o4 = reinterpret_cast<const float4*>(a.partials) + __shfl_sync(0xffffffffu, off, k) + lane;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const float4 v = __ldcg(o4 + 32 * c);
+          if (wk != 0.f) {
+            acc[c][0] = fmaf(wk, v.x, acc[c][0]);
+            acc[c][1] = fmaf(wk, v.y, acc[c][1]);
+            acc[c][2] = fmaf(wk, v.z, acc[c][2]);
+            acc[c][3] = fmaf(wk, v.w, acc[c][3]);
           }
         }
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int q = 0; q < RW; ++q) L[q] += __shfl_xor_sync(0xffffffffu, L[q], o);
-#pragma unroll
-    for (int q = 0; q < RW; ++q) {
-      if (r0 + q >= u.rows) break;
-      uint16_t* dst = a.out + query_row(a, u, r0 + q);
-      const float inv = 1.f / L[q];
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
-        float v[4] = {acc[q][c][0] * inv, acc[q][c][1] * inv, acc[q][c][2] * inv, acc[q][c][3] * inv};
-        if (a.lo.flags & KVQ_ROTATE_V) rotate_lanes(v, s2, s1);
-        *reinterpret_cast<uint2*>(dst + 128 * c + 4 * lane) = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
-        if (fix) add_nonfinite<DT>(a, run, u.T - u.n + div_g(a, u.r0 + r0 + q), 128 * c + 4 * lane, 4, dst);
-      }
-    }
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    write(r, acc, L);
   }
 }
 
@@ -1675,40 +1703,53 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
       const int cols = NT / a.rep, col0 = (my_lane / lanes_per) * cols;  // this row's tokens of a tile
       const int my_row = (PAIRED ? stream * 128 : 0) + (my_lane & (lanes_per - 1));  // query row of the row tile
       const float sc = 1.4426950408889634f * rsqrtf((float)D);
-      // queries: rows quad, quad + 4, ... of this stream's tile (each repetition a copy), 128 channels a
-      // turn, the next turns' loads in flight
+      // queries into shared memory
       if (PAIRED || stream == 0) {
-        constexpr int NC = D / 128, AHEAD = 6;
-        const int first = PAIRED ? stream * 128 : 0;
-        const int n = (max(0, min(lanes_per, run.u.rows - first) - quad + 3) >> 2) * NC;  // turns
+        const int first = PAIRED ? stream * 128 : 0, n = min(lanes_per, run.u.rows - first);  // rows
         const uint32_t q0 = q_at + (PAIRED ? stream * C::Q_BYTES : 0);
-        auto load = [&](int i) {
-          if (i >= n) return make_uint2(0, 0);
-          const uint16_t* src = a.q + query_row(a, run.u, first + quad + 4 * (i / NC)) + 128 * (i % NC);
-          return __ldg(reinterpret_cast<const uint2*>(src) + lane);
-        };
-        uint2 ahead[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) ahead[i] = load(i);
-        const bool turn = (a.lo.flags & KVQ_ROTATE_K) != 0;
-        const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
+        if (a.turn_here) {
+          // few rows, turned into the rotated domain here: a warp a row (each repetition a copy)
+          const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
+          constexpr int NC = D / 128;
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-          uint2 w = ahead[0];
-#pragma unroll
-          for (int k = 0; k + 1 < AHEAD; ++k) ahead[k] = ahead[k + 1];
-          ahead[AHEAD - 1] = load(i + AHEAD);
-          if (turn) {
+          for (int e = quad; e < n * NC; e += 4) {
+            const int r = e / NC, c = e % NC;
+            uint2 w = __ldcg(reinterpret_cast<const uint2*>(a.q + query_row(a, run.u, first + r) + 128 * c) + lane);
             float v[4] = {in_to_f32((uint16_t)w.x, DT), in_to_f32((uint16_t)(w.x >> 16), DT),
                           in_to_f32((uint16_t)w.y, DT), in_to_f32((uint16_t)(w.y >> 16), DT)};
             rotate_lanes(v, s1, s2);
             w = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
-          }
-          const int ch = 128 * (i % NC) + 4 * lane, r = quad + 4 * (i / NC);
+            const int ch = 128 * c + 4 * lane;
 #pragma unroll 1
-          for (int k = 0; k < a.rep; ++k) {
-            const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r + k * lanes_per, (ch & 63) >> 3) + (ch & 4) * 2;
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
+            for (int k = 0; k < a.rep; ++k) {
+              const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r + k * lanes_per, (ch & 63) >> 3) + (ch & 4) * 2;
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
+            }
+          }
+        } else {
+          constexpr int LPR = D / 8, RPT = 32 / LPR, U = 4;  // lanes a row, rows a turn, turns in flight
+          const int ch = 8 * (lane & (LPR - 1)), sub = lane / LPR;
+          const uint32_t col = q0 + (uint32_t)(ch >> 6) * 16384;
+#pragma unroll 1
+          for (int r0 = quad * RPT + sub; r0 - sub < n; r0 += 4 * RPT * U) {
+            uint4 w[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              const int r = r0 + 4 * RPT * i;
+              w[i] = make_uint4(0, 0, 0, 0);
+              if (r < n) w[i] = __ldcg(reinterpret_cast<const uint4*>(a.q + query_row(a, run.u, first + r) + ch));
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              const int r = r0 + 4 * RPT * i;
+              if (r < n) {
+#pragma unroll 1
+                for (int k = 0; k < a.rep; ++k)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(col + swz(r + k * lanes_per, (ch & 63) >> 3)),
+                               "r"(w[i].x), "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
+                               : "memory");
+              }
+            }
           }
         }
         proxy_fence();
@@ -1872,6 +1913,49 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   }
 }
 
+// Queries of a rotated format turned into the rotated domain, into their rows
+// of `out` (which a row's outputs replace when everything that reads it has been read): a
+// warp per (layer, row).  With many rows a sequence, turning them as they are loaded kept the products
+// waiting a fifth of the time.
+template <int D, int DT>
+__global__ void __launch_bounds__(256) turn_queries_kernel(const __grid_constant__ ChunkArgs a) {
+  const int lane = threadIdx.x & 31;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (w >= (int64_t)a.n_layers * a.total_q) return;
+  const int row = (int)(w % a.total_q);
+  int lo = 0, hi = a.lo.B;  // the last b with cu_q[b] <= row
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (__ldg(a.cu_q + mid) <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  int n, T, cu;
+  if (!valid_seq(a, lo, &n, &T, &cu) || row < cu || row >= cu + n) return;  // rows of no sequence stay as they are
+  const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
+  const uint2* src = reinterpret_cast<const uint2*>(a.q + w * a.lo.Hq * D) + lane;
+  uint2* dst = reinterpret_cast<uint2*>(a.out + w * a.lo.Hq * D) + lane;
+  const int chunks = a.lo.Hq * (D / 128);
+#pragma unroll 1
+  for (int c0 = 0; c0 < chunks; c0 += 4) {
+    uint2 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c0 + k < chunks) x[k] = __ldg(src + 32 * (c0 + k));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c0 + k < chunks) {
+        float v[4] = {in_to_f32((uint16_t)x[k].x, DT), in_to_f32((uint16_t)(x[k].x >> 16), DT),
+                      in_to_f32((uint16_t)x[k].y, DT), in_to_f32((uint16_t)(x[k].y >> 16), DT)};
+        rotate_lanes(v, s1, s2);
+        dst[32 * (c0 + k)] = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+      }
+  }
+}
+
 template <int D, int DT, bool PAIRED>
 cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   using C = ChunkShape<D, PAIRED>;
@@ -1882,8 +1966,15 @@ cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   if (a.slots > kChunkMaxSlots) a.slots = kChunkMaxSlots;
   if (a.slots < 1) return cudaErrorInvalidConfiguration;
   const uint32_t smem = C::FIXED + 16 + a.slots * a.slot_bytes;
+  cudaError_t e;
+  if ((a.lo.flags & KVQ_ROTATE_K) && !a.turn_here) {
+    const int64_t rows = (int64_t)a.n_layers * a.total_q;
+    e = launch_dependent(turn_queries_kernel<D, DT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+    if (e != cudaSuccess) return e;
+    a.q = a.out;
+  }
   // set on every call: the attribute belongs to the current device
-  cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, PAIRED>,
+  e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, PAIRED>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(chunk_attention_kernel<D, DT, PAIRED>, dim3(grid), dim3(C::THREADS), smem, s, a);

@@ -550,8 +550,9 @@ KVQ_API kvq_status kvq_pages_compact(const kvq_config* cfg, const kvq_cache* cac
  * p_i = seq_lens[b] - n_b + i.  One call covers a decode step (n_b = 1), the
  * verification of a draft (a few) and prefill chunks (thousands), over every
  * format, tier and page layout of the cache as kvq_append left it.
- *  q, out:   [n_layers][total_q][H_q][D] in_dtype, device, 16-byte aligned; the rows of
- *            a sequence back to back in batch order; q post-RoPE.
+ *  q, out:   [n_layers][total_q][H_q][D] in_dtype, device, 16-byte aligned, not
+ *            overlapping; the rows of a sequence back to back in batch order; q post-RoPE.
+ *            (A sequence's rows of out may hold intermediate values while the call runs.)
  *  cu_q:     [batch + 1] int32, device, cu_q[0] = 0.  Rows from cu_q[batch]
  *            to total_q are left as they are; a sequence may have no rows.
  *  total_q, max_q: host values: rows of q, and a bound on every n_b.

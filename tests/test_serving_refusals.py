@@ -170,7 +170,7 @@ def _ca(cfg=None, cache=None, layer0=0, n_layers=1, q=A, cu=A, total=4, most=2, 
     (dict(layer0=1, n_layers=2 ** 31 - 1), 1), (dict(q=None), 1), (dict(cu=None), 1), (dict(lens=None), 1),
     (dict(out=None), 1), (dict(total=-1), 1), (dict(most=5), 1), (dict(most=-1), 1), (dict(total=100, most=65), 4),
     (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(q=A + 8), 1), (dict(out=2 * A + 2), 1), (dict(ws=None), 5),
-    (dict(ws=A + 16), 5), (dict(nbytes=16), 5), (dict(cu=A + 2), 1), (dict(lens=A + 1), 1),
+    (dict(ws=A + 16), 5), (dict(nbytes=16), 5), (dict(cu=A + 2), 1), (dict(lens=A + 1), 1), (dict(out=A), 1), (dict(out=A + 256), 1),
 ])
 def test_chunk_attention_refusals(kw, status):
     assert _ca(**kw) == status
