@@ -1131,9 +1131,11 @@ __device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, 
   return (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + u.h * a.lo.g + (row - tok * a.lo.g)) * a.lo.D;
 }
 
-// Joins the partial rows of one unit and writes its output rows; all softmax threads.
+// Joins the partial rows of one unit and writes its output rows; all softmax
+// threads.  scratch: 8 rows of D + 4 floats in shared memory.  False once a warp has given up.
 template <int D, int DT, bool PAIRED>
-__device__ __forceinline__ void join_unit(const ChunkArgs& a, const Run& run, const LineStart& line, bool cut, bool fix) {
+__device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, const LineStart& line, bool cut, bool fix,
+                                          float* scratch, uint32_t soft, uint32_t& syncs, uint32_t* gave_up) {
   using C = ChunkShape<D, PAIRED>;
   constexpr int N = D / 128;
   constexpr int PR = chunk_part_row(D), SLOT = chunk_slot_rows(D) * PR;
@@ -1144,11 +1146,11 @@ __device__ __forceinline__ void join_unit(const ChunkArgs& a, const Run& run, co
   const int c1 = cut ? (unit_pos + u.nt - 1) / line.per_cta : blockIdx.x;
   const int slot0 = !cut ? 2 : unit_pos == c0 * line.per_cta ? 0 : 1;  // of the first CTA; the others' is 0
   const int copies = PAIRED ? 1 : C::STREAMS * a.rep;  // partial rows of one query row in one slot
-  const int lanes_per = 128 / a.rep;
+  const int rep_log = a.rep == 4 ? 2 : a.rep - 1, copies_log = PAIRED ? 0 : rep_log + C::STREAMS - 1;
   const int parts = (c1 - c0 + 1) * copies;
   auto part = [&](int i, int r) {
-    const int c = PAIRED ? i : i / copies, k = PAIRED ? 0 : i - c * copies;  // k: stream k / rep, repetition k % rep
-    const int s = k / a.rep, row = PAIRED ? r : s * 128 + (k - s * a.rep) * lanes_per + r;
+    // copy k of a slot: stream k / rep (128 rows each), repetition k % rep (128 / rep rows each)
+    const int c = i >> copies_log, row = PAIRED ? r : ((i & (copies - 1)) << (7 - rep_log)) + r;
     return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
   const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
@@ -1213,46 +1215,84 @@ __device__ __forceinline__ void join_unit(const ChunkArgs& a, const Run& run, co
       load(r + 1);
       write(r, acc, __shfl_sync(0xffffffffu, L, r - r0));
     }
-    return;
+    return true;
   }
+  // Few rows: `wpr` warps share a row's parts and join their sums in shared memory.
+  const int wpr = u.rows >= C::SOFT_WARPS ? 1 : u.rows > C::SOFT_WARPS / 2 ? 1 : u.rows > C::SOFT_WARPS / 4 ? 2 : u.rows > 1 || C::SOFT_WARPS == 4 ? 4 : 8;
+  const int sub = warp & (wpr - 1), len = (parts + wpr - 1) / wpr, i0 = sub * len, i1 = min(parts, i0 + len);
+  const int per = C::SOFT_WARPS / wpr;  // rows at a time
 #pragma unroll 1
-  for (int r = warp; r < u.rows; r += C::SOFT_WARPS) {
+  for (int rr = warp / wpr; rr < (u.rows + per - 1) / per * per; rr += per) {
+    const int r = min(rr, u.rows - 1);
     float M = -INFINITY, L = 0.f, acc[N][4];
 #pragma unroll
     for (int c = 0; c < N; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(part(i, r) + D));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll 1
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      const float* p = part(min(i0 + lane, parts - 1), r);
+    for (int i = i0; i < i1; i += 32) {
+      const float* p = part(min(i + lane, parts - 1), r);
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
-      const bool none = i0 + lane >= parts || (ml.x == -INFINITY && ml.y == 0.f);
+      // a part that saw none of the row's tokens has m = -inf and l = 0
+      const bool none = i + lane >= i1 || (ml.x == -INFINITY && ml.y == 0.f);
       const float w = none ? 0.f : ex2(ml.x - M);
       L += none ? 0.f : w * ml.y;
       const uint32_t off = (uint32_t)((p - a.partials) >> 2);  // in 16-byte words
-      const int k1 = min(32, parts - i0);
-#pragma unroll 4
-      for (int k = 0; k < k1; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float4* o4 = reinterpret_cast<const float4*>(a.partials) + __shfl_sync(0xffffffffu, off, k) + lane;
+      const int k1 = min(32, i1 - i);
+      constexpr int U = 8 / N;  // loads in flight
+#pragma unroll 1
+      for (int k = 0; k < k1; k += U) {
+        float4 v[U][N];
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-          const float4 v = __ldcg(o4 + 32 * c);
-          if (wk != 0.f) {
-            acc[c][0] = fmaf(wk, v.x, acc[c][0]);
-            acc[c][1] = fmaf(wk, v.y, acc[c][1]);
-            acc[c][2] = fmaf(wk, v.z, acc[c][2]);
-            acc[c][3] = fmaf(wk, v.w, acc[c][3]);
+        for (int q = 0; q < U; ++q) {
+          const float4* o4 = reinterpret_cast<const float4*>(a.partials) + __shfl_sync(0xffffffffu, off, min(k + q, 31)) + lane;
+#pragma unroll
+          for (int c = 0; c < N; ++c) v[q][c] = __ldcg(o4 + 32 * c);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const float wk = __shfl_sync(0xffffffffu, w, min(k + q, 31));
+          if (k + q < k1 && wk != 0.f) {
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+              acc[c][0] = fmaf(wk, v[q][c].x, acc[c][0]);
+              acc[c][1] = fmaf(wk, v[q][c].y, acc[c][1]);
+              acc[c][2] = fmaf(wk, v[q][c].z, acc[c][2]);
+              acc[c][3] = fmaf(wk, v[q][c].w, acc[c][3]);
+            }
           }
         }
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    write(r, acc, L);
+    if (wpr > 1) {
+      float* mine = scratch + warp * (D + 4);
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        *reinterpret_cast<float4*>(mine + 128 * c + 4 * lane) = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
+      if (lane == 0) mine[D] = L;
+      if (!soft_sync(soft, syncs, gave_up)) return false;
+      if (sub) continue;  // one turn: fewer rows than warps
+#pragma unroll 1
+      for (int k = 1; k < wpr; ++k) {
+        const float* o = mine + k * (D + 4);
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(o + 128 * c + 4 * lane);
+          acc[c][0] += v.x;
+          acc[c][1] += v.y;
+          acc[c][2] += v.z;
+          acc[c][3] += v.w;
+        }
+        L += o[D];
+      }
+    }
+    if (rr < u.rows) write(r, acc, L);
   }
+  return true;
 }
 
 // The butterflies of the 128-point transform on TMEM columns [col, col + 128)
@@ -1894,7 +1934,9 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         } else {
           fix = *(volatile uint32_t*)&sh.nonfinite != 0;
         }
-        if (join) join_unit<D, DT, PAIRED>(a, run, sh.start, cut, fix);
+        // (the queries' shared memory is free: the run's products are done)
+        if (join && !(ok = join_unit<D, DT, PAIRED>(a, run, sh.start, cut, fix, reinterpret_cast<float*>(smem), soft, syncs, gave_up)))
+          break;
         if (!(ok = soft_sync(soft, syncs, gave_up))) break;
         if (join && cut && tid == 0) {
           a.tickets[tick] = 0;
