@@ -4,9 +4,8 @@
 // Bound by HBM: 2 bytes in and 2 bytes out per value, and a few fp32
 // operations.  A row (one token's head) belongs to D / 8 lanes of 8 channels
 // (one 16-byte load and store each), so the mean square is a shuffle sum and
-// the partner of a half-split pair sits in another lane of the same row.  The
-// cosines and sines of a token are worked out once per block, in shared
-// memory, and used by all of its heads.
+// the partner of a half-split pair sits in another lane of the same row.  A
+// warp works out a token's cosines and sines once, in registers, for all the heads it takes.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -30,7 +29,7 @@ struct NormRopeArgs {
   int vec[2];            // 16-byte loads and stores fit
   int w_vec[2];
   const int32_t* positions;
-  int n_tokens, tokens_per_block, rows_per_block;
+  int n_tokens, shares, rows_per_share;  // warps of a token, and heads of each
   float eps, scale;
   int rot_dim;
   uint64_t turns[128];
@@ -86,22 +85,47 @@ __device__ __forceinline__ void to_f32(uint4 v, float (&f)[8]) {
   }
 }
 
-// One row in f (this lane's 8 channels from 8c): norm, turn, rounded result.
+// Where pair i's frequency sits in shared memory: lanes read pairs 8 (or 4)
+// apart, which this order puts next to each other.
+template <int MODE>
+__device__ __forceinline__ int turn_slot(int i) {
+  return MODE == kTurnInterleaved ? (i & 3) * 32 + (i >> 2) : (i & 7) * 16 + (i >> 3);
+}
+
+// Cosine and sine of a lane's channel pairs at one position: 4 adjacent pairs
+// (interleaved), or one for each of its 8 channels (half split).
+template <int MODE>
+__device__ __forceinline__ void angles(const NormRopeArgs& a, const uint64_t* turns, int64_t pos, int c, float2 (&cs)[8]) {
+  const int half = a.rot_dim / 2;
+#pragma unroll
+  for (int j = 0; j < (MODE == kTurnInterleaved ? 4 : 8); ++j) {
+    const int ch = MODE == kTurnInterleaved ? 8 * c + 2 * j : 8 * c + j;
+    const int i = MODE == kTurnInterleaved ? 4 * c + j : ch < half ? ch : ch - half;
+    cs[j] = make_float2(1.f, 0.f);
+    if (ch < a.rot_dim) {
+      // the angle in turns as a 64-bit fraction: exact for every position, so
+      // only its top 32 bits, as a signed number of half turns, see fp32
+      float s, co;
+      sincospif((float)(int32_t)((uint64_t)pos * turns[turn_slot<MODE>(i)] >> 32) * 0x1p-31f, &s, &co);
+      cs[j] = make_float2(co * a.scale, s * a.scale);
+    }
+  }
+}
+
+// One row in f (this lane's 8 channels from 8c): norm (with the weights w) and turn.
 template <int DT, int D, int MODE>
-__device__ __forceinline__ uint4 row_result(float (&f)[8], const uint16_t* w, bool w_vec, float eps, int rot,
-                                            const float2* cs, float* buf, int c) {
+__device__ __forceinline__ void row_result(float (&f)[8], bool norm, uint4 w, float eps, int rot,
+                                           const float2 (&cs)[8], float* buf, int c) {
   constexpr int LPR = D / 8;
-  // The shuffles of the sum run for every row: rows of one warp may differ in
-  // tensor, and so in having a weight.
-  float ss = 0.f;
+  if (norm) {  // of the whole warp: its rows are of one tensor
+    float ss = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+    for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (w) {
-    const float r = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(ss * (1.0f / D) + eps);
     float wf[8];
-    to_f32<DT>(load8(w + 8 * c, w_vec), wf);
+    to_f32<DT>(w, wf);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = f[j] * r * wf[j];
   }
@@ -109,106 +133,103 @@ __device__ __forceinline__ uint4 row_result(float (&f)[8], const uint16_t* w, bo
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (8 * c + 2 * j < rot) {
-        const float2 t = cs[4 * c + j];
-        const float a = f[2 * j], b = f[2 * j + 1];
-        f[2 * j] = a * t.x - b * t.y;
-        f[2 * j + 1] = b * t.x + a * t.y;
-      }
-    }
-  } else if constexpr (MODE == kTurnHalf8) {
-    // rot / 2 is a multiple of 8: the partner channels are another lane's 8
-    const int half = rot / 2, hl = half / 8;
-    const bool first = c < hl, in = 8 * c < rot;
-    const int src = (threadIdx.x & 31 & ~(LPR - 1)) + (in ? (first ? c + hl : c - hl) : c);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float o = __shfl_sync(0xffffffffu, f[j], src);
-      if (in) {
-        const float2 t = cs[8 * c + j - (first ? 0 : half)];
-        f[j] = first ? f[j] * t.x - o * t.y : f[j] * t.x + o * t.y;
+        const float x = f[2 * j], y = f[2 * j + 1];
+        f[2 * j] = x * cs[j].x - y * cs[j].y;
+        f[2 * j + 1] = y * cs[j].x + x * cs[j].y;
       }
     }
   } else {
-    // any even rot: through the row's buffer in shared memory
-#pragma unroll
-    for (int j = 0; j < 8; ++j) buf[8 * c + j] = f[j];
-    __syncwarp();
     const int half = rot / 2;
+    float o[8];
+    if constexpr (MODE == kTurnHalf8) {
+      // rot / 2 is a multiple of 8: the partner channels are another lane's 8
+      const int hl = half / 8, src = (threadIdx.x & 31 & ~(LPR - 1)) + (8 * c >= rot ? c : c < hl ? c + hl : c - hl);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, f[j], src);
+    } else {
+      // any even rot: through the row's buffer in shared memory
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) buf[8 * c + j] = f[j];
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = 8 * c + j;
+        o[j] = buf[i < half ? i + half : i < rot ? i - half : i];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = 8 * c + j;
-      if (i < rot) {
-        const bool first = i < half;
-        const float o = buf[first ? i + half : i - half];
-        const float2 t = cs[first ? i : i - half];
-        f[j] = first ? f[j] * t.x - o * t.y : f[j] * t.x + o * t.y;
-      }
+      if (i < rot) f[j] = i < half ? f[j] * cs[j].x - o[j] * cs[j].y : f[j] * cs[j].x + o[j] * cs[j].y;
     }
-    __syncwarp();
   }
-  uint4 v;
-  v.x = pack2<DT>(f[0], f[1]);
-  v.y = pack2<DT>(f[2], f[3]);
-  v.z = pack2<DT>(f[4], f[5]);
-  v.w = pack2<DT>(f[6], f[7]);
-  return v;
 }
 
-// Block (x, y): tokens [x * tokens_per_block, ...), rows (token, head) [y *
-// rows_per_block, ...) of them, queries' heads before keys'.
+// A warp per (token, share of its heads): the angles once, in registers, then
+// row after row.  With a block per token and the
+// angles in shared memory 8192 tokens of 40 heads took 93 us.
 template <int DT, int D, int MODE>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  constexpr int LPR = D / 8, RPP = kThreads / LPR;  // rows per pass
-  constexpr int U = 2;                               // rows in flight per lane
-  extern __shared__ float2 cs[];                     // [tokens_per_block][rot_dim / 2]
-  __shared__ float buf[MODE == kTurnHalfAny ? RPP * D : 1];
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 2;  // lanes a row, rows a pass, passes a turn (the next turn's loads in flight)
+  __shared__ float buf[MODE == kTurnHalfAny ? kThreads / 32 * RPW * D : 1];
+  __shared__ uint64_t turns[128];  // a lane's own word of the parameters would be a serialized load, every time
+  if (threadIdx.x < 128) turns[turn_slot<MODE>(threadIdx.x)] = a.turns[threadIdx.x];
+  __syncthreads();
   grid_launch_dependents();
   grid_dependency_wait();
-  const int t0 = blockIdx.x * a.tokens_per_block;
-  const int nt = min(a.tokens_per_block, a.n_tokens - t0);
-  const int half = a.rot_dim / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+  const int64_t tok = w / a.shares;
+  if (tok >= a.n_tokens) return;
   const int H = a.heads[0] + a.heads[1];
-  const int r0 = blockIdx.y * a.rows_per_block, r1 = min(nt * H, r0 + a.rows_per_block);
-  if (r0 >= r1) return;
-  const int ta = r0 / H, tb = (r1 - 1) / H;  // tokens this block's rows touch
-  for (int e = ta * half + threadIdx.x; e < (tb + 1) * half; e += kThreads) {
-    // the angle in turns as a 64-bit fraction: exact for every position, so
-    // only its top 32 bits, as a signed number of half turns, see fp32
-    const int64_t pos = a.positions[t0 + e / half];
-    const uint64_t turn = (uint64_t)pos * a.turns[e % half];
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-    cs[e] = make_float2(c * a.scale, s * a.scale);
-  }
-  __syncthreads();
-  const int slot = threadIdx.x / LPR, c = threadIdx.x % LPR;
-  for (int r = r0 + slot; r - slot < r1; r += RPP * U) {
-    uint4 raw[U];
-    int which[U], tok[U], head[U];
+  const int r0 = (int)(w - tok * a.shares) * a.rows_per_share, r1 = min(H, r0 + a.rows_per_share);
+  const int c = lane & (LPR - 1), sub = lane / LPR;
+  float2 cs[8];
+  bool have = false;
+#pragma unroll 1
+  for (int t = 0; t < 2; ++t) {
+    // this share's heads of tensor t
+    const int h0 = max(0, r0 - (t ? a.heads[0] : 0)), h1 = min(a.heads[t], r1 - (t ? a.heads[0] : 0));
+    if (h0 >= h1) continue;
+    const uint16_t* src = a.x[t] + tok * a.st[t] + 8 * c;
+    uint16_t* dst = a.y[t] + tok * (int64_t)a.heads[t] * D + 8 * c;
+    const int64_t sh = a.sh[t];
+    const bool vec = a.vec[t] != 0, norm = a.w[t] != nullptr;
+    uint4 wt = make_uint4(0, 0, 0, 0);
+    if (norm) wt = load8(a.w[t] + 8 * c, a.w_vec[t]);
+    auto load = [&](uint4 (&raw)[U], int h) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int ru = r + u * RPP;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      which[u] = tok[u] = head[u] = 0;
-      if (ru < r1) {
-        tok[u] = ru / H;
-        head[u] = ru - tok[u] * H;
-        which[u] = head[u] >= a.heads[0];
-        if (which[u]) head[u] -= a.heads[0];
-        const int w = which[u];
-        raw[u] = load8(a.x[w] + (t0 + tok[u]) * a.st[w] + head[u] * a.sh[w] + 8 * c, a.vec[w]);
+      for (int u = 0; u < U; ++u) {
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (h + u * RPW < h1) raw[u] = load8(src + (h + u * RPW) * sh, vec);
       }
+    };
+    uint4 raw[U], next[U];
+    load(raw, h0 + sub);
+    if (!have) {  // while the first rows load
+      angles<MODE>(a, turns, a.rot_dim ? a.positions[tok] : 0, c, cs);
+      have = true;
     }
+#pragma unroll 1
+    for (int h = h0 + sub; h - sub < h1; h += RPW * U) {
+      load(next, h + RPW * U);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int w = which[u];
-      float f[8];
-      to_f32<DT>(raw[u], f);
-      // rows past the end take part in the shuffles only
-      const uint4 v = row_result<DT, D, MODE>(f, a.w[w], a.w_vec[w], a.eps, a.rot_dim, cs + tok[u] * half,
-                                              MODE == kTurnHalfAny ? buf + slot * D : buf, c);
-      if (r + u * RPP < r1)
-        store8(a.y[w] + ((int64_t)(t0 + tok[u]) * a.heads[w] + head[u]) * D + 8 * c, v, a.vec[w]);
+      for (int u = 0; u < U; ++u) {
+        float f[8];
+        to_f32<DT>(raw[u], f);
+        // rows past the end take part in the shuffles only
+        row_result<DT, D, MODE>(f, norm, wt, a.eps, a.rot_dim, cs, MODE == kTurnHalfAny ? buf + (warp * RPW + sub) * D : buf, c);
+        if (h + u * RPW < h1) {
+          uint4 v;
+          v.x = pack2<DT>(f[0], f[1]);
+          v.y = pack2<DT>(f[2], f[3]);
+          v.z = pack2<DT>(f[4], f[5]);
+          v.w = pack2<DT>(f[6], f[7]);
+          store8(dst + (int64_t)(h + u * RPW) * D, v, vec);
+        }
+        raw[u] = next[u];
+      }
     }
   }
 }
@@ -335,20 +356,18 @@ kvq_status kvq_qk_norm_rope(const kvq_config* cfg, const kvq_rope_plan* plan, co
     std::memcpy(a.turns, plan->turns, sizeof(a.turns));
     if (!plan->interleaved) mode = plan->rot_dim % 16 == 0 ? kTurnHalf8 : kTurnHalfAny;
   }
-  // Rows per block: enough passes to keep loads in flight once every SM has
-  // several blocks; fewer rows (down to one pass) while blocks are scarce.
-  const int H = a.heads[0] + a.heads[1], rpp = kThreads / (cfg->D / 8);
-  const int64_t rows = (int64_t)n_tokens * H;
-  const int64_t want = (int64_t)sm_count() * 8;
-  int64_t per = rows / want;
-  per = std::max<int64_t>(rpp, std::min<int64_t>((per + rpp - 1) / rpp * rpp, 4 * rpp));
-  a.tokens_per_block = (int)std::max<int64_t>(1, per / H);
-  const int64_t block_rows = (int64_t)std::min(a.tokens_per_block, n_tokens) * H;
-  a.rows_per_block = (int)std::min<int64_t>(block_rows, a.tokens_per_block > 1 ? block_rows : per);
-  const int64_t gy = (block_rows + a.rows_per_block - 1) / a.rows_per_block;
-  if (gy > 65535) return fail(KVQ_ERR_UNSUPPORTED, "%d heads", H);
-  const dim3 grid((n_tokens + a.tokens_per_block - 1) / a.tokens_per_block, (unsigned)gy);
-  const size_t smem = sizeof(float2) * (size_t)a.tokens_per_block * (a.rot_dim / 2);
+  // Shares of a token's heads: one warp takes them all once every SM has its
+  // fill of warps (the angles are worked out once), fewer passes while warps are scarce.
+  const int H = a.heads[0] + a.heads[1], rpw = 32 / (cfg->D / 8);
+  const int64_t warps = (int64_t)sm_count() * 24;
+  int64_t shares = std::max<int64_t>(1, warps / n_tokens);
+  shares = std::min<int64_t>(shares, (H + rpw - 1) / rpw);
+  a.rows_per_share = (int)(((H + shares - 1) / shares + rpw - 1) / rpw * rpw);
+  a.shares = (H + a.rows_per_share - 1) / a.rows_per_share;
+  const int64_t blocks = ((int64_t)n_tokens * a.shares + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 0x7fffffff) return fail(KVQ_ERR_UNSUPPORTED, "%d tokens of %d heads", n_tokens, H);
+  const dim3 grid((unsigned)blocks);
+  const size_t smem = 0;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   if (cfg->in_dtype == KVQ_DT_F16)
