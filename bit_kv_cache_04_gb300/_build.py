@@ -40,6 +40,7 @@ SOURCES = [
     ("chunk_attention.cu", []),
     ("chunk_attention_d128.cu", []),
     ("chunk_attention_d256.cu", []),
+    ("chunk_attention_few.cu", []),
 ]
 
 

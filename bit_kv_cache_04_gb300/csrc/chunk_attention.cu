@@ -104,16 +104,16 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
   a.partials = (float*)((char*)workspace + w.partials);
   const int64_t rows = (int64_t)max_q * a.lo.g;
   if (rows > (int64_t)1 << 28) return fail(KVQ_ERR_UNSUPPORTED, "max_q=%d x %d heads", max_q, a.lo.g);
-  const bool paired = cfg->D == 128 && rows > 128;
-  const int tile = chunk_tile(cfg->D), row_tile = paired ? 256 : 128;
+  const int mode = cfg->D != 128 ? kChunkShared : rows <= kFewRows ? kChunkFew : rows > 128 ? kChunkPaired : kChunkShared;
+  const int tile = chunk_tile(cfg->D), row_tile = mode == kChunkPaired ? 256 : 128;
   // the kernel counts its tiles in 32 bits
   const int64_t units = ((int64_t)total_q * a.lo.g / row_tile + cfg->batch) * n_layers * cfg->H_kv;
   if (units * (cfg->max_T / tile + 2) > 0x7fffffff - 2 * w.grid)
     return fail(KVQ_ERR_UNSUPPORTED, "too many tiles for one call: pass fewer layers or rows");
   a.g_magic = (uint32_t)((1ull << 32) / a.lo.g + 1);
-  const int most = cfg->D == 128 ? 4 : 2;  // a repetition keeps at least 32 tokens of a tile
   a.turn_here = (cfg->flags & KVQ_ROTATE_K) && rows <= 64 ? 1 : 0;
-  a.rep = rows <= 32 ? most : rows <= 64 ? 2 : 1;
+  a.rep = rows <= 64 ? 2 : 1;
+  a.cols = rows <= 16 ? 16 : kFewRows;
   a.by_warp = rows > 4 * row_tile;
   // Staging: 32-token subtiles as single bulk copies; pages of fewer tokens
   // as copies of their own when their bytes are whole 16-byte words and a
@@ -134,8 +134,9 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
       a.direct = 1;
     }
   }
-  cudaError_t e = cfg->D == 128 ? launch_chunk_d128(a, paired, w.grid, (cudaStream_t)stream)
-                                : launch_chunk_d256(a, w.grid, (cudaStream_t)stream);
+  cudaError_t e = mode == kChunkFew ? launch_chunk_few(a, w.grid, (cudaStream_t)stream)
+                  : cfg->D == 128   ? launch_chunk_d128(a, mode, w.grid, (cudaStream_t)stream)
+                                    : launch_chunk_d256(a, w.grid, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention kernel");
   return ok();
 }

@@ -36,7 +36,10 @@
 
 namespace kvq {
 
-constexpr int kChunkDequantWarps = 8;  // two for each piece of a tile: K, V, two halves each
+// what a launch's rows ask of the kernel: at most 32 a sequence (D = 128); more than 128 (D = 128); else
+constexpr int kChunkShared = 0, kChunkPaired = 1, kChunkFew = 2;
+constexpr int kFewRows = 32;
+constexpr uint32_t kFewBytes = kFewRows * 128 * 2;  // of a few queries, or of their P over a tile
 constexpr int kChunkSlots = 3;       // partial slots per CTA: first cut unit, last cut unit, whole units
 constexpr int kChunkTickets = 2;     // per CTA: units whose first run is the CTA's first or last one
 constexpr int kChunkMaxSlots = 16;   // staging ring, in pieces
@@ -60,6 +63,7 @@ struct ChunkArgs {
   int total_q, max_q, window, sinks;
   int turn_here;  // rotated formats: the kernel turns the (few) queries itself; else a pass before it does
   int rep;      // repetitions of the query rows over the lanes: 1, 2, 4
+  int cols;     // few rows: columns of the products, 16 or 32
   uint32_t g_magic;  // floor(2^32 / g) + 1
   int by_warp;  // row tiles per sequence are many: count them with a warp per sequence
   int direct;       // 1: pages cannot be staged by bulk copies
@@ -75,7 +79,8 @@ struct ChunkArgs {
   uint64_t turns[128];  // pre-RoPE keys: turns per position of every pair, 64-bit fractions
 };
 
-cudaError_t launch_chunk_d128(const ChunkArgs& a, bool paired, int grid, cudaStream_t s);
+cudaError_t launch_chunk_d128(const ChunkArgs& a, int mode, int grid, cudaStream_t s);
+cudaError_t launch_chunk_few(const ChunkArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_chunk_d256(const ChunkArgs& a, int grid, cudaStream_t s);
 
 }  // namespace kvq

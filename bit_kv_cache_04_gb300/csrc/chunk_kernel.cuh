@@ -460,24 +460,18 @@ struct CachePos {
 template <int D>
 struct RunPlace {
   static constexpr int NT = chunk_tile(D), PIECE = NT / 2;
-  // run e (0..255) of a piece: first token from the piece's, row and run in the tile's first half
-  __device__ __forceinline__ static void of(bool per_channel, int e, int* toff, int* row, int* run) {
+  // run i of lane `lane` of the piece's warp `part`: first token from the piece's, row and run in the tile's first half.
+  // i steps along rows.  Per-channel: a warp takes a 32-token group (of two) or half of the channels.
+  // Per-token: four runs of a row side by side; a warp takes half of the tokens, or of the channels (D = 256).
+  __device__ __forceinline__ static void of(bool per_channel, int part, int i, int lane, int* toff, int* row, int* run) {
     if (per_channel) {
-      constexpr int G = PIECE / 32;
-      *row = (e & 7) | ((e / (8 * G)) << 3);
-      *run = (e >> 3) % G;
+      *row = i * 32 + lane + (D == 128 ? 0 : 128 * part);
+      *run = D == 128 ? part : 0;
       *toff = 32 * *run;
     } else {
-      constexpr int R = D / 32;
-      *run = (e >> 3) % R;
-      *row = *toff = (e & 7) | ((e / (8 * R)) << 3);
+      *row = *toff = (lane & 7) + 8 * i + (D == 128 ? 32 * part : 0);
+      *run = (lane >> 3) + (D == 128 ? 0 : 4 * part);
     }
-  }
-  // number in the piece of run i of lane `lane` of the piece's warp `part`: i steps along rows
-  __device__ __forceinline__ static int number(bool per_channel, int part, int i, int lane) {
-    // per-token rows of 256 channels are eight runs long: a warp takes four of them
-    if (D == 256 && !per_channel) return i * 64 + part * 32 + lane;
-    return part * 128 + i * 32 + lane;
   }
   // block and codes of a run (channel `row` of a 32-token group, or run `run` of a token) in the staged piece
   __device__ __forceinline__ static void at(bool per_channel, const RunFmt& f, int sub_bytes, int t, int row, int run,
@@ -589,13 +583,14 @@ template <int D, int DT>
 __device__ __forceinline__ void window_groups(const ChunkArgs& a, const CachePos& u, int which, int part, uint32_t dst, int tile0,
                                               int t0, int t1, int lane, volatile uint32_t* nonfinite) {
   for (int g = t0; g < t1; g += 32) {
+    if (D == 128 && ((g - tile0) >> 5 & 1) != part) continue;  // D = 128: the warp's group of the piece
     const int t = g + lane, col = t - tile0;  // column of the channel rows
     const bool in = t < u.T;
     const uint4* p = reinterpret_cast<const uint4*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, in ? t : g));
     const uint32_t blk = dst + (uint32_t)(col >> 6) * D * 128 + (col & 7) * 2;
     const int c16 = (col & 63) >> 3;
 #pragma unroll 1
-    for (int c0 = part * (D / 16); c0 < (part + 1) * (D / 16); c0 += 4) {
+    for (int c0 = D == 128 ? 0 : part * 16; c0 < (D == 128 ? 16 : part * 16 + 16); c0 += 4) {
       uint4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = p[c0 + k];
@@ -697,7 +692,7 @@ __device__ __forceinline__ void mixed_piece(const ChunkArgs& a, const CachePos& 
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     int toff, row, run;
-    RunPlace<D>::of(per_channel, RunPlace<D>::number(per_channel, part, i, lane), &toff, &row, &run);
+    RunPlace<D>::of(per_channel, part, i, lane, &toff, &row, &run);
     const int t = a0 + toff, row_t = row + (per_channel ? 0 : half * (NT / 2)), run_t = run + (per_channel ? half * (NT / 64) : 0);
     const uint32_t line = RunPlace<D>::line_at(dst, row_t, run_t, per_channel ? D : NT);
     const bool in = t >= v0 && t < v1;
@@ -928,20 +923,22 @@ __device__ __forceinline__ void copy_each(bool mine, uint32_t dst, const uint8_t
 
 // ---- the kernel ----------------------------------------------------------------------
 
-template <int D, bool PAIRED>
+template <int D, int MODE>
 struct ChunkShape {
+  static constexpr bool PAIRED = MODE == kChunkPaired, FEW = MODE == kChunkFew;
   static constexpr int NT = chunk_tile(D);
-  static constexpr int STREAMS = chunk_streams(D);
+  static constexpr int STREAMS = FEW ? 1 : chunk_streams(D);
   static constexpr int QTILES = PAIRED ? 2 : 1;
   static constexpr int RT = 128 * QTILES;  // rows of a row tile
-  static constexpr int SOFT_WARPS = 4 * STREAMS;
-  static constexpr int LOAD_WARP = SOFT_WARPS + kChunkDequantWarps, MMA_WARP = LOAD_WARP + 2;  // two loaders: K, V
+  static constexpr int SOFT_WARPS = FEW ? 8 : 4 * STREAMS;
+  static constexpr int LOAD_WARP = SOFT_WARPS + 8, MMA_WARP = LOAD_WARP + 2;  // two loaders: K, V
   static constexpr int WARPS = MMA_WARP + 1;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr uint32_t Q_BYTES = 128u * D * 2;
   static constexpr uint32_t TILE_BYTES = (uint32_t)NT * D * 2;  // 32 KiB
-  static constexpr uint32_t FIXED = 1024 + QTILES * Q_BYTES + 4 * TILE_BYTES;  // the rest of the SM's is staging
-  static constexpr uint32_t S_COL = 0, O_COL = D == 128 ? 256 : 256;
+  static constexpr uint32_t FRONT = FEW ? 4 * kFewBytes : QTILES * Q_BYTES;  // queries; FEW: two tiles' P, ones
+  static constexpr uint32_t FIXED = 1024 + FRONT + 4 * TILE_BYTES;  // the rest of the SM's is staging
+  static constexpr uint32_t S_COL = 0, O_COL = 256, L_COL = O_COL + kFewRows;  // columns of TMEM
 };
 
 struct ChunkShared {
@@ -954,6 +951,9 @@ struct ChunkShared {
   uint32_t last;  // this CTA joins the unit's partials
   LineStart start;
   Run runs[19];   // one per warp
+  Run next;       // FEW: the softmax warps' runs are here and in runs[0] in turn
+  alignas(16) float few_part[8][16], few_mneg[8][16], few_fac[8][16], few_sum[kFewRows];
+  int few_pos[8][16];
   int scan[32];
   uint32_t pair_table[256];  // TBQ4: centroids of a byte's two indices
 };
@@ -1131,12 +1131,42 @@ __device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, 
   return (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + u.h * a.lo.g + (row - tok * a.lo.g)) * a.lo.D;
 }
 
+// One output row, four channels of a 128-chunk a lane: acc / L, out of the rotated domain.  (s1, s2): the lane's signs.
+template <int D, int DT>
+__device__ __forceinline__ void write_row(const ChunkArgs& a, const Run& run, int r, float (&acc)[D / 128][4], float L, uint32_t s1,
+                                          uint32_t s2, bool fix) {
+  const int lane = threadIdx.x & 31;
+  uint16_t* dst = a.out + query_row(a, run.u, r);
+  const float inv = 1.f / L;
+#pragma unroll
+  for (int c = 0; c < D / 128; ++c) {
+    float v[4] = {acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv};
+    if (a.lo.flags & KVQ_ROTATE_V) rotate_lanes(v, s2, s1);
+    *reinterpret_cast<uint2*>(dst + 128 * c + 4 * lane) = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+    if (fix) add_nonfinite<DT>(a, run, run.u.T - run.u.n + div_g(a, run.u.r0 + r), 128 * c + 4 * lane, 4, dst);
+  }
+}
+
+// The softmax warps of FEW meet, N of them: whether p holds for any thread.  A hardware barrier, so all of them come
+// by it equally often, also when one has given up waiting for another role.
+template <int N>
+__device__ __forceinline__ bool few_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id), "n"(32 * N)
+      : "memory");
+  return r != 0;
+}
+
 // Joins the partial rows of one unit and writes its output rows; all softmax
 // threads.  scratch: 8 rows of D + 4 floats in shared memory.  False once a warp has given up.
-template <int D, int DT, bool PAIRED>
+template <int D, int DT, int MODE>
 __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, const LineStart& line, bool cut, bool fix,
                                           float* scratch, uint32_t soft, uint32_t& syncs, uint32_t* gave_up) {
-  using C = ChunkShape<D, PAIRED>;
+  using C = ChunkShape<D, MODE>;
+  constexpr bool PAIRED = C::PAIRED;
   constexpr int N = D / 128;
   constexpr int PR = chunk_part_row(D), SLOT = chunk_slot_rows(D) * PR;
   const Unit& u = run.u;
@@ -1145,26 +1175,17 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
   const int c0 = cut ? unit_pos / line.per_cta : blockIdx.x;
   const int c1 = cut ? (unit_pos + u.nt - 1) / line.per_cta : blockIdx.x;
   const int slot0 = !cut ? 2 : unit_pos == c0 * line.per_cta ? 0 : 1;  // of the first CTA; the others' is 0
-  const int copies = PAIRED ? 1 : C::STREAMS * a.rep;  // partial rows of one query row in one slot
-  const int rep_log = a.rep == 4 ? 2 : a.rep - 1, copies_log = PAIRED ? 0 : rep_log + C::STREAMS - 1;
+  constexpr bool ONE = PAIRED || C::FEW;
+  const int copies = ONE ? 1 : C::STREAMS * a.rep;  // partial rows of one query row in one slot
+  const int rep_log = a.rep == 4 ? 2 : a.rep - 1, copies_log = ONE ? 0 : rep_log + C::STREAMS - 1;
   const int parts = (c1 - c0 + 1) * copies;
   auto part = [&](int i, int r) {
     // copy k of a slot: stream k / rep (128 rows each), repetition k % rep (128 / rep rows each)
-    const int c = i >> copies_log, row = PAIRED ? r : ((i & (copies - 1)) << (7 - rep_log)) + r;
+    const int c = i >> copies_log, row = ONE ? r : ((i & (copies - 1)) << (7 - rep_log)) + r;
     return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
   const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
-  auto write = [&](int r, float (&acc)[N][4], float L) {
-    uint16_t* dst = a.out + query_row(a, u, r);
-    const float inv = 1.f / L;
-#pragma unroll
-    for (int c = 0; c < N; ++c) {
-      float v[4] = {acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv};
-      if (a.lo.flags & KVQ_ROTATE_V) rotate_lanes(v, s2, s1);
-      *reinterpret_cast<uint2*>(dst + 128 * c + 4 * lane) = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
-      if (fix) add_nonfinite<DT>(a, run, u.T - u.n + div_g(a, u.r0 + r), 128 * c + 4 * lane, 4, dst);
-    }
-  };
+  auto write = [&](int r, float (&acc)[N][4], float L) { write_row<D, DT>(a, run, r, acc, L, s1, s2, fix); };
   if (PAIRED && parts <= 4) {
     // Many rows of few parts: a lane works out the weights of one row of the
     // warp's 32; then row by row, the next row's loads in flight.
@@ -1274,7 +1295,10 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
       for (int c = 0; c < N; ++c)
         *reinterpret_cast<float4*>(mine + 128 * c + 4 * lane) = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
       if (lane == 0) mine[D] = L;
-      if (!soft_sync(soft, syncs, gave_up)) return false;
+      if constexpr (C::FEW)
+        (void)few_any<8>(3, false);
+      else if (!soft_sync(soft, syncs, gave_up))
+        return false;
       if (sub) continue;  // one turn: fewer rows than warps
 #pragma unroll 1
       for (int k = 1; k < wpr; ++k) {
@@ -1421,16 +1445,295 @@ __device__ __forceinline__ void rescale_columns(uint32_t o_col, float f) {
   tmem_wait_st();
 }
 
-template <int D, int DT, bool PAIRED>
-__global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
+// ---- few rows ------------------------------------------------------------------------
+// At most 32 query rows a sequence, D = 128: the products are turned over, S^T = K Q^T and O^T = V^T P^T, so that
+// the rows are columns (16 or 32 of them) and not lanes: both products cost a quarter or an eighth, and the
+// accumulator, its rescaling and its output shrink with them.  A thread holds one token of a tile, then
+// one channel of the output; P goes through shared memory.  The rows' reference maxima are common to
+// the four warps: lane r of each of them holds row r's.
+
+// A run's queries into shared memory (row r of 64 channels a block of kFewBytes / 2), a warp a row.
+template <int DT>
+__device__ __forceinline__ void few_queries(const ChunkArgs& a, const Unit& u, uint32_t q_at, int w, int lane) {
+  const bool turn = a.lo.flags & KVQ_ROTATE_K;
+  const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
+  const int rows = u.rows, ch = 4 * lane;
+  const uint32_t col = q_at + (uint32_t)(ch >> 6) * (kFewBytes / 2) + (ch & 4) * 2;
+  uint2 x = make_uint2(0, 0);
+  if (w < rows) x = __ldcg(reinterpret_cast<const uint2*>(a.q + query_row(a, u, w)) + lane);
+#pragma unroll 1
+  for (int r = w; r < rows; r += 8) {
+    uint2 next = x;
+    if (r + 8 < rows) next = __ldcg(reinterpret_cast<const uint2*>(a.q + query_row(a, u, r + 8)) + lane);
+    if (turn) {
+      float v[4] = {in_to_f32((uint16_t)x.x, DT), in_to_f32((uint16_t)(x.x >> 16), DT), in_to_f32((uint16_t)x.y, DT),
+                    in_to_f32((uint16_t)(x.y >> 16), DT)};
+      rotate_lanes(v, s1, s2);
+      x = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+    }
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(col + swz(r, (ch & 63) >> 3)), "r"(x.x), "r"(x.y) : "memory");
+    x = next;
+  }
+  proxy_fence();
+  __syncwarp();
+}
+
+// Over the warp's lanes, row by row: lane r and lane r + 16 get row r's maximum.
+__device__ __forceinline__ float max_across(float (&x)[16], int lane) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float give = up ? x[i] : x[i + o], keep = up ? x[i + o] : x[i], got = __shfl_xor_sync(0xffffffffu, give, o);
+      x[i] = fmaxf(keep, got);
+    }
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, x[0], 16);
+  return fmaxf(x[0], got);
+}
+
+// The softmax warps' work of FEW: two groups of four warps, 16 rows each.
+template <int DT>
+__device__ __forceinline__ void few_rows(const ChunkArgs& a, ChunkShared& sh, bool more, uint8_t* smem, uint32_t tmem) {
+  constexpr int D = 128, NT = 128, PR = chunk_part_row(D);
+  using C = ChunkShape<D, kChunkFew>;
+  const int lane = threadIdx.x & 31;
+  int w = threadIdx.x >> 5;
+  asm volatile("" : "+r"(w));
+  const int quad = w & 3, row0 = (w >> 2) * 16;  // rows [row0, row0 + 16)
+  const int my = 32 * quad + lane;               // token of a tile; channel of the output
+  const uint32_t q_at = smem_addr(smem), lane_base = tmem + ((uint32_t)(32 * quad) << 16) + row0, o_col = lane_base + C::O_COL;
+  const float sc = 1.4426950408889634f * rsqrtf((float)D);
+  uint32_t* const gave_up = &sh.gave_up;
+  float* const mneg = sh.few_mneg[w];  // minus the references
+  float* const fac = sh.few_fac[w];
+  int* const pos = sh.few_pos[w];
+  float* const stage = reinterpret_cast<float*>(smem + kFewBytes);  // outputs [row][channel], where P was
+  // this thread's token in P: row r's 64 tokens are 128 bytes, their 16-byte parts swizzled by r mod 8
+  const uint32_t p_at = q_at + kFewBytes + (uint32_t)(my >> 6) * (kFewBytes / 2) + row0 * 128 + (my & 63) * 2;
+  uint32_t ns0 = 0, ns1 = 0, runs = 0, steps = 0, syncs = 0;
+  asm volatile("" : "+r"(ns0), "+r"(ns1), "+r"(runs), "+r"(steps));
+  // the warps follow one run: their barriers must match whatever the lengths in memory do meanwhile
+  Run *now = &sh.runs[0], *after = &sh.next;
+  more = few_any<8>(3, w == 0 && more);
+  if (more) {
+    few_queries<DT>(a, now->u, q_at, w, lane);
+    if (lane == 0) bar_arrive(smem_addr(&sh.q_full[0]));
+  }
+  while (more) {
+    const Run& run = *now;
+    const int rows = run.u.rows - row0, t0 = run.t0, t1 = run.t1;  // the group's: 16 or fewer, none
+    bool ok = true;
+    // row row0 + lane's reference (+inf past the rows: it never moves); and minus all rows'
+    float m = lane < rows ? -INFINITY : INFINITY;
+    if (row0 < a.cols) {
+      const int st = run.u.st, skip = run.u.lo_tile - st, p_lo = run.u.p_lo, p_hi = run.u.p_hi;
+      float n[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) n[r] = r < rows ? INFINITY : -INFINITY;
+      __syncwarp();
+      if (lane < 16) pos[lane] = run.u.T - run.u.n + div_g(a, min(row0 + lane, run.u.rows - 1));
+      __syncwarp();
+#pragma unroll 1
+      for (int j = t0; j < t1; ++j, ++steps) {
+        const int b = (j - t0) & 1, tile0 = (j < st ? j : j + skip) * NT;
+        const uint32_t s_col = lane_base + C::S_COL + b * kFewRows;
+        const bool here = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
+        ns0 += b ^ 1;
+        ns1 += b;
+        const bool masked = tile0 + NT - 1 > p_lo || (a.window && tile0 <= p_hi - a.window && tile0 + NT > a.sinks);
+        // -inf where this thread's token is out of a row's view
+        auto hide = [&](float (&x)[16]) {
+          const int t = tile0 + my, window = a.window ? a.window : 1 << 30;
+          const bool sink = t < a.sinks;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int p = pos[i];
+            if (t > p || (t <= p - window && !sink)) x[i] = -INFINITY;
+          }
+        };
+        // log2 P
+        auto powers = [&](float (&x)[16]) {
+          uint32_t s16[16];
+          tmem_ld16(s_col, s16);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(s16[i]), sc, n[i]);
+          if (masked) hide(x);
+        };
+        float x[16], most = -INFINITY;
+        if (here) {
+          tc_fence_after();
+          powers(x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) most = fmaxf(most, x[i]);
+        }
+        // The references follow when some score passes its row's by 2^8 (P stays below 2^8; a row that has seen
+        // nothing has the reference -inf): then the group's all go to their rows' maxima so far and the accumulator is
+        // rescaled.  References are whole numbers: factors are powers of two, and P rounds alike whatever the reference.
+        if (few_any<4>(1 + (w >> 2), most > 8.f || !here)) {
+          if (here) {
+            uint32_t s16[16];
+            tmem_ld16(s_col, s16);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(s16[i]);
+            if (masked) hide(x);
+            const float top = max_across(x, lane) * sc;
+            if (lane < 16) sh.few_part[w][lane] = top;
+          }
+          // the products of the step before must have left the accumulator
+          const bool left = here && (j == t0 || __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.pv_done), (steps - 1) & 1, gave_up)));
+          if (few_any<4>(1 + (w >> 2), !left)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float top = m;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = fmaxf(top, floorf(sh.few_part[(w & 4) + k][lane & 15]));
+          if (lane < 16) {
+            fac[lane] = top == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
+            mneg[lane] = -top;
+          }
+          m = top;
+          __syncwarp();
+          if (j > t0) {
+#pragma unroll 1
+            for (int c = 0; c < 2 * kFewRows; c += kFewRows) {  // outputs, then sums
+              uint32_t o[16];
+              tmem_ld16(o_col + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[i]);
+              tmem_st16(o_col + c, o);
+            }
+            tmem_wait_st();
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(mneg + i);
+            n[i] = v.x;
+            n[i + 1] = v.y;
+            n[i + 2] = v.z;
+            n[i + 3] = v.w;
+          }
+          powers(x);
+          __syncwarp();
+        }
+        // P, eight rows at a time (that of the columns behind the last rows is what it was)
+        const uint32_t p_row = p_at + b * kFewBytes;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (8 * q < rows) {
+            uint32_t p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = pack16<DT>(ex2(x[q * 8 + 2 * i]), ex2(x[q * 8 + 2 * i + 1]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // rows 8 q + 2 i and the next: 2 i and 2 i + 1 are their swizzles
+              asm volatile("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n st.shared.b16 [%0], lo;\n st.shared.b16 [%1], hi;\n}\n" ::"r"(
+                               (p_row ^ (32 * i)) + (8 * q + 2 * i) * 128),
+                           "r"((p_row ^ (32 * i + 16)) + (8 * q + 2 * i + 1) * 128), "r"(p[i]));
+          }
+        proxy_fence();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&sh.p_full[b]));
+      }
+    }
+    // ---- the run's outputs ---------------------------------------------------------------
+    const bool here = ok && __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.o_full), runs & 1, gave_up));
+    if (few_any<8>(3, !here)) break;
+    ++runs;
+    tc_fence_after();
+    // the next run's queries first: its scores are worked out meanwhile
+    static_assert(sizeof(Run) % 4 == 0 && sizeof(Run) <= 128, "a word a lane");
+    if (w == 0) {
+      if (lane < (int)sizeof(Run) / 4) reinterpret_cast<int*>(after)[lane] = reinterpret_cast<const int*>(now)[lane];
+      more = warp_run<D, 128>(a, sh.start, *after, 1);
+    }
+    more = few_any<8>(3, w == 0 && more);
+    if (more) {
+      few_queries<DT>(a, after->u, q_at, w, lane);
+      if (lane == 0) bar_arrive(smem_addr(&sh.q_full[0]));
+    }
+    uint32_t x[16];
+    float L = 0.f;  // row row0 + lane's sum, from TMEM lane 0
+    if (quad == 0 && rows > 0) {
+      tmem_ld16(lane_base + C::L_COL, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float v = __uint_as_float(__shfl_sync(0xffffffffu, x[i], 0));
+        if (lane == i) L = v;
+      }
+    }
+    if (rows > 0) {
+      tmem_ld16(o_col, x);
+      tmem_wait_ld();
+    }
+    if (t0 == 0 && t1 == run.u.nt) {
+      if (rows > 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) stage[(row0 + i) * D + my] = __uint_as_float(x[i]);
+        if (quad == 0 && lane < 16) sh.few_sum[row0 + lane] = L;
+      }
+      (void)few_any<8>(3, false);
+      const bool fix = *(volatile uint32_t*)&sh.nonfinite != 0;
+      const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
+#pragma unroll 1
+      for (int r = w; r < run.u.rows; r += 8) {
+        const float4 v = *reinterpret_cast<const float4*>(stage + r * D + 4 * lane);
+        float acc[1][4] = {{v.x, v.y, v.z, v.w}};
+        write_row<D, DT>(a, run, r, acc, sh.few_sum[r], s1, s2, fix);
+      }
+    } else {
+      float* part = a.partials + ((int64_t)blockIdx.x * kChunkSlots + (run.first ? 0 : 1)) * chunk_slot_rows(D) * PR + row0 * PR;
+      if (quad == 0 && lane < min(rows, 16)) *reinterpret_cast<float2*>(part + lane * PR + D) = make_float2(m, L);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < rows) part[i * PR + my] = __uint_as_float(x[i]);
+      __threadfence();
+      (void)few_any<8>(3, false);
+      const int unit_pos = run.pos - t0, c0 = unit_pos / sh.start.per_cta;  // the unit's ticket: as below
+      const int tick = c0 * kChunkTickets + (unit_pos == c0 * sh.start.per_cta ? 0 : 1);
+      bool last = false;
+      if (w == 0 && lane == 0) {
+        if (*(volatile uint32_t*)&sh.nonfinite) atomicOr(a.nonfinite + tick, 1u);
+        __threadfence();
+        last = atomicAdd(a.tickets + tick, 1u) == (uint32_t)((unit_pos + run.u.nt - 1) / sh.start.per_cta - c0);
+      }
+      if (few_any<8>(3, last)) {
+        __threadfence();
+        const bool fix = __ldcg(a.nonfinite + tick) != 0;
+        (void)join_unit<D, DT, kChunkFew>(a, run, sh.start, true, fix, stage, 0, syncs, gave_up);
+        (void)few_any<8>(3, false);
+        if (w == 0 && lane == 0) {
+          a.tickets[tick] = 0;
+          a.nonfinite[tick] = 0;
+        }
+      }
+    }
+    // (the next P over the staged outputs: behind the next run's first barriers)
+    (void)few_any<8>(3, false);
+    Run* const t = now;
+    now = after;
+    after = t;
+  }
+}
+
+template <int D, int DT, int MODE>
+__global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkArgs a) {
-  using C = ChunkShape<D, PAIRED>;
+  using C = ChunkShape<D, MODE>;
+  constexpr bool PAIRED = C::PAIRED, FEW = C::FEW;
   constexpr int NT = C::NT, RT = C::RT;
   extern __shared__ uint8_t raw_smem[];
   __shared__ ChunkShared sh;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
-  const uint32_t q_at = smem_addr(smem), k_at = q_at + C::QTILES * C::Q_BYTES, v_at = k_at + 2 * C::TILE_BYTES;
+  const uint32_t q_at = smem_addr(smem), k_at = q_at + C::FRONT, v_at = k_at + 2 * C::TILE_BYTES;
   const uint32_t raw_at = v_at + 2 * C::TILE_BYTES;
 
   // set-up that needs nothing of the stream's earlier work
@@ -1443,13 +1746,13 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   if (tid == 0) {
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      bar_init(smem_addr(&sh.k_full[i]), kChunkDequantWarps / 2);
-      bar_init(smem_addr(&sh.v_full[i]), kChunkDequantWarps / 2);
+      bar_init(smem_addr(&sh.k_full[i]), 4);
+      bar_init(smem_addr(&sh.v_full[i]), 4);
       bar_init(smem_addr(&sh.k_empty[i]), 1);
       bar_init(smem_addr(&sh.v_empty[i]), 1);
-      bar_init(smem_addr(&sh.q_full[i]), 4);
+      bar_init(smem_addr(&sh.q_full[i]), FEW ? 8 : 4);
       bar_init(smem_addr(&sh.s_full[i]), 1);
-      bar_init(smem_addr(&sh.p_full[i]), 4);
+      bar_init(smem_addr(&sh.p_full[i]), FEW ? a.cols / 4 : 4);
     }
     bar_init(smem_addr(&sh.o_full), 1);
     bar_init(smem_addr(&sh.pv_done), 1);
@@ -1465,8 +1768,13 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
   }
   // query rows that no unit writes are zeros
 #pragma unroll 1
-  for (uint32_t e = tid * 16; e < C::QTILES * C::Q_BYTES; e += C::THREADS * 16)
+  for (uint32_t e = tid * 16; e < (FEW ? 3 * kFewBytes : C::FRONT); e += C::THREADS * 16)
     *reinterpret_cast<uint4*>(smem + e) = make_uint4(0, 0, 0, 0);
+  if constexpr (FEW) {  // 64 rows of 64 ones
+    constexpr uint32_t one = DT == KVQ_DT_F16 ? 0x3c003c00u : 0x3f803f80u;
+    for (uint32_t e = tid * 16; e < kFewBytes; e += C::THREADS * 16)
+      *reinterpret_cast<uint4*>(smem + 3 * kFewBytes + e) = make_uint4(one, one, one, one);
+  }
   if (a.lo.flags & (KVQ_TBQ4_K | KVQ_TBQ4_V))
     for (int i = tid; i < 256; i += C::THREADS) {
       const __half2 p = __floats2half2_rn(a.lo.cb[i & 15], a.lo.cb[i >> 4]);
@@ -1489,8 +1797,11 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
     // ---- products: one thread ----------------------------------------------------
     constexpr uint32_t F = DT == KVQ_DT_F16 ? 0 : 1;
     constexpr uint32_t base = (1u << 4) | (F << 7) | (F << 10) | ((128u >> 4) << 24);
-    const uint32_t qk_desc = base | ((uint32_t)k_chan << 16) | ((uint32_t)(NT >> 3) << 17);
-    const uint32_t pv_desc = base | ((uint32_t)!v_chan << 16) | ((uint32_t)(D >> 3) << 17);
+    // FEW: keys and values are the left operands, the rows the columns of both products
+    const uint32_t qk_desc = base | ((uint32_t)k_chan << (FEW ? 15 : 16)) | ((uint32_t)((FEW ? a.cols : NT) >> 3) << 17);
+    const uint32_t pv_desc = base | ((uint32_t)!v_chan << (FEW ? 15 : 16)) | ((uint32_t)((FEW ? a.cols : D) >> 3) << 17);
+    const uint64_t p_desc = operand_desc(q_at + kFewBytes, 0, 1024), one_desc = operand_desc(q_at + 3 * kFewBytes, 0, 1024);
+    const uint32_t sum_desc = (base & 0xffffffu) | ((64u >> 4) << 24) | ((uint32_t)(a.cols >> 3) << 17);
     const uint64_t q_desc = operand_desc(q_at, 0, 1024), k_desc = operand_desc(k_at, k_chan ? D * 128 : 0, 1024),
                    v_desc = operand_desc(v_at, v_chan ? 0 : NT * 128, 1024);
     uint32_t kt = 0;             // tiles of this CTA so far
@@ -1507,7 +1818,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
           const bool scores = i < 2 || (i & 1);
           if (s >= steps) continue;
           const uint32_t t = kt + (PAIRED ? s >> 1 : s), st = t & 1, b = s & 1;
-          const uint32_t s_col = tmem + C::S_COL + b * NT;
+          const uint32_t s_col = tmem + C::S_COL + b * (FEW ? kFewRows : NT);
           if (scores) {
             if (s < C::QTILES) ok = bar_wait(smem_addr(&sh.q_full[s]), runs & 1, gave_up);
             ok = __all_sync(0xffffffffu, ok && bar_wait(smem_addr(&sh.k_full[st]), (t >> 1) & 1, gave_up));
@@ -1516,7 +1827,12 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
             // descriptors differ in their address alone: steps of 16 summed values
             const uint64_t da = q_desc + (PAIRED ? b * (C::Q_BYTES >> 4) : 0), db = k_desc + st * (C::TILE_BYTES >> 4);
             if (elect_one()) {
-              if (k_chan) {
+              if constexpr (FEW) {
+                const uint64_t dk = k_chan ? 128 : 2, dk4 = k_chan ? 512 : NT * 8;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                  mma_ss(s_col, db + (k >> 2) * dk4 + (k & 3) * dk, da + (k >> 2) * (kFewBytes >> 5) + (k & 3) * 2, qk_desc, k > 0);
+              } else if (k_chan) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                   mma_ss(s_col, da + (k >> 2) * 1024 + (k & 3) * 2, db + k * 128, qk_desc, k > 0);
@@ -1541,7 +1857,17 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
             const uint32_t o = tmem + C::O_COL + (C::STREAMS == 2 ? b * D : 0);
             const bool add = C::STREAMS == 2 ? s >= 2 : s > 0;
             if (elect_one()) {
-              if (v_chan) {
+              if constexpr (FEW) {
+                const uint64_t dv = v_chan ? 2 : 128, dv4 = v_chan ? D * 8 : 512, dp = p_desc + b * (kFewBytes >> 4);
+#pragma unroll
+                for (int k = 0; k < NT / 16; ++k)
+                  mma_ss(o, db + (k >> 2) * dv4 + (k & 3) * dv, dp + (k >> 2) * (kFewBytes >> 5) + (k & 3) * 2, pv_desc,
+                         add || k > 0);
+                // the rows' sums of P, in every lane
+#pragma unroll
+                for (int k = 0; k < NT / 16; ++k)
+                  mma_ss(tmem + C::L_COL, one_desc, dp + (k >> 2) * (kFewBytes >> 5) + (k & 3) * 2, sum_desc, add || k > 0);
+              } else if (v_chan) {
 #pragma unroll
                 for (int k = 0; k < NT / 16; ++k)
                   mma_ts(o, s_col + k * 8, db + (k >> 2) * (D * 8) + (k & 3) * 2, pv_desc, add || k > 0);
@@ -1663,44 +1989,39 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         PiecePlace q;
         {
           int toff, row, run32;
-          RunPlace<D>::of(per_channel, RunPlace<D>::number(per_channel, part, 0, lane), &toff, &row, &run32);
+          RunPlace<D>::of(per_channel, part, 0, lane, &toff, &row, &run32);
           RunPlace<D>::at(per_channel, f, a.sub_bytes, toff, row, run32, &q.blk, &q.codes);
-          q.step = per_channel ? (D == 128 ? 16 : 32) * f.bb : 8 * f.row;
-          q.line_step = (per_channel ? (D == 128 ? 16 : 32) : 8) * 128;
+          q.step = per_channel ? 32 * f.bb : 8 * f.row;
+          q.line_step = (per_channel ? 32 : 8) * 128;
           const int tile_row = row + (per_channel ? 0 : half * (NT / 2)), tile_run = run32 + (per_channel ? half * (NT / 64) : 0);
           q.line = RunPlace<D>::line_at(which ? v_at : k_at, tile_row, tile_run, per_channel ? D : NT);
 #pragma unroll
           for (int k = 0; k < 4; ++k) q.piece16[k] = (((tile_run & 1) * 4 + k) ^ (row & 7)) << 4;
         }
         bool landed = false;
+        // tiles behind the window's first lie in one format and in view up to this token (to whole 32-token subtiles)
+        const int st0 = run.u.st, safe = min(cold ? ce : qe, run.u.p_hi + 32);
+        auto stretch = [&](auto fill) {
+        int a1 = 1 << 30;  // the piece's end
 #pragma unroll 1
         for (; j < j1; ++j, ++kt) {
           const uint32_t st = kt & 1, bar = kt & (kChunkBars - 1);
-          const TileTokens tt = tile_tokens<D>(run.u, j);
-          const int a0 = tt.t0 + half * (NT / 2), a1 = a0 + NT / 2;
-          if ((a0 < ce) != cold) break;  // the other tier's format
+          bool plain = true;
+          a1 += NT;
+          if (j <= st0 || a1 > safe) {
+            const TileTokens tt = tile_tokens<D>(run.u, j);
+            const int a0 = tt.t0 + half * (NT / 2);
+            a1 = a0 + NT / 2;
+            if ((a0 < ce) != cold) break;  // the other tier's format
+            // of one format, wholly in view (to whole 32-token subtiles) and in range: the common case
+            plain = a0 + 31 >= tt.v0 && a1 - 31 <= tt.v1 && a1 <= qe && (!cold || a1 <= ce);
+          }
           ok = __all_sync(0xffffffffu, bar_wait(empty_at + 8 * st, ((kt >> 1) & 1) ^ 1, gave_up) &&
                                            bar_wait(full_at + 8 * bar, kt / kChunkBars & 1, gave_up));
           if (!ok) break;
           landed = true;
-          // a piece of one format, wholly in view (to whole 32-token subtiles) and in range: the common case
-          const uint32_t bad = *(volatile uint32_t*)&sh.bad_pages[piece * kChunkBars + bar];
-          if (!(a0 + 31 >= tt.v0 && a1 - 31 <= tt.v1 && a1 <= qe && (!cold || a1 <= ce) && !bad)) break;
-          const uint32_t staged = raw_at + slot * a.slot_bytes, dst = st * C::TILE_BYTES;
-          bool done = false;
-          if (kind == 4)
-            done = fill_piece<DT, 4, false>(q, staged, dst);
-          else if (kind == 8)
-            done = fill_piece<DT, 8, false>(q, staged, dst);
-          else if (kind == 2)
-            done = fill_piece<DT, 2, false>(q, staged, dst);
-          else if (kind == 3)
-            done = fill_piece<DT, 3, false>(q, staged, dst);
-          else if (kind == 20)
-            done = fill_piece<DT, 4, true>(q, staged, dst);
-          else if (kind == 18)
-            done = fill_piece<DT, 2, true>(q, staged, dst);
-          if (!done) break;
+          if (!plain || *(volatile uint32_t*)&sh.bad_pages[piece * kChunkBars + bar]) break;
+          if (!fill(raw_at + slot * a.slot_bytes, st * C::TILE_BYTES)) break;
           proxy_fence();
           __syncwarp();
           if (lane == 0) {
@@ -1711,6 +2032,22 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
           while (slot >= slots) slot -= slots;
           landed = false;
         }
+        };
+        // (a loop a format: the formats' branches are outside of it)
+        if (kind == 4)
+          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 4, false>(q, staged, dst); });
+        else if (kind == 8)
+          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 8, false>(q, staged, dst); });
+        else if (kind == 2)
+          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 2, false>(q, staged, dst); });
+        else if (kind == 3)
+          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 3, false>(q, staged, dst); });
+        else if (kind == 20)
+          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 4, true>(q, staged, dst); });
+        else if (kind == 18)
+          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 2, true>(q, staged, dst); });
+        else
+          stretch([&](uint32_t, uint32_t) { return false; });
         if (!ok || j >= j1) break;
         if (landed) {
           cold_piece<D, DT>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j);
@@ -1727,6 +2064,8 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
         }
       }
     }
+  } else if constexpr (FEW) {
+    few_rows<DT>(a, sh, more, smem, tmem);
   } else {
     // ---- softmax and outputs -----------------------------------------------------------
     uint32_t ns0 = 0, ns1 = 0, runs = 0, steps_done = 0, syncs = 0;
@@ -1935,7 +2274,7 @@ __global__ void __launch_bounds__(ChunkShape<D, PAIRED>::THREADS, 1)
           fix = *(volatile uint32_t*)&sh.nonfinite != 0;
         }
         // (the queries' shared memory is free: the run's products are done)
-        if (join && !(ok = join_unit<D, DT, PAIRED>(a, run, sh.start, cut, fix, reinterpret_cast<float*>(smem), soft, syncs, gave_up)))
+        if (join && !(ok = join_unit<D, DT, MODE>(a, run, sh.start, cut, fix, reinterpret_cast<float*>(smem), soft, syncs, gave_up)))
           break;
         if (!(ok = soft_sync(soft, syncs, gave_up))) break;
         if (join && cut && tid == 0) {
@@ -1998,9 +2337,9 @@ __global__ void __launch_bounds__(256) turn_queries_kernel(const __grid_constant
   }
 }
 
-template <int D, int DT, bool PAIRED>
+template <int D, int DT, int MODE>
 cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
-  using C = ChunkShape<D, PAIRED>;
+  using C = ChunkShape<D, MODE>;
   // all of the SM's shared memory that the tiles leave is staging
   const uint32_t all = 227 * 1024 - (uint32_t)sizeof(ChunkShared);
   const uint32_t left = all - C::FIXED - 16;
@@ -2016,10 +2355,10 @@ cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
     a.q = a.out;
   }
   // set on every call: the attribute belongs to the current device
-  e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, PAIRED>,
+  e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, MODE>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_attention_kernel<D, DT, PAIRED>, dim3(grid), dim3(C::THREADS), smem, s, a);
+  return launch_dependent(chunk_attention_kernel<D, DT, MODE>, dim3(grid), dim3(C::THREADS), smem, s, a);
 }
 
 }  // namespace

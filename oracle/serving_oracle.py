@@ -157,7 +157,8 @@ def chunk_attention(cfg: O.Config, bufs: Dict[str, np.ndarray], layer: int, q: n
       ds_j = (key_roundings u + 2^-24 D + 2^-20) sum_c |q_c k_jc| / sqrt(D)
     (keys rounded to the dtype, rotated queries too, fp32 sums, the base-2
     exponent), a probability by the factor exp(ds_j + max ds), rounded once
-    (u), a value once or twice (2 u), the output once (u |o|)."""
+    (u), a value once or twice (2 u), the output once (u |o|).  The sum l may be taken of the
+    rounded probabilities: off by u l at most, which is u |o| <= u sum_j p_j |v_j| of the output."""
     g, D = cfg.H_q // cfg.H_kv, cfg.D
     u = 2.0 ** -11 if cfg.in_dtype == 0 else 2.0 ** -8
     out = np.full(q.shape, np.nan)
@@ -195,8 +196,9 @@ def chunk_attention(cfg: O.Config, bufs: Dict[str, np.ndarray], layer: int, q: n
                     if cfg.in_dtype == 0:
                         # P in fp16 is counted from a reference no larger than the row's
                         # maximum, so the row's largest P, and with it l, is at least 1; below
-                        # 2^-14 P rounds to multiples of 2^-24: half of one per token
-                        e = e + 2.0 ** -25 * va[see].sum(0)
+                        # 2^-14 P rounds to multiples of 2^-24: half of one per token, in the sum l too
+                        oa = np.abs(stored(o, cfg.flags & O.ROTATE_V))
+                        e = e + 2.0 ** -25 * (va[see].sum(0) + len(va[see]) * oa)
                     if cfg.flags & O.ROTATE_V:  # errors of the rotated domain spread over the block
                         e = np.repeat(np.sqrt(np.sum(e.reshape(g, -1, 128) ** 2, -1)), 128, -1)
                     bound[cu_q[b] + i, h * g:(h + 1) * g] = e + u * np.abs(o) + 2.0 ** -24
