@@ -1,6 +1,8 @@
 // The chunk attention kernel (design in chunk_attention.cuh).
 #pragma once
 
+#include <type_traits>
+
 #include "chunk_attention.cuh"
 
 namespace kvq {
@@ -878,8 +880,8 @@ struct Loader {
     if (!a.lo.paged || c >= (PIECE >> a.copy_shift) || t >= u.qe) return -1;
     return __ldg(a.cp.block_table + (int64_t)u.b * a.lo.max_pages + t / a.lo.pt);
   }
-  // source and bytes of copy c (0 bytes: nothing to copy)
-  __device__ __forceinline__ int source(const ChunkArgs& a, const CachePos& u, const TileTokens& tt, int c, int pid,
+  // source and bytes of copy c of a piece (0 bytes: nothing to copy)
+  __device__ __forceinline__ int source(const ChunkArgs& a, const CachePos& u, const TileTokens& tt, int half, int c, int pid,
                                         const uint8_t** src, int* at, bool* bad) const {
     const int t = tt.t0 + half * PIECE + (c << a.copy_shift), sub = t & ~31;
     if (c >= (PIECE >> a.copy_shift) || t >= u.qe || sub + 32 <= tt.v0 || sub >= tt.v1) return 0;
@@ -902,30 +904,23 @@ struct Loader {
   }
 };
 
-// The lanes' bulk copies, one after the other with uniform operands (see elect_one).
-__device__ __forceinline__ void copy_each(bool mine, uint32_t dst, const uint8_t* src, int bytes, uint32_t bar) {
-  const uint64_t from = reinterpret_cast<uint64_t>(src);
-  uint32_t todo = __ballot_sync(0xffffffffu, mine);
-#pragma unroll 1
-  while (todo) {
-    const int c = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const uint32_t d = __shfl_sync(0xffffffffu, dst, c), n = __shfl_sync(0xffffffffu, (uint32_t)bytes, c),
-                   b = __shfl_sync(0xffffffffu, bar, c);
-    const uint64_t f = __shfl_sync(0xffffffffu, from, c);
-    if (elect_one())
-      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(d),
-                   "l"(f), "r"(n), "r"(b)
-                   : "memory");
-    __syncwarp();
-  }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, uint32_t src_lo, uint32_t src_hi, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .b64 src;\n mov.b64 src, {%1, %2};\n"
+      " cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [src], %3, [%4];\n}\n" ::"r"(dst),
+      "r"(src_lo), "r"(src_hi), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 // ---- the kernel ----------------------------------------------------------------------
 
+struct ChunkShared;
+struct FewShared;
+
 template <int D, int MODE>
 struct ChunkShape {
   static constexpr bool PAIRED = MODE == kChunkPaired, FEW = MODE == kChunkFew;
+  using Shared = std::conditional_t<FEW, FewShared, ChunkShared>;
   static constexpr int NT = chunk_tile(D);
   static constexpr int STREAMS = FEW ? 1 : chunk_streams(D);
   static constexpr int QTILES = PAIRED ? 2 : 1;
@@ -936,9 +931,10 @@ struct ChunkShape {
   static constexpr int THREADS = 32 * WARPS;
   static constexpr uint32_t Q_BYTES = 128u * D * 2;
   static constexpr uint32_t TILE_BYTES = (uint32_t)NT * D * 2;  // 32 KiB
-  static constexpr uint32_t FRONT = FEW ? 4 * kFewBytes : QTILES * Q_BYTES;  // queries; FEW: two tiles' P, ones
+  static constexpr uint32_t FRONT = FEW ? 3 * kFewBytes : QTILES * Q_BYTES;  // queries; FEW: and two tiles' P
   static constexpr uint32_t FIXED = 1024 + FRONT + 4 * TILE_BYTES;  // the rest of the SM's is staging
-  static constexpr uint32_t S_COL = 0, O_COL = 256, L_COL = O_COL + kFewRows;  // columns of TMEM
+  static constexpr uint32_t S_COL = 0, O_COL = 256, L_COL = O_COL + kFewRows,
+                            ONE_COL = L_COL + kFewRows;  // columns of TMEM
 };
 
 struct ChunkShared {
@@ -951,11 +947,15 @@ struct ChunkShared {
   uint32_t last;  // this CTA joins the unit's partials
   LineStart start;
   Run runs[19];   // one per warp
-  Run next;       // FEW: the softmax warps' runs are here and in runs[0] in turn
-  alignas(16) float few_part[8][16], few_mneg[8][16], few_fac[8][16], few_sum[kFewRows];
-  int few_pos[8][16];
+  uint4 orders[2][32];  // the loaders' copies: source, place, bytes
   int scan[32];
   uint32_t pair_table[256];  // TBQ4: centroids of a byte's two indices
+};
+
+struct FewShared : ChunkShared {
+  Run next;  // the softmax warps' runs are here and in runs[0] in turn
+  alignas(16) float few_part[8][16], few_mneg[8][16], few_fac[8][16], few_sum[kFewRows];
+  int few_pos[8][16];
 };
 
 // The loader's work for pages whose rows are no whole 16-byte words, or do not divide a subtile: piece
@@ -1495,7 +1495,7 @@ __device__ __forceinline__ float max_across(float (&x)[16], int lane) {
 
 // The softmax warps' work of FEW: two groups of four warps, 16 rows each.
 template <int DT>
-__device__ __forceinline__ void few_rows(const ChunkArgs& a, ChunkShared& sh, bool more, uint8_t* smem, uint32_t tmem) {
+__device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool more, uint8_t* smem, uint32_t tmem) {
   constexpr int D = 128, NT = 128, PR = chunk_part_row(D);
   using C = ChunkShape<D, kChunkFew>;
   const int lane = threadIdx.x & 31;
@@ -1514,6 +1514,13 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, ChunkShared& sh, bo
   const uint32_t p_at = q_at + kFewBytes + (uint32_t)(my >> 6) * (kFewBytes / 2) + row0 * 128 + (my & 63) * 2;
   uint32_t ns0 = 0, ns1 = 0, runs = 0, steps = 0, syncs = 0;
   asm volatile("" : "+r"(ns0), "+r"(ns1), "+r"(runs), "+r"(steps));
+  if (w < 4) {  // the left operand of the sums: 16 ones a lane
+    uint32_t one[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) one[i] = DT == KVQ_DT_F16 ? 0x3c003c00u : 0x3f803f80u;
+    tmem_st16(lane_base + C::ONE_COL, one);
+    tmem_wait_st();
+  }
   // the warps follow one run: their barriers must match whatever the lengths in memory do meanwhile
   Run *now = &sh.runs[0], *after = &sh.next;
   more = few_any<8>(3, w == 0 && more);
@@ -1730,7 +1737,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
   constexpr bool PAIRED = C::PAIRED, FEW = C::FEW;
   constexpr int NT = C::NT, RT = C::RT;
   extern __shared__ uint8_t raw_smem[];
-  __shared__ ChunkShared sh;
+  __shared__ typename C::Shared sh;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_at = smem_addr(smem), k_at = q_at + C::FRONT, v_at = k_at + 2 * C::TILE_BYTES;
@@ -1768,13 +1775,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
   }
   // query rows that no unit writes are zeros
 #pragma unroll 1
-  for (uint32_t e = tid * 16; e < (FEW ? 3 * kFewBytes : C::FRONT); e += C::THREADS * 16)
+  for (uint32_t e = tid * 16; e < C::FRONT; e += C::THREADS * 16)
     *reinterpret_cast<uint4*>(smem + e) = make_uint4(0, 0, 0, 0);
-  if constexpr (FEW) {  // 64 rows of 64 ones
-    constexpr uint32_t one = DT == KVQ_DT_F16 ? 0x3c003c00u : 0x3f803f80u;
-    for (uint32_t e = tid * 16; e < kFewBytes; e += C::THREADS * 16)
-      *reinterpret_cast<uint4*>(smem + 3 * kFewBytes + e) = make_uint4(one, one, one, one);
-  }
   if (a.lo.flags & (KVQ_TBQ4_K | KVQ_TBQ4_V))
     for (int i = tid; i < 256; i += C::THREADS) {
       const __half2 p = __floats2half2_rn(a.lo.cb[i & 15], a.lo.cb[i >> 4]);
@@ -1800,8 +1802,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     // FEW: keys and values are the left operands, the rows the columns of both products
     const uint32_t qk_desc = base | ((uint32_t)k_chan << (FEW ? 15 : 16)) | ((uint32_t)((FEW ? a.cols : NT) >> 3) << 17);
     const uint32_t pv_desc = base | ((uint32_t)!v_chan << (FEW ? 15 : 16)) | ((uint32_t)((FEW ? a.cols : D) >> 3) << 17);
-    const uint64_t p_desc = operand_desc(q_at + kFewBytes, 0, 1024), one_desc = operand_desc(q_at + 3 * kFewBytes, 0, 1024);
-    const uint32_t sum_desc = (base & 0xffffffu) | ((64u >> 4) << 24) | ((uint32_t)(a.cols >> 3) << 17);
+    const uint64_t p_desc = operand_desc(q_at + kFewBytes, 0, 1024);
+    const uint32_t sum_desc = base | ((uint32_t)(a.cols >> 3) << 17);
     const uint64_t q_desc = operand_desc(q_at, 0, 1024), k_desc = operand_desc(k_at, k_chan ? D * 128 : 0, 1024),
                    v_desc = operand_desc(v_at, v_chan ? 0 : NT * 128, 1024);
     uint32_t kt = 0;             // tiles of this CTA so far
@@ -1866,7 +1868,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
                 // the rows' sums of P, in every lane
 #pragma unroll
                 for (int k = 0; k < NT / 16; ++k)
-                  mma_ss(tmem + C::L_COL, one_desc, dp + (k >> 2) * (kFewBytes >> 5) + (k & 3) * 2, sum_desc, add || k > 0);
+                  mma_ts(tmem + C::L_COL, tmem + C::ONE_COL, dp + (k >> 2) * (kFewBytes >> 5) + (k & 3) * 2, sum_desc, add || k > 0);
               } else if (v_chan) {
 #pragma unroll
                 for (int k = 0; k < NT / 16; ++k)
@@ -1896,6 +1898,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     ld.lanes(a, w - C::LOAD_WARP, lane);
     const int piece = 2 * ld.which + ld.half;
     const uint32_t slots = a.slots;
+    uint4* const orders = sh.orders[w - C::LOAD_WARP];
     uint32_t kt = 0, slot = piece, todo = 3;  // tiles so far; this lane's piece's slot; pieces to ask for
     while (slot >= slots) slot -= slots;
     bool ok = true;
@@ -1910,15 +1913,25 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         // the next tile's page ids load while this one waits for slots
         const TileTokens next = tile_tokens<D>(run.u, min(j + 1, t1 - 1));
         const int next_pid = ld.page_id(a, u, next.t0, ld.ln);
+        // A lane works out a copy and notes it; one lane then asks for all of a piece's.  (Passing the operands
+        // by shuffles took 200 to 500 cycles a copy: every one queues behind the dequantizing
+        // warps' shared-memory traffic.)
         const uint8_t* src = nullptr;
         int at = 0;
         bool bad = false;
-        const int bytes = ld.source(a, u, tt, ld.ln, pid, &src, &at, &bad);
+        const int bytes = ld.source(a, u, tt, ld.half, ld.ln, pid, &src, &at, &bad);
         const uint32_t bads = __ballot_sync(0xffffffffu, bad) >> (16 * ld.half) & 0xffffu;
+        const uint32_t copies = __ballot_sync(0xffffffffu, bytes != 0);
         const uint32_t total0 = __reduce_add_sync(0xffffffffu, ld.half ? 0u : (uint32_t)bytes),
                        total1 = __reduce_add_sync(0xffffffffu, ld.half ? (uint32_t)bytes : 0u);
+        if (bytes) {
+          const uint64_t from = reinterpret_cast<uint64_t>(src);
+          orders[16 * ld.half + __popc(copies >> (16 * ld.half) & ((1u << ld.ln) - 1))] =
+              make_uint4((uint32_t)from, (uint32_t)(from >> 32), raw_at + slot * a.slot_bytes + at, (uint32_t)bytes);
+        }
+        __syncwarp();
         const uint32_t number = 4 * kt + piece, bar = piece * kChunkBars + (kt & (kChunkBars - 1));
-        const uint32_t full = smem_addr(&sh.raw_full[bar]), dst = raw_at + slot * a.slot_bytes + at;
+        const uint32_t full0 = smem_addr(&sh.raw_full[2 * ld.which * kChunkBars + (kt & (kChunkBars - 1))]);
         // the slot's last piece must have been read
         const uint32_t last = number - slots;
         const uint32_t empty = smem_addr(&sh.raw_empty[(last & 3) * kChunkBars + ((last >> 2) & (kChunkBars - 1))]);
@@ -1931,11 +1944,23 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           if (ready) {
             sh.bad_pages[bar] = bads;
             if (bads) atomicOr(a.status, KVQ_DEV_PAGE);
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full), "r"(ld.half ? total1 : total0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_addr(&sh.raw_full[bar])),
+                         "r"(ld.half ? total1 : total0)
                          : "memory");
           }
           __syncwarp();
-          copy_each((now >> ld.half & 1) && bytes, dst, src, bytes, full);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int n = now >> h & 1 ? __popc(copies >> (16 * h) & 0xffffu) : 0;
+            if (elect_one()) {
+#pragma unroll 4
+              for (int c = 0; c < n; ++c) {
+                const uint4 x = orders[16 * h + c];
+                bulk_copy(x.z, x.x, x.y, x.w, full0 + h * (8 * kChunkBars));
+              }
+            }
+            __syncwarp();
+          }
           todo &= ~now;
           if (!now && (spin > kChunkSpin || __any_sync(0xffffffffu, *(volatile uint32_t*)gave_up != 0))) {
             if (lane == 0) *(volatile uint32_t*)gave_up = 1;
@@ -2341,7 +2366,7 @@ template <int D, int DT, int MODE>
 cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   using C = ChunkShape<D, MODE>;
   // all of the SM's shared memory that the tiles leave is staging
-  const uint32_t all = 227 * 1024 - (uint32_t)sizeof(ChunkShared);
+  const uint32_t all = 227 * 1024 - (uint32_t)sizeof(typename C::Shared);
   const uint32_t left = all - C::FIXED - 16;
   a.slots = (int)(left / a.slot_bytes);
   if (a.slots > kChunkMaxSlots) a.slots = kChunkMaxSlots;
