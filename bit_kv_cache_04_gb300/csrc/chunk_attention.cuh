@@ -22,9 +22,13 @@
 // dequantized once for both).  Not PAIRED: the streams share the rows and take alternate tiles.
 // D = 256: tiles of 64 tokens, 128 rows, one output accumulator and one group
 // of softmax warps over two S buffers (TMEM holds no more).
-// Few rows: with at most 32 (64) rows the queries are repeated in every
-// quarter (half) of the 128 lanes and each repetition takes its own quarter
-// (half) of a tile's tokens, so that all four warps of a stream share the exponentials.
+// FEW (D = 128, at most 32 rows a sequence): rows are the products' columns, see the kernel.
+// Else, with at most 64 rows, the queries are repeated in both halves of the 128 lanes and each
+// repetition takes its own half of a tile's tokens, so that all warps share the exponentials.
+//
+// Roundings: keys, values, P and turned queries go to the input's 16-bit type, as in a cache of that type: the
+// tensor cores multiply nothing wider at this rate.  Scores, row sums and outputs are fp32 until the
+// last store.
 //
 // The tiles of all (layer, kv head, sequence, row tile) units form one line
 // that is cut into equal runs, one per CTA, whatever the lengths; a unit cut
@@ -62,7 +66,7 @@ struct ChunkArgs {
   const int32_t* seq_lens;
   int total_q, max_q, window, sinks;
   int turn_here;  // rotated formats: the kernel turns the (few) queries itself; else a pass before it does
-  int rep;      // repetitions of the query rows over the lanes: 1, 2, 4
+  int rep;      // repetitions of the query rows over the lanes: 1, 2
   int cols;     // few rows: columns of the products, 16 or 32
   uint32_t g_magic;  // floor(2^32 / g) + 1
   int by_warp;  // row tiles per sequence are many: count them with a warp per sequence

@@ -53,7 +53,7 @@ __device__ __forceinline__ T uniform(T x) {
 }
 // One lane of a converged warp.  The instructions below and the bulk copies take their
 // operands from uniform registers: issued by `lane == 0`, or by several lanes with
-// operands of their own, each becomes a loop over the lanes (270 cycles a product).
+// operands of their own, each becomes a loop over the lanes.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -649,7 +649,7 @@ __device__ __forceinline__ void general_run(RunFmt f, uint32_t blk, uint32_t cod
 // One lane's four runs of a piece that lies in one format, wholly in view:
 // the hot path.  Its loop is kept short, and everything else out of line: the five roles run
 // different code at the same time, and what they run has to fit the instruction cache (with
-// this loop unrolled eight times a batch of 64 sequences took 512 us, with one run a turn 393 us).
+// this loop unrolled eight times the single tokens of 64 sequences took 1.3 times as long).
 struct PiecePlace {
   uint32_t blk, codes, step;  // first run's block and codes in the staged piece; to the next run
   uint32_t line, line_step;   // the same in the tile
@@ -880,8 +880,8 @@ struct Loader {
     if (!a.lo.paged || c >= (PIECE >> a.copy_shift) || t >= u.qe) return -1;
     return __ldg(a.cp.block_table + (int64_t)u.b * a.lo.max_pages + t / a.lo.pt);
   }
-  // source and bytes of copy c of a piece (0 bytes: nothing to copy)
-  __device__ __forceinline__ int source(const ChunkArgs& a, const CachePos& u, const TileTokens& tt, int half, int c, int pid,
+  // source and bytes of copy c of this lane's piece (0 bytes: nothing to copy)
+  __device__ __forceinline__ int source(const ChunkArgs& a, const CachePos& u, const TileTokens& tt, int c, int pid,
                                         const uint8_t** src, int* at, bool* bad) const {
     const int t = tt.t0 + half * PIECE + (c << a.copy_shift), sub = t & ~31;
     if (c >= (PIECE >> a.copy_shift) || t >= u.qe || sub + 32 <= tt.v0 || sub >= tt.v1) return 0;
@@ -1177,7 +1177,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
   const int slot0 = !cut ? 2 : unit_pos == c0 * line.per_cta ? 0 : 1;  // of the first CTA; the others' is 0
   constexpr bool ONE = PAIRED || C::FEW;
   const int copies = ONE ? 1 : C::STREAMS * a.rep;  // partial rows of one query row in one slot
-  const int rep_log = a.rep == 4 ? 2 : a.rep - 1, copies_log = ONE ? 0 : rep_log + C::STREAMS - 1;
+  const int rep_log = a.rep - 1, copies_log = ONE ? 0 : rep_log + C::STREAMS - 1;
   const int parts = (c1 - c0 + 1) * copies;
   auto part = [&](int i, int r) {
     // copy k of a slot: stream k / rep (128 rows each), repetition k % rep (128 / rep rows each)
@@ -1449,8 +1449,13 @@ __device__ __forceinline__ void rescale_columns(uint32_t o_col, float f) {
 // At most 32 query rows a sequence, D = 128: the products are turned over, S^T = K Q^T and O^T = V^T P^T, so that
 // the rows are columns (16 or 32 of them) and not lanes: both products cost a quarter or an eighth, and the
 // accumulator, its rescaling and its output shrink with them.  A thread holds one token of a tile, then
-// one channel of the output; P goes through shared memory.  The rows' reference maxima are common to
-// the four warps: lane r of each of them holds row r's.
+// one channel of the output; P goes through shared memory.  Row sums come from a third product, ones times
+// P^T, so that no thread keeps 16 of them (32 registers of sums spilled: 8-token drafts of 16
+// sequences took 414 us).  The rows' reference maxima are common to a group's four warps.
+// Against rows as lanes, repeated to share the exponentials: one token over one long window 46 -> 29 us, single
+// tokens of 64 sequences 254 -> 229 us, drafts of 16 sequences 314 -> 271 us.  (More than 32 rows are not two
+// groups of 16 a thread any more, and there the lanes are full enough.)  Bound now by the dequantizing warps' issue slots and the shared memory's bandwidth (a tile's
+// values are written once and read by the products once: 128 KiB of shared-memory traffic for 17 KiB of cache).
 
 // A run's queries into shared memory (row r of 64 channels a block of kFewBytes / 2), a warp a row.
 template <int DT>
@@ -1913,13 +1918,13 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         // the next tile's page ids load while this one waits for slots
         const TileTokens next = tile_tokens<D>(run.u, min(j + 1, t1 - 1));
         const int next_pid = ld.page_id(a, u, next.t0, ld.ln);
-        // A lane works out a copy and notes it; one lane then asks for all of a piece's.  (Passing the operands
-        // by shuffles took 200 to 500 cycles a copy: every one queues behind the dequantizing
-        // warps' shared-memory traffic.)
+        // A lane works out a copy and notes it; one lane then asks for all of a piece's.  (Operands passed by
+        // shuffles took 200 to 500 cycles a copy, queued behind the dequantizing warps' shared-memory
+        // traffic; an odd chunk of 256-channel heads took 824 us so, 773 us with the notes.)
         const uint8_t* src = nullptr;
         int at = 0;
         bool bad = false;
-        const int bytes = ld.source(a, u, tt, ld.half, ld.ln, pid, &src, &at, &bad);
+        const int bytes = ld.source(a, u, tt, ld.ln, pid, &src, &at, &bad);
         const uint32_t bads = __ballot_sync(0xffffffffu, bad) >> (16 * ld.half) & 0xffffu;
         const uint32_t copies = __ballot_sync(0xffffffffu, bytes != 0);
         const uint32_t total0 = __reduce_add_sync(0xffffffffu, ld.half ? 0u : (uint32_t)bytes),
