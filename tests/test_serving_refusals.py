@@ -207,3 +207,36 @@ def test_chunk_attention_wrapper_refuses_other_tensors():
         args.update(kw)
         with pytest.raises(ValueError):
             c.chunk_attention(0, args["n_layers"], args["q"], args["cu_q"], 4, 2, args["seq_lens"], args["out"])
+
+
+def test_tensors_of_another_device():
+    torch = pytest.importorskip("torch")
+    cfg = _cfg(**PAGED)
+    c = K.KVCache.__new__(K.KVCache)
+    c.cfg, c.workspace, c.chunk_workspace = cfg, torch.empty(1), torch.empty(1)
+    q, n = torch.empty(1, 3, 4, 128, dtype=torch.float16), torch.zeros(3, dtype=torch.int32)
+    cu = torch.zeros(4, dtype=torch.int32)
+    for args in ((q.to("meta"), cu, 3, 1, n, q), (q, cu.to("meta"), 3, 1, n, q), (q, cu, 3, 1, n.to("meta"), q),
+                 (q, cu, 3, 1, n, q.to("meta"))):
+        with pytest.raises(ValueError, match="is on"):
+            c.chunk_attention(0, 1, *args)
+    with pytest.raises(ValueError, match="is on"):
+        K.qk_norm_rope(cfg, q[0], None, None, q[0].to("meta"), None)
+    pool = K.PagePool.__new__(K.PagePool)
+    pool.cache, pool.workspace = c, torch.empty(1)
+    with pytest.raises(ValueError, match="is on"):
+        pool.release(n.to("meta"), n)
+
+
+def test_buffers_of_the_caller():
+    torch = pytest.importorskip("torch")
+    cfg = _cfg(**PAGED)
+    sizes = dict(zip(K.BUFFER_NAMES, K.kvq_buffer_sizes(cfg)))
+    full = {k: torch.empty(v, dtype=torch.uint8) for k, v in sizes.items() if v}
+    for table in (None, torch.zeros(cfg.batch, cfg.max_pages_per_seq - 1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="block table"):
+            K.KVCache.from_buffers(cfg, full, table)
+    with pytest.raises(ValueError, match="needed"):
+        K.KVCache.from_buffers(cfg, {**full, "k_main": full["k_main"][1:]}, torch.zeros(12, dtype=torch.int32))
+    with pytest.raises(ValueError, match="one device"):
+        K.KVCache.from_buffers(cfg, {**full, "v_main": full["v_main"].to("meta")}, torch.zeros(12, dtype=torch.int32))
