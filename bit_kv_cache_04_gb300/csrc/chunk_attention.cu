@@ -112,7 +112,6 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
     return fail(KVQ_ERR_UNSUPPORTED, "too many tiles for one call: pass fewer layers or rows");
   a.g_magic = (uint32_t)((1ull << 32) / a.lo.g + 1);
   a.turn_here = (cfg->flags & KVQ_ROTATE_K) && rows <= 64 ? 1 : 0;
-  a.rep = rows <= 64 ? 2 : 1;
   a.cols = rows <= 16 ? 16 : kFewRows;
   a.by_warp = rows > 4 * row_tile;
   // Staging: 32-token subtiles as single bulk copies; pages of fewer tokens

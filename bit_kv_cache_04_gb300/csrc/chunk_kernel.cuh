@@ -1176,12 +1176,10 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
   const int c1 = cut ? (unit_pos + u.nt - 1) / line.per_cta : blockIdx.x;
   const int slot0 = !cut ? 2 : unit_pos == c0 * line.per_cta ? 0 : 1;  // of the first CTA; the others' is 0
   constexpr bool ONE = PAIRED || C::FEW;
-  const int copies = ONE ? 1 : C::STREAMS * a.rep;  // partial rows of one query row in one slot
-  const int rep_log = a.rep - 1, copies_log = ONE ? 0 : rep_log + C::STREAMS - 1;
+  constexpr int copies = ONE ? 1 : C::STREAMS, copies_log = copies - 1;  // partial rows of one query row in one slot
   const int parts = (c1 - c0 + 1) * copies;
   auto part = [&](int i, int r) {
-    // copy k of a slot: stream k / rep (128 rows each), repetition k % rep (128 / rep rows each)
-    const int c = i >> copies_log, row = ONE ? r : ((i & (copies - 1)) << (7 - rep_log)) + r;
+    const int c = i >> copies_log, row = ((i & (copies - 1)) << 7) + r;  // a stream's 128 rows after the other's
     return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
   const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
@@ -1380,12 +1378,13 @@ __device__ __forceinline__ void hide(uint32_t (&x)[32], int t, const RowSeen& se
       if (t + i > see.pos || (t + i < see.win_lo && t + i >= see.sinks)) x[i] = 0xff800000u;
   }
 }
-// largest score of the row's columns [c0, c1) of S at s_col (tile's first token t0)
-template <bool MASKED>
-__device__ __forceinline__ float tile_max(uint32_t s_col, int c0, int c1, int t0, const RowSeen& see, uint32_t (&x)[32]) {
+// largest score of the row's columns of S at s_col (tile's first token t0)
+template <int NT, bool MASKED>
+__device__ __forceinline__ float tile_max(uint32_t s_col, int t0, const RowSeen& see) {
   float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll 1
-  for (int c = c0; c < c1; c += 32) {
+  for (int c = 0; c < NT; c += 32) {
+    uint32_t x[32];
     tmem_ld32(s_col + c, x);
     tmem_wait_ld();
     hide<MASKED>(x, t0 + c, see);
@@ -1397,21 +1396,17 @@ __device__ __forceinline__ float tile_max(uint32_t s_col, int c0, int c1, int t0
   }
   return fmaxf(m0, m1);
 }
-// P = 2^(S sc + mneg) over S, in the input dtype; the sum of P.  x holds the
-// columns already when there are only 32.
-template <int DT, bool MASKED>
-__device__ __forceinline__ float tile_exp(uint32_t s_col, int c0, int c1, int t0, const RowSeen& see, float sc, float mneg,
-                                          uint32_t (&x)[32]) {
+// P = 2^(S sc + mneg) over S, in the input dtype; the sum of P
+template <int DT, int NT, bool MASKED>
+__device__ __forceinline__ float tile_exp(uint32_t s_col, int t0, const RowSeen& see, float sc, float mneg) {
   const uint64_t sc2 = pk2(sc, sc), mneg2 = pk2(mneg, mneg);  // packed pairs: half the instructions
   uint64_t la = 0, lb = 0;
-  const bool have = c1 - c0 == 32;
 #pragma unroll 1
-  for (int c = c0; c < c1; c += 32) {
-    if (!have) {
-      tmem_ld32(s_col + c, x);
-      tmem_wait_ld();
-      hide<MASKED>(x, t0 + c, see);
-    }
+  for (int c = 0; c < NT; c += 32) {
+    uint32_t x[32];
+    tmem_ld32(s_col + c, x);
+    tmem_wait_ld();
+    hide<MASKED>(x, t0 + c, see);
     uint32_t p[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -1452,8 +1447,8 @@ __device__ __forceinline__ void rescale_columns(uint32_t o_col, float f) {
 // one channel of the output; P goes through shared memory.  Row sums come from a third product, ones times
 // P^T, so that no thread keeps 16 of them (32 registers of sums spilled: 8-token drafts of 16
 // sequences took 414 us).  The rows' reference maxima are common to a group's four warps.
-// Against rows as lanes, repeated to share the exponentials: one token over one long window 46 -> 29 us, single
-// tokens of 64 sequences 254 -> 229 us, drafts of 16 sequences 314 -> 271 us.  (More than 32 rows are not two
+// Against rows as lanes: one token over one long window 34 -> 28 us, single tokens of 64 sequences 265 -> 229 us,
+// drafts of 16 sequences 291 -> 272 us; 16 columns instead of 32 for the single tokens 238 -> 229 us.  (More than 32 rows are not two
 // groups of 16 a thread any more, and there the lanes are full enough.)  Bound now by the dequantizing warps' issue slots and the shared memory's bandwidth (a tile's
 // values are written once and read by the products once: 128 KiB of shared-memory traffic for 17 KiB of cache).
 
@@ -2108,16 +2103,14 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       const int my_lane = quad * 32 + lane;  // TMEM lane: row of the 128-row tile
       const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
       const uint32_t o_col = lane_base + C::O_COL + (C::STREAMS == 2 ? stream * D : 0);
-      const int lanes_per = 128 / a.rep;
-      const int cols = NT / a.rep, col0 = (my_lane / lanes_per) * cols;  // this row's tokens of a tile
-      const int my_row = (PAIRED ? stream * 128 : 0) + (my_lane & (lanes_per - 1));  // query row of the row tile
+      const int my_row = (PAIRED ? stream * 128 : 0) + my_lane;  // query row of the row tile
       const float sc = 1.4426950408889634f * rsqrtf((float)D);
       // queries into shared memory
       if (PAIRED || stream == 0) {
-        const int first = PAIRED ? stream * 128 : 0, n = min(lanes_per, run.u.rows - first);  // rows
+        const int first = PAIRED ? stream * 128 : 0, n = min(128, run.u.rows - first);  // rows
         const uint32_t q0 = q_at + (PAIRED ? stream * C::Q_BYTES : 0);
         if (a.turn_here) {
-          // few rows, turned into the rotated domain here: a warp a row (each repetition a copy)
+          // few rows, turned into the rotated domain here: a warp a row
           const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
           constexpr int NC = D / 128;
 #pragma unroll 1
@@ -2129,11 +2122,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
             rotate_lanes(v, s1, s2);
             w = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
             const int ch = 128 * c + 4 * lane;
-#pragma unroll 1
-            for (int k = 0; k < a.rep; ++k) {
-              const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r + k * lanes_per, (ch & 63) >> 3) + (ch & 4) * 2;
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
-            }
+            const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r, (ch & 63) >> 3) + (ch & 4) * 2;
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
           }
         } else {
           constexpr int LPR = D / 8, RPT = 32 / LPR, U = 4;  // lanes a row, rows a turn, turns in flight
@@ -2151,13 +2141,10 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < U; ++i) {
               const int r = r0 + 4 * RPT * i;
-              if (r < n) {
-#pragma unroll 1
-                for (int k = 0; k < a.rep; ++k)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(col + swz(r + k * lanes_per, (ch & 63) >> 3)),
-                               "r"(w[i].x), "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
-                               : "memory");
-              }
+              if (r < n)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(col + swz(r, (ch & 63) >> 3)), "r"(w[i].x),
+                             "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
+                             : "memory");
             }
           }
         }
@@ -2185,9 +2172,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         ns0 += b ^ 1;
         ns1 += b;
         tc_fence_after();
-        uint32_t x[32];
-        const float mt = sc * (masked ? tile_max<true>(s_col, col0, col0 + cols, t0, see, x)
-                                      : tile_max<false>(s_col, col0, col0 + cols, t0, see, x));
+        const float mt = sc * (masked ? tile_max<NT, true>(s_col, t0, see) : tile_max<NT, false>(s_col, t0, see));
         // the reference maximum follows only when it falls behind by 2^8: P
         // stays below 2^8 and the accumulator is rescaled rarely
         const bool grow = mt > m + 8.f;
@@ -2208,16 +2193,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         }
         first_step = false;
         const float mneg = m == -INFINITY ? 0.f : -m;
-        l += masked ? tile_exp<DT, true>(s_col, col0, col0 + cols, t0, see, sc, mneg, x)
-                    : tile_exp<DT, false>(s_col, col0, col0 + cols, t0, see, sc, mneg, x);
-        if (a.rep > 1) {  // the other repetitions' tokens count nothing in this row
-          uint32_t z[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] = 0;
-#pragma unroll 1
-          for (int c = 0; c < NT; c += 32)
-            if (c < col0 || c >= col0 + cols) tmem_st16(s_col + c / 2, z);
-        }
+        l += masked ? tile_exp<DT, NT, true>(s_col, t0, see, sc, mneg) : tile_exp<DT, NT, false>(s_col, t0, see, sc, mneg);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -2230,7 +2206,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       const bool cut = run.t0 > 0 || run.t1 < run.u.nt, mine = my_row < run.u.rows;
-      const bool direct = !cut && (PAIRED || (C::STREAMS == 1 && a.rep == 1));
+      const bool direct = !cut && (PAIRED || C::STREAMS == 1);
       uint32_t x[16];
       if (direct) {
         const bool rotated = (a.lo.flags & KVQ_ROTATE_V) != 0, fix = *(volatile uint32_t*)&sh.nonfinite != 0;

@@ -253,15 +253,19 @@ def _stream(stream) -> Optional[int]:
 BUFFER_NAMES = ("k_main", "v_main", "k_cold", "v_cold", "k_resid", "v_resid")
 
 
-def _here(device, *tensors) -> None:
-    """The tensors live on `device`, and it is the current one: streams and launches belong to that."""
+def _here(index, *tensors) -> None:
+    """The tensors live on device `index` (-1: the host), and that is the current one: streams and launches belong to it."""
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a tensor is on {t.device}, not on device {index}")
+    if index >= 0 and index != _current_device():
+        raise ValueError(f"device {index} is not the current one")
+
+
+def _current_device() -> int:
     import torch
 
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"a tensor is on {t.device}, not on {device}")
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
-        raise ValueError(f"{device} is not the current device")
+    return torch.cuda.current_device()
 
 
 class KVCache:
@@ -297,6 +301,7 @@ class KVCache:
                 raise ValueError("a paged cache needs a block table [batch, max_pages_per_seq]")
         self.ws_bytes = kvq_workspace_bytes(cfg)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self.index = self.workspace.get_device()
         self.c_cache = _Cache(*[_ptr(self.buffers[n]) for n in BUFFER_NAMES], _ptr(self.block_table))
         _check(LIB.kvq_workspace_init(ctypes.byref(self.c_cfg), _ptr(self.workspace), self.ws_bytes,
                                       _stream(None)))
@@ -358,7 +363,7 @@ class KVCache:
                     raise RuntimeError("the first chunk_attention prepares its workspace: make it before the capture")
                 self.chunk_workspace = self.make_chunk_workspace(stream)
             workspace = self.chunk_workspace
-        _here(self.workspace.device, q, out, cu_q, seq_lens, workspace)
+        _here(self.index, q, out, cu_q, seq_lens, workspace)
         _check(LIB.kvq_chunk_attention(ctypes.byref(self.c_cfg), ctypes.byref(self.c_cache), layer0, n_layers,
                                        _ptr(q), _ptr(cu_q), total_q, max_q, _ptr(seq_lens), window, sinks, _ptr(out),
                                        _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -421,7 +426,7 @@ def qk_norm_rope(cfg: Config, q, k, positions, q_out, k_out, plan=None, q_weight
     if plan is not None and (positions is None or positions.dtype != torch.int32 or positions.numel() != n or
                              not positions.is_contiguous()):
         raise ValueError("positions is a contiguous int32 tensor, one of each token")
-    _here(some.device, q, k, q_out, k_out, q_weight, k_weight, positions)
+    _here(some.get_device(), q, k, q_out, k_out, q_weight, k_weight, positions)
     qs = (0, 0) if q is None else q.stride()
     ks = (0, 0) if k is None else k.stride()
     _check(LIB.kvq_qk_norm_rope(ctypes.byref(_to_c(cfg)), None if plan is None else ctypes.byref(plan), _ptr(q), qs[0],
@@ -436,13 +441,13 @@ class PagePool:
     def __init__(self, cache: KVCache, refs=None, stream=None):
         import torch
 
-        self.cache = cache
+        self.cache, self.index = cache, cache.index
         self.ws_bytes = kvq_pages_workspace_bytes(cache.cfg)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=cache.device)
         self.refs = refs if refs is not None else torch.empty(cache.cfg.n_pages, dtype=torch.int32, device=cache.device)
         if self.refs.dtype != torch.int32 or self.refs.numel() != cache.cfg.n_pages or not self.refs.is_contiguous():
             raise ValueError("refs is a contiguous int32 tensor of n_pages")
-        _here(self.workspace.device, self.refs)
+        _here(self.index, self.refs)
         _check(LIB.kvq_pages_init(self._cfg(), _ptr(cache.block_table), _ptr(self.refs), *self._ws(stream)))
 
     def _cfg(self):
@@ -459,7 +464,7 @@ class PagePool:
                 raise ValueError("lengths and lists are contiguous int32 tensors")
         if seq_lens.numel() != self.cache.cfg.batch or len({t.numel() for t in lists}) != 1:
             raise ValueError("seq_lens is [batch]; lists have one length")
-        _here(self.workspace.device, seq_lens, *lists)
+        _here(self.index, seq_lens, *lists)
 
     def release(self, seqs, seq_lens, stream=None):
         """Frees the listed sequences."""
@@ -489,7 +494,7 @@ class PagePool:
         for t, like in ((refs_out, self.refs), (table_out, table)):
             if t is not None and (t.dtype != torch.int32 or t.numel() != like.numel() or not t.is_contiguous()):
                 raise ValueError("outputs are contiguous int32 tensors like the inputs")
-        _here(self.workspace.device, refs_out, table_out)
+        _here(self.index, refs_out, table_out)
         _check(LIB.kvq_pages_compact(self._cfg(), ctypes.byref(self.cache.c_cache), _ptr(table), _ptr(self.refs),
                                      _ptr(table if table_out is None else table_out),
                                      _ptr(self.refs if refs_out is None else refs_out), *self._ws(stream)))

@@ -209,23 +209,34 @@ def test_chunk_attention_wrapper_refuses_other_tensors():
             c.chunk_attention(0, args["n_layers"], args["q"], args["cu_q"], 4, 2, args["seq_lens"], args["out"])
 
 
-def test_tensors_of_another_device():
+def test_tensors_of_another_device(monkeypatch):
     torch = pytest.importorskip("torch")
+
+    class There(torch.Tensor):  # a host tensor that says it is on device 1
+        def get_device(self):
+            return 1
+
+    def there(t):
+        return t.as_subclass(There)
+
     cfg = _cfg(**PAGED)
     c = K.KVCache.__new__(K.KVCache)
-    c.cfg, c.workspace, c.chunk_workspace = cfg, torch.empty(1), torch.empty(1)
+    c.cfg, c.index, c.chunk_workspace = cfg, -1, torch.empty(1)
     q, n = torch.empty(1, 3, 4, 128, dtype=torch.float16), torch.zeros(3, dtype=torch.int32)
     cu = torch.zeros(4, dtype=torch.int32)
-    for args in ((q.to("meta"), cu, 3, 1, n, q), (q, cu.to("meta"), 3, 1, n, q), (q, cu, 3, 1, n.to("meta"), q),
-                 (q, cu, 3, 1, n, q.to("meta"))):
-        with pytest.raises(ValueError, match="is on"):
+    for args in ((there(q), cu, 3, 1, n, q), (q, there(cu), 3, 1, n, q), (q, cu, 3, 1, there(n), q), (q, cu, 3, 1, n, there(q))):
+        with pytest.raises(ValueError, match="not on device"):
             c.chunk_attention(0, 1, *args)
-    with pytest.raises(ValueError, match="is on"):
-        K.qk_norm_rope(cfg, q[0], None, None, q[0].to("meta"), None)
+    with pytest.raises(ValueError, match="not on device"):
+        K.qk_norm_rope(cfg, q[0], None, None, there(q[0]), None)
     pool = K.PagePool.__new__(K.PagePool)
-    pool.cache, pool.workspace = c, torch.empty(1)
-    with pytest.raises(ValueError, match="is on"):
-        pool.release(n.to("meta"), n)
+    pool.cache, pool.index = c, -1
+    with pytest.raises(ValueError, match="not on device"):
+        pool.release(there(n), n)
+    # all on one device, but not the current one
+    monkeypatch.setattr(K, "_current_device", lambda: 0)
+    with pytest.raises(ValueError, match="not the current"):
+        K.qk_norm_rope(cfg, there(q[0]), None, None, there(q[0]), None)
 
 
 def test_buffers_of_the_caller():
