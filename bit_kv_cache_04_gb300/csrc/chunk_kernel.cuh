@@ -1559,13 +1559,15 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
     const Run& run = *now;
     const int rows = run.u.rows - row0, t0 = run.t0, t1 = run.t1;  // the group's: 16 or fewer, none
     bool ok = true;
-    // row row0 + lane's reference (+inf past the rows: it never moves); and minus all rows'
-    float m = lane < rows ? -INFINITY : INFINITY;
+    // row row0 + lane's reference; and minus all rows'.  +inf past the rows: it never moves.  The lowest to begin with is
+    // finite, so that a score of -inf alone in a run counts nothing instead of making a NaN.
+    constexpr float LOWEST = -3e38f;
+    float m = lane < rows ? LOWEST : INFINITY;
     if (row0 < a.cols) {
       const int st = run.u.st, skip = run.u.lo_tile - st, p_lo = run.u.p_lo, p_hi = run.u.p_hi;
       float n[16];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) n[r] = r < rows ? INFINITY : -INFINITY;
+      for (int r = 0; r < 16; ++r) n[r] = r < rows ? -LOWEST : -INFINITY;
       __syncwarp();
       if (lane < 16) pos[lane] = run.u.T - run.u.n + div_g(a, min(row0 + lane, run.u.rows - 1));
       __syncwarp();
@@ -1603,8 +1605,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
 #pragma unroll
           for (int i = 0; i < 16; ++i) most = fmaxf(most, x[i]);
         }
-        // The references follow when some score passes its row's by 2^8 (P stays below 2^8; a row that has seen
-        // nothing has the reference -inf): then the group's all go to their rows' maxima so far and the accumulator is
+        // The references follow when some score passes its row's by 2^8 (P stays below 2^8): then the group's all go to their rows' maxima so far and the accumulator is
         // rescaled.  References are whole numbers: factors are powers of two, and P rounds alike whatever the reference.
         if (few_any<4>(1 + (w >> 2), most > 8.f || !here)) {
           if (here) {
@@ -1628,7 +1629,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
 #pragma unroll
           for (int k = 0; k < 4; ++k) top = fmaxf(top, floorf(sh.few_part[(w & 4) + k][lane & 15]));
           if (lane < 16) {
-            fac[lane] = top == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
+            fac[lane] = top == m ? 1.f : ex2(m - top);
             mneg[lane] = -top;
           }
           m = top;

@@ -233,6 +233,28 @@ def test_not_finite_window_values_reach_only_rows_that_see_them():
                             assert torch.all(torch.isnan(got[0, i, 4:]))
 
 
+@pytest.mark.parametrize("n", [1, 5, 20, 40])
+def test_a_score_of_minus_infinity_counts_nothing(n):
+    """The last token is alone in its tile, and its key makes scores of -inf and +inf: the first leave it out, the second are NaN."""
+    for dt in (0, 1):
+        w = workload("llama2_7b_kivi4", [257], heads=(2, 4), in_dtype=dt)
+        cache, lens, q, _ = check(w, [n], pad=0)
+        cache.buffers["k_resid"].view(DT[dt]).view(2, 160, 128)[1, 256 % 160, 9] = float("-inf")
+        got = torch.empty_like(q)
+        cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        cache.chunk_attention(0, 1, q, cu, n, n, lens, got)
+        last = raw16(q[0, n - 1:])
+        oc = oracle_cfg(w.cfg)
+        bufs = gpu_buffers_as_oracle(cache, oc)
+        want, bound = S.chunk_attention(oc, bufs, 0, last, np.array([0, 1]), [256], with_bound=True)  # without the token
+        x = O.input_to_f32(raw16(got[0, n - 1:]), dt).astype(np.float64)
+        for h in range(4, 8):
+            if float(q[0, n - 1, h, 9]) > 0:
+                assert np.all(np.abs(x[0, h] - want[0, h]) <= bound[0, h]), h
+            else:
+                assert np.all(np.isnan(x[0, h])), h
+
+
 def test_stale_bytes_past_the_length_do_not_matter():
     w = workload("gqa8b_hadamard4_paged", [300, 40], heads=(2, 4), extra=64)
     cache, lens, q, out = check(w, [5, 5], pad=0)
