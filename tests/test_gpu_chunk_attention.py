@@ -233,6 +233,38 @@ def test_not_finite_window_values_reach_only_rows_that_see_them():
                             assert torch.all(torch.isnan(got[0, i, 4:]))
 
 
+def test_not_finite_window_values_among_few_rows():
+    """The same with 28 rows a head, which share their exponentials' warps."""
+    for dt in (0, 1):
+        w = workload("llama2_7b_kivi4", [200], heads=(2, 4), in_dtype=dt)
+        cache, lens, q, out = check(w, [7], pad=0)
+        cu = torch.tensor([0, 7], dtype=torch.int32, device="cuda")
+        for window in (0, 3):
+            clean = torch.empty_like(out)
+            cache.chunk_attention(0, 1, q, cu, 7, 7, lens, clean, window, 0)
+            see = [196 <= 193 + i and (not window or 196 > 193 + i - window) for i in range(7)]
+            for name in ("k_resid", "v_resid"):
+                for bad in (float("nan"), float("inf"), float("-inf")):
+                    buf = cache.buffers[name].view(DT[dt]).view(2, 160, 128)
+                    keep = buf[1, 196 % 160, 9].clone()
+                    buf[1, 196 % 160, 9] = bad
+                    got = torch.empty_like(out)
+                    cache.chunk_attention(0, 1, q, cu, 7, 7, lens, got, window, 0)
+                    buf[1, 196 % 160, 9] = keep
+                    assert torch.equal(got[0, :, :4], clean[0, :, :4])  # the other kv head
+                    for i in range(7):
+                        mine, ref = got[0, i, 4:], clean[0, i, 4:]
+                        if name == "v_resid" and see[i]:
+                            assert torch.all(torch.isnan(mine[:, 9])) if bad != bad else torch.all(mine[:, 9] == bad)
+                            assert torch.equal(mine[:, :9], ref[:, :9]) and torch.equal(mine[:, 10:], ref[:, 10:])
+                        elif see[i] and bad != bad:
+                            assert torch.all(torch.isnan(mine))
+                        elif not see[i]:
+                            # an infinite score of another row moves the group's references: same values, P's
+                            # smallest roundings apart; otherwise the same bits
+                            assert torch.equal(mine, ref) if name == "v_resid" or bad != bad else torch.isfinite(mine).all()
+
+
 @pytest.mark.parametrize("n", [1, 5, 20, 40])
 def test_a_score_of_minus_infinity_counts_nothing(n):
     """The last token is alone in its tile, and its key makes scores of -inf and +inf: the first leave it out, the second are NaN."""
