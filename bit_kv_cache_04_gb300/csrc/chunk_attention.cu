@@ -93,6 +93,7 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
   a.max_q = max_q;
   a.window = window;
   a.sinks = sinks;
+  a.stall_polls = stall_polls();
   a.status = (uint32_t*)workspace;
   a.cp.status = a.status;
   if (cfg->flags & KVQ_K_PRE_ROPE)

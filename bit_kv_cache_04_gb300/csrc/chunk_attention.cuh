@@ -76,6 +76,7 @@ struct ChunkArgs {
   int sub_bytes;    // staged bytes of a 32-token subtile, the largest of the formats
   int slot_bytes;   // of a staged piece (half a tile of one tensor)
   int slots;        // pieces in the ring
+  int stall_polls;  // > 0: failure-detection test mode (kvq_test_force_stall)
   uint32_t* status;
   uint32_t* tickets;    // [grid][kChunkTickets]
   uint32_t* nonfinite;  // [grid][kChunkTickets]: a 16-bit window value of the unit is not finite

@@ -967,7 +967,8 @@ struct ChunkShape {
 struct ChunkShared {
   uint64_t raw_full[4 * kChunkBars], raw_empty[4 * kChunkBars];  // [piece kind][tile mod kChunkBars]
   uint32_t bad_pages[4 * kChunkBars];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], s_full[2], p_full[2], o_full, pv_done, soft;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], s_full[2], p_full[2], o_full, pv_done, soft, drained,
+      never;
   uint32_t tmem;
   uint32_t gave_up;
   uint32_t nonfinite;
@@ -1792,6 +1793,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     bar_init(smem_addr(&sh.o_full), 1);
     bar_init(smem_addr(&sh.pv_done), 1);
     bar_init(smem_addr(&sh.soft), C::SOFT_WARPS);
+    bar_init(smem_addr(&sh.drained), 1);
+    bar_init(smem_addr(&sh.never), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     sh.gave_up = 0;
     sh.nonfinite = 0;
@@ -1822,6 +1825,19 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
   uint32_t* const gave_up = &sh.gave_up;
   const bool k_chan = a.lo.kf.axis == KVQ_AXIS_CHANNEL, v_chan = a.lo.vf.axis == KVQ_AXIS_CHANNEL;
   bool more = warp_run<D, RT>(a, sh.start, run, 0);
+  // Test mode (kvq_test_force_stall): in every second CTA one of the four roles first waits on a barrier that
+  // nothing completes, gives up and leaves; the CTAs between finish their runs.
+  if (a.stall_polls && (blockIdx.x & 1) && more) {
+    const int role = warp == C::MMA_WARP ? 0 : warp >= C::LOAD_WARP ? 1 : warp >= C::SOFT_WARPS ? 2 : 3;
+    if (role == (int)(blockIdx.x >> 1 & 3)) {
+#pragma unroll 1
+      for (int i = 0; i < a.stall_polls && !bar_test(smem_addr(&sh.never), 0); ++i) {
+      }
+      *(volatile uint32_t*)gave_up = 1;
+      __syncwarp();
+      more = false;
+    }
+  }
 
   if (warp == C::MMA_WARP) {
     // ---- products: one thread ----------------------------------------------------
@@ -1916,6 +1932,14 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       }
       kt += tiles;
     }
+    // Every product issued has left its operands, its accumulators and its barriers before the CTA's
+    // shared memory and TMEM go, also after a wait that gave up (else the softmax warps have waited already).
+    if (elect_one()) tc_commit(smem_addr(&sh.drained));
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < kChunkSpin && !bar_test(smem_addr(&sh.drained), 0); ++i) {
+    }
+    __syncwarp();
   } else if (warp >= C::LOAD_WARP && a.direct) {
     if (warp == C::LOAD_WARP) load_direct<D, RT>(a, sh, run, more, raw_at, lane);
   } else if (warp >= C::LOAD_WARP) {

@@ -25,6 +25,11 @@ static std::atomic<int> g_bounds_shrink{0};
 
 static thread_local std::string g_last_error;
 
+// Failure-detection test mode (kvq_test_force_stall).
+static std::atomic<int> g_stall_polls{0};
+
+int stall_polls() { return g_stall_polls.load(); }
+
 kvq_status fail(kvq_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -609,8 +614,6 @@ kvq_status kvq_commit_lengths(const kvq_config* cfg, const int32_t* cu_new, int3
   return ok();
 }
 
-// Failure-detection test mode of the tensor-core decode (kvq_test_force_stall).
-std::atomic<int> g_stall_polls{0};
 
 // Checks the decode arguments and fills *a (everything but the step).
 static kvq_status prep_decode(const kvq_config* cfg, const kvq_cache* cache, int32_t layer0, int32_t n_layers,
@@ -651,7 +654,7 @@ static kvq_status prep_decode(const kvq_config* cfg, const kvq_cache* cache, int
   a->partials = (float*)((char*)workspace + w.partials);
   a->rope = (const float2*)((char*)workspace + w.rope);
   a->rope_base_rows = w.rope_base_rows;
-  a->stall_polls = g_stall_polls.load();
+  a->stall_polls = stall_polls();
   return KVQ_OK;
 }
 
@@ -871,7 +874,7 @@ extern "C" kvq_status kvq_decode_attention_static(const kvq_config* cfg, const k
   a.partials = (float*)((char*)base + off_partials);
   a.rope = (const float2*)((char*)base + off_rope);
   a.rope_base_rows = rope_rows;
-  a.stall_polls = g_stall_polls.load();
+  a.stall_polls = stall_polls();
   e = launch_decode(a, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode kernel");
   return ok();

@@ -20,5 +20,7 @@ kvq_status cache_ptrs(const kvq_config* c, const kvq_cache* cache, CachePtrs* cp
 // Streaming multiprocessors of the current device (a GB300's count without one).
 int sm_count();
 size_t align_up(size_t x);
+// Polls of the failure-detection test mode (kvq_test_force_stall), 0 = off.
+int stall_polls();
 
 }  // namespace kvq

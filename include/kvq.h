@@ -31,8 +31,9 @@
  *    runtime data found by a kernel (a length beyond capacity, a page id out
  *    of range) sets a bit of the device status word in the workspace and
  *    skips that piece of work; nothing traps.  The only waits are bounded
- *    waits of a kernel for its own copies into shared memory
- *    (KVQ_DEV_STALL when one runs out).
+ *    waits of a CTA for its own copies into shared memory and, in
+ *    kvq_chunk_attention, of its roles for one another (KVQ_DEV_STALL when
+ *    one runs out).
  *  - Head mapping: query head h reads kv head h / (H_q / H_kv).
  *  - Softmax scale: fixed at 1/sqrt(D).
  *
@@ -145,8 +146,9 @@ enum {
   KVQ_DEV_PAGE = 1u << 1,     /* a block_table entry outside [0, n_pages) */
   KVQ_DEV_RANGE = 1u << 2,    /* kvq_dequantize range outside [0, T) */
   KVQ_DEV_LENGTH = 1u << 3,   /* a sequence length < 0 or > max_T, or cu_new not ascending */
-  KVQ_DEV_STALL = 1u << 4,    /* a decode kernel's own bulk copy into shared memory did not complete
-                                 within its bounded wait; that call's outputs are undefined */
+  KVQ_DEV_STALL = 1u << 4,    /* a bounded wait ran out: of a decode kernel for its own bulk copy into shared
+                                 memory, or of a chunk attention role for another one of its CTA; that call's
+                                 outputs are undefined */
   KVQ_DEV_BOUNDS = 1u << 5,   /* bounds-checked build only (libkvq_checked.so): a computed cache address
                                  fell outside its buffer segment; the access was skipped */
   KVQ_DEV_SEQ = 1u << 6       /* a sequence index of a page call outside [0, batch), listed twice where that is
@@ -380,7 +382,10 @@ KVQ_API kvq_status kvq_tbq4_codebook(float centroids[16], float thresholds[15]);
  * wait on a shared-memory barrier that nothing ever completes, bounded by
  * `polls` polls: the wait runs out, KVQ_DEV_STALL is set, the warp waits
  * (with the normal bound) for its bulk copies still in flight and the
- * kernel finishes; that call's outputs are undefined.  polls = 0 (the
+ * kernel finishes; that call's outputs are undefined.  In every second CTA
+ * of kvq_chunk_attention one of the roles (products, loads, dequantization,
+ * softmax, in turn) does the same and leaves; the others give up in turn, and the CTAs between
+ * finish their runs.  polls = 0 (the
  * default) turns it off.  Process-wide; polls outside [0, 2^20] give
  * KVQ_ERR_ARG.  Not for production use. */
 KVQ_API kvq_status kvq_test_force_stall(int32_t polls);
