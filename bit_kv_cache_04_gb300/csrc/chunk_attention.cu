@@ -10,7 +10,8 @@
 namespace kvq {
 namespace {
 
-// Workspace: status word, tickets and flags (zero between calls), partial rows.
+// Workspace: status word and the count of finished CTAs, tickets and flags (these zero between calls, also after one
+// that stalled), partial rows.
 struct ChunkWs {
   size_t tickets, nonfinite, partials, total;
   int grid;
@@ -99,6 +100,7 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
   if (cfg->flags & KVQ_K_PRE_ROPE)
     for (int i = 0; i < cfg->D / 2; ++i)
       a.turns[i] = (uint64_t)std::ldexp(std::pow((double)cfg->rope_theta, -2.0 * i / cfg->D) / 6.283185307179586476925286766559, 64);
+  a.left = a.status + 1;
   const ChunkWs w = chunk_ws(cfg);
   a.tickets = (uint32_t*)((char*)workspace + w.tickets);
   a.nonfinite = (uint32_t*)((char*)workspace + w.nonfinite);

@@ -78,6 +78,7 @@ struct ChunkArgs {
   int slots;        // pieces in the ring
   int stall_polls;  // > 0: failure-detection test mode (kvq_test_force_stall)
   uint32_t* status;
+  uint32_t* left;       // CTAs that have finished, and in the upper half those that gave up; zero between calls
   uint32_t* tickets;    // [grid][kChunkTickets]
   uint32_t* nonfinite;  // [grid][kChunkTickets]: a 16-bit window value of the unit is not finite
   float* partials;      // [grid][kChunkSlots][slot rows][part row]

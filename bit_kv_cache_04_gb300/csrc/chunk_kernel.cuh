@@ -2345,7 +2345,19 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
   // every role ends here, also after a wait that gave up
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && sh.gave_up) atomicOr(a.status, KVQ_DEV_STALL);
+  if (tid == 0) {
+    if (sh.gave_up) atomicOr(a.status, KVQ_DEV_STALL);
+    // Every CTA comes by here, whether its waits held or not.  The last one takes back what a stalled call has
+    // counted: its cut units have tickets that no CTA draws any more, and the next call would count on from them.
+    __threadfence();
+    const uint32_t before = atomicAdd(a.left, sh.gave_up ? 0x10001u : 1u);
+    if ((before & 0xffffu) == gridDim.x - 1) {
+      __threadfence();
+      if (sh.gave_up || before >> 16)
+        for (int i = 0; i < (int)gridDim.x * kChunkTickets; ++i) a.tickets[i] = a.nonfinite[i] = 0;
+      *a.left = 0;
+    }
+  }
   if (warp == C::MMA_WARP) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));

@@ -148,7 +148,7 @@ enum {
   KVQ_DEV_LENGTH = 1u << 3,   /* a sequence length < 0 or > max_T, or cu_new not ascending */
   KVQ_DEV_STALL = 1u << 4,    /* a bounded wait ran out: of a decode kernel for its own bulk copy into shared
                                  memory, or of a chunk attention role for another one of its CTA; that call's
-                                 outputs are undefined */
+                                 outputs are undefined, and the next call on the workspace is whole again */
   KVQ_DEV_BOUNDS = 1u << 5,   /* bounds-checked build only (libkvq_checked.so): a computed cache address
                                  fell outside its buffer segment; the access was skipped */
   KVQ_DEV_SEQ = 1u << 6       /* a sequence index of a page call outside [0, batch), listed twice where that is

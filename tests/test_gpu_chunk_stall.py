@@ -41,11 +41,11 @@ def started(name):
     cu = torch.tensor([sum(new[:i]) for i in range(len(new) + 1)], dtype=torch.int32, device="cuda")
     gen = torch.Generator(device="cuda").manual_seed(5)
     dt = torch.float16 if cfg.in_dtype == K.DT_F16 else torch.bfloat16
-    q = torch.randn((1, sum(new), cfg.H_q, cfg.D), generator=gen, device="cuda").to(dt)
+    qs = torch.randn((2, 1, sum(new), cfg.H_q, cfg.D), generator=gen, device="cuda").to(dt)
 
-    def call(ws):
-        out = torch.empty_like(q)
-        cache.chunk_attention(0, 1, q, cu, sum(new), max(new), lens, out, 0, 0, workspace=ws)
+    def call(ws, which=0):
+        out = torch.full_like(qs[0], float("nan"))
+        cache.chunk_attention(0, 1, qs[which], cu, sum(new), max(new), lens, out, 0, 0, workspace=ws)
         torch.cuda.synchronize()
         return out, ws[:4].view(torch.int32).item()
 
@@ -65,3 +65,22 @@ def test_a_wait_that_runs_out_sets_stall_and_returns(name):
         K.kvq_test_force_stall(0)
     out, status = call(cache.make_chunk_workspace())
     assert status == 0 and torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_the_next_call_on_the_same_workspace_is_whole(name):
+    """Sequences cut among CTAs are joined by a count of their parts: parts that a
+    stalled call counted must not be counted again."""
+    cache, call = started(name)
+    ws = cache.make_chunk_workspace()
+    refs = [call(ws, i)[0] for i in range(2)]
+    for _ in range(3):
+        K.kvq_test_force_stall(256)
+        try:
+            call(ws)
+        finally:
+            K.kvq_test_force_stall(0)
+        K._check(K.LIB.kvq_clear_device_status(ws.data_ptr(), None))
+        for i in (1, 0, 1):
+            out, status = call(ws, i)
+            assert status == 0 and torch.equal(out, refs[i])
