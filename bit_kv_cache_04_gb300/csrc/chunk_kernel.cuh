@@ -2417,17 +2417,17 @@ cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   if (a.slots > kChunkMaxSlots) a.slots = kChunkMaxSlots;
   if (a.slots < 1) return cudaErrorInvalidConfiguration;
   const uint32_t smem = C::FIXED + 16 + a.slots * a.slot_bytes;
-  cudaError_t e;
+  // The attribute belongs to the function and the current device, so it is set on every call, and always to the same
+  // value: another thread's call, of another format, may come between this and the launch.  Before the queries
+  // are turned: a failure here leaves `out` as it was.
+  cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
+  if (e != cudaSuccess) return e;
   if ((a.lo.flags & KVQ_ROTATE_K) && !a.turn_here) {
     const int64_t rows = (int64_t)a.n_layers * a.total_q;
     e = launch_dependent(turn_queries_kernel<D, DT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
     if (e != cudaSuccess) return e;
     a.q = a.out;
   }
-  // set on every call: the attribute belongs to the current device
-  e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, MODE>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   return launch_dependent(chunk_attention_kernel<D, DT, MODE>, dim3(grid), dim3(C::THREADS), smem, s, a);
 }
 

@@ -602,8 +602,8 @@ kvq_status kvq_pages_reserve(const kvq_config* cfg, const kvq_cache* cache, int3
   if (n == 0) return ok();
   const size_t smem = sizeof(int32_t) * (size_t)n;
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 48 * 1024)  // always to the same value: another thread may call between this and the launch
+    e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(sizeof(int32_t) * kMaxPageBatch));
   if (e == cudaSuccess) e = launch_dependent(reserve_kernel, dim3(1), dim3(kPlanThreads), smem, (cudaStream_t)stream, a);
   if (e == cudaSuccess) e = launch_copy<false>(a, n, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "page reserve kernels");
