@@ -7,6 +7,7 @@ memory and streams.  Importing this module without a built libkvq.so raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -250,6 +251,17 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _on(stream):
+    """The given stream (None: the current one) as torch's current one.  Memory
+    made in here belongs to it: the allocator hands out no block that another
+    stream's pending work still writes."""
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
+
+
 BUFFER_NAMES = ("k_main", "v_main", "k_cold", "v_cold", "k_resid", "v_resid")
 
 
@@ -306,7 +318,8 @@ class KVCache:
         _check(LIB.kvq_workspace_init(ctypes.byref(self.c_cfg), _ptr(self.workspace), self.ws_bytes,
                                       _stream(None)))
         self.chunk_ws_bytes = kvq_chunk_workspace_bytes(cfg)
-        self.chunk_workspace = None  # made by the first chunk_attention
+        self.chunk_workspace = None  # the last one that chunk_attention chose by itself
+        self._chunk_workspaces = {}  # by stream
 
     @classmethod
     def from_buffers(cls, cfg: Config, buffers: dict, block_table=None) -> "KVCache":
@@ -336,17 +349,22 @@ class KVCache:
                                    _ptr(self.workspace), self.ws_bytes, _stream(stream)))
 
     def make_chunk_workspace(self, stream=None):
-        """A prepared workspace for chunk_attention.  Calls that may run at
+        """A prepared workspace for chunk_attention, made on `stream`.  Calls that may run at
         the same time (other streams, graphs replayed side by side) each need one."""
         import torch
 
-        ws = torch.empty(self.chunk_ws_bytes, dtype=torch.uint8, device=self.device)
+        with _on(stream):
+            ws = torch.empty(self.chunk_ws_bytes, dtype=torch.uint8, device=self.device)
         _check(LIB.kvq_chunk_workspace_init(ctypes.byref(self.c_cfg), _ptr(ws), self.chunk_ws_bytes, _stream(stream)))
         return ws
 
     def chunk_attention(self, layer0, n_layers, q, cu_q, total_q, max_q, seq_lens, out, window=0, sinks=0, stream=None,
                         workspace=None):
-        """Attention of the last cu_q[b+1] - cu_q[b] cached tokens of every sequence (kvq_chunk_attention)."""
+        """Attention of the last cu_q[b+1] - cu_q[b] cached tokens of every sequence (kvq_chunk_attention).
+
+        Without a workspace the cache keeps one for each stream (chunk_ws_bytes,
+        made by the stream's first call).  A captured call without one takes the capturing stream's, else the one
+        of the cache's last call: its replays then must not run beside other calls with that workspace."""
         import torch
 
         cfg = self.cfg
@@ -357,16 +375,26 @@ class KVCache:
         for t, n in ((cu_q, cfg.batch + 1), (seq_lens, cfg.batch)):
             if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
                 raise ValueError("cu_q [batch + 1] and seq_lens [batch] are contiguous int32 tensors")
-        if workspace is None:
-            if self.chunk_workspace is None:
-                if torch.cuda.is_current_stream_capturing():
-                    raise RuntimeError("the first chunk_attention prepares its workspace: make it before the capture")
-                self.chunk_workspace = self.make_chunk_workspace(stream)
-            workspace = self.chunk_workspace
         _here(self.index, q, out, cu_q, seq_lens, workspace)
+        if workspace is None:
+            workspace = self.chunk_workspace = self._chunk_workspace_of(stream)
         _check(LIB.kvq_chunk_attention(ctypes.byref(self.c_cfg), ctypes.byref(self.c_cache), layer0, n_layers,
                                        _ptr(q), _ptr(cu_q), total_q, max_q, _ptr(seq_lens), window, sinks, _ptr(out),
                                        _ptr(workspace), workspace.numel(), _stream(stream)))
+
+    def _chunk_workspace_of(self, stream):
+        import torch
+
+        handle = _stream(stream)
+        if handle not in self._chunk_workspaces:
+            with _on(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if capturing:  # nothing can be prepared in here once and for all
+                if self.chunk_workspace is None:
+                    raise RuntimeError("the first chunk_attention prepares its workspace: make it before the capture")
+                return self.chunk_workspace
+            self._chunk_workspaces[handle] = self.make_chunk_workspace(stream)
+        return self._chunk_workspaces[handle]
 
     def dequantize(self, layer, seq, t0, t1, seq_lens, k_out, v_out, stream=None):
         _check(LIB.kvq_dequantize(ctypes.byref(self.c_cfg), ctypes.byref(self.c_cache), layer, seq, t0, t1,
@@ -443,8 +471,9 @@ class PagePool:
 
         self.cache, self.index = cache, cache.index
         self.ws_bytes = kvq_pages_workspace_bytes(cache.cfg)
-        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=cache.device)
-        self.refs = refs if refs is not None else torch.empty(cache.cfg.n_pages, dtype=torch.int32, device=cache.device)
+        with _on(stream):
+            self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=cache.device)
+            self.refs = refs if refs is not None else torch.empty(cache.cfg.n_pages, dtype=torch.int32, device=cache.device)
         if self.refs.dtype != torch.int32 or self.refs.numel() != cache.cfg.n_pages or not self.refs.is_contiguous():
             raise ValueError("refs is a contiguous int32 tensor of n_pages")
         _here(self.index, self.refs)

@@ -1,0 +1,91 @@
+"""The serving entries on several streams: workspaces that the cache makes by
+itself, and memory that another stream still writes."""
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+from bit_kv_cache_04_gb300 import kvq as K  # noqa: E402
+from tests.test_gpu_serving_threads import started  # noqa: E402
+
+LONG = 50_000_000  # clock cycles: some 25 ms
+
+
+def dirty_block(nbytes):
+    """A block of the allocator that holds ones, free again, with a write of the current stream still to come."""
+    torch.cuda.empty_cache()
+    x = torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(LONG)
+    x.fill_(255)
+
+
+def test_a_workspace_made_for_another_stream_is_not_overwritten():
+    cache, call, refs = started()
+    side, out = torch.cuda.Stream(), torch.empty_like(refs[0])
+    dirty_block(cache.chunk_ws_bytes)
+    ws = cache.make_chunk_workspace(stream=side)
+    torch.cuda.synchronize()
+    assert not ws[:1024].any()  # prepared, and nothing has written to it since
+    call(out, workspace=ws, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, refs[0])
+
+
+def test_the_cache_s_own_workspace_on_several_streams():
+    cache, call, refs = started()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = torch.full_like(refs, float("nan"))
+    dirty_block(cache.chunk_ws_bytes)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(streams[0]):
+        torch.cuda._sleep(LONG)  # the first call waits here, with the preparation of its workspace
+    for i, s in enumerate(streams):
+        call(outs[i], i, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs, refs)
+    for _ in range(50):
+        outs.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            call(outs[i], i, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(outs, refs)
+
+
+def test_a_page_pool_made_on_another_stream_is_not_overwritten():
+    cache, _, _ = started()
+    ref = K.PagePool(cache).refs.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for nbytes in (K.kvq_pages_workspace_bytes(cache.cfg), 4 * cache.cfg.n_pages):
+        dirty_block(nbytes)
+        pool = K.PagePool(cache, stream=side)
+        torch.cuda.synchronize()
+        assert pool.refs.tolist() == ref.tolist() and pool.device_status() == 0
+
+
+def test_a_captured_call_takes_a_prepared_workspace():
+    cache, call, refs = started()
+    out, g = torch.empty_like(refs[0]), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(RuntimeError, match="before the capture"):
+            call(out)
+    call(out, 1)
+    own = cache.chunk_workspace
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        call(out)  # the eager call's workspace
+    assert cache.chunk_workspace is own
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, refs[0])
+    with torch.cuda.stream(side):
+        call(out, 2)  # now the stream has one
+    torch.cuda.synchronize()
+    assert cache.chunk_workspace is not own and torch.equal(out, refs[2])
