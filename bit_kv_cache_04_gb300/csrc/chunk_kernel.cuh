@@ -545,10 +545,15 @@ __device__ __forceinline__ uint32_t clean(uint32_t w, int which, volatile uint32
 template <int DT>
 __device__ __forceinline__ void raw_token_run(const ChunkArgs& a, const CachePos& u, int which, int t, int run,
                                               volatile uint32_t* nonfinite, uint32_t (&h)[16]) {
+  if (t >= u.T) {  // no address is formed: a cache without a window has no slots (and comes by here behind its last token)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) h[j] = 0;
+    return;
+  }
   const uint4* p = reinterpret_cast<const uint4*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t)) + run * 4;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint4 v = t < u.T ? p[j] : make_uint4(0, 0, 0, 0);
+    const uint4 v = p[j];
     h[4 * j] = clean<DT>(v.x, which, nonfinite);
     h[4 * j + 1] = clean<DT>(v.y, which, nonfinite);
     h[4 * j + 2] = clean<DT>(v.z, which, nonfinite);
