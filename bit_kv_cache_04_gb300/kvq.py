@@ -455,6 +455,8 @@ def qk_norm_rope(cfg: Config, q, k, positions, q_out, k_out, plan=None, q_weight
                              not positions.is_contiguous()):
         raise ValueError("positions is a contiguous int32 tensor, one of each token")
     _here(some.get_device(), q, k, q_out, k_out, q_weight, k_weight, positions)
+    if n == 0:  # empty tensors have no address
+        return
     qs = (0, 0) if q is None else q.stride()
     ks = (0, 0) if k is None else k.stride()
     _check(LIB.kvq_qk_norm_rope(ctypes.byref(_to_c(cfg)), None if plan is None else ctypes.byref(plan), _ptr(q), qs[0],

@@ -1,0 +1,28 @@
+"""Calls at the edge of what the serving entries take, on the CPU: nothing is launched here."""
+
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+K = pytest.importorskip("bit_kv_cache_04_gb300.kvq")
+
+A = 1 << 20  # an aligned address that nothing reads
+
+
+def _cfg(**kw):
+    base = dict(L=2, H_kv=2, H_q=4, D=128, batch=3, max_T=64, k_fmt=K.Fmt(4, 128), v_fmt=K.Fmt(4, 128))
+    base.update(kw)
+    return K.Config(**base)
+
+
+@pytest.mark.parametrize("with_k", [False, True])
+@pytest.mark.parametrize("plan", [None, 128])
+def test_norm_rope_of_no_tokens_is_nothing_in_python(with_k, plan):
+    """Empty tensors have no address, which the C entry takes for a missing tensor."""
+    q, k = torch.zeros((0, 4, 128), dtype=torch.float16), torch.zeros((0, 2, 128), dtype=torch.float16)
+    w, pos = torch.ones(128, dtype=torch.float16), torch.zeros(0, dtype=torch.int32)
+    K.qk_norm_rope(_cfg(), q, k if with_k else None, pos, q.clone(), k.clone() if with_k else None,
+                   plan=plan and K.rope_plan(plan), q_weight=w, k_weight=w if with_k else None, stream=0)
+    with pytest.raises(ValueError):  # the checks stay
+        K.qk_norm_rope(_cfg(), q, None, pos, q.float(), None, stream=0)
