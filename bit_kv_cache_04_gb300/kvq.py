@@ -266,11 +266,13 @@ BUFFER_NAMES = ("k_main", "v_main", "k_cold", "v_cold", "k_resid", "v_resid")
 
 
 def _here(index, *tensors) -> None:
-    """The tensors live on device `index` (-1: the host), and that is the current one: streams and launches belong to it."""
+    """The tensors live on GPU `index`, and that is the current one: streams and launches belong to it."""
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError(f"a tensor is on {t.device}, not on device {index}")
-    if index >= 0 and index != _current_device():
+    if index < 0:
+        raise ValueError("tensors must be on a GPU")
+    if index != _current_device():
         raise ValueError(f"device {index} is not the current one")
 
 
@@ -454,9 +456,9 @@ def qk_norm_rope(cfg: Config, q, k, positions, q_out, k_out, plan=None, q_weight
     if plan is not None and (positions is None or positions.dtype != torch.int32 or positions.numel() != n or
                              not positions.is_contiguous()):
         raise ValueError("positions is a contiguous int32 tensor, one of each token")
-    _here(some.get_device(), q, k, q_out, k_out, q_weight, k_weight, positions)
     if n == 0:  # empty tensors have no address
         return
+    _here(some.get_device(), q, k, q_out, k_out, q_weight, k_weight, positions)
     qs = (0, 0) if q is None else q.stride()
     ks = (0, 0) if k is None else k.stride()
     _check(LIB.kvq_qk_norm_rope(ctypes.byref(_to_c(cfg)), None if plan is None else ctypes.byref(plan), _ptr(q), qs[0],

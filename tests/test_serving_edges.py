@@ -26,3 +26,18 @@ def test_norm_rope_of_no_tokens_is_nothing_in_python(with_k, plan):
                    plan=plan and K.rope_plan(plan), q_weight=w, k_weight=w if with_k else None, stream=0)
     with pytest.raises(ValueError):  # the checks stay
         K.qk_norm_rope(_cfg(), q, None, pos, q.float(), None, stream=0)
+
+
+def test_host_tensors_are_refused():
+    """Their addresses would go to a kernel."""
+    q, n = torch.zeros((3, 4, 128), dtype=torch.float16), torch.ones(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        K.qk_norm_rope(_cfg(), q, None, None, q.clone(), None, stream=0)
+    c = K.KVCache.__new__(K.KVCache)
+    c.cfg, c.index, c.chunk_workspace = _cfg(), -1, None
+    with pytest.raises(ValueError, match="GPU"):
+        c.chunk_attention(0, 1, q[None], torch.zeros(4, dtype=torch.int32), 3, 1, n, q[None].clone(), stream=0)
+    pool = K.PagePool.__new__(K.PagePool)
+    pool.cache, pool.index = c, -1
+    with pytest.raises(ValueError, match="GPU"):
+        pool.release(n, n)
