@@ -311,8 +311,8 @@ class KVCache:
         if buffers is not None:
             if len({t.device for t in (*self.buffers.values(), self.block_table) if t is not None}) > 1:
                 raise ValueError("buffers and block table are on one device")
-            if cfg.page_tokens and (block_table is None or self.block_table.numel() < cfg.batch * cfg.max_pages_per_seq):
-                raise ValueError("a paged cache needs a block table [batch, max_pages_per_seq]")
+            if cfg.page_tokens:
+                self._check_table()
         self.ws_bytes = kvq_workspace_bytes(cfg)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self.index = self.workspace.get_device()
@@ -329,6 +329,10 @@ class KVCache:
         BUFFER_NAMES, in the layout of include/kvq.h); they are used as they
         are, and so is an int32 block table on their device."""
         return cls(cfg, next(iter(buffers.values())).device, block_table, buffers)
+
+    def _check_table(self):
+        if self.block_table is None or self.block_table.numel() < self.cfg.batch * self.cfg.max_pages_per_seq:
+            raise ValueError("a paged cache needs a block table [batch, max_pages_per_seq]")
 
     # -- the C calls ----------------------------------------------------------
 
@@ -378,6 +382,8 @@ class KVCache:
             if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
                 raise ValueError("cu_q [batch + 1] and seq_lens [batch] are contiguous int32 tensors")
         _here(self.index, q, out, cu_q, seq_lens, workspace)
+        if cfg.page_tokens:
+            self._check_table()
         if workspace is None:
             workspace = self.chunk_workspace = self._chunk_workspace_of(stream)
         _check(LIB.kvq_chunk_attention(ctypes.byref(self.c_cfg), ctypes.byref(self.c_cache), layer0, n_layers,
@@ -473,6 +479,7 @@ class PagePool:
     def __init__(self, cache: KVCache, refs=None, stream=None):
         import torch
 
+        cache._check_table()
         self.cache, self.index = cache, cache.index
         self.ws_bytes = kvq_pages_workspace_bytes(cache.cfg)
         with _on(stream):

@@ -41,3 +41,19 @@ def test_host_tensors_are_refused():
     pool.cache, pool.index = c, -1
     with pytest.raises(ValueError, match="GPU"):
         pool.release(n, n)
+
+
+def test_a_paged_cache_needs_its_whole_block_table(monkeypatch):
+    """The page calls write the table of every sequence, and chunk attention reads it."""
+    monkeypatch.setattr(K, "_here", lambda *_: None)
+    cfg = _cfg(page_tokens=16, n_pages=20, max_pages_per_seq=4)
+    c = K.KVCache.__new__(K.KVCache)
+    c.cfg, c.c_cfg, c.index, c.device = cfg, K._to_c(cfg), -1, torch.device("cpu")
+    for table in (None, torch.zeros((3, 3), dtype=torch.int32)):
+        c.block_table = table
+        with pytest.raises(ValueError, match="block table"):
+            K.PagePool(c, stream=None)
+    c.chunk_workspace, c.index = None, -1
+    q, n = torch.zeros((1, 3, 4, 128), dtype=torch.float16), torch.ones(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="block table"):
+        c.chunk_attention(0, 1, q, torch.zeros(4, dtype=torch.int32), 3, 1, n, q.clone(), stream=0)
