@@ -482,12 +482,21 @@ cudaError_t launch_copy(const PagesArgs& a, int64_t max_moves, cudaStream_t s) {
 
 // ---- host checks shared by the entries ------------------------------------------------
 
-kvq_status pages_args(const kvq_config* cfg, const kvq_cache* cache, bool need_cache, const int32_t* table,
-                      const int32_t* refs, void* workspace, size_t ws_bytes, PagesArgs* a) {
-  kvq_status st = check_config(cfg, false);
+// What the bookkeeping holds: pages needed by one call, a copy for each sequence among them, are counted in 32 bits.
+kvq_status pages_config(const kvq_config* cfg) {
+  const kvq_status st = check_config(cfg, false);
   if (st != KVQ_OK) return st;
   if (cfg->page_tokens < 1) return fail(KVQ_ERR_ARG, "the cache is not paged");
   if (cfg->batch > kMaxPageBatch) return fail(KVQ_ERR_UNSUPPORTED, "batch=%d > %d", cfg->batch, kMaxPageBatch);
+  if ((int64_t)cfg->batch * ((int64_t)cfg->max_pages_per_seq + 1) > 0x7fffffff)
+    return fail(KVQ_ERR_UNSUPPORTED, "a block table of %d x %d entries", cfg->batch, cfg->max_pages_per_seq);
+  return KVQ_OK;
+}
+
+kvq_status pages_args(const kvq_config* cfg, const kvq_cache* cache, bool need_cache, const int32_t* table,
+                      const int32_t* refs, void* workspace, size_t ws_bytes, PagesArgs* a) {
+  kvq_status st = pages_config(cfg);
+  if (st != KVQ_OK) return st;
   if (!table || !refs) return fail(KVQ_ERR_ARG, "block_table / refs is NULL");
   if (((uintptr_t)table | (uintptr_t)refs) & 3u) return fail(KVQ_ERR_ARG, "block_table / refs must be 4-byte aligned");
   if (!workspace) return fail(KVQ_ERR_WORKSPACE, "workspace is NULL");
@@ -533,11 +542,9 @@ using namespace kvq;
 extern "C" {
 
 kvq_status kvq_pages_workspace_bytes(const kvq_config* cfg, size_t* bytes) {
-  kvq_status st = check_config(cfg, false);
+  const kvq_status st = pages_config(cfg);
   if (st != KVQ_OK) return st;
   if (!bytes) return fail(KVQ_ERR_ARG, "bytes is NULL");
-  if (cfg->page_tokens < 1) return fail(KVQ_ERR_ARG, "the cache is not paged");
-  if (cfg->batch > kMaxPageBatch) return fail(KVQ_ERR_UNSUPPORTED, "batch=%d > %d", cfg->batch, kMaxPageBatch);
   *bytes = pages_ws_layout(cfg, nullptr, nullptr);
   return ok();
 }

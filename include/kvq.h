@@ -490,7 +490,8 @@ KVQ_API kvq_status kvq_qk_norm_rope(const kvq_config* cfg, const kvq_rope_plan* 
  * is read by all of them and written by none: before tokens are appended,
  * kvq_pages_reserve gives the sequence its own copy of a partly filled page.
  *
- * All need a paged config (page_tokens > 0) with batch <= 32768.  The
+ * All need a paged config (page_tokens > 0) with batch <= 32768 and
+ * batch * (max_pages_per_seq + 1) < 2^31.  The
  * workspace is of kvq_pages_workspace_bytes, 256-byte aligned, prepared by
  * kvq_pages_init; its first word is the device status word
  * (kvq_read_device_status).  Lists (seqs, src, dst, n_new) are int32 on the

@@ -57,3 +57,25 @@ def test_a_paged_cache_needs_its_whole_block_table(monkeypatch):
     q, n = torch.zeros((1, 3, 4, 128), dtype=torch.float16), torch.ones(3, dtype=torch.int32)
     with pytest.raises(ValueError, match="block table"):
         c.chunk_attention(0, 1, q, torch.zeros(4, dtype=torch.int32), 3, 1, n, q.clone(), stream=0)
+
+
+PAGED = dict(page_tokens=16, n_pages=20, max_pages_per_seq=4)
+
+
+def _cache():
+    return ctypes.byref(K._Cache(A, A, None, None, A, A, A))
+
+
+def test_page_calls_count_pages_in_32_bits():
+    """One reservation may ask for every page of the table: more than 2^31 - 1 wrapped, and passed for enough."""
+    out = ctypes.c_size_t()
+    for batch, pages, good in ((32768, 65534, True), (32768, 65535, False), (30000, 2 ** 30, False), (1, 2 ** 31 - 2, True)):
+        cfg = _cfg(L=1, batch=batch, page_tokens=1, n_pages=20, max_pages_per_seq=pages)
+        c = ctypes.byref(K._to_c(cfg))
+        assert K.LIB.kvq_pages_workspace_bytes(c, ctypes.byref(out)) == (0 if good else 2), (batch, pages)
+        if not good:
+            assert K.LIB.kvq_pages_init(c, A, A, A, 1 << 40, None) == 2
+            assert K.LIB.kvq_pages_release(c, A, A, A, A, 1, A, 1 << 40, None) == 2
+            assert K.LIB.kvq_pages_fork(c, _cache(), A, A, A, A, A, 1, A, 1 << 40, None) == 2
+            assert K.LIB.kvq_pages_reserve(c, _cache(), A, A, A, A, A, 1, A, 1 << 40, None) == 2
+            assert K.LIB.kvq_pages_compact(c, _cache(), A, A, A, A, A, 1 << 40, None) == 2
