@@ -583,10 +583,10 @@ kvq_status kvq_pages_fork(const kvq_config* cfg, const kvq_cache* cache, int32_t
   kvq_status st = pages_args(cfg, cache, true, block_table, refs, workspace, ws_bytes, &a);
   if (st != KVQ_OK) return st;
   if ((st = list_args(cfg, seq_lens, src, dst, n, &a)) != KVQ_OK) return st;
+  if (a.lo.ring && a.lo.L > 65535) return fail(KVQ_ERR_UNSUPPORTED, "L=%d", a.lo.L);  // a row of the windows' grid each
   if (n == 0) return ok();
   cudaError_t e = launch_dependent(fork_kernel, dim3(n), dim3(256), 0, (cudaStream_t)stream, a);
   if (e == cudaSuccess && a.lo.ring) {
-    if (a.lo.L > 65535) return fail(KVQ_ERR_UNSUPPORTED, "L=%d", a.lo.L);
     // parts of a window of about 64 KiB, more while the grid is small
     const int64_t bytes = (int64_t)a.lo.H * a.lo.ring * a.lo.D * 2;
     const int64_t blocks = (int64_t)n * a.lo.L * 2;

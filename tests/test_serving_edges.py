@@ -79,3 +79,10 @@ def test_page_calls_count_pages_in_32_bits():
             assert K.LIB.kvq_pages_fork(c, _cache(), A, A, A, A, A, 1, A, 1 << 40, None) == 2
             assert K.LIB.kvq_pages_reserve(c, _cache(), A, A, A, A, A, 1, A, 1 << 40, None) == 2
             assert K.LIB.kvq_pages_compact(c, _cache(), A, A, A, A, A, 1 << 40, None) == 2
+
+
+def test_fork_refuses_before_it_launches():
+    """The table's part was launched before the windows' grid was looked at."""
+    cfg = _cfg(L=65536, H_kv=1, H_q=1, residual_window=8, **PAGED)
+    n = K.kvq_pages_workspace_bytes(cfg)
+    assert K.LIB.kvq_pages_fork(ctypes.byref(K._to_c(cfg)), _cache(), A, A, A, A, A, 1, A, n, None) == 2
