@@ -327,9 +327,13 @@ kvq_status kvq_qk_norm_rope(const kvq_config* cfg, const kvq_rope_plan* plan, co
   if (any & 1u) return fail(KVQ_ERR_ARG, "tensors must be aligned to their elements");
   if (q_token_stride < 0 || q_head_stride < 0 || k_token_stride < 0 || k_head_stride < 0)
     return fail(KVQ_ERR_ARG, "negative stride");
-  if (q && q == q_out && (q_head_stride != cfg->D || q_token_stride != (int64_t)cfg->H_q * cfg->D))
+  // the stride of a dimension of one element says nothing
+  auto contiguous = [&](int64_t token_stride, int64_t head_stride, int64_t heads) {
+    return (heads == 1 || head_stride == cfg->D) && (n_tokens <= 1 || token_stride == heads * cfg->D);
+  };
+  if (q && q == q_out && !contiguous(q_token_stride, q_head_stride, cfg->H_q))
     return fail(KVQ_ERR_ARG, "q in place must be contiguous");
-  if (k && k == k_out && (k_head_stride != cfg->D || k_token_stride != (int64_t)cfg->H_kv * cfg->D))
+  if (k && k == k_out && !contiguous(k_token_stride, k_head_stride, cfg->H_kv))
     return fail(KVQ_ERR_ARG, "k in place must be contiguous");
   if (n_tokens == 0) return ok();
   NormRopeArgs a{};
