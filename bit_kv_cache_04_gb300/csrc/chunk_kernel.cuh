@@ -932,6 +932,8 @@ struct Loader {
       *src = (cold ? cold0 : main0) + (int64_t)r * row;
     }
     const int bytes = per_channel ? row : row << a.copy_shift;
+    [[maybe_unused]] const CachePtrs& cp = a.cp;
+    if (!KVQ_CHECK(*at + bytes <= a.slot_bytes)) return 0;
     return span_ok(a.lo, a.cp, which + (cold ? 2 : 0), *src, bytes) ? bytes : 0;
   }
 };

@@ -168,6 +168,9 @@ __global__ void fork_window_kernel(PagesArgs a, int parts) {
   const int which = blockIdx.z / parts, part = blockIdx.z % parts;
   const int64_t unit = (int64_t)a.lo.H * a.lo.ring * a.lo.D / 8;  // 16-byte words of one (layer, sequence)
   uint4* base = reinterpret_cast<uint4*>(which ? a.cp.v_resid : a.cp.k_resid);
+  [[maybe_unused]] const CachePtrs& cp = a.cp;
+  if (!KVQ_CHECK((int)blockIdx.y < a.lo.L && (uint32_t)a.seqs[i] < (uint32_t)a.lo.B && (uint32_t)a.other[i] < (uint32_t)a.lo.B))
+    return;
   const uint4* from = base + ((int64_t)blockIdx.y * a.lo.B + a.seqs[i]) * unit;
   uint4* to = base + ((int64_t)blockIdx.y * a.lo.B + a.other[i]) * unit;
   const int64_t per = (unit + parts - 1) / parts, e1 = min(unit, (part + 1) * per);
@@ -448,6 +451,10 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(PagesArgs a, int k_word
     const int64_t m = q / a.lo.L;
     const int words = which ? v_words : k_words;
     V* base = reinterpret_cast<V*>(which ? a.cp.v_main : a.cp.k_main);
+    [[maybe_unused]] const CachePtrs& cp = a.cp;
+    if (!KVQ_CHECK((uint32_t)a.ws.src[m] < (uint32_t)(a.lo.n_pages - a.lo.bounds_shrink) &&
+                   (uint32_t)a.ws.dst[m] < (uint32_t)(a.lo.n_pages - a.lo.bounds_shrink)))
+      continue;
     const V* from = base + ((int64_t)layer * a.lo.n_pages + a.ws.src[m]) * words;
     V* to = base + ((int64_t)layer * a.lo.n_pages + a.ws.dst[m]) * words;
     int e = threadIdx.x;
@@ -516,6 +523,7 @@ kvq_status pages_args(const kvq_config* cfg, const kvq_cache* cache, bool need_c
   if ((int64_t)a->lo.H * a->lo.pt * std::max(a->lo.kf.row, a->lo.vf.row) > (int64_t)1 << 30)
     return fail(KVQ_ERR_UNSUPPORTED, "pages of more than 1 GiB");
   pages_ws_layout(cfg, workspace, &a->ws);
+  a->cp.status = a->ws.status;
   a->table = const_cast<int32_t*>(table);
   a->refs = const_cast<int32_t*>(refs);
   return KVQ_OK;

@@ -1,8 +1,8 @@
 """The serving operators in the bounds-checked build (libkvq_checked.so, see
 tests/test_gpu_bounds.py): chunk attention of every format, with windows and
-without, at ragged lengths, in all forms.  No check fires, the outputs keep
-their bounds, and with every segment's last row taken away the checks do
-fire."""
+without, at ragged lengths, in all forms; histories of page calls.  No check
+fires, the results are those of the oracle, and with every segment's last row (or
+the pool's last page) taken away the checks do fire."""
 
 import json
 import os
@@ -24,6 +24,7 @@ def _checked_run():
     """Runs in a fresh interpreter with KVQ_LIBRARY pointing at the checked build."""
     from bit_kv_cache_04_gb300 import kvq as K
     from tests import test_gpu_chunk_attention as C
+    from tests import test_gpu_pages as P
 
     assert K.LIB_PATH.endswith("libkvq_checked.so"), K.LIB_PATH
     for key, (name, kw) in C.FORMATS.items():
@@ -34,12 +35,18 @@ def _checked_run():
     for T in (1, 31, 33, 64, 65, 129):
         C.check(C.workload("gqa8b_hadamard4_paged", [T], heads=(1, 8)), [T])
         C.check(C.workload("ctx262k_hadamard4", [T], heads=(1, 6)), [T])
+    for shape in (dict(), dict(R=20), dict(pt=1, pages=300, max_T=40), dict(pt=7, R=5, D=256, pages=60),
+                  dict(fmt=K.Fmt(3, 128), vfmt=K.Fmt(4, 32), pt=5, H=1, L=1, pages=80)):
+        P.test_random_histories(shape)  # ends with a clean status word
+    P.test_compact_out_of_place(1025)
+    P.test_last_reader_keeps_the_page()
     print("clean")
 
 
 def _shrunk_run():
     from bit_kv_cache_04_gb300 import kvq as K
     from tests import test_gpu_chunk_attention as C
+    from tests import test_gpu_pages as P
     from tests.gpu_cases import appended_cache
 
     res = {}
@@ -56,6 +63,15 @@ def _shrunk_run():
         finally:
             K.kvq_test_shrink_bounds(0)
         res[name] = cache.chunk_workspace[:4].view(torch.int32).item()
+    # the pool's last page, moved to the first
+    cache, pool, _, _ = P.make(batch=2, max_T=64, pages=8, table=[[7, -1, -1, -1], [-1, -1, -1, -1]])
+    K.kvq_test_shrink_bounds(1)
+    try:
+        pool.compact()
+        torch.cuda.synchronize()
+    finally:
+        K.kvq_test_shrink_bounds(0)
+    res["compact"] = pool.device_status()
     print(json.dumps(res))
 
 
