@@ -1134,21 +1134,78 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, ChunkShared& sh) 
   }
 }
 
+// Row r of a row tile: where its query (or output) starts.
+__device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, int r) {
+  const int row = u.r0 + r, tok = div_g(a, row);
+  return (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + u.h * a.lo.g + (row - tok * a.lo.g)) * a.lo.D;
+}
+
 // V's values that are not finite were left out of the products: every row
-// that sees such a window token gets the value itself (an infinity stays one
-// under any positive weight, a NaN stays NaN).  Channels [ch, ch + n) of the written output row of
-// query position p.
-template <int DT>
-__device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Run& run, int p, int ch, int n, uint16_t* out) {
-  const int qe = q_end_of(a.lo, run.u.T);
-  for (int t = qe; t <= p; ++t) {
-    if (a.window && t <= p - a.window && t >= a.sinks) continue;
-    const uint16_t* v = resid_row(a.lo, a.cp, 1, run.u.layer + a.layer0, run.u.b, run.u.h, t);
-    for (int c = ch; c < ch + n; ++c) {
-      const float x = in_to_f32(v[c], DT);
-      if (!(fabsf(x) <= 3.402823466e38f)) out[c] = (uint16_t)pack16<DT>(in_to_f32(out[c], DT) + x, 0.f);
+// that sees such a window token gets them afterwards (an infinity stays one
+// under any positive weight, a NaN stays NaN).  What a row gets depends on the kinds that it sees in a channel,
+// not on how many: the tokens that all rows of a run's unit see are gone through once a warp, and a
+// row adds the few that only some see.  (Gone through by every row, one such value in a 16-bit window of 16K tokens
+// held a call of 128 rows of 256 channels up for 585 ms.)
+
+// Kinds among window tokens [t0, t1) of this lane's channels (4 lane .. of every 128-chunk): of chunk c, bits
+// 12 c + e: +inf in channel e, + 4: -inf, + 8: NaN.
+template <int D, int DT>
+__device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, const Run& run, int t0, int t1) {
+  constexpr uint32_t E = DT == KVQ_DT_F16 ? 0x7c00u : 0x7f80u;
+  constexpr int N = D / 128, U = 16 / N;  // loads in flight
+  const int lane = threadIdx.x & 31;
+  uint32_t kinds = 0;
+#pragma unroll 1
+  for (int t = max(t0, q_end_of(a.lo, run.u.T)); t < t1; t += U) {
+    uint2 v[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint2* p = reinterpret_cast<const uint2*>(
+                           resid_row(a.lo, a.cp, 1, run.u.layer + a.layer0, run.u.b, run.u.h, min(t + u, t1 - 1))) + lane;
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[u][c] = p[32 * c];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = e & 2 ? v[u][c].y : v[u][c].x, x = e & 1 ? w >> 16 : w & 0xffffu;
+          if ((x & E) == E) kinds |= 1u << (12 * c + e + (x & (0x7fffu & ~E) ? 8 : x >> 15 ? 4 : 0));
+        }
+  }
+  return kinds;
+}
+// Adds them to the unit's output rows r0, r0 + step, .. below r1, which this warp has written.
+template <int D, int DT>
+__device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Run& run, int r0, int r1, int step) {
+  const Unit& u = run.u;
+  const int lo = a.window ? max(0, u.p_hi - a.window + 1) : 0;
+  __syncwarp();
+  if (r0 >= r1) return;
+  // what every row of the unit sees
+  const uint32_t common = window_kinds<D, DT>(a, run, 0, u.sink) | window_kinds<D, DT>(a, run, lo, u.p_lo + 1);
+#pragma unroll 1
+  for (int r = r0; r < r1; r += step) {
+    const int p = u.T - u.n + div_g(a, u.r0 + r), w = a.window ? max(0, p - a.window + 1) : 0;
+    // and the row alone: the sinks that have left its window, what is before and behind the common tokens
+    const uint32_t kinds = common | window_kinds<D, DT>(a, run, u.sink, min(a.sinks, w)) |
+                           window_kinds<D, DT>(a, run, w, min(lo, p + 1)) | window_kinds<D, DT>(a, run, max(u.p_lo + 1, w), p + 1);
+    uint16_t* out = a.out + query_row(a, u, r) + 4 * (threadIdx.x & 31);
+#pragma unroll 1
+    for (int e = 0; e < D / 32; ++e) {  // channel e & 3 of chunk e >> 2
+      const uint32_t k = kinds >> (12 * (e >> 2) + (e & 3));
+      if (!(k & 0x111u)) continue;
+      uint16_t* o = out + 128 * (e >> 2) + (e & 3);
+      float x = in_to_f32(*o, DT);
+      if (k & 1u) x += INFINITY;
+      if (k & 0x10u) x -= INFINITY;
+      if (k & 0x100u) x = NAN;
+      *o = (uint16_t)pack16<DT>(x, 0.f);
     }
   }
+  __syncwarp();
 }
 
 // All softmax warps meet (boundedly, like every wait): false once a warp has given up.
@@ -1160,16 +1217,10 @@ __device__ __forceinline__ bool soft_sync(uint32_t bar, uint32_t& phase, volatil
   return ok;
 }
 
-// Row r of a row tile: where its query (or output) starts.
-__device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, int r) {
-  const int row = u.r0 + r, tok = div_g(a, row);
-  return (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + u.h * a.lo.g + (row - tok * a.lo.g)) * a.lo.D;
-}
-
 // One output row, four channels of a 128-chunk a lane: acc / L, out of the rotated domain.  (s1, s2): the lane's signs.
 template <int D, int DT>
 __device__ __forceinline__ void write_row(const ChunkArgs& a, const Run& run, int r, float (&acc)[D / 128][4], float L, uint32_t s1,
-                                          uint32_t s2, bool fix) {
+                                          uint32_t s2) {
   const int lane = threadIdx.x & 31;
   uint16_t* dst = a.out + query_row(a, run.u, r);
   const float inv = 1.f / L;
@@ -1178,7 +1229,6 @@ __device__ __forceinline__ void write_row(const ChunkArgs& a, const Run& run, in
     float v[4] = {acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv};
     if (a.lo.flags & KVQ_ROTATE_V) rotate_lanes(v, s2, s1);
     *reinterpret_cast<uint2*>(dst + 128 * c + 4 * lane) = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
-    if (fix) add_nonfinite<DT>(a, run, run.u.T - run.u.n + div_g(a, run.u.r0 + r), 128 * c + 4 * lane, 4, dst);
   }
 }
 
@@ -1218,7 +1268,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
     return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
   const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
-  auto write = [&](int r, float (&acc)[N][4], float L) { write_row<D, DT>(a, run, r, acc, L, s1, s2, fix); };
+  auto write = [&](int r, float (&acc)[N][4], float L) { write_row<D, DT>(a, run, r, acc, L, s1, s2); };
   if (PAIRED && parts <= 4) {
     // Many rows of few parts: a lane works out the weights of one row of the
     // warp's 32; then row by row, the next row's loads in flight.
@@ -1269,6 +1319,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
       load(r + 1);
       write(r, acc, __shfl_sync(0xffffffffu, L, r - r0));
     }
+    if (fix) add_nonfinite<D, DT>(a, run, r0, min(r0 + 32, u.rows), 1);
     return true;
   }
   // Few rows: `wpr` warps share a row's parts and join their sums in shared memory.
@@ -1349,6 +1400,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
     }
     if (rr < u.rows) write(r, acc, L);
   }
+  if (fix && sub == 0) add_nonfinite<D, DT>(a, run, warp / wpr, u.rows, per);
   return true;
 }
 
@@ -1729,8 +1781,9 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
       for (int r = w; r < run.u.rows; r += 8) {
         const float4 v = *reinterpret_cast<const float4*>(stage + r * D + 4 * lane);
         float acc[1][4] = {{v.x, v.y, v.z, v.w}};
-        write_row<D, DT>(a, run, r, acc, sh.few_sum[r], s1, s2, fix);
+        write_row<D, DT>(a, run, r, acc, sh.few_sum[r], s1, s2);
       }
+      if (fix) add_nonfinite<D, DT>(a, run, w, run.u.rows, 8);
     } else {
       float* part = a.partials + ((int64_t)blockIdx.x * kChunkSlots + (run.first ? 0 : 1)) * chunk_slot_rows(D) * PR + row0 * PR;
       if (quad == 0 && lane < min(rows, 16)) *reinterpret_cast<float2*>(part + lane * PR + D) = make_float2(m, L);
@@ -2291,7 +2344,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           }
           __syncwarp();
         }
-        if (fix && mine) add_nonfinite<DT>(a, run, see.pos, 0, D, dst);
+        if (fix) add_nonfinite<D, DT>(a, run, my_row - lane, min(my_row - lane + 32, run.u.rows), 1);
         __syncwarp();
         tc_fence_before();
       } else {
