@@ -390,6 +390,25 @@ class KVCache:
                                        _ptr(q), _ptr(cu_q), total_q, max_q, _ptr(seq_lens), window, sinks, _ptr(out),
                                        _ptr(workspace), workspace.numel(), _stream(stream)))
 
+    def chunk_status(self, workspace=None, stream=None) -> int:
+        """KVQ_DEV_* bits that chunk_attention has set in a workspace since they
+        were cleared, read on `stream`; without a workspace those of all that the cache has
+        made by itself, each read on its own stream."""
+        bits, out = 0, ctypes.c_uint32()
+        for ws, s in self._chunk_words(workspace, stream):
+            _check(LIB.kvq_read_device_status(_ptr(ws), ctypes.byref(out), s))
+            bits |= out.value
+        return bits
+
+    def clear_chunk_status(self, workspace=None, stream=None):
+        for ws, s in self._chunk_words(workspace, stream):
+            _check(LIB.kvq_clear_device_status(_ptr(ws), s))
+
+    def _chunk_words(self, workspace, stream):
+        if workspace is not None:
+            return [(workspace, _stream(stream))]
+        return [(ws, handle) for handle, ws in self._chunk_workspaces.items()]
+
     def _chunk_workspace_of(self, stream):
         import torch
 

@@ -89,3 +89,24 @@ def test_a_captured_call_takes_a_prepared_workspace():
         call(out, 2)  # now the stream has one
     torch.cuda.synchronize()
     assert cache.chunk_workspace is not own and torch.equal(out, refs[2])
+
+
+def test_the_status_of_every_workspace():
+    """A bad length shows in the workspace of the call that met it, and in the cache's own taken together."""
+    cache, call, refs = started()
+    out, side, ws = torch.empty_like(refs[0]), torch.cuda.Stream(), cache.make_chunk_workspace()
+    q = torch.zeros_like(out)
+    cu = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    bad = torch.tensor([3, 1700], dtype=torch.int32, device="cuda")  # fewer tokens than rows
+    assert cache.chunk_status() == 0
+    call(out)
+    torch.cuda.synchronize()
+    cache.chunk_attention(0, 1, q, cu, 8, 4, bad, out, workspace=ws)
+    assert cache.chunk_status() == 0 and cache.chunk_status(ws) == K.DEV_LENGTH
+    cache.clear_chunk_status(ws)
+    assert cache.chunk_status(ws) == 0
+    torch.cuda.synchronize()
+    cache.chunk_attention(0, 1, q, cu, 8, 4, bad, out, stream=side)
+    assert cache.chunk_status() == K.DEV_LENGTH
+    cache.clear_chunk_status()
+    assert cache.chunk_status() == 0 and cache.device_status() == 0
