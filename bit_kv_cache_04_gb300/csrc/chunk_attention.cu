@@ -95,6 +95,11 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
   a.window = window;
   a.sinks = sinks;
   a.stall_polls = stall_polls();
+  const bool wide = a.lo.kf.bits == 8 || (a.lo.tiered && a.lo.kc.bits == 8);
+  const int shift = cfg->in_dtype == KVQ_DT_F16 ? 0 : wide ? 8 : 4;  // the largest code's bits: code times scale stays in fp16's range
+  a.k_pre = std::ldexp(1.f, -shift);
+  a.k_post = std::ldexp(1.f, shift);
+  a.k_one = ((25u - shift) << 10) * 0x10001u;
   a.status = (uint32_t*)workspace;
   a.cp.status = a.status;
   if (cfg->flags & KVQ_K_PRE_ROPE)

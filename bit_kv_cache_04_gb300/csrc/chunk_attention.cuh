@@ -27,9 +27,10 @@
 // Otherwise rows are lanes, however few.  (Repeating few rows over the lanes, each copy with its share of a tile's tokens,
 // gained nothing: 48 rows of 128 channels 301 us both ways, 48 rows of 256 channels 207 us against 165 us.)
 //
-// Roundings: keys, values, P and turned queries go to the input's 16-bit type, as in a cache of that type: the
-// tensor cores multiply nothing wider at this rate.  Scores, row sums and outputs are fp32 until the
-// last store.
+// Roundings: values and P go to the input's 16-bit type, keys and turned queries to fp16 whatever that is: the
+// tensor cores multiply nothing wider at this rate, and a key's rounding weighs most.  (Keys in bf16: 2-norm
+// errors of 3.7e-3 with rotated keys and 5.3e-3 with per-channel ones that have outlier channels, where the output's own rounding is 1.7e-3.)
+// Scores, row sums and outputs are fp32 until the last store.
 //
 // The tiles of all (layer, kv head, sequence, row tile) units form one line
 // that is cut into equal runs, one per CTA, whatever the lengths; a unit cut
@@ -82,6 +83,8 @@ struct ChunkArgs {
   uint32_t* tickets;    // [grid][kChunkTickets]
   uint32_t* nonfinite;  // [grid][kChunkTickets]: a 16-bit window value of the unit is not finite
   float* partials;      // [grid][kChunkSlots][slot rows][part row]
+  float k_pre, k_post;  // factor on a bf16 cache's keys (a power of two), and its inverse on the scores; 1 in an fp16 cache
+  uint32_t k_one;       // the fp16 number whose last bit counts k_pre, twice
   uint64_t turns[128];  // pre-RoPE keys: turns per position of every pair, 64-bit fractions
 };
 

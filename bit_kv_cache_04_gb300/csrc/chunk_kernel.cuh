@@ -293,16 +293,18 @@ __device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 // fields at bits [0, w) of each half, as fp16 integers minus the bias: 1024 + field is exact in fp16
-// (BF: the same in bf16, where 128 + field is exact)
+// (BF: the same in bf16, where 128 + field is exact).  `one`: 1024 in both halves, whose last bit counts 1; or 64 or 4, whose
+// last bit counts 2^-4 or 2^-8, for codes times that.
+constexpr uint32_t kOnes = 0x64006400u;
 template <bool BF = false>
-__device__ __forceinline__ uint32_t field_pair(uint32_t x, uint32_t mask, uint32_t bias) {
+__device__ __forceinline__ uint32_t field_pair(uint32_t x, uint32_t mask, uint32_t bias, uint32_t one = kOnes) {
   if constexpr (BF) {
     const uint32_t v = (x & mask) | 0x43004300u, b = 0x43004300u + bias * 0x10001u;
     const __nv_bfloat162 r =
         __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
   }
-  return hsub2u((x & mask) | 0x64006400u, 0x64006400u + bias * 0x10001u);
+  return hsub2u((x & mask) | one, one + bias * 0x10001u);
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   uint32_t v;
@@ -327,7 +329,7 @@ __device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
   for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], sh);
 }
 template <int BITS, bool RAW, bool BF = false>
-__device__ __forceinline__ void codes32(uint32_t p, uint32_t (&h)[16]) {
+__device__ __forceinline__ void codes32(uint32_t p, uint32_t (&h)[16], uint32_t one = kOnes) {
   uint32_t w[BITS];
   load_words(p, w);
   if constexpr (BITS == 4) {
@@ -335,17 +337,17 @@ __device__ __forceinline__ void codes32(uint32_t p, uint32_t (&h)[16]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t v = w[i] >> 4;
-      h[4 * i] = field_pair<BF>(__byte_perm(w[i], v, 0x0400), 0x000f000fu, bias);
-      h[4 * i + 1] = field_pair<BF>(__byte_perm(w[i], v, 0x1511), 0x000f000fu, bias);
-      h[4 * i + 2] = field_pair<BF>(__byte_perm(w[i], v, 0x2622), 0x000f000fu, bias);
-      h[4 * i + 3] = field_pair<BF>(__byte_perm(w[i], v, 0x3733), 0x000f000fu, bias);
+      h[4 * i] = field_pair<BF>(__byte_perm(w[i], v, 0x0400), 0x000f000fu, bias, one);
+      h[4 * i + 1] = field_pair<BF>(__byte_perm(w[i], v, 0x1511), 0x000f000fu, bias, one);
+      h[4 * i + 2] = field_pair<BF>(__byte_perm(w[i], v, 0x2622), 0x000f000fu, bias, one);
+      h[4 * i + 3] = field_pair<BF>(__byte_perm(w[i], v, 0x3733), 0x000f000fu, bias, one);
     }
   } else if constexpr (BITS == 8) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t u = w[i] ^ 0x80808080u;
-      h[2 * i] = hsub2u(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
-      h[2 * i + 1] = hsub2u(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+      h[2 * i] = hsub2u(__byte_perm(u, one, 0x5150), one + 0x00800080u);
+      h[2 * i + 1] = hsub2u(__byte_perm(u, one, 0x5352), one + 0x00800080u);
     }
   } else if constexpr (BITS == 3) {
     const uint32_t g[4] = {w[0], __funnelshift_r(w[0], w[1], 24), __funnelshift_r(w[1], w[2], 16), w[2] >> 8};
@@ -354,7 +356,7 @@ __device__ __forceinline__ void codes32(uint32_t p, uint32_t (&h)[16]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t t = g[k] >> (6 * j);
-        h[4 * k + j] = field_pair<BF>((t & 7u) | ((t & 0x38u) << 13), 0x00070007u, 4);
+        h[4 * k + j] = field_pair<BF>((t & 7u) | ((t & 0x38u) << 13), 0x00070007u, 4, one);
       }
   } else {
     constexpr uint32_t bias = RAW ? 0 : 2;
@@ -364,8 +366,8 @@ __device__ __forceinline__ void codes32(uint32_t p, uint32_t (&h)[16]) {
       for (int b = 0; b < 4; ++b) {
         const uint32_t x = (w[i] >> (8 * b)) & 0xffu;
         const uint32_t y = x | (x << 14);  // fields 0 and 2 low; 1 and 3 at bits 16 and 20
-        h[8 * i + 2 * b] = field_pair<BF>(y, 0x00030003u, bias);
-        h[8 * i + 2 * b + 1] = field_pair<BF>(y >> 4, 0x00030003u, bias);
+        h[8 * i + 2 * b] = field_pair<BF>(y, 0x00030003u, bias, one);
+        h[8 * i + 2 * b + 1] = field_pair<BF>(y >> 4, 0x00030003u, bias, one);
       }
   }
 }
@@ -452,6 +454,29 @@ template <int DT>
 __device__ __forceinline__ float keep_range(float x) {
   if constexpr (DT == KVQ_DT_F16) return isinf(x) || isnan(x) ? x : fminf(fmaxf(x, -65504.f), 65504.f);
   return x;
+}
+
+// The scores' operands are fp16 whatever the input's type: 11 bits instead of bf16's 8, where it counts most (with a
+// 15-fold outlier channel a bf16 key is off by 2^-9 of the score).  Keys of a bf16 cache go in times k_pre, 2^-4
+// (2^-8 with 8-bit codes), which takes in all that their fp16 scales can hold; the scores are multiplied back.
+__device__ __forceinline__ uint32_t score_pack(float x, float y) {
+  if (fmaxf(fabsf(x), fabsf(y)) > 65504.f) {  // hardly ever
+    x = keep_range<KVQ_DT_F16>(x);
+    y = keep_range<KVQ_DT_F16>(y);
+  }
+  return pack16<KVQ_DT_F16>(x, y);
+}
+// four channels of a turned query
+template <int DT>
+__device__ __forceinline__ uint2 query_pack(const float (&v)[4]) {
+  if constexpr (DT == KVQ_DT_F16) return make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+  return make_uint2(score_pack(v[0], v[1]), score_pack(v[2], v[3]));
+}
+// a pair of the input's type
+template <int DT>
+__device__ __forceinline__ uint32_t score_pair(uint32_t w, float pre) {
+  if constexpr (DT == KVQ_DT_F16) return w;
+  return score_pack(__uint_as_float(w << 16) * pre, __uint_as_float(w & 0xffff0000u) * pre);
 }
 
 struct TileTokens {
@@ -599,9 +624,15 @@ __device__ __forceinline__ void rotated_window(const ChunkArgs& a, const CachePo
       rotate_lanes(v, lane_signs(a.lo.d1, lane), lane_signs(a.lo.d2, lane));
       const int ch = 128 * c + 4 * lane;
       const uint32_t at = dst + (uint32_t)(ch >> 6) * NT * 128 + swz(t - tile0, (ch & 63) >> 3) + (ch & 4) * 2;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(pack16<DT>(keep_range<DT>(v[0]), keep_range<DT>(v[1]))),
-                   "r"(pack16<DT>(keep_range<DT>(v[2]), keep_range<DT>(v[3])))
-                   : "memory");
+      uint32_t o0, o1;
+      if (DT == KVQ_DT_F16 || which) {
+        o0 = pack16<DT>(keep_range<DT>(v[0]), keep_range<DT>(v[1]));
+        o1 = pack16<DT>(keep_range<DT>(v[2]), keep_range<DT>(v[3]));
+      } else {
+        o0 = score_pack(v[0] * a.k_pre, v[1] * a.k_pre);
+        o1 = score_pack(v[2] * a.k_pre, v[3] * a.k_pre);
+      }
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(o0), "r"(o1) : "memory");
     }
   }
 }
@@ -626,8 +657,12 @@ __device__ __forceinline__ void window_groups(const ChunkArgs& a, const CachePos
       for (int k = 0; k < 4; ++k) v[k] = p[c0 + k];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t w[4] = {clean<DT>(in ? v[k].x : 0u, which, nonfinite), clean<DT>(in ? v[k].y : 0u, which, nonfinite),
-                               clean<DT>(in ? v[k].z : 0u, which, nonfinite), clean<DT>(in ? v[k].w : 0u, which, nonfinite)};
+        uint32_t w[4] = {clean<DT>(in ? v[k].x : 0u, which, nonfinite), clean<DT>(in ? v[k].y : 0u, which, nonfinite),
+                         clean<DT>(in ? v[k].z : 0u, which, nonfinite), clean<DT>(in ? v[k].w : 0u, which, nonfinite)};
+        if (which == 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = score_pair<DT>(w[e], a.k_pre);
+        }
         const int row = (c0 + k) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e)  // row + e has low bits e
@@ -643,7 +678,7 @@ __device__ __forceinline__ void window_groups(const ChunkArgs& a, const CachePos
 // saturate in fp16 (an infinity would turn a masked token's zero probability into NaN).
 template <int DT>
 __device__ __forceinline__ void general_run(RunFmt f, uint32_t blk, uint32_t codes, const uint32_t* pair_table,
-                                         uint32_t line, int row, int run) {
+                                         uint32_t line, int row, int run, bool key, float pre) {
   uint32_t h[16];
   if (f.codebook) {
     uint32_t w[4];
@@ -669,7 +704,7 @@ __device__ __forceinline__ void general_run(RunFmt f, uint32_t blk, uint32_t cod
       x = fminf(fmaxf(x, -65504.f), 65504.f);
       y = fminf(fmaxf(y, -65504.f), 65504.f);
     }
-    h[i] = pack16<DT>(x, y);
+    h[i] = DT == KVQ_DT_F16 || !key ? pack16<DT>(x, y) : score_pack(x * pre, y * pre);
   }
   store_run(line, row, run, h);
 }
@@ -684,21 +719,25 @@ struct PiecePlace {
   uint32_t piece16[4];        // swizzled places of the run's four 16-byte parts
 };
 // False when a block's values leave fp16's range, or its scale is not finite (the piece is then done again).
-template <int DT, int BITS, bool ZP>
-__device__ __forceinline__ bool fill_piece(const PiecePlace& q, uint32_t staged, uint32_t tile) {
+// KEY: keys of a bf16 cache, fp16 values times k_pre (`one` is a.k_one); their codes take the factor, exactly.
+template <int DT, bool KEY, int BITS, bool ZP>
+__device__ __forceinline__ bool fill_piece(const PiecePlace& q, uint32_t staged, uint32_t tile, uint32_t one = kOnes) {
   uint32_t most = 0, blk = staged + q.blk, line = tile + q.line;
   const uint32_t codes = q.codes - q.blk;
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const uint32_t s16 = lds16(blk), z16 = ZP ? lds16(blk + 2) : 0u;
     uint32_t h[16];
-    constexpr bool BF = DT == KVQ_DT_BF16 && !ZP && BITS < 8;
-    codes32<BITS, ZP, BF>(blk + codes, h);
+    constexpr bool BF = DT == KVQ_DT_BF16 && !KEY && !ZP && BITS < 8;
+    codes32<BITS, ZP, BF>(blk + codes, h, KEY ? one : kOnes);
     most = max(most, s16 & 0x7fffu);
     // the zero's bound is four times the scale's
     if (ZP) most = max(most, DT == KVQ_DT_F16 ? max(z16 & 0x7fffu, 0x800u) - 0x800u : z16 & 0x7fffu);
     if constexpr (BF)
       scale32_bf(h, s16);
+    else if constexpr (KEY)  // (0x2800: from 1024, 64 or 4 to 1, 2^-4 or 2^-8)
+      scale32<KVQ_DT_F16, ZP>(
+          h, s16, ZP ? __half_as_ushort(__hmul(__ushort_as_half((uint16_t)z16), __ushort_as_half((uint16_t)(one - 0x2800u)))) : 0u);
     else
       scale32<DT, ZP>(h, s16, z16);
 #pragma unroll
@@ -734,10 +773,14 @@ __device__ __forceinline__ void mixed_piece(const ChunkArgs& a, const CachePos& 
       const RunFmt f = run_fmt(a.lo, which, t < u.ce);
       uint32_t blk, codes;
       RunPlace<D>::at(per_channel, f, a.sub_bytes, toff, row, run, &blk, &codes);
-      general_run<DT>(f, staged + blk, staged + codes, pair_table, line, row_t, run_t);
+      general_run<DT>(f, staged + blk, staged + codes, pair_table, line, row_t, run_t, which == 0, a.k_pre);
     } else if (in && t >= u.qe && !per_channel && !(rotated && t < u.T)) {
       uint32_t h[16];
       raw_token_run<DT>(a, u, which, t, run, nonfinite, h);
+      if (which == 0) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) h[k] = score_pair<DT>(h[k], a.k_pre);
+      }
       store_run(line, row_t, run_t, h);
     } else if ((in && t < u.qe) || fresh) {
       // a page out of range; or a run out of view in a buffer that V has not filled yet: what shared
@@ -837,8 +880,8 @@ __device__ __forceinline__ void turned_piece(const ChunkArgs& a, const CachePos&
         k = make_float2(k.x * step.x - k.y * step.y, k.y * step.x + k.x * step.y);
         const float x1 = xa.y * k.x - ya.y * k.y, y1 = ya.y * k.x + xa.y * k.y;
         k = make_float2(k.x * step.x - k.y * step.y, k.y * step.x + k.x * step.y);
-        x.h[i] = pack16<DT>(keep_range<DT>(x0), keep_range<DT>(x1));
-        y.h[i] = pack16<DT>(keep_range<DT>(y0), keep_range<DT>(y1));
+        x.h[i] = score_pack(x0 * a.k_pre, x1 * a.k_pre);
+        y.h[i] = score_pack(y0 * a.k_pre, y1 * a.k_pre);
       }
       store_run(RunPlace<D>::line_at(dst, c, run, D), c, run, x.h);
       store_run(RunPlace<D>::line_at(dst, c + D / 2, run, D), c + D / 2, run, y.h);
@@ -856,8 +899,8 @@ __device__ __forceinline__ void turned_piece(const ChunkArgs& a, const CachePos&
         const float2 k0 = cos_sin((uint64_t)t * a.turns[32 * run + 2 * i]);
         const float2 k1 = cos_sin((uint64_t)t * a.turns[32 * run + 2 * i + 1]);
         const float2 xa = x.value(i), ya = y.value(i);
-        x.h[i] = pack16<DT>(keep_range<DT>(xa.x * k0.x - ya.x * k0.y), keep_range<DT>(xa.y * k1.x - ya.y * k1.y));
-        y.h[i] = pack16<DT>(keep_range<DT>(ya.x * k0.x + xa.x * k0.y), keep_range<DT>(ya.y * k1.x + xa.y * k1.y));
+        x.h[i] = score_pack((xa.x * k0.x - ya.x * k0.y) * a.k_pre, (xa.y * k1.x - ya.y * k1.y) * a.k_pre);
+        y.h[i] = score_pack((ya.x * k0.x + xa.x * k0.y) * a.k_pre, (ya.y * k1.x + xa.y * k1.y) * a.k_pre);
       }
       store_run(RunPlace<D>::line_at(dst, row, run, NT), row, run, x.h);
       store_run(RunPlace<D>::line_at(dst, row, run + R, NT), row, run + R, y.h);
@@ -1556,7 +1599,9 @@ __device__ __forceinline__ void few_queries(const ChunkArgs& a, const Unit& u, u
       float v[4] = {in_to_f32((uint16_t)x.x, DT), in_to_f32((uint16_t)(x.x >> 16), DT), in_to_f32((uint16_t)x.y, DT),
                     in_to_f32((uint16_t)(x.y >> 16), DT)};
       rotate_lanes(v, s1, s2);
-      x = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+      x = query_pack<DT>(v);
+    } else {
+      x = make_uint2(score_pair<DT>(x.x, 1.f), score_pair<DT>(x.y, 1.f));
     }
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(col + swz(r, (ch & 63) >> 3)), "r"(x.x), "r"(x.y) : "memory");
     x = next;
@@ -1591,7 +1636,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
   const int quad = w & 3, row0 = (w >> 2) * 16;  // rows [row0, row0 + 16)
   const int my = 32 * quad + lane;               // token of a tile; channel of the output
   const uint32_t q_at = smem_addr(smem), lane_base = tmem + ((uint32_t)(32 * quad) << 16) + row0, o_col = lane_base + C::O_COL;
-  const float sc = 1.4426950408889634f * rsqrtf((float)D);
+  const float sc = 1.4426950408889634f * rsqrtf((float)D) * (DT == KVQ_DT_F16 ? 1.f : a.k_post);
   uint32_t* const gave_up = &sh.gave_up;
   float* const mneg = sh.few_mneg[w];  // minus the references
   float* const fac = sh.few_fac[w];
@@ -1902,9 +1947,9 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
   if (warp == C::MMA_WARP) {
     // ---- products: one thread ----------------------------------------------------
     constexpr uint32_t F = DT == KVQ_DT_F16 ? 0 : 1;
-    constexpr uint32_t base = (1u << 4) | (F << 7) | (F << 10) | ((128u >> 4) << 24);
+    constexpr uint32_t half = (1u << 4) | ((128u >> 4) << 24), base = half | (F << 7) | (F << 10);
     // FEW: keys and values are the left operands, the rows the columns of both products
-    const uint32_t qk_desc = base | ((uint32_t)k_chan << (FEW ? 15 : 16)) | ((uint32_t)((FEW ? a.cols : NT) >> 3) << 17);
+    const uint32_t qk_desc = half | ((uint32_t)k_chan << (FEW ? 15 : 16)) | ((uint32_t)((FEW ? a.cols : NT) >> 3) << 17);
     const uint32_t pv_desc = base | ((uint32_t)!v_chan << (FEW ? 15 : 16)) | ((uint32_t)((FEW ? a.cols : D) >> 3) << 17);
     const uint64_t p_desc = operand_desc(q_at + kFewBytes, 0, 1024);
     const uint32_t sum_desc = base | ((uint32_t)(a.cols >> 3) << 17);
@@ -2171,20 +2216,28 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         }
         };
         // (a loop a format: the formats' branches are outside of it)
-        if (kind == 4)
-          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 4, false>(q, staged, dst); });
-        else if (kind == 8)
-          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 8, false>(q, staged, dst); });
-        else if (kind == 2)
-          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 2, false>(q, staged, dst); });
-        else if (kind == 3)
-          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 3, false>(q, staged, dst); });
-        else if (kind == 20)
-          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 4, true>(q, staged, dst); });
-        else if (kind == 18)
-          stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, 2, true>(q, staged, dst); });
+        auto by_kind = [&](auto key) {
+          constexpr bool KEY = decltype(key)::value;
+          const uint32_t one = KEY ? a.k_one : kOnes;
+          if (kind == 4)
+            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 4, false>(q, staged, dst, one); });
+          else if (kind == 8)
+            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 8, false>(q, staged, dst, one); });
+          else if (kind == 2)
+            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 2, false>(q, staged, dst, one); });
+          else if (kind == 3)
+            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 3, false>(q, staged, dst, one); });
+          else if (kind == 20)
+            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 4, true>(q, staged, dst, one); });
+          else if (kind == 18)
+            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 2, true>(q, staged, dst, one); });
+          else
+            stretch([&](uint32_t, uint32_t) { return false; });
+        };
+        if (DT == KVQ_DT_BF16 && which == 0)
+          by_kind(std::integral_constant<bool, DT == KVQ_DT_BF16>{});
         else
-          stretch([&](uint32_t, uint32_t) { return false; });
+          by_kind(std::false_type{});
         if (!ok || j >= j1) break;
         if (landed) {
           cold_piece<D, DT>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j);
@@ -2216,7 +2269,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
       const uint32_t o_col = lane_base + C::O_COL + (C::STREAMS == 2 ? stream * D : 0);
       const int my_row = (PAIRED ? stream * 128 : 0) + my_lane;  // query row of the row tile
-      const float sc = 1.4426950408889634f * rsqrtf((float)D);
+      const float sc = 1.4426950408889634f * rsqrtf((float)D) * (DT == KVQ_DT_F16 ? 1.f : a.k_post);
       // queries into shared memory
       if (PAIRED || stream == 0) {
         const int first = PAIRED ? stream * 128 : 0, n = min(128, run.u.rows - first);  // rows
@@ -2232,7 +2285,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
             float v[4] = {in_to_f32((uint16_t)w.x, DT), in_to_f32((uint16_t)(w.x >> 16), DT),
                           in_to_f32((uint16_t)w.y, DT), in_to_f32((uint16_t)(w.y >> 16), DT)};
             rotate_lanes(v, s1, s2);
-            w = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+            w = query_pack<DT>(v);
             const int ch = 128 * c + 4 * lane;
             const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r, (ch & 63) >> 3) + (ch & 4) * 2;
             asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
@@ -2253,6 +2306,9 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < U; ++i) {
               const int r = r0 + 4 * RPT * i;
+              if (DT == KVQ_DT_BF16 && !(a.lo.flags & KVQ_ROTATE_K))  // (turned queries are fp16 already)
+                w[i] = make_uint4(score_pair<DT>(w[i].x, 1.f), score_pair<DT>(w[i].y, 1.f), score_pair<DT>(w[i].z, 1.f),
+                                  score_pair<DT>(w[i].w, 1.f));
               if (r < n)
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(col + swz(r, (ch & 63) >> 3)), "r"(w[i].x),
                              "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
@@ -2462,7 +2518,7 @@ __global__ void __launch_bounds__(256) turn_queries_kernel(const __grid_constant
         float v[4] = {in_to_f32((uint16_t)x[k].x, DT), in_to_f32((uint16_t)(x[k].x >> 16), DT),
                       in_to_f32((uint16_t)x[k].y, DT), in_to_f32((uint16_t)(x[k].y >> 16), DT)};
         rotate_lanes(v, s1, s2);
-        dst[32 * (c0 + k)] = make_uint2(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]));
+        dst[32 * (c0 + k)] = query_pack<DT>(v);
       }
   }
 }

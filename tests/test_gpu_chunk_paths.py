@@ -41,17 +41,17 @@ def expected_square(oc, k, v, r):
     and evenly distributed below that at worst: variance (u x)^2 / 3.  To first order
       d o = sum_j p_j (d s_j) (v_j - o) + sum_j p_j (e_j + f_j) v_j + g o,
     d s_j = (sum_c r_c k_jc (a_jc + b_c)) / sqrt(D): a the keys' roundings, b the turned query's (one for
-    all keys; rotated formats only), e those of P, f the values', g the output's; all independent."""
-    u, D = 2.0 ** -11 if oc.in_dtype == 0 else 2.0 ** -8, oc.D
+    all keys; rotated formats only), both to fp16, e those of P, f the values', g the output's; all independent."""
+    u, uk, D = 2.0 ** -11 if oc.in_dtype == 0 else 2.0 ** -8, 2.0 ** -11, oc.D
     s = k @ r / np.sqrt(D)
     p = np.exp(s - s.max())
     p /= p.sum()
     o = p @ v
     ds = np.sum((k * r) ** 2, -1) / D
-    var = (p ** 2 * ds) @ ((v - o) ** 2) + 2 * (p ** 2) @ v ** 2 + o ** 2
+    keys = (p ** 2 * ds) @ ((v - o) ** 2)
     if oc.flags & O.ROTATE_K:
-        var = var + np.sum(((k * r).T @ (p[:, None] * (v - o))) ** 2, 0) / D
-    return u * u / 3 * var.sum()
+        keys = keys + np.sum(((k * r).T @ (p[:, None] * (v - o))) ** 2, 0) / D
+    return (uk * uk * keys + u * u * (2 * (p ** 2) @ v ** 2 + o ** 2)).sum() / 3
 
 
 def expected_error(oc, bufs, rows, lens, window, sinks, table):
@@ -178,3 +178,37 @@ def test_errors_are_those_of_the_stated_roundings(name, heads, dt, n):
     err, allowed = np.linalg.norm(got - want), expected_error(oc, bufs, rows, w.lengths, 0, 0, table)
     print(f"error {err:.3e}, expected {allowed:.3e}, ratio {err / allowed:.3f}")
     assert err <= 1.25 * allowed
+
+
+@pytest.mark.parametrize("n", [3, 20, 150])
+@pytest.mark.parametrize("name,kw", [
+    ("llama2_7b_kivi4", dict()), ("llama2_7b_kivi4_zp", dict()), ("gqa8b_hadamard4_paged", dict(residual_window=37)),
+    ("q8_0_mha_1k", dict(residual_window=20)), ("mistral7b_hotcold", dict(hot_window=96, residual_window=40)),
+    ("q4_0_mha_1k", dict(flags=K.K_PRE_ROPE))])
+@pytest.mark.parametrize("size", [3e4, 1e-3])
+def test_bf16_keys_out_of_fp16_s_range(name, kw, n, size):
+    """Keys of some 10^5 (queries as much smaller) and of 10^-3, quantized and in the window, against the per-value bound of bf16 keys."""
+    w = workload(name, [300], heads=(2, 4), in_dtype=K.DT_BF16, **kw)
+    cfg, oc = w.cfg, oracle_cfg(w.cfg)
+    T = 300
+    table = None
+    if cfg.page_tokens:
+        table = torch.arange(cfg.max_pages_per_seq, dtype=torch.int32).view(1, -1)
+    cache = K.KVCache(cfg, "cuda", block_table=table)
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    k, v, q = (torch.randn((1, m, h, cfg.D), generator=gen, device="cuda") for m, h in ((T, cfg.H_kv), (T, cfg.H_kv), (n, cfg.H_q)))
+    k, v, q = (k * size).bfloat16(), v.bfloat16(), (q / size).bfloat16()
+    assert size < 1 or k.abs().max() > 65504
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu_T, cu = (torch.tensor([0, x], dtype=torch.int32, device="cuda") for x in (T, n))
+    cache.append(0, 1, k, v, cu_T, lens, T, T)
+    cache.commit_lengths(cu_T, lens)
+    out = torch.empty_like(q)
+    cache.chunk_attention(0, 1, q, cu, n, n, lens, out)
+    torch.cuda.synchronize()
+    assert cache.chunk_status() == 0
+    bufs = gpu_buffers_as_oracle(cache, oc)
+    want, bound = S.chunk_attention(oc, bufs, 0, raw16(q[0]), np.array([0, n]), [T], 0, 0, None if table is None else table.numpy(), True,
+                                    4.0 if cfg.flags & (K.ZP_K | K.ZP_V) else 2.0)
+    err = np.abs(O.input_to_f32(raw16(out[0]), 1).astype(np.float64) - want)
+    assert np.all(err <= bound), float(np.max(err / bound))
