@@ -98,7 +98,8 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
   const bool wide = a.lo.kf.bits == 8 || (a.lo.tiered && a.lo.kc.bits == 8);
   const int shift = cfg->in_dtype == KVQ_DT_F16 ? 0 : wide ? 8 : 4;  // the largest code's bits: code times scale stays in fp16's range
   a.k_pre = std::ldexp(1.f, -shift);
-  a.k_post = std::ldexp(1.f, shift);
+  a.q_pre = cfg->flags & KVQ_ROTATE_K ? 0.0625f : 1.f;
+  a.score_scale = (float)(1.4426950408889634 / std::sqrt((double)cfg->D)) / (a.k_pre * a.q_pre);
   a.k_one = ((25u - shift) << 10) * 0x10001u;
   a.status = (uint32_t*)workspace;
   a.cp.status = a.status;

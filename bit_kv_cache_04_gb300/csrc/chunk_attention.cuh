@@ -83,7 +83,8 @@ struct ChunkArgs {
   uint32_t* tickets;    // [grid][kChunkTickets]
   uint32_t* nonfinite;  // [grid][kChunkTickets]: a 16-bit window value of the unit is not finite
   float* partials;      // [grid][kChunkSlots][slot rows][part row]
-  float k_pre, k_post;  // factor on a bf16 cache's keys (a power of two), and its inverse on the scores; 1 in an fp16 cache
+  float k_pre, q_pre;  // factors (powers of two) on a bf16 cache's keys and on turned queries
+  float score_scale;   // log2(e) / sqrt(D), both factors undone
   uint32_t k_one;       // the fp16 number whose last bit counts k_pre, twice
   uint64_t turns[128];  // pre-RoPE keys: turns per position of every pair, 64-bit fractions
 };

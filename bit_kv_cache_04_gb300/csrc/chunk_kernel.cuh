@@ -147,12 +147,12 @@ __device__ __forceinline__ uint32_t lane_signs(const uint32_t* d, int lane) {
   return (lane & 8 ? hi : lo) >> (4 * (lane & 7));
 }
 // The transform of a 128-chunk held four channels a lane, between the signs s1 and s2 of lane_signs: forward with
-// (d1, d2), inverse with (d2, d1).
-__device__ __forceinline__ void rotate_lanes(float (&v)[4], uint32_t s1, uint32_t s2) {
+// (d1, d2), inverse with (d2, d1).  `factor`: on the result.
+__device__ __forceinline__ void rotate_lanes(float (&v)[4], uint32_t s1, uint32_t s2, float factor = 1.f) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(__float_as_uint(v[e]) ^ ((s1 << (31 - e)) & 0x80000000u));
   warp_fwht128(v);
-  const float c = hadamard_scale();
+  const float c = hadamard_scale() * factor;
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(__float_as_uint(v[e] * c) ^ ((s2 << (31 - e)) & 0x80000000u));
 }
@@ -458,7 +458,8 @@ __device__ __forceinline__ float keep_range(float x) {
 
 // The scores' operands are fp16 whatever the input's type: 11 bits instead of bf16's 8, where it counts most (with a
 // 15-fold outlier channel a bf16 key is off by 2^-9 of the score).  Keys of a bf16 cache go in times k_pre, 2^-4
-// (2^-8 with 8-bit codes), which takes in all that their fp16 scales can hold; the scores are multiplied back.
+// (2^-8 with 8-bit codes), which takes in all that their fp16 scales can hold, and turned queries times q_pre, 2^-4 (the
+// turn makes a value up to 11.4 times the largest); the scores are multiplied back.
 __device__ __forceinline__ uint32_t score_pack(float x, float y) {
   if (fmaxf(fabsf(x), fabsf(y)) > 65504.f) {  // hardly ever
     x = keep_range<KVQ_DT_F16>(x);
@@ -1598,7 +1599,7 @@ __device__ __forceinline__ void few_queries(const ChunkArgs& a, const Unit& u, u
     if (turn) {
       float v[4] = {in_to_f32((uint16_t)x.x, DT), in_to_f32((uint16_t)(x.x >> 16), DT), in_to_f32((uint16_t)x.y, DT),
                     in_to_f32((uint16_t)(x.y >> 16), DT)};
-      rotate_lanes(v, s1, s2);
+      rotate_lanes(v, s1, s2, a.q_pre);
       x = query_pack<DT>(v);
     } else {
       x = make_uint2(score_pair<DT>(x.x, 1.f), score_pair<DT>(x.y, 1.f));
@@ -1636,7 +1637,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
   const int quad = w & 3, row0 = (w >> 2) * 16;  // rows [row0, row0 + 16)
   const int my = 32 * quad + lane;               // token of a tile; channel of the output
   const uint32_t q_at = smem_addr(smem), lane_base = tmem + ((uint32_t)(32 * quad) << 16) + row0, o_col = lane_base + C::O_COL;
-  const float sc = 1.4426950408889634f * rsqrtf((float)D) * (DT == KVQ_DT_F16 ? 1.f : a.k_post);
+  const float sc = a.score_scale;
   uint32_t* const gave_up = &sh.gave_up;
   float* const mneg = sh.few_mneg[w];  // minus the references
   float* const fac = sh.few_fac[w];
@@ -2269,7 +2270,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
       const uint32_t o_col = lane_base + C::O_COL + (C::STREAMS == 2 ? stream * D : 0);
       const int my_row = (PAIRED ? stream * 128 : 0) + my_lane;  // query row of the row tile
-      const float sc = 1.4426950408889634f * rsqrtf((float)D) * (DT == KVQ_DT_F16 ? 1.f : a.k_post);
+      const float sc = a.score_scale;
       // queries into shared memory
       if (PAIRED || stream == 0) {
         const int first = PAIRED ? stream * 128 : 0, n = min(128, run.u.rows - first);  // rows
@@ -2284,7 +2285,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
             uint2 w = __ldcg(reinterpret_cast<const uint2*>(a.q + query_row(a, run.u, first + r) + 128 * c) + lane);
             float v[4] = {in_to_f32((uint16_t)w.x, DT), in_to_f32((uint16_t)(w.x >> 16), DT),
                           in_to_f32((uint16_t)w.y, DT), in_to_f32((uint16_t)(w.y >> 16), DT)};
-            rotate_lanes(v, s1, s2);
+            rotate_lanes(v, s1, s2, a.q_pre);
             w = query_pack<DT>(v);
             const int ch = 128 * c + 4 * lane;
             const uint32_t at = q0 + (uint32_t)(ch >> 6) * 16384 + swz(r, (ch & 63) >> 3) + (ch & 4) * 2;
@@ -2517,7 +2518,7 @@ __global__ void __launch_bounds__(256) turn_queries_kernel(const __grid_constant
       if (c0 + k < chunks) {
         float v[4] = {in_to_f32((uint16_t)x[k].x, DT), in_to_f32((uint16_t)(x[k].x >> 16), DT),
                       in_to_f32((uint16_t)x[k].y, DT), in_to_f32((uint16_t)(x[k].y >> 16), DT)};
-        rotate_lanes(v, s1, s2);
+        rotate_lanes(v, s1, s2, a.q_pre);
         dst[32 * (c0 + k)] = query_pack<DT>(v);
       }
   }

@@ -569,7 +569,7 @@ KVQ_API kvq_status kvq_pages_compact(const kvq_config* cfg, const kvq_cache* cac
  * Products run on the tensor cores with fp32 sums: keys and queries in fp16 (queries turned into a
  * rotated format's domain are rounded to it), values and probabilities in in_dtype; softmax statistics
  * and outputs are held in fp32 and rounded once.  What passes fp16's range counts as its end: queries
- * beyond 65504; in a bf16 cache, keys beyond 2^20 (2^24 with 8-bit key formats), which is more than its quantized tokens can hold.
+ * beyond 65504 (2^20 after the turn of a rotated format); in a bf16 cache, keys beyond 2^20 (2^24 with 8-bit key formats), which is more than its quantized tokens can hold.
  * A sequence with cu_q not ascending, n_b > max_q, a length outside [0,
  * max_T] or n_b > length sets KVQ_DEV_LENGTH and its rows are left as they are; a page
  * id out of range sets KVQ_DEV_PAGE and that page's tokens count as zeros.

@@ -212,3 +212,33 @@ def test_bf16_keys_out_of_fp16_s_range(name, kw, n, size):
                                     4.0 if cfg.flags & (K.ZP_K | K.ZP_V) else 2.0)
     err = np.abs(O.input_to_f32(raw16(out[0]), 1).astype(np.float64) - want)
     assert np.all(err <= bound), float(np.max(err / bound))
+
+
+@pytest.mark.parametrize("n", [3, 20, 150])
+@pytest.mark.parametrize("name,dt", [("gqa8b_hadamard4_paged", K.DT_F16), ("gqa8b_hadamard4_paged", K.DT_BF16),
+                                     ("ctx262k_hadamard4", K.DT_F16), ("ctx262k_tbq4", K.DT_BF16)])
+def test_turned_queries_past_fp16_s_range(name, dt, n):
+    """A query along a row of the transform gathers in one channel: 8000 becomes 90500."""
+    w = workload(name, [300], heads=(1, 4), in_dtype=dt)
+    cfg, oc = w.cfg, oracle_cfg(w.cfg)
+    T = 300
+    table = torch.arange(cfg.max_pages_per_seq, dtype=torch.int32).view(1, -1) if cfg.page_tokens else None
+    cache = K.KVCache(cfg, "cuda", block_table=table)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn((1, T, 1, cfg.D), generator=gen, device="cuda") for _ in range(2))
+    k, v = (k * 1e-3).to(DT[dt]), v.to(DT[dt])
+    q = torch.randn((1, n, 4, cfg.D), generator=gen, device="cuda") * 8
+    rows = O.rotation_matrix_f64(*O.hadamard_signs(oc.sign_seed))  # entries of +-1 / sqrt(128)
+    q[..., :128] = torch.as_tensor(np.sign(rows[np.arange(4 * n) % 128]).reshape(1, n, 4, 128) * 8000.0, device="cuda")
+    q = q.to(DT[dt])
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu_T, cu = (torch.tensor([0, x], dtype=torch.int32, device="cuda") for x in (T, n))
+    cache.append(0, 1, k, v, cu_T, lens, T, T)
+    cache.commit_lengths(cu_T, lens)
+    out = torch.empty_like(q)
+    cache.chunk_attention(0, 1, q, cu, n, n, lens, out)
+    torch.cuda.synchronize()
+    bufs = gpu_buffers_as_oracle(cache, oc)
+    want, bound = S.chunk_attention(oc, bufs, 0, raw16(q[0]), np.array([0, n]), [T], 0, 0, None if table is None else table.numpy(), True)
+    err = np.abs(O.input_to_f32(raw16(out[0]), dt).astype(np.float64) - want)
+    assert np.all(err <= bound), float(np.max(err / bound))
