@@ -19,7 +19,7 @@
 // its own S and output accumulator, so that one stream's exponentials run
 // under the other's products.  PAIRED (more than 128 rows a sequence): both
 // streams take the same tokens and different rows (256 rows a CTA, a tile is
-// dequantized once for both: two chunks of 2048 tokens over a 4096-token window 391 us, 703 TFLOP/s, twice
+// dequantized once for both: two chunks of 2048 tokens over a 4096-token window 395 us, 695 TFLOP/s, twice
 // as long unpaired).  Not PAIRED: the streams share the rows and take alternate tiles.
 // D = 256: tiles of 64 tokens, 128 rows, one output accumulator and one group
 // of softmax warps over two S buffers (TMEM holds no more).

@@ -437,7 +437,8 @@ __device__ __forceinline__ void scale32(uint32_t (&h)[16], uint32_t s16, uint32_
 
 // The same for bf16 codes of at most 4 bits, symmetric blocks, two instructions a pair: the scale is the exact sum of
 // two bf16 (11 bits: 8 and the rest), a code times the rest is exact (4 + 3 bits), and the fused product rounds
-// once, so the values are those of the fp32 path bit for bit (1000-token chunk of 256-channel heads: 756 -> 709 us).
+// once, so the values are those of the fp32 path bit for bit (1000-token chunk of 256-channel heads, when keys took it too:
+// 756 -> 709 us).
 __device__ __forceinline__ void scale32_bf(uint32_t (&h)[16], uint32_t s16) {
   const float s = __half2float(__ushort_as_half((uint16_t)s16));
   const __nv_bfloat16 hi = __float2bfloat16_rn(s), lo = __float2bfloat16_rn(s - __bfloat162float(hi));

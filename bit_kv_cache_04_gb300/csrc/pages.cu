@@ -3,7 +3,10 @@
 //
 // The bookkeeping is integers: a few thousand table entries and counts, so
 // one block decides (its passes over refs are the only ones longer than the
-// lists), and launch latency is what these calls cost.  The bytes that have to move (shared
+// lists), and launch latency is what these calls cost: a reservation for 64
+// sequences 9 us, for 256 of them 23 us (32 us with a copy for every second one), compaction of 6000 pages' counts 6 us.
+// Beyond that the one block shows: 1024 sequences 76 us (108 us), 4096 298 us (524 us), 32768 2.6 ms (13 ms: the ranks
+// among sequences that share a page are quadratic); 65536 pages 42 us, 2^20 614 us.  The bytes that have to move (shared
 // pages that get written, windows of forked sequences, compacted pages) are
 // copied by a second, grid-wide kernel that reads the decision from the
 // workspace: 2 bytes of traffic per byte moved, HBM-bound (6000 pages half used compacted in 288 us, 83 % of the copy

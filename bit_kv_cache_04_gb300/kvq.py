@@ -546,7 +546,9 @@ class PagePool:
                                      *self._ws(stream)))
 
     def compact(self, refs_out=None, table_out=None, stream=None):
-        """Moves the used pages together.  Without outputs the cache's table and the counts are changed in place."""
+        """Moves the used pages together.  Without outputs the cache's table and the counts are changed in place.  With
+        them the pages have moved all the same, and nothing may use the cache until the caller has copied table_out into
+        its block table and refs_out into the counts."""
         import torch
 
         table = self.cache.block_table
