@@ -1579,8 +1579,8 @@ __device__ __forceinline__ void rescale_columns(uint32_t o_col, float f) {
 // one channel of the output; P goes through shared memory.  Row sums come from a third product, ones times
 // P^T, so that no thread keeps 16 of them (32 registers of sums spilled: 8-token drafts of 16
 // sequences took 414 us).  The rows' reference maxima are common to a group's four warps.
-// Against rows as lanes: one token over one long window 34 -> 28 us, single tokens of 64 sequences 265 -> 229 us,
-// drafts of 16 sequences 291 -> 272 us; 16 columns instead of 32 for the single tokens 238 -> 229 us.  (More than 32 rows are not two
+// Against rows as lanes: one token over one long window 34 -> 29 us, single tokens of 64 sequences 265 -> 228 us,
+// drafts of 16 sequences 291 -> 274 us; 16 columns instead of 32 for the single tokens 238 -> 229 us.  (More than 32 rows are not two
 // groups of 16 a thread any more, and there the lanes are full enough.)  Bound now by the dequantizing warps' issue slots and the shared memory's bandwidth (a tile's
 // values are written once and read by the products once: 128 KiB of shared-memory traffic for 17 KiB of cache).
 

@@ -356,7 +356,8 @@ class KVCache:
 
     def make_chunk_workspace(self, stream=None):
         """A prepared workspace for chunk_attention, made on `stream`.  Calls that may run at
-        the same time (other streams, graphs replayed side by side) each need one."""
+        the same time (other streams, graphs replayed side by side) each need one; calls in
+        order may share one, also those of other caches of the same head size (62 MB for each)."""
         import torch
 
         with _on(stream):
@@ -393,7 +394,7 @@ class KVCache:
     def chunk_status(self, workspace=None, stream=None) -> int:
         """KVQ_DEV_* bits that chunk_attention has set in a workspace since they
         were cleared, read on `stream`; without a workspace those of all that the cache has
-        made by itself, each read on its own stream."""
+        made by itself, when the device has finished its work."""
         bits, out = 0, ctypes.c_uint32()
         for ws, s in self._chunk_words(workspace, stream):
             _check(LIB.kvq_read_device_status(_ptr(ws), ctypes.byref(out), s))
@@ -407,7 +408,10 @@ class KVCache:
     def _chunk_words(self, workspace, stream):
         if workspace is not None:
             return [(workspace, _stream(stream))]
-        return [(ws, handle) for handle, ws in self._chunk_workspaces.items()]
+        import torch
+
+        torch.cuda.synchronize(self.device)  # of every stream; some may not exist any more
+        return [(ws, _stream(stream)) for ws in list(self._chunk_workspaces.values())]
 
     def _chunk_workspace_of(self, stream):
         import torch

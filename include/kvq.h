@@ -522,9 +522,7 @@ KVQ_API kvq_status kvq_pages_fork(const kvq_config* cfg, const kvq_cache* cache,
                                   int32_t* seq_lens, const int32_t* src, const int32_t* dst, int32_t n,
                                   void* workspace, size_t ws_bytes, void* stream);
 
-/* (One block does the bookkeeping, so the time grows with the list: some 10 us for 64 sequences, 0.3 to 0.5 ms for 4096,
- * 3 to 13 ms for 32768.)
- * Makes room for n_new[i] more tokens of sequence seqs[i] (lengths as before
+/* Makes room for n_new[i] more tokens of sequence seqs[i] (lengths as before
  * the append, and not advanced): its table row gets pages for tokens [0,
  * length + n_new[i]), and if the page that the next quantized token goes to
  * is partly filled and has other readers, a copy of it (all layers, K and V).  New pages
@@ -534,7 +532,9 @@ KVQ_API kvq_status kvq_pages_fork(const kvq_config* cfg, const kvq_cache* cache,
  * All or nothing: with too few free pages or a length beyond max_T
  * (KVQ_DEV_CAPACITY), a bad or repeated index (KVQ_DEV_SEQ), a bad length or
  * count (KVQ_DEV_LENGTH), or a table that breaks the rules above
- * (KVQ_DEV_PAGE), nothing changes. */
+ * (KVQ_DEV_PAGE), nothing changes.
+ * One block does the bookkeeping, so the time grows with the list: some 10 us
+ * for 64 sequences, 0.3 to 0.5 ms for 4096, 3 to 13 ms for 32768. */
 KVQ_API kvq_status kvq_pages_reserve(const kvq_config* cfg, const kvq_cache* cache, int32_t* block_table,
                                      int32_t* refs, const int32_t* seq_lens, const int32_t* seqs,
                                      const int32_t* n_new, int32_t n, void* workspace, size_t ws_bytes,

@@ -110,3 +110,16 @@ def test_the_status_of_every_workspace():
     assert cache.chunk_status() == K.DEV_LENGTH
     cache.clear_chunk_status()
     assert cache.chunk_status() == 0 and cache.device_status() == 0
+
+
+def test_one_workspace_for_caches_in_turn():
+    """Other formats, heads and forms of one head size, one call after the other."""
+    kinds = [started(), started("llama2_7b_kivi4", H_kv=2, H_q=8), started("q8_0_mha_1k", H_kv=2, H_q=4, new=(60, 200), lengths=(700, 300))]
+    ws = kinds[0][0].make_chunk_workspace()
+    for _ in range(3):
+        for cache, call, refs in kinds:
+            assert cache.chunk_ws_bytes == ws.numel()
+            out = torch.full_like(refs[0], float("nan"))
+            call(out, 2, workspace=ws)
+            assert torch.equal(out, refs[2])
+    assert kinds[0][0].chunk_status(ws) == 0
