@@ -242,3 +242,20 @@ def test_turned_queries_past_fp16_s_range(name, dt, n):
     want, bound = S.chunk_attention(oc, bufs, 0, raw16(q[0]), np.array([0, n]), [T], 0, 0, None if table is None else table.numpy(), True)
     err = np.abs(O.input_to_f32(raw16(out[0]), dt).astype(np.float64) - want)
     assert np.all(err <= bound), float(np.max(err / bound))
+
+
+CH = K.AXIS_CHANNEL
+
+
+@pytest.mark.parametrize("dt", [K.DT_F16, K.DT_BF16])
+@pytest.mark.parametrize("kw", [
+    dict(flags=0), dict(flags=0, k_fmt=K.Fmt(8, 32, CH), k_cold=K.Fmt(4, 32, CH)), dict(flags=0, k_fmt=K.Fmt(3, 32, CH), k_cold=K.Fmt(8, 32, CH)),
+    dict(flags=K.ZP_K | K.ZP_V), dict(flags=K.ZP_K, v_fmt=K.Fmt(8, 32), v_cold=K.Fmt(3, 32)),
+    dict(flags=K.K_PRE_ROPE, k_fmt=K.Fmt(8, 32, CH), k_cold=K.Fmt(2, 32, CH)),
+    dict(flags=0, k_fmt=K.Fmt(4, 32), k_cold=K.Fmt(8, 32), v_fmt=K.Fmt(4, 32, CH), v_cold=K.Fmt(2, 32, CH))])
+def test_two_tiers_of_every_width(dt, kw):
+    """Hot and cold keys share one factor, whichever of them is the wider."""
+    w = workload("mistral7b_hotcold", [391, 200], L=1, heads=(2, 4), hot_window=96, residual_window=40, in_dtype=dt, **kw)
+    for n in ([3, 1], [20, 9], [150, 33]):
+        check(w, n)
+        check(w, n, window=150, sinks=40)
