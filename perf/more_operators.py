@@ -234,7 +234,8 @@ def _reorder_inputs(case, seed):
     s = {"case": case, "table": table}
     s["refs"] = torch.bincount(table[table >= 0].long(), minlength=pages).to(torch.int32)
     s["seq_lens"] = torch.full((B,), case["context"], dtype=torch.int32, device="cuda")
-    s["seq_lens"] -= torch.randint(0, 2, (B,), generator=g, device="cuda", dtype=torch.int32)  # a finished beam is a token behind
+    behind = torch.randint(0, 2, (B,), generator=g, device="cuda", dtype=torch.int32)  # a finished beam is a token behind
+    s["seq_lens"] -= behind * (end % PAGE != 1)  # in the same pages: none holds pages that it has not begun
     live = torch.rand((G, K), generator=g, device="cuda").argsort(-1)[:, : (K + 1) // 2]  # each with two children
     mix = torch.rand((G, K), generator=g, device="cuda").argsort(-1)
     s["parents"] = live.repeat(1, 2)[:, :K].gather(1, mix).to(torch.int32)
