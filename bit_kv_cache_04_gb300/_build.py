@@ -37,6 +37,7 @@ SOURCES = [
     ("dequant.cu", []),
     ("qk_norm_rope.cu", []),
     ("pages.cu", []),
+    ("beam_select.cu", []),
     ("chunk_attention.cu", []),
     ("chunk_attention_d128.cu", []),
     ("chunk_attention_d256.cu", []),

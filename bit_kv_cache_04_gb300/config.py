@@ -22,6 +22,7 @@ ZP_K = 32
 ZP_V = 64
 DT_F16 = 0
 DT_BF16 = 1
+DT_F32 = 2  # logits only
 
 DEV_CAPACITY = 1
 DEV_PAGE = 2

@@ -21,12 +21,14 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxPageBatch = 32768;
+constexpr int kMaxReorder = 32;  // slots of a group
+constexpr int kReorderThreads = 128;
 
 // Workspace (int32 words after the status block): header, then arrays.
 struct PagesWs {
   uint32_t* status;
   int32_t* n_moves;  // pages to copy
-  int32_t* mark;     // [batch] 1 while a sequence is in the current list; zero between calls
+  int32_t* mark;     // [batch] 1 while a sequence is in the current list; reorder: a group's blocks that have begun; zero between calls
   int32_t* src;      // [n] moves: page copied from
   int32_t* dst;      // [n] and to
   int32_t* map;      // [n_pages] compact: new id, or -1 of a free page
@@ -422,6 +424,136 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesArgs a)
   if (threadIdx.x == 0) *a.ws.n_moves = movers;
 }
 
+// ---- reorder -------------------------------------------------------------------------
+
+// A group's slots after a selection: slot b becomes what slot parents[b] was.  Every column of the table (and every
+// 16-byte word of the windows) belongs to one thread, which reads all it needs of the group before it writes: no copy
+// of the old state is kept.
+
+// The group's parents and lengths into shared memory; 0, or the status bit of what is wrong with them.
+__device__ __forceinline__ uint32_t group_state(const PagesArgs& a, int group, int* parent, int* len) {
+  bool bad = false, bad_len = false;
+  if ((int)threadIdx.x < a.n) {
+    const int p = a.other[(int64_t)group * a.n + threadIdx.x], T = a.seq_lens[(int64_t)group * a.n + threadIdx.x];
+    parent[threadIdx.x] = p;
+    len[threadIdx.x] = T;
+    bad = p < 0 || p >= a.n;
+    bad_len = T < 0 || T > a.lo.max_T;
+  }
+  const int any = __syncthreads_or(bad), any_len = __syncthreads_or(bad_len);
+  return any ? KVQ_DEV_SEQ : any_len ? KVQ_DEV_LENGTH : 0;
+}
+
+// Block (group, run of table columns).  Pages that hold quantized tokens go to all children; pages behind them, taken by a
+// reservation, must stay one sequence's own: the heir's, which is the slot itself or else its lowest child.
+// A page's count changes by what its entries become, summed over the group's slots that hold it in this column: pages that all of
+// them share, the prompt's, take no atomics.
+__global__ void __launch_bounds__(kReorderThreads) reorder_kernel(PagesArgs a) {
+  __shared__ int parent[kMaxReorder], children[kMaxReorder], heir[kMaxReorder], len[kMaxReorder], share[kMaxReorder];
+  __shared__ int column[kMaxReorder][kReorderThreads];
+  __shared__ bool last;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int group = blockIdx.x, K = a.n, mp = a.lo.max_pages;
+  if (const uint32_t wrong = group_state(a, group, parent, len)) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.ws.status, wrong);
+    return;
+  }
+  if ((int)threadIdx.x < K) {
+    int n = 0, low = -1;
+    for (int b = K - 1; b >= 0; --b)
+      if (parent[b] == (int)threadIdx.x) {
+        ++n;
+        low = b;
+      }
+    children[threadIdx.x] = n;
+    heir[threadIdx.x] = parent[threadIdx.x] == (int)threadIdx.x ? (int)threadIdx.x : low;
+    share[threadIdx.x] = (int)(((int64_t)q_end_of(a.lo, len[threadIdx.x]) + a.lo.pt - 1) / a.lo.pt);
+  }
+  // the lengths are written by the group's last block: the others have read them
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(a.ws.mark + (int64_t)group * K, 1) == (int)gridDim.y - 1;
+  }
+  __syncthreads();
+  if (last) {
+    if (threadIdx.x == 0) a.ws.mark[(int64_t)group * K] = 0;
+    if ((int)threadIdx.x < K) a.seq_lens[(int64_t)group * K + threadIdx.x] = len[parent[threadIdx.x]];
+  }
+  const int j = blockIdx.y * kReorderThreads + threadIdx.x;
+  if (j >= mp) return;
+  int32_t* at = a.table + (int64_t)group * K * mp + j;
+  int* mine = &column[0][threadIdx.x];
+  bool same = true;
+#pragma unroll 8
+  for (int b = 0; b < K; ++b) mine[b * kReorderThreads] = at[(int64_t)b * mp];
+  const int p0 = mine[0];
+  for (int b = 0; b < K; ++b) same &= mine[b * kReorderThreads] == p0 && (p0 == -1 || j < share[b]);
+  if (same && p0 >= -1 && p0 < a.lo.n_pages) return;
+  for (int b = 0; b < K; ++b) {
+    const int p = mine[b * kReorderThreads];
+    if (p == -1) continue;
+    if (p < 0 || p >= a.lo.n_pages) {
+      atomicOr(a.ws.status, KVQ_DEV_PAGE);
+      continue;
+    }
+    bool again = false;
+    int change = 0;
+    for (int c = 0; c < K; ++c)
+      if (mine[c * kReorderThreads] == p) {
+        again |= c < b;
+        change += (j < share[c] ? children[c] : children[c] > 0) - 1;
+      }
+    if (!again && change) atomicAdd(a.refs + p, change);
+  }
+  for (int b = 0; b < K; ++b) {
+    const int s = parent[b];
+    if (s != b) at[(int64_t)b * mp] = j < share[s] || heir[s] == b ? mine[s * kReorderThreads] : -1;
+  }
+}
+
+// The 16-bit windows of one (group, layer, K or V): a thread a word.  Only slots that change are written, and
+// only those that they come from are read, each once.  N: sources that fit a thread's registers.
+template <int N>
+__global__ void __launch_bounds__(kReorderThreads) reorder_window_kernel(PagesArgs a) {
+  __shared__ int parent[kMaxReorder], len[kMaxReorder], source[kMaxReorder], first[kMaxReorder + 1], to[kMaxReorder];
+  __shared__ int n_sources;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int group = blockIdx.z, K = a.n, layer = blockIdx.y >> 1;
+  if (group_state(a, group, parent, len)) return;  // (the other kernel has said so; lengths that it has moved are good ones)
+  if (threadIdx.x == 0) {  // the moves, by source
+    int n = 0, m = 0;
+    for (int s = 0; s < K; ++s) {
+      const int m0 = m;
+      for (int b = 0; b < K; ++b)
+        if (parent[b] == s && b != s) to[m++] = b;
+      if (m > m0) {
+        source[n] = s;
+        first[n++] = m0;
+      }
+    }
+    first[n] = m;
+    n_sources = n;
+  }
+  __syncthreads();
+  const int64_t unit = (int64_t)a.lo.H * a.lo.ring * a.lo.D / 8;  // 16-byte words of one (layer, sequence)
+  [[maybe_unused]] const CachePtrs& cp = a.cp;
+  if (!KVQ_CHECK(layer < a.lo.L && (group + 1) * K <= a.lo.B)) return;
+  uint4* base = reinterpret_cast<uint4*>(blockIdx.y & 1 ? a.cp.v_resid : a.cp.k_resid) + ((int64_t)layer * a.lo.B + (int64_t)group * K) * unit;
+  const int sources = n_sources;
+  for (int64_t e = blockIdx.x * (int64_t)kReorderThreads + threadIdx.x; e < unit; e += (int64_t)gridDim.x * kReorderThreads) {
+    uint4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < sources) v[i] = base[source[i] * unit + e];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < sources)
+        for (int m = first[i]; m < first[i + 1]; ++m) base[to[m] * unit + e] = v[i];
+  }
+}
+
 // ---- copies --------------------------------------------------------------------
 
 // Copies page src[m] to dst[m] for every move, all layers, K and V.  The rows
@@ -625,6 +757,39 @@ kvq_status kvq_pages_reserve(const kvq_config* cfg, const kvq_cache* cache, int3
   if (e == cudaSuccess) e = launch_dependent(reserve_kernel, dim3(1), dim3(kPlanThreads), smem, (cudaStream_t)stream, a);
   if (e == cudaSuccess) e = launch_copy<false>(a, n, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "page reserve kernels");
+  return ok();
+}
+
+kvq_status kvq_pages_reorder(const kvq_config* cfg, const kvq_cache* cache, int32_t* block_table, int32_t* refs,
+                             int32_t* seq_lens, const int32_t* parents, int32_t group, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  PagesArgs a{};
+  kvq_status st = pages_args(cfg, cache, true, block_table, refs, workspace, ws_bytes, &a);
+  if (st != KVQ_OK) return st;
+  if (group < 1 || cfg->batch % group) return fail(KVQ_ERR_ARG, "group=%d does not divide batch=%d", group, cfg->batch);
+  if (group > kMaxReorder) return fail(KVQ_ERR_UNSUPPORTED, "group=%d > %d", group, kMaxReorder);
+  if (!seq_lens || !parents) return fail(KVQ_ERR_ARG, "seq_lens / parents is NULL");
+  if (((uintptr_t)seq_lens | (uintptr_t)parents) & 3u) return fail(KVQ_ERR_ARG, "lists must be 4-byte aligned");
+  if (a.lo.ring && a.lo.L > 32767) return fail(KVQ_ERR_UNSUPPORTED, "L=%d", a.lo.L);  // two rows of the windows' grid each
+  const int64_t columns = ((int64_t)cfg->max_pages_per_seq + kReorderThreads - 1) / kReorderThreads;
+  if (columns > 65535) return fail(KVQ_ERR_UNSUPPORTED, "max_pages_per_seq=%d", cfg->max_pages_per_seq);
+  a.seq_lens = seq_lens;
+  a.other = parents;
+  a.n = group;
+  const int groups = cfg->batch / group;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = launch_dependent(reorder_kernel, dim3(groups, (unsigned)columns), dim3(kReorderThreads), 0, s, a);
+  if (e == cudaSuccess && a.lo.ring && group > 1) {
+    // words in turn once the grid fills the card several times
+    const int64_t unit = (int64_t)a.lo.H * a.lo.ring * a.lo.D / 8, blocks = (int64_t)groups * a.lo.L * 2;
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((unit + kReorderThreads - 1) / kReorderThreads,
+                                                                 std::max<int64_t>(1, (int64_t)sm_count() * 64 / blocks)));
+    const dim3 grid((unsigned)parts, (unsigned)(2 * a.lo.L), (unsigned)groups);
+    e = group <= 8    ? launch_dependent(reorder_window_kernel<8>, grid, dim3(kReorderThreads), 0, s, a)
+        : group <= 16 ? launch_dependent(reorder_window_kernel<16>, grid, dim3(kReorderThreads), 0, s, a)
+                      : launch_dependent(reorder_window_kernel<32>, grid, dim3(kReorderThreads), 0, s, a);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "page reorder kernels");
   return ok();
 }
 

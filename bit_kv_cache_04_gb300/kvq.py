@@ -13,7 +13,7 @@ import os
 from typing import Optional, Tuple
 
 from .config import (AXIS_CHANNEL, AXIS_TOKEN, DEV_BOUNDS, DEV_CAPACITY, DEV_LENGTH, DEV_PAGE,  # noqa: F401
-                     DEV_RANGE, DEV_SEQ, DEV_STALL, DT_BF16, DT_F16, K_PRE_ROPE, ROPE_BANDS, ROPE_LINEAR, ROPE_NONE,
+                     DEV_RANGE, DEV_SEQ, DEV_STALL, DT_BF16, DT_F16, DT_F32, K_PRE_ROPE, ROPE_BANDS, ROPE_LINEAR, ROPE_NONE,
                      ROPE_NTK, ROPE_YARN, ROTATE_K, ROTATE_V, TBQ4_K, TBQ4_V, ZP_K, ZP_V, Config, Fmt)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -116,6 +116,10 @@ def _load():
         "kvq_pages_fork": ([cfgp, cachep, vp, vp, vp, vp, vp, i32, vp, sz, vp], ctypes.c_int),
         "kvq_pages_reserve": ([cfgp, cachep, vp, vp, vp, vp, vp, i32, vp, sz, vp], ctypes.c_int),
         "kvq_pages_compact": ([cfgp, cachep, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+        "kvq_pages_reorder": ([cfgp, cachep, vp, vp, vp, vp, i32, vp, sz, vp], ctypes.c_int),
+        "kvq_beam_workspace_bytes": ([i32, i32, i32, P(sz)], ctypes.c_int),
+        "kvq_beam_workspace_init": ([i32, i32, i32, vp, sz, vp], ctypes.c_int),
+        "kvq_beam_select": ([vp, i32, i64, i64, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
         "kvq_chunk_workspace_bytes": ([cfgp, P(sz)], ctypes.c_int),
         "kvq_chunk_workspace_init": ([cfgp, vp, sz, vp], ctypes.c_int),
         "kvq_chunk_attention": ([cfgp, cachep, i32, i32, vp, vp, i32, i32, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
@@ -139,6 +143,7 @@ EXPORTED = ("kvq_version", "kvq_last_error", "kvq_validate_config", "kvq_block_b
             "kvq_read_device_status", "kvq_clear_device_status", "kvq_test_force_stall",
             "kvq_test_shrink_bounds", "kvq_rope_plan_init", "kvq_qk_norm_rope", "kvq_pages_workspace_bytes",
             "kvq_pages_init", "kvq_pages_release", "kvq_pages_fork", "kvq_pages_reserve", "kvq_pages_compact",
+            "kvq_pages_reorder", "kvq_beam_workspace_bytes", "kvq_beam_workspace_init", "kvq_beam_select",
             "kvq_chunk_workspace_bytes", "kvq_chunk_workspace_init", "kvq_chunk_attention")
 
 
@@ -219,6 +224,12 @@ def kvq_decode_splits(cfg: Config, n_layers: int) -> int:
 def kvq_pages_workspace_bytes(cfg: Config) -> int:
     out = ctypes.c_size_t()
     _check(LIB.kvq_pages_workspace_bytes(ctypes.byref(_to_c(cfg)), ctypes.byref(out)))
+    return out.value
+
+
+def kvq_beam_workspace_bytes(n_groups: int, beams: int, vocab: int) -> int:
+    out = ctypes.c_size_t()
+    _check(LIB.kvq_beam_workspace_bytes(n_groups, beams, vocab, ctypes.byref(out)))
     return out.value
 
 
@@ -549,6 +560,14 @@ class PagePool:
                                      _ptr(self.refs), _ptr(seq_lens), _ptr(seqs), _ptr(n_new), seqs.numel(),
                                      *self._ws(stream)))
 
+    def reorder(self, parents, group, seq_lens, stream=None):
+        """Slot b of every `group` consecutive sequences becomes what slot parents[b] of the group was (kvq_pages_reorder)."""
+        self._lists(seq_lens, parents)
+        if parents.numel() != self.cache.cfg.batch:
+            raise ValueError("parents is [batch]")
+        _check(LIB.kvq_pages_reorder(self._cfg(), ctypes.byref(self.cache.c_cache), _ptr(self.cache.block_table),
+                                     _ptr(self.refs), _ptr(seq_lens), _ptr(parents), group, *self._ws(stream)))
+
     def compact(self, refs_out=None, table_out=None, stream=None):
         """Moves the used pages together.  Without outputs the cache's table and the counts are changed in place.  With
         them the pages have moved all the same, and nothing may use the cache until the caller has copied table_out into
@@ -571,3 +590,39 @@ class PagePool:
 
     def clear_status(self, stream=None):
         _check(LIB.kvq_clear_device_status(_ptr(self.workspace), _stream(stream)))
+
+
+class BeamSelect:
+    """Selection of the next tokens of beam searches (kvq_beam_select) and its workspace: for calls in order, of
+    these sizes.  Calls that may run at the same time need an object each."""
+
+    def __init__(self, groups: int, beams: int, vocab: int, device="cuda", stream=None):
+        import torch
+
+        self.sizes = (groups, beams, vocab)
+        self.ws_bytes = kvq_beam_workspace_bytes(*self.sizes)
+        with _on(stream):
+            self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.index = self.workspace.get_device()
+        _here(self.index)
+        _check(LIB.kvq_beam_workspace_init(*self.sizes, _ptr(self.workspace), self.ws_bytes, _stream(stream)))
+
+    def select(self, logits, scores, scores_out, tokens, parents, done=None, done_out=None, eos=-1, stream=None):
+        """The best continuations of logits [groups, beams, vocab] (fp16, bf16 or fp32; any strides of groups and
+        beams) and scores [groups, beams]: into scores_out, tokens, parents and done_out, all [groups, beams]."""
+        import torch
+
+        kinds = {torch.float16: DT_F16, torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+        groups, beams, vocab = self.sizes
+        if logits.dtype not in kinds or logits.shape != self.sizes or (vocab > 1 and logits.stride(2) != 1):
+            raise ValueError("logits are [groups, beams, vocab] of fp16, bf16 or fp32 with contiguous tokens")
+        for t in (scores, scores_out):
+            if t.dtype != torch.float32 or t.shape != (groups, beams) or not t.is_contiguous():
+                raise ValueError("scores are contiguous fp32 tensors [groups, beams]")
+        for t in (tokens, parents, done, done_out):
+            if t is not None and (t.dtype != torch.int32 or t.shape != (groups, beams) or not t.is_contiguous()):
+                raise ValueError("tokens, parents and done are contiguous int32 tensors [groups, beams]")
+        _here(self.index, logits, scores, scores_out, tokens, parents, done, done_out)
+        _check(LIB.kvq_beam_select(_ptr(logits), kinds[logits.dtype], logits.stride(0), logits.stride(1), groups, beams,
+                                   vocab, _ptr(scores), _ptr(done), eos, _ptr(scores_out), _ptr(tokens), _ptr(parents),
+                                   _ptr(done_out), _ptr(self.workspace), self.ws_bytes, _stream(stream)))

@@ -98,7 +98,7 @@ typedef enum {
   KVQ_ERR_WORKSPACE = 5     /* workspace missing or too small */
 } kvq_status;
 
-typedef enum { KVQ_DT_F16 = 0, KVQ_DT_BF16 = 1 } kvq_dtype;
+typedef enum { KVQ_DT_F16 = 0, KVQ_DT_BF16 = 1, KVQ_DT_F32 = 2 /* logits only */ } kvq_dtype;
 
 /* A block spans G consecutive channels of one token (TOKEN) or one channel
  * over G consecutive tokens (CHANNEL). */
@@ -548,6 +548,48 @@ KVQ_API kvq_status kvq_pages_reserve(const kvq_config* cfg, const kvq_cache* cac
 KVQ_API kvq_status kvq_pages_compact(const kvq_config* cfg, const kvq_cache* cache, const int32_t* block_table,
                                      const int32_t* refs, int32_t* table_out, int32_t* refs_out, void* workspace,
                                      size_t ws_bytes, void* stream);
+
+/* Reorders the sequences of a beam search: the batch is groups of `group`
+ * consecutive slots (1..32, dividing batch), and slot b of a group becomes what slot
+ * parents[b] of the same group was before the call: its pages that hold quantized tokens, length and 16-bit
+ * window (all layers).  Pages that are reserved behind those stay one sequence's own: the slot's that keeps
+ * it (parents[b] = b), else its lowest child's; without a child they are freed, and the other children have -1 there.
+ * parents [batch] int32, device, counted from the group's
+ * first slot, as kvq_beam_select writes them.  refs follow the table: a page that no slot
+ * holds any more is free, one that several hold is copied by kvq_pages_reserve before
+ * it is written.  No page moves.  A group with a parent outside [0, group) (KVQ_DEV_SEQ) or a bad length (KVQ_DEV_LENGTH)
+ * stays as it was; a table entry outside the pool sets KVQ_DEV_PAGE, moves along and is not counted. */
+KVQ_API kvq_status kvq_pages_reorder(const kvq_config* cfg, const kvq_cache* cache, int32_t* block_table,
+                                     int32_t* refs, int32_t* seq_lens, const int32_t* parents, int32_t group,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- selection of a beam search ----------------------------------------------------
+ * The `beams` best continuations of every group's beams over the whole vocabulary.  With x the logits of beam b and s its
+ * score, the candidate (b, v) scores
+ *   c = s + x_v - log sum_u e^(x_u);
+ * a finished beam has one candidate, the end token with c = s.  The group's candidates in descending order, ties to the
+ * lower beam and then the lower token:
+ *   scores_out[i] = c, tokens[i] = v, parents[i] = b, done_out[i] = the beam was finished, or v is the end token.
+ * Maxima are taken of the logits as they are, sums in fp32 a thread and in 64 bits across threads' pieces, scores are compared
+ * in 64 bits and rounded once.
+ *  logits: [n_groups][beams][vocab] of dtype (KVQ_DT_F16, BF16 or F32), device; strides in elements between groups and beams, tokens
+ *          contiguous.  -inf: the token may not follow.  NaN counts as -inf, +inf as the largest finite fp32 number.
+ *  scores: [n_groups][beams] fp32 (-inf: an empty beam, e.g. all but the first of a new search; NaN counts as -inf).
+ *  done:   [n_groups][beams] int32, not 0: finished; or NULL (none is).  Needs an end token.
+ *  eos:    the end token, or -1 for none.
+ *  scores_out, tokens, parents, done_out: [n_groups][beams]; scores_out may be scores and done_out may be done,
+ *          nothing else may overlap; done_out may be NULL.
+ * With fewer candidates above -inf than beams the rest have -inf, the lowest beams and tokens first.
+ * beams in 1..32, vocab below 2^26, n_groups * beams at most 2^24.
+ *  workspace: kvq_beam_workspace_bytes bytes, 256-byte aligned, prepared once by kvq_beam_workspace_init for
+ *          these sizes; calls that may run at the same time (captured ones that are replayed side by side, too) need one each. */
+KVQ_API kvq_status kvq_beam_workspace_bytes(int32_t n_groups, int32_t beams, int32_t vocab, size_t* bytes);
+KVQ_API kvq_status kvq_beam_workspace_init(int32_t n_groups, int32_t beams, int32_t vocab, void* workspace, size_t ws_bytes,
+                                           void* stream);
+KVQ_API kvq_status kvq_beam_select(const void* logits, int32_t dtype, int64_t group_stride, int64_t beam_stride,
+                                   int32_t n_groups, int32_t beams, int32_t vocab, const float* scores, const int32_t* done,
+                                   int32_t eos, float* scores_out, int32_t* tokens, int32_t* parents, int32_t* done_out,
+                                   void* workspace, size_t ws_bytes, void* stream);
 
 /* ---- attention of a chunk of new tokens over the packed cache ---------------------
  * The last n_b = cu_q[b+1] - cu_q[b] cached tokens of sequence b attend to

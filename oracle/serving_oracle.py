@@ -135,6 +135,61 @@ class Pages:
                 x[:, d] = x[:, s]
 
 
+    def reorder(self, parents: List[int], group: int):
+        """Slot b of every `group` slots becomes what slot parents[b] of the group was.  Pages behind the quantized tokens stay
+        one sequence's: the slot's own, or its lowest child's."""
+        B = len(self.table)
+        src = [b // group * group + int(parents[b]) for b in range(B)]
+        old, lens = self.table.copy(), self.lens.copy()
+        windows = [w.copy() for w in self.windows]
+        for b in range(B):
+            s = src[b]
+            row = old[s].copy()
+            heir = s if src[s] == s else src.index(s)
+            if heir != b:
+                row[-(-self.q_end(lens[s]) // self.pt):] = -1
+            self.table[b], self.lens[b] = row, lens[s]
+            for w, o in zip(self.windows, windows):
+                w[:, b] = o[:, s]
+        self.refs[:] = 0
+        for p in self.table.flat:
+            if p >= 0:
+                self.refs[p] += 1
+
+
+# ---- selection of a beam search ---------------------------------------------------
+
+
+def beam_select(logits: np.ndarray, scores: np.ndarray, done=None, eos=-1):
+    """(scores, tokens, parents, done) of the best continuations; logits [groups, beams, vocab] as fp64 values."""
+    G, K, V = logits.shape
+    x = np.array(logits, np.float64)
+    top = float(np.finfo(np.float32).max)
+    x[np.isnan(x)] = -np.inf
+    x[x == np.inf] = top
+    s = np.array(scores, np.float64)
+    s[np.isnan(s)] = -np.inf
+    s = np.minimum(s, top)
+    res = [np.empty((G, K)), *(np.empty((G, K), np.int64) for _ in range(3))]
+    for g in range(G):
+        c = []  # (-score, beam, token)
+        for b in range(K):
+            if done is not None and done[g, b]:
+                c.append((-s[g, b], b, eos))
+                continue
+            m = x[g, b].max()
+            if m == -np.inf:
+                c += [(np.inf, b, v) for v in range(V)]
+                continue
+            d = x[g, b] - m
+            total = math.log(math.fsum(np.exp(d)))
+            c += [(-(s[g, b] + (d[v] - total)), b, v) for v in range(V)]
+        for i, (score, b, v) in enumerate(sorted(c)[:K]):
+            res[0][g, i], res[1][g, i], res[2][g, i] = -score, v, b
+            res[3][g, i] = int(v == eos or bool(done is not None and done[g, b]))
+    return res
+
+
 # ---- chunk attention ------------------------------------------------------------------
 
 
