@@ -42,6 +42,10 @@ SOURCES = [
     ("chunk_attention_d128.cu", []),
     ("chunk_attention_d256.cu", []),
     ("chunk_attention_few.cu", []),
+    ("prefix_attention.cu", []),
+    ("prefix_attention_d128.cu", []),
+    ("prefix_attention_d256.cu", []),
+    ("prefix_attention_few.cu", []),
 ]
 
 

@@ -30,6 +30,71 @@ ChunkWs chunk_ws(const kvq_config* c) {
 }
 
 }  // namespace
+
+size_t chunk_workspace_bytes(const kvq_config* cfg, size_t* zeroed) {
+  const ChunkWs w = chunk_ws(cfg);
+  if (zeroed) *zeroed = w.partials;
+  return w.total;
+}
+
+int chunk_workspace(const kvq_config* cfg, void* workspace, ChunkArgs* a) {
+  const ChunkWs w = chunk_ws(cfg);
+  a->status = (uint32_t*)workspace;
+  a->cp.status = a->status;
+  a->left = a->status + 1;
+  a->tickets = (uint32_t*)((char*)workspace + w.tickets);
+  a->nonfinite = (uint32_t*)((char*)workspace + w.nonfinite);
+  a->partials = (float*)((char*)workspace + w.partials);
+  return w.grid;
+}
+
+kvq_status chunk_common(const kvq_config* cfg, ChunkArgs* args, int most, int64_t owners, int* form) {
+  ChunkArgs& a = *args;
+  a.stall_polls = stall_polls();
+  const bool wide = a.lo.kf.bits == 8 || (a.lo.tiered && a.lo.kc.bits == 8);
+  const int shift = cfg->in_dtype == KVQ_DT_F16 ? 0 : wide ? 8 : 4;  // the largest code's bits: code times scale stays in fp16's range
+  a.k_pre = std::ldexp(1.f, -shift);
+  a.q_pre = cfg->flags & KVQ_ROTATE_K ? 0.0625f : 1.f;
+  a.score_scale = (float)(1.4426950408889634 / std::sqrt((double)cfg->D)) / (a.k_pre * a.q_pre);
+  a.k_one = ((25u - shift) << 10) * 0x10001u;
+  if (cfg->flags & KVQ_K_PRE_ROPE)
+    for (int i = 0; i < cfg->D / 2; ++i)
+      a.turns[i] = (uint64_t)std::ldexp(std::pow((double)cfg->rope_theta, -2.0 * i / cfg->D) / 6.283185307179586476925286766559, 64);
+  const int64_t rows = (int64_t)most * a.lo.g;
+  if (rows > (int64_t)1 << 28) return fail(KVQ_ERR_UNSUPPORTED, "%d tokens x %d heads", most, a.lo.g);
+  const int mode = cfg->D != 128 ? kChunkShared : rows <= kFewRows ? kChunkFew : rows > 128 ? kChunkPaired : kChunkShared;
+  const int tile = chunk_tile(cfg->D), row_tile = mode == kChunkPaired ? 256 : 128;
+  // the kernel counts its tiles in 32 bits
+  const int64_t units = ((int64_t)a.total_q * a.lo.g / row_tile + owners) * a.n_layers * cfg->H_kv;
+  if (units * (cfg->max_T / tile + 2) > 0x7fffffff - 2 * sm_count())
+    return fail(KVQ_ERR_UNSUPPORTED, "too many tiles for one call: pass fewer layers or rows");
+  a.g_magic = (uint32_t)((1ull << 32) / a.lo.g + 1);
+  a.turn_here = (cfg->flags & KVQ_ROTATE_K) && rows <= 64 ? 1 : 0;
+  a.cols = rows <= 16 ? 16 : kFewRows;
+  a.by_warp = rows > 4 * row_tile;
+  // Staging: 32-token subtiles as single bulk copies; pages of fewer tokens
+  // as copies of their own when their bytes are whole 16-byte words and a
+  // tile has at most one page per lane; other pages by plain loads.
+  int sub = 0;
+  for (const FmtInfo* f : {&a.lo.kf, &a.lo.vf, &a.lo.kc, &a.lo.vc})
+    sub = std::max(sub, f->axis == KVQ_AXIS_CHANNEL ? f->row : 32 * f->row);
+  a.sub_bytes = (sub + 15) & ~15;
+  a.slot_bytes = a.sub_bytes * (chunk_tile(cfg->D) / 64);
+  a.copy_shift = 5;
+  if (a.lo.paged && a.lo.pt % 32 != 0) {
+    const bool fits = 32 % a.lo.pt == 0 && chunk_tile(cfg->D) / a.lo.pt <= 32 &&
+                      (a.lo.pt * a.lo.kf.row) % 16 == 0 && (a.lo.pt * a.lo.vf.row) % 16 == 0;
+    if (fits) {
+      a.small_pages = 1;
+      while ((1 << a.copy_shift) > a.lo.pt) --a.copy_shift;
+    } else {
+      a.direct = 1;
+    }
+  }
+  *form = mode;
+  return KVQ_OK;
+}
+
 }  // namespace kvq
 
 using namespace kvq;
@@ -94,57 +159,12 @@ kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* cache, in
   a.max_q = max_q;
   a.window = window;
   a.sinks = sinks;
-  a.stall_polls = stall_polls();
-  const bool wide = a.lo.kf.bits == 8 || (a.lo.tiered && a.lo.kc.bits == 8);
-  const int shift = cfg->in_dtype == KVQ_DT_F16 ? 0 : wide ? 8 : 4;  // the largest code's bits: code times scale stays in fp16's range
-  a.k_pre = std::ldexp(1.f, -shift);
-  a.q_pre = cfg->flags & KVQ_ROTATE_K ? 0.0625f : 1.f;
-  a.score_scale = (float)(1.4426950408889634 / std::sqrt((double)cfg->D)) / (a.k_pre * a.q_pre);
-  a.k_one = ((25u - shift) << 10) * 0x10001u;
-  a.status = (uint32_t*)workspace;
-  a.cp.status = a.status;
-  if (cfg->flags & KVQ_K_PRE_ROPE)
-    for (int i = 0; i < cfg->D / 2; ++i)
-      a.turns[i] = (uint64_t)std::ldexp(std::pow((double)cfg->rope_theta, -2.0 * i / cfg->D) / 6.283185307179586476925286766559, 64);
-  a.left = a.status + 1;
-  const ChunkWs w = chunk_ws(cfg);
-  a.tickets = (uint32_t*)((char*)workspace + w.tickets);
-  a.nonfinite = (uint32_t*)((char*)workspace + w.nonfinite);
-  a.partials = (float*)((char*)workspace + w.partials);
-  const int64_t rows = (int64_t)max_q * a.lo.g;
-  if (rows > (int64_t)1 << 28) return fail(KVQ_ERR_UNSUPPORTED, "max_q=%d x %d heads", max_q, a.lo.g);
-  const int mode = cfg->D != 128 ? kChunkShared : rows <= kFewRows ? kChunkFew : rows > 128 ? kChunkPaired : kChunkShared;
-  const int tile = chunk_tile(cfg->D), row_tile = mode == kChunkPaired ? 256 : 128;
-  // the kernel counts its tiles in 32 bits
-  const int64_t units = ((int64_t)total_q * a.lo.g / row_tile + cfg->batch) * n_layers * cfg->H_kv;
-  if (units * (cfg->max_T / tile + 2) > 0x7fffffff - 2 * w.grid)
-    return fail(KVQ_ERR_UNSUPPORTED, "too many tiles for one call: pass fewer layers or rows");
-  a.g_magic = (uint32_t)((1ull << 32) / a.lo.g + 1);
-  a.turn_here = (cfg->flags & KVQ_ROTATE_K) && rows <= 64 ? 1 : 0;
-  a.cols = rows <= 16 ? 16 : kFewRows;
-  a.by_warp = rows > 4 * row_tile;
-  // Staging: 32-token subtiles as single bulk copies; pages of fewer tokens
-  // as copies of their own when their bytes are whole 16-byte words and a
-  // tile has at most one page per lane; other pages by plain loads.
-  int sub = 0;
-  for (const FmtInfo* f : {&a.lo.kf, &a.lo.vf, &a.lo.kc, &a.lo.vc})
-    sub = std::max(sub, f->axis == KVQ_AXIS_CHANNEL ? f->row : 32 * f->row);
-  a.sub_bytes = (sub + 15) & ~15;
-  a.slot_bytes = a.sub_bytes * (chunk_tile(cfg->D) / 64);
-  a.copy_shift = 5;
-  if (a.lo.paged && a.lo.pt % 32 != 0) {
-    const bool fits = 32 % a.lo.pt == 0 && chunk_tile(cfg->D) / a.lo.pt <= 32 &&
-                      (a.lo.pt * a.lo.kf.row) % 16 == 0 && (a.lo.pt * a.lo.vf.row) % 16 == 0;
-    if (fits) {
-      a.small_pages = 1;
-      while ((1 << a.copy_shift) > a.lo.pt) --a.copy_shift;
-    } else {
-      a.direct = 1;
-    }
-  }
-  cudaError_t e = mode == kChunkFew ? launch_chunk_few(a, w.grid, (cudaStream_t)stream)
-                  : cfg->D == 128   ? launch_chunk_d128(a, mode, w.grid, (cudaStream_t)stream)
-                                    : launch_chunk_d256(a, w.grid, (cudaStream_t)stream);
+  const int grid = chunk_workspace(cfg, workspace, &a);
+  int mode;
+  if ((st = chunk_common(cfg, &a, max_q, cfg->batch, &mode)) != KVQ_OK) return st;
+  cudaError_t e = mode == kChunkFew ? launch_chunk_few(a, grid, (cudaStream_t)stream)
+                  : cfg->D == 128   ? launch_chunk_d128(a, mode, grid, (cudaStream_t)stream)
+                                    : launch_chunk_d256(a, grid, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention kernel");
   return ok();
 }

@@ -58,6 +58,17 @@ KVQ_HD constexpr int chunk_streams(int D) { return D == 128 ? 2 : 1; }
 KVQ_HD constexpr int chunk_slot_rows(int D) { return 128 * chunk_streams(D); }
 KVQ_HD constexpr int chunk_part_row(int D) { return D + 4; }  // O, m, l, two pads
 
+// Shared prefixes (kvq_prefix_attention, csrc/prefix_attention.cu): the units are those of segments, which a plan on the device
+// writes: a group's new rows over the prefix that its sequences share (all of them see all of it), and every sequence's rows over
+// the tokens behind that.  A row with both has its two parts in `rows`, joined by a kernel of its own.
+struct Segment {
+  int n, T, cu;  // tokens of rows (0: none), tokens of the cache up to its end, first row of q
+  int b;         // the sequence whose pages are read
+  int from;      // first token
+  int shared;    // 1: a prefix
+  int pad[2];
+};
+
 struct ChunkArgs {
   Layout lo;
   CachePtrs cp;
@@ -87,8 +98,21 @@ struct ChunkArgs {
   float score_scale;   // log2(e) / sqrt(D), both factors undone
   uint32_t k_one;       // the fp16 number whose last bit counts k_pre, twice
   uint64_t turns[128];  // pre-RoPE keys: turns per position of every pair, 64-bit fractions
+  const Segment* segs;  // shared prefixes: [n_groups] prefixes, then [batch] sequences
+  int n_groups, max_group_q;
+  float* rows;          // [prefix, own][n_layers * total_q][H_q][part row]: output, log2 of the sum of 2^scores
 };
 
+// Bytes of the workspace, and of its front part that is zero between calls.
+size_t chunk_workspace_bytes(const kvq_config* cfg, size_t* zeroed);
+// Its parts into the arguments; the grid.
+int chunk_workspace(const kvq_config* cfg, void* workspace, ChunkArgs* a);
+// What follows from the configuration and the rows, at most `most` tokens of each of `owners` (sequences and shared
+// prefixes); the form of the kernel.
+kvq_status chunk_common(const kvq_config* cfg, ChunkArgs* a, int most, int64_t owners, int* form);
+cudaError_t launch_prefix_d128(const ChunkArgs& a, int mode, int grid, cudaStream_t s);
+cudaError_t launch_prefix_few(const ChunkArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_prefix_d256(const ChunkArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_chunk_d128(const ChunkArgs& a, int mode, int grid, cudaStream_t s);
 cudaError_t launch_chunk_few(const ChunkArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_chunk_d256(const ChunkArgs& a, int grid, cudaStream_t s);

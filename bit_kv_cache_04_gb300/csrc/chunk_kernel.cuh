@@ -1,6 +1,7 @@
 // The chunk attention kernel (design in chunk_attention.cuh).
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "chunk_attention.cuh"
@@ -167,6 +168,7 @@ struct Unit {
   int lo;                // first token of the window
   int sink;              // tokens [0, sink) visible besides
   int st, lo_tile, nt;   // sink tiles, first window tile, tiles
+  int seg, from, shared;  // of a segment (SEG): its number, first token, and whether it is a shared prefix
 };
 
 // One CTA's run of a unit: tiles [t0, t1) of it.  Each warp keeps its own in shared memory: registers are short.
@@ -196,15 +198,55 @@ __device__ __forceinline__ bool valid_seq(const ChunkArgs& a, int b, int* n, int
   return c0 >= 0 && c1 >= c0 && c1 <= a.total_q && c1 - c0 <= a.max_q && t >= c1 - c0 && t <= a.lo.max_T;
 }
 
-template <int D, int RT>
+// The owners of rows, in the order of the line: the sequences, or (SEG) the segments.
+template <bool SEG>
+__device__ __forceinline__ int owners(const ChunkArgs& a) {
+  return SEG ? a.n_groups + a.lo.B : a.lo.B;
+}
+template <bool SEG>
+__device__ __forceinline__ int owner(const Unit& u) {
+  return SEG ? u.seg : u.b;
+}
+// Segment i of the plan; what could lead outside the call's tensors is checked again.
+__device__ __forceinline__ bool valid_segment(const ChunkArgs& a, int i, Unit& u) {
+  const int4 x = __ldg(reinterpret_cast<const int4*>(a.segs + i)), y = __ldg(reinterpret_cast<const int4*>(a.segs + i) + 1);
+  u.seg = i;
+  u.n = x.x;
+  u.T = x.y;
+  u.cu = x.z;
+  u.b = x.w;
+  u.from = y.x;
+  u.shared = y.y;
+  const int most = u.shared ? a.max_group_q : a.max_q, seen = u.shared ? u.T : u.T - u.n;
+  return u.n > 0 && u.n <= most && u.cu >= 0 && u.cu <= a.total_q - u.n && u.T > 0 && u.T <= a.lo.max_T && u.b >= 0 &&
+         u.b < a.lo.B && u.from >= 0 && u.from <= seen;
+}
+// Rows' owner i: whether it takes part, and (SEG == false) whether what it says is in order.
+template <bool SEG>
+__device__ __forceinline__ bool load_owner(const ChunkArgs& a, int i, Unit& u) {
+  if constexpr (SEG) return valid_segment(a, i, u);
+  u.b = i;
+  return valid_seq(a, i, &u.n, &u.T, &u.cu);
+}
+// First token that the packed tiers do not hold; a shared prefix is packed to its end.
+template <bool SEG>
+__device__ __forceinline__ int unit_qe(const ChunkArgs& a, const Unit& u) {
+  return SEG && u.shared ? u.T : q_end_of(a.lo, u.T);
+}
+// Position of query row r (counted from the owner's first): the last token that it sees.
+template <bool SEG>
+__device__ __forceinline__ int row_pos(const ChunkArgs& a, const Unit& u, int r) {
+  return SEG && u.shared ? u.T - 1 : u.T - u.n + div_g(a, r);
+}
+template <int D, int RT, bool SEG>
 __device__ __forceinline__ void unit_tiles(const ChunkArgs& a, Unit& u) {
   constexpr int NT = chunk_tile(D);
   u.r0 = u.rt * RT;
   u.rows = min(RT, u.n * a.lo.g - u.r0);
-  u.p_lo = u.T - u.n + div_g(a, u.r0);
-  u.p_hi = u.T - u.n + div_g(a, u.r0 + u.rows - 1);
-  u.lo = a.window ? max(0, u.p_lo - a.window + 1) : 0;
-  u.sink = min(a.sinks, u.lo);
+  u.p_lo = row_pos<SEG>(a, u, u.r0);
+  u.p_hi = row_pos<SEG>(a, u, u.r0 + u.rows - 1);
+  u.lo = SEG ? u.from : a.window ? max(0, u.p_lo - a.window + 1) : 0;
+  u.sink = SEG ? 0 : min(a.sinks, u.lo);
   u.lo_tile = u.lo / NT;
   u.st = min((u.sink + NT - 1) / NT, u.lo_tile);
   u.nt = u.st + u.p_hi / NT - u.lo_tile + 1;
@@ -215,26 +257,26 @@ __device__ __forceinline__ int seq_row_tiles(const ChunkArgs& a, int n) {
   return (n * a.lo.g + RT - 1) / RT;
 }
 
-// Tiles of sequence b (one layer and kv head): summed by one thread, or by the 32 lanes of a warp.
-template <int D, int RT>
+// Tiles of owner b (one layer and kv head): summed by one thread, or by the 32 lanes of a warp.
+template <int D, int RT, bool SEG>
 __device__ __forceinline__ int seq_tiles(const ChunkArgs& a, int b, int lane, int lanes, bool* bad) {
   Unit u;
-  if (!valid_seq(a, b, &u.n, &u.T, &u.cu)) {
-    *bad = true;
+  if (!load_owner<SEG>(a, b, u)) {
+    if (!SEG) *bad = true;  // (of segments the plan has said so)
     return 0;
   }
   int sum = 0;
   const int nrt = seq_row_tiles<D, RT>(a, u.n);
 #pragma unroll 1
   for (u.rt = lane; u.rt < nrt; u.rt += lanes) {
-    unit_tiles<D, RT>(a, u);
+    unit_tiles<D, RT, SEG>(a, u);
     sum += u.nt;
   }
   return sum;
 }
 
 // The CTA's first run (step 0) or the one after r; false past the last.  One lane of a warp.
-template <int D, int RT>
+template <int D, int RT, bool SEG>
 __device__ __forceinline__ bool step_run(const ChunkArgs& a, const LineStart& s, Run& r, int step) {
   Unit u = r.u;
   int pos, t0;
@@ -243,9 +285,8 @@ __device__ __forceinline__ bool step_run(const ChunkArgs& a, const LineStart& s,
     if (pos >= s.end) return false;
     u.layer = s.lh / a.lo.H;
     u.h = s.lh % a.lo.H;
-    u.b = s.b;
+    (void)load_owner<SEG>(a, s.b, u);
     u.rt = s.rt;
-    (void)valid_seq(a, s.b, &u.n, &u.T, &u.cu);
     t0 = s.tile;
   } else {
     pos = r.pos + r.t1 - r.t0;
@@ -255,19 +296,20 @@ __device__ __forceinline__ bool step_run(const ChunkArgs& a, const LineStart& s,
     if (u.rt >= seq_row_tiles<D, RT>(a, u.n)) {  // the next sequence with rows, of the same or the next kv head, layer
       u.rt = 0;
       bool found;
+      int i = owner<SEG>(u);
       do {
-        if (++u.b == a.lo.B) {
-          u.b = 0;
+        if (++i == owners<SEG>(a)) {
+          i = 0;
           if (++u.h == a.lo.H) {
             u.h = 0;
             if (++u.layer == a.n_layers) return false;  // only where lengths changed under the kernel
           }
         }
-        found = valid_seq(a, u.b, &u.n, &u.T, &u.cu) && u.n > 0;
+        found = load_owner<SEG>(a, i, u) && u.n > 0;
       } while (!found);
     }
   }
-  unit_tiles<D, RT>(a, u);
+  unit_tiles<D, RT, SEG>(a, u);
   r.u = u;
   r.t0 = t0;
   r.t1 = min(u.nt, t0 + s.end - pos);
@@ -275,11 +317,11 @@ __device__ __forceinline__ bool step_run(const ChunkArgs& a, const LineStart& s,
   r.first = step == 0;
   return true;
 }
-template <int D, int RT>
+template <int D, int RT, bool SEG>
 __device__ __forceinline__ bool warp_run(const ChunkArgs& a, const LineStart& s, Run& r, int step) {
   bool more = false;
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) more = step_run<D, RT>(a, s, r, step);
+  if ((threadIdx.x & 31) == 0) more = step_run<D, RT, SEG>(a, s, r, step);
   __syncwarp();  // the run is read by every lane
   return __shfl_sync(0xffffffffu, (int)more, 0) != 0;
 }
@@ -503,6 +545,10 @@ __device__ __forceinline__ TileTokens tile_tokens(const Unit& u, int j) {
 struct CachePos {
   int layer, b, h, T, qe, ce;
 };
+template <bool SEG>
+__device__ __forceinline__ CachePos cache_pos(const ChunkArgs& a, const Unit& u) {
+  return CachePos{u.layer + a.layer0, u.b, u.h, u.T, unit_qe<SEG>(a, u), SEG ? 0 : c_end_of(a.lo, u.T)};
+}
 
 // Where the runs of 32 values of a tensor's tile sit.  Rows of the tile in
 // shared memory are tokens (per-token blocks, runs along channels) or
@@ -1040,11 +1086,11 @@ struct FewShared : ChunkShared {
 
 // The loader's work for pages whose rows are no whole 16-byte words, or do not divide a subtile: piece
 // by piece, 2 bytes at a time.  A page out of range reads as blocks of scale 0 (and zero 0).
-template <int D, int RT>
+template <int D, int RT, bool SEG>
 __device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Run& run, bool more, uint32_t raw_at, int lane) {
   uint32_t kt = 0, slot = 0, n = 0;
-  for (; more; more = warp_run<D, RT>(a, sh.start, run, 1)) {
-    const CachePos u{run.u.layer + a.layer0, run.u.b, run.u.h, run.u.T, q_end_of(a.lo, run.u.T), c_end_of(a.lo, run.u.T)};
+  for (; more; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
+    const CachePos u = cache_pos<SEG>(a, run.u);
     for (int j = run.t0; j < run.t1; ++j, ++kt) {
       const TileTokens tt = tile_tokens<D>(run.u, j);
       for (int piece = 0; piece < 4; ++piece, ++n) {
@@ -1079,13 +1125,13 @@ __device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Ru
 
 // A dequantizing warp's half of a piece that the hot path does not cover: one
 // call with few arguments (the caller's registers are short), everything else worked out again.
-template <int D, int DT>
+template <int D, int DT, bool SEG>
 __device__ __forceinline__ void cold_piece(const ChunkArgs& a, ChunkShared& sh, const Run& run, uint32_t tiles_at,
                                         uint32_t raw_at, int dw, uint32_t kt, uint32_t slot, int j) {
   constexpr int NT = chunk_tile(D);
   const int piece = dw >> 1, which = dw >> 2, half = piece & 1, part = dw & 1, lane = threadIdx.x & 31;
   const bool per_channel = (which ? a.lo.vf.axis : a.lo.kf.axis) == KVQ_AXIS_CHANNEL;
-  const CachePos u{run.u.layer + a.layer0, run.u.b, run.u.h, run.u.T, q_end_of(a.lo, run.u.T), c_end_of(a.lo, run.u.T)};
+  const CachePos u = cache_pos<SEG>(a, run.u);
   const TileTokens tt = tile_tokens<D>(run.u, j);
   const int a0 = tt.t0 + half * (NT / 2);
   const uint32_t staged = raw_at + slot * a.slot_bytes, bad = sh.bad_pages[piece * kChunkBars + (kt & (kChunkBars - 1))];
@@ -1118,21 +1164,21 @@ __device__ __forceinline__ int block_sum(int x, int* scan, int* total) {
 }
 
 // Finds this CTA's stretch of the line of tiles and the unit it starts in.
-template <int D, int RT, int THREADS>
+template <int D, int RT, int THREADS, bool SEG>
 __device__ __forceinline__ void find_start(const ChunkArgs& a, ChunkShared& sh) {
   const int lane = a.by_warp ? threadIdx.x & 31 : 0, lanes = a.by_warp ? 32 : 1;
   const int group = a.by_warp ? threadIdx.x >> 5 : threadIdx.x, groups = a.by_warp ? THREADS / 32 : THREADS;
   bool bad = false;
   int line = 0, mine = 0, at = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.lo.B; b0 += groups) {
+  for (int b0 = 0; b0 < owners<SEG>(a); b0 += groups) {
     const int b = b0 + group;
-    mine = b < a.lo.B ? seq_tiles<D, RT>(a, b, lane, lanes, &bad) : 0;
+    mine = b < owners<SEG>(a) ? seq_tiles<D, RT, SEG>(a, b, lane, lanes, &bad) : 0;
     int sum;
     at = line + block_sum<THREADS>(mine, sh.scan, &sum);
     line += sum;
   }
-  if (blockIdx.x == 0) {
+  if (!SEG && blockIdx.x == 0) {
     if (threadIdx.x == 0 && __ldg(a.cu_q) != 0) bad = true;
     if (bad) atomicOr(a.status, KVQ_DEV_LENGTH);
   }
@@ -1149,11 +1195,11 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, ChunkShared& sh) 
   const int lh = begin / line, x = begin - lh * line;  // place within one (layer, kv head)
   int base = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.lo.B && base <= x; b0 += groups) {
+  for (int b0 = 0; b0 < owners<SEG>(a) && base <= x; b0 += groups) {
     const int b = b0 + group;
-    if (a.lo.B > groups) {  // else the sums of the pass above are still there
+    if (owners<SEG>(a) > groups) {  // else the sums of the pass above are still there
       bool ignore = false;
-      mine = b < a.lo.B ? seq_tiles<D, RT>(a, b, lane, lanes, &ignore) : 0;
+      mine = b < owners<SEG>(a) ? seq_tiles<D, RT, SEG>(a, b, lane, lanes, &ignore) : 0;
       int sum;
       at = base + block_sum<THREADS>(mine, sh.scan, &sum);
       base += sum;
@@ -1161,13 +1207,13 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, ChunkShared& sh) 
       base = line;
     }
     const int tiles = a.by_warp ? __reduce_add_sync(0xffffffffu, mine) : mine;  // the sequence's, seen from lane 0
-    if (lane == 0 && b < a.lo.B && x >= at && x < at + tiles) {
+    if (lane == 0 && b < owners<SEG>(a) && x >= at && x < at + tiles) {
       Unit u;
-      (void)valid_seq(a, b, &u.n, &u.T, &u.cu);
+      (void)load_owner<SEG>(a, b, u);
       int left = x - at;
 #pragma unroll 1
       for (u.rt = 0;; ++u.rt) {
-        unit_tiles<D, RT>(a, u);
+        unit_tiles<D, RT, SEG>(a, u);
         if (left < u.nt) break;
         left -= u.nt;
       }
@@ -1185,6 +1231,18 @@ __device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, 
   return (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + u.h * a.lo.g + (row - tok * a.lo.g)) * a.lo.D;
 }
 
+// SEG: whether the unit's rows are one of two parts each, and where row r's part starts.
+template <bool SEG>
+__device__ __forceinline__ bool two_parts(const Unit& u) {
+  return SEG && (u.shared || u.from > 0);
+}
+__device__ __forceinline__ float* part_of_row(const ChunkArgs& a, const Unit& u, int r) {
+  const int64_t row = query_row(a, u, r) / a.lo.D, all = (int64_t)a.n_layers * a.total_q * a.lo.Hq;
+  return a.rows + ((u.shared ? 0 : all) + row) * chunk_part_row(a.lo.D);
+}
+// log2 of a row's sum of 2^scores, L times 2^m; no token seen or none above -inf: -inf
+__device__ __forceinline__ float log2_sum(float m, float L) { return L == 0.f ? -INFINITY : m + log2f(L); }
+
 // V's values that are not finite were left out of the products: every row
 // that sees such a window token gets them afterwards (an infinity stays one
 // under any positive weight, a NaN stays NaN).  What a row gets depends on the kinds that it sees in a channel,
@@ -1194,14 +1252,14 @@ __device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, 
 
 // Kinds among window tokens [t0, t1) of this lane's channels (4 lane .. of every 128-chunk): of chunk c, bits
 // 12 c + e: +inf in channel e, + 4: -inf, + 8: NaN.
-template <int D, int DT>
+template <int D, int DT, bool SEG>
 __device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, const Run& run, int t0, int t1) {
   constexpr uint32_t E = DT == KVQ_DT_F16 ? 0x7c00u : 0x7f80u;
   constexpr int N = D / 128, U = 16 / N;  // loads in flight
   const int lane = threadIdx.x & 31;
   uint32_t kinds = 0;
 #pragma unroll 1
-  for (int t = max(t0, q_end_of(a.lo, run.u.T)); t < t1; t += U) {
+  for (int t = max(t0, unit_qe<SEG>(a, run.u)); t < t1; t += U) {
     uint2 v[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -1223,25 +1281,34 @@ __device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, const Run& run
   return kinds;
 }
 // Adds them to the unit's output rows r0, r0 + step, .. below r1, which this warp has written.
-template <int D, int DT>
+template <int D, int DT, bool SEG>
 __device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Run& run, int r0, int r1, int step) {
   const Unit& u = run.u;
-  const int lo = a.window ? max(0, u.p_hi - a.window + 1) : 0;
+  const int lo = SEG ? u.from : a.window ? max(0, u.p_hi - a.window + 1) : 0;
   __syncwarp();
   if (r0 >= r1) return;
   // what every row of the unit sees
-  const uint32_t common = window_kinds<D, DT>(a, run, 0, u.sink) | window_kinds<D, DT>(a, run, lo, u.p_lo + 1);
+  const uint32_t common = window_kinds<D, DT, SEG>(a, run, 0, u.sink) | window_kinds<D, DT, SEG>(a, run, lo, u.p_lo + 1);
 #pragma unroll 1
   for (int r = r0; r < r1; r += step) {
-    const int p = u.T - u.n + div_g(a, u.r0 + r), w = a.window ? max(0, p - a.window + 1) : 0;
+    const int p = row_pos<SEG>(a, u, u.r0 + r), w = SEG ? u.from : a.window ? max(0, p - a.window + 1) : 0;
     // and the row alone: the sinks that have left its window, what is before and behind the common tokens
-    const uint32_t kinds = common | window_kinds<D, DT>(a, run, u.sink, min(a.sinks, w)) |
-                           window_kinds<D, DT>(a, run, w, min(lo, p + 1)) | window_kinds<D, DT>(a, run, max(u.p_lo + 1, w), p + 1);
+    const uint32_t kinds = common | window_kinds<D, DT, SEG>(a, run, u.sink, SEG ? 0 : min(a.sinks, w)) |
+                           window_kinds<D, DT, SEG>(a, run, w, min(lo, p + 1)) | window_kinds<D, DT, SEG>(a, run, max(u.p_lo + 1, w), p + 1);
     uint16_t* out = a.out + query_row(a, u, r) + 4 * (threadIdx.x & 31);
 #pragma unroll 1
     for (int e = 0; e < D / 32; ++e) {  // channel e & 3 of chunk e >> 2
       const uint32_t k = kinds >> (12 * (e >> 2) + (e & 3));
       if (!(k & 0x111u)) continue;
+      if (two_parts<SEG>(u)) {
+        float* o = part_of_row(a, u, r) + 128 * (e >> 2) + 4 * (threadIdx.x & 31) + (e & 3);
+        float x = *o;
+        if (k & 1u) x += INFINITY;
+        if (k & 0x10u) x -= INFINITY;
+        if (k & 0x100u) x = NAN;
+        *o = x;
+        continue;
+      }
       uint16_t* o = out + 128 * (e >> 2) + (e & 3);
       float x = in_to_f32(*o, DT);
       if (k & 1u) x += INFINITY;
@@ -1263,10 +1330,22 @@ __device__ __forceinline__ bool soft_sync(uint32_t bar, uint32_t& phase, volatil
 }
 
 // One output row, four channels of a 128-chunk a lane: acc / L, out of the rotated domain.  (s1, s2): the lane's signs.
-template <int D, int DT>
-__device__ __forceinline__ void write_row(const ChunkArgs& a, const Run& run, int r, float (&acc)[D / 128][4], float L, uint32_t s1,
-                                          uint32_t s2) {
+template <int D, int DT, bool SEG>
+__device__ __forceinline__ void write_row(const ChunkArgs& a, const Run& run, int r, float (&acc)[D / 128][4], float m, float L,
+                                          uint32_t s1, uint32_t s2) {
   const int lane = threadIdx.x & 31;
+  if (two_parts<SEG>(run.u)) {
+    float* dst = part_of_row(a, run.u, r);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int c = 0; c < D / 128; ++c) {
+      float v[4] = {acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv};
+      if (a.lo.flags & KVQ_ROTATE_V) rotate_lanes(v, s2, s1);
+      *reinterpret_cast<float4*>(dst + 128 * c + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+    if (lane == 0) dst[D] = log2_sum(m, L);
+    return;
+  }
   uint16_t* dst = a.out + query_row(a, run.u, r);
   const float inv = 1.f / L;
 #pragma unroll
@@ -1292,7 +1371,7 @@ __device__ __forceinline__ bool few_any(int id, bool p) {
 
 // Joins the partial rows of one unit and writes its output rows; all softmax
 // threads.  scratch: 8 rows of D + 4 floats in shared memory.  False once a warp has given up.
-template <int D, int DT, int MODE>
+template <int D, int DT, int MODE, bool SEG>
 __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, const LineStart& line, bool cut, bool fix,
                                           float* scratch, uint32_t soft, uint32_t& syncs, uint32_t* gave_up) {
   using C = ChunkShape<D, MODE>;
@@ -1313,7 +1392,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
     return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
   const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
-  auto write = [&](int r, float (&acc)[N][4], float L) { write_row<D, DT>(a, run, r, acc, L, s1, s2); };
+  auto write = [&](int r, float (&acc)[N][4], float m, float L) { write_row<D, DT, SEG>(a, run, r, acc, m, L, s1, s2); };
   if (PAIRED && parts <= 4) {
     // Many rows of few parts: a lane works out the weights of one row of the
     // warp's 32; then row by row, the next row's loads in flight.
@@ -1362,9 +1441,9 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
         }
       }
       load(r + 1);
-      write(r, acc, __shfl_sync(0xffffffffu, L, r - r0));
+      write(r, acc, SEG ? __shfl_sync(0xffffffffu, M, r - r0) : 0.f, __shfl_sync(0xffffffffu, L, r - r0));
     }
-    if (fix) add_nonfinite<D, DT>(a, run, r0, min(r0 + 32, u.rows), 1);
+    if (fix) add_nonfinite<D, DT, SEG>(a, run, r0, min(r0 + 32, u.rows), 1);
     return true;
   }
   // Few rows: `wpr` warps share a row's parts and join their sums in shared memory.
@@ -1443,9 +1522,9 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
         L += o[D];
       }
     }
-    if (rr < u.rows) write(r, acc, L);
+    if (rr < u.rows) write(r, acc, M, L);
   }
-  if (fix && sub == 0) add_nonfinite<D, DT>(a, run, warp / wpr, u.rows, per);
+  if (fix && sub == 0) add_nonfinite<D, DT, SEG>(a, run, warp / wpr, u.rows, per);
   return true;
 }
 
@@ -1628,7 +1707,7 @@ __device__ __forceinline__ float max_across(float (&x)[16], int lane) {
 }
 
 // The softmax warps' work of FEW: two groups of four warps, 16 rows each.
-template <int DT>
+template <int DT, bool SEG>
 __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool more, uint8_t* smem, uint32_t tmem) {
   constexpr int D = 128, NT = 128, PR = chunk_part_row(D);
   using C = ChunkShape<D, kChunkFew>;
@@ -1676,7 +1755,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
 #pragma unroll
       for (int r = 0; r < 16; ++r) n[r] = r < rows ? -LOWEST : -INFINITY;
       __syncwarp();
-      if (lane < 16) pos[lane] = run.u.T - run.u.n + div_g(a, min(row0 + lane, run.u.rows - 1));
+      if (lane < 16) pos[lane] = row_pos<SEG>(a, run.u, min(row0 + lane, run.u.rows - 1));
       __syncwarp();
 #pragma unroll 1
       for (int j = t0; j < t1; ++j, ++steps) {
@@ -1793,7 +1872,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
     static_assert(sizeof(Run) % 4 == 0 && sizeof(Run) <= 128, "a word a lane");
     if (w == 0) {
       if (lane < (int)sizeof(Run) / 4) reinterpret_cast<int*>(after)[lane] = reinterpret_cast<const int*>(now)[lane];
-      more = warp_run<D, 128>(a, sh.start, *after, 1);
+      more = warp_run<D, 128, SEG>(a, sh.start, *after, 1);
     }
     more = few_any<8>(3, w == 0 && more);
     if (more) {
@@ -1819,7 +1898,10 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
       if (rows > 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) stage[(row0 + i) * D + my] = __uint_as_float(x[i]);
-        if (quad == 0 && lane < 16) sh.few_sum[row0 + lane] = L;
+        if (quad == 0 && lane < 16) {
+          sh.few_sum[row0 + lane] = L;
+          if (SEG) sh.few_part[w][lane] = m;  // (the references of the next run's tiles go there behind its first barrier)
+        }
       }
       (void)few_any<8>(3, false);
       const bool fix = *(volatile uint32_t*)&sh.nonfinite != 0;
@@ -1828,9 +1910,9 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
       for (int r = w; r < run.u.rows; r += 8) {
         const float4 v = *reinterpret_cast<const float4*>(stage + r * D + 4 * lane);
         float acc[1][4] = {{v.x, v.y, v.z, v.w}};
-        write_row<D, DT>(a, run, r, acc, sh.few_sum[r], s1, s2);
+        write_row<D, DT, SEG>(a, run, r, acc, SEG ? sh.few_part[r >> 2 & 4][r & 15] : 0.f, sh.few_sum[r], s1, s2);
       }
-      if (fix) add_nonfinite<D, DT>(a, run, w, run.u.rows, 8);
+      if (fix) add_nonfinite<D, DT, SEG>(a, run, w, run.u.rows, 8);
     } else {
       float* part = a.partials + ((int64_t)blockIdx.x * kChunkSlots + (run.first ? 0 : 1)) * chunk_slot_rows(D) * PR + row0 * PR;
       if (quad == 0 && lane < min(rows, 16)) *reinterpret_cast<float2*>(part + lane * PR + D) = make_float2(m, L);
@@ -1850,7 +1932,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
       if (few_any<8>(3, last)) {
         __threadfence();
         const bool fix = __ldcg(a.nonfinite + tick) != 0;
-        (void)join_unit<D, DT, kChunkFew>(a, run, sh.start, true, fix, stage, 0, syncs, gave_up);
+        (void)join_unit<D, DT, kChunkFew, SEG>(a, run, sh.start, true, fix, stage, 0, syncs, gave_up);
         (void)few_any<8>(3, false);
         if (w == 0 && lane == 0) {
           a.tickets[tick] = 0;
@@ -1866,7 +1948,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
   }
 }
 
-template <int D, int DT, int MODE>
+template <int D, int DT, int MODE, bool SEG>
 __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkArgs a) {
   using C = ChunkShape<D, MODE>;
@@ -1922,7 +2004,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     }
   grid_launch_dependents();
   grid_dependency_wait();
-  find_start<D, RT, C::THREADS>(a, sh);
+  find_start<D, RT, C::THREADS, SEG>(a, sh);
   proxy_fence();
   tc_fence_before();
   __syncthreads();
@@ -1931,7 +2013,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
   Run& run = sh.runs[warp];
   uint32_t* const gave_up = &sh.gave_up;
   const bool k_chan = a.lo.kf.axis == KVQ_AXIS_CHANNEL, v_chan = a.lo.vf.axis == KVQ_AXIS_CHANNEL;
-  bool more = warp_run<D, RT>(a, sh.start, run, 0);
+  bool more = warp_run<D, RT, SEG>(a, sh.start, run, 0);
   // Test mode (kvq_test_force_stall): in every second CTA one of the four roles first waits on a barrier that
   // nothing completes, gives up and leaves; the CTAs between finish their runs.
   if (a.stall_polls && (blockIdx.x & 1) && more) {
@@ -1961,7 +2043,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     uint32_t np0 = 0, np1 = 0;   // steps of each S buffer so far
     uint32_t runs = 0;
     bool ok = true;
-    for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1), ++runs) {
+    for (; more && ok; more = warp_run<D, RT, SEG>(a, sh.start, run, 1), ++runs) {
       const int tiles = uniform(run.t1 - run.t0), steps = PAIRED ? 2 * tiles : tiles;
       {
 #pragma unroll 1
@@ -2048,7 +2130,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= C::LOAD_WARP && a.direct) {
-    if (warp == C::LOAD_WARP) load_direct<D, RT>(a, sh, run, more, raw_at, lane);
+    if (warp == C::LOAD_WARP) load_direct<D, RT, SEG>(a, sh, run, more, raw_at, lane);
   } else if (warp >= C::LOAD_WARP) {
     // ---- staging ------------------------------------------------------------------------
     int w = warp;
@@ -2061,8 +2143,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     uint32_t kt = 0, slot = piece, todo = 3;  // tiles so far; this lane's piece's slot; pieces to ask for
     while (slot >= slots) slot -= slots;
     bool ok = true;
-    for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1)) {
-      const CachePos u{run.u.layer + a.layer0, run.u.b, run.u.h, run.u.T, q_end_of(a.lo, run.u.T), c_end_of(a.lo, run.u.T)};
+    for (; more && ok; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
+      const CachePos u = cache_pos<SEG>(a, run.u);
       ld.unit(a, u);
       const int t1 = run.t1;
       TileTokens tt = tile_tokens<D>(run.u, run.t0);
@@ -2152,7 +2234,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     asm volatile("" : "+r"(kt), "+r"(slot));  // not uniform registers: they live across a call
     while (slot >= slots) slot -= slots;
     bool ok = true;
-    for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1)) {
+    for (; more && ok; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
       int j = run.t0;
 #pragma unroll 1
       while (ok) {
@@ -2165,7 +2247,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         const uint32_t empty_at = smem_addr(which ? &sh.v_empty[0] : &sh.k_empty[0]),
                        filled_at = smem_addr(which ? &sh.v_full[0] : &sh.k_full[0]);
         const uint32_t full_at = smem_addr(&sh.raw_full[piece * kChunkBars]), read_at = smem_addr(&sh.raw_empty[piece * kChunkBars]);
-        const int T = run.u.T, qe = q_end_of(a.lo, T), ce = c_end_of(a.lo, T);
+        const int qe = unit_qe<SEG>(a, run.u), ce = SEG ? 0 : c_end_of(a.lo, run.u.T);
         const bool cold = j < j1 && tile_tokens<D>(run.u, j).t0 + half * (NT / 2) < ce;
         const RunFmt f = run_fmt(a.lo, which, cold);
         // the hot path's format: bits, 16 for asymmetric blocks; 0: none
@@ -2242,7 +2324,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           by_kind(std::false_type{});
         if (!ok || j >= j1) break;
         if (landed) {
-          cold_piece<D, DT>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j);
+          cold_piece<D, DT, SEG>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j);
           proxy_fence();
           __syncwarp();
           if (lane == 0) {
@@ -2257,13 +2339,13 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       }
     }
   } else if constexpr (FEW) {
-    few_rows<DT>(a, sh, more, smem, tmem);
+    few_rows<DT, SEG>(a, sh, more, smem, tmem);
   } else {
     // ---- softmax and outputs -----------------------------------------------------------
     uint32_t ns0 = 0, ns1 = 0, runs = 0, steps_done = 0, syncs = 0;
     asm volatile("" : "+r"(ns0), "+r"(ns1), "+r"(runs), "+r"(steps_done), "+r"(syncs));  // as above
     bool ok = true;
-    for (; more && ok; more = warp_run<D, RT>(a, sh.start, run, 1), ++runs) {
+    for (; more && ok; more = warp_run<D, RT, SEG>(a, sh.start, run, 1), ++runs) {
       int w = warp;  // worked out anew for every run: see the dequantizing warps
       asm volatile("" : "+r"(w));
       const int stream = w >> 2, quad = w & 3;
@@ -2323,7 +2405,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         if (lane == 0) bar_arrive(smem_addr(&sh.q_full[PAIRED ? stream : 0]));
       }
       RowSeen see;
-      see.pos = run.u.T - run.u.n + div_g(a, run.u.r0 + my_row);
+      see.pos = row_pos<SEG>(a, run.u, run.u.r0 + my_row);
       see.win_lo = a.window ? max(0, see.pos - a.window + 1) : 0;
       see.sinks = a.sinks;
       const int steps = (PAIRED ? 2 : 1) * (run.t1 - run.t0), first_tile = run.t0;
@@ -2380,18 +2462,30 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       uint32_t x[16];
       if (direct) {
         const bool rotated = (a.lo.flags & KVQ_ROTATE_V) != 0, fix = *(volatile uint32_t*)&sh.nonfinite != 0;
-        const float inv = 1.f / l, f = rotated ? 1.f : inv;
+        const bool joined = two_parts<SEG>(run.u);
+        const float inv = joined && l == 0.f ? 0.f : 1.f / l, f = rotated ? 1.f : inv;
         if (rotated) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 128) unrotate_columns(a, o_col + c, inv);
         }
         uint16_t* dst = a.out + query_row(a, run.u, mine ? my_row : 0);
+        float* dst32 = joined ? part_of_row(a, run.u, mine ? my_row : 0) : nullptr;
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           tmem_ld16(o_col + c, x);
           const uint32_t signs = rotated ? a.lo.d1[c >> 5 & 3] >> (c & 16) : 0u;
           tmem_wait_ld();
-          if (mine) {
+          if (mine && joined) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              float4 v;
+              v.x = __uint_as_float(x[i] ^ ((signs << (31 - i)) & 0x80000000u)) * f;
+              v.y = __uint_as_float(x[i + 1] ^ ((signs << (30 - i)) & 0x80000000u)) * f;
+              v.z = __uint_as_float(x[i + 2] ^ ((signs << (29 - i)) & 0x80000000u)) * f;
+              v.w = __uint_as_float(x[i + 3] ^ ((signs << (28 - i)) & 0x80000000u)) * f;
+              *reinterpret_cast<float4*>(dst32 + c + i) = v;
+            }
+          } else if (mine) {
             uint32_t p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -2402,7 +2496,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           }
           __syncwarp();
         }
-        if (fix) add_nonfinite<D, DT>(a, run, my_row - lane, min(my_row - lane + 32, run.u.rows), 1);
+        if (mine && joined) dst32[D] = log2_sum(m, l);
+        if (fix) add_nonfinite<D, DT, SEG>(a, run, my_row - lane, min(my_row - lane + 32, run.u.rows), 1);
         __syncwarp();
         tc_fence_before();
       } else {
@@ -2450,7 +2545,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           fix = *(volatile uint32_t*)&sh.nonfinite != 0;
         }
         // (the queries' shared memory is free: the run's products are done)
-        if (join && !(ok = join_unit<D, DT, MODE>(a, run, sh.start, cut, fix, reinterpret_cast<float*>(smem), soft, syncs, gave_up)))
+        if (join && !(ok = join_unit<D, DT, MODE, SEG>(a, run, sh.start, cut, fix, reinterpret_cast<float*>(smem), soft, syncs, gave_up)))
           break;
         if (!(ok = soft_sync(soft, syncs, gave_up))) break;
         if (join && cut && tid == 0) {
@@ -2525,7 +2620,71 @@ __global__ void __launch_bounds__(256) turn_queries_kernel(const __grid_constant
   }
 }
 
-template <int D, int DT, int MODE>
+// The same for segments: a block's eight warps take rows of one sequence.
+template <int D, int DT>
+__global__ void __launch_bounds__(256) turn_segments_kernel(const __grid_constant__ ChunkArgs a) {
+  const int lane = threadIdx.x & 31;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  Unit u;
+  if (!valid_segment(a, a.n_groups + blockIdx.x, u) || u.shared) return;
+  const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
+  const int chunks = a.lo.Hq * (D / 128);
+  const int64_t items = (int64_t)a.n_layers * u.n * ((chunks + 3) / 4);
+#pragma unroll 1
+  for (int64_t i = blockIdx.y * 8 + (threadIdx.x >> 5); i < items; i += gridDim.y * 8) {
+    const int c0 = (int)(i % ((chunks + 3) / 4)) * 4;
+    const int64_t r = i / ((chunks + 3) / 4), row = r / u.n * a.total_q + u.cu + r % u.n;
+    const uint2* src = reinterpret_cast<const uint2*>(a.q + row * a.lo.Hq * D) + lane;
+    uint2* dst = reinterpret_cast<uint2*>(a.out + row * a.lo.Hq * D) + lane;
+    uint2 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c0 + k < chunks) x[k] = __ldg(src + 32 * (c0 + k));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c0 + k < chunks) {
+        float v[4] = {in_to_f32((uint16_t)x[k].x, DT), in_to_f32((uint16_t)(x[k].x >> 16), DT),
+                      in_to_f32((uint16_t)x[k].y, DT), in_to_f32((uint16_t)(x[k].y >> 16), DT)};
+        rotate_lanes(v, s1, s2, a.q_pre);
+        dst[32 * (c0 + k)] = query_pack<DT>(v);
+      }
+  }
+}
+
+// A row's two parts: out = (2^a A + 2^b B) / (2^a + 2^b), a and b their log2-sums.  A warp a row.  What is not finite comes
+// from the sequence's own 16-bit window, where it counts whatever its weight.
+template <int D, int DT>
+__global__ void __launch_bounds__(256) join_segments_kernel(const __grid_constant__ ChunkArgs a) {
+  constexpr int N = D / 128, PR = chunk_part_row(D);
+  const int lane = threadIdx.x & 31;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  Unit u;
+  if (!valid_segment(a, a.n_groups + blockIdx.x, u) || !two_parts<true>(u)) return;
+  const int64_t items = (int64_t)a.n_layers * u.n * a.lo.Hq, all = (int64_t)a.n_layers * a.total_q * a.lo.Hq;
+#pragma unroll 1
+  for (int64_t i = blockIdx.y * 8 + (threadIdx.x >> 5); i < items; i += gridDim.y * 8) {
+    const int64_t layer = i / ((int64_t)u.n * a.lo.Hq), row = i + (layer * (a.total_q - u.n) + u.cu) * a.lo.Hq;
+    const float *p = a.rows + row * PR, *o = p + all * PR;
+    float4 x[N], y[N];
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      x[c] = __ldcg(reinterpret_cast<const float4*>(p) + 32 * c + lane);
+      y[c] = __ldcg(reinterpret_cast<const float4*>(o) + 32 * c + lane);
+    }
+    const float la = __ldcg(p + D), lb = __ldcg(o + D), top = fmaxf(la, lb);
+    const float wa = la == -INFINITY ? 0.f : exp2f(la - top), wb = lb == -INFINITY ? 0.f : exp2f(lb - top), inv = 1.f / (wa + wb);
+    const float fa = wa * inv, fb = wb * inv;
+    auto join = [&](float s, float t) { return isfinite(t) ? fmaf(fa, s, fb * t) : t; };
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      *reinterpret_cast<uint2*>(a.out + row * D + 128 * c + 4 * lane) =
+          make_uint2(pack16<DT>(join(x[c].x, y[c].x), join(x[c].y, y[c].y)), pack16<DT>(join(x[c].z, y[c].z), join(x[c].w, y[c].w)));
+  }
+}
+
+template <int D, int DT, int MODE, bool SEG = false>
 cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   using C = ChunkShape<D, MODE>;
   // all of the SM's shared memory that the tiles leave is staging
@@ -2538,15 +2697,26 @@ cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   // The attribute belongs to the function and the current device, so it is set on every call, and always to the same
   // value: another thread's call, of another format, may come between this and the launch.  Before the queries
   // are turned: a failure here leaves `out` as it was.
-  cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
+  cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<D, DT, MODE, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
   if (e != cudaSuccess) return e;
   if ((a.lo.flags & KVQ_ROTATE_K) && !a.turn_here) {
-    const int64_t rows = (int64_t)a.n_layers * a.total_q;
-    e = launch_dependent(turn_queries_kernel<D, DT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+    if constexpr (SEG) {
+      const int64_t items = (int64_t)a.n_layers * a.max_q * ((a.lo.Hq * (D / 128) + 3) / 4);
+      e = launch_dependent(turn_segments_kernel<D, DT>, dim3(a.lo.B, (unsigned)std::min<int64_t>((items + 7) / 8, 1024)), dim3(256), 0, s, a);
+    } else {
+      const int64_t rows = (int64_t)a.n_layers * a.total_q;
+      e = launch_dependent(turn_queries_kernel<D, DT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+    }
     if (e != cudaSuccess) return e;
     a.q = a.out;
   }
-  return launch_dependent(chunk_attention_kernel<D, DT, MODE>, dim3(grid), dim3(C::THREADS), smem, s, a);
+  e = launch_dependent(chunk_attention_kernel<D, DT, MODE, SEG>, dim3(grid), dim3(C::THREADS), smem, s, a);
+  if constexpr (SEG) {
+    if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)a.n_layers * a.max_q * a.lo.Hq;
+    e = launch_dependent(join_segments_kernel<D, DT>, dim3(a.lo.B, (unsigned)std::min<int64_t>((items + 7) / 8, 1024)), dim3(256), 0, s, a);
+  }
+  return e;
 }
 
 }  // namespace

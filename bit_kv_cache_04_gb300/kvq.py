@@ -123,6 +123,10 @@ def _load():
         "kvq_chunk_workspace_bytes": ([cfgp, P(sz)], ctypes.c_int),
         "kvq_chunk_workspace_init": ([cfgp, vp, sz, vp], ctypes.c_int),
         "kvq_chunk_attention": ([cfgp, cachep, i32, i32, vp, vp, i32, i32, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
+        "kvq_prefix_workspace_bytes": ([cfgp, i32, i64, P(sz)], ctypes.c_int),
+        "kvq_prefix_workspace_init": ([cfgp, i32, i64, vp, sz, vp], ctypes.c_int),
+        "kvq_prefix_plan": ([cfgp, vp, vp, i32, vp, i32, i32, i32, vp, vp, sz, vp], ctypes.c_int),
+        "kvq_prefix_attention": ([cfgp, cachep, i32, i32, i32, vp, i32, i32, i32, vp, vp, sz, vp], ctypes.c_int),
         "kvq_read_device_status": ([vp, P(u32), vp], ctypes.c_int),
         "kvq_clear_device_status": ([vp, vp], ctypes.c_int),
     }
@@ -144,7 +148,8 @@ EXPORTED = ("kvq_version", "kvq_last_error", "kvq_validate_config", "kvq_block_b
             "kvq_test_shrink_bounds", "kvq_rope_plan_init", "kvq_qk_norm_rope", "kvq_pages_workspace_bytes",
             "kvq_pages_init", "kvq_pages_release", "kvq_pages_fork", "kvq_pages_reserve", "kvq_pages_compact",
             "kvq_pages_reorder", "kvq_beam_workspace_bytes", "kvq_beam_workspace_init", "kvq_beam_select",
-            "kvq_chunk_workspace_bytes", "kvq_chunk_workspace_init", "kvq_chunk_attention")
+            "kvq_chunk_workspace_bytes", "kvq_chunk_workspace_init", "kvq_chunk_attention", "kvq_prefix_workspace_bytes",
+            "kvq_prefix_workspace_init", "kvq_prefix_plan", "kvq_prefix_attention")
 
 
 def _check(st: int):
@@ -230,6 +235,12 @@ def kvq_pages_workspace_bytes(cfg: Config) -> int:
 def kvq_beam_workspace_bytes(n_groups: int, beams: int, vocab: int) -> int:
     out = ctypes.c_size_t()
     _check(LIB.kvq_beam_workspace_bytes(n_groups, beams, vocab, ctypes.byref(out)))
+    return out.value
+
+
+def kvq_prefix_workspace_bytes(cfg: Config, n_groups: int, rows: int) -> int:
+    out = ctypes.c_size_t()
+    _check(LIB.kvq_prefix_workspace_bytes(ctypes.byref(_to_c(cfg)), n_groups, rows, ctypes.byref(out)))
     return out.value
 
 
@@ -626,3 +637,62 @@ class BeamSelect:
         _check(LIB.kvq_beam_select(_ptr(logits), kinds[logits.dtype], logits.stride(0), logits.stride(1), groups, beams,
                                    vocab, _ptr(scores), _ptr(done), eos, _ptr(scores_out), _ptr(tokens), _ptr(parents),
                                    _ptr(done_out), _ptr(self.workspace), self.ws_bytes, _stream(stream)))
+
+
+class PrefixAttention:
+    """Attention of groups of sequences that share the pages of a prefix (kvq_prefix_plan, kvq_prefix_attention)
+    and its workspace.  `rows`: the largest n_layers * total_q of a call.  Calls that may run at the same time (also graphs
+    replayed side by side) need an object each."""
+
+    def __init__(self, cache: KVCache, groups: int, rows: int, stream=None):
+        import torch
+
+        cache._check_table()
+        self.cache, self.index, self.groups = cache, cache.index, groups
+        self.ws_bytes = kvq_prefix_workspace_bytes(cache.cfg, groups, rows)
+        _here(self.index)
+        with _on(stream):
+            self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=cache.device)
+        self.planned = None  # total_q, max_q, max_group_q
+        _check(LIB.kvq_prefix_workspace_init(ctypes.byref(cache.c_cfg), groups, rows, _ptr(self.workspace), self.ws_bytes,
+                                             _stream(stream)))
+
+    def plan(self, cu_groups, cu_q, total_q, max_q, max_group_q, seq_lens, stream=None):
+        """What the groups share, found on the device; serves `attention` until the lengths, the table or the rows change."""
+        import torch
+
+        c = self.cache
+        for t, n in ((cu_groups, self.groups + 1), (cu_q, c.cfg.batch + 1), (seq_lens, c.cfg.batch)):
+            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+                raise ValueError("cu_groups [groups + 1], cu_q [batch + 1] and seq_lens [batch] are contiguous int32 tensors")
+        _here(self.index, cu_groups, cu_q, seq_lens)
+        c._check_table()
+        _check(LIB.kvq_prefix_plan(ctypes.byref(c.c_cfg), _ptr(c.block_table), _ptr(cu_groups), self.groups, _ptr(cu_q),
+                                   total_q, max_q, max_group_q, _ptr(seq_lens), _ptr(self.workspace), self.ws_bytes,
+                                   _stream(stream)))
+        self.planned = (total_q, max_q, max_group_q)
+
+    def attention(self, layer0, n_layers, q, out, stream=None):
+        """The planned rows of q [n_layers, total_q, H_q, D] over the cache, into out."""
+        import torch
+
+        if self.planned is None:
+            raise RuntimeError("plan comes before attention")
+        c, cfg = self.cache, self.cache.cfg
+        total_q, max_q, max_group_q = self.planned
+        dt = torch.float16 if cfg.in_dtype == DT_F16 else torch.bfloat16
+        for t in (q, out):
+            if t.dtype != dt or t.shape != (n_layers, total_q, cfg.H_q, cfg.D) or not t.is_contiguous():
+                raise ValueError("q and out are contiguous [n_layers, total_q, H_q, D] tensors of the cache's dtype")
+        _here(self.index, q, out)
+        _check(LIB.kvq_prefix_attention(ctypes.byref(c.c_cfg), ctypes.byref(c.c_cache), layer0, n_layers, self.groups,
+                                        _ptr(q), total_q, max_q, max_group_q, _ptr(out), _ptr(self.workspace),
+                                        self.ws_bytes, _stream(stream)))
+
+    def device_status(self, stream=None) -> int:
+        out = ctypes.c_uint32()
+        _check(LIB.kvq_read_device_status(_ptr(self.workspace), ctypes.byref(out), _stream(stream)))
+        return out.value
+
+    def clear_status(self, stream=None):
+        _check(LIB.kvq_clear_device_status(_ptr(self.workspace), _stream(stream)))
