@@ -48,6 +48,10 @@ int chunk_workspace(const kvq_config* cfg, void* workspace, ChunkArgs* a) {
   return w.grid;
 }
 
+int chunk_form(const kvq_config* cfg, int64_t rows) {
+  return cfg->D != 128 ? kChunkShared : rows <= kFewRows ? kChunkFew : rows > 128 ? kChunkPaired : kChunkShared;
+}
+
 kvq_status chunk_common(const kvq_config* cfg, ChunkArgs* args, int most, int64_t owners, int* form) {
   ChunkArgs& a = *args;
   a.stall_polls = stall_polls();
@@ -62,7 +66,7 @@ kvq_status chunk_common(const kvq_config* cfg, ChunkArgs* args, int most, int64_
       a.turns[i] = (uint64_t)std::ldexp(std::pow((double)cfg->rope_theta, -2.0 * i / cfg->D) / 6.283185307179586476925286766559, 64);
   const int64_t rows = (int64_t)most * a.lo.g;
   if (rows > (int64_t)1 << 28) return fail(KVQ_ERR_UNSUPPORTED, "%d tokens x %d heads", most, a.lo.g);
-  const int mode = cfg->D != 128 ? kChunkShared : rows <= kFewRows ? kChunkFew : rows > 128 ? kChunkPaired : kChunkShared;
+  const int mode = chunk_form(cfg, rows);
   const int tile = chunk_tile(cfg->D), row_tile = mode == kChunkPaired ? 256 : 128;
   // the kernel counts its tiles in 32 bits
   const int64_t units = ((int64_t)a.total_q * a.lo.g / row_tile + owners) * a.n_layers * cfg->H_kv;

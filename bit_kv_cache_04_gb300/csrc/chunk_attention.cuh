@@ -58,15 +58,18 @@ KVQ_HD constexpr int chunk_streams(int D) { return D == 128 ? 2 : 1; }
 KVQ_HD constexpr int chunk_slot_rows(int D) { return 128 * chunk_streams(D); }
 KVQ_HD constexpr int chunk_part_row(int D) { return D + 4; }  // O, m, l, two pads
 
-// Shared prefixes (kvq_prefix_attention, csrc/prefix_attention.cu): the units are those of segments, which a plan on the device
-// writes: a group's new rows over the prefix that its sequences share (all of them see all of it), and every sequence's rows over
-// the tokens behind that.  A row with both has its two parts in `rows`, joined by a kernel of its own.
-struct Segment {
-  int n, T, cu;  // tokens of rows (0: none), tokens of the cache up to its end, first row of q
-  int b;         // the sequence whose pages are read
-  int from;      // first token
-  int shared;    // 1: a prefix
-  int pad[2];
+// Shared prefixes (kvq_prefix_attention, csrc/prefix_attention.cu; SEG in the kernel): a unit is a row tile of a
+// group's new tokens, over the tokens [0, prefix) that all its rows see, read through the pages of sequence `first`, and then over the tiles that
+// each of its sequences has of its own behind that.  A plan on the device writes the units and the list of their own tiles.
+struct SharedUnit {
+  int cu, r0, rows;  // the group's first row of q, the unit's first row (token * g + head) and rows (0: none)
+  int first, prefix;
+  int own, n_own;    // its own tiles in the list
+  int p_lo;          // the smallest position of its rows
+};
+struct OwnTile {
+  int b, t0, T;      // sequence, first token, cached tokens of the sequence
+  int rows;          // the unit's rows that see the tile: first | end << 16
 };
 
 struct ChunkArgs {
@@ -98,9 +101,13 @@ struct ChunkArgs {
   float score_scale;   // log2(e) / sqrt(D), both factors undone
   uint32_t k_one;       // the fp16 number whose last bit counts k_pre, twice
   uint64_t turns[128];  // pre-RoPE keys: turns per position of every pair, 64-bit fractions
-  const Segment* segs;  // shared prefixes: [n_groups] prefixes, then [batch] sequences
-  int n_groups, max_group_q;
-  float* rows;          // [prefix, own][n_layers * total_q][H_q][part row]: output, log2 of the sum of 2^scores
+  // shared prefixes
+  const SharedUnit* units;
+  const OwnTile* own;
+  const int2* where;    // [total_q]: position and sequence of every row's token
+  const int32_t* lens;  // [batch], as planned
+  const int32_t* plan;  // the sizes that it was made for
+  int n_units, unit_cost, own_tiles, most_rows, max_group_q, n_groups;
 };
 
 // Bytes of the workspace, and of its front part that is zero between calls.
@@ -109,6 +116,7 @@ size_t chunk_workspace_bytes(const kvq_config* cfg, size_t* zeroed);
 int chunk_workspace(const kvq_config* cfg, void* workspace, ChunkArgs* a);
 // What follows from the configuration and the rows, at most `most` tokens of each of `owners` (sequences and shared
 // prefixes); the form of the kernel.
+int chunk_form(const kvq_config* cfg, int64_t rows);
 kvq_status chunk_common(const kvq_config* cfg, ChunkArgs* a, int most, int64_t owners, int* form);
 cudaError_t launch_prefix_d128(const ChunkArgs& a, int mode, int grid, cudaStream_t s);
 cudaError_t launch_prefix_few(const ChunkArgs& a, int grid, cudaStream_t s);

@@ -167,8 +167,8 @@ struct Unit {
   int p_lo, p_hi;        // positions of its first and last token
   int lo;                // first token of the window
   int sink;              // tokens [0, sink) visible besides
-  int st, lo_tile, nt;   // sink tiles, first window tile, tiles
-  int seg, from, shared;  // of a segment (SEG): its number, first token, and whether it is a shared prefix
+  int st, lo_tile, nt;   // sink tiles (SEG: prefix tiles), first window tile, tiles
+  int seg, own;          // SEG: the unit's number; its own tiles in the list
 };
 
 // One CTA's run of a unit: tiles [t0, t1) of it.  Each warp keeps its own in shared memory: registers are short.
@@ -198,55 +198,48 @@ __device__ __forceinline__ bool valid_seq(const ChunkArgs& a, int b, int* n, int
   return c0 >= 0 && c1 >= c0 && c1 <= a.total_q && c1 - c0 <= a.max_q && t >= c1 - c0 && t <= a.lo.max_T;
 }
 
-// The owners of rows, in the order of the line: the sequences, or (SEG) the segments.
-template <bool SEG>
-__device__ __forceinline__ int owners(const ChunkArgs& a) {
-  return SEG ? a.n_groups + a.lo.B : a.lo.B;
-}
-template <bool SEG>
-__device__ __forceinline__ int owner(const Unit& u) {
-  return SEG ? u.seg : u.b;
-}
-// Segment i of the plan; what could lead outside the call's tensors is checked again.
-__device__ __forceinline__ bool valid_segment(const ChunkArgs& a, int i, Unit& u) {
-  const int4 x = __ldg(reinterpret_cast<const int4*>(a.segs + i)), y = __ldg(reinterpret_cast<const int4*>(a.segs + i) + 1);
+// (The plan is read past the first-level cache: this grid may begin while the plan is still being written, and what an
+// SM has cached of an earlier one at that time would stay.  With non-coherent loads the roles of a CTA saw different units, now and then.)
+// SEG: unit i of the plan; false where it is none.  What could lead outside the call's tensors is checked again.
+template <int D, int RT>
+__device__ __forceinline__ bool planned_unit(const ChunkArgs& a, int i, Unit& u) {
+  constexpr int NT = chunk_tile(D);
+  const int4 x = __ldcg(reinterpret_cast<const int4*>(a.units + i)), y = __ldcg(reinterpret_cast<const int4*>(a.units + i) + 1);
   u.seg = i;
-  u.n = x.x;
-  u.T = x.y;
-  u.cu = x.z;
+  u.cu = x.x;
+  u.r0 = x.y;
+  u.rows = x.z;
   u.b = x.w;
-  u.from = y.x;
-  u.shared = y.y;
-  const int most = u.shared ? a.max_group_q : a.max_q, seen = u.shared ? u.T : u.T - u.n;
-  return u.n > 0 && u.n <= most && u.cu >= 0 && u.cu <= a.total_q - u.n && u.T > 0 && u.T <= a.lo.max_T && u.b >= 0 &&
-         u.b < a.lo.B && u.from >= 0 && u.from <= seen;
+  u.T = y.x;
+  u.own = y.y;
+  u.p_lo = y.w;
+  u.p_hi = u.T - 1;
+  u.n = u.rt = u.lo = u.sink = u.lo_tile = 0;
+  u.st = u.T / NT;
+  u.nt = u.st + y.z;
+  return u.rows > 0 && u.rows <= min(RT, a.most_rows) && u.r0 >= 0 && u.cu >= 0 && u.cu + div_g(a, u.r0 + u.rows - 1) < a.total_q &&
+         (uint32_t)u.b < (uint32_t)a.lo.B && (uint32_t)u.T <= (uint32_t)a.lo.max_T && u.own >= 0 && y.z >= 0 && u.own <= a.own_tiles - y.z && u.nt > 0;
 }
-// Rows' owner i: whether it takes part, and (SEG == false) whether what it says is in order.
+// Whether the plan is one for the call's sizes: then its units and tiles are where the call looks for them.
+__device__ __forceinline__ bool plan_fits(const ChunkArgs& a) {
+  const int4 x = __ldcg(reinterpret_cast<const int4*>(a.plan));
+  return x.x == a.total_q && x.y == a.max_q && x.z == a.max_group_q && x.w == a.n_groups;
+}
+// Places on the line before a unit's tiles: what a unit costs whatever its length, in tiles (SEG).
 template <bool SEG>
-__device__ __forceinline__ bool load_owner(const ChunkArgs& a, int i, Unit& u) {
-  if constexpr (SEG) return valid_segment(a, i, u);
-  u.b = i;
-  return valid_seq(a, i, &u.n, &u.T, &u.cu);
+__device__ __forceinline__ int unit_cost(const ChunkArgs& a) {
+  return SEG ? a.unit_cost : 0;
 }
-// First token that the packed tiers do not hold; a shared prefix is packed to its end.
-template <bool SEG>
-__device__ __forceinline__ int unit_qe(const ChunkArgs& a, const Unit& u) {
-  return SEG && u.shared ? u.T : q_end_of(a.lo, u.T);
-}
-// Position of query row r (counted from the owner's first): the last token that it sees.
-template <bool SEG>
-__device__ __forceinline__ int row_pos(const ChunkArgs& a, const Unit& u, int r) {
-  return SEG && u.shared ? u.T - 1 : u.T - u.n + div_g(a, r);
-}
-template <int D, int RT, bool SEG>
+
+template <int D, int RT>
 __device__ __forceinline__ void unit_tiles(const ChunkArgs& a, Unit& u) {
   constexpr int NT = chunk_tile(D);
   u.r0 = u.rt * RT;
   u.rows = min(RT, u.n * a.lo.g - u.r0);
-  u.p_lo = row_pos<SEG>(a, u, u.r0);
-  u.p_hi = row_pos<SEG>(a, u, u.r0 + u.rows - 1);
-  u.lo = SEG ? u.from : a.window ? max(0, u.p_lo - a.window + 1) : 0;
-  u.sink = SEG ? 0 : min(a.sinks, u.lo);
+  u.p_lo = u.T - u.n + div_g(a, u.r0);
+  u.p_hi = u.T - u.n + div_g(a, u.r0 + u.rows - 1);
+  u.lo = a.window ? max(0, u.p_lo - a.window + 1) : 0;
+  u.sink = min(a.sinks, u.lo);
   u.lo_tile = u.lo / NT;
   u.st = min((u.sink + NT - 1) / NT, u.lo_tile);
   u.nt = u.st + u.p_hi / NT - u.lo_tile + 1;
@@ -257,19 +250,20 @@ __device__ __forceinline__ int seq_row_tiles(const ChunkArgs& a, int n) {
   return (n * a.lo.g + RT - 1) / RT;
 }
 
-// Tiles of owner b (one layer and kv head): summed by one thread, or by the 32 lanes of a warp.
+// Tiles of sequence b (one layer and kv head): summed by one thread, or by the 32 lanes of a warp.  SEG: of unit b, one thread.
 template <int D, int RT, bool SEG>
 __device__ __forceinline__ int seq_tiles(const ChunkArgs& a, int b, int lane, int lanes, bool* bad) {
   Unit u;
-  if (!load_owner<SEG>(a, b, u)) {
-    if (!SEG) *bad = true;  // (of segments the plan has said so)
+  if constexpr (SEG) return planned_unit<D, RT>(a, b, u) ? u.nt + unit_cost<SEG>(a) : 0;
+  if (!valid_seq(a, b, &u.n, &u.T, &u.cu)) {
+    *bad = true;
     return 0;
   }
   int sum = 0;
   const int nrt = seq_row_tiles<D, RT>(a, u.n);
 #pragma unroll 1
   for (u.rt = lane; u.rt < nrt; u.rt += lanes) {
-    unit_tiles<D, RT, SEG>(a, u);
+    unit_tiles<D, RT>(a, u);
     sum += u.nt;
   }
   return sum;
@@ -280,13 +274,51 @@ template <int D, int RT, bool SEG>
 __device__ __forceinline__ bool step_run(const ChunkArgs& a, const LineStart& s, Run& r, int step) {
   Unit u = r.u;
   int pos, t0;
+  if constexpr (SEG) {
+    const int cost = unit_cost<SEG>(a);
+    if (step == 0) {
+      pos = s.begin;
+      if (pos >= s.end) return false;
+      u.layer = s.lh / a.lo.H;
+      u.h = s.lh % a.lo.H;
+      (void)planned_unit<D, RT>(a, s.b, u);
+      t0 = s.tile - cost;
+      if (t0 < 0) {  // the stretch begins before the unit's tiles
+        pos -= t0;
+        t0 = 0;
+      }
+    } else {
+      pos = r.pos + r.t1 - r.t0;
+      if (pos >= s.end) return false;
+      pos += cost;
+      t0 = 0;
+      int i = u.seg;
+      do {
+        if (++i == a.n_units) {
+          i = 0;
+          if (++u.h == a.lo.H) {
+            u.h = 0;
+            if (++u.layer == a.n_layers) return false;
+          }
+        }
+      } while (!planned_unit<D, RT>(a, i, u));
+    }
+    if (pos >= s.end) return false;
+    r.u = u;
+    r.t0 = t0;
+    r.t1 = min(u.nt, t0 + s.end - pos);
+    r.pos = pos;
+    r.first = step == 0;
+    return true;
+  }
   if (step == 0) {
     pos = s.begin;
     if (pos >= s.end) return false;
     u.layer = s.lh / a.lo.H;
     u.h = s.lh % a.lo.H;
-    (void)load_owner<SEG>(a, s.b, u);
+    u.b = s.b;
     u.rt = s.rt;
+    (void)valid_seq(a, s.b, &u.n, &u.T, &u.cu);
     t0 = s.tile;
   } else {
     pos = r.pos + r.t1 - r.t0;
@@ -296,20 +328,19 @@ __device__ __forceinline__ bool step_run(const ChunkArgs& a, const LineStart& s,
     if (u.rt >= seq_row_tiles<D, RT>(a, u.n)) {  // the next sequence with rows, of the same or the next kv head, layer
       u.rt = 0;
       bool found;
-      int i = owner<SEG>(u);
       do {
-        if (++i == owners<SEG>(a)) {
-          i = 0;
+        if (++u.b == a.lo.B) {
+          u.b = 0;
           if (++u.h == a.lo.H) {
             u.h = 0;
             if (++u.layer == a.n_layers) return false;  // only where lengths changed under the kernel
           }
         }
-        found = load_owner<SEG>(a, i, u) && u.n > 0;
+        found = valid_seq(a, u.b, &u.n, &u.T, &u.cu) && u.n > 0;
       } while (!found);
     }
   }
-  unit_tiles<D, RT, SEG>(a, u);
+  unit_tiles<D, RT>(a, u);
   r.u = u;
   r.t0 = t0;
   r.t1 = min(u.nt, t0 + s.end - pos);
@@ -545,9 +576,42 @@ __device__ __forceinline__ TileTokens tile_tokens(const Unit& u, int j) {
 struct CachePos {
   int layer, b, h, T, qe, ce;
 };
+
+// Tile j of a unit: its tokens, and where they are.
+template <int D, bool SEG>
+__device__ __forceinline__ TileTokens unit_tile(const ChunkArgs& a, const Unit& u, int j, CachePos& at) {
+  constexpr int NT = chunk_tile(D);
+  at.layer = u.layer + a.layer0;
+  at.h = u.h;
+  if constexpr (SEG) {
+    TileTokens r;
+    at.b = u.b;  // of the prefix: packed to its end
+    at.T = at.qe = u.T;
+    at.ce = 0;
+    r.t0 = j * NT;
+    if (j >= u.st) {
+      const int4 x = __ldcg(reinterpret_cast<const int4*>(a.own + u.own + (j - u.st)));
+      at.b = x.x;
+      at.T = x.z;
+      at.qe = q_end_of(a.lo, x.z);
+      r.t0 = x.y;
+    }
+    r.v0 = r.t0;
+    r.v1 = min(r.t0 + NT, at.T);
+    return r;
+  } else {
+    at.b = u.b;
+    at.T = u.T;
+    at.qe = q_end_of(a.lo, u.T);
+    at.ce = c_end_of(a.lo, u.T);
+    return tile_tokens<D>(u, j);
+  }
+}
+// Position of the unit's row r: the last token that it sees.
 template <bool SEG>
-__device__ __forceinline__ CachePos cache_pos(const ChunkArgs& a, const Unit& u) {
-  return CachePos{u.layer + a.layer0, u.b, u.h, u.T, unit_qe<SEG>(a, u), SEG ? 0 : c_end_of(a.lo, u.T)};
+__device__ __forceinline__ int row_pos(const ChunkArgs& a, const Unit& u, int r) {
+  const int tok = div_g(a, u.r0 + r);
+  return SEG ? __ldcg(&a.where[u.cu + tok].x) : u.T - u.n + tok;
 }
 
 // Where the runs of 32 values of a tensor's tile sit.  Rows of the tile in
@@ -1090,9 +1154,9 @@ template <int D, int RT, bool SEG>
 __device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Run& run, bool more, uint32_t raw_at, int lane) {
   uint32_t kt = 0, slot = 0, n = 0;
   for (; more; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
-    const CachePos u = cache_pos<SEG>(a, run.u);
     for (int j = run.t0; j < run.t1; ++j, ++kt) {
-      const TileTokens tt = tile_tokens<D>(run.u, j);
+      CachePos u;
+      const TileTokens tt = unit_tile<D, SEG>(a, run.u, j, u);
       for (int piece = 0; piece < 4; ++piece, ++n) {
         const int which = piece >> 1, a0 = tt.t0 + (piece & 1) * (chunk_tile(D) / 2), row = which ? a.lo.vf.row : a.lo.kf.row;
         if (n >= (uint32_t)a.slots) {  // the slot's last piece must have been read
@@ -1131,8 +1195,8 @@ __device__ __forceinline__ void cold_piece(const ChunkArgs& a, ChunkShared& sh, 
   constexpr int NT = chunk_tile(D);
   const int piece = dw >> 1, which = dw >> 2, half = piece & 1, part = dw & 1, lane = threadIdx.x & 31;
   const bool per_channel = (which ? a.lo.vf.axis : a.lo.kf.axis) == KVQ_AXIS_CHANNEL;
-  const CachePos u = cache_pos<SEG>(a, run.u);
-  const TileTokens tt = tile_tokens<D>(run.u, j);
+  CachePos u;
+  const TileTokens tt = unit_tile<D, SEG>(a, run.u, j, u);
   const int a0 = tt.t0 + half * (NT / 2);
   const uint32_t staged = raw_at + slot * a.slot_bytes, bad = sh.bad_pages[piece * kChunkBars + (kt & (kChunkBars - 1))];
   const uint32_t dst = tiles_at + (kt & 1) * (uint32_t)NT * D * 2;
@@ -1168,16 +1232,18 @@ template <int D, int RT, int THREADS, bool SEG>
 __device__ __forceinline__ void find_start(const ChunkArgs& a, ChunkShared& sh) {
   const int lane = a.by_warp ? threadIdx.x & 31 : 0, lanes = a.by_warp ? 32 : 1;
   const int group = a.by_warp ? threadIdx.x >> 5 : threadIdx.x, groups = a.by_warp ? THREADS / 32 : THREADS;
+  const int owners = SEG ? (plan_fits(a) ? a.n_units : 0) : a.lo.B;
   bool bad = false;
   int line = 0, mine = 0, at = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < owners<SEG>(a); b0 += groups) {
+  for (int b0 = 0; b0 < owners; b0 += groups) {
     const int b = b0 + group;
-    mine = b < owners<SEG>(a) ? seq_tiles<D, RT, SEG>(a, b, lane, lanes, &bad) : 0;
+    mine = b < owners ? seq_tiles<D, RT, SEG>(a, b, lane, lanes, &bad) : 0;
     int sum;
     at = line + block_sum<THREADS>(mine, sh.scan, &sum);
     line += sum;
   }
+  if (SEG && blockIdx.x == 0 && threadIdx.x == 0 && !owners) atomicOr(a.status, KVQ_DEV_SEQ);
   if (!SEG && blockIdx.x == 0) {
     if (threadIdx.x == 0 && __ldg(a.cu_q) != 0) bad = true;
     if (bad) atomicOr(a.status, KVQ_DEV_LENGTH);
@@ -1195,11 +1261,11 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, ChunkShared& sh) 
   const int lh = begin / line, x = begin - lh * line;  // place within one (layer, kv head)
   int base = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < owners<SEG>(a) && base <= x; b0 += groups) {
+  for (int b0 = 0; b0 < owners && base <= x; b0 += groups) {
     const int b = b0 + group;
-    if (owners<SEG>(a) > groups) {  // else the sums of the pass above are still there
+    if (owners > groups) {  // else the sums of the pass above are still there
       bool ignore = false;
-      mine = b < owners<SEG>(a) ? seq_tiles<D, RT, SEG>(a, b, lane, lanes, &ignore) : 0;
+      mine = b < owners ? seq_tiles<D, RT, SEG>(a, b, lane, lanes, &ignore) : 0;
       int sum;
       at = base + block_sum<THREADS>(mine, sh.scan, &sum);
       base += sum;
@@ -1207,15 +1273,19 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, ChunkShared& sh) 
       base = line;
     }
     const int tiles = a.by_warp ? __reduce_add_sync(0xffffffffu, mine) : mine;  // the sequence's, seen from lane 0
-    if (lane == 0 && b < owners<SEG>(a) && x >= at && x < at + tiles) {
+    if (lane == 0 && b < owners && x >= at && x < at + tiles) {
       Unit u;
-      (void)load_owner<SEG>(a, b, u);
       int left = x - at;
+      if constexpr (SEG) {
+        u.rt = 0;
+      } else {
+        (void)valid_seq(a, b, &u.n, &u.T, &u.cu);
 #pragma unroll 1
-      for (u.rt = 0;; ++u.rt) {
-        unit_tiles<D, RT, SEG>(a, u);
-        if (left < u.nt) break;
-        left -= u.nt;
+        for (u.rt = 0;; ++u.rt) {
+          unit_tiles<D, RT>(a, u);
+          if (left < u.nt) break;
+          left -= u.nt;
+        }
       }
       sh.start.lh = lh;
       sh.start.b = b;
@@ -1231,18 +1301,6 @@ __device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, 
   return (((int64_t)u.layer * a.total_q + u.cu + tok) * a.lo.Hq + u.h * a.lo.g + (row - tok * a.lo.g)) * a.lo.D;
 }
 
-// SEG: whether the unit's rows are one of two parts each, and where row r's part starts.
-template <bool SEG>
-__device__ __forceinline__ bool two_parts(const Unit& u) {
-  return SEG && (u.shared || u.from > 0);
-}
-__device__ __forceinline__ float* part_of_row(const ChunkArgs& a, const Unit& u, int r) {
-  const int64_t row = query_row(a, u, r) / a.lo.D, all = (int64_t)a.n_layers * a.total_q * a.lo.Hq;
-  return a.rows + ((u.shared ? 0 : all) + row) * chunk_part_row(a.lo.D);
-}
-// log2 of a row's sum of 2^scores, L times 2^m; no token seen or none above -inf: -inf
-__device__ __forceinline__ float log2_sum(float m, float L) { return L == 0.f ? -INFINITY : m + log2f(L); }
-
 // V's values that are not finite were left out of the products: every row
 // that sees such a window token gets them afterwards (an infinity stays one
 // under any positive weight, a NaN stays NaN).  What a row gets depends on the kinds that it sees in a channel,
@@ -1252,19 +1310,19 @@ __device__ __forceinline__ float log2_sum(float m, float L) { return L == 0.f ? 
 
 // Kinds among window tokens [t0, t1) of this lane's channels (4 lane .. of every 128-chunk): of chunk c, bits
 // 12 c + e: +inf in channel e, + 4: -inf, + 8: NaN.
-template <int D, int DT, bool SEG>
-__device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, const Run& run, int t0, int t1) {
+template <int D, int DT>
+__device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, int layer, int b, int h, int T, int t0, int t1) {
   constexpr uint32_t E = DT == KVQ_DT_F16 ? 0x7c00u : 0x7f80u;
   constexpr int N = D / 128, U = 16 / N;  // loads in flight
   const int lane = threadIdx.x & 31;
   uint32_t kinds = 0;
 #pragma unroll 1
-  for (int t = max(t0, unit_qe<SEG>(a, run.u)); t < t1; t += U) {
+  for (int t = max(t0, q_end_of(a.lo, T)); t < t1; t += U) {
     uint2 v[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint2* p = reinterpret_cast<const uint2*>(
-                           resid_row(a.lo, a.cp, 1, run.u.layer + a.layer0, run.u.b, run.u.h, min(t + u, t1 - 1))) + lane;
+                           resid_row(a.lo, a.cp, 1, layer + a.layer0, b, h, min(t + u, t1 - 1))) + lane;
 #pragma unroll
       for (int c = 0; c < N; ++c) v[u][c] = p[32 * c];
     }
@@ -1284,31 +1342,37 @@ __device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, const Run& run
 template <int D, int DT, bool SEG>
 __device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Run& run, int r0, int r1, int step) {
   const Unit& u = run.u;
-  const int lo = SEG ? u.from : a.window ? max(0, u.p_hi - a.window + 1) : 0;
+  const int lo = a.window ? max(0, u.p_hi - a.window + 1) : 0;
   __syncwarp();
   if (r0 >= r1) return;
-  // what every row of the unit sees
-  const uint32_t common = window_kinds<D, DT, SEG>(a, run, 0, u.sink) | window_kinds<D, DT, SEG>(a, run, lo, u.p_lo + 1);
+  // what every row of the unit sees (SEG: every row of one of its sequences)
+  uint32_t common = SEG ? 0 : window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, 0, u.sink) | window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, lo, u.p_lo + 1);
+  int seq = -1, from = 0, T = 0;  // SEG: the sequence of `common`, its first row's position, its length
 #pragma unroll 1
   for (int r = r0; r < r1; r += step) {
-    const int p = row_pos<SEG>(a, u, u.r0 + r), w = SEG ? u.from : a.window ? max(0, p - a.window + 1) : 0;
-    // and the row alone: the sinks that have left its window, what is before and behind the common tokens
-    const uint32_t kinds = common | window_kinds<D, DT, SEG>(a, run, u.sink, SEG ? 0 : min(a.sinks, w)) |
-                           window_kinds<D, DT, SEG>(a, run, w, min(lo, p + 1)) | window_kinds<D, DT, SEG>(a, run, max(u.p_lo + 1, w), p + 1);
+    const int p = row_pos<SEG>(a, u, r);
+    uint32_t kinds;
+    if constexpr (SEG) {
+      const int b = __ldcg(&a.where[u.cu + div_g(a, u.r0 + r)].y);
+      if (b != seq) {
+        seq = b;
+        from = p;
+        T = __ldcg(a.lens + b);
+        common = window_kinds<D, DT>(a, u.layer, b, u.h, T, 0, p + 1);
+      }
+      kinds = common | window_kinds<D, DT>(a, u.layer, b, u.h, T, from + 1, p + 1);
+    } else {
+      const int w = a.window ? max(0, p - a.window + 1) : 0;
+      // and the row alone: the sinks that have left its window, what is before and behind the common tokens
+      kinds = common | window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, u.sink, min(a.sinks, w)) |
+              window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, w, min(lo, p + 1)) |
+              window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, max(u.p_lo + 1, w), p + 1);
+    }
     uint16_t* out = a.out + query_row(a, u, r) + 4 * (threadIdx.x & 31);
 #pragma unroll 1
     for (int e = 0; e < D / 32; ++e) {  // channel e & 3 of chunk e >> 2
       const uint32_t k = kinds >> (12 * (e >> 2) + (e & 3));
       if (!(k & 0x111u)) continue;
-      if (two_parts<SEG>(u)) {
-        float* o = part_of_row(a, u, r) + 128 * (e >> 2) + 4 * (threadIdx.x & 31) + (e & 3);
-        float x = *o;
-        if (k & 1u) x += INFINITY;
-        if (k & 0x10u) x -= INFINITY;
-        if (k & 0x100u) x = NAN;
-        *o = x;
-        continue;
-      }
       uint16_t* o = out + 128 * (e >> 2) + (e & 3);
       float x = in_to_f32(*o, DT);
       if (k & 1u) x += INFINITY;
@@ -1330,22 +1394,10 @@ __device__ __forceinline__ bool soft_sync(uint32_t bar, uint32_t& phase, volatil
 }
 
 // One output row, four channels of a 128-chunk a lane: acc / L, out of the rotated domain.  (s1, s2): the lane's signs.
-template <int D, int DT, bool SEG>
-__device__ __forceinline__ void write_row(const ChunkArgs& a, const Run& run, int r, float (&acc)[D / 128][4], float m, float L,
-                                          uint32_t s1, uint32_t s2) {
+template <int D, int DT>
+__device__ __forceinline__ void write_row(const ChunkArgs& a, const Run& run, int r, float (&acc)[D / 128][4], float L, uint32_t s1,
+                                          uint32_t s2) {
   const int lane = threadIdx.x & 31;
-  if (two_parts<SEG>(run.u)) {
-    float* dst = part_of_row(a, run.u, r);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-    for (int c = 0; c < D / 128; ++c) {
-      float v[4] = {acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv};
-      if (a.lo.flags & KVQ_ROTATE_V) rotate_lanes(v, s2, s1);
-      *reinterpret_cast<float4*>(dst + 128 * c + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-    if (lane == 0) dst[D] = log2_sum(m, L);
-    return;
-  }
   uint16_t* dst = a.out + query_row(a, run.u, r);
   const float inv = 1.f / L;
 #pragma unroll
@@ -1383,7 +1435,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
   const int unit_pos = run.pos - run.t0;
   const int c0 = cut ? unit_pos / line.per_cta : blockIdx.x;
   const int c1 = cut ? (unit_pos + u.nt - 1) / line.per_cta : blockIdx.x;
-  const int slot0 = !cut ? 2 : unit_pos == c0 * line.per_cta ? 0 : 1;  // of the first CTA; the others' is 0
+  const int slot0 = !cut ? 2 : unit_pos - unit_cost<SEG>(a) <= c0 * line.per_cta ? 0 : 1;  // of the first CTA; the others' is 0
   constexpr bool ONE = PAIRED || C::FEW;
   constexpr int copies = ONE ? 1 : C::STREAMS, copies_log = copies - 1;  // partial rows of one query row in one slot
   const int parts = (c1 - c0 + 1) * copies;
@@ -1392,7 +1444,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
     return a.partials + ((int64_t)(c0 + c) * kChunkSlots + (c ? 0 : slot0)) * SLOT + row * PR;
   };
   const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
-  auto write = [&](int r, float (&acc)[N][4], float m, float L) { write_row<D, DT, SEG>(a, run, r, acc, m, L, s1, s2); };
+  auto write = [&](int r, float (&acc)[N][4], float L) { write_row<D, DT>(a, run, r, acc, L, s1, s2); };
   if (PAIRED && parts <= 4) {
     // Many rows of few parts: a lane works out the weights of one row of the
     // warp's 32; then row by row, the next row's loads in flight.
@@ -1441,7 +1493,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
         }
       }
       load(r + 1);
-      write(r, acc, SEG ? __shfl_sync(0xffffffffu, M, r - r0) : 0.f, __shfl_sync(0xffffffffu, L, r - r0));
+      write(r, acc, __shfl_sync(0xffffffffu, L, r - r0));
     }
     if (fix) add_nonfinite<D, DT, SEG>(a, run, r0, min(r0 + 32, u.rows), 1);
     return true;
@@ -1522,7 +1574,7 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
         L += o[D];
       }
     }
-    if (rr < u.rows) write(r, acc, M, L);
+    if (rr < u.rows) write(r, acc, L);
   }
   if (fix && sub == 0) add_nonfinite<D, DT, SEG>(a, run, warp / wpr, u.rows, per);
   return true;
@@ -1759,12 +1811,23 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
       __syncwarp();
 #pragma unroll 1
       for (int j = t0; j < t1; ++j, ++steps) {
-        const int b = (j - t0) & 1, tile0 = (j < st ? j : j + skip) * NT;
+        const int b = (j - t0) & 1;
+        int tile0 = (j < st ? j : j + skip) * NT, r_lo = 0, r_hi = 0;  // SEG: rows of the group that see an own tile
+        bool masked = tile0 + NT - 1 > p_lo || (a.window && tile0 <= p_hi - a.window && tile0 + NT > a.sinks);
+        if constexpr (SEG) {
+          masked = false;  // of the prefix every row sees every token
+          if (j >= st) {
+            const int4 x = __ldcg(reinterpret_cast<const int4*>(a.own + run.u.own + (j - st)));
+            tile0 = x.y;
+            r_lo = (x.w & 0xffff) - row0;
+            r_hi = (x.w >> 16) - row0;
+            masked = tile0 + NT - 1 > p_lo || r_lo > 0 || r_hi < rows;
+          }
+        }
         const uint32_t s_col = lane_base + C::S_COL + b * kFewRows;
         const bool here = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
         ns0 += b ^ 1;
         ns1 += b;
-        const bool masked = tile0 + NT - 1 > p_lo || (a.window && tile0 <= p_hi - a.window && tile0 + NT > a.sinks);
         // -inf where this thread's token is out of a row's view
         auto hide = [&](float (&x)[16]) {
           const int t = tile0 + my, window = a.window ? a.window : 1 << 30;
@@ -1772,7 +1835,11 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int p = pos[i];
-            if (t > p || (t <= p - window && !sink)) x[i] = -INFINITY;
+            if constexpr (SEG) {
+              if (t > p || i < r_lo || i >= r_hi) x[i] = -INFINITY;
+            } else {
+              if (t > p || (t <= p - window && !sink)) x[i] = -INFINITY;
+            }
           }
         };
         // log2 P
@@ -1898,10 +1965,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
       if (rows > 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) stage[(row0 + i) * D + my] = __uint_as_float(x[i]);
-        if (quad == 0 && lane < 16) {
-          sh.few_sum[row0 + lane] = L;
-          if (SEG) sh.few_part[w][lane] = m;  // (the references of the next run's tiles go there behind its first barrier)
-        }
+        if (quad == 0 && lane < 16) sh.few_sum[row0 + lane] = L;
       }
       (void)few_any<8>(3, false);
       const bool fix = *(volatile uint32_t*)&sh.nonfinite != 0;
@@ -1910,7 +1974,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
       for (int r = w; r < run.u.rows; r += 8) {
         const float4 v = *reinterpret_cast<const float4*>(stage + r * D + 4 * lane);
         float acc[1][4] = {{v.x, v.y, v.z, v.w}};
-        write_row<D, DT, SEG>(a, run, r, acc, SEG ? sh.few_part[r >> 2 & 4][r & 15] : 0.f, sh.few_sum[r], s1, s2);
+        write_row<D, DT>(a, run, r, acc, sh.few_sum[r], s1, s2);
       }
       if (fix) add_nonfinite<D, DT, SEG>(a, run, w, run.u.rows, 8);
     } else {
@@ -1922,7 +1986,7 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
       __threadfence();
       (void)few_any<8>(3, false);
       const int unit_pos = run.pos - t0, c0 = unit_pos / sh.start.per_cta;  // the unit's ticket: as below
-      const int tick = c0 * kChunkTickets + (unit_pos == c0 * sh.start.per_cta ? 0 : 1);
+      const int tick = c0 * kChunkTickets + (unit_pos - unit_cost<SEG>(a) <= c0 * sh.start.per_cta ? 0 : 1);
       bool last = false;
       if (w == 0 && lane == 0) {
         if (*(volatile uint32_t*)&sh.nonfinite) atomicOr(a.nonfinite + tick, 1u);
@@ -2144,16 +2208,17 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     while (slot >= slots) slot -= slots;
     bool ok = true;
     for (; more && ok; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
-      const CachePos u = cache_pos<SEG>(a, run.u);
+      CachePos u;
+      TileTokens tt = unit_tile<D, SEG>(a, run.u, run.t0, u);
       ld.unit(a, u);
       const int t1 = run.t1;
-      TileTokens tt = tile_tokens<D>(run.u, run.t0);
       int pid = ld.page_id(a, u, tt.t0, ld.ln);
 #pragma unroll 1
       for (int j = run.t0; j < t1; ++j, ++kt) {
         // the next tile's page ids load while this one waits for slots
-        const TileTokens next = tile_tokens<D>(run.u, min(j + 1, t1 - 1));
-        const int next_pid = ld.page_id(a, u, next.t0, ld.ln);
+        CachePos next_u = u;
+        const TileTokens next = SEG ? unit_tile<D, SEG>(a, run.u, min(j + 1, t1 - 1), next_u) : tile_tokens<D>(run.u, min(j + 1, t1 - 1));
+        const int next_pid = ld.page_id(a, next_u, next.t0, ld.ln);
         // A lane works out a copy and notes it; one lane then asks for all of a piece's.  (Operands passed by
         // shuffles took 200 to 500 cycles a copy, queued behind the dequantizing warps' shared-memory
         // traffic; an odd chunk of 256-channel heads took 824 us so, 773 us with the notes.)
@@ -2212,6 +2277,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         if (!ok) break;
         pid = next_pid;
         tt = next;
+        if (SEG) u = next_u;
         slot += 4;
         while (slot >= slots) slot -= slots;
       }
@@ -2247,8 +2313,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         const uint32_t empty_at = smem_addr(which ? &sh.v_empty[0] : &sh.k_empty[0]),
                        filled_at = smem_addr(which ? &sh.v_full[0] : &sh.k_full[0]);
         const uint32_t full_at = smem_addr(&sh.raw_full[piece * kChunkBars]), read_at = smem_addr(&sh.raw_empty[piece * kChunkBars]);
-        const int qe = unit_qe<SEG>(a, run.u), ce = SEG ? 0 : c_end_of(a.lo, run.u.T);
-        const bool cold = j < j1 && tile_tokens<D>(run.u, j).t0 + half * (NT / 2) < ce;
+        const int T = run.u.T, q_last = SEG ? T : q_end_of(a.lo, T), ce = SEG ? 0 : c_end_of(a.lo, T);
+        const bool cold = !SEG && j < j1 && tile_tokens<D>(run.u, j).t0 + half * (NT / 2) < ce;
         const RunFmt f = run_fmt(a.lo, which, cold);
         // the hot path's format: bits, 16 for asymmetric blocks; 0: none
         const int kind = (which == 0 && (a.lo.flags & KVQ_K_PRE_ROPE)) || f.codebook ? 0 : f.bits + (f.zp ? 16 : 0);
@@ -2266,7 +2332,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         }
         bool landed = false;
         // tiles behind the window's first lie in one format and in view up to this token (to whole 32-token subtiles)
-        const int st0 = run.u.st, safe = min(cold ? ce : qe, run.u.p_hi + 32);
+        const int st0 = run.u.st, safe = min(cold ? ce : q_last, run.u.p_hi + 32);
         auto stretch = [&](auto fill) {
         int a1 = 1 << 30;  // the piece's end
 #pragma unroll 1
@@ -2274,9 +2340,10 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           const uint32_t st = kt & 1, bar = kt & (kChunkBars - 1);
           bool plain = true;
           a1 += NT;
-          if (j <= st0 || a1 > safe) {
-            const TileTokens tt = tile_tokens<D>(run.u, j);
-            const int a0 = tt.t0 + half * (NT / 2);
+          if (SEG ? j >= st0 || a1 > safe : j <= st0 || a1 > safe) {
+            CachePos at;
+            const TileTokens tt = SEG ? unit_tile<D, SEG>(a, run.u, j, at) : tile_tokens<D>(run.u, j);
+            const int a0 = tt.t0 + half * (NT / 2), qe = SEG ? at.qe : q_last;
             a1 = a0 + NT / 2;
             if ((a0 < ce) != cold) break;  // the other tier's format
             // of one format, wholly in view (to whole 32-token subtiles) and in range: the common case
@@ -2404,10 +2471,10 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(smem_addr(&sh.q_full[PAIRED ? stream : 0]));
       }
-      RowSeen see;
-      see.pos = row_pos<SEG>(a, run.u, run.u.r0 + my_row);
-      see.win_lo = a.window ? max(0, see.pos - a.window + 1) : 0;
-      see.sinks = a.sinks;
+      RowSeen row_sees;
+      row_sees.pos = row_pos<SEG>(a, run.u, SEG ? min(my_row, run.u.rows - 1) : my_row);
+      row_sees.win_lo = !SEG && a.window ? max(0, row_sees.pos - a.window + 1) : 0;
+      row_sees.sinks = a.sinks;
       const int steps = (PAIRED ? 2 : 1) * (run.t1 - run.t0), first_tile = run.t0;
       const int st = run.u.st, skip = run.u.lo_tile - st, p_lo = run.u.p_lo, p_hi = run.u.p_hi;
       float m = -INFINITY, l = 0.f;
@@ -2416,8 +2483,19 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       for (int s = C::STREAMS == 2 ? stream : 0; s < steps; s += C::STREAMS) {
         const int b = s & 1;
         const int j = first_tile + (PAIRED ? s >> 1 : s);
-        const int t0 = (j < st ? j : j + skip) * NT;
-        const bool masked = t0 + NT - 1 > p_lo || (a.window && t0 <= p_hi - a.window && t0 + NT > a.sinks);
+        int t0 = (j < st ? j : j + skip) * NT;
+        bool masked = t0 + NT - 1 > p_lo || (a.window && t0 <= p_hi - a.window && t0 + NT > a.sinks);
+        RowSeen see = row_sees;
+        if constexpr (SEG) {
+          masked = false;  // of the prefix every row sees every token
+          if (j >= st) {
+            const int4 x = __ldcg(reinterpret_cast<const int4*>(a.own + run.u.own + (j - st)));
+            const int r_lo = x.w & 0xffff, r_hi = x.w >> 16;
+            t0 = x.y;
+            masked = t0 + NT - 1 > p_lo || r_lo > 0 || r_hi < run.u.rows;
+            if (my_row < r_lo || my_row >= r_hi) see.pos = -1;
+          }
+        }
         const uint32_t s_col = lane_base + C::S_COL + b * NT;
         ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
         if (!ok) break;
@@ -2462,30 +2540,18 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       uint32_t x[16];
       if (direct) {
         const bool rotated = (a.lo.flags & KVQ_ROTATE_V) != 0, fix = *(volatile uint32_t*)&sh.nonfinite != 0;
-        const bool joined = two_parts<SEG>(run.u);
-        const float inv = joined && l == 0.f ? 0.f : 1.f / l, f = rotated ? 1.f : inv;
+        const float inv = 1.f / l, f = rotated ? 1.f : inv;
         if (rotated) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 128) unrotate_columns(a, o_col + c, inv);
         }
         uint16_t* dst = a.out + query_row(a, run.u, mine ? my_row : 0);
-        float* dst32 = joined ? part_of_row(a, run.u, mine ? my_row : 0) : nullptr;
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           tmem_ld16(o_col + c, x);
           const uint32_t signs = rotated ? a.lo.d1[c >> 5 & 3] >> (c & 16) : 0u;
           tmem_wait_ld();
-          if (mine && joined) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              float4 v;
-              v.x = __uint_as_float(x[i] ^ ((signs << (31 - i)) & 0x80000000u)) * f;
-              v.y = __uint_as_float(x[i + 1] ^ ((signs << (30 - i)) & 0x80000000u)) * f;
-              v.z = __uint_as_float(x[i + 2] ^ ((signs << (29 - i)) & 0x80000000u)) * f;
-              v.w = __uint_as_float(x[i + 3] ^ ((signs << (28 - i)) & 0x80000000u)) * f;
-              *reinterpret_cast<float4*>(dst32 + c + i) = v;
-            }
-          } else if (mine) {
+          if (mine) {
             uint32_t p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -2496,7 +2562,6 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           }
           __syncwarp();
         }
-        if (mine && joined) dst32[D] = log2_sum(m, l);
         if (fix) add_nonfinite<D, DT, SEG>(a, run, my_row - lane, min(my_row - lane + 32, run.u.rows), 1);
         __syncwarp();
         tc_fence_before();
@@ -2525,7 +2590,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         // a unit's ticket belongs to its first CTA: entry 0 when the unit
         // starts with that CTA's stretch, else 1
         const int unit_pos = run.pos - run.t0, c0 = unit_pos / sh.start.per_cta;
-        const int tick = c0 * kChunkTickets + (unit_pos == c0 * sh.start.per_cta ? 0 : 1);
+        const int tick = c0 * kChunkTickets + (unit_pos - unit_cost<SEG>(a) <= c0 * sh.start.per_cta ? 0 : 1);
         if (cut) __threadfence();
         if (!(ok = soft_sync(soft, syncs, gave_up))) break;
         if (cut) {
@@ -2620,21 +2685,22 @@ __global__ void __launch_bounds__(256) turn_queries_kernel(const __grid_constant
   }
 }
 
-// The same for segments: a block's eight warps take rows of one sequence.
-template <int D, int DT>
-__global__ void __launch_bounds__(256) turn_segments_kernel(const __grid_constant__ ChunkArgs a) {
+// The same for planned units: a block a unit, its tokens' heads four 128-chunks a warp at a time.  (A token of two units is turned twice.)
+template <int D, int DT, int RT>
+__global__ void __launch_bounds__(256) turn_units_kernel(const __grid_constant__ ChunkArgs a) {
   const int lane = threadIdx.x & 31;
   grid_launch_dependents();
   grid_dependency_wait();
   Unit u;
-  if (!valid_segment(a, a.n_groups + blockIdx.x, u) || u.shared) return;
+  if (!plan_fits(a) || !planned_unit<D, RT>(a, blockIdx.x, u)) return;
   const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
-  const int chunks = a.lo.Hq * (D / 128);
-  const int64_t items = (int64_t)a.n_layers * u.n * ((chunks + 3) / 4);
+  const int chunks = a.lo.Hq * (D / 128), per = (chunks + 3) / 4;
+  const int tok0 = div_g(a, u.r0), n = div_g(a, u.r0 + u.rows - 1) - tok0 + 1;
+  const int64_t items = (int64_t)a.n_layers * n * per;
 #pragma unroll 1
   for (int64_t i = blockIdx.y * 8 + (threadIdx.x >> 5); i < items; i += gridDim.y * 8) {
-    const int c0 = (int)(i % ((chunks + 3) / 4)) * 4;
-    const int64_t r = i / ((chunks + 3) / 4), row = r / u.n * a.total_q + u.cu + r % u.n;
+    const int c0 = (int)(i % per) * 4;
+    const int64_t r = i / per, row = r / n * a.total_q + u.cu + tok0 + r % n;
     const uint2* src = reinterpret_cast<const uint2*>(a.q + row * a.lo.Hq * D) + lane;
     uint2* dst = reinterpret_cast<uint2*>(a.out + row * a.lo.Hq * D) + lane;
     uint2 x[4];
@@ -2649,38 +2715,6 @@ __global__ void __launch_bounds__(256) turn_segments_kernel(const __grid_constan
         rotate_lanes(v, s1, s2, a.q_pre);
         dst[32 * (c0 + k)] = query_pack<DT>(v);
       }
-  }
-}
-
-// A row's two parts: out = (2^a A + 2^b B) / (2^a + 2^b), a and b their log2-sums.  A warp a row.  What is not finite comes
-// from the sequence's own 16-bit window, where it counts whatever its weight.
-template <int D, int DT>
-__global__ void __launch_bounds__(256) join_segments_kernel(const __grid_constant__ ChunkArgs a) {
-  constexpr int N = D / 128, PR = chunk_part_row(D);
-  const int lane = threadIdx.x & 31;
-  grid_launch_dependents();
-  grid_dependency_wait();
-  Unit u;
-  if (!valid_segment(a, a.n_groups + blockIdx.x, u) || !two_parts<true>(u)) return;
-  const int64_t items = (int64_t)a.n_layers * u.n * a.lo.Hq, all = (int64_t)a.n_layers * a.total_q * a.lo.Hq;
-#pragma unroll 1
-  for (int64_t i = blockIdx.y * 8 + (threadIdx.x >> 5); i < items; i += gridDim.y * 8) {
-    const int64_t layer = i / ((int64_t)u.n * a.lo.Hq), row = i + (layer * (a.total_q - u.n) + u.cu) * a.lo.Hq;
-    const float *p = a.rows + row * PR, *o = p + all * PR;
-    float4 x[N], y[N];
-#pragma unroll
-    for (int c = 0; c < N; ++c) {
-      x[c] = __ldcg(reinterpret_cast<const float4*>(p) + 32 * c + lane);
-      y[c] = __ldcg(reinterpret_cast<const float4*>(o) + 32 * c + lane);
-    }
-    const float la = __ldcg(p + D), lb = __ldcg(o + D), top = fmaxf(la, lb);
-    const float wa = la == -INFINITY ? 0.f : exp2f(la - top), wb = lb == -INFINITY ? 0.f : exp2f(lb - top), inv = 1.f / (wa + wb);
-    const float fa = wa * inv, fb = wb * inv;
-    auto join = [&](float s, float t) { return isfinite(t) ? fmaf(fa, s, fb * t) : t; };
-#pragma unroll
-    for (int c = 0; c < N; ++c)
-      *reinterpret_cast<uint2*>(a.out + row * D + 128 * c + 4 * lane) =
-          make_uint2(pack16<DT>(join(x[c].x, y[c].x), join(x[c].y, y[c].y)), pack16<DT>(join(x[c].z, y[c].z), join(x[c].w, y[c].w)));
   }
 }
 
@@ -2701,8 +2735,9 @@ cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if ((a.lo.flags & KVQ_ROTATE_K) && !a.turn_here) {
     if constexpr (SEG) {
-      const int64_t items = (int64_t)a.n_layers * a.max_q * ((a.lo.Hq * (D / 128) + 3) / 4);
-      e = launch_dependent(turn_segments_kernel<D, DT>, dim3(a.lo.B, (unsigned)std::min<int64_t>((items + 7) / 8, 1024)), dim3(256), 0, s, a);
+      const int64_t items = (int64_t)a.n_layers * C::RT / a.lo.g * ((a.lo.Hq * (D / 128) + 3) / 4);
+      const unsigned parts = (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 7) / 8, 4 * 152 / a.n_units + 1));
+      e = launch_dependent(turn_units_kernel<D, DT, C::RT>, dim3(a.n_units, parts), dim3(256), 0, s, a);
     } else {
       const int64_t rows = (int64_t)a.n_layers * a.total_q;
       e = launch_dependent(turn_queries_kernel<D, DT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
@@ -2710,13 +2745,7 @@ cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     a.q = a.out;
   }
-  e = launch_dependent(chunk_attention_kernel<D, DT, MODE, SEG>, dim3(grid), dim3(C::THREADS), smem, s, a);
-  if constexpr (SEG) {
-    if (e != cudaSuccess) return e;
-    const int64_t items = (int64_t)a.n_layers * a.max_q * a.lo.Hq;
-    e = launch_dependent(join_segments_kernel<D, DT>, dim3(a.lo.B, (unsigned)std::min<int64_t>((items + 7) / 8, 1024)), dim3(256), 0, s, a);
-  }
-  return e;
+  return launch_dependent(chunk_attention_kernel<D, DT, MODE, SEG>, dim3(grid), dim3(C::THREADS), smem, s, a);
 }
 
 }  // namespace

@@ -1,18 +1,21 @@
 // kvq_prefix_attention: attention of the newest tokens of every sequence where groups of sequences hold the same
 // pages for a common prefix.
 //
-// With P the tokens that a group shares, a row's softmax splits at P:
-//   out = (e^a A + e^b B) / (e^a + e^b),
-// A and a the output and log-sum over tokens [0, P), B and b over [P, p_i].  All rows of the group see all of [0, P), so
-// that part is one unit of (rows of the group) x (prefix): its packed tokens are read and dequantized once instead of once a
-// sequence.  Both parts run in one launch of the chunk attention kernel (chunk_kernel.cuh), on one line of tiles cut into equal runs;
-// a pass over the rows joins them.
+// A group's rows are the new tokens of all its sequences times the query heads of a kv head.  A unit of work is a row tile of
+// them over the tokens [0, P) that the group shares, which all of the rows see, and then over the tiles that each of its
+// sequences has behind P, which only that sequence's rows see (the others' scores are -inf there).  So the shared packed tokens are read,
+// dequantized and multiplied once for all rows of the tile instead of once a sequence, and a row's softmax runs over both parts
+// like over any other tiles: no second pass joins them.  The chunk attention kernel (chunk_kernel.cuh, SEG) takes
+// the units in place of its own.
+// (First built as two units a row, prefix and own tokens, joined by a pass of its own: a unit of one tile of own tokens took
+// 13 us of latency, and 64 beams over 8 prompts of 8192 tokens 142 us where they now take a third less.)
 //
 // The prefix is what the block table says: the pages that the group's sequences hold in the same places, as far as
-// they are quantized in all of them and before every new token, in whole tiles (so that neither part needs a mask
-// at the border).  kvq_prefix_plan finds it, on the device.
+// they are quantized in all of them and before every new token, in whole tiles.  kvq_prefix_plan finds it and writes the units
+// and the list of own tiles, on the device.
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 
 #include "chunk_attention.cuh"
 #include "kvq_host.cuh"
@@ -20,7 +23,8 @@
 namespace kvq {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanColumns = 2048;  // table columns of a block
 
 struct PlanArgs {
   Layout lo;
@@ -28,115 +32,295 @@ struct PlanArgs {
   const int32_t* cu_groups;
   const int32_t* cu_q;
   const int32_t* seq_lens;
-  int n_groups, total_q, max_q, max_group_q, tile;
+  int n_groups, total_q, max_q, max_group_q, tile, row_tile, n_units, own_tiles;
   uint32_t* status;
-  Segment* segs;  // [n_groups] prefixes, [batch] sequences
+  int32_t* plan;     // total_q, max_q, max_group_q, n_groups
+  uint32_t* ticket;  // blocks that are done; zero between calls
+  int32_t* parts;    // [n_groups] INT_MAX less the first column where the group's sequences part, 0: none; zero between calls
+  int32_t* lens;     // [batch] lengths of the sequences that take part, else 0
+  int32_t* n;        // [batch] new tokens of those
+  int32_t* owner_n;  // [batch] tokens of the rows that begin with this sequence: its own, its group's, or 0
+  int32_t* owner_p;  // [batch] the prefix that its group shares
+  int32_t* owner_end;  // [batch] the sequence behind its last one
+  int32_t* unit_at;  // [batch] its first unit
+  int2* where;
+  SharedUnit* units;
+  OwnTile* own;
 };
 
-// One block a group: its sequences' lengths, the pages that they have in common, its segments.
-__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PlanArgs a) {
-  __shared__ int common, limit, live;
-  __shared__ uint32_t bad;
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int g = blockIdx.x, tid = threadIdx.x, B = a.lo.B, mp = a.lo.max_pages;
-  if (tid == 0) {
-    common = limit = INT_MAX;
-    live = 0;
-    bad = 0;
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
+
+// New tokens of sequence b (0: none, or its rows or length are out of order, which sets *bad), its first row and length.
+__device__ __forceinline__ int new_tokens(const PlanArgs& a, int b, int* cu, int* T, bool* bad) {
+  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], t = a.seq_lens[b], n = (int)((uint32_t)c1 - (uint32_t)c0);
+  *cu = c0;
+  *T = t;
+  if (c0 < 0 || c1 < c0 || c1 > a.total_q || n > a.max_q || t < n || t > a.lo.max_T) {
+    *bad = true;
+    return 0;
   }
-  // the groups cover the batch, in order
+  return n;
+}
+
+// The groups cover the batch, in order.  All threads of a block.
+__device__ __forceinline__ bool groups_in_order(const PlanArgs& a) {
   bool wrong = false;
-  for (int i = tid; i <= a.n_groups; i += kPlanThreads) {
+  for (int i = threadIdx.x; i <= a.n_groups; i += kPlanThreads) {
     const int at = a.cu_groups[i];
     wrong |= i == 0 ? at != 0 : at < a.cu_groups[i - 1];
-    if (i == a.n_groups) wrong |= at != B;
+    if (i == a.n_groups) wrong |= at != a.lo.B;
   }
-  const Segment none{};
-  if (__syncthreads_or(wrong)) {  // every block says the same: nothing to do
-    for (int b = g * kPlanThreads + tid; b < B; b += a.n_groups * kPlanThreads) a.segs[a.n_groups + b] = none;
-    if (tid == 0) {
-      a.segs[g] = none;
-      atomicOr(a.status, KVQ_DEV_SEQ);
-    }
-    return;
-  }
-  const int b0 = a.cu_groups[g], b1 = a.cu_groups[g + 1];
-  // sequences: what is in order, and how far a prefix of those with new tokens may go
-  for (int b = b0 + tid; b < b1; b += kPlanThreads) {
-    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], T = a.seq_lens[b];
-    const int n = (int)((uint32_t)c1 - (uint32_t)c0);
-    Segment s{};
-    if (c0 < 0 || c1 < c0 || c1 > a.total_q || n > a.max_q || T < n || T > a.lo.max_T) {
-      atomicOr(&bad, KVQ_DEV_LENGTH);
-    } else if (n > 0) {
-      s.n = n;
-      s.T = T;
-      s.cu = c0;
-      s.b = b;
-      atomicMin(&limit, min(q_end_of(a.lo, T), T - n));
-      atomicAdd(&live, 1);
-    }
-    a.segs[a.n_groups + b] = s;
-  }
-  __syncthreads();
+  return !__syncthreads_or(wrong);
+}
+
+// Group g's part of the table, columns [j0, j1): the first one where its sequences with new tokens do not hold the same page.
+__device__ __forceinline__ void find_parting(const PlanArgs& a, int g, int j0, int j1) {
+  __shared__ int limit, first, live, found;
+  const int tid = threadIdx.x, mp = a.lo.max_pages, b0 = a.cu_groups[g], b1 = a.cu_groups[g + 1];
   if (tid == 0) {
-    if (g == 0 && a.cu_q[0] != 0) atomicOr(&bad, KVQ_DEV_LENGTH);
-    if (live > 1 && !bad && a.cu_q[b1] - a.cu_q[b0] > a.max_group_q) atomicOr(&bad, KVQ_DEV_LENGTH);
+    limit = first = found = INT_MAX;
+    live = 0;
   }
   __syncthreads();
-  // (with a sequence out of order the rows of the others are not one run: they go without a common prefix)
-  const bool share = live > 1 && !bad;
-  if (share) {
-    // the first page that the group's live sequences do not all hold: a thread compares a page with the first live sequence's
-    int first = b0;
-    while (a.cu_q[first + 1] == a.cu_q[first]) ++first;
-    const int pages = limit / a.lo.pt;
-    const int32_t* ref = a.table + (int64_t)first * mp;
-    // few pages: threads share a page's sequences
-    const int per = max(1, min(b1 - first, kPlanThreads / max(1, pages)));
-    for (int64_t e = tid; e < (int64_t)pages * per; e += kPlanThreads) {
-      const int j = (int)(e % pages), sub = (int)(e / pages);
-      if (j >= *(volatile int*)&common) continue;
+  for (int b = b0 + tid; b < b1; b += kPlanThreads) {
+    int cu, T;
+    bool bad = false;
+    const int n = new_tokens(a, b, &cu, &T, &bad);
+    if (n == 0) continue;
+    atomicMin(&limit, min(q_end_of(a.lo, T), T - n));
+    atomicMin(&first, b);
+    atomicAdd(&live, 1);
+  }
+  __syncthreads();
+  if (live < 2) return;
+  j1 = min(j1, limit / a.lo.pt);
+  const int columns = j1 - j0;
+  if (columns <= 0) return;
+  // threads side by side take columns; few columns: threads share a column's sequences
+  const int32_t* ref = a.table + (int64_t)first * mp;
+  const int wide = min((columns + 31) & ~31, kPlanThreads), subs = kPlanThreads / wide, sub = tid / wide;
+  int mine = INT_MAX;
+  if (sub < subs)
+    for (int j = j0 + tid % wide; j < j1; j += wide) {
       const int p = ref[j];
       bool same = p >= 0 && p < a.lo.n_pages;
+      const int32_t* at = a.table + j;
 #pragma unroll 8
-      for (int b = first + 1 + sub; b < b1; b += per) same &= a.table[(int64_t)b * mp + j] == p || a.cu_q[b + 1] == a.cu_q[b];
-      if (!same) atomicMin(&common, j);
+      for (int b = first + 1 + sub; b < b1; b += subs)
+        if (at[(int64_t)b * mp] != p) same &= a.cu_q[b + 1] == a.cu_q[b];  // (a slot without new tokens has no say)
+      if (!same) {
+        mine = j;
+        break;
+      }
+    }
+  if (mine != INT_MAX) atomicMin(&found, mine);
+  __syncthreads();
+  if (tid == 0 && found != INT_MAX) atomicMax(a.parts + g, INT_MAX - found);
+}
+
+// What a group shares: the sequences' lengths and rows, the prefix, and whether taking it in common saves tiles.  A warp.
+__device__ __forceinline__ void plan_group(const PlanArgs& a, int g) {
+  const int lane = threadIdx.x & 31, b0 = a.cu_groups[g], b1 = a.cu_groups[g + 1], gq = a.lo.g, RT = a.row_tile, NT = a.tile;
+  int live = 0, limit = INT_MAX, first = INT_MAX;
+  bool bad = false;
+  for (int b = b0 + lane; b < b1; b += 32) {
+    int cu, T;
+    const int n = new_tokens(a, b, &cu, &T, &bad);
+    a.n[b] = n;
+    a.lens[b] = n ? T : 0;
+    a.owner_n[b] = n;
+    a.owner_p[b] = 0;
+    a.owner_end[b] = b + 1;
+    if (n) {
+      ++live;
+      limit = min(limit, min(q_end_of(a.lo, T), T - n));
+      first = min(first, b);
     }
   }
-  __syncthreads();
-  if (tid == 0 && bad) atomicOr(a.status, bad);
-  const int pages = share ? min(common, limit / a.lo.pt) : 0;
-  const int P = (int)((int64_t)pages * a.lo.pt / a.tile) * a.tile;
-  if (P > 0)
-    for (int b = b0 + tid; b < b1; b += kPlanThreads)
-      if (a.segs[a.n_groups + b].n) a.segs[a.n_groups + b].from = P;  // (written by this thread)
-  if (tid == 0) {
-    Segment s{};
-    if (P > 0) {
-      int first = b0;
-      while (a.cu_q[first + 1] == a.cu_q[first]) ++first;
-      s.n = a.cu_q[b1] - a.cu_q[b0];
-      s.T = P;
-      s.cu = a.cu_q[b0];
-      s.b = first;
-      s.shared = 1;
-    }
-    a.segs[g] = s;
+  live = warp_sum(live);
+  limit = __reduce_min_sync(0xffffffffu, limit);
+  first = __reduce_min_sync(0xffffffffu, first);
+  bad = __any_sync(0xffffffffu, bad);
+  const int parting = __ldcg(a.parts + g);
+  if (lane == 0) a.parts[g] = 0;
+  if (!bad && live > 1 && a.cu_q[b1] - a.cu_q[b0] > a.max_group_q) bad = true;
+  if (bad && lane == 0) atomicOr(a.status, KVQ_DEV_LENGTH);
+  // (with a sequence out of order the others' rows need not be one run: they go without a common prefix)
+  if (bad || live < 2) return;
+  const int pages = min(parting ? INT_MAX - parting : INT_MAX, limit / a.lo.pt);
+  const int P = (int)((int64_t)pages * a.lo.pt / NT) * NT;
+  if (P == 0) return;
+  // tiles taken apart (row tiles of each sequence over all it has cached), and together
+  __syncwarp();
+  const int cu0 = a.cu_q[b0];
+  int64_t apart = 0, together = 0;
+  int rows = 0;
+  for (int b = b0 + lane; b < b1; b += 32) {
+    const int n = a.n[b];
+    if (!n) continue;
+    const int tiles = ceil_div(a.lens[b], NT), r0 = (a.cu_q[b] - cu0) * gq, r1 = r0 + n * gq;
+    apart += (int64_t)ceil_div(n * gq, RT) * tiles;
+    together += (int64_t)((r1 - 1) / RT - r0 / RT + 1) * (tiles - P / NT);
+    rows += n * gq;
+  }
+  rows = warp_sum(rows);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    apart += __shfl_xor_sync(0xffffffffu, apart, o);
+    together += __shfl_xor_sync(0xffffffffu, together, o);
+  }
+  together += (int64_t)ceil_div(rows, RT) * (P / NT);
+  if (together >= apart) return;
+  for (int b = b0 + lane; b < b1; b += 32) {
+    a.owner_n[b] = b == first ? rows / gq : 0;
+    a.owner_p[b] = b == first ? P : 0;
+    a.owner_end[b] = b1;
   }
 }
 
-// Workspace: that of the chunk attention, segments, two parts of every row.
+// Unit i of the list, whose first row and owner are known: its rows, prefix and own tiles.  A warp.
+__device__ __forceinline__ void plan_unit(const PlanArgs& a, int i, int* own_count) {
+  const int lane = threadIdx.x & 31, gq = a.lo.g, NT = a.tile;
+  SharedUnit u = a.units[i];
+  const int b0 = u.first, shared = a.owner_p[b0];
+  u.rows = min(a.row_tile, a.owner_n[b0] * gq - u.r0);
+  const int tok0 = u.r0 / gq, tok1 = (u.r0 + u.rows - 1) / gq;  // of the owner's
+  if (shared)
+    u.prefix = shared;
+  else  // one sequence: what all of the rows see of it in the packed tiers
+    u.prefix = min(q_end_of(a.lo, a.lens[b0]), a.lens[b0] - a.n[b0] + tok0 + 1) / NT * NT;
+  const int end = a.owner_end[b0];
+  auto tiles_of = [&](int b, int* p_lo, int* ra, int* rb) {
+    if (b >= end || !a.n[b]) return 0;
+    const int off = a.cu_q[b] - u.cu, n = a.n[b], T = a.lens[b], t0 = max(tok0, off), t1 = min(tok1, off + n - 1);
+    if (t0 > t1) return 0;
+    *ra = max(0, off * gq - u.r0);
+    *rb = min(u.rows, (off + n) * gq - u.r0);
+    *p_lo = T - n + t0 - off;
+    return (T - n + t1 - off) / NT - u.prefix / NT + 1;
+  };
+  int total = 0, low = INT_MAX;
+  for (int b = b0 + lane; b - lane < end; b += 32) {
+    int p = INT_MAX, ra, rb;
+    total += tiles_of(b, &p, &ra, &rb);
+    low = min(low, p);
+  }
+  total = warp_sum(total);
+  u.p_lo = __reduce_min_sync(0xffffffffu, low);
+  u.n_own = total;
+  int at = 0;
+  if (lane == 0) at = atomicAdd(own_count, total);  // (which places a unit gets changes no result)
+  u.own = at = __shfl_sync(0xffffffffu, at, 0);
+  if (at > a.own_tiles - total) u.rows = 0;  // (the list holds all that lengths up to max_T need)
+  __syncwarp();
+  if (lane == 0) a.units[i] = u;
+  if (u.rows == 0) return;
+  for (int b = b0 + lane; b - lane < end; b += 32) {
+    int p, ra = 0, rb = 0;
+    const int mine = tiles_of(b, &p, &ra, &rb);
+    uint32_t have = __ballot_sync(0xffffffffu, mine > 0);
+    while (have) {
+      const int src = __ffs(have) - 1;
+      have &= have - 1;
+      const int count = __shfl_sync(0xffffffffu, mine, src), s = b - lane + src;
+      const int rows = __shfl_sync(0xffffffffu, ra | rb << 16, src), T = a.lens[s];
+      for (int k = lane; k < count; k += 32) a.own[at + k] = OwnTile{s, u.prefix + k * NT, T, rows};
+      at += count;
+    }
+  }
+}
+
+// Grid (groups, runs of table columns); the last block to finish writes the plan.
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PlanArgs a) {
+  __shared__ bool last;
+  __shared__ int scan[kPlanWarps], own_count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.lo.B;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const bool in_order = groups_in_order(a);
+  if (in_order) find_parting(a, blockIdx.x, blockIdx.y * kPlanColumns, (blockIdx.y + 1) * kPlanColumns);
+  if (tid == 0) {
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    own_count = 0;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  if (tid == 0) {
+    *a.ticket = 0;
+    a.plan[0] = a.total_q;
+    a.plan[1] = a.max_q;
+    a.plan[2] = a.max_group_q;
+    a.plan[3] = a.n_groups;
+    const uint32_t bad = !in_order ? KVQ_DEV_SEQ : a.cu_q[0] != 0 ? KVQ_DEV_LENGTH : 0;
+    if (bad) atomicOr(a.status, bad);
+  }
+  int units = 0;
+  if (in_order) {
+    for (int g = warp; g < a.n_groups; g += kPlanWarps) plan_group(a, g);
+    __syncthreads();
+    // positions and sequences of the rows
+    for (int b = warp; b < B; b += kPlanWarps) {
+      const int n = a.n[b], cu = a.cu_q[b], p = a.lens[b] - n;
+      for (int i = lane; i < n; i += 32) a.where[cu + i] = make_int2(p + i, b);
+    }
+    // every owner's row tiles
+    for (int base = 0; base < B; base += kPlanThreads) {
+      const int b = base + tid, mine = b < B ? ceil_div(a.owner_n[b] * a.lo.g, a.row_tile) : 0;
+      int x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = x;
+      __syncthreads();
+      const int s = scan[lane], before = warp_sum(lane < warp ? s : 0);
+      if (b < B) a.unit_at[b] = units + before + x - mine;
+      units += warp_sum(s);
+    }
+    units = min(units, a.n_units);
+    __syncthreads();
+    for (int b = warp; b < B; b += kPlanWarps) {
+      const int n = ceil_div(a.owner_n[b] * a.lo.g, a.row_tile), at = a.unit_at[b];
+      for (int k = lane; k < n && at + k < a.n_units; k += 32) {
+        SharedUnit u{};
+        u.cu = a.cu_q[b];
+        u.r0 = k * a.row_tile;
+        u.first = b;
+        a.units[at + k] = u;
+      }
+    }
+    __syncthreads();
+    for (int i = warp; i < units; i += kPlanWarps) plan_unit(a, i, &own_count);
+  }
+  for (int i = units + tid; i < a.n_units; i += kPlanThreads) a.units[i] = SharedUnit{};
+}
+
+// Workspace: that of the chunk attention, then the plan.
 struct PrefixWs {
-  size_t segs, rows, total, zeroed;
+  size_t plan, parts, seqs, where, units, own, total, zeroed;
+  int n_units, own_tiles;
 };
-PrefixWs prefix_ws(const kvq_config* c, int n_groups, int64_t rows) {
+kvq_status prefix_ws(const kvq_config* c, int n_groups, int64_t rows, PrefixWs* out) {
   PrefixWs w{};
-  w.segs = align_up(chunk_workspace_bytes(c, &w.zeroed));
-  w.rows = w.segs + align_up(sizeof(Segment) * ((size_t)n_groups + c->batch));
-  w.total = w.rows + align_up(sizeof(float) * 2 * (size_t)rows * c->H_q * chunk_part_row(c->D));
-  return w;
+  const int64_t g = c->H_q / c->H_kv, tiles = c->max_T / chunk_tile(c->D) + 2;
+  const int64_t units = rows * g / 128 + c->batch, own = (units + c->batch) * tiles;
+  if (units > 1 << 24 || own > 1 << 28) return fail(KVQ_ERR_UNSUPPORTED, "a plan of %lld row tiles over %lld tiles", (long long)units, (long long)own);
+  w.n_units = (int)units;
+  w.own_tiles = (int)own;
+  w.plan = align_up(chunk_workspace_bytes(c, &w.zeroed));
+  w.parts = w.plan + kWsAlign;
+  w.seqs = w.parts + align_up(sizeof(int32_t) * (size_t)n_groups);
+  w.where = w.seqs + align_up(sizeof(int32_t) * 6 * (size_t)c->batch);
+  w.units = w.where + align_up(sizeof(int2) * (size_t)rows);
+  w.own = w.units + align_up(sizeof(SharedUnit) * (size_t)units);
+  w.total = w.own + align_up(sizeof(OwnTile) * (size_t)own);
+  *out = w;
+  return KVQ_OK;
 }
 
 kvq_status prefix_config(const kvq_config* cfg, int32_t n_groups, int64_t rows) {
@@ -148,10 +332,11 @@ kvq_status prefix_config(const kvq_config* cfg, int32_t n_groups, int64_t rows) 
   return KVQ_OK;
 }
 
-kvq_status check_prefix_ws(const kvq_config* cfg, int32_t n_groups, int64_t rows, void* ws, size_t bytes) {
+kvq_status check_prefix_ws(const kvq_config* cfg, int32_t n_groups, int64_t rows, void* ws, size_t bytes, PrefixWs* w) {
   if (!ws) return fail(KVQ_ERR_WORKSPACE, "workspace is NULL");
-  const size_t need = prefix_ws(cfg, n_groups, rows).total;
-  if (bytes < need) return fail(KVQ_ERR_WORKSPACE, "workspace %zu B < %zu B needed", bytes, need);
+  const kvq_status st = prefix_ws(cfg, n_groups, rows, w);
+  if (st != KVQ_OK) return st;
+  if (bytes < w->total) return fail(KVQ_ERR_WORKSPACE, "workspace %zu B < %zu B needed", bytes, w->total);
   if (((uintptr_t)ws) % kWsAlign) return fail(KVQ_ERR_WORKSPACE, "workspace not 256-byte aligned");
   return KVQ_OK;
 }
@@ -160,6 +345,7 @@ kvq_status check_rows(const kvq_config* cfg, int32_t total_q, int32_t max_q, int
   if (total_q < 0 || max_q < 0 || max_group_q < max_q || max_group_q > total_q)
     return fail(KVQ_ERR_ARG, "total_q=%d, max_q=%d, max_group_q=%d", total_q, max_q, max_group_q);
   if (max_q > cfg->max_T) return fail(KVQ_ERR_CAPACITY, "max_q=%d > max_T=%d", max_q, cfg->max_T);
+  if ((int64_t)max_group_q * (cfg->H_q / cfg->H_kv) > 1 << 28) return fail(KVQ_ERR_UNSUPPORTED, "max_group_q=%d", max_group_q);
   return KVQ_OK;
 }
 
@@ -170,22 +356,24 @@ using namespace kvq;
 
 extern "C" {
 
-kvq_status kvq_prefix_workspace_bytes(const kvq_config* cfg, int32_t n_groups, int64_t rows, size_t* bytes) {
-  const kvq_status st = prefix_config(cfg, n_groups, rows);
+kvq_status kvq_prefix_workspace_bytes(const kvq_config* cfg, int32_t n_groups, int32_t rows, size_t* bytes) {
+  kvq_status st = prefix_config(cfg, n_groups, rows);
   if (st != KVQ_OK) return st;
   if (!bytes) return fail(KVQ_ERR_ARG, "bytes is NULL");
-  *bytes = prefix_ws(cfg, n_groups, rows).total;
+  PrefixWs w;
+  if ((st = prefix_ws(cfg, n_groups, rows, &w)) != KVQ_OK) return st;
+  *bytes = w.total;
   return ok();
 }
 
-kvq_status kvq_prefix_workspace_init(const kvq_config* cfg, int32_t n_groups, int64_t rows, void* workspace, size_t ws_bytes,
+kvq_status kvq_prefix_workspace_init(const kvq_config* cfg, int32_t n_groups, int32_t rows, void* workspace, size_t ws_bytes,
                                      void* stream) {
   kvq_status st = prefix_config(cfg, n_groups, rows);
   if (st != KVQ_OK) return st;
-  if ((st = check_prefix_ws(cfg, n_groups, rows, workspace, ws_bytes)) != KVQ_OK) return st;
-  const PrefixWs w = prefix_ws(cfg, n_groups, rows);
+  PrefixWs w;
+  if ((st = check_prefix_ws(cfg, n_groups, rows, workspace, ws_bytes, &w)) != KVQ_OK) return st;
   cudaError_t e = cudaMemsetAsync(workspace, 0, w.zeroed, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync((char*)workspace + w.segs, 0, w.rows - w.segs, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync((char*)workspace + w.plan, 0, w.own - w.plan, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
   return ok();
 }
@@ -199,7 +387,8 @@ kvq_status kvq_prefix_plan(const kvq_config* cfg, const int32_t* block_table, co
   if (!block_table || !cu_groups || !cu_q || !seq_lens) return fail(KVQ_ERR_ARG, "block_table / cu_groups / cu_q / seq_lens is NULL");
   if (((uintptr_t)block_table | (uintptr_t)cu_groups | (uintptr_t)cu_q | (uintptr_t)seq_lens) & 3u)
     return fail(KVQ_ERR_ARG, "block_table / cu_groups / cu_q / seq_lens must be 4-byte aligned");
-  if ((st = check_prefix_ws(cfg, n_groups, 0, workspace, ws_bytes)) != KVQ_OK) return st;
+  PrefixWs w;
+  if ((st = check_prefix_ws(cfg, n_groups, total_q, workspace, ws_bytes, &w)) != KVQ_OK) return st;
   PlanArgs a{};
   a.lo = make_layout(cfg);
   a.table = block_table;
@@ -211,9 +400,25 @@ kvq_status kvq_prefix_plan(const kvq_config* cfg, const int32_t* block_table, co
   a.max_q = max_q;
   a.max_group_q = max_group_q;
   a.tile = chunk_tile(cfg->D);
+  a.row_tile = chunk_form(cfg, (int64_t)max_group_q * a.lo.g) == kChunkPaired ? 256 : 128;
+  a.n_units = w.n_units;
+  a.own_tiles = w.own_tiles;
+  char* base = (char*)workspace;
   a.status = (uint32_t*)workspace;
-  a.segs = (Segment*)((char*)workspace + prefix_ws(cfg, n_groups, 0).segs);
-  const cudaError_t e = launch_dependent(prefix_plan_kernel, dim3(n_groups), dim3(kPlanThreads), 0, (cudaStream_t)stream, a);
+  a.plan = (int32_t*)(base + w.plan);
+  a.ticket = (uint32_t*)(base + w.plan) + 4;
+  a.parts = (int32_t*)(base + w.parts);
+  a.lens = (int32_t*)(base + w.seqs);
+  a.n = a.lens + cfg->batch;
+  a.owner_n = a.n + cfg->batch;
+  a.owner_p = a.owner_n + cfg->batch;
+  a.owner_end = a.owner_p + cfg->batch;
+  a.unit_at = a.owner_end + cfg->batch;
+  a.where = (int2*)(base + w.where);
+  a.units = (SharedUnit*)(base + w.units);
+  a.own = (OwnTile*)(base + w.own);
+  const unsigned runs = (unsigned)std::min((cfg->max_T / cfg->page_tokens + kPlanColumns) / kPlanColumns, 65535);
+  const cudaError_t e = launch_dependent(prefix_plan_kernel, dim3(n_groups, runs), dim3(kPlanThreads), 0, (cudaStream_t)stream, a);
   if (e != cudaSuccess) return cuda_fail(e, "prefix plan kernel");
   return ok();
 }
@@ -234,9 +439,8 @@ kvq_status kvq_prefix_attention(const kvq_config* cfg, const kvq_cache* cache, i
   }
   ChunkArgs a{};
   if ((st = cache_ptrs(cfg, cache, &a.cp)) != KVQ_OK) return st;
-  const int64_t rows = (int64_t)n_layers * total_q;
-  if (rows > 0x7fffffff) return fail(KVQ_ERR_UNSUPPORTED, "%d layers of %d rows", n_layers, total_q);
-  if ((st = check_prefix_ws(cfg, n_groups, rows, workspace, ws_bytes)) != KVQ_OK) return st;
+  PrefixWs w;
+  if ((st = check_prefix_ws(cfg, n_groups, total_q, workspace, ws_bytes, &w)) != KVQ_OK) return st;
   if (total_q == 0 || max_q == 0) return ok();
   a.lo = make_layout(cfg);
   a.layer0 = layer0;
@@ -246,15 +450,25 @@ kvq_status kvq_prefix_attention(const kvq_config* cfg, const kvq_cache* cache, i
   a.total_q = total_q;
   a.max_q = max_q;
   const int grid = chunk_workspace(cfg, workspace, &a);
-  const PrefixWs w = prefix_ws(cfg, n_groups, rows);
-  a.segs = (const Segment*)((char*)workspace + w.segs);
-  a.rows = (float*)((char*)workspace + w.rows);
+  a.unit_cost = getenv("KVQ_W") ? atoi(getenv("KVQ_W")) : 2;
+  // the kernel counts its tiles in 32 bits: prefixes of all units, the own tiles, and what a unit costs besides
+  const int64_t line = (int64_t)w.n_units * (cfg->max_T / chunk_tile(cfg->D) + a.unit_cost) + w.own_tiles;
+  if (line * n_layers * cfg->H_kv > 0x7fffffff - 2 * grid)
+    return fail(KVQ_ERR_UNSUPPORTED, "too many tiles for one call: pass fewer layers or rows");
+  int mode;
+  if ((st = chunk_common(cfg, &a, max_group_q, cfg->batch, &mode)) != KVQ_OK) return st;
+  a.by_warp = 0;
+  const char* base = (const char*)workspace;
+  a.plan = (const int32_t*)(base + w.plan);
+  a.lens = (const int32_t*)(base + w.seqs);
+  a.where = (const int2*)(base + w.where);
+  a.units = (const SharedUnit*)(base + w.units);
+  a.own = (const OwnTile*)(base + w.own);
+  a.n_units = w.n_units;
+  a.own_tiles = w.own_tiles;
   a.n_groups = n_groups;
   a.max_group_q = max_group_q;
-  int mode;
-  // owners: sequences and prefixes, and the rows of the prefixes' row tiles once more
-  const int64_t owners = (int64_t)cfg->batch + n_groups + (int64_t)total_q * a.lo.g / 128;
-  if ((st = chunk_common(cfg, &a, max_group_q, owners, &mode)) != KVQ_OK) return st;
+  a.most_rows = mode == kChunkFew ? a.cols : mode == kChunkPaired ? 256 : 128;
   cudaError_t e = mode == kChunkFew ? launch_prefix_few(a, grid, (cudaStream_t)stream)
                   : cfg->D == 128   ? launch_prefix_d128(a, mode, grid, (cudaStream_t)stream)
                                     : launch_prefix_d256(a, grid, (cudaStream_t)stream);

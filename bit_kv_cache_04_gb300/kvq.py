@@ -123,8 +123,8 @@ def _load():
         "kvq_chunk_workspace_bytes": ([cfgp, P(sz)], ctypes.c_int),
         "kvq_chunk_workspace_init": ([cfgp, vp, sz, vp], ctypes.c_int),
         "kvq_chunk_attention": ([cfgp, cachep, i32, i32, vp, vp, i32, i32, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
-        "kvq_prefix_workspace_bytes": ([cfgp, i32, i64, P(sz)], ctypes.c_int),
-        "kvq_prefix_workspace_init": ([cfgp, i32, i64, vp, sz, vp], ctypes.c_int),
+        "kvq_prefix_workspace_bytes": ([cfgp, i32, i32, P(sz)], ctypes.c_int),
+        "kvq_prefix_workspace_init": ([cfgp, i32, i32, vp, sz, vp], ctypes.c_int),
         "kvq_prefix_plan": ([cfgp, vp, vp, i32, vp, i32, i32, i32, vp, vp, sz, vp], ctypes.c_int),
         "kvq_prefix_attention": ([cfgp, cachep, i32, i32, i32, vp, i32, i32, i32, vp, vp, sz, vp], ctypes.c_int),
         "kvq_read_device_status": ([vp, P(u32), vp], ctypes.c_int),
@@ -641,7 +641,7 @@ class BeamSelect:
 
 class PrefixAttention:
     """Attention of groups of sequences that share the pages of a prefix (kvq_prefix_plan, kvq_prefix_attention)
-    and its workspace.  `rows`: the largest n_layers * total_q of a call.  Calls that may run at the same time (also graphs
+    and its workspace.  `rows`: the largest total_q of a plan.  Calls that may run at the same time (also graphs
     replayed side by side) need an object each."""
 
     def __init__(self, cache: KVCache, groups: int, rows: int, stream=None):

@@ -639,8 +639,9 @@ KVQ_API kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* c
  *
  * kvq_prefix_plan works out, on the device, what the groups share: the pages that all sequences of the group with
  * new tokens hold in the same places of their table rows, as far as they are quantized and before the new tokens of all of them, in
- * whole tiles of 128 tokens (64 with D = 256).  A group that shares less, or has one sequence with new tokens, is attended to as by
- * kvq_chunk_attention.  One plan serves the calls of all layers; it holds until the lengths, the table or the rows change.
+ * whole tiles of 128 tokens (64 with D = 256).  A group that shares less, has one sequence with new tokens, or has so many rows a
+ * sequence that row tiles across sequences save nothing is attended to sequence by sequence.
+ * One plan serves the calls of all layers; it holds until the lengths, the table or the rows change.
  *  cu_groups: [n_groups + 1] int32, device, ascending from 0 to batch: group i is sequences [cu_groups[i], cu_groups[i + 1])
  *             (else KVQ_DEV_SEQ, and no rows are written).
  *  cu_q, total_q, max_q, seq_lens: as for kvq_chunk_attention (lengths INCLUDING the new tokens; pages for them are
@@ -648,13 +649,13 @@ KVQ_API kvq_status kvq_chunk_attention(const kvq_config* cfg, const kvq_cache* c
  *  max_group_q: a host bound on the new tokens of any group, max_q <= max_group_q <= total_q (the larger it is, the more rows the
  *             kernel expects at a time).  A group with more sets KVQ_DEV_LENGTH and goes without its common prefix, as does a group with
  *             a sequence whose rows or length are out of order (KVQ_DEV_LENGTH; that sequence's rows are left as they are).
- * kvq_prefix_attention takes n_groups, total_q, max_q and max_group_q as the plan did; q, out, roundings, values out of range and
- * pages out of range as kvq_chunk_attention.
- *  workspace: kvq_prefix_workspace_bytes for `rows` = the largest n_layers * total_q (none for a plan alone), 256-byte aligned,
- *             prepared once by kvq_prefix_workspace_init; holds the plan; calls that may run at the same time need one each.
- *             Its first word is the device status word. */
-KVQ_API kvq_status kvq_prefix_workspace_bytes(const kvq_config* cfg, int32_t n_groups, int64_t rows, size_t* bytes);
-KVQ_API kvq_status kvq_prefix_workspace_init(const kvq_config* cfg, int32_t n_groups, int64_t rows, void* workspace,
+ * kvq_prefix_attention takes n_groups, total_q, max_q and max_group_q as the plan did (else KVQ_DEV_SEQ, and no rows are
+ * written); q, out, roundings, values out of range and pages out of range as kvq_chunk_attention.
+ *  workspace: kvq_prefix_workspace_bytes for `rows` = the largest total_q, 256-byte aligned,
+ *             prepared once by kvq_prefix_workspace_init for the same n_groups and rows; holds the plan; calls that may run at the same
+ *             time need one each.  Its first word is the device status word. */
+KVQ_API kvq_status kvq_prefix_workspace_bytes(const kvq_config* cfg, int32_t n_groups, int32_t rows, size_t* bytes);
+KVQ_API kvq_status kvq_prefix_workspace_init(const kvq_config* cfg, int32_t n_groups, int32_t rows, void* workspace,
                                              size_t ws_bytes, void* stream);
 KVQ_API kvq_status kvq_prefix_plan(const kvq_config* cfg, const int32_t* block_table, const int32_t* cu_groups, int32_t n_groups,
                                    const int32_t* cu_q, int32_t total_q, int32_t max_q, int32_t max_group_q,

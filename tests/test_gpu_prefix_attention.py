@@ -89,16 +89,17 @@ def build(groups, own, new, L=1, H_kv=2, g=4, D=128, seed=0, page_tokens=16, val
 
 
 def shared_of(pa):
-    """(P of every group, first own token of every sequence) of the plan, from the workspace."""
-    import ctypes
+    """The prefix that every group shares, from the plan in the workspace: the longest of its sequences'."""
+    cfg = pa.cache.cfg
+    B = cfg.batch
 
-    ws = pa.workspace
-    zeroed = K.kvq_chunk_workspace_bytes(pa.cache.cfg)
-    n = pa.groups + pa.cache.cfg.batch
-    at = (zeroed + 255) // 256 * 256
-    segs = ws[at:at + n * 32].view(torch.int32).view(n, 8).cpu().numpy()
-    assert ctypes.sizeof(ctypes.c_int32) * 8 == 32
-    return [int(x[1]) if x[0] else 0 for x in segs[:pa.groups]], [int(x[4]) for x in segs[pa.groups:]]
+    def up(x):
+        return (x + 255) // 256 * 256
+
+    at = up(K.kvq_chunk_workspace_bytes(cfg)) + 256 + up(4 * pa.groups)
+    p = pa.workspace[at:at + 16 * B].view(torch.int32).view(4, B)[3].cpu().numpy()  # lens, new tokens, rows' tokens, prefix
+    cu = pa.cu_groups.tolist()
+    return [int(p[cu[i]:cu[i + 1]].max(initial=0)) for i in range(pa.groups)]
 
 
 def attend(cache, lens, cu_g, n_new, most, q=None, pad=2, seed=1, pa=None):
@@ -109,7 +110,8 @@ def attend(cache, lens, cu_g, n_new, most, q=None, pad=2, seed=1, pa=None):
         g = torch.Generator(device="cuda").manual_seed(seed)
         q = torch.randn((cfg.L, total, cfg.H_q, cfg.D), generator=g, device="cuda").to(DT[cfg.in_dtype])
     out = torch.full_like(q, -7.0)
-    pa = pa or K.PrefixAttention(cache, cu_g.numel() - 1, cfg.L * total)
+    pa = pa or K.PrefixAttention(cache, cu_g.numel() - 1, total)
+    pa.cu_groups = cu_g
     pa.plan(cu_g, torch.as_tensor(cu, device="cuda"), total, max(n_new), most, lens)
     pa.attention(0, cfg.L, q, out)
     torch.cuda.synchronize()
@@ -122,7 +124,7 @@ def check(cache, lens, cu_g, n_new, most, want_shared=None, **kw):
     q, out, cu, pa = attend(cache, lens, cu_g, n_new, most, **kw)
     assert pa.device_status() == 0
     if want_shared is not None:
-        assert shared_of(pa)[0] == want_shared
+        assert shared_of(pa) == want_shared
     oc = oracle_cfg(cfg)
     bufs = gpu_buffers_as_oracle(cache, oc)
     table = cache.block_table.cpu().numpy()
@@ -201,7 +203,8 @@ def _bits(cache, lens, cu_g, n, most, cu=None, pad=0):
     total = sum(n) + pad
     q = torch.randn((cfg.L, total, cfg.H_q, cfg.D), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").half()
     out = torch.full_like(q, -7.0)
-    pa = K.PrefixAttention(cache, cu_g.numel() - 1, cfg.L * total)
+    pa = K.PrefixAttention(cache, cu_g.numel() - 1, total)
+    pa.cu_groups = cu_g
     pa.plan(cu_g, torch.as_tensor(cu, device="cuda"), total, max(n), most, lens)
     pa.attention(0, cfg.L, q, out)
     torch.cuda.synchronize()
@@ -212,19 +215,19 @@ def test_what_is_out_of_order():
     c = build([300, 300], [[30, 40, 50], [10, 20, 30]], [[1, 2, 1], [1, 1, 1]])
     cache, lens, cu_g, n = c[0], c[2], c[3], c[4]
     q, good, pa = _bits(cache, lens, cu_g, n, 4)
-    assert pa.device_status() == 0 and shared_of(pa)[0] == [256, 256]
+    assert pa.device_status() == 0 and shared_of(pa) == [256, 256]
     # a bad length: that sequence's rows stay, its group goes without the prefix, the others get theirs
     for bad in (-1, 1, cache.cfg.max_T + 1):
         l2 = lens.clone()
         l2[1] = bad
         _, out, pa = _bits(cache, l2, cu_g, n, 4)
-        assert pa.device_status() == K.DEV_LENGTH and shared_of(pa)[0] == [0, 256]
+        assert pa.device_status() == K.DEV_LENGTH and shared_of(pa) == [0, 256]
         assert torch.all(out[:, 1:3] == -7.0)
         keep = [0, 3, 4, 5, 6]
         assert (out[:, keep].float() - good[:, keep].float()).norm() <= 2.0 ** -9 * good[:, keep].float().norm()
     # more new tokens in a group than the bound
     _, out, pa = _bits(cache, lens, cu_g, n, 3)
-    assert pa.device_status() == K.DEV_LENGTH and shared_of(pa)[0] == [0, 256]
+    assert pa.device_status() == K.DEV_LENGTH and shared_of(pa) == [0, 256]
     assert (out.float() - good.float()).norm() <= 2.0 ** -9 * good.float().norm()
     # rows that do not ascend, or begin late
     for cu in ([0, 1, 0, 4, 5, 6, 7], [1, 1, 3, 4, 5, 6, 7], [0, 1, 3, 4, 5, 6, 99]):
@@ -241,7 +244,7 @@ def test_pages_out_of_range():
     cache, lens, cu_g, n = c[0], c[2], c[3], c[4]
     cache.block_table[:, 9] = cache.cfg.n_pages  # the same in all: the prefix ends before it
     _, out, pa = _bits(cache, lens, cu_g, n, 3)
-    assert pa.device_status() == K.DEV_PAGE and shared_of(pa)[0] == [128]
+    assert pa.device_status() == K.DEV_PAGE and shared_of(pa) == [128]
     assert torch.isfinite(out).all()
 
 
@@ -275,7 +278,7 @@ def test_window_values_that_are_not_finite(key, new):
     c = build([300], [[45, 60, 50]], [[new, new, new]], values=spoil, **kw)
     cache, lens, cu_g, n = c[0], c[2], c[3], c[4]
     q, out, cu, pa = attend(cache, lens, cu_g, n, c[5])
-    assert pa.device_status() == 0 and shared_of(pa)[0] == [256]
+    assert pa.device_status() == 0 and shared_of(pa) == [256]
     ref = torch.full_like(q, -7.0)
     cache.chunk_attention(0, 1, q, torch.as_tensor(cu, device="cuda"), q.shape[1], max(n), lens, ref)
     torch.cuda.synchronize()
@@ -314,12 +317,53 @@ def test_captured_and_on_two_streams():
     assert torch.equal(o1, again) and torch.equal(o2, again)
 
 
-def test_a_workspace_without_a_plan_writes_nothing():
-    c = build([300], [[30, 40]], [[1, 1]])
-    pa = K.PrefixAttention(c[0], 1, 2)
-    pa.planned = (2, 1, 2)
-    q = torch.randn((1, 2, c[0].cfg.H_q, 128), device="cuda").half()
+@pytest.mark.parametrize("beams,g", [(2, 4), (2, 17), (40, 8)])
+@pytest.mark.parametrize("fmt", [{}, ROT4])
+def test_a_call_without_its_plan_writes_nothing(beams, g, fmt):
+    """None yet, and one for other sizes: said in the status word."""
+    new = g if g > 8 else 1
+    c = build([300], [[30 + new + i for i in range(beams)]], [[new] * beams], g=min(g, 8), H_kv=1, **fmt)
+    cache, lens, cu_g, n = c[0], c[2], c[3], c[4]
+    total = sum(n)
+    pa = K.PrefixAttention(cache, 1, total)
+    q = torch.randn((1, total, cache.cfg.H_q, 128), device="cuda").half()
     out = torch.full_like(q, -7.0)
+    pa.planned = (total, new, total)
     pa.attention(0, 1, q, out)
     torch.cuda.synchronize()
-    assert torch.all(out == -7.0) and pa.device_status() == 0
+    assert torch.all(out == -7.0) and pa.device_status() == K.DEV_SEQ
+    pa.clear_status()
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")
+    pa.plan(cu_g, cu, total, new, total, lens)
+    assert pa.device_status() == 0
+    for planned in ((total, new, total - 1), (total - 1, new, total - 1), (total, max(1, new - 1), total)):
+        if planned == (total, new, total) or planned[2] < planned[1]:
+            continue
+        pa.planned = planned
+        pa.attention(0, 1, q[:, :planned[0]].contiguous(), out[:, :planned[0]].contiguous())
+        torch.cuda.synchronize()
+        assert pa.device_status() == K.DEV_SEQ
+        pa.clear_status()
+    assert torch.all(out == -7.0)
+    pa.planned = (total, new, total)
+    pa.attention(0, 1, q, out)
+    torch.cuda.synchronize()
+    assert pa.device_status() == 0 and torch.isfinite(out).all() and not (out == -7.0).any()
+
+
+def test_one_workspace_for_plans_of_several_sizes():
+    c = build([300, 150], [[30, 40, 50], [20, 10]], [[3, 2, 1], [1, 4]], **ROT4)
+    cache, lens, cu_g, n = c[0], c[2], c[3], c[4]
+    pa = K.PrefixAttention(cache, 2, 40)
+    for pad in (0, 29, 5, 0):
+        check(cache, lens, cu_g, n, 6, pa=pa, pad=pad)
+    check(cache, lens, cu_g, [1] * 5, 3, pa=pa, pad=1)
+
+
+def test_rows_of_many_sequences_in_several_row_tiles():
+    """Row tiles that cut sequences, and sequences of more than a row tile, in one group."""
+    for D, g, H in ((128, 8, 1), (256, 4, 1), (128, 5, 1)):
+        own = [[9 + (13 * i) % 200 for i in range(12)]]
+        new = [[1 + (5 * i) % 9 if i != 4 else 61 for i in range(12)]]
+        c = build([700], own, new, D=D, H_kv=H, g=g, L=2)
+        check(c[0], c[2], c[3], c[4], c[5])
