@@ -577,28 +577,34 @@ struct CachePos {
   int layer, b, h, T, qe, ce;
 };
 
+// SEG: an own tile's entry of the list, as the loader has left it in shared memory; of the prefix's tiles the unit tells all.
+template <int D, bool SEG>
+__device__ __forceinline__ TileTokens listed_tile(const ChunkArgs& a, const Unit& u, int j, const int4& entry, CachePos& at) {
+  constexpr int NT = chunk_tile(D);
+  TileTokens r;
+  const bool own = j >= u.st;
+  at.layer = u.layer + a.layer0;
+  at.h = u.h;
+  at.b = own ? entry.x : u.b;
+  at.T = own ? entry.z : u.T;
+  at.qe = own ? q_end_of(a.lo, at.T) : u.T;  // a prefix is packed to its end
+  at.ce = 0;
+  r.t0 = own ? entry.y : j * NT;
+  r.v0 = r.t0;
+  r.v1 = min(r.t0 + NT, at.T);
+  return r;
+}
+__device__ __forceinline__ int4 list_entry(const ChunkArgs& a, const Unit& u, int j) {
+  if (j < u.st || j >= u.nt) return make_int4(0, 0, 0, 0);
+  return __ldcg(reinterpret_cast<const int4*>(a.own + u.own + (j - u.st)));
+}
 // Tile j of a unit: its tokens, and where they are.
 template <int D, bool SEG>
-__device__ __forceinline__ TileTokens unit_tile(const ChunkArgs& a, const Unit& u, int j, CachePos& at) {
-  constexpr int NT = chunk_tile(D);
+__device__ __forceinline__ TileTokens unit_tile(const ChunkArgs& a, const Unit& u, int j, CachePos& at, const int4* entry) {
   at.layer = u.layer + a.layer0;
   at.h = u.h;
   if constexpr (SEG) {
-    TileTokens r;
-    at.b = u.b;  // of the prefix: packed to its end
-    at.T = at.qe = u.T;
-    at.ce = 0;
-    r.t0 = j * NT;
-    if (j >= u.st) {
-      const int4 x = __ldcg(reinterpret_cast<const int4*>(a.own + u.own + (j - u.st)));
-      at.b = x.x;
-      at.T = x.z;
-      at.qe = q_end_of(a.lo, x.z);
-      r.t0 = x.y;
-    }
-    r.v0 = r.t0;
-    r.v1 = min(r.t0 + NT, at.T);
-    return r;
+    return listed_tile<D, SEG>(a, u, j, *entry, at);
   } else {
     at.b = u.b;
     at.T = u.T;
@@ -718,24 +724,43 @@ __device__ __forceinline__ void raw_channel_run(const ChunkArgs& a, const CacheP
   for (int j = 0; j < 16; ++j) h[j] = clean<DT>(x[2 * j] | (x[2 * j + 1] << 16), which, nonfinite);
 }
 
-// Window tokens [t0, t1) of a rotated format, turned into the rotated domain by one warp.
+// Window tokens [t0, t1) of a rotated format, turned into the rotated domain by one warp, the next tokens' loads in
+// flight.  (One token at a time, a load's latency each, a tile of 128 window tokens took some 40 us: 8 prompts with 8 beams each behind
+// 16-bit windows 307 us, XXX us like this.)
 template <int D, int DT>
 __device__ __forceinline__ void rotated_window(const ChunkArgs& a, const CachePos& u, int which, int part, uint32_t dst,
                                                int tile0, int a0, int t0, int t1, int lane, volatile uint32_t* nonfinite) {
-  constexpr int NT = chunk_tile(D);
-  for (int t = t0; t < t1; ++t) {
-    if (D == 128 && ((t - a0) >> 5) != part) continue;  // D = 128: the warp's 32 tokens
-    const uint2* p = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t));
+  constexpr int NT = chunk_tile(D), U = 4;
+  const int c = D == 256 ? part : 0;  // D = 256: the warp's 128 channels
+  if (D == 128) {                     // D = 128: its 32 tokens
+    t0 = max(t0, a0 + 32 * part);
+    t1 = min(t1, a0 + 32 * part + 32);
+  }
+  if (t0 >= t1) return;
+  const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
+  const int ch = 128 * c + 4 * lane;
+  const uint32_t col = dst + (uint32_t)(ch >> 6) * NT * 128 + (ch & 4) * 2;
+  uint2 next[U];
+  auto load = [&](int t) {
 #pragma unroll
-    for (int c = 0; c < D / 128; ++c) {
-      if (D == 256 && c != part) continue;  // D = 256: the warp's 128 channels
-      const uint2 w = p[32 * c + lane];
-      const uint32_t w0 = clean<DT>(w.x, which, nonfinite), w1 = clean<DT>(w.y, which, nonfinite);
+    for (int i = 0; i < U; ++i)
+      if (t + i < t1)
+        next[i] = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t + i))[32 * c + lane];
+  };
+  load(t0);
+#pragma unroll 1
+  for (int t = t0; t < t1; t += U) {
+    uint2 now[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) now[i] = next[i];
+    load(t + U);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (t + i >= t1) break;
+      const uint32_t w0 = clean<DT>(now[i].x, which, nonfinite), w1 = clean<DT>(now[i].y, which, nonfinite);
       float v[4] = {in_to_f32((uint16_t)w0, DT), in_to_f32((uint16_t)(w0 >> 16), DT), in_to_f32((uint16_t)w1, DT),
                     in_to_f32((uint16_t)(w1 >> 16), DT)};
-      rotate_lanes(v, lane_signs(a.lo.d1, lane), lane_signs(a.lo.d2, lane));
-      const int ch = 128 * c + 4 * lane;
-      const uint32_t at = dst + (uint32_t)(ch >> 6) * NT * 128 + swz(t - tile0, (ch & 63) >> 3) + (ch & 4) * 2;
+      rotate_lanes(v, s1, s2);
       uint32_t o0, o1;
       if (DT == KVQ_DT_F16 || which) {
         o0 = pack16<DT>(keep_range<DT>(v[0]), keep_range<DT>(v[1]));
@@ -744,7 +769,7 @@ __device__ __forceinline__ void rotated_window(const ChunkArgs& a, const CachePo
         o0 = score_pack(v[0] * a.k_pre, v[1] * a.k_pre);
         o1 = score_pack(v[2] * a.k_pre, v[3] * a.k_pre);
       }
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(o0), "r"(o1) : "memory");
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(col + swz(t + i - tile0, (ch & 63) >> 3)), "r"(o0), "r"(o1) : "memory");
     }
   }
 }
@@ -829,16 +854,23 @@ struct PiecePlace {
   uint32_t blk, codes, step;  // first run's block and codes in the staged piece; to the next run
   uint32_t line, line_step;   // the same in the tile
   uint32_t piece16[4];        // swizzled places of the run's four 16-byte parts
+  int tok;                    // the first run's token of the piece (per-token blocks; the next ones' are 8 apart)
 };
 // False when a block's values leave fp16's range, or its scale is not finite (the piece is then done again).
 // KEY: keys of a bf16 cache, fp16 values times k_pre (`one` is a.k_one); their codes take the factor, exactly.
-template <int DT, bool KEY, int BITS, bool ZP>
-__device__ __forceinline__ bool fill_piece(const PiecePlace& q, uint32_t staged, uint32_t tile, uint32_t one = kOnes) {
+// RAGGED: only the first `valid` tokens of the piece are there (per-token blocks); the others' values are zeros.
+template <int DT, bool KEY, int BITS, bool ZP, bool RAGGED>
+__device__ __forceinline__ bool fill_piece(const PiecePlace& q, uint32_t staged, uint32_t tile, int valid, uint32_t one = kOnes) {
   uint32_t most = 0, blk = staged + q.blk, line = tile + q.line;
+  int tok = RAGGED ? q.tok : 0;
   const uint32_t codes = q.codes - q.blk;
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
-    const uint32_t s16 = lds16(blk), z16 = ZP ? lds16(blk + 2) : 0u;
+    uint32_t s16 = lds16(blk), z16 = ZP ? lds16(blk + 2) : 0u;
+    if constexpr (RAGGED) {
+      if (tok >= valid) s16 = z16 = 0;
+      tok += 8;
+    }
     uint32_t h[16];
     constexpr bool BF = DT == KVQ_DT_BF16 && !KEY && !ZP && BITS < 8;
     codes32<BITS, ZP, BF>(blk + codes, h, KEY ? one : kOnes);
@@ -1105,6 +1137,12 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, uint32_t src_lo, uint32_
 
 struct ChunkShared;
 struct FewShared;
+// SEG: the list's entries of the tiles in flight, written by the loader with a piece: [piece kind][tile mod kChunkBars].  A slot is
+// written again eight tiles later: by then the piece four tiles back has been read, the scores six tiles back are
+// issued, and with them the outputs eight tiles back, whose softmax was the last to look.
+struct TileEntries {
+  int4 at[4 * kChunkBars];
+};
 
 template <int D, int MODE>
 struct ChunkShape {
@@ -1151,12 +1189,14 @@ struct FewShared : ChunkShared {
 // The loader's work for pages whose rows are no whole 16-byte words, or do not divide a subtile: piece
 // by piece, 2 bytes at a time.  A page out of range reads as blocks of scale 0 (and zero 0).
 template <int D, int RT, bool SEG>
-__device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Run& run, bool more, uint32_t raw_at, int lane) {
+__device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Run& run, bool more, uint32_t raw_at, int lane,
+                                         TileEntries* entries) {
   uint32_t kt = 0, slot = 0, n = 0;
   for (; more; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
     for (int j = run.t0; j < run.t1; ++j, ++kt) {
       CachePos u;
-      const TileTokens tt = unit_tile<D, SEG>(a, run.u, j, u);
+      const int4 entry = SEG ? list_entry(a, run.u, j) : make_int4(0, 0, 0, 0);
+      const TileTokens tt = unit_tile<D, SEG>(a, run.u, j, u, &entry);
       for (int piece = 0; piece < 4; ++piece, ++n) {
         const int which = piece >> 1, a0 = tt.t0 + (piece & 1) * (chunk_tile(D) / 2), row = which ? a.lo.vf.row : a.lo.kf.row;
         if (n >= (uint32_t)a.slots) {  // the slot's last piece must have been read
@@ -1179,6 +1219,7 @@ __device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Ru
         if (lane == 0) {
           const int bar = piece * kChunkBars + (kt & (kChunkBars - 1));
           sh.bad_pages[bar] = 0;
+          if (SEG) entries->at[bar] = entry;
           bar_arrive(smem_addr(&sh.raw_full[bar]));
         }
         if (++slot == (uint32_t)a.slots) slot = 0;
@@ -1191,12 +1232,12 @@ __device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Ru
 // call with few arguments (the caller's registers are short), everything else worked out again.
 template <int D, int DT, bool SEG>
 __device__ __forceinline__ void cold_piece(const ChunkArgs& a, ChunkShared& sh, const Run& run, uint32_t tiles_at,
-                                        uint32_t raw_at, int dw, uint32_t kt, uint32_t slot, int j) {
+                                        uint32_t raw_at, int dw, uint32_t kt, uint32_t slot, int j, const TileEntries* entries) {
   constexpr int NT = chunk_tile(D);
   const int piece = dw >> 1, which = dw >> 2, half = piece & 1, part = dw & 1, lane = threadIdx.x & 31;
   const bool per_channel = (which ? a.lo.vf.axis : a.lo.kf.axis) == KVQ_AXIS_CHANNEL;
   CachePos u;
-  const TileTokens tt = unit_tile<D, SEG>(a, run.u, j, u);
+  const TileTokens tt = unit_tile<D, SEG>(a, run.u, j, u, SEG ? &entries->at[piece * kChunkBars + (kt & (kChunkBars - 1))] : nullptr);
   const int a0 = tt.t0 + half * (NT / 2);
   const uint32_t staged = raw_at + slot * a.slot_bytes, bad = sh.bad_pages[piece * kChunkBars + (kt & (kChunkBars - 1))];
   const uint32_t dst = tiles_at + (kt & 1) * (uint32_t)NT * D * 2;
@@ -1760,7 +1801,8 @@ __device__ __forceinline__ float max_across(float (&x)[16], int lane) {
 
 // The softmax warps' work of FEW: two groups of four warps, 16 rows each.
 template <int DT, bool SEG>
-__device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool more, uint8_t* smem, uint32_t tmem) {
+__device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool more, uint8_t* smem, uint32_t tmem,
+                                         const TileEntries* entries) {
   constexpr int D = 128, NT = 128, PR = chunk_part_row(D);
   using C = ChunkShape<D, kChunkFew>;
   const int lane = threadIdx.x & 31;
@@ -1814,10 +1856,13 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
         const int b = (j - t0) & 1;
         int tile0 = (j < st ? j : j + skip) * NT, r_lo = 0, r_hi = 0;  // SEG: rows of the group that see an own tile
         bool masked = tile0 + NT - 1 > p_lo || (a.window && tile0 <= p_hi - a.window && tile0 + NT > a.sinks);
+        const bool here = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
+        ns0 += b ^ 1;
+        ns1 += b;
         if constexpr (SEG) {
           masked = false;  // of the prefix every row sees every token
           if (j >= st) {
-            const int4 x = __ldcg(reinterpret_cast<const int4*>(a.own + run.u.own + (j - st)));
+            const int4 x = entries->at[steps & (kChunkBars - 1)];
             tile0 = x.y;
             r_lo = (x.w & 0xffff) - row0;
             r_hi = (x.w >> 16) - row0;
@@ -1825,9 +1870,6 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
           }
         }
         const uint32_t s_col = lane_base + C::S_COL + b * kFewRows;
-        const bool here = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
-        ns0 += b ^ 1;
-        ns1 += b;
         // -inf where this thread's token is out of a row's view
         auto hide = [&](float (&x)[16]) {
           const int t = tile0 + my, window = a.window ? a.window : 1 << 30;
@@ -2020,6 +2062,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
   constexpr int NT = C::NT, RT = C::RT;
   extern __shared__ uint8_t raw_smem[];
   __shared__ typename C::Shared sh;
+  __shared__ std::conditional_t<SEG, TileEntries, uint32_t> entry_slots;
+  TileEntries* const entries = SEG ? reinterpret_cast<TileEntries*>(&entry_slots) : nullptr;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_at = smem_addr(smem), k_at = q_at + C::FRONT, v_at = k_at + 2 * C::TILE_BYTES;
@@ -2194,7 +2238,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= C::LOAD_WARP && a.direct) {
-    if (warp == C::LOAD_WARP) load_direct<D, RT, SEG>(a, sh, run, more, raw_at, lane);
+    if (warp == C::LOAD_WARP) load_direct<D, RT, SEG>(a, sh, run, more, raw_at, lane, entries);
   } else if (warp >= C::LOAD_WARP) {
     // ---- staging ------------------------------------------------------------------------
     int w = warp;
@@ -2209,7 +2253,13 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     bool ok = true;
     for (; more && ok; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
       CachePos u;
-      TileTokens tt = unit_tile<D, SEG>(a, run.u, run.t0, u);
+      // (entries of the list load two tiles ahead, page ids one)
+      int4 entry = make_int4(0, 0, 0, 0), next_entry = entry;
+      if constexpr (SEG) {
+        entry = list_entry(a, run.u, run.t0);
+        next_entry = list_entry(a, run.u, min(run.t0 + 1, run.t1 - 1));
+      }
+      TileTokens tt = unit_tile<D, SEG>(a, run.u, run.t0, u, &entry);
       ld.unit(a, u);
       const int t1 = run.t1;
       int pid = ld.page_id(a, u, tt.t0, ld.ln);
@@ -2217,7 +2267,9 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       for (int j = run.t0; j < t1; ++j, ++kt) {
         // the next tile's page ids load while this one waits for slots
         CachePos next_u = u;
-        const TileTokens next = SEG ? unit_tile<D, SEG>(a, run.u, min(j + 1, t1 - 1), next_u) : tile_tokens<D>(run.u, min(j + 1, t1 - 1));
+        int4 after_next = next_entry;
+        if constexpr (SEG) after_next = list_entry(a, run.u, min(j + 2, t1 - 1));
+        const TileTokens next = SEG ? unit_tile<D, SEG>(a, run.u, min(j + 1, t1 - 1), next_u, &next_entry) : tile_tokens<D>(run.u, min(j + 1, t1 - 1));
         const int next_pid = ld.page_id(a, next_u, next.t0, ld.ln);
         // A lane works out a copy and notes it; one lane then asks for all of a piece's.  (Operands passed by
         // shuffles took 200 to 500 cycles a copy, queued behind the dequantizing warps' shared-memory
@@ -2249,6 +2301,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           const uint32_t b = __ballot_sync(0xffffffffu, ready), now = (b & 1) | (b >> 15 & 2);
           if (ready) {
             sh.bad_pages[bar] = bads;
+            if (SEG) entries->at[bar] = entry;
             if (bads) atomicOr(a.status, KVQ_DEV_PAGE);
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_addr(&sh.raw_full[bar])),
                          "r"(ld.half ? total1 : total0)
@@ -2277,7 +2330,11 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         if (!ok) break;
         pid = next_pid;
         tt = next;
-        if (SEG) u = next_u;
+        if constexpr (SEG) {
+          u = next_u;
+          entry = next_entry;
+          next_entry = after_next;
+        }
         slot += 4;
         while (slot >= slots) slot -= slots;
       }
@@ -2323,6 +2380,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           int toff, row, run32;
           RunPlace<D>::of(per_channel, part, 0, lane, &toff, &row, &run32);
           RunPlace<D>::at(per_channel, f, a.sub_bytes, toff, row, run32, &q.blk, &q.codes);
+          q.tok = toff;
           q.step = per_channel ? 32 * f.bb : 8 * f.row;
           q.line_step = (per_channel ? 32 : 8) * 128;
           const int tile_row = row + (per_channel ? 0 : half * (NT / 2)), tile_run = run32 + (per_channel ? half * (NT / 64) : 0);
@@ -2339,11 +2397,11 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         for (; j < j1; ++j, ++kt) {
           const uint32_t st = kt & 1, bar = kt & (kChunkBars - 1);
           bool plain = true;
+          int valid = NT / 2;  // SEG: tokens of the piece before the sequence's end
           a1 += NT;
-          if (SEG ? j >= st0 || a1 > safe : j <= st0 || a1 > safe) {
-            CachePos at;
-            const TileTokens tt = SEG ? unit_tile<D, SEG>(a, run.u, j, at) : tile_tokens<D>(run.u, j);
-            const int a0 = tt.t0 + half * (NT / 2), qe = SEG ? at.qe : q_last;
+          if (!SEG && (j <= st0 || a1 > safe)) {
+            const TileTokens tt = tile_tokens<D>(run.u, j);
+            const int a0 = tt.t0 + half * (NT / 2), qe = q_last;
             a1 = a0 + NT / 2;
             if ((a0 < ce) != cold) break;  // the other tier's format
             // of one format, wholly in view (to whole 32-token subtiles) and in range: the common case
@@ -2353,8 +2411,14 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
                                            bar_wait(full_at + 8 * bar, kt / kChunkBars & 1, gave_up));
           if (!ok) break;
           landed = true;
+          if (SEG && j >= st0) {  // the packed tokens alone, or a piece with none of the 16-bit window
+            const int4 entry = entries->at[piece * kChunkBars + bar];
+            const int left = entry.z - entry.y - half * (NT / 2);
+            plain = entry.y + half * (NT / 2) + min(left, NT / 2) <= q_end_of(a.lo, entry.z);
+            valid = min(left, NT / 2);
+          }
           if (!plain || *(volatile uint32_t*)&sh.bad_pages[piece * kChunkBars + bar]) break;
-          if (!fill(raw_at + slot * a.slot_bytes, st * C::TILE_BYTES)) break;
+          if (!fill(raw_at + slot * a.slot_bytes, st * C::TILE_BYTES, valid)) break;
           proxy_fence();
           __syncwarp();
           if (lane == 0) {
@@ -2371,19 +2435,19 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           constexpr bool KEY = decltype(key)::value;
           const uint32_t one = KEY ? a.k_one : kOnes;
           if (kind == 4)
-            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 4, false>(q, staged, dst, one); });
+            stretch([&](uint32_t staged, uint32_t dst, int valid) { return fill_piece<DT, KEY, 4, false, SEG>(q, staged, dst, valid, one); });
           else if (kind == 8)
-            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 8, false>(q, staged, dst, one); });
+            stretch([&](uint32_t staged, uint32_t dst, int valid) { return fill_piece<DT, KEY, 8, false, SEG>(q, staged, dst, valid, one); });
           else if (kind == 2)
-            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 2, false>(q, staged, dst, one); });
+            stretch([&](uint32_t staged, uint32_t dst, int valid) { return fill_piece<DT, KEY, 2, false, SEG>(q, staged, dst, valid, one); });
           else if (kind == 3)
-            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 3, false>(q, staged, dst, one); });
+            stretch([&](uint32_t staged, uint32_t dst, int valid) { return fill_piece<DT, KEY, 3, false, SEG>(q, staged, dst, valid, one); });
           else if (kind == 20)
-            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 4, true>(q, staged, dst, one); });
+            stretch([&](uint32_t staged, uint32_t dst, int valid) { return fill_piece<DT, KEY, 4, true, SEG>(q, staged, dst, valid, one); });
           else if (kind == 18)
-            stretch([&](uint32_t staged, uint32_t dst) { return fill_piece<DT, KEY, 2, true>(q, staged, dst, one); });
+            stretch([&](uint32_t staged, uint32_t dst, int valid) { return fill_piece<DT, KEY, 2, true, SEG>(q, staged, dst, valid, one); });
           else
-            stretch([&](uint32_t, uint32_t) { return false; });
+            stretch([&](uint32_t, uint32_t, int) { return false; });
         };
         if (DT == KVQ_DT_BF16 && which == 0)
           by_kind(std::integral_constant<bool, DT == KVQ_DT_BF16>{});
@@ -2391,7 +2455,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           by_kind(std::false_type{});
         if (!ok || j >= j1) break;
         if (landed) {
-          cold_piece<D, DT, SEG>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j);
+          cold_piece<D, DT, SEG>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j, entries);
           proxy_fence();
           __syncwarp();
           if (lane == 0) {
@@ -2406,10 +2470,11 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
       }
     }
   } else if constexpr (FEW) {
-    few_rows<DT, SEG>(a, sh, more, smem, tmem);
+    few_rows<DT, SEG>(a, sh, more, smem, tmem, entries);
   } else {
     // ---- softmax and outputs -----------------------------------------------------------
     uint32_t ns0 = 0, ns1 = 0, runs = 0, steps_done = 0, syncs = 0;
+    [[maybe_unused]] int tiles_done = 0;  // of the runs before
     asm volatile("" : "+r"(ns0), "+r"(ns1), "+r"(runs), "+r"(steps_done), "+r"(syncs));  // as above
     bool ok = true;
     for (; more && ok; more = warp_run<D, RT, SEG>(a, sh.start, run, 1), ++runs) {
@@ -2485,20 +2550,20 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         const int j = first_tile + (PAIRED ? s >> 1 : s);
         int t0 = (j < st ? j : j + skip) * NT;
         bool masked = t0 + NT - 1 > p_lo || (a.window && t0 <= p_hi - a.window && t0 + NT > a.sinks);
+        const uint32_t s_col = lane_base + C::S_COL + b * NT;
+        ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
+        if (!ok) break;
         RowSeen see = row_sees;
         if constexpr (SEG) {
           masked = false;  // of the prefix every row sees every token
           if (j >= st) {
-            const int4 x = __ldcg(reinterpret_cast<const int4*>(a.own + run.u.own + (j - st)));
+            const int4 x = entries->at[(tiles_done + (j - first_tile)) & (kChunkBars - 1)];
             const int r_lo = x.w & 0xffff, r_hi = x.w >> 16;
             t0 = x.y;
             masked = t0 + NT - 1 > p_lo || r_lo > 0 || r_hi < run.u.rows;
             if (my_row < r_lo || my_row >= r_hi) see.pos = -1;
           }
         }
-        const uint32_t s_col = lane_base + C::S_COL + b * NT;
-        ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
-        if (!ok) break;
         ns0 += b ^ 1;
         ns1 += b;
         tc_fence_after();
@@ -2530,6 +2595,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         if (lane == 0) bar_arrive(smem_addr(&sh.p_full[b]));
         ++steps_done;
       }
+      if constexpr (SEG) tiles_done += run.t1 - first_tile;
       // ---- the run's outputs -----------------------------------------------------------
       if (!ok) break;
       ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.o_full), runs & 1, gave_up));
@@ -2722,7 +2788,7 @@ template <int D, int DT, int MODE, bool SEG = false>
 cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   using C = ChunkShape<D, MODE>;
   // all of the SM's shared memory that the tiles leave is staging
-  const uint32_t all = 227 * 1024 - (uint32_t)sizeof(typename C::Shared);
+  const uint32_t all = 227 * 1024 - (uint32_t)sizeof(typename C::Shared) - (SEG ? (uint32_t)sizeof(TileEntries) : 0);
   const uint32_t left = all - C::FIXED - 16;
   a.slots = (int)(left / a.slot_bytes);
   if (a.slots > kChunkMaxSlots) a.slots = kChunkMaxSlots;

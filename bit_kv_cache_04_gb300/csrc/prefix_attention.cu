@@ -24,7 +24,17 @@ namespace kvq {
 namespace {
 
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanColumns = 2048;  // table columns of a block
+constexpr int kPlanSmall = 1024;  // sequences whose state fits shared memory; more have it in the workspace
+
+// What the plan keeps of every sequence.
+struct SeqState {
+  int32_t *cu, *lens, *n;  // first row; length and new tokens of those that take part, else 0
+  int32_t *owner_n;        // tokens of the rows that begin with this sequence: its own, its group's, or 0
+  int32_t *owner_p;        // the prefix that its group shares
+  int32_t *owner_end;      // the sequence behind the last one of the rows
+  int32_t *unit_at;        // its first unit
+};
+constexpr int kSeqWords = 7;
 
 struct PlanArgs {
   Layout lo;
@@ -32,17 +42,13 @@ struct PlanArgs {
   const int32_t* cu_groups;
   const int32_t* cu_q;
   const int32_t* seq_lens;
-  int n_groups, total_q, max_q, max_group_q, tile, row_tile, n_units, own_tiles;
+  int n_groups, total_q, max_q, max_group_q, tile, row_tile, n_units, own_tiles, columns;
   uint32_t* status;
   int32_t* plan;     // total_q, max_q, max_group_q, n_groups
   uint32_t* ticket;  // blocks that are done; zero between calls
   int32_t* parts;    // [n_groups] INT_MAX less the first column where the group's sequences part, 0: none; zero between calls
-  int32_t* lens;     // [batch] lengths of the sequences that take part, else 0
-  int32_t* n;        // [batch] new tokens of those
-  int32_t* owner_n;  // [batch] tokens of the rows that begin with this sequence: its own, its group's, or 0
-  int32_t* owner_p;  // [batch] the prefix that its group shares
-  int32_t* owner_end;  // [batch] the sequence behind its last one
-  int32_t* unit_at;  // [batch] its first unit
+  int32_t* lens;     // [batch] as SeqState's, for the attention
+  int32_t* seqs;     // [kSeqWords][batch], large batches
   int2* where;
   SharedUnit* units;
   OwnTile* own;
@@ -63,17 +69,6 @@ __device__ __forceinline__ int new_tokens(const PlanArgs& a, int b, int* cu, int
   return n;
 }
 
-// The groups cover the batch, in order.  All threads of a block.
-__device__ __forceinline__ bool groups_in_order(const PlanArgs& a) {
-  bool wrong = false;
-  for (int i = threadIdx.x; i <= a.n_groups; i += kPlanThreads) {
-    const int at = a.cu_groups[i];
-    wrong |= i == 0 ? at != 0 : at < a.cu_groups[i - 1];
-    if (i == a.n_groups) wrong |= at != a.lo.B;
-  }
-  return !__syncthreads_or(wrong);
-}
-
 // Group g's part of the table, columns [j0, j1): the first one where its sequences with new tokens do not hold the same page.
 __device__ __forceinline__ void find_parting(const PlanArgs& a, int g, int j0, int j1) {
   __shared__ int limit, first, live, found;
@@ -82,6 +77,7 @@ __device__ __forceinline__ void find_parting(const PlanArgs& a, int g, int j0, i
     limit = first = found = INT_MAX;
     live = 0;
   }
+  if (b0 < 0 || b1 < b0 || b1 > a.lo.B) return;  // (uniform; the last block says so)
   __syncthreads();
   for (int b = b0 + tid; b < b1; b += kPlanThreads) {
     int cu, T;
@@ -93,10 +89,9 @@ __device__ __forceinline__ void find_parting(const PlanArgs& a, int g, int j0, i
     atomicAdd(&live, 1);
   }
   __syncthreads();
-  if (live < 2) return;
   j1 = min(j1, limit / a.lo.pt);
   const int columns = j1 - j0;
-  if (columns <= 0) return;
+  if (live < 2 || columns <= 0) return;
   // threads side by side take columns; few columns: threads share a column's sequences
   const int32_t* ref = a.table + (int64_t)first * mp;
   const int wide = min((columns + 31) & ~31, kPlanThreads), subs = kPlanThreads / wide, sub = tid / wide;
@@ -119,32 +114,35 @@ __device__ __forceinline__ void find_parting(const PlanArgs& a, int g, int j0, i
   if (tid == 0 && found != INT_MAX) atomicMax(a.parts + g, INT_MAX - found);
 }
 
-// What a group shares: the sequences' lengths and rows, the prefix, and whether taking it in common saves tiles.  A warp.
-__device__ __forceinline__ void plan_group(const PlanArgs& a, int g) {
-  const int lane = threadIdx.x & 31, b0 = a.cu_groups[g], b1 = a.cu_groups[g + 1], gq = a.lo.g, RT = a.row_tile, NT = a.tile;
-  int live = 0, limit = INT_MAX, first = INT_MAX;
+// What group g, sequences [b0, b1), shares: the prefix, and whether taking it in common saves tiles.  A warp.
+__device__ __forceinline__ void plan_group(const PlanArgs& a, const SeqState& q, int g, int b0, int b1) {
+  const int lane = threadIdx.x & 31, gq = a.lo.g, RT = a.row_tile, NT = a.tile;
+  int live = 0, limit = INT_MAX, first = INT_MAX, rows = 0;
   bool bad = false;
+  const int parting = __ldcg(a.parts + g);
   for (int b = b0 + lane; b < b1; b += 32) {
     int cu, T;
     const int n = new_tokens(a, b, &cu, &T, &bad);
-    a.n[b] = n;
-    a.lens[b] = n ? T : 0;
-    a.owner_n[b] = n;
-    a.owner_p[b] = 0;
-    a.owner_end[b] = b + 1;
+    q.cu[b] = cu;
+    q.n[b] = n;
+    q.lens[b] = a.lens[b] = n ? T : 0;
+    q.owner_n[b] = n;
+    q.owner_p[b] = 0;
+    q.owner_end[b] = b + 1;
     if (n) {
       ++live;
+      rows += n;
       limit = min(limit, min(q_end_of(a.lo, T), T - n));
       first = min(first, b);
     }
   }
   live = warp_sum(live);
+  rows = warp_sum(rows);
   limit = __reduce_min_sync(0xffffffffu, limit);
   first = __reduce_min_sync(0xffffffffu, first);
   bad = __any_sync(0xffffffffu, bad);
-  const int parting = __ldcg(a.parts + g);
   if (lane == 0) a.parts[g] = 0;
-  if (!bad && live > 1 && a.cu_q[b1] - a.cu_q[b0] > a.max_group_q) bad = true;
+  if (!bad && live > 1 && rows > a.max_group_q) bad = true;
   if (bad && lane == 0) atomicOr(a.status, KVQ_DEV_LENGTH);
   // (with a sequence out of order the others' rows need not be one run: they go without a common prefix)
   if (bad || live < 2) return;
@@ -153,79 +151,74 @@ __device__ __forceinline__ void plan_group(const PlanArgs& a, int g) {
   if (P == 0) return;
   // tiles taken apart (row tiles of each sequence over all it has cached), and together
   __syncwarp();
-  const int cu0 = a.cu_q[b0];
+  const int cu0 = q.cu[first];
   int64_t apart = 0, together = 0;
-  int rows = 0;
   for (int b = b0 + lane; b < b1; b += 32) {
-    const int n = a.n[b];
+    const int n = q.n[b];
     if (!n) continue;
-    const int tiles = ceil_div(a.lens[b], NT), r0 = (a.cu_q[b] - cu0) * gq, r1 = r0 + n * gq;
+    const int tiles = ceil_div(q.lens[b], NT), r0 = (q.cu[b] - cu0) * gq, r1 = r0 + n * gq;
     apart += (int64_t)ceil_div(n * gq, RT) * tiles;
     together += (int64_t)((r1 - 1) / RT - r0 / RT + 1) * (tiles - P / NT);
-    rows += n * gq;
   }
-  rows = warp_sum(rows);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     apart += __shfl_xor_sync(0xffffffffu, apart, o);
     together += __shfl_xor_sync(0xffffffffu, together, o);
   }
-  together += (int64_t)ceil_div(rows, RT) * (P / NT);
+  together += (int64_t)ceil_div(rows * gq, RT) * (P / NT);
   if (together >= apart) return;
   for (int b = b0 + lane; b < b1; b += 32) {
-    a.owner_n[b] = b == first ? rows / gq : 0;
-    a.owner_p[b] = b == first ? P : 0;
-    a.owner_end[b] = b1;
+    q.owner_n[b] = b == first ? rows : 0;
+    q.owner_p[b] = b == first ? P : 0;
+    q.owner_end[b] = b1;
   }
 }
 
-// Unit i of the list, whose first row and owner are known: its rows, prefix and own tiles.  A warp.
-__device__ __forceinline__ void plan_unit(const PlanArgs& a, int i, int* own_count) {
-  const int lane = threadIdx.x & 31, gq = a.lo.g, NT = a.tile;
-  SharedUnit u = a.units[i];
-  const int b0 = u.first, shared = a.owner_p[b0];
-  u.rows = min(a.row_tile, a.owner_n[b0] * gq - u.r0);
+// Row tile k of the rows that begin with sequence b0, unit i: its rows, prefix and own tiles.  A warp.
+__device__ __forceinline__ void plan_unit(const PlanArgs& a, const SeqState& q, int i, int b0, int k, int* own_count) {
+  const int lane = threadIdx.x & 31, gq = a.lo.g, NT = a.tile, shared = q.owner_p[b0], end = q.owner_end[b0];
+  SharedUnit u;
+  u.cu = q.cu[b0];
+  u.first = b0;
+  u.r0 = k * a.row_tile;
+  u.rows = min(a.row_tile, q.owner_n[b0] * gq - u.r0);
   const int tok0 = u.r0 / gq, tok1 = (u.r0 + u.rows - 1) / gq;  // of the owner's
   if (shared)
     u.prefix = shared;
   else  // one sequence: what all of the rows see of it in the packed tiers
-    u.prefix = min(q_end_of(a.lo, a.lens[b0]), a.lens[b0] - a.n[b0] + tok0 + 1) / NT * NT;
-  const int end = a.owner_end[b0];
-  auto tiles_of = [&](int b, int* p_lo, int* ra, int* rb) {
-    if (b >= end || !a.n[b]) return 0;
-    const int off = a.cu_q[b] - u.cu, n = a.n[b], T = a.lens[b], t0 = max(tok0, off), t1 = min(tok1, off + n - 1);
+    u.prefix = min(q_end_of(a.lo, q.lens[b0]), q.lens[b0] - q.n[b0] + tok0 + 1) / NT * NT;
+  auto tiles_of = [&](int b, int* p_lo, int* rows) {
+    if (b >= end || !q.n[b]) return 0;
+    const int off = q.cu[b] - u.cu, n = q.n[b], T = q.lens[b], t0 = max(tok0, off), t1 = min(tok1, off + n - 1);
     if (t0 > t1) return 0;
-    *ra = max(0, off * gq - u.r0);
-    *rb = min(u.rows, (off + n) * gq - u.r0);
+    *rows = max(0, off * gq - u.r0) | min(u.rows, (off + n) * gq - u.r0) << 16;
     *p_lo = T - n + t0 - off;
     return (T - n + t1 - off) / NT - u.prefix / NT + 1;
   };
   int total = 0, low = INT_MAX;
   for (int b = b0 + lane; b - lane < end; b += 32) {
-    int p = INT_MAX, ra, rb;
-    total += tiles_of(b, &p, &ra, &rb);
+    int p = INT_MAX, rows;
+    total += tiles_of(b, &p, &rows);
     low = min(low, p);
   }
-  total = warp_sum(total);
+  u.n_own = total = warp_sum(total);
   u.p_lo = __reduce_min_sync(0xffffffffu, low);
-  u.n_own = total;
   int at = 0;
   if (lane == 0) at = atomicAdd(own_count, total);  // (which places a unit gets changes no result)
   u.own = at = __shfl_sync(0xffffffffu, at, 0);
   if (at > a.own_tiles - total) u.rows = 0;  // (the list holds all that lengths up to max_T need)
-  __syncwarp();
   if (lane == 0) a.units[i] = u;
   if (u.rows == 0) return;
   for (int b = b0 + lane; b - lane < end; b += 32) {
-    int p, ra = 0, rb = 0;
-    const int mine = tiles_of(b, &p, &ra, &rb);
+    int p, rows = 0;
+    const int mine = tiles_of(b, &p, &rows);
     uint32_t have = __ballot_sync(0xffffffffu, mine > 0);
     while (have) {
       const int src = __ffs(have) - 1;
       have &= have - 1;
       const int count = __shfl_sync(0xffffffffu, mine, src), s = b - lane + src;
-      const int rows = __shfl_sync(0xffffffffu, ra | rb << 16, src), T = a.lens[s];
-      for (int k = lane; k < count; k += 32) a.own[at + k] = OwnTile{s, u.prefix + k * NT, T, rows};
+      const int seen_by = __shfl_sync(0xffffffffu, rows, src), T = q.lens[s];
+      for (int t = lane; t < count; t += 32) a.own[at + t] = OwnTile{s, u.prefix + t * NT, T, seen_by};
       at += count;
     }
   }
@@ -235,11 +228,11 @@ __device__ __forceinline__ void plan_unit(const PlanArgs& a, int i, int* own_cou
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PlanArgs a) {
   __shared__ bool last;
   __shared__ int scan[kPlanWarps], own_count;
+  __shared__ int32_t small[kSeqWords][kPlanSmall];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.lo.B;
   grid_launch_dependents();
   grid_dependency_wait();
-  const bool in_order = groups_in_order(a);
-  if (in_order) find_parting(a, blockIdx.x, blockIdx.y * kPlanColumns, (blockIdx.y + 1) * kPlanColumns);
+  find_parting(a, blockIdx.x, blockIdx.y * a.columns, (blockIdx.y + 1) * a.columns);
   if (tid == 0) {
     __threadfence();
     last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
@@ -248,6 +241,14 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   __syncthreads();
   if (!last) return;
   __threadfence();
+  // the groups cover the batch, in order
+  bool wrong = false;
+  for (int i = tid; i <= a.n_groups; i += kPlanThreads) {
+    const int at = a.cu_groups[i];
+    wrong |= i == 0 ? at != 0 : at < a.cu_groups[i - 1];
+    if (i == a.n_groups) wrong |= at != B;
+  }
+  const bool in_order = !__syncthreads_or(wrong);
   if (tid == 0) {
     *a.ticket = 0;
     a.plan[0] = a.total_q;
@@ -259,16 +260,15 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   }
   int units = 0;
   if (in_order) {
-    for (int g = warp; g < a.n_groups; g += kPlanWarps) plan_group(a, g);
+    SeqState q;
+    int32_t** const field[kSeqWords] = {&q.cu, &q.lens, &q.n, &q.owner_n, &q.owner_p, &q.owner_end, &q.unit_at};
+#pragma unroll
+    for (int i = 0; i < kSeqWords; ++i) *field[i] = B <= kPlanSmall ? small[i] : a.seqs + (int64_t)i * B;
+    for (int g = warp; g < a.n_groups; g += kPlanWarps) plan_group(a, q, g, a.cu_groups[g], a.cu_groups[g + 1]);
     __syncthreads();
-    // positions and sequences of the rows
-    for (int b = warp; b < B; b += kPlanWarps) {
-      const int n = a.n[b], cu = a.cu_q[b], p = a.lens[b] - n;
-      for (int i = lane; i < n; i += 32) a.where[cu + i] = make_int2(p + i, b);
-    }
     // every owner's row tiles
     for (int base = 0; base < B; base += kPlanThreads) {
-      const int b = base + tid, mine = b < B ? ceil_div(a.owner_n[b] * a.lo.g, a.row_tile) : 0;
+      const int b = base + tid, mine = b < B ? ceil_div(q.owner_n[b] * a.lo.g, a.row_tile) : 0;
       int x = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -279,30 +279,36 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       if (lane == 31) scan[warp] = x;
       __syncthreads();
       const int s = scan[lane], before = warp_sum(lane < warp ? s : 0);
-      if (b < B) a.unit_at[b] = units + before + x - mine;
+      if (b < B) q.unit_at[b] = units + before + x - mine;
       units += warp_sum(s);
     }
     units = min(units, a.n_units);
     __syncthreads();
-    for (int b = warp; b < B; b += kPlanWarps) {
-      const int n = ceil_div(a.owner_n[b] * a.lo.g, a.row_tile), at = a.unit_at[b];
-      for (int k = lane; k < n && at + k < a.n_units; k += 32) {
-        SharedUnit u{};
-        u.cu = a.cu_q[b];
-        u.r0 = k * a.row_tile;
-        u.first = b;
-        a.units[at + k] = u;
+    for (int i = warp; i < units; i += kPlanWarps) {
+      int lo = 0, hi = B;  // the last sequence whose units begin at or before i: it has some
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (q.unit_at[mid] <= i)
+          lo = mid;
+        else
+          hi = mid;
       }
+      plan_unit(a, q, i, lo, i - q.unit_at[lo], &own_count);
     }
-    __syncthreads();
-    for (int i = warp; i < units; i += kPlanWarps) plan_unit(a, i, &own_count);
+    // positions and sequences of the rows
+    for (int b = warp; b < B; b += kPlanWarps) {
+      const int n = q.n[b], cu = q.cu[b], p = q.lens[b] - n;
+      for (int i = lane; i < n; i += 32) a.where[cu + i] = make_int2(p + i, b);
+    }
+  } else {
+    for (int g = tid; g < a.n_groups; g += kPlanThreads) a.parts[g] = 0;
   }
   for (int i = units + tid; i < a.n_units; i += kPlanThreads) a.units[i] = SharedUnit{};
 }
 
 // Workspace: that of the chunk attention, then the plan.
 struct PrefixWs {
-  size_t plan, parts, seqs, where, units, own, total, zeroed;
+  size_t plan, parts, lens, seqs, where, units, own, total, zeroed;
   int n_units, own_tiles;
 };
 kvq_status prefix_ws(const kvq_config* c, int n_groups, int64_t rows, PrefixWs* out) {
@@ -314,8 +320,9 @@ kvq_status prefix_ws(const kvq_config* c, int n_groups, int64_t rows, PrefixWs* 
   w.own_tiles = (int)own;
   w.plan = align_up(chunk_workspace_bytes(c, &w.zeroed));
   w.parts = w.plan + kWsAlign;
-  w.seqs = w.parts + align_up(sizeof(int32_t) * (size_t)n_groups);
-  w.where = w.seqs + align_up(sizeof(int32_t) * 6 * (size_t)c->batch);
+  w.lens = w.parts + align_up(sizeof(int32_t) * (size_t)n_groups);
+  w.seqs = w.lens + align_up(sizeof(int32_t) * (size_t)c->batch);
+  w.where = w.seqs + (c->batch > kPlanSmall ? align_up(sizeof(int32_t) * kSeqWords * (size_t)c->batch) : 0);
   w.units = w.where + align_up(sizeof(int2) * (size_t)rows);
   w.own = w.units + align_up(sizeof(SharedUnit) * (size_t)units);
   w.total = w.own + align_up(sizeof(OwnTile) * (size_t)own);
@@ -408,16 +415,15 @@ kvq_status kvq_prefix_plan(const kvq_config* cfg, const int32_t* block_table, co
   a.plan = (int32_t*)(base + w.plan);
   a.ticket = (uint32_t*)(base + w.plan) + 4;
   a.parts = (int32_t*)(base + w.parts);
-  a.lens = (int32_t*)(base + w.seqs);
-  a.n = a.lens + cfg->batch;
-  a.owner_n = a.n + cfg->batch;
-  a.owner_p = a.owner_n + cfg->batch;
-  a.owner_end = a.owner_p + cfg->batch;
-  a.unit_at = a.owner_end + cfg->batch;
+  a.lens = (int32_t*)(base + w.lens);
+  a.seqs = (int32_t*)(base + w.seqs);
   a.where = (int2*)(base + w.where);
   a.units = (SharedUnit*)(base + w.units);
   a.own = (OwnTile*)(base + w.own);
-  const unsigned runs = (unsigned)std::min((cfg->max_T / cfg->page_tokens + kPlanColumns) / kPlanColumns, 65535);
+  // columns of a block: 256, more where that would be more than two blocks an SM
+  const int64_t all = (int64_t)cfg->max_T / cfg->page_tokens + 1, most = std::max<int64_t>(1, 2 * (int64_t)sm_count() / n_groups);
+  a.columns = (int)std::max<int64_t>(256, (all + most - 1) / most);
+  const unsigned runs = (unsigned)((all + a.columns - 1) / a.columns);
   const cudaError_t e = launch_dependent(prefix_plan_kernel, dim3(n_groups, runs), dim3(kPlanThreads), 0, (cudaStream_t)stream, a);
   if (e != cudaSuccess) return cuda_fail(e, "prefix plan kernel");
   return ok();
@@ -460,7 +466,7 @@ kvq_status kvq_prefix_attention(const kvq_config* cfg, const kvq_cache* cache, i
   a.by_warp = 0;
   const char* base = (const char*)workspace;
   a.plan = (const int32_t*)(base + w.plan);
-  a.lens = (const int32_t*)(base + w.seqs);
+  a.lens = (const int32_t*)(base + w.lens);
   a.where = (const int2*)(base + w.where);
   a.units = (const SharedUnit*)(base + w.units);
   a.own = (const OwnTile*)(base + w.own);

@@ -89,17 +89,23 @@ def build(groups, own, new, L=1, H_kv=2, g=4, D=128, seed=0, page_tokens=16, val
 
 
 def shared_of(pa):
-    """The prefix that every group shares, from the plan in the workspace: the longest of its sequences'."""
+    """The prefix that every group shares, from the units of the plan in the workspace."""
     cfg = pa.cache.cfg
-    B = cfg.batch
+    B, (total_q, _, _) = cfg.batch, pa.planned
 
     def up(x):
         return (x + 255) // 256 * 256
 
-    at = up(K.kvq_chunk_workspace_bytes(cfg)) + 256 + up(4 * pa.groups)
-    p = pa.workspace[at:at + 16 * B].view(torch.int32).view(4, B)[3].cpu().numpy()  # lens, new tokens, rows' tokens, prefix
-    cu = pa.cu_groups.tolist()
-    return [int(p[cu[i]:cu[i + 1]].max(initial=0)) for i in range(pa.groups)]
+    at = up(K.kvq_chunk_workspace_bytes(cfg)) + 256 + up(4 * pa.groups) + up(4 * B) + up(8 * total_q)
+    n = total_q * (cfg.H_q // cfg.H_kv) // 128 + B
+    units = pa.workspace[at:at + 32 * n].view(torch.int32).view(n, 8).cpu().numpy()  # first row, row, rows, sequence, prefix, own ..
+    own = pa.workspace[at + up(32 * n):].view(torch.int32)
+    cu, got = pa.cu_groups.tolist(), []
+    for i in range(pa.groups):
+        mine = [u for u in units if u[2] and cu[i] <= u[3] < cu[i + 1]]
+        seqs = {own[4 * (u[5] + k)].item() for u in mine for k in range(u[6])}
+        got.append(int(mine[0][4]) if len(seqs) > len({u[3] for u in mine}) else 0)  # several sequences behind one prefix
+    return got
 
 
 def attend(cache, lens, cu_g, n_new, most, q=None, pad=2, seed=1, pa=None):
