@@ -577,34 +577,52 @@ struct CachePos {
   int layer, b, h, T, qe, ce;
 };
 
-// SEG: an own tile's entry of the list, as the loader has left it in shared memory; of the prefix's tiles the unit tells all.
-template <int D, bool SEG>
-__device__ __forceinline__ TileTokens listed_tile(const ChunkArgs& a, const Unit& u, int j, const int4& entry, CachePos& at) {
+// SEG: a tile's entry says where it is.  Of a unit's `nt` tiles the `n` own ones are spread evenly among those of the prefix, so that every
+// CTA's stretch has its share of them: they cost more (pages of another sequence each, ragged ends, 16-bit windows: 8 prompts with 8 beams each
+// behind 16-bit windows of 128 tokens took XXX us with the own tiles in a row).  The loader goes through the unit, and leaves every
+// tile's entry in shared memory for the other roles.
+struct TileOrder {
+  int own, err;  // own tiles before this one; its place times n, less own times nt
+  __device__ __forceinline__ void start(const Unit& u, int j) {
+    const uint64_t x = (uint64_t)j * (uint32_t)(u.nt - u.st);
+    own = (int)(x / (uint32_t)u.nt);
+    err = (int)(x - (uint64_t)own * (uint32_t)u.nt);
+  }
+  // tile j's entry (rows -1: of the prefix, which every row sees), and on to the next one
+  __device__ __forceinline__ int4 entry(const ChunkArgs& a, const Unit& u, int j, int NT) {
+    const int before = own, n = u.nt - u.st;
+    if (j >= u.nt) return make_int4(0, 0, 0, 0);
+    err -= u.nt - n;  // (err + n may pass 31 bits where both are large)
+    if (err >= 0) {
+      ++own;
+      return __ldcg(reinterpret_cast<const int4*>(a.own + u.own + before));
+    }
+    err += u.nt;
+    return make_int4(u.b, (j - before) * NT, u.T, -1);
+  }
+};
+template <int D>
+__device__ __forceinline__ TileTokens listed_tile(const ChunkArgs& a, const Unit& u, const int4& entry, CachePos& at) {
   constexpr int NT = chunk_tile(D);
   TileTokens r;
-  const bool own = j >= u.st;
   at.layer = u.layer + a.layer0;
   at.h = u.h;
-  at.b = own ? entry.x : u.b;
-  at.T = own ? entry.z : u.T;
-  at.qe = own ? q_end_of(a.lo, at.T) : u.T;  // a prefix is packed to its end
+  at.b = entry.x;
+  at.T = entry.z;
+  at.qe = entry.w < 0 ? at.T : q_end_of(a.lo, at.T);  // a prefix is packed to its end
   at.ce = 0;
-  r.t0 = own ? entry.y : j * NT;
-  r.v0 = r.t0;
+  r.t0 = r.v0 = entry.y;
   r.v1 = min(r.t0 + NT, at.T);
   return r;
 }
-__device__ __forceinline__ int4 list_entry(const ChunkArgs& a, const Unit& u, int j) {
-  if (j < u.st || j >= u.nt) return make_int4(0, 0, 0, 0);
-  return __ldcg(reinterpret_cast<const int4*>(a.own + u.own + (j - u.st)));
-}
+
 // Tile j of a unit: its tokens, and where they are.
 template <int D, bool SEG>
 __device__ __forceinline__ TileTokens unit_tile(const ChunkArgs& a, const Unit& u, int j, CachePos& at, const int4* entry) {
   at.layer = u.layer + a.layer0;
   at.h = u.h;
   if constexpr (SEG) {
-    return listed_tile<D, SEG>(a, u, j, *entry, at);
+    return listed_tile<D>(a, u, *entry, at);
   } else {
     at.b = u.b;
     at.T = u.T;
@@ -1193,9 +1211,11 @@ __device__ __noinline__ void load_direct(const ChunkArgs& a, ChunkShared& sh, Ru
                                          TileEntries* entries) {
   uint32_t kt = 0, slot = 0, n = 0;
   for (; more; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
+    TileOrder order;
+    if (SEG) order.start(run.u, run.t0);
     for (int j = run.t0; j < run.t1; ++j, ++kt) {
       CachePos u;
-      const int4 entry = SEG ? list_entry(a, run.u, j) : make_int4(0, 0, 0, 0);
+      const int4 entry = SEG ? order.entry(a, run.u, j, chunk_tile(D)) : make_int4(0, 0, 0, 0);
       const TileTokens tt = unit_tile<D, SEG>(a, run.u, j, u, &entry);
       for (int piece = 0; piece < 4; ++piece, ++n) {
         const int which = piece >> 1, a0 = tt.t0 + (piece & 1) * (chunk_tile(D) / 2), row = which ? a.lo.vf.row : a.lo.kf.row;
@@ -1462,6 +1482,69 @@ __device__ __forceinline__ bool few_any(int id, bool p) {
   return r != 0;
 }
 
+// The same for 5 to 32 rows by eight warps: rows warp, warp + 8, .. below `rows`, RW of them side by side, so that their loads are in
+// flight together (a part at a time, row after row, the joins of units of 32 rows in 3 parts took 15 us).
+// part(i, r): row r of part i.
+template <int RW, class Part, class Write>
+__device__ __forceinline__ void join_rows(const ChunkArgs& a, int parts, int rows, const Part& part, const Write& write) {
+  constexpr int D = 128, U = 4 / RW;  // parts in flight of each row
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float M[RW], L[RW], acc[RW][1][4];
+#pragma unroll
+  for (int k = 0; k < RW; ++k) {
+    M[k] = -INFINITY;
+    L[k] = acc[k][0][0] = acc[k][0][1] = acc[k][0][2] = acc[k][0][3] = 0.f;
+  }
+#pragma unroll 1
+  for (int i = lane; i - lane < parts; i += 32)
+#pragma unroll
+    for (int k = 0; k < RW; ++k)
+      if (i < parts) M[k] = fmaxf(M[k], __ldcg(part(i, min(warp + 8 * k, rows - 1)) + D));
+#pragma unroll
+  for (int k = 0; k < RW; ++k)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], o));
+#pragma unroll 1
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    float w[RW];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(min(i0 + lane, parts - 1), min(warp + 8 * k, rows - 1)) + D));
+      // a part that saw none of the row's tokens has m = -inf, or the lowest reference, and l = 0
+      const bool none = i0 + lane >= parts || ml.y == 0.f;
+      w[k] = none ? 0.f : ex2(ml.x - M[k]);
+      L[k] += none ? 0.f : w[k] * ml.y;
+    }
+#pragma unroll 1
+    for (int i = 0; i < min(32, parts - i0); i += U) {
+      float4 v[RW][U];
+#pragma unroll
+      for (int k = 0; k < RW; ++k)
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+          v[k][q] = __ldcg(reinterpret_cast<const float4*>(part(min(i0 + i + q, parts - 1), min(warp + 8 * k, rows - 1))) + lane);
+#pragma unroll
+      for (int k = 0; k < RW; ++k)
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const float wk = __shfl_sync(0xffffffffu, w[k], (i + q) & 31);
+          if (i0 + i + q < parts && wk != 0.f) {
+            acc[k][0][0] = fmaf(wk, v[k][q].x, acc[k][0][0]);
+            acc[k][0][1] = fmaf(wk, v[k][q].y, acc[k][0][1]);
+            acc[k][0][2] = fmaf(wk, v[k][q].z, acc[k][0][2]);
+            acc[k][0][3] = fmaf(wk, v[k][q].w, acc[k][0][3]);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < RW; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L[k] += __shfl_xor_sync(0xffffffffu, L[k], o);
+    if (warp + 8 * k < rows) write(warp + 8 * k, acc[k], L[k]);
+  }
+}
+
 // Joins the partial rows of one unit and writes its output rows; all softmax
 // threads.  scratch: 8 rows of D + 4 floats in shared memory.  False once a warp has given up.
 template <int D, int DT, int MODE, bool SEG>
@@ -1538,6 +1621,18 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
     }
     if (fix) add_nonfinite<D, DT, SEG>(a, run, r0, min(r0 + 32, u.rows), 1);
     return true;
+  }
+  if constexpr (SEG && C::FEW) {
+    if (u.rows > 4) {
+      if (u.rows <= 8)
+        join_rows<1>(a, parts, u.rows, part, write);
+      else if (u.rows <= 16)
+        join_rows<2>(a, parts, u.rows, part, write);
+      else
+        join_rows<4>(a, parts, u.rows, part, write);
+      if (fix) add_nonfinite<D, DT, SEG>(a, run, warp, u.rows, 8);
+      return true;
+    }
   }
   // Few rows: `wpr` warps share a row's parts and join their sums in shared memory.
   const int wpr = u.rows >= C::SOFT_WARPS ? 1 : u.rows > C::SOFT_WARPS / 2 ? 1 : u.rows > C::SOFT_WARPS / 4 ? 2 : u.rows > 1 || C::SOFT_WARPS == 4 ? 4 : 8;
@@ -1860,9 +1955,9 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
         ns0 += b ^ 1;
         ns1 += b;
         if constexpr (SEG) {
+          const int4 x = entries->at[steps & (kChunkBars - 1)];
           masked = false;  // of the prefix every row sees every token
-          if (j >= st) {
-            const int4 x = entries->at[steps & (kChunkBars - 1)];
+          if (x.w >= 0) {
             tile0 = x.y;
             r_lo = (x.w & 0xffff) - row0;
             r_hi = (x.w >> 16) - row0;
@@ -2254,10 +2349,12 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
     for (; more && ok; more = warp_run<D, RT, SEG>(a, sh.start, run, 1)) {
       CachePos u;
       // (entries of the list load two tiles ahead, page ids one)
+      TileOrder order;
       int4 entry = make_int4(0, 0, 0, 0), next_entry = entry;
       if constexpr (SEG) {
-        entry = list_entry(a, run.u, run.t0);
-        next_entry = list_entry(a, run.u, min(run.t0 + 1, run.t1 - 1));
+        order.start(run.u, run.t0);
+        entry = order.entry(a, run.u, run.t0, NT);
+        next_entry = order.entry(a, run.u, run.t0 + 1, NT);
       }
       TileTokens tt = unit_tile<D, SEG>(a, run.u, run.t0, u, &entry);
       ld.unit(a, u);
@@ -2268,7 +2365,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         // the next tile's page ids load while this one waits for slots
         CachePos next_u = u;
         int4 after_next = next_entry;
-        if constexpr (SEG) after_next = list_entry(a, run.u, min(j + 2, t1 - 1));
+        if constexpr (SEG) after_next = order.entry(a, run.u, j + 2, NT);
         const TileTokens next = SEG ? unit_tile<D, SEG>(a, run.u, min(j + 1, t1 - 1), next_u, &next_entry) : tile_tokens<D>(run.u, min(j + 1, t1 - 1));
         const int next_pid = ld.page_id(a, next_u, next.t0, ld.ln);
         // A lane works out a copy and notes it; one lane then asks for all of a piece's.  (Operands passed by
@@ -2411,11 +2508,13 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
                                            bar_wait(full_at + 8 * bar, kt / kChunkBars & 1, gave_up));
           if (!ok) break;
           landed = true;
-          if (SEG && j >= st0) {  // the packed tokens alone, or a piece with none of the 16-bit window
+          if (SEG) {
             const int4 entry = entries->at[piece * kChunkBars + bar];
-            const int left = entry.z - entry.y - half * (NT / 2);
-            plain = entry.y + half * (NT / 2) + min(left, NT / 2) <= q_end_of(a.lo, entry.z);
-            valid = min(left, NT / 2);
+            if (entry.w >= 0) {  // packed as far as the sequence goes, or with tokens of the 16-bit window
+              const int left = entry.z - entry.y - half * (NT / 2);
+              plain = entry.y + half * (NT / 2) + min(left, NT / 2) <= q_end_of(a.lo, entry.z);
+              valid = min(left, NT / 2);
+            }
           }
           if (!plain || *(volatile uint32_t*)&sh.bad_pages[piece * kChunkBars + bar]) break;
           if (!fill(raw_at + slot * a.slot_bytes, st * C::TILE_BYTES, valid)) break;
@@ -2555,9 +2654,9 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         if (!ok) break;
         RowSeen see = row_sees;
         if constexpr (SEG) {
+          const int4 x = entries->at[(tiles_done + (j - first_tile)) & (kChunkBars - 1)];
           masked = false;  // of the prefix every row sees every token
-          if (j >= st) {
-            const int4 x = entries->at[(tiles_done + (j - first_tile)) & (kChunkBars - 1)];
+          if (x.w >= 0) {
             const int r_lo = x.w & 0xffff, r_hi = x.w >> 16;
             t0 = x.y;
             masked = t0 + NT - 1 > p_lo || r_lo > 0 || r_hi < run.u.rows;
