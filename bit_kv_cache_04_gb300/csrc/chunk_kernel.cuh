@@ -167,8 +167,8 @@ struct Unit {
   int p_lo, p_hi;        // positions of its first and last token
   int lo;                // first token of the window
   int sink;              // tokens [0, sink) visible besides
-  int st, lo_tile, nt;   // sink tiles (SEG: prefix tiles), first window tile, tiles
-  int seg, own;          // SEG: the unit's number; its own tiles in the list
+  int st, lo_tile, nt;   // sink tiles, first window tile, tiles
+  // of a planned unit (SEG): b and T: the prefix; rt: its number; n: where its own tiles begin in the list; st: prefix tiles
 };
 
 // One CTA's run of a unit: tiles [t0, t1) of it.  Each warp keeps its own in shared memory: registers are short.
@@ -205,20 +205,20 @@ template <int D, int RT>
 __device__ __forceinline__ bool planned_unit(const ChunkArgs& a, int i, Unit& u) {
   constexpr int NT = chunk_tile(D);
   const int4 x = __ldcg(reinterpret_cast<const int4*>(a.units + i)), y = __ldcg(reinterpret_cast<const int4*>(a.units + i) + 1);
-  u.seg = i;
+  u.rt = i;
   u.cu = x.x;
   u.r0 = x.y;
   u.rows = x.z;
   u.b = x.w;
   u.T = y.x;
-  u.own = y.y;
+  u.n = y.y;
   u.p_lo = y.w;
   u.p_hi = u.T - 1;
-  u.n = u.rt = u.lo = u.sink = u.lo_tile = 0;
+  u.lo = u.sink = u.lo_tile = 0;
   u.st = u.T / NT;
   u.nt = u.st + y.z;
   return u.rows > 0 && u.rows <= min(RT, a.most_rows) && u.r0 >= 0 && u.cu >= 0 && u.cu + div_g(a, u.r0 + u.rows - 1) < a.total_q &&
-         (uint32_t)u.b < (uint32_t)a.lo.B && (uint32_t)u.T <= (uint32_t)a.lo.max_T && u.own >= 0 && y.z >= 0 && u.own <= a.own_tiles - y.z && u.nt > 0;
+         (uint32_t)u.b < (uint32_t)a.lo.B && (uint32_t)u.T <= (uint32_t)a.lo.max_T && u.n >= 0 && y.z >= 0 && u.n <= a.own_tiles - y.z && u.nt > 0;
 }
 // Whether the plan is one for the call's sizes: then its units and tiles are where the call looks for them.
 __device__ __forceinline__ bool plan_fits(const ChunkArgs& a) {
@@ -292,7 +292,7 @@ __device__ __forceinline__ bool step_run(const ChunkArgs& a, const LineStart& s,
       if (pos >= s.end) return false;
       pos += cost;
       t0 = 0;
-      int i = u.seg;
+      int i = u.rt;
       do {
         if (++i == a.n_units) {
           i = 0;
@@ -579,7 +579,7 @@ struct CachePos {
 
 // SEG: a tile's entry says where it is.  Of a unit's `nt` tiles the `n` own ones are spread evenly among those of the prefix, so that every
 // CTA's stretch has its share of them: they cost more (pages of another sequence each, ragged ends, 16-bit windows: 8 prompts with 8 beams each
-// behind 16-bit windows of 128 tokens took XXX us with the own tiles in a row).  The loader goes through the unit, and leaves every
+// behind 16-bit windows of 128 tokens took 301 us with the own tiles in a row, 255 us so).  The loader goes through the unit, and leaves every
 // tile's entry in shared memory for the other roles.
 struct TileOrder {
   int own, err;  // own tiles before this one; its place times n, less own times nt
@@ -595,7 +595,7 @@ struct TileOrder {
     err -= u.nt - n;  // (err + n may pass 31 bits where both are large)
     if (err >= 0) {
       ++own;
-      return __ldcg(reinterpret_cast<const int4*>(a.own + u.own + before));
+      return __ldcg(reinterpret_cast<const int4*>(a.own + u.n + before));
     }
     err += u.nt;
     return make_int4(u.b, (j - before) * NT, u.T, -1);
@@ -742,11 +742,77 @@ __device__ __forceinline__ void raw_channel_run(const ChunkArgs& a, const CacheP
   for (int j = 0; j < 16; ++j) h[j] = clean<DT>(x[2 * j] | (x[2 * j + 1] << 16), which, nonfinite);
 }
 
-// Window tokens [t0, t1) of a rotated format, turned into the rotated domain by one warp, the next tokens' loads in
-// flight.  (One token at a time, a load's latency each, a tile of 128 window tokens took some 40 us: 8 prompts with 8 beams each behind
-// 16-bit windows 307 us, XXX us like this.)
+// Window tokens [t0, t1) of a rotated format, turned into the rotated domain by one warp.
 template <int D, int DT>
 __device__ __forceinline__ void rotated_window(const ChunkArgs& a, const CachePos& u, int which, int part, uint32_t dst,
+                                               int tile0, int a0, int t0, int t1, int lane, volatile uint32_t* nonfinite) {
+  constexpr int NT = chunk_tile(D);
+  for (int t = t0; t < t1; ++t) {
+    if (D == 128 && ((t - a0) >> 5) != part) continue;  // D = 128: the warp's 32 tokens
+    const uint2* p = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t));
+#pragma unroll
+    for (int c = 0; c < D / 128; ++c) {
+      if (D == 256 && c != part) continue;  // D = 256: the warp's 128 channels
+      const uint2 w = p[32 * c + lane];
+      const uint32_t w0 = clean<DT>(w.x, which, nonfinite), w1 = clean<DT>(w.y, which, nonfinite);
+      float v[4] = {in_to_f32((uint16_t)w0, DT), in_to_f32((uint16_t)(w0 >> 16), DT), in_to_f32((uint16_t)w1, DT),
+                    in_to_f32((uint16_t)(w1 >> 16), DT)};
+      rotate_lanes(v, lane_signs(a.lo.d1, lane), lane_signs(a.lo.d2, lane));
+      const int ch = 128 * c + 4 * lane;
+      const uint32_t at = dst + (uint32_t)(ch >> 6) * NT * 128 + swz(t - tile0, (ch & 63) >> 3) + (ch & 4) * 2;
+      uint32_t o0, o1;
+      if (DT == KVQ_DT_F16 || which) {
+        o0 = pack16<DT>(keep_range<DT>(v[0]), keep_range<DT>(v[1]));
+        o1 = pack16<DT>(keep_range<DT>(v[2]), keep_range<DT>(v[3]));
+      } else {
+        o0 = score_pack(v[0] * a.k_pre, v[1] * a.k_pre);
+        o1 = score_pack(v[2] * a.k_pre, v[3] * a.k_pre);
+      }
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(o0), "r"(o1) : "memory");
+    }
+  }
+}
+
+// rotate_lanes of U rows side by side: the same operations in the same order, a stage of all rows at a time, so that
+// the rows hide one another's shuffles.
+template <int U>
+__device__ __forceinline__ void rotate_rows(float (&v)[U][4], uint32_t s1, uint32_t s2) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[i][e] = __uint_as_float(__float_as_uint(v[i][e]) ^ ((s1 << (31 - e)) & 0x80000000u));
+    const float a0 = v[i][0] + v[i][1], a1 = v[i][0] - v[i][1], a2 = v[i][2] + v[i][3], a3 = v[i][2] - v[i][3];
+    v[i][0] = a0 + a2;
+    v[i][2] = a0 - a2;
+    v[i][1] = a1 + a3;
+    v[i][3] = a1 - a3;
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const float sign = lane & m ? -1.f : 1.f;
+    float o[U][4];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = __shfl_xor_sync(0xffffffffu, v[i][e], m);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = fmaf(v[i][e], sign, o[i][e]);  // exact: v + o or o - v, rounded once
+  }
+  const float c = hadamard_scale();
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[i][e] = __uint_as_float(__float_as_uint(v[i][e] * c) ^ ((s2 << (31 - e)) & 0x80000000u));
+}
+
+// The same (SEG), four tokens at a time and the next four's loads in flight.  (One token at a time, with a load's and the shuffles' latencies each, a tile of 128 window tokens took
+// some 40 us.  With this and the packed tokens beside it filled in on the hot path, 8 prompts with 8 beams each behind 16-bit
+// windows of 128 tokens went from 255 to 204 us.)
+template <int D, int DT>
+__device__ __forceinline__ void rotated_window4(const ChunkArgs& a, const CachePos& u, int which, int part, uint32_t dst,
                                                int tile0, int a0, int t0, int t1, int lane, volatile uint32_t* nonfinite) {
   constexpr int NT = chunk_tile(D), U = 4;
   const int c = D == 256 ? part : 0;  // D = 256: the warp's 128 channels
@@ -761,33 +827,35 @@ __device__ __forceinline__ void rotated_window(const ChunkArgs& a, const CachePo
   uint2 next[U];
   auto load = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (t + i < t1)
-        next[i] = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t + i))[32 * c + lane];
+    for (int i = 0; i < U; ++i)  // (behind the last token it again)
+      next[i] = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, min(t + i, t1 - 1)))[32 * c + lane];
   };
   load(t0);
 #pragma unroll 1
   for (int t = t0; t < t1; t += U) {
-    uint2 now[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) now[i] = next[i];
-    load(t + U);
+    float v[U][4];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (t + i >= t1) break;
-      const uint32_t w0 = clean<DT>(now[i].x, which, nonfinite), w1 = clean<DT>(now[i].y, which, nonfinite);
-      float v[4] = {in_to_f32((uint16_t)w0, DT), in_to_f32((uint16_t)(w0 >> 16), DT), in_to_f32((uint16_t)w1, DT),
-                    in_to_f32((uint16_t)(w1 >> 16), DT)};
-      rotate_lanes(v, s1, s2);
+      const uint32_t w0 = clean<DT>(next[i].x, which, nonfinite), w1 = clean<DT>(next[i].y, which, nonfinite);
+      v[i][0] = in_to_f32((uint16_t)w0, DT);
+      v[i][1] = in_to_f32((uint16_t)(w0 >> 16), DT);
+      v[i][2] = in_to_f32((uint16_t)w1, DT);
+      v[i][3] = in_to_f32((uint16_t)(w1 >> 16), DT);
+    }
+    load(t + U);
+    rotate_rows(v, s1, s2);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
       uint32_t o0, o1;
       if (DT == KVQ_DT_F16 || which) {
-        o0 = pack16<DT>(keep_range<DT>(v[0]), keep_range<DT>(v[1]));
-        o1 = pack16<DT>(keep_range<DT>(v[2]), keep_range<DT>(v[3]));
+        o0 = pack16<DT>(keep_range<DT>(v[i][0]), keep_range<DT>(v[i][1]));
+        o1 = pack16<DT>(keep_range<DT>(v[i][2]), keep_range<DT>(v[i][3]));
       } else {
-        o0 = score_pack(v[0] * a.k_pre, v[1] * a.k_pre);
-        o1 = score_pack(v[2] * a.k_pre, v[3] * a.k_pre);
+        o0 = score_pack(v[i][0] * a.k_pre, v[i][1] * a.k_pre);
+        o1 = score_pack(v[i][2] * a.k_pre, v[i][3] * a.k_pre);
       }
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(col + swz(t + i - tile0, (ch & 63) >> 3)), "r"(o0), "r"(o1) : "memory");
+      if (t + i < t1)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(col + swz(t + i - tile0, (ch & 63) >> 3)), "r"(o0), "r"(o1) : "memory");
     }
   }
 }
@@ -918,7 +986,7 @@ __device__ __forceinline__ bool fill_piece(const PiecePlace& q, uint32_t staged,
 
 // Half of a piece whose tokens differ in tier, are partly out of view, include pages out of range or the
 // 16-bit window, or whose blocks are TBQ4 or hold values past the range: run by run.
-template <int D, int DT>
+template <int D, int DT, bool SEG>
 __device__ __forceinline__ void mixed_piece(const ChunkArgs& a, const CachePos& u, int which, int half, int part, int lane,
                                          bool per_channel, bool rotated, int a0, int v0, int v1, uint32_t staged,
                                          uint32_t bad, uint32_t dst, int tile0, bool fresh, const uint32_t* pair_table,
@@ -956,8 +1024,11 @@ __device__ __forceinline__ void mixed_piece(const ChunkArgs& a, const CachePos& 
   // the window tokens of this warp's own half: the same rows or channels as its runs
   if (rotated) {
     __syncwarp();
-    rotated_window<D, DT>(a, u, which, part, dst, tile0, a0, max(max(u.qe, a0), v0), min(min(u.T, a0 + NT / 2), v1), lane,
-                          nonfinite);
+    const int w0 = max(max(u.qe, a0), v0), w1 = min(min(u.T, a0 + NT / 2), v1);
+    if constexpr (SEG)
+      rotated_window4<D, DT>(a, u, which, part, dst, tile0, a0, w0, w1, lane, nonfinite);
+    else
+      rotated_window<D, DT>(a, u, which, part, dst, tile0, a0, w0, w1, lane, nonfinite);
   }
   if (per_channel && v1 > max(u.qe, a0)) {
     __syncwarp();
@@ -1264,9 +1335,40 @@ __device__ __forceinline__ void cold_piece(const ChunkArgs& a, ChunkShared& sh, 
   if (which == 0 && (a.lo.flags & KVQ_K_PRE_ROPE))
     turned_piece<D, DT>(a, u, tt, a0, staged, bad, dst, part * 32 + lane, &sh.nonfinite);
   else
-    mixed_piece<D, DT>(a, u, which, half, part, lane, per_channel, (a.lo.flags & (which ? KVQ_ROTATE_V : KVQ_ROTATE_K)) != 0, a0,
+    mixed_piece<D, DT, SEG>(a, u, which, half, part, lane, per_channel, (a.lo.flags & (which ? KVQ_ROTATE_V : KVQ_ROTATE_K)) != 0, a0,
                        tt.v0 & ~31, (tt.v1 + 31) & ~31, staged, bad, dst, tt.t0, which == 1 && kt < 2, sh.pair_table,
                        &sh.nonfinite);
+}
+
+// SEG: a dequantizing warp's share of the 16-bit window's tokens of a piece whose packed tokens it has filled in.
+template <int D, int DT>
+__device__ __forceinline__ void window_tokens(const ChunkArgs& a, ChunkShared& sh, const Run& run, uint32_t tiles_at, int dw,
+                                              uint32_t kt, const TileEntries* entries) {
+  constexpr int NT = chunk_tile(D);
+  const int piece = dw >> 1, which = dw >> 2, half = piece & 1, part = dw & 1, lane = threadIdx.x & 31;
+  CachePos u;
+  const TileTokens tt = listed_tile<D>(a, run.u, entries->at[piece * kChunkBars + (kt & (kChunkBars - 1))], u);
+  const int a0 = tt.t0 + half * (NT / 2), t0 = max(a0, u.qe), t1 = min(a0 + NT / 2, u.T);
+  const uint32_t dst = tiles_at + (kt & 1) * (uint32_t)NT * D * 2;
+  __syncwarp();  // the zeros of its other lanes are there
+  if (a.lo.flags & (which ? KVQ_ROTATE_V : KVQ_ROTATE_K)) {
+    rotated_window4<D, DT>(a, u, which, part, dst, tt.t0, a0, t0, t1, lane, &sh.nonfinite);
+    return;
+  }
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    int toff, row, run32;
+    RunPlace<D>::of(false, part, i, lane, &toff, &row, &run32);
+    if (a0 + toff < t0 || a0 + toff >= t1) continue;
+    uint32_t h[16];
+    raw_token_run<DT>(a, u, which, a0 + toff, run32, &sh.nonfinite, h);
+    if (which == 0) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) h[k] = score_pair<DT>(h[k], a.k_pre);
+    }
+    row += half * (NT / 2);
+    store_run(RunPlace<D>::line_at(dst, row, run32, NT), row, run32, h);
+  }
 }
 
 // Sum over the block's threads of x, and the exclusive prefix.
@@ -1372,7 +1474,7 @@ __device__ __forceinline__ int64_t query_row(const ChunkArgs& a, const Unit& u, 
 // Kinds among window tokens [t0, t1) of this lane's channels (4 lane .. of every 128-chunk): of chunk c, bits
 // 12 c + e: +inf in channel e, + 4: -inf, + 8: NaN.
 template <int D, int DT>
-__device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, int layer, int b, int h, int T, int t0, int t1) {
+__device__ __forceinline__ uint32_t sequence_kinds(const ChunkArgs& a, int layer, int b, int h, int T, int t0, int t1) {
   constexpr uint32_t E = DT == KVQ_DT_F16 ? 0x7c00u : 0x7f80u;
   constexpr int N = D / 128, U = 16 / N;  // loads in flight
   const int lane = threadIdx.x & 31;
@@ -1399,6 +1501,15 @@ __device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, int layer, int
   }
   return kinds;
 }
+template <int D, int DT>
+__device__ __noinline__ uint32_t window_kinds(const ChunkArgs& a, const Run& run, int t0, int t1) {
+  return sequence_kinds<D, DT>(a, run.u.layer, run.u.b, run.u.h, run.u.T, t0, t1);
+}
+// of sequence b of T tokens (SEG)
+template <int D, int DT>
+__device__ __noinline__ uint32_t window_kinds_of(const ChunkArgs& a, const Run& run, int b, int T, int t0, int t1) {
+  return sequence_kinds<D, DT>(a, run.u.layer, b, run.u.h, T, t0, t1);
+}
 // Adds them to the unit's output rows r0, r0 + step, .. below r1, which this warp has written.
 template <int D, int DT, bool SEG>
 __device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Run& run, int r0, int r1, int step) {
@@ -1407,7 +1518,7 @@ __device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Run& run, i
   __syncwarp();
   if (r0 >= r1) return;
   // what every row of the unit sees (SEG: every row of one of its sequences)
-  uint32_t common = SEG ? 0 : window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, 0, u.sink) | window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, lo, u.p_lo + 1);
+  uint32_t common = SEG ? 0 : window_kinds<D, DT>(a, run, 0, u.sink) | window_kinds<D, DT>(a, run, lo, u.p_lo + 1);
   int seq = -1, from = 0, T = 0;  // SEG: the sequence of `common`, its first row's position, its length
 #pragma unroll 1
   for (int r = r0; r < r1; r += step) {
@@ -1419,15 +1530,15 @@ __device__ __noinline__ void add_nonfinite(const ChunkArgs& a, const Run& run, i
         seq = b;
         from = p;
         T = __ldcg(a.lens + b);
-        common = window_kinds<D, DT>(a, u.layer, b, u.h, T, 0, p + 1);
+        common = window_kinds_of<D, DT>(a, run, b, T, 0, p + 1);
       }
-      kinds = common | window_kinds<D, DT>(a, u.layer, b, u.h, T, from + 1, p + 1);
+      kinds = common | window_kinds_of<D, DT>(a, run, b, T, from + 1, p + 1);
     } else {
       const int w = a.window ? max(0, p - a.window + 1) : 0;
       // and the row alone: the sinks that have left its window, what is before and behind the common tokens
-      kinds = common | window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, u.sink, min(a.sinks, w)) |
-              window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, w, min(lo, p + 1)) |
-              window_kinds<D, DT>(a, u.layer, u.b, u.h, u.T, max(u.p_lo + 1, w), p + 1);
+      kinds = common | window_kinds<D, DT>(a, run, u.sink, min(a.sinks, w)) |
+              window_kinds<D, DT>(a, run, w, min(lo, p + 1)) |
+              window_kinds<D, DT>(a, run, max(u.p_lo + 1, w), p + 1);
     }
     uint16_t* out = a.out + query_row(a, u, r) + 4 * (threadIdx.x & 31);
 #pragma unroll 1
@@ -1949,11 +2060,13 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
 #pragma unroll 1
       for (int j = t0; j < t1; ++j, ++steps) {
         const int b = (j - t0) & 1;
-        int tile0 = (j < st ? j : j + skip) * NT, r_lo = 0, r_hi = 0;  // SEG: rows of the group that see an own tile
-        bool masked = tile0 + NT - 1 > p_lo || (a.window && tile0 <= p_hi - a.window && tile0 + NT > a.sinks);
+        int tile0 = (j < st ? j : j + skip) * NT;
+        const uint32_t s_col = lane_base + C::S_COL + b * kFewRows;
         const bool here = __all_sync(0xffffffffu, bar_wait(smem_addr(&sh.s_full[b]), (b ? ns1 : ns0) & 1, gave_up));
         ns0 += b ^ 1;
         ns1 += b;
+        [[maybe_unused]] int r_lo = 0, r_hi = 0;  // SEG: rows of the group that see an own tile
+        bool masked;
         if constexpr (SEG) {
           const int4 x = entries->at[steps & (kChunkBars - 1)];
           masked = false;  // of the prefix every row sees every token
@@ -1963,8 +2076,9 @@ __device__ __forceinline__ void few_rows(const ChunkArgs& a, FewShared& sh, bool
             r_hi = (x.w >> 16) - row0;
             masked = tile0 + NT - 1 > p_lo || r_lo > 0 || r_hi < rows;
           }
+        } else {
+          masked = tile0 + NT - 1 > p_lo || (a.window && tile0 <= p_hi - a.window && tile0 + NT > a.sinks);
         }
-        const uint32_t s_col = lane_base + C::S_COL + b * kFewRows;
         // -inf where this thread's token is out of a row's view
         auto hide = [&](float (&x)[16]) {
           const int t = tile0 + my, window = a.window ? a.window : 1 << 30;
@@ -2486,6 +2600,7 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           for (int k = 0; k < 4; ++k) q.piece16[k] = (((tile_run & 1) * 4 + k) ^ (row & 7)) << 4;
         }
         bool landed = false;
+        [[maybe_unused]] bool filled = false;  // SEG: all but the window's tokens
         // tiles behind the window's first lie in one format and in view up to this token (to whole 32-token subtiles)
         const int st0 = run.u.st, safe = min(cold ? ce : q_last, run.u.p_hi + 32);
         auto stretch = [&](auto fill) {
@@ -2494,7 +2609,8 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
         for (; j < j1; ++j, ++kt) {
           const uint32_t st = kt & 1, bar = kt & (kChunkBars - 1);
           bool plain = true;
-          int valid = NT / 2;  // SEG: tokens of the piece before the sequence's end
+          int valid = NT / 2;  // SEG: packed tokens of the piece (per-token blocks; the others become zeros)
+          [[maybe_unused]] bool raw = false;  // SEG: and tokens of the 16-bit window behind them
           a1 += NT;
           if (!SEG && (j <= st0 || a1 > safe)) {
             const TileTokens tt = tile_tokens<D>(run.u, j);
@@ -2510,14 +2626,18 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           landed = true;
           if (SEG) {
             const int4 entry = entries->at[piece * kChunkBars + bar];
-            if (entry.w >= 0) {  // packed as far as the sequence goes, or with tokens of the 16-bit window
-              const int left = entry.z - entry.y - half * (NT / 2);
-              plain = entry.y + half * (NT / 2) + min(left, NT / 2) <= q_end_of(a.lo, entry.z);
-              valid = min(left, NT / 2);
+            if (entry.w >= 0) {
+              const int a0 = entry.y + half * (NT / 2), qe = q_end_of(a.lo, entry.z);
+              valid = qe - a0;
+              raw = valid < NT / 2 && max(a0, qe) < entry.z;
             }
           }
           if (!plain || *(volatile uint32_t*)&sh.bad_pages[piece * kChunkBars + bar]) break;
           if (!fill(raw_at + slot * a.slot_bytes, st * C::TILE_BYTES, valid)) break;
+          if (SEG && raw) {
+            filled = true;
+            break;
+          }
           proxy_fence();
           __syncwarp();
           if (lane == 0) {
@@ -2554,7 +2674,10 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
           by_kind(std::false_type{});
         if (!ok || j >= j1) break;
         if (landed) {
-          cold_piece<D, DT, SEG>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j, entries);
+          if (SEG && filled)
+            window_tokens<D, DT>(a, sh, run, which ? v_at : k_at, dw, kt, entries);
+          else
+            cold_piece<D, DT, SEG>(a, sh, run, which ? v_at : k_at, raw_at, dw, kt, slot, j, entries);
           proxy_fence();
           __syncwarp();
           if (lane == 0) {
