@@ -9,12 +9,17 @@
 // A row is cut into `splits` blocks so that small batches fill the card too; the group's last block
 // (a ticket; no block waits) joins the pieces and picks the K best in 64 bits.
 //
-// The K largest: a warp keeps its list sorted over its lanes and looks closer at a batch of values only where one passes
-// the list's last or the block's bound (the best of its warps' last ones).  Of n values in random order
-// about K ln(n / K) ever enter a list, so the stream's cost is that of the maximum and the exponentials.
+// The K largest: a warp keeps its list sorted over its lanes.  A value and its place are one 64-bit key (larger value, then lower place),
+// so a comparison decides both.  Of a turn's values (32 a lane) only those at or above a bound are looked at: the block's
+// best known K-th value, in a warp's first turn the K-th of its half lanes' largest, found bit by bit with votes.  Those join the list by
+// rank: every lane counts how many of the few new keys are before its own.  Of n values in random order about K ln(n / K)
+// ever enter a list, so the stream's cost is that of the maximum and the exponentials.
+// (Sorting networks over the warp instead of ranks took 2200 cycles a time, 64-bit floating-point comparisons in the last step
+// 5000: the smallest search 39 us, 20.8 us so; every value offered by itself, unrolled, 144 us for 64 groups of 8 beams over 131072 tokens.)
 #include <algorithm>
 #include <climits>
 #include <cfloat>
+#include <type_traits>
 
 #include "block_codec.cuh"
 #include "kvq_host.cuh"
@@ -30,7 +35,7 @@ constexpr int kMaxVocab = (1 << 26) - 1;  // beam * vocab + token stays below IN
 struct SelectWs {
   uint32_t* tickets;  // [groups], zero between calls
   float2* sums;       // [rows][splits]: maximum, sum of e^(x - maximum)
-  int2* best;         // [rows][splits][beams]: fp32 bits of a logit and its token, descending
+  int64_t* best;      // [rows][splits][beams]: keys of logits and tokens, descending
 };
 
 struct SelectArgs {
@@ -44,54 +49,64 @@ struct SelectArgs {
   int beams, vocab, eos, splits;
 };
 
-// a before b in a list: larger value, then lower place
-template <class V>
-__device__ __forceinline__ bool before(V av, int ai, V bv, int bi) {
-  return av > bv || (av == bv && ai < bi);
-}
-
-// A warp's sorted list, entry i in lane i, and its K-th entry.
-template <class V>
-struct BestList {
-  V v, last_v;
-  int i, last_i;
-  __device__ __forceinline__ void clear(V lowest) {
-    v = last_v = lowest;
-    i = last_i = INT_MAX;
-  }
-  __device__ __forceinline__ bool takes(V x, int at) const { return before(x, at, last_v, last_i); }
-  // x, at: equal in all lanes
-  __device__ __forceinline__ void insert(V x, int at, int beams) {
-    const int lane = threadIdx.x & 31;
-    const int pos = __popc(__ballot_sync(0xffffffffu, before(v, i, x, at)));
-    const V up = __shfl_up_sync(0xffffffffu, v, 1);
-    const int upi = __shfl_up_sync(0xffffffffu, i, 1);
-    if (lane >= pos) {
-      v = lane == pos ? x : up;
-      i = lane == pos ? at : upi;
-    }
-    last_v = __shfl_sync(0xffffffffu, v, beams - 1);
-    last_i = __shfl_sync(0xffffffffu, i, beams - 1);
-  }
-  // the lanes' x where `in`, each if it belongs into the list
-  __device__ __forceinline__ void offer(V x, int at, bool in, int beams) {
-    uint32_t hits = __ballot_sync(0xffffffffu, in && takes(x, at));
-    while (hits) {
-      const int src = __ffs(hits) - 1;
-      hits &= hits - 1;
-      const V xv = __shfl_sync(0xffffffffu, x, src);
-      const int xi = __shfl_sync(0xffffffffu, at, src);
-      if (takes(xv, xi)) insert(xv, xi, beams);
-    }
-  }
-};
-
 // fp32 as an int of the same order
 __device__ __forceinline__ int ordered(float f) {
   const int b = __float_as_int(f);
   return b ^ ((b >> 31) & 0x7fffffff);
 }
 __device__ __forceinline__ float unordered(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7fffffff)); }
+
+// A logit and its token.
+struct LogitKey {
+  int64_t k;
+  __device__ __forceinline__ static LogitKey none() { return LogitKey{INT64_MIN}; }
+  __device__ __forceinline__ static LogitKey of(float v, int token) {
+    return LogitKey{(int64_t)(((uint64_t)(uint32_t)ordered(v + 0.f) << 32) | (uint32_t)~token)};  // (-0 counts as 0)
+  }
+  __device__ __forceinline__ float value() const { return unordered((int)(k >> 32)); }
+  __device__ __forceinline__ int token() const { return (int)~(uint32_t)k; }
+  __device__ __forceinline__ bool before(const LogitKey& o) const { return k > o.k; }
+  __device__ __forceinline__ bool real() const { return k != INT64_MIN; }
+  __device__ __forceinline__ LogitKey of_lane(int l) const { return LogitKey{__shfl_sync(0xffffffffu, k, l)}; }
+};
+// A score, as an integer of the same order, and a place (beam * vocab + token).
+struct alignas(16) ScoreKey {
+  int64_t s;
+  int at, pad;
+  __device__ __forceinline__ static ScoreKey none() { return ScoreKey{INT64_MIN, INT_MAX, 0}; }
+  __device__ __forceinline__ static ScoreKey of(double v, int at) {
+    const int64_t b = __double_as_longlong(v + 0.0);
+    return ScoreKey{b ^ ((b >> 63) & INT64_MAX), at, 0};
+  }
+  __device__ __forceinline__ double value() const { return __longlong_as_double(s ^ ((s >> 63) & INT64_MAX)); }
+  __device__ __forceinline__ bool before(const ScoreKey& o) const { return s > o.s || (s == o.s && at < o.at); }
+  __device__ __forceinline__ bool real() const { return at != INT_MAX; }
+  __device__ __forceinline__ ScoreKey of_lane(int l) const {
+    return ScoreKey{__shfl_sync(0xffffffffu, s, l), __shfl_sync(0xffffffffu, at, l), 0};
+  }
+};
+
+// n <= 32 keys in shared memory join a warp's sorted list (entry i in lane i), by rank; `room`: 32 keys of scratch.
+template <class Key>
+__device__ __forceinline__ void join_found(Key& list, const Key* found, int n, Key* room) {
+  const int lane = threadIdx.x & 31;
+  const Key mine = lane < n ? found[lane] : Key::none();
+  int at_list = lane, at_mine = 0;
+#pragma unroll 2
+  for (int j = 0; j < n; ++j) {
+    const Key c = found[j];
+    const bool b = c.before(list);
+    at_list += b;
+    at_mine += c.before(mine);
+    const int ahead = __popc(__ballot_sync(0xffffffffu, !b));  // entries of the list before it
+    if (lane == j) at_mine += ahead;
+  }
+  __syncwarp();
+  if (at_list < 32) room[at_list] = list;
+  if (lane < n && at_mine < 32) room[at_mine] = mine;
+  __syncwarp();
+  list = room[lane];
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -121,6 +136,44 @@ struct LogitType {
     }
   }
 };
+
+// Natural logarithm, good to 2^-24: the exponent's share in 64 bits, the mantissa's in 32.
+__device__ __forceinline__ double log_of(double x) {
+  const int hi = __double2hiint(x), e = (hi >> 20 & 0x7ff) - 1023;
+  const double f = __hiloint2double((hi & 0xfffff) | 0x3ff00000, __double2loint(x));
+  const float g = (float)f;
+  return e * 0.69314718055994531 + ((double)logf(g) + (double)((float)(f - (double)g) / g));
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {  // of a NaN and a number the number
+  if constexpr (DT == KVQ_DT_BF16) {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// The largest of N words (-inf for NaN alone)
+template <int DT, int N>
+__device__ __forceinline__ float words_max(const uint4 (&w)[N]) {
+  float top = -INFINITY;
+  if constexpr (DT == KVQ_DT_F32) {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      top = fmaxf(top, fmaxf(fmaxf(__uint_as_float(w[u].x), __uint_as_float(w[u].y)),
+                             fmaxf(__uint_as_float(w[u].z), __uint_as_float(w[u].w))));
+  } else {
+    uint32_t p = LogitType<DT>::LOWEST;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      p = pair_max<DT>(p, pair_max<DT>(pair_max<DT>(w[u].x, w[u].y), pair_max<DT>(w[u].z, w[u].w)));
+    float x[LogitType<DT>::PER];
+    LogitType<DT>::widen(make_uint4(p, p, p, p), x);
+    top = fmaxf(top, fmaxf(x[0], x[1]));
+  }
+  return top;
+}
 
 // NaN counts as -inf, +inf as the largest finite number
 __device__ __forceinline__ float tame(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
@@ -163,16 +216,40 @@ __device__ __forceinline__ uint4 straddle(uint4 a, uint4 b, int shift) {
                     __funnelshift_r(x[3], x[4], bits));
 }
 
+constexpr int kWords = 4;  // 16-byte words of a thread in flight, and looked at together
+
 struct SelectShared {
-  int bound;  // ordered(): no value below it is among the block's K largest
+  uint4 words[kSelWarps][32][kWords];  // a warp's values while it looks for candidates among them
+  ScoreKey found[kSelWarps][64];       // (or LogitKeys) on their way into a warp's list
+  ScoreKey room[kSelWarps][32];
+  ScoreKey all[kSelWarps * kMaxBeams];
+  int bound;                           // ordered(): no value below it is among the block's K largest
   float m[kSelWarps], s[kSelWarps];
-  float v[kSelWarps][kMaxBeams];
-  double dv[kSelWarps][kMaxBeams];
-  int i[kSelWarps][kMaxBeams];
   double max[kMaxBeams], log_sum[kMaxBeams], score[kMaxBeams];
   int done[kMaxBeams];
   bool last;
 };
+
+// The warps' lists joined, by rank, into the first K lanes of warp 0.
+template <class Key>
+__device__ __forceinline__ Key join_warps(SelectShared& sh, const Key& list, int K) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Key *const all = reinterpret_cast<Key*>(sh.all), *const out = reinterpret_cast<Key*>(sh.room[0]);
+  __syncthreads();  // what the shared memory held before has been read
+  if (lane < K) all[warp * K + lane] = list;
+  if (threadIdx.x < 32) out[threadIdx.x] = Key::none();
+  __syncthreads();
+  const int n = kSelWarps * K;
+  if ((int)threadIdx.x - lane < n) {
+    const Key mine = (int)threadIdx.x < n ? all[threadIdx.x] : Key::none();
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += all[j].before(mine);
+    if (mine.real() && rank < K) out[rank] = mine;
+  }
+  __syncthreads();
+  return out[lane];
+}
 
 // Words [w0, w1) of a row, counted from its start: the block's maximum, sum and K largest into the workspace.  A warp takes
 // `up` times 32 words side by side, so that a row that starts off a 16-byte boundary has its words put together from the
@@ -182,24 +259,26 @@ template <int DT>
 __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, const char* row, int skew, int w0, int w1,
                                          int64_t piece) {
   using T = LogitType<DT>;
-  constexpr int U = 4;  // words in flight
+  constexpr int U = kWords;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // finite, so that rows of -inf alone sum up to nothing instead of NaN
   float m = -FLT_MAX, s = 0.f;
-  BestList<float> list;
-  list.clear(-INFINITY);
+  LogitKey list = LogitKey::none(), last = list;  // last: the K-th
+  LogitKey *const found = reinterpret_cast<LogitKey*>(sh.found[warp]), *const room = reinterpret_cast<LogitKey*>(sh.room[warp]);
   const int up = min(U, (w1 - w0 + kSelThreads - 1) / kSelThreads), stride = up * kSelThreads;
+  const uint4 none = make_uint4(T::LOWEST, T::LOWEST, T::LOWEST, T::LOWEST);
   uint4 next[U], tail;
   auto load = [&](int w) {
-    tail = make_uint4(T::LOWEST, T::LOWEST, T::LOWEST, T::LOWEST);
+    tail = none;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      next[u] = tail;
+      next[u] = none;
       if (u < up && w + u * 32 < w1 + (skew ? 1 : 0)) next[u] = row_word<DT>(row, skew, a.vocab, w + u * 32);
     }
     if (skew && lane == 0 && w + up * 32 <= w1) tail = row_word<DT>(row, skew, a.vocab, w + up * 32);
   };
   int w = w0 + warp * up * 32 + lane;
+  bool first = true;
   load(w);
 #pragma unroll 1
   for (; w - lane < w1; w += stride) {  // whole warps
@@ -219,55 +298,102 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
         n.w = __shfl_sync(0xffffffffu, n.w, from);
         now[u] = straddle(now[u], n, skew * T::BYTES);
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (w + u * 32 >= w1 || u >= up) now[u] = none;  // the next block's, or another warp's
     }
     load(w + stride);
+    float top = words_max<DT>(now);
+    if (top == INFINITY) top = FLT_MAX;
+    if (top > m) {
+      s *= exp2_approx((m - top) * kLog2e);
+      m = top;
+    }
+    auto sum = [&](auto tamed) {  // x - m is exact where it matters, near the maximum
+      const uint64_t mm = pk2(m, m), c = pk2(kLog2e, kLog2e);
+      uint64_t t = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u >= up) break;
-      if (w + u * 32 >= w1) now[u] = make_uint4(T::LOWEST, T::LOWEST, T::LOWEST, T::LOWEST);  // the next block's
-      float x[T::PER];
-      T::widen(now[u], x);
-      float top = x[0];
-#pragma unroll
-      for (int e = 1; e < T::PER; ++e) top = fmaxf(top, x[e]);  // of a NaN and a number the number
-      if (top == INFINITY) {
-#pragma unroll
-        for (int e = 0; e < T::PER; ++e) x[e] = tame(x[e]);
-        top = FLT_MAX;
-      }
-      if (top > m) {
-        s *= exp2_approx((m - top) * kLog2e);
-        m = top;
-      }
-      auto sum = [&] {  // x - m is exact where it matters, near the maximum
-        const uint64_t mm = pk2(m, m), c = pk2(kLog2e, kLog2e);
-        uint64_t t = 0;
+      for (int u = 0; u < U; ++u) {
+        float x[T::PER];
+        T::widen(now[u], x);
 #pragma unroll
         for (int e = 0; e < T::PER; e += 2) {
+          if constexpr (decltype(tamed)::value) {
+            x[e] = tame(x[e]);
+            x[e + 1] = tame(x[e + 1]);
+          }
           float e0, e1;
           upk2(mul2(sub2(pk2(x[e], x[e + 1]), mm), c), e0, e1);
           t = add2(t, pk2(exp2_approx(e0), exp2_approx(e1)));
         }
-        float t0, t1;
-        upk2(t, t0, t1);
-        return t0 + t1;
-      };
-      float t = sum();
-      if (t != t) {
-#pragma unroll
-        for (int e = 0; e < T::PER; ++e) x[e] = tame(x[e]);
-        top = fmaxf(top, -INFINITY);
-        t = sum();
       }
-      s += t;
-      const float bound = unordered(*(volatile int*)&sh.bound);
-      if (__any_sync(0xffffffffu, top >= list.last_v && top >= bound)) {
-        const int first = (w + u * 32) * T::PER, end = min(a.vocab, w1 * T::PER);
-#pragma unroll
-        for (int e = 0; e < T::PER; ++e) list.offer(x[e], first + e, x[e] >= bound && first + e < end, a.beams);
-        if (lane == 0) atomicMax(&sh.bound, ordered(list.last_v));
+      float t0, t1;
+      upk2(t, t0, t1);
+      return t0 + t1;
+    };
+    float t = sum(std::false_type{});
+    if (!(t <= (float)(U * T::PER))) t = sum(std::true_type{});  // hardly ever: a NaN or an infinity
+    s += t;
+    float bound = unordered(*(volatile int*)&sh.bound);
+    // (behind the first turn values like the K-th have higher places than it)
+    uint32_t hits = __ballot_sync(0xffffffffu, top >= bound && (!last.real() || top > last.value()));
+    if (hits) {
+      if (first) {
+        // K of the 64 half lanes' largest values are at least their K-th: no value below that is among the K best.  (Of 1024 values
+        // some 10 pass for K = 8 and 43 for K = 32.)  The upper 18 bits of the ordered number will do.
+        const uint4 half0[2] = {now[0], now[1]}, half1[2] = {now[2], now[3]};
+        const uint32_t x0 = (uint32_t)ordered(fminf(words_max<DT>(half0), FLT_MAX)) ^ 0x80000000u, x1 = (uint32_t)ordered(fminf(words_max<DT>(half1), FLT_MAX)) ^ 0x80000000u;
+        uint32_t t = 0;
+#pragma unroll 2
+        for (uint32_t bit = 0x80000000u; bit >= 1u << 14; bit >>= 1) {
+          const uint32_t c = t | bit;
+          if (__popc(__ballot_sync(0xffffffffu, x0 >= c)) + __popc(__ballot_sync(0xffffffffu, x1 >= c)) >= a.beams) t = c;
+        }
+        // (bits below -inf's are no number: then all values count)
+        const int o = (int)(t ^ 0x80000000u);
+        if (o > ordered(-INFINITY)) bound = fmaxf(bound, unordered(o));
+        hits = __ballot_sync(0xffffffffu, top >= bound);
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) sh.words[warp][lane][u] = now[u];
+      __syncwarp();
+      // a lane's values side by side over the warp
+      const int u = lane / T::PER, e = lane % T::PER, end = min(a.vocab, w1 * T::PER);
+      int n = 0;  // candidates found
+#pragma unroll 1
+      while (hits) {
+        const int src = __ffs(hits) - 1;
+        hits &= hits - 1;
+        float x = -INFINITY;
+        if (u < up) {
+          const uint32_t raw = reinterpret_cast<const uint32_t*>(sh.words[warp][src])[lane * T::BYTES / 4];
+          if constexpr (DT == KVQ_DT_F32)
+            x = __uint_as_float(raw);
+          else if constexpr (DT == KVQ_DT_BF16)
+            x = __uint_as_float(lane & 1 ? raw & 0xffff0000u : raw << 16);
+          else
+            x = __half2float(__ushort_as_half((uint16_t)(lane & 1 ? raw >> 16 : raw)));
+        }
+        x = tame(x);
+        const int at = (w - lane + src + u * 32) * T::PER + e;
+        const LogitKey key = LogitKey::of(x, at);
+        const bool in = u < up && x >= bound && at < end && key.before(last);
+        const uint32_t pass = __ballot_sync(0xffffffffu, in);
+        if (in) found[n + __popc(pass & ((1u << lane) - 1u))] = key;
+        n += __popc(pass);
+#pragma unroll 1
+        while (n >= 32 || (!hits && n > 0)) {
+          const int take = min(n, 32);
+          n -= take;
+          __syncwarp();
+          join_found(list, found + n, take, room);
+          last = list.of_lane(a.beams - 1);
+        }
+      }
+      __syncwarp();  // (before the words are written again)
+      if (lane == 0 && last.real()) atomicMax(&sh.bound, ordered(last.value()));
     }
+    first = false;
   }
   // the block's
   float wm = m;
@@ -280,16 +406,8 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
     sh.m[warp] = wm;
     sh.s[warp] = s;
   }
-  sh.v[warp][lane] = list.v;
-  sh.i[warp][lane] = list.i;
-  __syncthreads();
+  list = join_warps(sh, list, a.beams);
   if (warp) return;
-#pragma unroll 1
-  for (int k = 1; k < kSelWarps; ++k) {
-    const float v = sh.v[k][lane];
-    const int i = sh.i[k][lane];
-    list.offer(v, i, lane < a.beams && i != INT_MAX, a.beams);
-  }
   const float pm = lane < kSelWarps ? sh.m[lane] : -FLT_MAX, ps = lane < kSelWarps ? sh.s[lane] : 0.f;
   float bm = pm;
 #pragma unroll
@@ -298,7 +416,7 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) bs += __shfl_xor_sync(0xffffffffu, bs, o);
   if (lane == 0) a.ws.sums[piece] = make_float2(bm, bs);
-  if (lane < a.beams) a.ws.best[piece * a.beams + lane] = make_int2(__float_as_int(list.v), list.i);
+  if (lane < a.beams) a.ws.best[piece * a.beams + lane] = list.k;
   __threadfence();  // before the ticket
   __syncwarp();
 }
@@ -330,34 +448,50 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh
       sh.done[b] = done;
       // apart, so that rows of the type's lowest value keep their log-sum
       sh.max[b] = (double)m;
-      sh.log_sum[b] = sum > 0 ? log(sum) : 0.0;  // nothing may follow: every candidate is -inf all the same
+      sh.log_sum[b] = sum > 0 ? log_of(sum) : 0.0;  // nothing may follow: every candidate is -inf all the same
       sh.score[b] = (double)tame(a.scores[row0 + b]);
     }
   }
   __syncthreads();
-  BestList<double> list;
-  list.clear(-(double)INFINITY);
+  // 32 candidates a warp at a time, those before its K-th so far
+  ScoreKey list = ScoreKey::none(), last = list;
+  ScoreKey* const found = sh.found[warp];
+  const int N = K * S * K;
+  const int64_t* from = a.ws.best + row0 * S * K;
+  int64_t next = INT64_MIN;
+  if (warp * 32 + lane < N) next = __ldcg(from + warp * 32 + lane);
+  int n = 0;
 #pragma unroll 1
-  for (int q = warp; q < K * S; q += kSelWarps) {
-    const int b = q / S;
-    if (sh.done[b]) {
-      if (q == b * S) list.offer(sh.score[b], b * a.vocab + a.eos, lane == 0, K);
-      continue;
+  for (int c0 = warp * 32; c0 < N; c0 += kSelThreads) {
+    const LogitKey e{next};
+    next = INT64_MIN;
+    if (c0 + kSelThreads + lane < N) next = __ldcg(from + c0 + kSelThreads + lane);
+    const int c = c0 + lane, b = min(c / (S * K), K - 1);
+    ScoreKey x = ScoreKey::none();
+    if (c < N && sh.done[b]) {  // one candidate
+      if (c == b * S * K) x = ScoreKey::of(sh.score[b], b * a.vocab + a.eos);
+    } else if (e.real()) {
+      x = ScoreKey::of(sh.score[b] + (((double)e.value() - sh.max[b]) - sh.log_sum[b]), b * a.vocab + e.token());
     }
-    int2 e = make_int2(0, INT_MAX);
-    if (lane < K) e = __ldcg(a.ws.best + ((row0 + b) * S + (q - b * S)) * K + lane);
-    const double c = sh.score[b] + (((double)__int_as_float(e.x) - sh.max[b]) - sh.log_sum[b]);
-    list.offer(c, b * a.vocab + e.y, e.y != INT_MAX, K);
-  }
-  sh.dv[warp][lane] = list.v;
-  sh.i[warp][lane] = list.i;
-  __syncthreads();
-  if (warp) return;
+    const bool in = x.before(last);
+    const uint32_t pass = __ballot_sync(0xffffffffu, in);
+    if (in) found[n + __popc(pass & ((1u << lane) - 1u))] = x;
+    n += __popc(pass);
+    const bool end = c0 + kSelThreads >= N;
 #pragma unroll 1
-  for (int k = 1; k < kSelWarps; ++k) list.offer(sh.dv[k][lane], sh.i[k][lane], lane < K && sh.i[k][lane] != INT_MAX, K);
+    while (n >= 32 || (end && n > 0)) {
+      const int take = min(n, 32);
+      n -= take;
+      __syncwarp();
+      join_found(list, found + n, take, sh.room[warp]);
+      last = list.of_lane(K - 1);
+    }
+  }
+  list = join_warps(sh, list, K);
+  if (warp) return;
   if (lane < K) {
-    const int b = list.i / a.vocab, t = list.i - b * a.vocab;
-    a.scores_out[row0 + lane] = (float)list.v;
+    const int b = list.at / a.vocab, t = list.at - b * a.vocab;
+    a.scores_out[row0 + lane] = (float)list.value();
     a.tokens[row0 + lane] = t;
     a.parents[row0 + lane] = b;
     if (a.done_out) a.done_out[row0 + lane] = sh.done[b] || t == a.eos;
@@ -391,21 +525,21 @@ __global__ void __launch_bounds__(kSelThreads, 3) beam_select_kernel(const __gri
   join_group(a, sh, group);
 }
 
-// Blocks a row: about one wave of four blocks an SM, each with at least 2048 logits to read.
-int splits_of(int64_t rows, int vocab) {
+// Blocks a row: about one wave of four blocks an SM, each with at least 2048 logits to read; at most 4096 candidates a group.
+int splits_of(int64_t rows, int beams, int vocab) {
   const int64_t want = (int64_t)sm_count() * 4 / std::max<int64_t>(1, rows);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)vocab / 2048, 1024}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)vocab / 2048, (int64_t)4096 / (beams * beams)}));
 }
 
 size_t select_ws(int groups, int beams, int vocab, void* base, SelectWs* w) {
-  const int64_t rows = (int64_t)groups * beams, pieces = rows * splits_of(rows, vocab);
+  const int64_t rows = (int64_t)groups * beams, pieces = rows * splits_of(rows, beams, vocab);
   const size_t sums = align_up(sizeof(uint32_t) * (size_t)groups), best = sums + align_up(sizeof(float2) * (size_t)pieces);
   if (w) {
     w->tickets = (uint32_t*)base;
     w->sums = (float2*)((char*)base + sums);
-    w->best = (int2*)((char*)base + best);
+    w->best = (int64_t*)((char*)base + best);
   }
-  return best + align_up(sizeof(int2) * (size_t)pieces * beams);
+  return best + align_up(sizeof(int64_t) * (size_t)pieces * beams);
 }
 
 kvq_status check_select(int32_t groups, int32_t beams, int32_t vocab) {
@@ -479,7 +613,7 @@ kvq_status kvq_beam_select(const void* logits, int32_t dtype, int64_t group_stri
   a.vocab = vocab;
   a.eos = eos;
   const int64_t rows = (int64_t)n_groups * beams;
-  a.splits = splits_of(rows, vocab);
+  a.splits = splits_of(rows, beams, vocab);
   select_ws(n_groups, beams, vocab, workspace, &a.ws);
   const dim3 grid((unsigned)(rows * a.splits));
   cudaStream_t s = (cudaStream_t)stream;

@@ -138,6 +138,38 @@ def test_ties_go_to_the_lowest_place(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_zeros_of_both_signs(dtype):
+    x = torch.full((1, 3, 900), -1.0, device="cuda")
+    x[0, :, 100:140:2], x[0, :, 101:140:2] = 0.0, -0.0
+    s = torch.tensor([[0.0, -0.0, 0.0]], device="cuda")
+    got = check(x.to(TYPES[dtype]), s)
+    assert got[1].tolist() == [[100, 101, 102]] and got[2].tolist() == [[0, 0, 0]]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B", [4, 32])
+def test_many_infinities_and_few_tokens_left(dtype, B):
+    """Every lane holds a value past the finite ones; and rows of which hardly anything may follow."""
+    x, s = random(3, B, 9000, dtype, seed=B)
+    x[0, 0, ::5] = float("inf")
+    x[1, :, 7:] = -float("inf")
+    x[2, :, :] = -float("inf")
+    x[2, B // 2, 8999] = 3.0
+    check(x, s)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("order", ["rising", "falling", "equal"])
+def test_rows_in_order(dtype, order):
+    """Rising rows pass every bound; falling ones are done with the first turn; in equal ones places decide."""
+    for B in (8, 32):
+        x = torch.arange(20000, device="cuda").float() / 2000 - 5
+        x = x.flip(0) if order == "falling" else x * 0 if order == "equal" else x
+        x = x.to(TYPES[dtype]).expand(2, B, 20000).contiguous()
+        check(x, torch.linspace(-3, -1, 2 * B, device="cuda").view(2, B))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_finished_beams(dtype):
     G, B, V = 4, 5, 2500
     x, s = random(G, B, V, dtype, seed=4)
