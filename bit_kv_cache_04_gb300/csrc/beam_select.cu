@@ -79,7 +79,7 @@ struct alignas(16) ScoreKey {
     return ScoreKey{b ^ ((b >> 63) & INT64_MAX), at, 0};
   }
   __device__ __forceinline__ double value() const { return __longlong_as_double(s ^ ((s >> 63) & INT64_MAX)); }
-  __device__ __forceinline__ bool before(const ScoreKey& o) const { return s > o.s || (s == o.s && at < o.at); }
+  __device__ __forceinline__ bool before(const ScoreKey& o) const { return (s > o.s) | ((s == o.s) & (at < o.at)); }
   __device__ __forceinline__ bool real() const { return at != INT_MAX; }
   __device__ __forceinline__ ScoreKey of_lane(int l) const {
     return ScoreKey{__shfl_sync(0xffffffffu, s, l), __shfl_sync(0xffffffffu, at, l), 0};
@@ -200,6 +200,19 @@ __device__ __forceinline__ uint4 row_word(const char* row, int skew, int vocab, 
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// The same into shared memory, whole words of the row asynchronously (one group a turn, see scan_row).
+template <int DT>
+__device__ __forceinline__ void fetch_word(uint4* to, const char* row, int skew, int vocab, int w) {
+  using T = LogitType<DT>;
+  const int first = w * T::PER - skew;
+  if (first >= 0 && first + T::PER <= vocab)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(row + (int64_t)first * T::BYTES)
+                 : "memory");
+  else
+    *to = row_word<DT>(row, skew, vocab, w);
+}
+
 // 16 bytes from byte `shift` of (a, b) on; shift is the same in all lanes.
 __device__ __forceinline__ uint4 straddle(uint4 a, uint4 b, int shift) {
   uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -219,10 +232,12 @@ __device__ __forceinline__ uint4 straddle(uint4 a, uint4 b, int shift) {
 constexpr int kWords = 4;  // 16-byte words of a thread in flight, and looked at together
 
 struct SelectShared {
-  uint4 words[kSelWarps][32][kWords];  // a warp's values while it looks for candidates among them
-  ScoreKey found[kSelWarps][64];       // (or LogitKeys) on their way into a warp's list
+  uint4 words[kSelWarps][2][kWords * 32 + 1];  // a warp's turn, and the next one on its way
+  union {
+    ScoreKey found[kSelWarps][64];             // (or LogitKeys) on their way into a warp's list
+    ScoreKey all[kSelWarps * kMaxBeams];
+  };
   ScoreKey room[kSelWarps][32];
-  ScoreKey all[kSelWarps * kMaxBeams];
   int bound;                           // ordered(): no value below it is among the block's K largest
   float m[kSelWarps], s[kSelWarps];
   double max[kMaxBeams], log_sum[kMaxBeams], score[kMaxBeams];
@@ -267,42 +282,32 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
   LogitKey *const found = reinterpret_cast<LogitKey*>(sh.found[warp]), *const room = reinterpret_cast<LogitKey*>(sh.room[warp]);
   const int up = min(U, (w1 - w0 + kSelThreads - 1) / kSelThreads), stride = up * kSelThreads;
   const uint4 none = make_uint4(T::LOWEST, T::LOWEST, T::LOWEST, T::LOWEST);
-  uint4 next[U], tail;
-  auto load = [&](int w) {
-    tail = none;
+  auto fetch = [&](int w, int slot) {  // (aligned words: one more where the row lies off the boundary)
+    uint4* to = sh.words[warp][slot];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      next[u] = none;
-      if (u < up && w + u * 32 < w1 + (skew ? 1 : 0)) next[u] = row_word<DT>(row, skew, a.vocab, w + u * 32);
-    }
-    if (skew && lane == 0 && w + up * 32 <= w1) tail = row_word<DT>(row, skew, a.vocab, w + up * 32);
+    for (int u = 0; u < U; ++u)
+      if (u < up && w + u * 32 < w1 + (skew ? 1 : 0)) fetch_word<DT>(to + u * 32 + lane, row, skew, a.vocab, w + u * 32);
+    if (skew && lane == 0 && w + up * 32 <= w1) fetch_word<DT>(to + up * 32, row, skew, a.vocab, w + up * 32);
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
-  int w = w0 + warp * up * 32 + lane;
+  int w = w0 + warp * up * 32 + lane, slot = 0;
   bool first = true;
-  load(w);
+  fetch(w, 0);
 #pragma unroll 1
-  for (; w - lane < w1; w += stride) {  // whole warps
+  for (; w - lane < w1; w += stride, slot ^= 1) {  // whole warps
+    fetch(w + stride, slot ^ 1);
+    asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    __syncwarp();
+    const uint4* const in_slot = sh.words[warp][slot];
     uint4 now[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) now[u] = next[u];
-    if (skew) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool end = u + 1 == U || u + 1 == up;
-        uint4 n = next[u];
-        if (lane == 0) n = end ? tail : next[u + 1 < U ? u + 1 : u];
-        const int from = (lane + 1) & 31;
-        n.x = __shfl_sync(0xffffffffu, n.x, from);
-        n.y = __shfl_sync(0xffffffffu, n.y, from);
-        n.z = __shfl_sync(0xffffffffu, n.z, from);
-        n.w = __shfl_sync(0xffffffffu, n.w, from);
-        now[u] = straddle(now[u], n, skew * T::BYTES);
+    for (int u = 0; u < U; ++u) {
+      now[u] = none;  // (the next block's, or another warp's)
+      if (u < up && w + u * 32 < w1) {
+        now[u] = in_slot[u * 32 + lane];
+        if (skew) now[u] = straddle(now[u], in_slot[u * 32 + lane + 1], skew * T::BYTES);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (w + u * 32 >= w1 || u >= up) now[u] = none;  // the next block's, or another warp's
     }
-    load(w + stride);
     float top = words_max<DT>(now);
     if (top == INFINITY) top = FLT_MAX;
     if (top > m) {
@@ -338,6 +343,8 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
     // (behind the first turn values like the K-th have higher places than it)
     uint32_t hits = __ballot_sync(0xffffffffu, top >= bound && (!last.real() || top > last.value()));
     if (hits) {
+      // of lanes with -inf alone only the lowest places matter, and only as long as the list is not full
+      if (first) hits &= __ballot_sync(0xffffffffu, top > -INFINITY) | (uint32_t)((1ull << (a.beams + T::PER - 1) / T::PER) - 1);
       if (first) {
         // K of the 64 half lanes' largest values are at least their K-th: no value below that is among the K best.  (Of 1024 values
         // some 10 pass for K = 8 and 43 for K = 32.)  The upper 18 bits of the ordered number will do.
@@ -352,11 +359,8 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
         // (bits below -inf's are no number: then all values count)
         const int o = (int)(t ^ 0x80000000u);
         if (o > ordered(-INFINITY)) bound = fmaxf(bound, unordered(o));
-        hits = __ballot_sync(0xffffffffu, top >= bound);
+        hits &= __ballot_sync(0xffffffffu, top >= bound);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) sh.words[warp][lane][u] = now[u];
-      __syncwarp();
       // a lane's values side by side over the warp
       const int u = lane / T::PER, e = lane % T::PER, end = min(a.vocab, w1 * T::PER);
       int n = 0;  // candidates found
@@ -366,13 +370,13 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
         hits &= hits - 1;
         float x = -INFINITY;
         if (u < up) {
-          const uint32_t raw = reinterpret_cast<const uint32_t*>(sh.words[warp][src])[lane * T::BYTES / 4];
+          const int i = (u * 32 + src) * T::PER + e + skew;
           if constexpr (DT == KVQ_DT_F32)
-            x = __uint_as_float(raw);
+            x = reinterpret_cast<const float*>(in_slot)[i];
           else if constexpr (DT == KVQ_DT_BF16)
-            x = __uint_as_float(lane & 1 ? raw & 0xffff0000u : raw << 16);
+            x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(in_slot)[i] << 16);
           else
-            x = __half2float(__ushort_as_half((uint16_t)(lane & 1 ? raw >> 16 : raw)));
+            x = __half2float(reinterpret_cast<const __half*>(in_slot)[i]);
         }
         x = tame(x);
         const int at = (w - lane + src + u * 32) * T::PER + e;
@@ -390,10 +394,10 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
           last = list.of_lane(a.beams - 1);
         }
       }
-      __syncwarp();  // (before the words are written again)
       if (lane == 0 && last.real()) atomicMax(&sh.bound, ordered(last.value()));
     }
     first = false;
+    __syncwarp();  // before the slot is written again
   }
   // the block's
   float wm = m;
@@ -473,6 +477,15 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh
     } else if (e.real()) {
       x = ScoreKey::of(sh.score[b] + (((double)e.value() - sh.max[b]) - sh.log_sum[b]), b * a.vocab + e.token());
     }
+    // of a first 32 only those that may be among their K best: at or above a bound found bit by bit, as above
+    if (c0 < kSelThreads) {
+      const uint32_t hi = (uint32_t)(x.s >> 32) ^ 0x80000000u;
+      uint32_t t = 0;
+#pragma unroll 2
+      for (uint32_t bit = 0x80000000u; bit >= 1u << 8; bit >>= 1)
+        if (__popc(__ballot_sync(0xffffffffu, hi >= (t | bit))) >= K) t |= bit;
+      if (hi < t) x = ScoreKey::none();
+    }
     const bool in = x.before(last);
     const uint32_t pass = __ballot_sync(0xffffffffu, in);
     if (in) found[n + __popc(pass & ((1u << lane) - 1u))] = x;
@@ -499,7 +512,7 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kSelThreads, 3) beam_select_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const __grid_constant__ SelectArgs a) {
   using T = LogitType<DT>;
   __shared__ SelectShared sh;
   const int64_t row = blockIdx.x / (uint32_t)a.splits;
