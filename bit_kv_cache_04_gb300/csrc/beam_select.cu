@@ -86,6 +86,25 @@ struct alignas(16) ScoreKey {
   }
 };
 
+// A number that at least K of the lanes' N (each) are not below: the K-th largest's upper 14 bits, two at a time.
+template <int N>
+__device__ __forceinline__ uint32_t bound_of(const uint32_t (&x)[N], int K) {
+  uint32_t t = 0;
+  auto enough = [&](uint32_t c) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popc(__ballot_sync(0xffffffffu, x[i] >= c));
+    return n >= K;
+  };
+#pragma unroll 1
+  for (int at = 30; at >= 18; at -= 2) {
+    const uint32_t c1 = t | 1u << at, c2 = t | 2u << at, c3 = t | 3u << at;
+    const bool e1 = enough(c1), e2 = enough(c2), e3 = enough(c3);
+    t = e3 ? c3 : e2 ? c2 : e1 ? c1 : t;
+  }
+  return t;
+}
+
 // n <= 32 keys in shared memory join a warp's sorted list (entry i in lane i), by rank; `room`: 32 keys of scratch.
 template <class Key>
 __device__ __forceinline__ void join_found(Key& list, const Key* found, int n, Key* room) {
@@ -234,7 +253,7 @@ constexpr int kWords = 4;  // 16-byte words of a thread in flight, and looked at
 struct SelectShared {
   uint4 words[kSelWarps][2][kWords * 32 + 1];  // a warp's turn, and the next one on its way
   union {
-    ScoreKey found[kSelWarps][64];             // (or LogitKeys) on their way into a warp's list
+    ScoreKey found[kSelWarps][64];             // (or 128 LogitKeys) on their way into a warp's list: 31, and two lanes' 32
     ScoreKey all[kSelWarps * kMaxBeams];
   };
   ScoreKey room[kSelWarps][32];
@@ -347,15 +366,11 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
       if (first) hits &= __ballot_sync(0xffffffffu, top > -INFINITY) | (uint32_t)((1ull << (a.beams + T::PER - 1) / T::PER) - 1);
       if (first) {
         // K of the 64 half lanes' largest values are at least their K-th: no value below that is among the K best.  (Of 1024 values
-        // some 10 pass for K = 8 and 43 for K = 32.)  The upper 18 bits of the ordered number will do.
+        // some 10 pass for K = 8 and 43 for K = 32.)
         const uint4 half0[2] = {now[0], now[1]}, half1[2] = {now[2], now[3]};
-        const uint32_t x0 = (uint32_t)ordered(fminf(words_max<DT>(half0), FLT_MAX)) ^ 0x80000000u, x1 = (uint32_t)ordered(fminf(words_max<DT>(half1), FLT_MAX)) ^ 0x80000000u;
-        uint32_t t = 0;
-#pragma unroll 2
-        for (uint32_t bit = 0x80000000u; bit >= 1u << 14; bit >>= 1) {
-          const uint32_t c = t | bit;
-          if (__popc(__ballot_sync(0xffffffffu, x0 >= c)) + __popc(__ballot_sync(0xffffffffu, x1 >= c)) >= a.beams) t = c;
-        }
+        const uint32_t x[2] = {(uint32_t)ordered(fminf(words_max<DT>(half0), FLT_MAX)) ^ 0x80000000u,
+                               (uint32_t)ordered(fminf(words_max<DT>(half1), FLT_MAX)) ^ 0x80000000u};
+        const uint32_t t = bound_of(x, a.beams);
         // (bits below -inf's are no number: then all values count)
         const int o = (int)(t ^ 0x80000000u);
         if (o > ordered(-INFINITY)) bound = fmaxf(bound, unordered(o));
@@ -364,10 +379,7 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
       // a lane's values side by side over the warp
       const int u = lane / T::PER, e = lane % T::PER, end = min(a.vocab, w1 * T::PER);
       int n = 0;  // candidates found
-#pragma unroll 1
-      while (hits) {
-        const int src = __ffs(hits) - 1;
-        hits &= hits - 1;
+      auto look = [&](int src) {
         float x = -INFINITY;
         if (u < up) {
           const int i = (u * 32 + src) * T::PER + e + skew;
@@ -378,13 +390,26 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
           else
             x = __half2float(reinterpret_cast<const __half*>(in_slot)[i]);
         }
-        x = tame(x);
+        return tame(x);
+      };
+      auto keep = [&](float x, int src, bool there) {
         const int at = (w - lane + src + u * 32) * T::PER + e;
         const LogitKey key = LogitKey::of(x, at);
-        const bool in = u < up && x >= bound && at < end && key.before(last);
+        const bool in = there && u < up && x >= bound && at < end && key.before(last);
         const uint32_t pass = __ballot_sync(0xffffffffu, in);
         if (in) found[n + __popc(pass & ((1u << lane) - 1u))] = key;
         n += __popc(pass);
+      };
+#pragma unroll 1
+      while (hits) {  // two lanes' at a time
+        const int s0 = __ffs(hits) - 1;
+        hits &= hits - 1;
+        const bool two = hits != 0;
+        const int s1 = two ? __ffs(hits) - 1 : s0;
+        hits &= hits - 1;
+        const float x0 = look(s0), x1 = look(s1);
+        keep(x0, s0, true);
+        keep(x1, s1, two);
 #pragma unroll 1
         while (n >= 32 || (!hits && n > 0)) {
           const int take = min(n, 32);
@@ -421,49 +446,47 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
   for (int o = 4; o > 0; o >>= 1) bs += __shfl_xor_sync(0xffffffffu, bs, o);
   if (lane == 0) a.ws.sums[piece] = make_float2(bm, bs);
   if (lane < a.beams) a.ws.best[piece * a.beams + lane] = list.k;
-  __threadfence();  // before the ticket
-  __syncwarp();
+  __syncwarp();  // before the ticket
 }
 
 // The group's last block: log-sums of its rows, then the K best of all their lists, in 64 bits.
 __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh, int group) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = a.beams, S = a.splits;
   const int64_t row0 = (int64_t)group * K;
+  const int N = K * S * K;
+  const int64_t* from = a.ws.best + row0 * S * K;
+  int64_t next = INT64_MIN;
+  if (warp * 32 + lane < N) next = __ldcg(from + warp * 32 + lane);
 #pragma unroll 1
   for (int b = warp; b < K; b += kSelWarps) {
-    const int done = a.done && a.done[row0 + b];
-    double sum = 0;
-    float m = -FLT_MAX;
-    if (!done) {
-      const float2* p = a.ws.sums + (row0 + b) * S;
+    const float2* p = a.ws.sums + (row0 + b) * S;
+    const int done = a.done ? a.done[row0 + b] != 0 : 0;
+    const float score = a.scores[row0 + b];
+    const float2 q = lane < S ? __ldcg(p + lane) : make_float2(-FLT_MAX, 0.f);  // (of a finished beam: nothing that counts)
+    float m = q.x;
 #pragma unroll 1
-      for (int k = lane; k < S; k += 32) m = fmaxf(m, __ldcg(&p[k].x));
+    for (int k = lane + 32; k < S; k += 32) m = fmaxf(m, __ldcg(&p[k].x));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    double sum = (double)q.y * (double)exp2_approx((q.x - m) * kLog2e);
 #pragma unroll 1
-      for (int k = lane; k < S; k += 32) {
-        const float2 q = __ldcg(p + k);
-        sum += (double)q.y * (double)exp2_approx((q.x - m) * kLog2e);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int k = lane + 32; k < S; k += 32) {
+      const float2 r = __ldcg(p + k);
+      sum += (double)r.y * (double)exp2_approx((r.x - m) * kLog2e);
     }
+    for (int o = S > 16 ? 16 : S > 1 ? 8 : 0; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
       sh.done[b] = done;
       // apart, so that rows of the type's lowest value keep their log-sum
       sh.max[b] = (double)m;
       sh.log_sum[b] = sum > 0 ? log_of(sum) : 0.0;  // nothing may follow: every candidate is -inf all the same
-      sh.score[b] = (double)tame(a.scores[row0 + b]);
+      sh.score[b] = (double)tame(score);
     }
   }
   __syncthreads();
   // 32 candidates a warp at a time, those before its K-th so far
   ScoreKey list = ScoreKey::none(), last = list;
   ScoreKey* const found = sh.found[warp];
-  const int N = K * S * K;
-  const int64_t* from = a.ws.best + row0 * S * K;
-  int64_t next = INT64_MIN;
-  if (warp * 32 + lane < N) next = __ldcg(from + warp * 32 + lane);
   int n = 0;
 #pragma unroll 1
   for (int c0 = warp * 32; c0 < N; c0 += kSelThreads) {
@@ -479,12 +502,8 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh
     }
     // of a first 32 only those that may be among their K best: at or above a bound found bit by bit, as above
     if (c0 < kSelThreads) {
-      const uint32_t hi = (uint32_t)(x.s >> 32) ^ 0x80000000u;
-      uint32_t t = 0;
-#pragma unroll 2
-      for (uint32_t bit = 0x80000000u; bit >= 1u << 8; bit >>= 1)
-        if (__popc(__ballot_sync(0xffffffffu, hi >= (t | bit))) >= K) t |= bit;
-      if (hi < t) x = ScoreKey::none();
+      const uint32_t hi[1] = {(uint32_t)(x.s >> 32) ^ 0x80000000u};
+      if (hi[0] < bound_of(hi, K)) x = ScoreKey::none();
     }
     const bool in = x.before(last);
     const uint32_t pass = __ballot_sync(0xffffffffu, in);
@@ -528,12 +547,13 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const __gri
     const int per = (words + a.splits - 1) / a.splits;
     scan_row<DT>(a, sh, p, skew, min(split * per, words), min((split + 1) * per, words), row * a.splits + split);
   }
-  if (threadIdx.x == 0) {
-    sh.last = atomicAdd(a.ws.tickets + group, 1u) == (uint32_t)(a.beams * a.splits - 1);
+  if (threadIdx.x == 0) {  // releases warp 0's results, and acquires the other blocks' where this is the last one
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;\n" : "=r"(before) : "l"(a.ws.tickets + group) : "memory");
+    sh.last = before == (uint32_t)(a.beams * a.splits - 1);
   }
   __syncthreads();
   if (!sh.last) return;
-  __threadfence();
   if (threadIdx.x == 0) a.ws.tickets[group] = 0;
   join_group(a, sh, group);
 }
