@@ -133,6 +133,15 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+// Sums of exponentials are of 2^(x kLog2e - r), one fused product a term, r = kLog2e times the largest value m, rounded: the same
+// number in every term, so its rounding costs nothing.  Past kBig, where products would leave fp32's range (rows
+// masked by the type's lowest value, infinities), of 2^((x - m) kLog2e).
+constexpr float kBig = 1e30f;
+__device__ __forceinline__ bool big(float m) { return fabsf(m) > kBig; }
+// What takes a sum from reference m to a larger one
+__device__ __forceinline__ float rescale(float m, float to) {
+  return exp2_approx(big(m) || big(to) ? (m - to) * kLog2e : m * kLog2e - to * kLog2e);
+}
 
 template <int DT>
 struct LogitType {
@@ -301,8 +310,23 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
   LogitKey *const found = reinterpret_cast<LogitKey*>(sh.found[warp]), *const room = reinterpret_cast<LogitKey*>(sh.room[warp]);
   const int up = min(U, (w1 - w0 + kSelThreads - 1) / kSelThreads), stride = up * kSelThreads;
   const uint4 none = make_uint4(T::LOWEST, T::LOWEST, T::LOWEST, T::LOWEST);
+  const char* const at0 = row + ((int64_t)(w0 + warp * up * 32 + lane) * T::PER - skew) * T::BYTES;  // of this lane's first word
+  const uint32_t to0 = (uint32_t)__cvta_generic_to_shared(&sh.words[warp][0][lane]);
   auto fetch = [&](int w, int slot) {  // (aligned words: one more where the row lies off the boundary)
     uint4* to = sh.words[warp][slot];
+    const int wb = w - lane;  // the warp's
+    if (up == U && wb * T::PER >= skew && (wb + U * 32 + 1) * T::PER <= a.vocab + skew && wb + U * 32 <= w1) {  // nothing but whole words
+      const char* at = at0 + (int64_t)(w - (w0 + warp * up * 32 + lane)) * 16;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to0 + slot * (uint32_t)sizeof(sh.words[0][0]) + u * 512), "l"(at + u * 512)
+                     : "memory");
+      if (skew && lane == 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to0 + slot * (uint32_t)sizeof(sh.words[0][0]) + U * 512), "l"(at + U * 512)
+                     : "memory");
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (u < up && w + u * 32 < w1 + (skew ? 1 : 0)) fetch_word<DT>(to + u * 32 + lane, row, skew, a.vocab, w + u * 32);
@@ -330,33 +354,42 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
     float top = words_max<DT>(now);
     if (top == INFINITY) top = FLT_MAX;
     if (top > m) {
-      s *= exp2_approx((m - top) * kLog2e);
+      s *= rescale(m, top);
       m = top;
     }
-    auto sum = [&](auto tamed) {  // x - m is exact where it matters, near the maximum
-      const uint64_t mm = pk2(m, m), c = pk2(kLog2e, kLog2e);
-      uint64_t t = 0;
+    const float r = m * kLog2e;
+    float t;
+    {
+      const uint64_t nr = pk2(-r, -r), c = pk2(kLog2e, kLog2e);
+      uint64_t sum = 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float x[T::PER];
         T::widen(now[u], x);
 #pragma unroll
         for (int e = 0; e < T::PER; e += 2) {
-          if constexpr (decltype(tamed)::value) {
-            x[e] = tame(x[e]);
-            x[e + 1] = tame(x[e + 1]);
-          }
           float e0, e1;
-          upk2(mul2(sub2(pk2(x[e], x[e + 1]), mm), c), e0, e1);
-          t = add2(t, pk2(exp2_approx(e0), exp2_approx(e1)));
+          upk2(fma2(pk2(x[e], x[e + 1]), c, nr), e0, e1);
+          sum = add2(sum, pk2(exp2_approx(e0), exp2_approx(e1)));
         }
       }
       float t0, t1;
-      upk2(t, t0, t1);
-      return t0 + t1;
-    };
-    float t = sum(std::false_type{});
-    if (!(t <= (float)(U * T::PER))) t = sum(std::true_type{});  // hardly ever: a NaN or an infinity
+      upk2(sum, t0, t1);
+      t = t0 + t1;
+    }
+    if (!(t <= (float)(U * T::PER)) || big(m)) {  // hardly ever: a NaN, infinities, or nothing yet
+      t = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[T::PER];
+        T::widen(now[u], x);
+#pragma unroll
+        for (int e = 0; e < T::PER; ++e) {
+          const float y = tame(x[e]);
+          t += exp2_approx(big(m) ? (y - m) * kLog2e : fmaf(y, kLog2e, -r));
+        }
+      }
+    }
     s += t;
     float bound = unordered(*(volatile int*)&sh.bound);
     // (behind the first turn values like the K-th have higher places than it)
@@ -428,7 +461,7 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
   float wm = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  s *= exp2_approx((m - wm) * kLog2e);
+  s *= rescale(m, wm);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) {
@@ -441,7 +474,7 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
   float bm = pm;
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-  float bs = ps * exp2_approx((pm - bm) * kLog2e);
+  float bs = ps * rescale(pm, bm);
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) bs += __shfl_xor_sync(0xffffffffu, bs, o);
   if (lane == 0) a.ws.sums[piece] = make_float2(bm, bs);
@@ -468,18 +501,19 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh
     for (int k = lane + 32; k < S; k += 32) m = fmaxf(m, __ldcg(&p[k].x));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    double sum = (double)q.y * (double)exp2_approx((q.x - m) * kLog2e);
+    double sum = (double)q.y * (double)rescale(q.x, m);
 #pragma unroll 1
     for (int k = lane + 32; k < S; k += 32) {
       const float2 r = __ldcg(p + k);
-      sum += (double)r.y * (double)exp2_approx((r.x - m) * kLog2e);
+      sum += (double)r.y * (double)rescale(r.x, m);
     }
     for (int o = S > 16 ? 16 : S > 1 ? 8 : 0; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
       sh.done[b] = done;
       // apart, so that rows of the type's lowest value keep their log-sum
       sh.max[b] = (double)m;
-      sh.log_sum[b] = sum > 0 ? log_of(sum) : 0.0;  // nothing may follow: every candidate is -inf all the same
+      // nothing may follow: every candidate is -inf all the same
+      sh.log_sum[b] = sum > 0 ? log_of(sum) + (big(m) ? 0.0 : (double)(m * kLog2e) * (1.0 / (double)kLog2e) - (double)m) : 0.0;
       sh.score[b] = (double)tame(score);
     }
   }
