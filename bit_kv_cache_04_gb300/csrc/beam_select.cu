@@ -592,10 +592,12 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const __gri
   join_group(a, sh, group);
 }
 
-// Blocks a row: about one wave of four blocks an SM, each with at least 2048 logits to read; at most 4096 candidates a group.
+// Blocks a row: up to two an SM in all, each with at least a turn of logits to read (8192 of two bytes); at most 4096 candidates a group.
+// More of them cost more in first turns and joins than they read sooner: 16 x 8 rows of 32000 took 18.6, 20.0, 24.4, 30.9 us with 1, 2, 4, 8
+// blocks a row; 64 rows of 131072 took 20.7, 16.6, 14.6, 16.6 us; one row 20.7, 14.6, 12.6, 10.5 us, and 12.5 us with 16.
 int splits_of(int64_t rows, int beams, int vocab) {
-  const int64_t want = (int64_t)sm_count() * 4 / std::max<int64_t>(1, rows);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)vocab / 2048, (int64_t)4096 / (beams * beams)}));
+  const int64_t want = (int64_t)sm_count() * 2 / std::max<int64_t>(1, rows);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)vocab / 8192, (int64_t)4096 / (beams * beams)}));
 }
 
 size_t select_ws(int groups, int beams, int vocab, void* base, SelectWs* w) {
