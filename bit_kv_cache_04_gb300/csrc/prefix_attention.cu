@@ -44,7 +44,8 @@ struct PlanArgs {
   const int32_t* cu_groups;
   const int32_t* cu_q;
   const int32_t* seq_lens;
-  int n_groups, total_q, max_q, max_group_q, tile, row_tile, n_units, own_tiles, columns;
+  int n_groups, total_q, max_q, max_group_q, tile_log, row_log, n_units, own_tiles, columns;  // (logarithms of tokens a tile, rows a row tile)
+  uint32_t g_magic;  // floor(2^32 / g) + 1
   uint32_t* status;
   int32_t* plan;     // total_q, max_q, max_group_q, n_groups
   uint32_t* ticket;  // blocks that are done; zero between calls
@@ -56,7 +57,9 @@ struct PlanArgs {
   OwnTile* own;
 };
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int ceil_shift(int a, int log) { return (a + (1 << log) - 1) >> log; }
+// r / g (r < 2^28)
+__device__ __forceinline__ int token_of(const PlanArgs& a, int r) { return a.lo.g == 1 ? r : (int)__umulhi((uint32_t)r, a.g_magic); }
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 
 // New tokens of sequence b (0: none, or its rows or length are out of order, which sets *bad), its first row and length.
@@ -103,9 +106,19 @@ __device__ __forceinline__ void find_parting(const PlanArgs& a, int g, int j0, i
       const int p = ref[j];
       bool same = p >= 0 && p < a.lo.n_pages;
       const int32_t* at = a.table + j;
-#pragma unroll 8
-      for (int b = first + 1 + sub; b < b1; b += subs)
-        if (at[(int64_t)b * mp] != p) same &= a.cu_q[b + 1] == a.cu_q[b];  // (a slot without new tokens has no say)
+#pragma unroll 1
+      for (int b = first + 1 + sub; b < b1 && same; b += 8 * subs) {
+        int v[8];
+        bool differ = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = b + i * subs < b1 ? at[(int64_t)(b + i * subs) * mp] : p;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) differ |= v[i] != p;
+        if (differ) {  // (a slot without new tokens has no say)
+#pragma unroll 1
+          for (int i = b; i < min(b + 8 * subs, b1); i += subs) same &= at[(int64_t)i * mp] == p || a.cu_q[i + 1] == a.cu_q[i];
+        }
+      }
       if (!same) {
         mine = j;
         break;
@@ -118,7 +131,7 @@ __device__ __forceinline__ void find_parting(const PlanArgs& a, int g, int j0, i
 
 // What group g, sequences [b0, b1), shares: the prefix, and whether taking it in common saves tiles.  A warp.
 __device__ __forceinline__ void plan_group(const PlanArgs& a, const SeqState& q, int g, int b0, int b1) {
-  const int lane = threadIdx.x & 31, gq = a.lo.g, RT = a.row_tile, NT = a.tile;
+  const int lane = threadIdx.x & 31, gq = a.lo.g;
   int live = 0, limit = INT_MAX, first = INT_MAX, rows = 0;
   bool bad = false;
   const int parting = __ldcg(a.parts + g);
@@ -149,7 +162,7 @@ __device__ __forceinline__ void plan_group(const PlanArgs& a, const SeqState& q,
   // (with a sequence out of order the others' rows need not be one run: they go without a common prefix)
   if (bad || live < 2) return;
   const int pages = min(parting ? INT_MAX - parting : INT_MAX, limit / a.lo.pt);
-  const int P = (int)((int64_t)pages * a.lo.pt / NT) * NT;
+  const int tiles_p = (int)((int64_t)pages * a.lo.pt >> a.tile_log), P = tiles_p << a.tile_log;
   if (P == 0) return;
   // tiles taken apart (row tiles of each sequence over all it has cached), and together
   __syncwarp();
@@ -158,16 +171,16 @@ __device__ __forceinline__ void plan_group(const PlanArgs& a, const SeqState& q,
   for (int b = b0 + lane; b < b1; b += 32) {
     const int n = q.n[b];
     if (!n) continue;
-    const int tiles = ceil_div(q.lens[b], NT), r0 = (q.cu[b] - cu0) * gq, r1 = r0 + n * gq;
-    apart += (int64_t)ceil_div(n * gq, RT) * tiles;
-    together += (int64_t)((r1 - 1) / RT - r0 / RT + 1) * (tiles - P / NT);
+    const int tiles = ceil_shift(q.lens[b], a.tile_log), r0 = (q.cu[b] - cu0) * gq, r1 = r0 + n * gq;
+    apart += (int64_t)ceil_shift(n * gq, a.row_log) * tiles;
+    together += (int64_t)(((r1 - 1) >> a.row_log) - (r0 >> a.row_log) + 1) * (tiles - tiles_p);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     apart += __shfl_xor_sync(0xffffffffu, apart, o);
     together += __shfl_xor_sync(0xffffffffu, together, o);
   }
-  together += (int64_t)ceil_div(rows * gq, RT) * (P / NT);
+  together += (int64_t)ceil_shift(rows * gq, a.row_log) * tiles_p;
   if (together >= apart) return;
   for (int b = b0 + lane; b < b1; b += 32) {
     q.owner_n[b] = b == first ? rows : 0;
@@ -178,29 +191,31 @@ __device__ __forceinline__ void plan_group(const PlanArgs& a, const SeqState& q,
 
 // Row tile k of the rows that begin with sequence b0, unit i: its rows, prefix and own tiles.  A warp.
 __device__ __forceinline__ void plan_unit(const PlanArgs& a, const SeqState& q, int i, int b0, int k, int* own_count) {
-  const int lane = threadIdx.x & 31, gq = a.lo.g, NT = a.tile, shared = q.owner_p[b0], end = q.owner_end[b0];
+  const int lane = threadIdx.x & 31, gq = a.lo.g, shared = q.owner_p[b0], end = q.owner_end[b0];
   SharedUnit u;
   u.cu = q.cu[b0];
   u.first = b0;
-  u.r0 = k * a.row_tile;
-  u.rows = min(a.row_tile, q.owner_n[b0] * gq - u.r0);
-  const int tok0 = u.r0 / gq, tok1 = (u.r0 + u.rows - 1) / gq;  // of the owner's
+  u.r0 = k << a.row_log;
+  u.rows = min(1 << a.row_log, q.owner_n[b0] * gq - u.r0);
+  const int tok0 = token_of(a, u.r0), tok1 = token_of(a, u.r0 + u.rows - 1);  // of the owner's
   if (shared)
     u.prefix = shared;
   else  // one sequence: what all of the rows see of it in the packed tiers
-    u.prefix = min(q_end_of(a.lo, q.lens[b0]), q.lens[b0] - q.n[b0] + tok0 + 1) / NT * NT;
+    u.prefix = min(q_end_of(a.lo, q.lens[b0]), q.lens[b0] - q.n[b0] + tok0 + 1) >> a.tile_log << a.tile_log;
   auto tiles_of = [&](int b, int* p_lo, int* rows) {
     if (b >= end || !q.n[b]) return 0;
     const int off = q.cu[b] - u.cu, n = q.n[b], T = q.lens[b], t0 = max(tok0, off), t1 = min(tok1, off + n - 1);
     if (t0 > t1) return 0;
     *rows = max(0, off * gq - u.r0) | min(u.rows, (off + n) * gq - u.r0) << 16;
     *p_lo = T - n + t0 - off;
-    return (T - n + t1 - off) / NT - u.prefix / NT + 1;
+    return ((T - n + t1 - off) >> a.tile_log) - (u.prefix >> a.tile_log) + 1;
   };
-  int total = 0, low = INT_MAX;
+  int total = 0, low = INT_MAX, tiles = 0, rows = 0;  // (the last turn's are kept: mostly it is the only one)
+#pragma unroll 1
   for (int b = b0 + lane; b - lane < end; b += 32) {
-    int p = INT_MAX, rows;
-    total += tiles_of(b, &p, &rows);
+    int p = INT_MAX;
+    tiles = tiles_of(b, &p, &rows);
+    total += tiles;
     low = min(low, p);
   }
   u.n_own = total = warp_sum(total);
@@ -211,18 +226,21 @@ __device__ __forceinline__ void plan_unit(const PlanArgs& a, const SeqState& q, 
   if (at > a.own_tiles - total) u.rows = 0;  // (the list holds all that lengths up to max_T need)
   if (lane == 0) a.units[i] = u;
   if (u.rows == 0) return;
+#pragma unroll 1
   for (int b = b0 + lane; b - lane < end; b += 32) {
-    int p, rows = 0;
-    const int mine = tiles_of(b, &p, &rows);
-    uint32_t have = __ballot_sync(0xffffffffu, mine > 0);
-    while (have) {
-      const int src = __ffs(have) - 1;
-      have &= have - 1;
-      const int count = __shfl_sync(0xffffffffu, mine, src), s = b - lane + src;
-      const int seen_by = __shfl_sync(0xffffffffu, rows, src), T = q.lens[s];
-      for (int t = lane; t < count; t += 32) a.own[at + t] = OwnTile{s, u.prefix + t * NT, T, seen_by};
-      at += count;
+    int p;
+    if (end - b0 > 32) tiles = tiles_of(b, &p, &rows);
+    // lanes' tiles one behind the other, each written by its lane
+    int before = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
     }
+    const int T = b < end ? q.lens[b] : 0;
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t) a.own[at + before - tiles + t] = OwnTile{b, u.prefix + (t << a.tile_log), T, rows};
+    at += __shfl_sync(0xffffffffu, before, 31);
   }
 }
 
@@ -270,7 +288,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     __syncthreads();
     // every owner's row tiles
     for (int base = 0; base < B; base += kPlanThreads) {
-      const int b = base + tid, mine = b < B ? ceil_div(q.owner_n[b] * a.lo.g, a.row_tile) : 0;
+      const int b = base + tid, mine = b < B ? ceil_shift(q.owner_n[b] * a.lo.g, a.row_log) : 0;
       int x = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -408,8 +426,9 @@ kvq_status kvq_prefix_plan(const kvq_config* cfg, const int32_t* block_table, co
   a.total_q = total_q;
   a.max_q = max_q;
   a.max_group_q = max_group_q;
-  a.tile = chunk_tile(cfg->D);
-  a.row_tile = chunk_form(cfg, (int64_t)max_group_q * a.lo.g) == kChunkPaired ? 256 : 128;
+  a.tile_log = chunk_tile(cfg->D) == 128 ? 7 : 6;
+  a.row_log = chunk_form(cfg, (int64_t)max_group_q * a.lo.g) == kChunkPaired ? 8 : 7;
+  a.g_magic = (uint32_t)((1ull << 32) / a.lo.g + 1);
   a.n_units = w.n_units;
   a.own_tiles = w.own_tiles;
   char* base = (char*)workspace;
