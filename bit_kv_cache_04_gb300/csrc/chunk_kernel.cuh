@@ -1593,66 +1593,77 @@ __device__ __forceinline__ bool few_any(int id, bool p) {
   return r != 0;
 }
 
-// The same for 5 to 32 rows by eight warps: rows warp, warp + 8, .. below `rows`, RW of them side by side, so that their loads are in
-// flight together (a part at a time, row after row, the joins of units of 32 rows in 3 parts took 15 us).
+// Joins of planned units (SEG): warp w of `warps` takes rows w, w + warps, .. below `rows`, RW of them side by side, so that their loads
+// are in flight together.  (Row after row, the joins of units of 32 rows in 3 parts took 15 us, of 256 rows in 10 parts 45 us.)
 // part(i, r): row r of part i.
-template <int RW, class Part, class Write>
-__device__ __forceinline__ void join_rows(const ChunkArgs& a, int parts, int rows, const Part& part, const Write& write) {
-  constexpr int D = 128, U = 4 / RW;  // parts in flight of each row
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float M[RW], L[RW], acc[RW][1][4];
-#pragma unroll
-  for (int k = 0; k < RW; ++k) {
-    M[k] = -INFINITY;
-    L[k] = acc[k][0][0] = acc[k][0][1] = acc[k][0][2] = acc[k][0][3] = 0.f;
-  }
+template <int D, int RW, class Part, class Write>
+__device__ __forceinline__ void join_rows(int parts, int rows, int warps, const Part& part, const Write& write) {
+  constexpr int N = D / 128, U = RW * N >= 4 ? 1 : 4 / (RW * N);  // parts in flight of each row
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int i = lane; i - lane < parts; i += 32)
-#pragma unroll
-    for (int k = 0; k < RW; ++k)
-      if (i < parts) M[k] = fmaxf(M[k], __ldcg(part(i, min(warp + 8 * k, rows - 1)) + D));
-#pragma unroll
-  for (int k = 0; k < RW; ++k)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], o));
-#pragma unroll 1
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    float w[RW];
+  for (int r0 = threadIdx.x >> 5; r0 < rows; r0 += warps * RW) {
+    float M[RW], L[RW], acc[RW][N][4];
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(min(i0 + lane, parts - 1), min(warp + 8 * k, rows - 1)) + D));
-      // a part that saw none of the row's tokens has m = -inf, or the lowest reference, and l = 0
-      const bool none = i0 + lane >= parts || ml.y == 0.f;
-      w[k] = none ? 0.f : ex2(ml.x - M[k]);
-      L[k] += none ? 0.f : w[k] * ml.y;
+      M[k] = -INFINITY;
+      L[k] = 0.f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[k][c][0] = acc[k][c][1] = acc[k][c][2] = acc[k][c][3] = 0.f;
     }
+    auto row = [&](int k) { return min(r0 + k * warps, rows - 1); };
 #pragma unroll 1
-    for (int i = 0; i < min(32, parts - i0); i += U) {
-      float4 v[RW][U];
+    for (int i = lane; i - lane < parts; i += 32)
 #pragma unroll
       for (int k = 0; k < RW; ++k)
+        if (i < parts) M[k] = fmaxf(M[k], __ldcg(part(i, row(k)) + D));
 #pragma unroll
-        for (int q = 0; q < U; ++q)
-          v[k][q] = __ldcg(reinterpret_cast<const float4*>(part(min(i0 + i + q, parts - 1), min(warp + 8 * k, rows - 1))) + lane);
+    for (int k = 0; k < RW; ++k)
 #pragma unroll
-      for (int k = 0; k < RW; ++k)
+      for (int o = 16; o > 0; o >>= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], o));
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float w[RW];
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-          const float wk = __shfl_sync(0xffffffffu, w[k], (i + q) & 31);
-          if (i0 + i + q < parts && wk != 0.f) {
-            acc[k][0][0] = fmaf(wk, v[k][q].x, acc[k][0][0]);
-            acc[k][0][1] = fmaf(wk, v[k][q].y, acc[k][0][1]);
-            acc[k][0][2] = fmaf(wk, v[k][q].z, acc[k][0][2]);
-            acc[k][0][3] = fmaf(wk, v[k][q].w, acc[k][0][3]);
+      for (int k = 0; k < RW; ++k) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(min(i0 + lane, parts - 1), row(k)) + D));
+        // a part that saw none of the row's tokens has m = -inf, or the lowest reference, and l = 0
+        const bool none = i0 + lane >= parts || ml.y == 0.f;
+        w[k] = none ? 0.f : ex2(ml.x - M[k]);
+        L[k] += none ? 0.f : w[k] * ml.y;
+      }
+#pragma unroll 1
+      for (int i = 0; i < min(32, parts - i0); i += U) {
+        float4 v[RW][U][N];
+#pragma unroll
+        for (int k = 0; k < RW; ++k)
+#pragma unroll
+          for (int q = 0; q < U; ++q)
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+              v[k][q][c] = __ldcg(reinterpret_cast<const float4*>(part(min(i0 + i + q, parts - 1), row(k))) + 32 * c + lane);
+#pragma unroll
+        for (int k = 0; k < RW; ++k)
+#pragma unroll
+          for (int q = 0; q < U; ++q) {
+            const float wk = __shfl_sync(0xffffffffu, w[k], (i + q) & 31);
+            if (i0 + i + q < parts && wk != 0.f) {
+#pragma unroll
+              for (int c = 0; c < N; ++c) {
+                acc[k][c][0] = fmaf(wk, v[k][q][c].x, acc[k][c][0]);
+                acc[k][c][1] = fmaf(wk, v[k][q][c].y, acc[k][c][1]);
+                acc[k][c][2] = fmaf(wk, v[k][q][c].z, acc[k][c][2]);
+                acc[k][c][3] = fmaf(wk, v[k][q][c].w, acc[k][c][3]);
+              }
+            }
           }
-        }
+      }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < RW; ++k) {
+    for (int k = 0; k < RW; ++k) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L[k] += __shfl_xor_sync(0xffffffffu, L[k], o);
-    if (warp + 8 * k < rows) write(warp + 8 * k, acc[k], L[k]);
+      for (int o = 16; o > 0; o >>= 1) L[k] += __shfl_xor_sync(0xffffffffu, L[k], o);
+      if (r0 + k * warps < rows) write(r0 + k * warps, acc[k], L[k]);
+    }
   }
 }
 
@@ -1733,15 +1744,15 @@ __device__ __forceinline__ bool join_unit(const ChunkArgs& a, const Run& run, co
     if (fix) add_nonfinite<D, DT, SEG>(a, run, r0, min(r0 + 32, u.rows), 1);
     return true;
   }
-  if constexpr (SEG && C::FEW) {
+  if constexpr (SEG) {
     if (u.rows > 4) {
-      if (u.rows <= 8)
-        join_rows<1>(a, parts, u.rows, part, write);
-      else if (u.rows <= 16)
-        join_rows<2>(a, parts, u.rows, part, write);
+      if (u.rows <= C::SOFT_WARPS)
+        join_rows<D, 1>(parts, u.rows, C::SOFT_WARPS, part, write);
+      else if (u.rows <= 2 * C::SOFT_WARPS)
+        join_rows<D, 2>(parts, u.rows, C::SOFT_WARPS, part, write);
       else
-        join_rows<4>(a, parts, u.rows, part, write);
-      if (fix) add_nonfinite<D, DT, SEG>(a, run, warp, u.rows, 8);
+        join_rows<D, 4>(parts, u.rows, C::SOFT_WARPS, part, write);
+      if (fix) add_nonfinite<D, DT, SEG>(a, run, warp, u.rows, C::SOFT_WARPS);
       return true;
     }
   }
@@ -2784,6 +2795,24 @@ __global__ void __launch_bounds__(ChunkShape<D, MODE>::THREADS, 1)
             t0 = x.y;
             masked = t0 + NT - 1 > p_lo || r_lo > 0 || r_hi < run.u.rows;
             if (my_row < r_lo || my_row >= r_hi) see.pos = -1;
+            // none of the warp's rows: P is zeros (drafts of 32 chats 243 -> 238 us)
+            if (my_row - lane >= r_hi || my_row - lane + 32 <= r_lo) {
+              ns0 += b ^ 1;
+              ns1 += b;
+              tc_fence_after();
+              uint32_t zero[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll
+              for (int c = 0; c < NT / 2; c += 16) tmem_st16(s_col + c, zero);
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(smem_addr(&sh.p_full[b]));
+              ++steps_done;
+              first_step = false;
+              continue;
+            }
           }
         }
         ns0 += b ^ 1;
