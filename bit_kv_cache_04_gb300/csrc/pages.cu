@@ -428,7 +428,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesArgs a)
 
 // A group's slots after a selection: slot b becomes what slot parents[b] was.  Every column of the table (and every
 // 16-byte word of the windows) belongs to one thread, which reads all it needs of the group before it writes: no copy
-// of the old state is kept.
+// of the old state is kept.  (The stream's next kernel is let go at these kernels' ends only: begun while an attention before them still ran, it could find that one's
+// table entries in the first-level cache, where it reads them with non-coherent loads.)
 
 // The group's parents and lengths into shared memory; 0, or the status bit of what is wrong with them.
 __device__ __forceinline__ uint32_t group_state(const PagesArgs& a, int group, int* parent, int* len) {
@@ -452,7 +453,6 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(PagesArgs a) {
   __shared__ int parent[kMaxReorder], children[kMaxReorder], heir[kMaxReorder], len[kMaxReorder], share[kMaxReorder];
   __shared__ int column[kMaxReorder][kReorderThreads];
   __shared__ bool last;
-  grid_launch_dependents();
   grid_dependency_wait();
   const int group = blockIdx.x, K = a.n, mp = a.lo.max_pages;
   if (const uint32_t wrong = group_state(a, group, parent, len)) {
@@ -518,7 +518,6 @@ template <int N>
 __global__ void __launch_bounds__(kReorderThreads) reorder_window_kernel(PagesArgs a) {
   __shared__ int parent[kMaxReorder], len[kMaxReorder], source[kMaxReorder], first[kMaxReorder + 1], to[kMaxReorder];
   __shared__ int n_sources;
-  grid_launch_dependents();
   grid_dependency_wait();
   const int group = blockIdx.z, K = a.n, layer = blockIdx.y >> 1;
   if (group_state(a, group, parent, len)) return;  // (the other kernel has said so; lengths that it has moved are good ones)

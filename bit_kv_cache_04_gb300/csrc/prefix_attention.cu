@@ -244,13 +244,13 @@ __device__ __forceinline__ void plan_unit(const PlanArgs& a, const SeqState& q, 
   }
 }
 
-// Grid (groups, runs of table columns); the last block to finish writes the plan.
+// Grid (groups, runs of table columns); the last block to finish writes the plan.  The attention is let go at this grid's end: begun while the attention before
+// still ran, an SM could have that one's table entries in its first-level cache.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PlanArgs a) {
   __shared__ bool last;
   __shared__ int scan[kPlanWarps], own_count;
   __shared__ int32_t small[kSeqWords][kPlanSmall];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.lo.B;
-  grid_launch_dependents();
   grid_dependency_wait();
   find_parting(a, blockIdx.x, blockIdx.y * a.columns, (blockIdx.y + 1) * a.columns);
   if (tid == 0) {
