@@ -773,89 +773,111 @@ __device__ __forceinline__ void rotated_window(const ChunkArgs& a, const CachePo
   }
 }
 
-// rotate_lanes of U rows side by side: the same operations in the same order, a stage of all rows at a time, so that
-// the rows hide one another's shuffles.
-template <int U>
-__device__ __forceinline__ void rotate_rows(float (&v)[U][4], uint32_t s1, uint32_t s2) {
+// rotate_lanes of four rows, eight lanes a row: lane 8 r + q holds channels 32 j + 4 q + e of row r.  The same operations in the same
+// order, with 48 shuffles where a row at a time takes 80.  Bits 4 j + e of s1 and s2: the signs.
+__device__ __forceinline__ void rotate_rows(float (&v)[4][4], uint32_t s1, uint32_t s2) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int j = 0; j < 4; ++j) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[i][e] = __uint_as_float(__float_as_uint(v[i][e]) ^ ((s1 << (31 - e)) & 0x80000000u));
-    const float a0 = v[i][0] + v[i][1], a1 = v[i][0] - v[i][1], a2 = v[i][2] + v[i][3], a3 = v[i][2] - v[i][3];
-    v[i][0] = a0 + a2;
-    v[i][2] = a0 - a2;
-    v[i][1] = a1 + a3;
-    v[i][3] = a1 - a3;
+    for (int e = 0; e < 4; ++e) v[j][e] = __uint_as_float(__float_as_uint(v[j][e]) ^ ((s1 << (31 - 4 * j - e)) & 0x80000000u));
+    const float a0 = v[j][0] + v[j][1], a1 = v[j][0] - v[j][1], a2 = v[j][2] + v[j][3], a3 = v[j][2] - v[j][3];
+    v[j][0] = a0 + a2;
+    v[j][2] = a0 - a2;
+    v[j][1] = a1 + a3;
+    v[j][3] = a1 - a3;
   }
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
+  for (int m = 1; m < 8; m <<= 1) {
     const float sign = lane & m ? -1.f : 1.f;
-    float o[U][4];
 #pragma unroll
-    for (int i = 0; i < U; ++i)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = __shfl_xor_sync(0xffffffffu, v[i][e], m);
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[i][e] = fmaf(v[i][e], sign, o[i][e]);  // exact: v + o or o - v, rounded once
+      for (int e = 0; e < 4; ++e) v[j][e] = fmaf(v[j][e], sign, __shfl_xor_sync(0xffffffffu, v[j][e], m));  // exact: v + o or o - v, rounded once
   }
   const float c = hadamard_scale();
 #pragma unroll
-  for (int i = 0; i < U; ++i)
+  for (int e = 0; e < 4; ++e) {
+    const float a0 = v[0][e] + v[1][e], a1 = v[0][e] - v[1][e], a2 = v[2][e] + v[3][e], a3 = v[2][e] - v[3][e];
+    v[0][e] = a0 + a2;
+    v[2][e] = a0 - a2;
+    v[1][e] = a1 + a3;
+    v[3][e] = a1 - a3;
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[i][e] = __uint_as_float(__float_as_uint(v[i][e] * c) ^ ((s2 << (31 - e)) & 0x80000000u));
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[j][e] = __uint_as_float(__float_as_uint(v[j][e] * c) ^ ((s2 << (31 - 4 * j - e)) & 0x80000000u));
 }
 
-// The same (SEG), four tokens at a time and the next four's loads in flight.  (One token at a time, with a load's and the shuffles' latencies each, a tile of 128 window tokens took
-// some 40 us.  With this and the packed tokens beside it filled in on the hot path, 8 prompts with 8 beams each behind 16-bit
-// windows of 128 tokens went from 255 to 204 us.)
+// 16 bytes from global memory to shared, in flight until copies_land.
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_land() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+
+// The same (SEG).  All tokens' values are first copied, as they are, to where the turned ones will stand, so that one load's latency
+// is paid a piece; then four tokens are turned at a time, by eight lanes each.
+// WINDOW_FIGURES
 template <int D, int DT>
 __device__ __forceinline__ void rotated_window4(const ChunkArgs& a, const CachePos& u, int which, int part, uint32_t dst,
                                                int tile0, int a0, int t0, int t1, int lane, volatile uint32_t* nonfinite) {
-  constexpr int NT = chunk_tile(D), U = 4;
+  constexpr int NT = chunk_tile(D);
   const int c = D == 256 ? part : 0;  // D = 256: the warp's 128 channels
   if (D == 128) {                     // D = 128: its 32 tokens
     t0 = max(t0, a0 + 32 * part);
     t1 = min(t1, a0 + 32 * part + 32);
   }
   if (t0 >= t1) return;
-  const uint32_t s1 = lane_signs(a.lo.d1, lane), s2 = lane_signs(a.lo.d2, lane);
-  const int ch = 128 * c + 4 * lane;
-  const uint32_t col = dst + (uint32_t)(ch >> 6) * NT * 128 + (ch & 4) * 2;
-  uint2 next[U];
-  auto load = [&](int t) {
+  dst += 2 * c * NT * 128;
+  // a lane's window row, passed on by shuffles: one division by the ring's size for all tokens
+  const uint64_t mine = (uint64_t)(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, min(t0 + lane, t1 - 1)) + 128 * c);
+  const int ch = lane & 15;  // a 16-byte piece
+#pragma unroll 4
+  for (int i = 0; i < t1 - t0; i += 2) {
+    const int t = i + (lane >> 4);
+    const uint64_t row = __shfl_sync(0xffffffffu, mine, t & 31);
+    if (t < t1 - t0) copy_16(dst + (uint32_t)(ch >> 3) * NT * 128 + swz(t0 + t - tile0, ch & 7), (const char*)row + 16 * ch);
+  }
+  const int q = lane & 7, r = lane >> 3;
+  uint32_t s1 = 0, s2 = 0;
 #pragma unroll
-    for (int i = 0; i < U; ++i)  // (behind the last token it again)
-      next[i] = reinterpret_cast<const uint2*>(resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, min(t + i, t1 - 1)))[32 * c + lane];
-  };
-  load(t0);
+  for (int j = 0; j < 4; ++j) {
+    s1 |= (a.lo.d1[j] >> (4 * q) & 15) << (4 * j);
+    s2 |= (a.lo.d2[j] >> (4 * q) & 15) << (4 * j);
+  }
+  copies_land();
+  __syncwarp();
+  // rows 0, 1, 4, 5 of eight, then 2, 3, 6, 7: their swizzled pieces lie in all banks
 #pragma unroll 1
-  for (int t = t0; t < t1; t += U) {
-    float v[U][4];
+  for (int i = 0; i < t1 - t0; i += (i & 2) ? 6 : 2) {
+    const int t = t0 + i + (r & 1) + 4 * (r >> 1), row = min(t, t1 - 1) - tile0;
+    uint32_t at[4];
+    float v[4][4];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t w0 = clean<DT>(next[i].x, which, nonfinite), w1 = clean<DT>(next[i].y, which, nonfinite);
-      v[i][0] = in_to_f32((uint16_t)w0, DT);
-      v[i][1] = in_to_f32((uint16_t)(w0 >> 16), DT);
-      v[i][2] = in_to_f32((uint16_t)w1, DT);
-      v[i][3] = in_to_f32((uint16_t)(w1 >> 16), DT);
+    for (int j = 0; j < 4; ++j) {
+      at[j] = dst + (uint32_t)(j >> 1) * NT * 128 + swz(row, 4 * (j & 1) + (q >> 1)) + 8 * (q & 1);
+      uint32_t w0, w1;
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(w0), "=r"(w1) : "r"(at[j]) : "memory");
+      w0 = clean<DT>(w0, which, nonfinite);
+      w1 = clean<DT>(w1, which, nonfinite);
+      v[j][0] = in_to_f32((uint16_t)w0, DT);
+      v[j][1] = in_to_f32((uint16_t)(w0 >> 16), DT);
+      v[j][2] = in_to_f32((uint16_t)w1, DT);
+      v[j][3] = in_to_f32((uint16_t)(w1 >> 16), DT);
     }
-    load(t + U);
     rotate_rows(v, s1, s2);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
+    for (int j = 0; j < 4; ++j) {
       uint32_t o0, o1;
       if (DT == KVQ_DT_F16 || which) {
-        o0 = pack16<DT>(keep_range<DT>(v[i][0]), keep_range<DT>(v[i][1]));
-        o1 = pack16<DT>(keep_range<DT>(v[i][2]), keep_range<DT>(v[i][3]));
+        o0 = pack16<DT>(keep_range<DT>(v[j][0]), keep_range<DT>(v[j][1]));
+        o1 = pack16<DT>(keep_range<DT>(v[j][2]), keep_range<DT>(v[j][3]));
       } else {
-        o0 = score_pack(v[i][0] * a.k_pre, v[i][1] * a.k_pre);
-        o1 = score_pack(v[i][2] * a.k_pre, v[i][3] * a.k_pre);
+        o0 = score_pack(v[j][0] * a.k_pre, v[j][1] * a.k_pre);
+        o1 = score_pack(v[j][2] * a.k_pre, v[j][3] * a.k_pre);
       }
-      if (t + i < t1)
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(col + swz(t + i - tile0, (ch & 63) >> 3)), "r"(o0), "r"(o1) : "memory");
+      if (t < t1) asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at[j]), "r"(o0), "r"(o1) : "memory");
     }
   }
 }
@@ -1355,20 +1377,29 @@ __device__ __forceinline__ void window_tokens(const ChunkArgs& a, ChunkShared& s
     rotated_window4<D, DT>(a, u, which, part, dst, tt.t0, a0, t0, t1, lane, &sh.nonfinite);
     return;
   }
+  // as in rotated_window4: copied into place, then put right there
+  auto each = [&](auto f) {
 #pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    int toff, row, run32;
-    RunPlace<D>::of(false, part, i, lane, &toff, &row, &run32);
-    if (a0 + toff < t0 || a0 + toff >= t1) continue;
-    uint32_t h[16];
-    raw_token_run<DT>(a, u, which, a0 + toff, run32, &sh.nonfinite, h);
-    if (which == 0) {
+    for (int i = 0; i < 4; ++i) {
+      int toff, row, run32;
+      RunPlace<D>::of(false, part, i, lane, &toff, &row, &run32);
+      if (a0 + toff < t0 || a0 + toff >= t1) continue;
+      row += half * (NT / 2);
+      const uint32_t line = RunPlace<D>::line_at(dst, row, run32, NT);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) h[k] = score_pair<DT>(h[k], a.k_pre);
+      for (int k = 0; k < 4; ++k) f(line + ((((run32 & 1) * 4 + k) ^ (row & 7)) << 4), a0 + toff, 32 * run32 + 8 * k);
     }
-    row += half * (NT / 2);
-    store_run(RunPlace<D>::line_at(dst, row, run32, NT), row, run32, h);
-  }
+  };
+  each([&](uint32_t at, int t, int ch) { copy_16(at, resid_row(a.lo, a.cp, which, u.layer, u.b, u.h, t) + ch); });
+  copies_land();
+  if (which == 0 && DT == KVQ_DT_F16) return;  // (keys stand as they are)
+  each([&](uint32_t at, int, int) {
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = which ? clean<DT>(w[e], which, &sh.nonfinite) : score_pair<DT>(w[e], a.k_pre);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+  });
 }
 
 // Sum over the block's threads of x, and the exclusive prefix.
