@@ -86,8 +86,8 @@ struct alignas(16) ScoreKey {
   }
 };
 
-// A number that at least K of the lanes' N (each) are not below: the K-th largest's upper 14 bits, two at a time.
-template <int N>
+// A number that at least K of the lanes' N (each) are not below: the K-th largest's bits from LOW on, two at a time.
+template <int LOW, int N>
 __device__ __forceinline__ uint32_t bound_of(const uint32_t (&x)[N], int K) {
   uint32_t t = 0;
   auto enough = [&](uint32_t c) {
@@ -97,7 +97,7 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t (&x)[N], int K) {
     return n >= K;
   };
 #pragma unroll 1
-  for (int at = 30; at >= 18; at -= 2) {
+  for (int at = 30; at >= LOW; at -= 2) {
     const uint32_t c1 = t | 1u << at, c2 = t | 2u << at, c3 = t | 3u << at;
     const bool e1 = enough(c1), e2 = enough(c2), e3 = enough(c3);
     t = e3 ? c3 : e2 ? c2 : e1 ? c1 : t;
@@ -266,6 +266,7 @@ struct SelectShared {
     ScoreKey all[kSelWarps * kMaxBeams];
   };
   ScoreKey room[kSelWarps][32];
+  int count;                           // candidates in `all`
   int bound;                           // ordered(): no value below it is among the block's K largest
   float m[kSelWarps], s[kSelWarps];
   double max[kMaxBeams], log_sum[kMaxBeams], score[kMaxBeams];
@@ -403,7 +404,7 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
         const uint4 half0[2] = {now[0], now[1]}, half1[2] = {now[2], now[3]};
         const uint32_t x[2] = {(uint32_t)ordered(fminf(words_max<DT>(half0), FLT_MAX)) ^ 0x80000000u,
                                (uint32_t)ordered(fminf(words_max<DT>(half1), FLT_MAX)) ^ 0x80000000u};
-        const uint32_t t = bound_of(x, a.beams);
+        const uint32_t t = bound_of<18>(x, a.beams);
         // (bits below -inf's are no number: then all values count)
         const int o = (int)(t ^ 0x80000000u);
         if (o > ordered(-INFINITY)) bound = fmaxf(bound, unordered(o));
@@ -482,63 +483,18 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
   __syncwarp();  // before the ticket
 }
 
-// The group's last block: log-sums of its rows, then the K best of all their lists, in 64 bits.
-__device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh, int group) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = a.beams, S = a.splits;
-  const int64_t row0 = (int64_t)group * K;
-  const int N = K * S * K;
-  const int64_t* from = a.ws.best + row0 * S * K;
-  int64_t next = INT64_MIN;
-  if (warp * 32 + lane < N) next = __ldcg(from + warp * 32 + lane);
-#pragma unroll 1
-  for (int b = warp; b < K; b += kSelWarps) {
-    const float2* p = a.ws.sums + (row0 + b) * S;
-    const int done = a.done ? a.done[row0 + b] != 0 : 0;
-    const float score = a.scores[row0 + b];
-    const float2 q = lane < S ? __ldcg(p + lane) : make_float2(-FLT_MAX, 0.f);  // (of a finished beam: nothing that counts)
-    float m = q.x;
-#pragma unroll 1
-    for (int k = lane + 32; k < S; k += 32) m = fmaxf(m, __ldcg(&p[k].x));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    double sum = (double)q.y * (double)rescale(q.x, m);
-#pragma unroll 1
-    for (int k = lane + 32; k < S; k += 32) {
-      const float2 r = __ldcg(p + k);
-      sum += (double)r.y * (double)rescale(r.x, m);
-    }
-    for (int o = S > 16 ? 16 : S > 1 ? 8 : 0; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      sh.done[b] = done;
-      // apart, so that rows of the type's lowest value keep their log-sum
-      sh.max[b] = (double)m;
-      // nothing may follow: every candidate is -inf all the same
-      sh.log_sum[b] = sum > 0 ? log_of(sum) + (big(m) ? 0.0 : (double)(m * kLog2e) * (1.0 / (double)kLog2e) - (double)m) : 0.0;
-      sh.score[b] = (double)tame(score);
-    }
-  }
-  __syncthreads();
-  // 32 candidates a warp at a time, those before its K-th so far
+// More candidates at one bound than shared memory takes: those of equal scores.  32 of them a warp at a time, those before its K-th so far.
+template <class F>
+__device__ __noinline__ ScoreKey join_ties(SelectShared& sh, int N, int K, const int64_t* from, const F& candidate) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   ScoreKey list = ScoreKey::none(), last = list;
   ScoreKey* const found = sh.found[warp];
   int n = 0;
+  __syncthreads();  // `found` is where the candidates were
 #pragma unroll 1
   for (int c0 = warp * 32; c0 < N; c0 += kSelThreads) {
-    const LogitKey e{next};
-    next = INT64_MIN;
-    if (c0 + kSelThreads + lane < N) next = __ldcg(from + c0 + kSelThreads + lane);
-    const int c = c0 + lane, b = min(c / (S * K), K - 1);
-    ScoreKey x = ScoreKey::none();
-    if (c < N && sh.done[b]) {  // one candidate
-      if (c == b * S * K) x = ScoreKey::of(sh.score[b], b * a.vocab + a.eos);
-    } else if (e.real()) {
-      x = ScoreKey::of(sh.score[b] + (((double)e.value() - sh.max[b]) - sh.log_sum[b]), b * a.vocab + e.token());
-    }
-    // of a first 32 only those that may be among their K best: at or above a bound found bit by bit, as above
-    if (c0 < kSelThreads) {
-      const uint32_t hi[1] = {(uint32_t)(x.s >> 32) ^ 0x80000000u};
-      if (hi[0] < bound_of(hi, K)) x = ScoreKey::none();
-    }
+    const int c = c0 + lane;
+    const ScoreKey x = c < N ? candidate(c, __ldcg(from + c)) : ScoreKey::none();
     const bool in = x.before(last);
     const uint32_t pass = __ballot_sync(0xffffffffu, in);
     if (in) found[n + __popc(pass & ((1u << lane) - 1u))] = x;
@@ -553,7 +509,99 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh
       last = list.of_lane(K - 1);
     }
   }
-  list = join_warps(sh, list, K);
+  return join_warps(sh, list, K);
+}
+
+// The group's last block: log-sums of its rows, then the K best of all their lists, in 64 bits.
+__device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh, int group) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = a.beams, S = a.splits;
+  const int64_t row0 = (int64_t)group * K;
+  const int N = K * S * K;
+  const int64_t* from = a.ws.best + row0 * S * K;
+  const int64_t mine_at_first = (int)threadIdx.x < N ? __ldcg(from + threadIdx.x) : INT64_MIN;
+  {
+    // all rows at a time, by 32 or 8 lanes each: 64-bit arithmetic is slow, and no faster for fewer lanes
+    const int G = K <= kSelWarps ? 32 : 8, b = (warp * 32 + lane) / G, l = lane & (G - 1);
+    const bool there = b < K;
+    const float2* p = a.ws.sums + (row0 + (there ? b : 0)) * S;
+    const int done = there && a.done ? a.done[row0 + b] != 0 : 0;
+    const float score = there ? a.scores[row0 + b] : 0.f;
+    const float2 q = l < S ? __ldcg(p + l) : make_float2(-FLT_MAX, 0.f);  // (of a finished beam: nothing that counts)
+    float m = q.x;
+#pragma unroll 1
+    for (int k = l + G; k < S; k += G) m = fmaxf(m, __ldcg(&p[k].x));
+#pragma unroll 1
+    for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    double sum = (double)q.y * (double)rescale(q.x, m);
+#pragma unroll 1
+    for (int k = l + G; k < S; k += G) {
+      const float2 r = __ldcg(p + k);
+      sum += (double)r.y * (double)rescale(r.x, m);
+    }
+#pragma unroll 1
+    for (int o = min(G / 2, S > 16 ? 16 : S > 8 ? 8 : S > 1 ? 4 : 0); o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (there && l == 0) {
+      sh.done[b] = done;
+      // apart, so that rows of the type's lowest value keep their log-sum
+      sh.max[b] = (double)m;
+      // nothing may follow: every candidate is -inf all the same
+      sh.log_sum[b] = sum > 0 ? log_of(sum) + (big(m) ? 0.0 : (double)(m * kLog2e) * (1.0 / (double)kLog2e) - (double)m) : 0.0;
+      sh.score[b] = (double)tame(score);
+    }
+    if (threadIdx.x == 0) sh.count = 0;
+    if (threadIdx.x < 32) sh.room[0][threadIdx.x] = ScoreKey::none();
+  }
+  __syncthreads();
+  auto candidate = [&](int c, int64_t key) {
+    const LogitKey e{key};
+    const int b = min(c / (S * K), K - 1);
+    if (sh.done[b]) return c == b * S * K ? ScoreKey::of(sh.score[b], b * a.vocab + a.eos) : ScoreKey::none();  // one candidate
+    if (!e.real()) return ScoreKey::none();
+    return ScoreKey::of(sh.score[b] + (((double)e.value() - sh.max[b]) - sh.log_sum[b]), b * a.vocab + e.token());
+  };
+  auto order = [](const ScoreKey& x) { return (uint32_t)(x.s >> 32) ^ 0x80000000u; };
+  // Candidates side by side in shared memory, and ranked there: all of them, or those at or above a bound that the best few of the
+  // rows' pieces give (of 32 beams' 1024 some 100).
+  int n = N;
+  if (N <= kSelThreads) {
+    if ((int)threadIdx.x < N) sh.all[threadIdx.x] = candidate(threadIdx.x, mine_at_first);
+  } else {
+    uint32_t x[4];
+    const int lists = K * S;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int list = lists <= 32 ? lane : lane + 32 * i, c = list * K + (lists <= 32 ? i : 0);
+      x[i] = list < lists && (lists > 32 || i < K) ? order(candidate(c, __ldcg(from + c))) : 0u;
+    }
+    const uint32_t t = bound_of<12>(x, K);
+#pragma unroll 1
+    for (int c0 = warp * 32; c0 < N; c0 += kSelThreads) {
+      const int c = c0 + lane;
+      const ScoreKey y = c >= N ? ScoreKey::none() : candidate(c, c0 < kSelThreads ? mine_at_first : __ldcg(from + c));
+      const uint32_t pass = __ballot_sync(0xffffffffu, y.real() && order(y) >= t);
+      int at = 0;
+      if (lane == 0 && pass) at = atomicAdd(&sh.count, __popc(pass));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(pass & ((1u << lane) - 1u));
+      if ((pass >> lane & 1) && at < kSelThreads) sh.all[at] = y;
+    }
+    __syncthreads();
+    n = sh.count;
+  }
+  __syncthreads();
+  ScoreKey list = ScoreKey::none();
+  if (n <= kSelThreads) {
+    if (warp * 32 < n) {
+      const ScoreKey mine = (int)threadIdx.x < n ? sh.all[threadIdx.x] : ScoreKey::none();
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) rank += sh.all[j].before(mine);
+      if (mine.real() && rank < K) sh.room[0][rank] = mine;
+    }
+    __syncthreads();
+    list = sh.room[0][lane];
+  } else {
+    list = join_ties(sh, N, K, from, candidate);
+  }
   if (warp) return;
   if (lane < K) {
     const int b = list.at / a.vocab, t = list.at - b * a.vocab;

@@ -229,3 +229,31 @@ def test_the_same_call_gives_the_same_bits():
         torch.cuda.synchronize()
         first = first or out
         assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
+@pytest.mark.parametrize("beams,vocab", [(32, 500), (32, 40000), (20, 9000), (17, 300)])
+@pytest.mark.parametrize("value", [0.0, -float("inf"), 1.5])
+def test_more_equal_candidates_than_are_ranked_at_once(beams, vocab, value):
+    """Beams without a difference: every candidate at the bound, the lowest tokens of the first beam."""
+    logits = torch.full((3, beams, vocab), value, device="cuda").to(torch.bfloat16)
+    scores = torch.zeros((3, beams), device="cuda")
+    logits[1, 0, vocab - 1] = 2.0  # one above the others
+    scores[2, 1] = 0.25
+    sel = K.BeamSelect(3, beams, vocab)
+    for _ in range(2):
+        got = check(logits, scores, sel=sel)
+    if value == 0:
+        assert got[1][0].tolist() == list(range(beams)) and not got[2][0].any()
+
+
+@pytest.mark.parametrize("near", [1e-3, 1.0, 30.0])
+def test_beams_apart_and_together(near):
+    """Of 32 beams' 1024 candidates those that come through the bound: all from one beam, some of each, nearly all."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.randn((4, 32, 2000), generator=g, device="cuda")
+    scores = -near * torch.rand((4, 32), generator=g, device="cuda")
+    scores[1] *= 100
+    done = torch.zeros((4, 32), dtype=torch.int32, device="cuda")
+    done[2, ::3] = 1
+    done[3] = 1
+    check(logits, scores, done, 7)
