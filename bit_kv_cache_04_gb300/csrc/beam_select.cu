@@ -266,6 +266,7 @@ struct SelectShared {
     ScoreKey all[kSelWarps * kMaxBeams];
   };
   ScoreKey room[kSelWarps][32];
+  uint32_t top[kSelThreads];           // the threads' largest of the first turn, as unsigned numbers of the same order
   int count;                           // candidates in `all`
   int bound;                           // ordered(): no value below it is among the block's K largest
   float m[kSelWarps], s[kSelWarps];
@@ -338,7 +339,7 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
   bool first = true;
   fetch(w, 0);
 #pragma unroll 1
-  for (; w - lane < w1; w += stride, slot ^= 1) {  // whole warps
+  for (; first || w - lane < w1; w += stride, slot ^= 1) {  // whole warps; a first turn also where there is nothing to read
     fetch(w + stride, slot ^ 1);
     asm volatile("cp.async.wait_group 1;\n" ::: "memory");
     __syncwarp();
@@ -393,23 +394,26 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
     }
     s += t;
     float bound = unordered(*(volatile int*)&sh.bound);
+    if (first) {
+      // The block's K-th largest of its 256 threads' largest values: no value below that is among the K best.  (Of 8192 values in random
+      // order some 8 come through for K = 8 and 34 for K = 32.)
+      sh.top[threadIdx.x] = (uint32_t)ordered(top) ^ 0x80000000u;
+      __syncthreads();
+      uint32_t x[kSelWarps];
+#pragma unroll
+      for (int i = 0; i < kSelWarps; ++i) x[i] = sh.top[32 * i + lane];
+      // (bits below -inf's are no number: then all values count)
+      const int o = (int)(bound_of<18>(x, a.beams) ^ 0x80000000u);
+      if (o > ordered(-INFINITY)) {
+        bound = unordered(o);
+        if (threadIdx.x == 0) atomicMax(&sh.bound, o);
+      }
+    }
     // (behind the first turn values like the K-th have higher places than it)
     uint32_t hits = __ballot_sync(0xffffffffu, top >= bound && (!last.real() || top > last.value()));
     if (hits) {
       // of lanes with -inf alone only the lowest places matter, and only as long as the list is not full
       if (first) hits &= __ballot_sync(0xffffffffu, top > -INFINITY) | (uint32_t)((1ull << (a.beams + T::PER - 1) / T::PER) - 1);
-      if (first) {
-        // K of the 64 half lanes' largest values are at least their K-th: no value below that is among the K best.  (Of 1024 values
-        // some 10 pass for K = 8 and 43 for K = 32.)
-        const uint4 half0[2] = {now[0], now[1]}, half1[2] = {now[2], now[3]};
-        const uint32_t x[2] = {(uint32_t)ordered(fminf(words_max<DT>(half0), FLT_MAX)) ^ 0x80000000u,
-                               (uint32_t)ordered(fminf(words_max<DT>(half1), FLT_MAX)) ^ 0x80000000u};
-        const uint32_t t = bound_of<18>(x, a.beams);
-        // (bits below -inf's are no number: then all values count)
-        const int o = (int)(t ^ 0x80000000u);
-        if (o > ordered(-INFINITY)) bound = fmaxf(bound, unordered(o));
-        hits &= __ballot_sync(0xffffffffu, top >= bound);
-      }
       // a lane's values side by side over the warp
       const int u = lane / T::PER, e = lane % T::PER, end = min(a.vocab, w1 * T::PER);
       int n = 0;  // candidates found
