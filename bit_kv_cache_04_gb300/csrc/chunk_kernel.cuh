@@ -579,7 +579,7 @@ struct CachePos {
 
 // SEG: a tile's entry says where it is.  Of a unit's `nt` tiles the `n` own ones are spread evenly among those of the prefix, so that every
 // CTA's stretch has its share of them: they cost more (pages of another sequence each, ragged ends, 16-bit windows: 8 prompts with 8 beams each
-// behind 16-bit windows of 128 tokens took 301 us with the own tiles in a row, 255 us so).  The loader goes through the unit, and leaves every
+// behind 16-bit windows of 128 tokens took 301 us with the own tiles in a row, 255 us so, when a window still took twice as long).  The loader goes through the unit, and leaves every
 // tile's entry in shared memory for the other roles.
 struct TileOrder {
   int own, err;  // own tiles before this one; its place times n, less own times nt
@@ -818,7 +818,9 @@ __device__ __forceinline__ void copies_land() { asm volatile("cp.async.wait_all;
 
 // The same (SEG).  All tokens' values are first copied, as they are, to where the turned ones will stand, so that one load's latency
 // is paid a piece; then four tokens are turned at a time, by eight lanes each.
-// WINDOW_FIGURES
+// (One token at a time, with a load's and the shuffles' latencies each, a tile of 128 window tokens took some 40 us.  8 prompts with 8 beams
+// each behind 16-bit windows of 128 tokens took 208 us with four tokens' loads in flight, 186 us with all of them, 172 us
+// with four rows by eight lanes each instead of one row by 32.)
 template <int D, int DT>
 __device__ __forceinline__ void rotated_window4(const ChunkArgs& a, const CachePos& u, int which, int part, uint32_t dst,
                                                int tile0, int a0, int t0, int t1, int lane, volatile uint32_t* nonfinite) {

@@ -8,7 +8,13 @@
 // like over any other tiles: no second pass joins them.  The chunk attention kernel (chunk_kernel.cuh, SEG) takes
 // the units in place of its own.
 // (First built as two units a row, prefix and own tokens, joined by a pass of its own: a unit of one tile of own tokens took
-// 13 us of latency, and 64 beams over 8 prompts of 8192 tokens 142 us where they now take a third less.)
+// 13 us of latency, and 8 x 8 beams over prompts of up to 8192 tokens with 16-bit windows 467 us.)
+//
+// On one GB300, plan and attention of one layer: 4 beams over 4096 tokens 28.8 us, 8 x 8 beams over prompts of up to 8192 tokens with 16-bit windows 185 us
+// (the chunk attention of each sequence 500 us), drafts of up to 4 tokens of 32 chats over 32768 tokens 212 us (767 us), 16 questions
+// of up to 200 tokens over 12007 tokens of 256-channel heads 1219 us.  The plan takes 10 to 17 us of that, a chain of dependent steps in one block.
+// What bounds the attention is latency between dependent steps, as in the chunk attention: a CTA's tile takes 2 us, whether all its rows see it or one
+// sequence's do; with few tiles, the 20 to 30 us that a run's start and its join cost.
 //
 // The prefix is what the block table says: the pages that the group's sequences hold in the same places, as far as
 // they are quantized in all of them and before every new token, in whole tiles.  kvq_prefix_plan finds it and writes the units
@@ -23,8 +29,8 @@ namespace kvq {
 namespace {
 
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
-// A unit's start (queries, first scores, outputs) against a tile's time: 64 units over 8 prompts of 8192 tokens took 94, 82, 95 us with 2, 4, 8
-// places on the line for it, drafts of 32 chats 250, 243, 234 us.
+// A unit's start (queries, first scores, outputs) against a tile's time, as places on the line.  With 4 and 8 of them 64 units over 8 prompts of 8192 tokens took
+// 84 and 98 us (128 tokens of their own) or 129 and 117 us (512), drafts of 32 chats 212 and 210 us; with 2 the drafts 221 us.
 constexpr int kUnitCost = 4;
 constexpr int kPlanSmall = 1024;  // sequences whose state fits shared memory; more have it in the workspace
 
