@@ -724,6 +724,21 @@ kvq_status kvq_beam_select(const void* logits, int32_t dtype, int64_t group_stri
        (uintptr_t)done_out) & 3u)
     return fail(KVQ_ERR_ARG, "scores, done and outputs must be 4-byte aligned");
   if ((st = check_select_ws(n_groups, beams, vocab, workspace, ws_bytes)) != KVQ_OK) return st;
+  {
+    // a group's results are written while other groups' inputs are still read
+    const uintptr_t list = 4 * (uintptr_t)n_groups * beams, size = dtype == KVQ_DT_F32 ? 4 : 2;
+    const uintptr_t all = size * (uintptr_t)((n_groups - 1) * group_stride + (beams - 1) * beam_stride + vocab);
+    auto meet = [](const void* x, uintptr_t n, const void* y, uintptr_t m) {
+      return x && y && (uintptr_t)x < (uintptr_t)y + m && (uintptr_t)y < (uintptr_t)x + n;
+    };
+    const void* const out[4] = {scores_out, tokens, parents, done_out};
+    for (int i = 0; i < 4; ++i) {
+      bool bad = meet(out[i], list, logits, all) || (meet(out[i], list, scores, list) && !(i == 0 && scores_out == scores)) ||
+                 (meet(out[i], list, done, list) && !(i == 3 && done_out == done));
+      for (int j = 0; j < i; ++j) bad |= meet(out[i], list, out[j], list);
+      if (bad) return fail(KVQ_ERR_ARG, "an output overlaps another one or an input");
+    }
+  }
   SelectArgs a{};
   a.logits = (const char*)logits;
   a.group_stride = group_stride;

@@ -578,7 +578,7 @@ KVQ_API kvq_status kvq_pages_reorder(const kvq_config* cfg, const kvq_cache* cac
  *  done:   [n_groups][beams] int32, not 0: finished; or NULL (none is).  Needs an end token.
  *  eos:    the end token, or -1 for none.
  *  scores_out, tokens, parents, done_out: [n_groups][beams]; scores_out may be scores and done_out may be done,
- *          nothing else may overlap; done_out may be NULL.
+ *          nothing else may overlap (KVQ_ERR_ARG); done_out may be NULL.
  * With fewer candidates above -inf than beams the rest have -inf, the lowest beams and tokens first.
  * beams in 1..32, vocab below 2^26, n_groups * beams at most 2^24.
  *  workspace: kvq_beam_workspace_bytes bytes, 256-byte aligned, prepared once by kvq_beam_workspace_init for

@@ -30,6 +30,22 @@ def test_select_refusals(kw, status):
     assert _select(**kw) == status
 
 
+def test_outputs_that_overlap():
+    """Every output apart from the others and from the inputs, but for scores and finished beams in place."""
+    at = {n: (i + 1) << 24 for i, n in enumerate(("logits", "scores", "done", "so", "tok", "par", "do"))}
+    for out in ("so", "tok", "par", "do"):
+        for other in at:
+            if other == out or (out, other) in (("so", "scores"), ("do", "done")):
+                continue
+            for shift in (0, 28, -28):  # lists of 32 bytes
+                if (other, shift) == ("logits", -28):
+                    shift = 15000  # logits reach 2 * (4000 + 3000 + 1000) bytes
+                assert _select(**{**at, out: at[other] + shift}, eos=1) == 1, (out, other)
+                assert b"overlaps" in K.LIB.kvq_last_error()
+    for out, other in (("so", "scores"), ("do", "done")):
+        assert _select(**{**at, out: at[other] + 4}, eos=1) == 1
+
+
 def test_workspace_sizes():
     out = ctypes.c_size_t()
     assert K.LIB.kvq_beam_workspace_bytes(2, 4, 1000, None) == 1
