@@ -373,3 +373,69 @@ def test_rows_of_many_sequences_in_several_row_tiles():
         new = [[1 + (5 * i) % 9 if i != 4 else 61 for i in range(12)]]
         c = build([700], own, new, D=D, H_kv=H, g=g, L=2)
         check(c[0], c[2], c[3], c[4], c[5])
+
+
+def test_large_batches():
+    """More sequences than the plan keeps in shared memory."""
+    G, beams = 260, 4
+    own = [[1 + (7 * i + 3 * j) % 40 for j in range(beams)] for i in range(G)]
+    c = build([(140, 17, 0, 260)[i % 4] for i in range(G)], own, [[1] * beams for _ in range(G)], H_kv=1, g=2)
+    check(c[0], c[2], c[3], c[4], c[5])
+
+
+def test_long_tables():
+    """Tables of more columns than a block of the plan looks at: whole, and apart in a later block's share."""
+    c = build([5000, 2500], [[30, 40, 50], [20, 300]], [[1, 1, 1], [2, 1]], page_tokens=8, H_kv=1)
+    cache, lens, cu_g, n = c[0], c[2], c[3], c[4]
+    want = check(cache, lens, cu_g, n, 3, want_shared=[4992, 2432])
+    page, free = cache.block_table[1, 300].item(), cache.cfg.n_pages - 1
+    for b in ("k_main", "v_main"):
+        x = cache.buffers[b].view(cache.cfg.L, cache.cfg.n_pages, -1)
+        x[:, free] = x[:, page]
+    cache.block_table[1, 300] = free
+    out = check(cache, lens, cu_g, n, 3, want_shared=[2304, 2432])
+    assert (out.float() - want.float()).norm() <= 2.0 ** -9 * want.float().norm()
+
+
+def test_some_layers():
+    c = build([300], [[30, 40, 50]], [[1, 2, 1]], L=4, **ROT4)
+    cache, lens, cu_g, n = c[0], c[2], c[3], c[4]
+    q, want, cu, pa = attend(cache, lens, cu_g, n, c[5])
+    for layer0, layers in ((0, 1), (1, 2), (3, 1)):
+        out = torch.full_like(q[:layers], -7.0)
+        pa.attention(layer0, layers, q[layer0:layer0 + layers].contiguous(), out)
+        torch.cuda.synchronize()
+        ref = want[layer0:layer0 + layers]
+        assert pa.device_status() == 0 and torch.equal(out[:, cu[-1]:], ref[:, cu[-1]:])
+        assert (out.float() - ref.float()).norm() <= 2.0 ** -9 * ref.float().norm()
+
+
+@pytest.mark.parametrize("key", ["q4_0", "rot4_d256", "rot4_bf16_window"])
+def test_reordered_and_attended_in_turn(key):
+    """Reordering, plan and attention over and over with nothing between: every attention sees the tables as they are then."""
+    c = build([300, 150], [[40, 90, 170], [20, 60, 130]], [[1] * 3, [1] * 3], **FORMATS[key])
+    cache, pool, lens, cu_g, n = c[0], c[1], c[2], c[3], c[4]
+    table, refs, lens0 = cache.block_table.clone(), pool.refs.clone(), lens.clone()
+    buffers = {k: v.clone() for k, v in cache.buffers.items() if v is not None}
+    cu = torch.arange(7, dtype=torch.int32, device="cuda")
+    turns = torch.tensor([[1, 2, 0, 2, 0, 1], [1, 0, 2, 0, 2, 1], [0, 1, 2, 2, 1, 0]] * 8, dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 6, cache.cfg.H_q, cache.cfg.D), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(DT[cache.cfg.in_dtype])
+    pa, outs = K.PrefixAttention(cache, 2, 6), []
+    for wait in (False, True):
+        cache.block_table.copy_(table)
+        pool.refs.copy_(refs)
+        lens.copy_(lens0)
+        for k, v in buffers.items():
+            cache.buffers[k].copy_(v)
+        out = torch.zeros((len(turns), *q.shape), dtype=q.dtype, device="cuda")
+        torch.cuda.synchronize()
+        for i, parents in enumerate(turns):
+            pool.reorder(parents, 3, lens)
+            pa.plan(cu_g, cu, 6, 1, 3, lens)
+            pa.attention(0, 1, q, out[i])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert pa.device_status() == 0 and pool.device_status() == 0
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and not torch.equal(outs[0][0], outs[0][1])
