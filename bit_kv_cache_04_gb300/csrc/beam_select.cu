@@ -142,9 +142,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // masked by the type's lowest value, infinities), of 2^((x - m) kLog2e).
 constexpr float kBig = 1e30f;
 __device__ __forceinline__ bool big(float m) { return fabsf(m) > kBig; }
-// What takes a sum from reference m to a larger one
+__device__ __forceinline__ float reference(float m) { return __fmul_rn(m, kLog2e); }
+// What takes a sum from the reference of m to that of a larger value.  (Both rounded as in the terms: contracted to one
+// fused product, m = to gave 2^(rounding of r) instead of 1, and rows 10000 away from zero scores up to 9e-4 off.)
 __device__ __forceinline__ float rescale(float m, float to) {
-  return exp2_approx(big(m) || big(to) ? (m - to) * kLog2e : m * kLog2e - to * kLog2e);
+  return exp2_approx(big(m) || big(to) ? (m - to) * kLog2e : __fsub_rn(reference(m), reference(to)));
 }
 
 template <int DT>
@@ -363,7 +365,7 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
       s *= rescale(m, top);
       m = top;
     }
-    const float r = m * kLog2e;
+    const float r = reference(m);
     float t;
     {
       const uint64_t nr = pk2(-r, -r), c = pk2(kLog2e, kLog2e);
@@ -553,7 +555,7 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh
       // apart, so that rows of the type's lowest value keep their log-sum
       sh.max[b] = (double)m;
       // nothing may follow: every candidate is -inf all the same
-      sh.log_sum[b] = sum > 0 ? log_of(sum) + (big(m) ? 0.0 : (double)(m * kLog2e) * (1.0 / (double)kLog2e) - (double)m) : 0.0;
+      sh.log_sum[b] = sum > 0 ? log_of(sum) + (big(m) ? 0.0 : (double)reference(m) * (1.0 / (double)kLog2e) - (double)m) : 0.0;
       sh.score[b] = (double)tame(score);
     }
     if (threadIdx.x == 0) sh.count = 0;
