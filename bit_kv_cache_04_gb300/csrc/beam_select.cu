@@ -138,15 +138,20 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 // Sums of exponentials are of 2^(x kLog2e - r), one fused product a term, r = kLog2e times the largest value m, rounded: the same
-// number in every term, so its rounding costs nothing.  Past kBig, where products would leave fp32's range (rows
-// masked by the type's lowest value, infinities), of 2^((x - m) kLog2e).
-constexpr float kBig = 1e30f;
+// number in every term, taken off again at the end.  It is off by up to half a step of r, and so is every exponent.  Up to kBig that is
+// 1/16 at most; beyond (from some 1e9 on all of a row's terms would overflow or vanish together: rows and tokens masked by
+// -1e10, by the type's lowest value, infinities) terms are of 2^((x - m) kLog2e), two roundings each, where the
+// difference is exact for all that count.
+constexpr float kBig = 1e6f;
 __device__ __forceinline__ bool big(float m) { return fabsf(m) > kBig; }
 __device__ __forceinline__ float reference(float m) { return __fmul_rn(m, kLog2e); }
-// What takes a sum from the reference of m to that of a larger value.  (Both rounded as in the terms: contracted to one
+// What takes a sum from the reference of m to that of a larger value: r below kBig, m kLog2e itself beyond, in one fused
+// product where they meet.  (Both rounded as in the terms: contracted to one
 // fused product, m = to gave 2^(rounding of r) instead of 1, and rows 10000 away from zero scores up to 9e-4 off.)
 __device__ __forceinline__ float rescale(float m, float to) {
-  return exp2_approx(big(m) || big(to) ? (m - to) * kLog2e : __fsub_rn(reference(m), reference(to)));
+  const float x = big(m) ? (big(to) ? (m - to) * kLog2e : __fmaf_rn(m, kLog2e, -reference(to)))
+                         : (big(to) ? __fmaf_rn(-to, kLog2e, reference(m)) : __fsub_rn(reference(m), reference(to)));
+  return exp2_approx(x);
 }
 
 template <int DT>
@@ -385,7 +390,7 @@ __device__ __forceinline__ void scan_row(const SelectArgs& a, SelectShared& sh, 
       upk2(sum, t0, t1);
       t = t0 + t1;
     }
-    if (!(t <= (float)(U * T::PER)) || big(m)) {  // hardly ever: a NaN, infinities, or nothing yet
+    if (!(t <= (float)(U * T::PER)) || big(m)) {  // hardly ever: a NaN, infinities, masked values alone, or nothing yet
       t = 0.f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
