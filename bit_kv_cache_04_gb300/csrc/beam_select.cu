@@ -283,6 +283,7 @@ struct SelectShared {
   float m[kSelWarps], s[kSelWarps];
   double max[kMaxBeams], log_sum[kMaxBeams], score[kMaxBeams];
   int done[kMaxBeams];
+  bool finished;                       // this block's beam
   bool last;
 };
 
@@ -636,8 +637,10 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const __gri
   if (threadIdx.x == 0) sh.bound = ordered(-INFINITY);
   grid_launch_dependents();
   grid_dependency_wait();
+  // read once, before the ticket: behind the group's last one done_out is written, which may be done
+  if (threadIdx.x == 0) sh.finished = a.done && a.done[row];
   __syncthreads();
-  if (!(a.done && a.done[row])) {
+  if (!sh.finished) {
     const char* p = a.logits + (group * a.group_stride + b * a.beam_stride) * T::BYTES;
     const int skew = (int)((uintptr_t)p & 15) / T::BYTES;  // elements between the 16-byte boundary and the row
     const int words = (a.vocab + T::PER - 1) / T::PER;
