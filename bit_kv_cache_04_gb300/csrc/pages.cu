@@ -77,6 +77,10 @@ size_t pages_ws_layout(const kvq_config* c, void* base, PagesWs* w) {
   return off;
 }
 
+// Kernels here that change the table or the lengths let the stream's next kernel go at their ends only.  The chunk attention reads both with
+// non-coherent loads: begun while an attention before these calls still ran, it could find in an SM's first-level cache what that one had read there
+// since.  (A kernel behind such an end begins after it, and may let the next one go at its start.)
+
 // ---- counts -----------------------------------------------------------------
 
 __global__ void count_refs_kernel(PagesArgs a) {
@@ -96,7 +100,6 @@ __global__ void count_refs_kernel(PagesArgs a) {
 // One block per listed sequence.  The exchange makes a second listing of the
 // same sequence find -1 everywhere, whichever block is first.
 __global__ void release_kernel(PagesArgs a) {
-  grid_launch_dependents();
   grid_dependency_wait();
   const int s = a.seqs[blockIdx.x];
   if (s < 0 || s >= a.lo.B) {
@@ -123,7 +126,6 @@ __global__ void release_kernel(PagesArgs a) {
 // One block per pair.  Every accepted target is empty, listed by no earlier
 // pair and no pair's source, so no block writes what another one reads.
 __global__ void fork_kernel(PagesArgs a) {
-  grid_launch_dependents();
   grid_dependency_wait();
   const int i = blockIdx.x, mp = a.lo.max_pages;
   const int s = a.seqs[i], d = a.other[i];
@@ -240,7 +242,6 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(PagesArgs a) {
   __shared__ int warp_sums[32];
   __shared__ uint32_t err;
   __shared__ int found;
-  grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = kPlanThreads / 32;
   const int n = a.n, mp = a.lo.max_pages;
@@ -430,8 +431,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesArgs a)
 
 // A group's slots after a selection: slot b becomes what slot parents[b] was.  Every column of the table (and every
 // 16-byte word of the windows) belongs to one thread, which reads all it needs of the group before it writes: no copy
-// of the old state is kept.  (The stream's next kernel is let go at these kernels' ends only: begun while an attention before them still ran, it could find that one's
-// table entries in the first-level cache, where it reads them with non-coherent loads.)
+// of the old state is kept.
 
 // The group's parents and lengths into shared memory; 0, or the status bit of what is wrong with them.
 __device__ __forceinline__ uint32_t group_state(const PagesArgs& a, int group, int* parent, int* len) {
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_window_kernel(PagesAr
 // word that divides both runs' bytes.  TABLE: the block table's entries through `map` too.
 template <class V, bool TABLE>
 __global__ void __launch_bounds__(256) copy_pages_kernel(PagesArgs a, int k_words, int v_words) {
-  grid_launch_dependents();
+  if constexpr (!TABLE) grid_launch_dependents();
   grid_dependency_wait();
   if constexpr (TABLE) {
     const int64_t total = (int64_t)a.lo.B * a.lo.max_pages;

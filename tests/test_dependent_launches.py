@@ -1,0 +1,36 @@
+"""A kernel that lets the stream's next one go at its start may still be running, and so may the one before it, when that next one's
+blocks begin.  What those read with non-coherent loads (__ldg) must not have been written since: an SM's
+first-level cache may hold it from before.  The sources are read here, nothing runs."""
+
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_kv_cache_04_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def kernels(text):
+    """Bodies of the kernels of a source, by name."""
+    found = {}
+    for m in re.finditer(r"__global__[^;{]*?(\w+)\((?:[^()]|\([^()]*\))*\)\s*\{", text):
+        depth, i = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            i += 1
+        found[m.group(1)] = text[m.end():i]
+    return found
+
+
+def test_kernels_that_change_tables_or_lengths_let_the_next_one_go_at_their_ends():
+    pages = kernels(source("pages.cu"))
+    assert {"release_kernel", "fork_kernel", "reserve_kernel", "reorder_kernel", "copy_pages_kernel"} <= set(pages)
+    for name in ("release_kernel", "fork_kernel", "reserve_kernel", "reorder_kernel"):
+        assert "grid_launch_dependents" not in pages[name], name
+    body = pages["copy_pages_kernel"]  # with TABLE it writes the compacted table
+    assert body.count("grid_launch_dependents") == body.count("if constexpr (!TABLE) grid_launch_dependents") == 1
+    assert "grid_launch_dependents" not in kernels(source("append.cu"))["commit_lengths_kernel"]
+    assert "grid_launch_dependents" not in kernels(source("prefix_attention.cu"))["prefix_plan_kernel"]
