@@ -51,8 +51,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// (Not with non-coherent loads: a call in place writes what it has read, and the stream's next call may begin before this one ends.)
 __device__ __forceinline__ uint4 load8(const uint16_t* p, bool vec) {
-  if (vec) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (vec) return __ldcg(reinterpret_cast<const uint4*>(p));
   uint4 v;
   v.x = p[0] | ((uint32_t)p[1] << 16);
   v.y = p[2] | ((uint32_t)p[3] << 16);

@@ -34,3 +34,13 @@ def test_kernels_that_change_tables_or_lengths_let_the_next_one_go_at_their_ends
     assert body.count("grid_launch_dependents") == body.count("if constexpr (!TABLE) grid_launch_dependents") == 1
     assert "grid_launch_dependents" not in kernels(source("append.cu"))["commit_lengths_kernel"]
     assert "grid_launch_dependents" not in kernels(source("prefix_attention.cu"))["prefix_plan_kernel"]
+
+
+def non_coherent(name):
+    """What a source reads with __ldg."""
+    return re.findall(r"__ldg\(((?:[^()]|\((?:[^()]|\([^()]*\))*\))*)\)", source(name))
+
+
+def test_norm_and_turn_reads_no_rows_that_kernels_write_with_non_coherent_loads():
+    """In place it writes them itself."""
+    assert non_coherent("qk_norm_rope.cu") == []
