@@ -3023,7 +3023,7 @@ __global__ void __launch_bounds__(256) turn_queries_kernel(const __grid_constant
     uint2 x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (c0 + k < chunks) x[k] = __ldg(src + 32 * (c0 + k));
+      if (c0 + k < chunks) x[k] = __ldcg(src + 32 * (c0 + k));
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (c0 + k < chunks) {

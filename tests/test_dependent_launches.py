@@ -44,3 +44,11 @@ def non_coherent(name):
 def test_norm_and_turn_reads_no_rows_that_kernels_write_with_non_coherent_loads():
     """In place it writes them itself."""
     assert non_coherent("qk_norm_rope.cu") == []
+
+
+def test_chunk_attention_reads_only_tables_and_lengths_with_non_coherent_loads():
+    """Those are written by kernels that let the next one go at their ends (above), or by the caller's; queries may come from
+    any kernel of the stream."""
+    got = non_coherent("chunk_kernel.cuh")
+    allowed = ("a.cu_q", "a.seq_lens", "a.cp.block_table")
+    assert got and all(x.startswith(allowed) for x in got), got
