@@ -3086,7 +3086,7 @@ cudaError_t launch_chunk(ChunkArgs a, int grid, cudaStream_t s) {
   if ((a.lo.flags & KVQ_ROTATE_K) && !a.turn_here) {
     if constexpr (SEG) {
       const int64_t items = (int64_t)a.n_layers * C::RT / a.lo.g * ((a.lo.Hq * (D / 128) + 3) / 4);
-      const unsigned parts = (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 7) / 8, 4 * 152 / a.n_units + 1));
+      const unsigned parts = (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 7) / 8, 4 * grid / a.n_units + 1));
       e = launch_dependent(turn_units_kernel<D, DT, C::RT>, dim3(a.n_units, parts), dim3(256), 0, s, a);
     } else {
       const int64_t rows = (int64_t)a.n_layers * a.total_q;
