@@ -15,8 +15,10 @@
 // rank: every lane counts how many of the few new keys are before its own.  Of n values in random order about K ln(n / K)
 // ever enter a list, so the stream's cost is that of the maximum and the exponentials.
 //
-// On one GB300: 1 x 4 beams over 32000 tokens 12.6 us (launch, one turn and two joins), 16 x 5 over 50257 (fp32) 18.7, 8 x 32 over 32001 31,
-// 64 x 8 over 131072 (bf16) 50 us or 2.7 TB/s, with 68 % of the issue slots taken: 459 instructions for a warp's turn.
+// On one GB300, one call a replayed graph: 1 x 4 beams over 32000 tokens 12.4 us (launch, one turn and two joins), 16 x 5 over 50257 (fp32) 18.5,
+// 8 x 32 over 32001 32, 64 x 8 over 131072 (bf16) 50 us.  Called one behind another, each one's blocks beginning while the one before still
+// runs: 12.9, 21.9, 41 and 47 us or 2.9 TB/s, with 68 % of the issue slots taken: 459 instructions for a warp's turn.
+// Turns of masked values alone go through their terms twice (see kBig): 64 x 8 rows of nothing but -1e9 69 us.
 // (Tried: sorting networks over the warp instead of ranks, 2200 cycles a time, and 64-bit floating-point comparisons in the last step, 5000: the smallest
 // search 39 us, 20.8 us without them.  Every value offered by itself, unrolled, the large batch 144 us.  A first bound for each warp instead of
 // one for the block: 8 x 32 beams 41 us.)
@@ -659,8 +661,10 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const __gri
 }
 
 // Blocks a row: up to two an SM in all, each with at least a turn of logits to read (8192 of two bytes); at most 4096 candidates a group.
-// More of them cost more in first turns and joins than they read sooner: 16 x 8 rows of 32000 took 18.6, 20.0, 24.4, 30.9 us with 1, 2, 4, 8
-// blocks a row; 64 rows of 131072 took 20.7, 16.6, 14.6, 16.6 us; one row 20.7, 14.6, 12.6, 10.5 us, and 12.5 us with 16.
+// More of them read sooner and cost more in first turns and joins.  In us with 1, 2, 4, 8, 16 blocks a row, the rule's in brackets (bf16, one call a
+// graph): 16 x 8 rows of 32000 20.0 [21.1] 31.3; 16 x 5 of 50257 22.9 21.4 [3: 20.9] 22.7 28.8; 8 x 8 of 131072 30.7 25.2 [27.6] 29.7 35.5;
+// 8 x 32 of 32001 [35.6] 45.9 60.2; 4 x 4 of 131072 27.2 21.6 18.3 17.2 [21.3]; 1 x 4 of 131072 26.3 20.7 17.7 16.7 [18.7]; one row of
+// 131072 23.3 18.6 15.7 14.6 [13.7].  So the rule is up to a tenth off the best count, a quarter for a few long rows.
 int splits_of(int64_t rows, int beams, int vocab) {
   const int64_t want = (int64_t)sm_count() * 2 / std::max<int64_t>(1, rows);
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)vocab / 8192, (int64_t)4096 / (beams * beams)}));

@@ -239,6 +239,8 @@ bool tbq4_bins_ok();
 // stream to complete with its memory visible, so the order of effects is the
 // plain stream order.  Consecutive decode calls then overlap one grid's tail
 // with the next one's block launch.
+// A kernel that lets the next one go at its start may still run, and the one before it too, when the next one's blocks begin.  So what a
+// kernel reads with non-coherent loads (__ldg) is written only by kernels that let the next one go at their ends.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::); }
 

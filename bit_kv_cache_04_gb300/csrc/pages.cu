@@ -11,8 +11,8 @@
 // copied by a second, grid-wide kernel that reads the decision from the
 // workspace: 2 bytes of traffic per byte moved, HBM-bound (6000 pages half used compacted in 288 us, 83 % of the copy
 // rate; two prompts forked twice, 14 us of dependent launches).  A reordering needs no plan: every group's columns are its own, a block for 128 of
-// them (4 beams of 4099 tokens 6.3 us); the windows, one read and one write for each slot that changes, go at 93 % of the copy rate (16 x 8 beams with 128
-// tokens in 16 layers, 228 us).
+// them (4 beams of 4099 tokens 6.2 us); the windows, one read and one write for each slot that changes, go at 93 to 97 % of the copy rate (16 x 8 beams
+// with 128 tokens in 16 layers, 225 to 235 us).
 #include <algorithm>
 
 #include "kvq_host.cuh"

@@ -11,8 +11,11 @@
 // 13 us of latency, and 8 x 8 beams over prompts of up to 8192 tokens with 16-bit windows 467 us.)
 //
 // On one GB300, plan and attention of one layer: 4 beams over 4096 tokens 28.8 us, 8 x 8 beams over prompts of up to 8192 tokens with 16-bit windows 185 us
-// (the chunk attention of each sequence 500 us), drafts of up to 4 tokens of 32 chats over 32768 tokens 212 us (767 us), 16 questions
-// of up to 200 tokens over 12007 tokens of 256-channel heads 1219 us.  The plan takes 10 to 17 us of that, a chain of dependent steps in one block.
+// (the chunk attention of each sequence 532 us), drafts of up to 4 tokens of 32 chats over 32768 tokens 212 us (767 us), 16 questions
+// of up to 200 tokens over 12007 tokens of 256-channel heads 1219 us (1271 us).  The plan takes 6 to 13 us of that (8 to 17 us by itself), a chain of
+// dependent steps in one block.  Single tokens can also go through the single-token decode, every sequence by itself, its shared pages from the L2: layer by
+// layer that is faster for few sequences behind short prompts (4 beams over 4096 tokens 17 us against 21.5 us and a plan for all layers, 16
+// beams 45 against 60 us) and slower for many (4 x 16 beams over 16384 tokens 344 against 106 us).
 // What bounds the attention is latency between dependent steps, as in the chunk attention: a CTA's tile takes 2 us, whether all its rows see it or one
 // sequence's do; with few tiles, the 20 to 30 us that a run's start and its join cost.
 //

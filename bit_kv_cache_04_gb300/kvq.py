@@ -642,7 +642,8 @@ class BeamSelect:
 class PrefixAttention:
     """Attention of groups of sequences that share the pages of a prefix (kvq_prefix_plan, kvq_prefix_attention)
     and its workspace.  `rows`: the largest total_q of a plan.  Calls that may run at the same time (also graphs
-    replayed side by side) need an object each."""
+    replayed side by side) need an object each.  For single tokens of few sequences behind short prompts `KVCache.decode` is
+    faster, and more exact."""
 
     def __init__(self, cache: KVCache, groups: int, rows: int, stream=None):
         import torch
