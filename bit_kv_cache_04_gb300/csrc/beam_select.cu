@@ -572,8 +572,10 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, SelectShared& sh
   __syncthreads();
   auto candidate = [&](int c, int64_t key) {
     const LogitKey e{key};
-    const int b = min(c / (S * K), K - 1);
-    if (sh.done[b]) return c == b * S * K ? ScoreKey::of(sh.score[b], b * a.vocab + a.eos) : ScoreKey::none();  // one candidate
+    const int b = min(c / (S * K), K - 1), i = c - b * S * K;
+    if (sh.done[b]) return i == 0 ? ScoreKey::of(sh.score[b], b * a.vocab + a.eos) : ScoreKey::none();  // one candidate
+    // an empty beam: all are -inf, whatever their logits
+    if (sh.score[b] == -INFINITY) return i < min(K, a.vocab) ? ScoreKey::of(-INFINITY, b * a.vocab + i) : ScoreKey::none();
     if (!e.real()) return ScoreKey::none();
     return ScoreKey::of(sh.score[b] + (((double)e.value() - sh.max[b]) - sh.log_sum[b]), b * a.vocab + e.token());
   };
